@@ -317,6 +317,152 @@ int et_mlp_chain(const void* x, const void* gamma, float eps, const void* w_gate
                  const et_opts* opts, void* stream);
 
 /* ------------------------------------------------------------------------
+ * The router's selection over given logits, with the losses of a training
+ * step (the source paper has no counterpart; the selection is et_moe_layer's).
+ *
+ *   a token is routed when token_mask[t] != 0 (NULL: every token) and at
+ *   least one of its logits is above -inf;
+ *   idx[t,:] = the k largest logits, ties to the lower expert index, -1 in
+ *              place of a logit of -inf and for a token that is not routed;
+ *   w[t,:]   = softmax over the chosen logits, 0 where idx is -1;
+ *   counts[e] = how often e was chosen, n = the number of routed tokens;
+ *   mean_prob[e] = (1/n) sum_t p[t,e],  p = softmax(logits[t,:]), routed t;
+ *   losses[0] = E sum_e counts[e] / (n k) * mean_prob[e]       (balance)
+ *   losses[1] = (1/n) sum_t log(sum_e exp logits[t,e])^2       (z)
+ *
+ * All of it fp32; sums over tokens run in a fixed order, so the results are
+ * the same bits on every run.  With n == 0 the losses and probabilities are 0.
+ * A NaN logit ranks above all others and makes the token's weights, and the
+ * losses, NaN.  The losses are in logits alone: counts carries no gradient.
+ *
+ * The gradient (et_router_topk_bwd), for d_losses fp32 [2] (NULL: 0) and
+ * d_topk_w fp32 [T,k] (NULL: 0; read only where idx is not -1):
+ *   d_logits[t,e] = d_losses[0] p (c_e - sum_f c_f p[t,f])
+ *                   + d_losses[1] (2/n) lse_t p
+ *                   + sum_{j: idx[t,j] = e} w[t,j] (d_w[t,j] - sum_i w[t,i] d_w[t,i]),
+ *   c_e = E counts[e] / (n^2 k); 0 for a token that is not routed.
+ * topk_idx, topk_w, expert_counts and n_routed are the forward's outputs.
+ *
+ * logits fp32 [T_max,E]; token_mask uint8 [T_max] or NULL; topk_idx int32
+ * [T_max,k]; topk_w fp32 [T_max,k]; expert_counts int32 [E], n_routed int32
+ * [1], mean_prob fp32 [E], losses fp32 [2] (each may be NULL in the forward);
+ * d_logits fp32 [T_max,E].  1 <= E <= 256, 1 <= k <= min(E, 8), 1 <= T_max <=
+ * 2^24.  Rows >= T are neither read nor written; T == 0 still writes counts,
+ * n, probabilities and losses (all 0).  The workspace is used by both calls
+ * (the backward needs its first 256 bytes only).  Errors as et_moe_layer.
+ * ---------------------------------------------------------------------- */
+size_t et_router_topk_workspace_bytes(int T_max, int E, int k);
+
+int et_router_topk(const float* logits, const uint8_t* token_mask, int32_t* topk_idx,
+                   float* topk_w, int32_t* expert_counts, int32_t* n_routed, float* mean_prob,
+                   float* losses, int T, const int32_t* d_T, int T_max, int E, int k,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+int et_router_topk_bwd(const float* logits, const uint8_t* token_mask, const int32_t* topk_idx,
+                       const float* topk_w, const int32_t* expert_counts,
+                       const int32_t* n_routed, const float* d_losses, const float* d_topk_w,
+                       float* d_logits, int T, const int32_t* d_T, int T_max, int E, int k,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The norms after one block and before the next, with the block's gate and
+ * residual scale, in one pass (the source paper has no counterpart):
+ *
+ *   n     = y / sqrt(mean(y^2) + eps) * gamma_post     (y without gamma_post)
+ *   z     = x + scale * gate * n                       (x without y)
+ *   x_out = bf16(z),   x_hat = bf16( z / sqrt(mean(z^2) + eps) * gamma_pre )
+ *
+ * computed in fp32 with one rounding for each output (x_hat is taken from z,
+ * not from the rounded x_out).  x is the residual stream, y the block's
+ * output, x_hat the next block's input.  y, gamma_post, gate and gamma_pre
+ * may be NULL; gamma_pre and x_hat go together; x_out may be NULL.
+ *   gate_kind 0: no gate (gate NULL); 1: per channel, bf16 [H]; 2: per token,
+ *   fp32 [T_max]; 3: per token and channel, bf16 [T_max,H].
+ * x, y, x_out, x_hat bf16 [T_max,H]; gamma bf16 [H]; eps > 0; 1 <= H <= 16384
+ * (multiples of 8 with 16-byte aligned tensors use 16-byte accesses; any
+ * other H or alignment is served element by element); 1 <= T_max <= 2^24.
+ * x_out may be x.  Sums of squares are fp32: a row's must stay below 3e38.
+ *
+ * et_block_norm_bwd: with d_x_out and d_x_hat (bf16 [T_max,H], one of them may
+ * be NULL: no gradient flows there), dx and dy (bf16; dy NULL exactly when y
+ * is), d_gamma_post and d_gamma_pre (fp32 [H] or NULL), d_gate (fp32 [H], fp32
+ * [T_max] or bf16 [T_max,H] by gate_kind, or NULL).  The parameter gradients
+ * are overwritten, not added to; they are summed in a fixed order (the same
+ * bits on every run) and are 0 when T == 0.  dx may be d_x_out, dy may be y.
+ * Workspace: et_block_norm_workspace_bytes; the forward needs its first 256
+ * bytes only.  Errors as et_moe_layer.
+ * ---------------------------------------------------------------------- */
+size_t et_block_norm_workspace_bytes(int T_max, int H);
+
+int et_block_norm(const void* x, const void* y, const void* gamma_post, const void* gate,
+                  int gate_kind, float scale, const void* gamma_pre, float eps, void* x_out,
+                  void* x_hat, int T, const int32_t* d_T, int T_max, int H, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+int et_block_norm_bwd(const void* x, const void* y, const void* gamma_post, const void* gate,
+                      int gate_kind, float scale, const void* gamma_pre, float eps,
+                      const void* d_x_out, const void* d_x_hat, void* dx, void* dy,
+                      float* d_gamma_post, float* d_gamma_pre, void* d_gate, int T,
+                      const int32_t* d_T, int T_max, int H, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Products with 4-bit weights, for decoding (the source paper has no
+ * counterpart; the small batches of et_splitk_gemm and et_moe_layer are bound
+ * by the bytes of their bf16 weights, which these hold in a quarter).
+ *
+ *   w[n,k] = scale[k / group, n] * (q[n,k] - 8),  q in 0..15
+ *
+ * q uint8 [N, K/2], row-major: q[n,2i] is the low half of byte i, q[n,2i+1]
+ * the high half; scale bf16 [K/group, N]; with E weights one behind the other
+ * [E, N, K/2] and [E, K/group, N].  group is 32, 64 or 128; K a positive
+ * multiple of group, N of 8, both up to 2^20.  All 16-byte aligned.
+ *
+ * et_w4_quantize makes them from bf16 [E,N,K]: scale = bf16(max|w| / 7) over a
+ * group, q = 8 + round-half-even(w / scale) within 0..15; a group whose scale
+ * is 0 becomes zeros, one with an infinity or NaN a scale of NaN (and q = 8).
+ * et_w4_dequantize gives bf16(w[n,k]) back, for batches beyond the calls
+ * below (through et_moe_layer or et_splitk_gemm).  1 <= E <= 65536.
+ *
+ * et_w4_gemv: Y[M,N] = bf16( X w^T ), X bf16 [M_max,K], Y bf16 [M_max,N], rows
+ * >= M untouched; 1 <= M_max <= 64.
+ *
+ * et_w4_experts: the routed experts of a few tokens, with et_router_topk's (or
+ * et_moe_layer's) topk_idx int32 [T_max,k] and topk_w fp32 [T_max,k]:
+ *   h[t,j] = bf16( silu(x_t Wg[e]^T) * (x_t Wu[e]^T) ),  e = idx[t,j];
+ *   out[t] = bf16( sum_j w[t,j] * (h[t,j] Wd[e]^T) )
+ * x, out bf16 [T_max,H]; gate and up weights [E,F,H], down [E,H,F] in 4 bits.
+ * An index of -1 leaves its expert out (its weight is not read); one outside
+ * [-1, E) is left out too and recorded as ET_ERR_BOUNDS (et_status).  A token
+ * may name an expert twice.  1 <= T_max <= 64, 1 <= E <= 256, 1 <= k <=
+ * min(E, 8); H and F are inputs and outputs in turn: multiples of group.
+ *
+ * Products are exact and summed in fp32; a group's sum of (q - 8) x is formed
+ * before it is scaled and has to be finite in fp32.  The results are the same
+ * bits on every run of a shape.  M, d_M, T and d_T as in et_splitk_gemm and
+ * et_moe_layer.  Errors as et_moe_layer.
+ * ---------------------------------------------------------------------- */
+int et_w4_quantize(const void* w, void* q, void* scale, int E, int N, int K, int group,
+                   void* stream);
+
+int et_w4_dequantize(const void* q, const void* scale, void* w, int E, int N, int K, int group,
+                     void* stream);
+
+size_t et_w4_gemv_workspace_bytes(int M_max, int N, int K, int group);
+
+int et_w4_gemv(const void* X, const void* q, const void* scale, void* Y, int M,
+               const int32_t* d_M, int M_max, int N, int K, int group, void* workspace,
+               size_t workspace_bytes, void* stream);
+
+size_t et_w4_experts_workspace_bytes(int T_max, int H, int F, int E, int k, int group);
+
+int et_w4_experts(const void* x, const int32_t* topk_idx, const float* topk_w,
+                  const void* q_gate, const void* s_gate, const void* q_up, const void* s_up,
+                  const void* q_down, const void* s_down, void* out, int T, const int32_t* d_T,
+                  int T_max, int H, int F, int E, int k, int group, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Status of the device side.  Synchronises `stream`, then copies the sticky
  * status word of `workspace` to *code_out / *detail_out (host pointers).
  * detail identifies where a wait ran out.  For tests and diagnostics only.

@@ -15,8 +15,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libetmoe.so")
-SOURCES = ["etmoe_api.cu", "moe_kernel.cu", "splitk_kernel.cu", "mlp_kernel.cu"]
-HEADERS = ["et_device.cuh", "et_gemm.cuh", "et_layout.h"]
+SOURCES = ["etmoe_api.cu", "moe_kernel.cu", "splitk_kernel.cu", "mlp_kernel.cu", "router_ops.cu",
+           "norm_ops.cu", "w4_ops.cu"]
+HEADERS = ["et_api.h", "et_device.cuh", "et_gemm.cuh", "et_layout.h", "ops_device.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -1,0 +1,65 @@
+// et_api.h -- host-side helpers shared by the translation units that hold C
+// entry points: the thread's error string, the current device, workspace checks.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+
+#include <string>
+#include <utility>
+
+#include "et_layout.h"
+
+namespace et {
+
+constexpr int kApiMaxDevices = 64;
+
+// Defined in etmoe_api.cu.
+void api_clear_error();
+int api_fail(int code, const std::string& msg);
+int api_fail_cuda(cudaError_t e, const char* what);
+int api_device(int* dev, int* sms);  // current device (sm_103a checked) and its SM count
+int api_check_ws(const void* ws, size_t have, size_t need);
+
+inline bool api_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// Runs a C entry point's body: clears the thread's error string first, and no
+// C++ exception (an error message that cannot be allocated) leaves the call.
+template <class F>
+int api_entry(F&& body) noexcept {
+    try {
+        api_clear_error();
+        return body();
+    } catch (...) {
+        return ET_ERR_CUDA;
+    }
+}
+
+// One-time cudaFuncSetAttribute(MaxDynamicSharedMemorySize) of a kernel on each
+// device; two threads that meet here both set the same value.
+struct SmemOptIn {
+    bool done[kApiMaxDevices] = {};
+};
+template <class K>
+cudaError_t api_smem_opt_in(SmemOptIn& st, int dev, K kernel, int bytes) {
+    if (__atomic_load_n(&st.done[dev], __ATOMIC_ACQUIRE)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) __atomic_store_n(&st.done[dev], true, __ATOMIC_RELEASE);
+    return e;
+}
+
+// One launch; the error is this launch's own (cudaGetLastError could return an
+// older one of the calling program).
+template <class... P, class... A>
+cudaError_t api_launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, void* stream,
+                       A&&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+}  // namespace et

@@ -8,6 +8,7 @@
 #include <mutex>
 #include <string>
 
+#include "et_api.h"
 #include "et_gemm.cuh"
 
 namespace et {
@@ -297,9 +298,30 @@ int check_ws(void* ws, size_t have, size_t need) {
 
 }  // namespace
 
+// The helpers of et_api.h, for the translation units with their own entry points.
+namespace et {
+
+void api_clear_error() { g_last_error.clear(); }
+int api_fail(int code, const std::string& msg) { return fail(code, msg); }
+int api_fail_cuda(cudaError_t e, const char* what) { return fail_cuda(e, what); }
+
+int api_device(int* dev, int* sms) {
+    static_assert(kApiMaxDevices == kMaxDevices, "one device table size");
+    DeviceState* st = nullptr;
+    const int rc = device_state(&st, dev);
+    if (rc == ET_OK) *sms = st->sms;
+    return rc;
+}
+
+int api_check_ws(const void* ws, size_t have, size_t need) {
+    return check_ws(const_cast<void*>(ws), have, need);
+}
+
+}  // namespace et
+
 extern "C" {
 
-int et_version(void) { return 100; }
+int et_version(void) { return 200; }
 
 const char* et_last_error_string(void) { return g_last_error.c_str(); }
 

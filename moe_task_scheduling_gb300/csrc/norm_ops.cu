@@ -1,0 +1,580 @@
+// norm_ops.cu -- the norms either side of a block with its gate and residual
+// scale, in one pass, and their gradient.
+//
+//   n = RMSNorm(y) * gamma_post (or y);  z = x + scale * gate * n;
+//   x_hat = RMSNorm(z) * gamma_pre
+#include <cmath>
+
+#include "../../include/etmoe.h"
+#include "et_api.h"
+#include "ops_device.cuh"
+
+namespace et {
+namespace {
+
+enum GateKind { kGateNone = 0, kGateChannel = 1, kGateToken = 2, kGateFull = 3 };
+
+constexpr int kNormHMax = 16384;
+constexpr int kNormParts = 304;  // most CTAs of the backward kernel = rows of partial sums
+
+struct NormArgs {
+    const bf16* x;           // [T, H]
+    const bf16* y;           // [T, H] or null (z = x)
+    const bf16* gamma_post;  // [H] or null
+    const void* gate;        // bf16 [H], fp32 [T], bf16 [T, H] or null
+    const bf16* gamma_pre;   // [H] or null
+    float scale, eps;
+    int gate_kind;
+    const int32_t* d_T;
+    int T_host, T_max, H;
+    EtHeader* hdr;
+    bf16* x_out;             // [T, H] or null
+    bf16* x_hat;             // [T, H] or null
+    // backward
+    const bf16* d_x_out;     // [T, H] or null
+    const bf16* d_x_hat;     // [T, H] or null
+    bf16* dx;
+    bf16* dy;
+    bf16* d_gate_full;       // [T, H]
+    float* d_gate_token;     // [T]
+    float* part;             // [kNormParts][3][H]: d_gamma_post, d_gamma_pre, d_gate per channel
+};
+
+// Eight consecutive bf16 of a row, packed.
+struct Vec8 {
+    uint32_t u[4];
+    __device__ __forceinline__ float operator[](int i) const {
+        return (i & 1) ? bf_hi(u[i >> 1]) : bf_lo(u[i >> 1]);
+    }
+};
+
+// Columns [c, c + 8) of a row of H.  VEC: one 16-byte access (H a multiple of 8
+// and the tensors 16-byte aligned); else element by element, for any H.
+template <bool VEC>
+__device__ __forceinline__ Vec8 load8(const bf16* row, int c, int H) {
+    Vec8 v{};
+    if (VEC) {
+        if (c < H) {
+            const uint4 q = *reinterpret_cast<const uint4*>(row + c);
+            v.u[0] = q.x; v.u[1] = q.y; v.u[2] = q.z; v.u[3] = q.w;
+        }
+    } else {
+        const uint16_t* r = reinterpret_cast<const uint16_t*>(row);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < H) v.u[i >> 1] |= static_cast<uint32_t>(r[c + i]) << (16 * (i & 1));
+    }
+    return v;
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(bf16* row, int c, int H, const float* f) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
+    if (VEC) {
+        if (c < H) *reinterpret_cast<uint4*>(row + c) = make_uint4(u[0], u[1], u[2], u[3]);
+    } else {
+        uint16_t* r = reinterpret_cast<uint16_t*>(row);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < H) r[c + i] = static_cast<uint16_t>(u[i >> 1] >> (16 * (i & 1)));
+    }
+}
+
+// Sum over the row's threads, the same bits in every one of them.  ROW: the
+// whole CTA holds one row; else a warp does.  Consecutive sums alternate
+// between two slots (n counts them), so one barrier a sum is enough: who has
+// passed the next sum's barrier knows that all have read this one.
+template <bool ROW>
+__device__ __forceinline__ float row_sum(float v, float (*red)[32], int& n) {
+    v = warp_sum(v);
+    if (ROW) {
+        const int slot = n++ & 1;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        if (lane == 0) red[slot][warp] = v;
+        __syncthreads();
+        v = warp_sum(lane < static_cast<int>(blockDim.x >> 5) ? red[slot][lane] : 0.0f);
+    }
+    return v;
+}
+
+// Gate values of columns [c, c + 8) of row t.
+template <bool VEC>
+__device__ __forceinline__ void gate8(const NormArgs& p, int t, int c, float* g) {
+    if (p.gate_kind == kGateNone) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = 1.0f;
+    } else if (p.gate_kind == kGateToken) {
+        const float v = static_cast<const float*>(p.gate)[t];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = v;
+    } else {
+        const bf16* row = static_cast<const bf16*>(p.gate) +
+                          (p.gate_kind == kGateFull ? static_cast<size_t>(t) * p.H : 0);
+        const Vec8 v = load8<VEC>(row, c, p.H);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = v[i];
+    }
+}
+
+// V vectors of 8 columns a thread; ROW: one row a CTA, else one row a warp.
+template <int V, bool VEC, bool ROW>
+__global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormArgs p) {
+    __shared__ float red[2][32];
+    int sums = 0;
+    bool ok;
+    const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
+    const int H = p.H;
+    const int width = ROW ? blockDim.x : 32;
+    const int lane = ROW ? threadIdx.x : threadIdx.x & 31;
+    const int rows_cta = ROW ? 1 : blockDim.x >> 5;
+    for (int t = blockIdx.x * rows_cta + (ROW ? 0 : threadIdx.x >> 5); t < T; t += gridDim.x * rows_cta) {
+        const size_t off = static_cast<size_t>(t) * H;
+        float z[V][8];
+        Vec8 yv[V];
+        float ss = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = (j * width + lane) * 8;
+            const Vec8 xv = load8<VEC>(p.x + off, c, H);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[j][i] = xv[i];
+            yv[j] = p.y ? load8<VEC>(p.y + off, c, H) : Vec8{};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss += yv[j][i] * yv[j][i];
+        }
+        float ry = 1.0f;
+        if (p.y && p.gamma_post) ry = 1.0f / sqrtf(row_sum<ROW>(ss, red, sums) / H + p.eps);
+        float zz = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = (j * width + lane) * 8;
+            if (p.y && c < H) {
+                float g[8];
+                gate8<VEC>(p, t, c, g);
+                const Vec8 gp = p.gamma_post ? load8<VEC>(p.gamma_post, c, H) : Vec8{};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float n = p.gamma_post ? yv[j][i] * ry * gp[i] : yv[j][i];
+                    z[j][i] += p.scale * g[i] * n;
+                }
+                if (!VEC)  // columns past H hold no value (a per-token gate is not zero there)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) z[j][i] = c + i < H ? z[j][i] : 0.0f;
+            }
+            if (p.x_out && c < H) store8<VEC>(p.x_out + off, c, H, z[j]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) zz += z[j][i] * z[j][i];
+        }
+        if (p.x_hat) {
+            const float rz = 1.0f / sqrtf(row_sum<ROW>(zz, red, sums) / H + p.eps);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int c = (j * width + lane) * 8;
+                if (c < H) {
+                    const Vec8 gp = load8<VEC>(p.gamma_pre, c, H);
+                    float o[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i] = z[j][i] * rz * gp[i];
+                    store8<VEC>(p.x_hat + off, c, H, o);
+                }
+            }
+        }
+    }
+}
+
+// The gradient.  A row's statistics are recomputed from x and y (they are read
+// anyway).  The parameter gradients are summed over this CTA's rows in
+// registers, thread by thread for its own columns, then over CTAs by
+// norm_sum_kernel in a fixed order.
+template <int V, bool VEC, bool ROW>
+__global__ void __launch_bounds__(V > 1 ? 1024 : 512) norm_bwd_kernel(const NormArgs p) {
+    __shared__ float red[2][32];
+    int sums = 0;
+    extern __shared__ float acc_sm[];  // !ROW: [warps][3][256]
+    bool ok;
+    int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
+    const int H = p.H;
+    const int width = ROW ? blockDim.x : 32;
+    const int lane = ROW ? threadIdx.x : threadIdx.x & 31;
+    const int rows_cta = ROW ? 1 : blockDim.x >> 5;
+    float a_post[V][8], a_pre[V][8], a_gate[V][8];
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a_post[j][i] = a_pre[j][i] = a_gate[j][i] = 0.0f;
+
+    for (int t = blockIdx.x * rows_cta + (ROW ? 0 : threadIdx.x >> 5); t < T; t += gridDim.x * rows_cta) {
+        const size_t off = static_cast<size_t>(t) * H;
+        Vec8 xv[V], yv[V], dz[V], dh[V];
+        float ss = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = (j * width + lane) * 8;
+            xv[j] = load8<VEC>(p.x + off, c, H);
+            yv[j] = p.y ? load8<VEC>(p.y + off, c, H) : Vec8{};
+            dz[j] = p.d_x_out ? load8<VEC>(p.d_x_out + off, c, H) : Vec8{};
+            dh[j] = p.d_x_hat ? load8<VEC>(p.d_x_hat + off, c, H) : Vec8{};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss += yv[j][i] * yv[j][i];
+        }
+        const bool post = p.y && p.gamma_post;
+        float ry = 1.0f;
+        if (post) ry = 1.0f / sqrtf(row_sum<ROW>(ss, red, sums) / H + p.eps);
+        // z, and with it the statistics of the second norm and sum(d_x_hat gamma_pre z)
+        float z[V][8], zz = 0.0f, az = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = (j * width + lane) * 8;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[j][i] = xv[j][i];
+            if (c < H) {
+                if (p.y) {
+                    float g[8];
+                    gate8<VEC>(p, t, c, g);
+                    const Vec8 gp = post ? load8<VEC>(p.gamma_post, c, H) : Vec8{};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        z[j][i] += p.scale * g[i] * (post ? yv[j][i] * ry * gp[i] : yv[j][i]);
+                    if (!VEC)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) z[j][i] = c + i < H ? z[j][i] : 0.0f;
+                }
+                if (p.d_x_hat) {
+                    const Vec8 gp = load8<VEC>(p.gamma_pre, c, H);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        zz += z[j][i] * z[j][i];
+                        az += dh[j][i] * gp[i] * z[j][i];
+                    }
+                }
+            }
+        }
+        float rz = 0.0f, k2 = 0.0f;
+        if (p.d_x_hat) {
+            rz = 1.0f / sqrtf(row_sum<ROW>(zz, red, sums) / H + p.eps);
+            k2 = row_sum<ROW>(az, red, sums) / H * rz * rz * rz;
+        }
+        // d z, the parameter gradients, and sum(d n gamma_post y)
+        float by = 0.0f, dgt = 0.0f;
+        float d[V][8];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = (j * width + lane) * 8;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[j][i] = 0.0f;
+            if (c < H) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[j][i] = dz[j][i];
+                if (p.d_x_hat) {
+                    const Vec8 gp = load8<VEC>(p.gamma_pre, c, H);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        d[j][i] += rz * (dh[j][i] * gp[i]) - z[j][i] * k2;
+                        a_pre[j][i] += dh[j][i] * (z[j][i] * rz);
+                    }
+                }
+                store8<VEC>(p.dx + off, c, H, d[j]);
+                if (p.y) {
+                    float g[8], dgf[8];
+                    gate8<VEC>(p, t, c, g);
+                    const Vec8 gp = post ? load8<VEC>(p.gamma_post, c, H) : Vec8{};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float u = yv[j][i] * ry;  // the normalised value
+                        const float n = post ? u * gp[i] : yv[j][i];
+                        dgf[i] = p.scale * n * d[j][i];
+                        d[j][i] *= p.scale * g[i];  // d n
+                        a_post[j][i] += d[j][i] * u;
+                        if (post) {
+                            d[j][i] *= gp[i];
+                            by += d[j][i] * yv[j][i];
+                        }
+                        a_gate[j][i] += dgf[i];
+                        dgt += dgf[i];
+                    }
+                    if (p.d_gate_full) store8<VEC>(p.d_gate_full + off, c, H, dgf);
+                }
+            }
+        }
+        if (p.y) {
+            float k1 = 0.0f;
+            if (post) k1 = row_sum<ROW>(by, red, sums) / H * ry * ry * ry;
+            if (p.d_gate_token) {
+                dgt = row_sum<ROW>(dgt, red, sums);
+                if (lane == 0) p.d_gate_token[t] = dgt;
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int c = (j * width + lane) * 8;
+                if (c < H) {
+                    float o[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i] = post ? ry * d[j][i] - yv[j][i] * k1 : d[j][i];
+                    store8<VEC>(p.dy + off, c, H, o);
+                }
+            }
+        }
+    }
+
+    if (!ok) return;
+    float* part = p.part + static_cast<size_t>(blockIdx.x) * 3 * H;
+    if (ROW) {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = (j * width + lane) * 8 + i;
+                if (c < H) {
+                    part[c] = a_post[j][i];
+                    part[H + c] = a_pre[j][i];
+                    part[2 * H + c] = a_gate[j][i];
+                }
+            }
+    } else {  // one row a warp (H <= 256): the CTA's warps in order
+        const int warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float* a = acc_sm + warp * 768 + lane * 8 + i;
+            a[0] = a_post[0][i];
+            a[256] = a_pre[0][i];
+            a[512] = a_gate[0][i];
+        }
+        __syncthreads();
+        for (int o = threadIdx.x; o < 3 * H; o += blockDim.x) {
+            const int arr = o / H, c = o - arr * H;
+            float s = 0.0f;
+            for (int w = 0; w < nwarps; ++w) s += acc_sm[w * 768 + arr * 256 + c];
+            part[o] = s;
+        }
+    }
+}
+
+struct NormSumArgs {
+    const float* part;
+    float* out[3];  // d_gamma_post, d_gamma_pre, d_gate; null: not wanted
+    int H, parts;
+    const int32_t* d_T;
+    int T_max;
+};
+
+// Column sums of the partial rows: 32 columns x 8 row groups a CTA.
+__global__ void __launch_bounds__(256) norm_sum_kernel(const NormSumArgs p) {
+    __shared__ float red[8][33];
+    if (p.d_T && (*p.d_T < 0 || *p.d_T > p.T_max)) return;
+    float* out = p.out[blockIdx.y];
+    if (!out) return;
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), grp = threadIdx.x >> 5;
+    float s = 0.0f;
+    if (c < p.H)
+        for (int g = grp; g < p.parts; g += 8) s += p.part[(static_cast<size_t>(g) * 3 + blockIdx.y) * p.H + c];
+    red[grp][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (grp == 0 && c < p.H) {
+        s = 0.0f;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) s += red[g][threadIdx.x];
+        out[c] = s;
+    }
+}
+
+size_t norm_ws_bytes(int T_max, int H) {
+    const size_t parts = T_max < kNormParts ? T_max : kNormParts;
+    return (kHeaderBytes + parts * 3 * H * sizeof(float) + 255) / 256 * 256;
+}
+
+bool norm_shape_ok(int T_max, int H, std::string* why) {
+    if (T_max < 1 || T_max > (1 << 24)) { *why = "T_max must be in [1, 2^24]"; return false; }
+    if (H < 1 || H > kNormHMax) { *why = "H must be in [1, 16384]"; return false; }
+    return true;
+}
+
+// Checks what both directions share.
+int norm_check(const void* x, const void* y, const void* gamma_post, const void* gate, int gate_kind,
+               float scale, const void* gamma_pre, float eps, int T, const int32_t* d_T, int T_max, int H) {
+    std::string why;
+    if (!norm_shape_ok(T_max, H, &why)) return api_fail(ET_ERR_UNSUPPORTED, why);
+    if (!x) return api_fail(ET_ERR_INVALID, "x must be non-NULL");
+    if (gate_kind < kGateNone || gate_kind > kGateFull)
+        return api_fail(ET_ERR_INVALID, "gate_kind must be in [0, 3]");
+    if ((gate_kind == kGateNone) != (gate == nullptr))
+        return api_fail(ET_ERR_INVALID, "gate must be given exactly when gate_kind is not 0");
+    if (!y && (gamma_post || gate)) return api_fail(ET_ERR_INVALID, "gamma_post and gate need y");
+    if (!(eps > 0.0f) || !std::isfinite(eps)) return api_fail(ET_ERR_INVALID, "eps must be > 0 and finite");
+    if (!std::isfinite(scale)) return api_fail(ET_ERR_INVALID, "scale must be finite");
+    const void* need2[] = {x, y, gamma_post, gamma_pre};
+    for (const void* q : need2)
+        if (!api_aligned(q, 2)) return api_fail(ET_ERR_INVALID, "tensors must be aligned to their element size");
+    if (!api_aligned(gate, gate_kind == kGateToken ? 4 : 2) || !api_aligned(d_T, 4))
+        return api_fail(ET_ERR_INVALID, "tensors must be aligned to their element size");
+    if (!d_T && (T < 0 || T > T_max)) return api_fail(ET_ERR_INVALID, "T must be in [0, T_max]");
+    return ET_OK;
+}
+
+// 16-byte accesses: H a multiple of 8 and every bf16 tensor 16-byte aligned.
+bool norm_vec(int H, std::initializer_list<const void*> ps) {
+    if (H % 8) return false;
+    for (const void* q : ps)
+        if (!api_aligned(q, 16)) return false;
+    return true;
+}
+
+// Threads of a row: one vector of 8 columns each up to `most`, then two.
+int norm_threads(int H, int most) {
+    const int vecs = (H + 7) / 8;
+    int t = (vecs + 31) / 32 * 32;
+    if (t > most) t = ((vecs + 1) / 2 + 31) / 32 * 32;
+    return t;
+}
+
+template <bool VEC>
+cudaError_t launch_fwd(const NormArgs& a, int rows, int sms, void* stream) {
+    if (a.H <= 256) {
+        const int warps = rows < 8 ? rows : 8;
+        int grid = (rows + warps - 1) / warps;
+        grid = grid < 8 * sms ? grid : 8 * sms;
+        return api_launch(norm_fwd_kernel<1, VEC, false>, grid, warps * 32, 0, stream, a);
+    }
+    const int th = norm_threads(a.H, 1024);
+    const int most = sms * (2048 / th < 32 ? 2048 / th : 32);
+    const int grid = rows < most ? rows : most;
+    if (th * 8 >= a.H) return api_launch(norm_fwd_kernel<1, VEC, true>, grid, th, 0, stream, a);
+    return api_launch(norm_fwd_kernel<2, VEC, true>, grid, th, 0, stream, a);
+}
+
+// The grid is also the number of partial rows that norm_sum_kernel reads.
+template <bool VEC>
+cudaError_t launch_bwd(const NormArgs& a, int rows, int parts_max, int* parts, void* stream) {
+    if (a.H <= 256) {
+        const int warps = 8;
+        const int need = (rows + warps - 1) / warps;
+        *parts = need < parts_max ? need : parts_max;
+        return api_launch(norm_bwd_kernel<1, VEC, false>, *parts, warps * 32, warps * 768 * sizeof(float),
+                          stream, a);
+    }
+    *parts = rows < parts_max ? rows : parts_max;
+    const int th = norm_threads(a.H, 512);
+    if (th * 8 >= a.H) return api_launch(norm_bwd_kernel<1, VEC, true>, *parts, th, 0, stream, a);
+    return api_launch(norm_bwd_kernel<2, VEC, true>, *parts, th, 0, stream, a);
+}
+
+}  // namespace
+}  // namespace et
+
+using namespace et;
+
+extern "C" {
+
+size_t et_block_norm_workspace_bytes(int T_max, int H) {
+    if (T_max < 1 || T_max > (1 << 24) || H < 1 || H > kNormHMax) return 0;
+    return norm_ws_bytes(T_max, H);
+}
+
+int et_block_norm(const void* x, const void* y, const void* gamma_post, const void* gate,
+                  int gate_kind, float scale, const void* gamma_pre, float eps, void* x_out,
+                  void* x_hat, int T, const int32_t* d_T, int T_max, int H, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+    return api_entry([&]() -> int {
+        int rc = norm_check(x, y, gamma_post, gate, gate_kind, scale, gamma_pre, eps, T, d_T, T_max, H);
+        if (rc) return rc;
+        if (!x_out && !x_hat) return api_fail(ET_ERR_INVALID, "x_out or x_hat must be given");
+        if ((x_hat == nullptr) != (gamma_pre == nullptr))
+            return api_fail(ET_ERR_INVALID, "x_hat and gamma_pre go together");
+        if (!api_aligned(x_out, 2) || !api_aligned(x_hat, 2))
+            return api_fail(ET_ERR_INVALID, "tensors must be aligned to their element size");
+        if ((rc = api_check_ws(workspace, workspace_bytes, kHeaderBytes))) return rc;
+        if (!d_T && T == 0) return ET_OK;
+        int dev = 0, sms = 0;
+        if ((rc = api_device(&dev, &sms))) return rc;
+        NormArgs a{};
+        a.x = static_cast<const bf16*>(x);
+        a.y = static_cast<const bf16*>(y);
+        a.gamma_post = static_cast<const bf16*>(gamma_post);
+        a.gate = gate;
+        a.gamma_pre = static_cast<const bf16*>(gamma_pre);
+        a.scale = scale;
+        a.eps = eps;
+        a.gate_kind = gate_kind;
+        a.d_T = d_T;
+        a.T_host = T;
+        a.T_max = T_max;
+        a.H = H;
+        a.hdr = static_cast<EtHeader*>(workspace);
+        a.x_out = static_cast<bf16*>(x_out);
+        a.x_hat = static_cast<bf16*>(x_hat);
+        const int rows = d_T ? T_max : T;
+        const bool vec = norm_vec(H, {x, y, gamma_post, gate_kind == kGateToken ? nullptr : gate,
+                                      gamma_pre, x_out, x_hat});
+        const cudaError_t e = vec ? launch_fwd<true>(a, rows, sms, stream) : launch_fwd<false>(a, rows, sms, stream);
+        if (e != cudaSuccess) return api_fail_cuda(e, "launch of the block norm kernel");
+        return ET_OK;
+    });
+}
+
+int et_block_norm_bwd(const void* x, const void* y, const void* gamma_post, const void* gate,
+                      int gate_kind, float scale, const void* gamma_pre, float eps,
+                      const void* d_x_out, const void* d_x_hat, void* dx, void* dy,
+                      float* d_gamma_post, float* d_gamma_pre, void* d_gate, int T,
+                      const int32_t* d_T, int T_max, int H, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+    return api_entry([&]() -> int {
+        int rc = norm_check(x, y, gamma_post, gate, gate_kind, scale, gamma_pre, eps, T, d_T, T_max, H);
+        if (rc) return rc;
+        if (!dx) return api_fail(ET_ERR_INVALID, "dx must be non-NULL");
+        if (!d_x_out && !d_x_hat) return api_fail(ET_ERR_INVALID, "d_x_out or d_x_hat must be given");
+        if (d_x_hat && !gamma_pre) return api_fail(ET_ERR_INVALID, "d_x_hat needs gamma_pre");
+        if ((y == nullptr) != (dy == nullptr)) return api_fail(ET_ERR_INVALID, "y and dy go together");
+        if ((d_gamma_post && !gamma_post) || (d_gamma_pre && !gamma_pre) || (d_gate && !gate))
+            return api_fail(ET_ERR_INVALID, "a parameter's gradient needs the parameter");
+        const void* need2[] = {d_x_out, d_x_hat, dx, dy};
+        for (const void* q : need2)
+            if (!api_aligned(q, 2)) return api_fail(ET_ERR_INVALID, "tensors must be aligned to their element size");
+        if (!api_aligned(d_gamma_post, 4) || !api_aligned(d_gamma_pre, 4) ||
+            !api_aligned(d_gate, gate_kind == kGateFull ? 2 : 4))
+            return api_fail(ET_ERR_INVALID, "tensors must be aligned to their element size");
+        if ((rc = api_check_ws(workspace, workspace_bytes, norm_ws_bytes(T_max, H)))) return rc;
+        int dev = 0, sms = 0;
+        if ((rc = api_device(&dev, &sms))) return rc;
+        NormArgs a{};
+        a.x = static_cast<const bf16*>(x);
+        a.y = static_cast<const bf16*>(y);
+        a.gamma_post = static_cast<const bf16*>(gamma_post);
+        a.gate = gate;
+        a.gamma_pre = static_cast<const bf16*>(gamma_pre);
+        a.scale = scale;
+        a.eps = eps;
+        a.gate_kind = gate_kind;
+        a.d_T = d_T;
+        a.T_host = T;
+        a.T_max = T_max;
+        a.H = H;
+        a.hdr = static_cast<EtHeader*>(workspace);
+        a.d_x_out = static_cast<const bf16*>(d_x_out);
+        a.d_x_hat = static_cast<const bf16*>(d_x_hat);
+        a.dx = static_cast<bf16*>(dx);
+        a.dy = static_cast<bf16*>(dy);
+        a.d_gate_full = gate_kind == kGateFull ? static_cast<bf16*>(d_gate) : nullptr;
+        a.d_gate_token = gate_kind == kGateToken ? static_cast<float*>(d_gate) : nullptr;
+        a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
+        const int parts_max = T_max < kNormParts ? T_max : kNormParts;
+        const int rows = d_T ? T_max : T;
+        int parts = 0;
+        if (rows > 0) {
+            const bool vec = norm_vec(H, {x, y, gamma_post, gate_kind == kGateToken ? nullptr : gate, gamma_pre,
+                                          d_x_out, d_x_hat, dx, dy, a.d_gate_full});
+            const cudaError_t e = vec ? launch_bwd<true>(a, rows, parts_max, &parts, stream)
+                                      : launch_bwd<false>(a, rows, parts_max, &parts, stream);
+            if (e != cudaSuccess) return api_fail_cuda(e, "launch of the block norm's backward kernel");
+        }
+        float* d_gate_channel = gate_kind == kGateChannel ? static_cast<float*>(d_gate) : nullptr;
+        if (d_gamma_post || d_gamma_pre || d_gate_channel) {
+            const NormSumArgs s{a.part, {d_gamma_post, d_gamma_pre, d_gate_channel}, H, parts, d_T, T_max};
+            const cudaError_t e = api_launch(norm_sum_kernel, dim3((H + 31) / 32, 3), 256, 0, stream, s);
+            if (e != cudaSuccess) return api_fail_cuda(e, "launch of the block norm's parameter sums");
+        }
+        return ET_OK;
+    });
+}
+
+}  // extern "C"

@@ -1,0 +1,412 @@
+// router_ops.cu -- the router's selection over given logits, with the balance
+// and z losses of a training step, and the gradient of all of them.
+#include <cmath>
+
+#include "../../include/etmoe.h"
+#include "et_api.h"
+#include "ops_device.cuh"
+
+namespace et {
+namespace {
+
+constexpr int kRouterWarpsMax = 32;
+constexpr int kRouterEMax = 256;
+constexpr int kRouterParts = 152;  // most CTAs of the forward kernel = rows of partial sums
+
+struct RouterArgs {
+    const float* logits;     // [T, E]
+    const uint8_t* mask;     // [T] or null
+    int32_t* idx;            // [T, k]
+    float* w;                // [T, k]
+    int32_t* counts;         // [E]
+    int32_t* n_routed;       // [1]
+    float* mean_prob;        // [E]
+    float* losses;           // [2]
+    const int32_t* d_T;
+    int T_host, T_max, E, k;
+    EtHeader* hdr;
+    float* part_p;           // [kRouterParts, E]
+    int32_t* part_c;         // [kRouterParts, E]
+    float* part_z;           // [kRouterParts]
+    int32_t* part_n;         // [kRouterParts]
+};
+
+// Order-preserving key of a logit: -0.0 ties with +0.0, NaN ranks above all
+// (it then shows in the weights and losses).  Every key is > 0.
+__device__ __forceinline__ uint32_t logit_key(float v) {
+    if (v != v) return 0xffffffffu;
+    const uint32_t b = __float_as_uint(v == 0.0f ? 0.0f : v);
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+// One row a warp, expert e = lane + 32 i in register i.  The k rounds of the
+// selection also give the row's largest logit, so the softmax needs no max
+// pass.  Sums over rows: per warp in registers, per CTA in shared memory, over
+// CTAs by the last one to finish -- each in a fixed order, so that losses and
+// mean probabilities are the same bits on every run.
+template <int EPL>
+__global__ void __launch_bounds__(kRouterWarpsMax * 32) router_topk_kernel(const RouterArgs p) {
+    extern __shared__ float sm[];
+    __shared__ int hist[kRouterEMax];
+    __shared__ float zsum[kRouterWarpsMax];
+    __shared__ int nsum[kRouterWarpsMax];
+    __shared__ int last;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+    const int E = p.E, k = p.k;
+    bool ok;
+    const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
+    if (!ok) return;
+    for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
+    __syncthreads();
+
+    float accp[EPL], accz = 0.0f;
+    int accn = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) accp[i] = 0.0f;
+
+    for (int t = blockIdx.x * nwarps + warp; t < T; t += gridDim.x * nwarps) {
+        const float* L = p.logits + static_cast<size_t>(t) * E;
+        float v[EPL];
+        uint32_t key[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const int e = lane + 32 * i;
+            v[i] = e < E ? L[e] : -INFINITY;
+            key[i] = e < E ? logit_key(v[i]) : 0u;
+        }
+        float myL = -INFINITY;
+        int myE = -1;
+#pragma unroll 1
+        for (int j = 0; j < k; ++j) {
+            uint32_t bk = key[0];
+            int bi = 0;
+#pragma unroll
+            for (int i = 1; i < EPL; ++i)
+                if (key[i] > bk) { bk = key[i]; bi = i; }
+            const uint32_t kmax = __reduce_max_sync(0xffffffffu, bk);
+            const uint32_t e = __reduce_min_sync(
+                0xffffffffu, bk == kmax ? static_cast<uint32_t>(lane + 32 * bi) : 0xffffffffu);
+            float Lw = 0.0f;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                if (static_cast<uint32_t>(lane + 32 * i) == e) { key[i] = 0u; Lw = v[i]; }
+            Lw = __shfl_sync(0xffffffffu, Lw, e & 31);
+            if (lane == j) { myL = Lw; myE = static_cast<int>(e); }
+        }
+        const float L0 = __shfl_sync(0xffffffffu, myL, 0);
+        const bool live = (!p.mask || p.mask[t] != 0) && !(L0 == -INFINITY);
+        const bool on = live && lane < k && !(myL == -INFINITY);
+        const float ex = on ? expf(myL - L0) : 0.0f;
+        const float z = warp_sum(ex);
+        if (lane < k) {
+            p.idx[static_cast<size_t>(t) * k + lane] = on ? myE : -1;
+            p.w[static_cast<size_t>(t) * k + lane] = on ? ex / z : 0.0f;
+        }
+        if (on) atomicAdd(&hist[myE], 1);
+        if (live) {
+            float pe[EPL], s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                pe[i] = lane + 32 * i < E ? expf(v[i] - L0) : 0.0f;
+                s += pe[i];
+            }
+            s = warp_sum(s);
+            const float inv = 1.0f / s;
+            const float lse = L0 + logf(s);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) accp[i] += pe[i] * inv;
+            accz += lse * lse;
+            ++accn;
+        }
+    }
+
+    // CTA sums, warps in order
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+        if (lane + 32 * i < E) sm[warp * E + lane + 32 * i] = accp[i];
+    if (lane == 0) { zsum[warp] = accz; nsum[warp] = accn; }
+    __syncthreads();
+    const int b = blockIdx.x;
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        float s = 0.0f;
+        for (int w = 0; w < nwarps; ++w) s += sm[w * E + e];
+        p.part_p[b * E + e] = s;
+        p.part_c[b * E + e] = hist[e];
+    }
+    if (threadIdx.x == 0) {
+        float s = 0.0f;
+        int n = 0;
+        for (int w = 0; w < nwarps; ++w) { s += zsum[w]; n += nsum[w]; }
+        p.part_z[b] = s;
+        p.part_n[b] = n;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        const int n = atomicAdd(&p.hdr->exit_count, 1);
+        last = n == static_cast<int>(gridDim.x) - 1;
+        if (last) p.hdr->exit_count = 0;
+        __threadfence();
+    }
+    __syncthreads();
+    if (!last) return;
+
+    // the last CTA: sums over CTAs (fp64: the order is fixed, the length is not)
+    const int G = gridDim.x;
+    double bal = 0.0;
+    __shared__ double red[kRouterWarpsMax];
+    __shared__ int n_all;
+    __shared__ double z_all;
+    if (warp == 0) {
+        int n = 0;
+        double z = 0.0;
+        for (int g = lane; g < G; g += 32) {
+            n += __ldcg(p.part_n + g);
+            z += __ldcg(p.part_z + g);
+        }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) {
+            n += __shfl_xor_sync(0xffffffffu, n, off);
+            z += __shfl_xor_sync(0xffffffffu, z, off);
+        }
+        if (lane == 0) { n_all = n; z_all = z; }
+    }
+    __syncthreads();
+    const double rows = n_all > 0 ? n_all : 1;
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        double s = 0.0;
+        int c = 0;
+        for (int g = 0; g < G; ++g) {
+            s += __ldcg(p.part_p + g * E + e);
+            c += __ldcg(p.part_c + g * E + e);
+        }
+        const double P = s / rows;
+        if (p.counts) p.counts[e] = c;
+        if (p.mean_prob) p.mean_prob[e] = static_cast<float>(P);
+        bal += c / (rows * k) * P;
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) bal += __shfl_xor_sync(0xffffffffu, bal, off);
+    if (lane == 0) red[warp] = bal;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double s = 0.0;
+        for (int w = 0; w < nwarps; ++w) s += red[w];
+        if (p.n_routed) *p.n_routed = n_all;
+        if (p.losses) {
+            p.losses[0] = static_cast<float>(E * s);
+            p.losses[1] = static_cast<float>(z_all / rows);
+        }
+    }
+}
+
+struct RouterBwdArgs {
+    const float* logits;
+    const uint8_t* mask;
+    const int32_t* idx;
+    const float* w;
+    const int32_t* counts;
+    const int32_t* n_routed;
+    const float* d_losses;  // [2] or null
+    const float* d_w;       // [T, k] or null
+    float* d_logits;
+    const int32_t* d_T;
+    int T_host, T_max, E, k;
+    EtHeader* hdr;
+};
+
+// One row a warp; the softmax is recomputed from the logits (4 bytes an entry
+// read, 4 written: storing the probabilities would add as much again).
+template <int EPL>
+__global__ void __launch_bounds__(256) router_bwd_kernel(const RouterBwdArgs p) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+    const int E = p.E, k = p.k;
+    bool ok;
+    const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
+    if (!ok) return;
+    const int n = *p.n_routed;
+    const float rows = n > 0 ? static_cast<float>(n) : 1.0f;
+    const float db = p.d_losses ? p.d_losses[0] : 0.0f;
+    const float dz = p.d_losses ? 2.0f * p.d_losses[1] / rows : 0.0f;
+    float cost[EPL];  // E f_e / n: what a unit of probability on expert e costs
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        const int e = lane + 32 * i;
+        cost[i] = e < E ? static_cast<float>(E) * (static_cast<float>(p.counts[e]) / (rows * k)) / rows : 0.0f;
+    }
+    for (int t = blockIdx.x * nwarps + warp; t < T; t += gridDim.x * nwarps) {
+        const float* L = p.logits + static_cast<size_t>(t) * E;
+        float v[EPL], m = -INFINITY;
+        bool nan = false;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const int e = lane + 32 * i;
+            v[i] = e < E ? L[e] : -INFINITY;
+            m = fmaxf(m, v[i]);
+            nan |= v[i] != v[i];
+        }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        nan = __any_sync(0xffffffffu, nan);
+        const bool live = (!p.mask || p.mask[t] != 0) && (nan || !(m == -INFINITY));
+        float d[EPL];
+        if (live) {
+            float pe[EPL], s = 0.0f, cp = 0.0f;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                pe[i] = lane + 32 * i < E ? expf(v[i] - m) : 0.0f;
+                s += pe[i];
+                cp += pe[i] * cost[i];
+            }
+            s = warp_sum(s);
+            cp = warp_sum(cp) / s;
+            const float inv = 1.0f / s;
+            const float zl = dz * (m + logf(s));
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const float pr = pe[i] * inv;
+                d[i] = db * pr * (cost[i] - cp) + zl * pr;
+            }
+            if (p.d_w) {
+                int e = -1;
+                float w = 0.0f, dw = 0.0f;
+                if (lane < k) {
+                    e = p.idx[static_cast<size_t>(t) * k + lane];
+                    if (e >= 0) {
+                        w = p.w[static_cast<size_t>(t) * k + lane];
+                        dw = p.d_w[static_cast<size_t>(t) * k + lane];
+                    }
+                }
+                const float dot = warp_sum(w * dw);
+                const float ds = w * (dw - dot);
+#pragma unroll 1
+                for (int j = 0; j < k; ++j) {
+                    const int ej = __shfl_sync(0xffffffffu, e, j);
+                    const float dj = __shfl_sync(0xffffffffu, ds, j);
+#pragma unroll
+                    for (int i = 0; i < EPL; ++i)
+                        if (ej == lane + 32 * i) d[i] += dj;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) d[i] = 0.0f;
+        }
+        float* out = p.d_logits + static_cast<size_t>(t) * E;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (lane + 32 * i < E) out[lane + 32 * i] = d[i];
+    }
+}
+
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+
+struct RouterLayout {
+    size_t part_p, part_c, part_z, part_n, total;
+};
+
+RouterLayout router_layout(int E) {
+    RouterLayout L{};
+    size_t off = kHeaderBytes;
+    L.part_p = off;
+    off = align256(off + sizeof(float) * kRouterParts * E);
+    L.part_c = off;
+    off = align256(off + sizeof(int) * kRouterParts * E);
+    L.part_z = off;
+    off = align256(off + sizeof(float) * kRouterParts);
+    L.part_n = off;
+    L.total = align256(off + sizeof(int) * kRouterParts);
+    return L;
+}
+
+bool router_shape_ok(int T_max, int E, int k, std::string* why) {
+    if (T_max < 1 || T_max > (1 << 24)) { *why = "T_max must be in [1, 2^24]"; return false; }
+    if (E < 1 || E > kRouterEMax) { *why = "E must be in [1, 256]"; return false; }
+    if (k < 1 || k > 8 || k > E) { *why = "k must be in [1, min(E, 8)]"; return false; }
+    return true;
+}
+
+int ceil_div_i(int a, int b) { return a / b + (a % b != 0); }
+
+}  // namespace
+}  // namespace et
+
+using namespace et;
+
+extern "C" {
+
+size_t et_router_topk_workspace_bytes(int T_max, int E, int k) {
+    if (T_max < 1 || T_max > (1 << 24) || E < 1 || E > kRouterEMax || k < 1 || k > 8 || k > E) return 0;
+    return router_layout(E).total;
+}
+
+int et_router_topk(const float* logits, const uint8_t* token_mask, int32_t* topk_idx, float* topk_w,
+                   int32_t* expert_counts, int32_t* n_routed, float* mean_prob, float* losses, int T,
+                   const int32_t* d_T, int T_max, int E, int k, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+    return api_entry([&]() -> int {
+        std::string why;
+        if (!router_shape_ok(T_max, E, k, &why)) return api_fail(ET_ERR_UNSUPPORTED, why);
+        if (!logits || !topk_idx || !topk_w)
+            return api_fail(ET_ERR_INVALID, "logits, topk_idx and topk_w must be non-NULL");
+        const void* need4[] = {logits, topk_idx, topk_w, expert_counts, n_routed, mean_prob, losses, d_T};
+        for (const void* q : need4)
+            if (!api_aligned(q, 4)) return api_fail(ET_ERR_INVALID, "tensors must be aligned to their element size");
+        if (!d_T && (T < 0 || T > T_max)) return api_fail(ET_ERR_INVALID, "T must be in [0, T_max]");
+        const RouterLayout L = router_layout(E);
+        int rc = api_check_ws(workspace, workspace_bytes, L.total);
+        if (rc) return rc;
+        int dev = 0, sms = 0;
+        if ((rc = api_device(&dev, &sms))) return rc;
+        uint8_t* ws = static_cast<uint8_t*>(workspace);
+        RouterArgs a{logits, token_mask, topk_idx, topk_w, expert_counts, n_routed, mean_prob, losses,
+                     d_T, T, T_max, E, k, reinterpret_cast<EtHeader*>(ws),
+                     reinterpret_cast<float*>(ws + L.part_p), reinterpret_cast<int32_t*>(ws + L.part_c),
+                     reinterpret_cast<float*>(ws + L.part_z), reinterpret_cast<int32_t*>(ws + L.part_n)};
+        const int rows = d_T ? T_max : (T > 0 ? T : 1);
+        const int warps = rows < kRouterWarpsMax ? rows : kRouterWarpsMax;
+        int grid = ceil_div_i(rows, warps);
+        grid = grid < kRouterParts ? grid : kRouterParts;
+        const size_t smem = sizeof(float) * warps * E;
+        auto kernel = E <= 32 ? router_topk_kernel<1> : E <= 64 ? router_topk_kernel<2>
+                    : E <= 128 ? router_topk_kernel<4> : router_topk_kernel<8>;
+        const cudaError_t e = api_launch(kernel, grid, warps * 32, smem, stream, a);
+        if (e != cudaSuccess) return api_fail_cuda(e, "launch of the router kernel");
+        return ET_OK;
+    });
+}
+
+int et_router_topk_bwd(const float* logits, const uint8_t* token_mask, const int32_t* topk_idx,
+                       const float* topk_w, const int32_t* expert_counts, const int32_t* n_routed,
+                       const float* d_losses, const float* d_topk_w, float* d_logits, int T,
+                       const int32_t* d_T, int T_max, int E, int k, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+    return api_entry([&]() -> int {
+        std::string why;
+        if (!router_shape_ok(T_max, E, k, &why)) return api_fail(ET_ERR_UNSUPPORTED, why);
+        if (!logits || !topk_idx || !topk_w || !expert_counts || !n_routed || !d_logits)
+            return api_fail(ET_ERR_INVALID, "logits, topk_idx, topk_w, expert_counts, n_routed and d_logits "
+                                            "must be non-NULL");
+        const void* need4[] = {logits, topk_idx, topk_w, expert_counts, n_routed, d_losses, d_topk_w, d_logits, d_T};
+        for (const void* q : need4)
+            if (!api_aligned(q, 4)) return api_fail(ET_ERR_INVALID, "tensors must be aligned to their element size");
+        if (!d_T && (T < 0 || T > T_max)) return api_fail(ET_ERR_INVALID, "T must be in [0, T_max]");
+        int rc = api_check_ws(workspace, workspace_bytes, kHeaderBytes);
+        if (rc) return rc;
+        if (!d_T && T == 0) return ET_OK;
+        int dev = 0, sms = 0;
+        if ((rc = api_device(&dev, &sms))) return rc;
+        RouterBwdArgs a{logits, token_mask, topk_idx, topk_w, expert_counts, n_routed, d_losses, d_topk_w,
+                        d_logits, d_T, T, T_max, E, k, static_cast<EtHeader*>(workspace)};
+        const int rows = d_T ? T_max : T;
+        int grid = ceil_div_i(rows, 8);
+        grid = grid < 8 * sms ? grid : 8 * sms;
+        auto kernel = E <= 32 ? router_bwd_kernel<1> : E <= 64 ? router_bwd_kernel<2>
+                    : E <= 128 ? router_bwd_kernel<4> : router_bwd_kernel<8>;
+        const cudaError_t e = api_launch(kernel, grid, 256, 0, stream, a);
+        if (e != cudaSuccess) return api_fail_cuda(e, "launch of the router's backward kernel");
+        return ET_OK;
+    });
+}
+
+}  // extern "C"

@@ -68,6 +68,20 @@ _SIGNATURES = {
                           _sz, _vp, _vp]),
     "et_splitk_noalloc_status": (_i, [_vp, ctypes.POINTER(ctypes.c_int32),
                                       ctypes.POINTER(ctypes.c_int32)]),
+    "et_router_topk_workspace_bytes": (_sz, [_i, _i, _i]),
+    "et_router_topk": (_i, [_vp] * 8 + [_i, _vp] + [_i] * 3 + [_vp, _sz, _vp]),
+    "et_router_topk_bwd": (_i, [_vp] * 9 + [_i, _vp] + [_i] * 3 + [_vp, _sz, _vp]),
+    "et_block_norm_workspace_bytes": (_sz, [_i, _i]),
+    "et_block_norm": (_i, [_vp] * 4 + [_i, ctypes.c_float, _vp, ctypes.c_float, _vp, _vp, _i, _vp,
+                                       _i, _i, _vp, _sz, _vp]),
+    "et_block_norm_bwd": (_i, [_vp] * 4 + [_i, ctypes.c_float, _vp, ctypes.c_float] + [_vp] * 7 +
+                          [_i, _vp, _i, _i, _vp, _sz, _vp]),
+    "et_w4_quantize": (_i, [_vp] * 3 + [_i] * 4 + [_vp]),
+    "et_w4_dequantize": (_i, [_vp] * 3 + [_i] * 4 + [_vp]),
+    "et_w4_gemv_workspace_bytes": (_sz, [_i] * 4),
+    "et_w4_gemv": (_i, [_vp] * 4 + [_i, _vp] + [_i] * 4 + [_vp, _sz, _vp]),
+    "et_w4_experts_workspace_bytes": (_sz, [_i] * 6),
+    "et_w4_experts": (_i, [_vp] * 10 + [_i, _vp] + [_i] * 6 + [_vp, _sz, _vp]),
     "et_status": (_i, [_vp, _vp, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)]),
     "et_reset_status": (_i, [_vp, _vp]),
 }
@@ -314,6 +328,221 @@ def et_mlp_chain(x, gamma, eps, w_gate, w_up, w_down, out, *, B=None, d_B=None, 
     if check:
         _check(rc)
     return rc
+
+
+# ------------------------------------------------------------------ router, norms, 4-bit weights
+#
+# These calls check what the C ABI cannot see: each tensor's type, shape,
+# contiguity and device (ValueError).  They run on the tensors' device, on
+# `stream` or else that device's current stream.
+
+def _args(device, specs):
+    """Device pointers of (name, tensor or None, dtype, shape), each checked.  All must be
+    contiguous CUDA tensors on `device`."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, not {device}")
+    out = []
+    for name, t, dtype, shape in specs:
+        if t is None:
+            out.append(None)
+            continue
+        if t.dtype is not dtype or t.shape != shape:
+            raise ValueError(f"{name} must be {dtype} {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}, not {t.device}")
+        out.append(t.data_ptr())
+    return out
+
+
+def _workspace_args(workspace, device):
+    import torch
+    if workspace is None:
+        raise ValueError("workspace must be given (alloc_workspace)")
+    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+    return workspace.data_ptr(), workspace.numel()
+
+
+def _count_arg(d_n, device):
+    import torch
+    if d_n is None or isinstance(d_n, int):
+        return d_n
+    if d_n.dtype is not torch.int32 or d_n.numel() != 1 or d_n.device != device:
+        raise ValueError(f"a device count must be one int32 on {device}")
+    return d_n.data_ptr()
+
+
+def _call(fn, device, stream, args, check):
+    """fn(*args, stream) with `device` current."""
+    import torch
+    if device.index is None or device.index == torch.cuda.current_device():
+        rc = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _stream(stream))
+    if check:
+        _check(rc)
+    return rc
+
+
+def et_router_topk_workspace_bytes(T_max, E, k) -> int:
+    return load().et_router_topk_workspace_bytes(T_max, E, k)
+
+
+def et_router_topk(logits, topk_idx, topk_w, *, token_mask=None, expert_counts=None, n_routed=None,
+                   mean_prob=None, losses=None, T=None, d_T=None, workspace, stream=None, check=True):
+    """Top-k of logits [T_max, E]: indices, gate weights, counts; losses[0] balance, losses[1] z."""
+    import torch
+    f32, i32 = torch.float32, torch.int32
+    (T_max, E), k, dev = logits.shape, topk_idx.shape[-1], logits.device
+    ptrs = _args(dev, (("logits", logits, f32, (T_max, E)), ("token_mask", token_mask, torch.uint8, (T_max,)),
+                       ("topk_idx", topk_idx, i32, (T_max, k)), ("topk_w", topk_w, f32, (T_max, k)),
+                       ("expert_counts", expert_counts, i32, (E,)), ("n_routed", n_routed, i32, (1,)),
+                       ("mean_prob", mean_prob, f32, (E,)), ("losses", losses, f32, (2,))))
+    return _call(load().et_router_topk, dev, stream,
+                 (*ptrs, T_max if T is None else T, _count_arg(d_T, dev), T_max, E, k,
+                  *_workspace_args(workspace, dev)), check)
+
+
+def et_router_topk_bwd(logits, topk_idx, topk_w, expert_counts, n_routed, d_logits, *, token_mask=None,
+                       d_losses=None, d_topk_w=None, T=None, d_T=None, workspace, stream=None, check=True):
+    """Gradient of et_router_topk's losses (d_losses [2]) and gate weights (d_topk_w [T_max, k])."""
+    import torch
+    f32, i32 = torch.float32, torch.int32
+    (T_max, E), k, dev = logits.shape, topk_idx.shape[-1], logits.device
+    ptrs = _args(dev, (("logits", logits, f32, (T_max, E)), ("token_mask", token_mask, torch.uint8, (T_max,)),
+                       ("topk_idx", topk_idx, i32, (T_max, k)), ("topk_w", topk_w, f32, (T_max, k)),
+                       ("expert_counts", expert_counts, i32, (E,)), ("n_routed", n_routed, i32, (1,)),
+                       ("d_losses", d_losses, f32, (2,)), ("d_topk_w", d_topk_w, f32, (T_max, k)),
+                       ("d_logits", d_logits, f32, (T_max, E))))
+    return _call(load().et_router_topk_bwd, dev, stream,
+                 (*ptrs, T_max if T is None else T, _count_arg(d_T, dev), T_max, E, k,
+                  *_workspace_args(workspace, dev)), check)
+
+
+def et_block_norm_workspace_bytes(T_max, H) -> int:
+    return load().et_block_norm_workspace_bytes(T_max, H)
+
+
+def _gate_kind(gate, T_max, H):
+    """(kind, dtype, shape) of a gate: bf16 [H], fp32 [T_max] or bf16 [T_max, H]."""
+    import torch
+    if gate is None:
+        return 0, None, None
+    if gate.dim() == 2:
+        return 3, torch.bfloat16, (T_max, H)
+    return (2, torch.float32, (T_max,)) if gate.dtype is torch.float32 else (1, torch.bfloat16, (H,))
+
+
+def et_block_norm(x, y, x_out, x_hat, *, gamma_post=None, gate=None, scale=1.0, gamma_pre=None, eps,
+                  T=None, d_T=None, workspace, stream=None, check=True):
+    """x_out = x + scale * gate * RMSNorm(y) * gamma_post and x_hat = RMSNorm(x_out) * gamma_pre."""
+    import torch
+    bf = torch.bfloat16
+    (T_max, H), dev = x.shape, x.device
+    kind, gdt, gsh = _gate_kind(gate, T_max, H)
+    rows = (T_max, H)
+    px, py, pgp, pg, pgr, po, ph = _args(dev, (
+        ("x", x, bf, rows), ("y", y, bf, rows), ("gamma_post", gamma_post, bf, (H,)), ("gate", gate, gdt, gsh),
+        ("gamma_pre", gamma_pre, bf, (H,)), ("x_out", x_out, bf, rows), ("x_hat", x_hat, bf, rows)))
+    return _call(load().et_block_norm, dev, stream,
+                 (px, py, pgp, pg, kind, scale, pgr, eps, po, ph, T_max if T is None else T,
+                  _count_arg(d_T, dev), T_max, H, *_workspace_args(workspace, dev)), check)
+
+
+def et_block_norm_bwd(x, y, d_x_out, d_x_hat, dx, dy, *, gamma_post=None, gate=None, scale=1.0, gamma_pre=None,
+                      eps, d_gamma_post=None, d_gamma_pre=None, d_gate=None, T=None, d_T=None, workspace,
+                      stream=None, check=True):
+    """Gradient of et_block_norm: dx, dy and, where given, the parameters' (fp32; a full gate's bf16)."""
+    import torch
+    bf, f32 = torch.bfloat16, torch.float32
+    (T_max, H), dev = x.shape, x.device
+    kind, gdt, gsh = _gate_kind(gate, T_max, H)
+    rows = (T_max, H)
+    px, py, pgp, pg, pgr, pdo, pdh, pdx, pdy, pdgp, pdgr, pdg = _args(dev, (
+        ("x", x, bf, rows), ("y", y, bf, rows), ("gamma_post", gamma_post, bf, (H,)), ("gate", gate, gdt, gsh),
+        ("gamma_pre", gamma_pre, bf, (H,)), ("d_x_out", d_x_out, bf, rows), ("d_x_hat", d_x_hat, bf, rows),
+        ("dx", dx, bf, rows), ("dy", dy, bf, rows), ("d_gamma_post", d_gamma_post, f32, (H,)),
+        ("d_gamma_pre", d_gamma_pre, f32, (H,)),
+        ("d_gate", d_gate, bf if kind == 3 else f32, gsh)))
+    return _call(load().et_block_norm_bwd, dev, stream,
+                 (px, py, pgp, pg, kind, scale, pgr, eps, pdo, pdh, pdx, pdy, pdgp, pdgr, pdg,
+                  T_max if T is None else T, _count_arg(d_T, dev), T_max, H,
+                  *_workspace_args(workspace, dev)), check)
+
+
+def _w4_weight(q, scale, N, K, E=None):
+    """Specs of one 4-bit weight ([N, K], or E of them) and its group."""
+    import torch
+    lead = () if E is None else (E,)
+    groups = scale.shape[-2] if scale.dim() == 2 + len(lead) else 0
+    group = K // groups if groups and K % groups == 0 else 0
+    return ((q, torch.uint8, lead + (N, K // 2)), (scale, torch.bfloat16, lead + (groups, N))), group
+
+
+def _w4_convert(w, q, scale):
+    import torch
+    dev = w.device
+    E = w.shape[0] if w.dim() == 3 else None
+    N, K = w.shape[-2:]
+    (sq, ss), group = _w4_weight(q, scale, N, K, E)
+    pw, pq, ps = _args(dev, (("w", w, torch.bfloat16, w.shape), ("q", *sq), ("scale", *ss)))
+    return pw, pq, ps, dev, (E or 1, N, K, group)
+
+
+def et_w4_quantize(w, q, scale, *, stream=None, check=True):
+    """bf16 w [N, K] or [E, N, K] -> q uint8 [.., N, K/2] and scale bf16 [.., K/group, N]; the group
+    is K / scale.shape[-2]."""
+    pw, pq, ps, dev, dims = _w4_convert(w, q, scale)
+    return _call(load().et_w4_quantize, dev, stream, (pw, pq, ps, *dims), check)
+
+
+def et_w4_dequantize(q, scale, w, *, stream=None, check=True):
+    """The bf16 values of a 4-bit weight (the inverse of et_w4_quantize's layout)."""
+    pw, pq, ps, dev, dims = _w4_convert(w, q, scale)
+    return _call(load().et_w4_dequantize, dev, stream, (pq, ps, pw, *dims), check)
+
+
+def et_w4_gemv_workspace_bytes(M_max, N, K, group) -> int:
+    return load().et_w4_gemv_workspace_bytes(M_max, N, K, group)
+
+
+def et_w4_gemv(X, q, scale, Y, *, M=None, d_M=None, workspace, stream=None, check=True):
+    """Y = X w^T for up to 64 rows, w in 4 bits (et_w4_quantize's layout)."""
+    import torch
+    (M_max, K), N, dev = X.shape, Y.shape[-1], X.device
+    (sq, ss), group = _w4_weight(q, scale, N, K)
+    ptrs = _args(dev, (("X", X, torch.bfloat16, (M_max, K)), ("q", *sq), ("scale", *ss),
+                       ("Y", Y, torch.bfloat16, (M_max, N))))
+    return _call(load().et_w4_gemv, dev, stream,
+                 (*ptrs, M_max if M is None else M, _count_arg(d_M, dev), M_max, N, K, group,
+                  *_workspace_args(workspace, dev)), check)
+
+
+def et_w4_experts_workspace_bytes(T_max, H, F, E, k, group) -> int:
+    return load().et_w4_experts_workspace_bytes(T_max, H, F, E, k, group)
+
+
+def et_w4_experts(x, topk_idx, topk_w, q_gate, s_gate, q_up, s_up, q_down, s_down, out, *, T=None, d_T=None,
+                  workspace, stream=None, check=True):
+    """The routed SwiGLU experts of up to 64 tokens, weights in 4 bits: gate, up [E, F, H], down [E, H, F]."""
+    import torch
+    bf = torch.bfloat16
+    (T_max, H), (E, F), k, dev = x.shape, q_gate.shape[:2], topk_idx.shape[-1], x.device
+    (gq, gs), group = _w4_weight(q_gate, s_gate, F, H, E)
+    (uq, us), gu = _w4_weight(q_up, s_up, F, H, E)
+    (dq, ds), gd = _w4_weight(q_down, s_down, H, F, E)
+    if not group == gu == gd:
+        raise ValueError(f"gate, up and down must have one group size, not {group}, {gu}, {gd}")
+    ptrs = _args(dev, (("x", x, bf, (T_max, H)), ("topk_idx", topk_idx, torch.int32, (T_max, k)),
+                       ("topk_w", topk_w, torch.float32, (T_max, k)), ("q_gate", *gq), ("s_gate", *gs),
+                       ("q_up", *uq), ("s_up", *us), ("q_down", *dq), ("s_down", *ds),
+                       ("out", out, bf, (T_max, H))))
+    return _call(load().et_w4_experts, dev, stream,
+                 (*ptrs, T_max if T is None else T, _count_arg(d_T, dev), T_max, H, F, E, k, group,
+                  *_workspace_args(workspace, dev)), check)
 
 
 def et_status(workspace, stream=None):
