@@ -14,15 +14,17 @@
 namespace et {
 namespace {
 
-constexpr int kW4Rows = 64;        // weight rows of a CTA (gate/up: 32 of each)
+constexpr int kW4Rows = 64;        // weight rows of a warp (gate/up: 32 of each)
 constexpr int kW4Blk = 128;        // inputs of a stage: 64 bytes of a row
 constexpr int kW4Warps = 4;
-constexpr int kW4Stages = 4;
+constexpr int kW4Stages = 2;
 constexpr int kW4RowsMax = 64;     // most rows of x (tokens)
 constexpr int kW4KMax = 8;         // experts of a token
 constexpr int kW4EMax = 256;
 constexpr int kW4ClusterMax = 8;
-constexpr int kW4Pad = kW4Rows + 8;  // row length of a CTA's fp32 tile, padded against bank conflicts
+constexpr int kSmemSm = 228 * 1024;  // shared memory of an SM; each CTA takes 1 KB beside its own
+constexpr int kW4Pad = kW4Rows + 8;  // row length of a warp's fp32 tile, padded against bank conflicts
+constexpr int kW4RoutedMax = kW4RowsMax * kW4KMax;
 
 enum W4Mode { kW4Gemv = 0, kW4GateUp = 1, kW4Down = 2 };
 
@@ -34,165 +36,132 @@ struct W4Args {
     const int32_t* idx;       // [T, k]
     const float* w;           // [T, k]
     const int32_t* d_T;
-    int T_host, T_max, N, K, group, E, k;
+    int T_host, T_max, N, K, E, k;
     EtHeader* hdr;
     int x_rows;               // rows of x a stage holds = rows of a pass or segment
-    int stage_bytes;
+    uint32_t magic;           // 0x43004300 (see unpack8)
 };
 
-// The warp's own ring: each stage is [64 rows][64 B] of weights, x_rows rows of
-// 256 B of x, and 128 / group rows of 64 scales.  16-byte pieces are swizzled
-// so that the fragment reads below touch every bank once.
-struct W4Stage {
-    uint32_t w, x, s;
-};
-
-__device__ __forceinline__ W4Stage stage_at(const W4Args& p, uint32_t base, int slot) {
-    const uint32_t b = base + slot * p.stage_bytes;
-    return {b, b + kW4Rows * 64, b + kW4Rows * 64 + static_cast<uint32_t>(p.x_rows) * 256};
-}
-
-// Post the copies of k-block kb: weights of rows [n0, n0 + 64) (gate/up: 32 + 32),
-// x rows cols[0..nc), scales.  Pieces outside the matrices are filled with zeros.
-template <int MODE>
-__device__ __forceinline__ void load_stage(const W4Args& p, const W4Stage& st, int e, int n0, int kb,
-                                           const int* cols, int nc) {
-    const int lane = threadIdx.x & 31;
-    const int k0 = kb * kW4Blk;
-    {
-        const int c = lane & 3;
-        const bool kin = k0 + c * 32 < p.K;
-        const size_t ld = static_cast<size_t>(p.K) / 2;
-        const size_t base = static_cast<size_t>(e) * p.N * ld + k0 / 2 + c * 16;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = (lane >> 2) + 8 * i;
-            const int n = MODE == kW4GateUp ? n0 + (r & 31) : n0 + r;
-            const uint8_t* q = (MODE == kW4GateUp && i >= 4) ? p.q1 : p.q0;
-            const bool in = kin && n < p.N;
-            cp_async16(st.w + r * 64 + ((c ^ ((r >> 1) & 3)) << 4), in ? q + base + n * ld : q, in);
-        }
-    }
-    {
-        const int c = lane & 15;
-        const bool kin = k0 + c * 8 < p.K;
-        for (int r = lane >> 4; r < nc; r += 2)
-            cp_async16(st.x + r * 256 + ((c ^ ((r & 1) << 2)) << 4),
-                       kin ? p.x + static_cast<size_t>(cols[r]) * p.K + k0 + c * 8 : p.x, kin);
-    }
-    {
-        const int gs = kW4Blk / p.group;  // groups of a k-block: 1, 2 or 4, of 8 pieces each
-        const int g = lane >> 3, c = lane & 7;
-        if (g < gs) {
-            const int gi = k0 / p.group + g;
-            const int G = p.K / p.group;
-            const int n = MODE == kW4GateUp ? n0 + (c & 3) * 8 : n0 + c * 8;
-            const bf16* s = (MODE == kW4GateUp && c >= 4) ? p.s1 : p.s0;
-            const bool in = gi < G && n < p.N;
-            cp_async16(st.s + g * 128 + (c << 4),
-                       in ? s + (static_cast<size_t>(e) * G + gi) * p.N + n : s, in);
-        }
-    }
-}
-
-__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(a));
-    return v;
-}
-__device__ __forceinline__ float ld_shared_bf16(uint32_t a) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-    return __uint_as_float(static_cast<uint32_t>(v) << 16);
-}
-
-// Eight 4-bit values -> four packed pairs of q - 8 in bf16, pairs (0,4) (1,5)
+// Eight 4-bit values -> four packed pairs of 128 + q in bf16, pairs (0,4) (1,5)
 // (2,6) (3,7).  0x4300 is 128.0 with a unit of 1 in its last place, so or-ing a
-// nibble in gives 128 + q exactly, and subtracting 136 gives q - 8 exactly.
-__device__ __forceinline__ void unpack8(uint32_t v, uint32_t (&o)[4]) {
-    const __nv_bfloat162 off = __floats2bfloat162_rn(136.0f, 136.0f);
+// nibble in gives 128 + q exactly; the 136 too many of each value are taken off
+// once a group, by starting its sum at -136 sum(x).  `magic` (0x43004300) comes
+// from a kernel parameter, because a second constant known to the compiler
+// makes and-or two operations instead of one.
+__device__ __forceinline__ void unpack8(uint32_t v, uint32_t magic, uint32_t (&o)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t b = ((v >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b), off);
-        o[i] = *reinterpret_cast<const uint32_t*>(&d);
+    for (int i = 0; i < 4; ++i)
+        asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(o[i]) : "r"(v >> (4 * i)), "r"(magic));
+}
+
+// d = a b + c
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1, const float (&c)[4]) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+
+// A warp's part of a stage in shared memory: 64 rows of 64 bytes of weights,
+// 128 / group rows of 64 scales; and the x rows (256 bytes each) that the RW
+// warps of a k-split share.
+struct W4Stage {
+    uint8_t *w, *s, *x;
+};
+
+// The order of the inputs inside a group's products is free as long as weights
+// and x agree.  Lane (r = lane / 4, t = lane % 4) takes G / 32 consecutive 32-bit
+// words of a group of a row, one 4-, 8- or 16-byte read; the 16-byte pieces of
+// weights (4 a row) and x (16 a row) are swizzled so that the lanes of each
+// phase of these reads, and of the x reads, touch different banks.
+template <int G>
+__device__ __forceinline__ int swz_w(int piece, int row) {
+    return G == 32 ? piece ^ ((row >> 1) & 3) : G == 64 ? piece ^ (row & 2) : piece;
+}
+template <int G>
+__device__ __forceinline__ int swz_x(int piece, int row) {
+    return G == 32 ? piece ^ ((row & 1) << 2) : G == 64 ? piece ^ (row & 1)
+                                              : piece ^ ((piece >> 3) & 1) ^ ((row & 1) << 1);
+}
+
+template <int W>
+__device__ __forceinline__ void ld_words(const uint8_t* a, uint32_t (&v)[W]) {
+    if (W == 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(a);
+        v[0] = u.x; v[1 % W] = u.y; v[2 % W] = u.z; v[3 % W] = u.w;
+    } else if (W == 2) {
+        const uint2 u = *reinterpret_cast<const uint2*>(a);
+        v[0] = u.x; v[1 % W] = u.y;
+    } else {
+        v[0] = *reinterpret_cast<const uint32_t*>(a);
     }
 }
 
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// One k-block: acc += scale * ((q - 8) x), the bracket exact products summed in
-// fp32 by the tensor core over a group, the scale applied in fp32 after it.
-// A fragment: lane (r = lane / 4, t = lane % 4) holds inputs 8t .. 8t + 7 of
-// each 32 (one 32-bit word) of rows r and r + 8; the order of the inputs inside
-// a product is free as long as x follows it, and x is paired (0,4) (1,5) ...
-// like the unpacked weights.
-template <int NT>
-__device__ __forceinline__ void compute_stage(const W4Args& p, const W4Stage& st, int nc,
+// One k-block: acc += scale * sum((q - 8) x) over each group, the products exact,
+// summed in fp32 by the tensor core, the scale applied in fp32 after it.  The
+// sum starts at -136 sum(x), a product of x with a matrix of -136 (exact in
+// bf16), and adds (128 + q) x: 30 times the magnitude of (q - 8) x, which costs
+// 5 of the fp32 sum's 24 bits and leaves 10 more than the bf16 result keeps.
+template <int NT, int G>
+__device__ __forceinline__ void compute_stage(const W4Stage& st, int nc, uint32_t magic,
                                               float (&acc)[4][NT][4]) {
+    constexpr int W = G / 32;  // words of a lane and row in a group
     const int lane = threadIdx.x & 31;
     const int r = lane >> 2, t = lane & 3;
-    const int per = p.group >> 5;  // 32-input pieces of a group
-    float part[4][NT][4];
+    const uint32_t neg = 0xc308c308u;  // -136, twice
+    const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        if ((c & (per - 1)) == 0) {
+    for (int g = 0; g < kW4Blk / G; ++g) {
+        uint32_t b[W][NT][4];
+        float off[NT][4];
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) part[m][j][i] = 0.0f;
-        }
-        uint32_t b[NT][4];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const int n = j * 8 + r;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (n < nc) v = ld_shared_v4(st.x + n * 256 + (((c * 4 + t) ^ ((n & 1) << 2)) << 4));
-            b[j][0] = __byte_perm(v.x, v.z, 0x5410);
-            b[j][1] = __byte_perm(v.x, v.z, 0x7632);
-            b[j][2] = __byte_perm(v.y, v.w, 0x5410);
-            b[j][3] = __byte_perm(v.y, v.w, 0x7632);
-        }
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            uint32_t lo[4], hi[4];
-            const uint32_t a = st.w + (m * 16 + r) * 64 + ((c ^ ((r >> 1) & 3)) << 4) + t * 4;
-            unpack8(ld_shared_u32(a), lo);
-            unpack8(ld_shared_u32(a + 8 * 64), hi);
+        for (int i = 0; i < W; ++i)
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                mma16816(part[m][j], lo[0], hi[0], lo[1], hi[1], b[j][0], b[j][1]);
-                mma16816(part[m][j], lo[2], hi[2], lo[3], hi[3], b[j][2], b[j][3]);
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (j * 8 + r < nc) v = *reinterpret_cast<const uint4*>(st.x + (j * 8 + r) * 256 + (swz_x<G>(g * (G / 8) + t * W + i, r) << 4));
+                b[i][j][0] = __byte_perm(v.x, v.z, 0x5410);
+                b[i][j][1] = __byte_perm(v.x, v.z, 0x7632);
+                b[i][j][2] = __byte_perm(v.y, v.w, 0x5410);
+                b[i][j][3] = __byte_perm(v.y, v.w, 0x7632);
+            }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            mma16816(off[j], neg, neg, neg, neg, b[0][j][0], b[0][j][1], zero);
+            mma16816(off[j], neg, neg, neg, neg, b[0][j][2], b[0][j][3], off[j]);
+#pragma unroll
+            for (int i = 1; i < W; ++i) {
+                mma16816(off[j], neg, neg, neg, neg, b[i][j][0], b[i][j][1], off[j]);
+                mma16816(off[j], neg, neg, neg, neg, b[i][j][2], b[i][j][3], off[j]);
             }
         }
-        if (((c + 1) & (per - 1)) == 0) {
-            const uint32_t sa = st.s + (c / per) * 128 + r * 2;
+        const __nv_bfloat16* sa = reinterpret_cast<const __nv_bfloat16*>(st.s + g * 128) + r;
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const float s0 = ld_shared_bf16(sa + m * 32), s1 = ld_shared_bf16(sa + m * 32 + 16);
+        for (int m = 0; m < 4; ++m) {
+            uint32_t lo[W], hi[W];
+            const uint8_t* a = st.w + (m * 16 + r) * 64 + (swz_w<G>(g * (G / 32) + (t * W >> 2), r) << 4) + ((t * W & 3) << 2);
+            ld_words<W>(a, lo);
+            ld_words<W>(a + 512, hi);
+            const float s0 = __bfloat162float(sa[m * 16]), s1 = __bfloat162float(sa[m * 16 + 8]);
+            float part[NT][4];
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                uint32_t u[4], v[4];
+                unpack8(lo[i], magic, u);
+                unpack8(hi[i], magic, v);
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    acc[m][j][0] += s0 * part[m][j][0];
-                    acc[m][j][1] += s0 * part[m][j][1];
-                    acc[m][j][2] += s1 * part[m][j][2];
-                    acc[m][j][3] += s1 * part[m][j][3];
+                    mma16816(part[j], u[0], v[0], u[1], v[1], b[i][j][0], b[i][j][1], i == 0 ? off[j] : part[j]);
+                    mma16816(part[j], u[2], v[2], u[3], v[3], b[i][j][2], b[i][j][3], part[j]);
                 }
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                acc[m][j][0] += s0 * part[j][0];
+                acc[m][j][1] += s0 * part[j][1];
+                acc[m][j][2] += s1 * part[j][2];
+                acc[m][j][3] += s1 * part[j][3];
             }
         }
     }
@@ -223,129 +192,276 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
 // The routed rows of a call, grouped by expert, in shared memory.  Rows r = t k + j
 // whose index is -1 are left out; an index outside [-1, E) is recorded and left out.
 struct W4Routing {
-    int e[kW4RowsMax * kW4KMax];        // row -> expert (-1: none)
-    int order[kW4RowsMax * kW4KMax];    // rows by expert, ascending within one
-    int start[kW4EMax + 1];             // first entry of an expert in `order`
-    int seg_e[kW4RowsMax * kW4KMax];    // segments: up to `width` rows of one expert
-    int seg_r[kW4RowsMax * kW4KMax];
-    int seg_n[kW4RowsMax * kW4KMax];
-    int cnt[kW4EMax];
+    int16_t e[kW4RoutedMax];        // row -> expert (-1: none)
+    int16_t order[kW4RoutedMax];    // rows by expert, ascending within one
+    float wt[kW4RoutedMax];         // their gate weights
+    int16_t seg_e[kW4RoutedMax];    // segments: up to `width` rows of one expert
+    int16_t seg_r[kW4RoutedMax];
+    int16_t seg_n[kW4RoutedMax];
+    int16_t cnt[kW4Warps][kW4EMax]; // rows of an expert in a warp's share, then their first entry in `order`
+    int total[kW4Warps];
     int n_seg;
+    int twice;                      // a token names an expert twice
 };
+static_assert(kW4Warps * 32 * 2 >= kW4EMax, "two experts a thread");
+static_assert(kW4RoutedMax <= kW4Warps * 128, "four rows a thread");
 
 __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, int T, int width) {
-    const int R = T * p.k;
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) rt.cnt[e] = 0;
-    __syncthreads();
-    for (int r = threadIdx.x; r < R; r += blockDim.x) {
-        int e = p.idx[r];
-        if (e < -1 || e >= p.E) {
-            record_status(p.hdr, ET_ERR_BOUNDS, kWhereExpertIndex);
-            e = -1;
-        }
-        rt.e[r] = e;
-        if (e >= 0) atomicAdd(&rt.cnt[e], 1);
-    }
-    __syncthreads();
-    if (threadIdx.x < 32) {  // exclusive sums over experts: of rows and of segments
-        const int lane = threadIdx.x;
-        int rows = 0, segs = 0;
-        for (int b = 0; b < p.E; b += 32) {
-            const int e = b + lane;
-            const int c = e < p.E ? rt.cnt[e] : 0;
-            const int s = (c + width - 1) / width;
-            int ci = c, si = s;
+    const int R = T * p.k, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int span = (R + kW4Warps * 32 - 1) / (kW4Warps * 32) * 32;  // consecutive rows of a warp
+    int e[4], at[4];
+    float wt[4];
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int a = __shfl_up_sync(0xffffffffu, ci, off), d = __shfl_up_sync(0xffffffffu, si, off);
-                if (lane >= off) { ci += a; si += d; }
-            }
-            const int r0 = rows + ci - c;
-            int s0 = segs + si - s;
-            if (e < p.E) rt.start[e] = r0;
-            for (int o = 0; o < c; o += width, ++s0) {
-                rt.seg_e[s0] = e;
-                rt.seg_r[s0] = r0 + o;
-                rt.seg_n[s0] = min(width, c - o);
-            }
-            rows += __shfl_sync(0xffffffffu, ci, 31);
-            segs += __shfl_sync(0xffffffffu, si, 31);
+    for (int i = 0; i < 4; ++i) {
+        const int r = warp * span + i * 32 + lane;
+        const bool in = i * 32 < span && r < R;
+        e[i] = in ? p.idx[r] : -1;
+        wt[i] = in ? p.w[r] : 0.0f;
+    }
+    for (int i = tid; i < kW4Warps * kW4EMax / 2; i += blockDim.x) reinterpret_cast<int*>(rt.cnt)[i] = 0;
+    if (tid == 0) rt.twice = 0;
+    __syncthreads();
+    // a row's place among its warp's rows of that expert
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (i * 32 >= span) break;
+        const int r = warp * span + i * 32 + lane;
+        if (e[i] < -1 || e[i] >= p.E) {
+            record_status(p.hdr, ET_ERR_BOUNDS, kWhereExpertIndex);
+            e[i] = -1;
         }
-        if (lane == 0) rt.n_seg = segs;
+        const uint32_t same = __match_any_sync(0xffffffffu, e[i]);
+        const int before = __popc(same & ((1u << lane) - 1u));
+        int have = 0;
+        if (e[i] >= 0) have = rt.cnt[warp][e[i]];
+        __syncwarp();
+        if (e[i] >= 0 && before == 0) rt.cnt[warp][e[i]] = static_cast<int16_t>(have + __popc(same));
+        __syncwarp();
+        at[i] = have + before;
+        if (r < R) rt.e[r] = static_cast<int16_t>(e[i]);
     }
     __syncthreads();
-    for (int r = threadIdx.x; r < R; r += blockDim.x) {
-        const int e = rt.e[r];
-        if (e < 0) continue;
-        int rank = 0;
-        for (int o = 0; o < r; ++o) rank += rt.e[o] == e;
-        rt.order[rt.start[e] + rank] = r;
+    // exclusive sums over the experts, of rows (low half) and segments (high half)
+    int c[2], v[2], sum = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int x = 2 * tid + h;
+        c[h] = 0;
+        if (x < kW4EMax)
+#pragma unroll
+            for (int w = 0; w < kW4Warps; ++w) c[h] += rt.cnt[w][x];
+        v[h] = c[h] | ((c[h] + width - 1) / width << 16);
+        sum += v[h];
+    }
+    int inc = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += up;
+    }
+    if (lane == 31) rt.total[warp] = inc;
+    // a token's rows against its earlier ones
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = warp * span + i * 32 + lane;
+        if (i * 32 < span && r < R && e[i] >= 0)
+            for (int o = r - r % p.k; o < r; ++o)
+                if (rt.e[o] == e[i]) rt.twice = 1;
+    }
+    __syncthreads();
+    int base = inc - sum;
+    for (int w = 0; w < warp; ++w) base += rt.total[w];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int x = 2 * tid + h;
+        if (c[h] > 0) {
+            const int r0 = base & 0xffff;
+            int s0 = base >> 16, a = r0;
+            for (int o = 0; o < c[h]; o += width, ++s0) {
+                rt.seg_e[s0] = static_cast<int16_t>(x);
+                rt.seg_r[s0] = static_cast<int16_t>(r0 + o);
+                rt.seg_n[s0] = static_cast<int16_t>(min(width, c[h] - o));
+            }
+#pragma unroll
+            for (int w = 0; w < kW4Warps; ++w) {
+                const int n = rt.cnt[w][x];
+                rt.cnt[w][x] = static_cast<int16_t>(a);
+                a += n;
+            }
+        }
+        base += v[h];
+    }
+    if (tid == static_cast<int>(blockDim.x) - 1) rt.n_seg = base >> 16;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = warp * span + i * 32 + lane;
+        if (i * 32 < span && r < R && e[i] >= 0) {
+            const int o = rt.cnt[warp][e[i]] + at[i];
+            rt.order[o] = static_cast<int16_t>(r);
+            rt.wt[o] = wt[i];
+        }
     }
     __syncthreads();
 }
 
-// One CTA: 64 weight rows (gate/up: 32 + 32).  The inputs are split over the
-// warps of the CTA and over the CTAs of its cluster; each warp streams its own
-// k-blocks through its own ring, and no barrier sits in the loop.
+// One CTA of four warps: RW row groups x 4 / RW splits of the inputs.  The inputs
+// are split further over the CTAs of the cluster.  The RW warps of a split share
+// its x rows and meet at a named barrier once a k-block; splits run on their
+// own, each through its own ring.
 //   kW4Gemv   x rows in chunks of x_rows <= 8 NT, all of K.
 //   kW4GateUp blockIdx.y picks the segment: up to x_rows rows of one expert.
 //   kW4Down   the work is the list of (segment, k-block); a warp adds what it
 //             has for a segment, times the gate weight, to its own fp32 rows by
-//             token, and the sum over warps and CTAs is the layer's output.
-template <int MODE, int NT>
+//             token, and the sum over splits and CTAs is the layer's output.
+template <int MODE, int NT, int G>
+struct W4Shape {
+    static constexpr int RW = NT == 1 ? 1 : NT == 2 ? 2 : 4;  // row groups
+    static constexpr int KW = kW4Warps / RW;                  // splits of the inputs
+    static constexpr int kTile = RW * kW4Rows;                // weight rows of a CTA
+    static constexpr int kOut = MODE == kW4GateUp ? kTile / 2 : kTile;
+    static constexpr int kWarpBytes = kW4Rows * 64 + (kW4Blk / G) * 128;
+    static __host__ __device__ int stage_bytes(int x_rows) { return RW * kWarpBytes + x_rows * 256; }
+    static __host__ __device__ int ring_bytes(int x_rows) { return KW * kW4Stages * stage_bytes(x_rows); }
+};
+
+template <int MODE, int NT, int G>
 __global__ void __launch_bounds__(kW4Warps * 32) w4_kernel(const W4Args p) {
+    using S = W4Shape<MODE, NT, G>;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int cols_s[MODE == kW4Down ? 1 : NT * 8];
+    __shared__ int x_row[NT * 8];    // gemv and gate/up: this pass's rows of x
+    __shared__ int out_row[NT * 8];  // gate/up: the routed rows
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rw = warp % S::RW, kw = warp / S::RW;
     const int csize = static_cast<int>(cluster_size()), crank = static_cast<int>(cluster_rank());
-    const int unit = crank * kW4Warps + warp, units = csize * kW4Warps;
-    constexpr int kOutRows = MODE == kW4GateUp ? 32 : 64;
-    const int n0 = (blockIdx.x / csize) * kOutRows;
+    const int unit = crank * S::KW + kw, units = csize * S::KW;
+    const int n0 = (blockIdx.x / csize) * S::kOut;                        // the CTA's first output
+    const int nw = n0 + rw * (MODE == kW4GateUp ? kW4Rows / 2 : kW4Rows);  // this warp's
     const int KB = (p.K + kW4Blk - 1) / kW4Blk;
     bool ok;
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
     if (!ok) return;  // the same for every CTA of the cluster
 
-    // shared memory: [routing][fp32 sums][rings]; the sums of the first two
-    // modes lie over the rings, which are empty by then
+    // shared memory.  gemv and gate/up: the rings, and over them (before: the
+    // routing; after: the fp32 sums).  down: [routing][fp32 sums by token][rings].
     W4Routing& rt = *reinterpret_cast<W4Routing*>(smem);
-    uint8_t* rest = smem + (MODE == kW4Gemv ? 0 : (sizeof(W4Routing) + 127) / 128 * 128);
+    uint8_t* rest = smem;
+    if (MODE == kW4Down) rest += (sizeof(W4Routing) + 127) / 128 * 128;
     float* sums = reinterpret_cast<float*>(rest);
     if (MODE == kW4Down) rest += (static_cast<size_t>(kW4Warps) * T * kW4Pad * 4 + 127) / 128 * 128;
-    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(rest)) +
-                          warp * kW4Stages * p.stage_bytes;
+    const int sbytes = S::stage_bytes(p.x_rows);
+    uint8_t* ring = rest + kw * kW4Stages * sbytes;
+
+    int nc0 = 0, e0 = 0;
     if (MODE != kW4Gemv) build_routing(p, rt, T, p.x_rows);
+    if (MODE == kW4GateUp) {
+        if (static_cast<int>(blockIdx.y) >= rt.n_seg) return;  // the whole cluster
+        nc0 = rt.seg_n[blockIdx.y];
+        e0 = rt.seg_e[blockIdx.y];
+        if (static_cast<int>(threadIdx.x) < nc0) {
+            const int r = rt.order[rt.seg_r[blockIdx.y] + threadIdx.x];
+            out_row[threadIdx.x] = r;
+            x_row[threadIdx.x] = r / p.k;
+        }
+        __syncthreads();  // the routing's memory becomes the rings'
+    }
+    if (MODE == kW4Down) {
+        for (int i = threadIdx.x; i < kW4Warps * T * kW4Pad; i += blockDim.x) sums[i] = 0.0f;
+        __syncthreads();
+    }
 
     const int passes = MODE == kW4Gemv ? (T + p.x_rows - 1) / p.x_rows : 1;
-    if (MODE == kW4GateUp && static_cast<int>(blockIdx.y) >= rt.n_seg) return;
-    if (MODE == kW4Down)
-        for (int i = threadIdx.x; i < kW4Warps * T * kW4Pad; i += blockDim.x) sums[i] = 0.0f;
-
     for (int pass = 0; pass < passes; ++pass) {
-        int nc0 = 0, e0 = 0;
         if (MODE == kW4Gemv) {
             nc0 = min(p.x_rows, T - pass * p.x_rows);
-            if (threadIdx.x < nc0) cols_s[threadIdx.x] = pass * p.x_rows + threadIdx.x;
-        } else if (MODE == kW4GateUp) {
-            nc0 = rt.seg_n[blockIdx.y];
-            e0 = rt.seg_e[blockIdx.y];
-            if (threadIdx.x < nc0) cols_s[threadIdx.x] = rt.order[rt.seg_r[blockIdx.y] + threadIdx.x] / p.k;
+            if (static_cast<int>(threadIdx.x) < nc0) x_row[threadIdx.x] = pass * p.x_rows + threadIdx.x;
+            __syncthreads();
         }
-        __syncthreads();
+        const int items = (MODE == kW4Down ? rt.n_seg : 1) * KB;
+        const int i0 = static_cast<int>(static_cast<long long>(items) * unit / units);
+        const int i1 = static_cast<int>(static_cast<long long>(items) * (unit + 1) / units);
 
-        const long long items = static_cast<long long>(MODE == kW4Down ? rt.n_seg : 1) * KB;
-        const int i0 = static_cast<int>(items * unit / units), i1 = static_cast<int>(items * (unit + 1) / units);
-        auto post = [&](int i) {
-            if (i < i1) {
-                const W4Stage st = stage_at(p, ring, (i - i0) % kW4Stages);
-                if (MODE == kW4Down) {
-                    const int s = i / KB;
-                    load_stage<MODE>(p, st, rt.seg_e[s], n0, i - s * KB, rt.order + rt.seg_r[s], rt.seg_n[s]);
+        auto stage_at = [&](int slot) {
+            uint8_t* b = ring + slot * sbytes;
+            return W4Stage{b + rw * S::kWarpBytes, b + rw * S::kWarpBytes + kW4Rows * 64, b + S::RW * S::kWarpBytes};
+        };
+        // Where the copies are: the next item to post, its ring slot, and this
+        // lane's first piece of its weights (row nw + lane / 4, 16 bytes lane % 4)
+        // and scales.  Rows [nw, nw + 64) of one matrix, or 32 + 32 of two.
+        const size_t ld = static_cast<size_t>(p.K) / 2, ld8 = ld * 8;
+        const int left = p.N - nw;  // rows there are: a multiple of 8
+        int item = i0, slot = 0, seg = MODE == kW4Down && i0 < i1 ? i0 / KB : 0, kb = i0 - seg * KB;
+        const uint8_t *qa, *qb;
+        const bf16* sp;
+        const int sg = lane >> 3, sc = lane & 7;  // this lane's group of the k-block and its 8 rows
+        const int sn8 = MODE == kW4GateUp ? (sc & 3) * 8 : sc * 8;
+        auto seek = [&]() {
+            const int e = MODE == kW4Down ? rt.seg_e[seg] : e0;
+            const size_t at = (static_cast<size_t>(e) * p.N + nw + (lane >> 2)) * ld + static_cast<size_t>(kb) * 64 + (lane & 3) * 16;
+            qa = p.q0 + at;
+            if (MODE == kW4GateUp) qb = p.q1 + at;
+            const bf16* s = (MODE == kW4GateUp && sc >= 4) ? p.s1 : p.s0;
+            sp = s + (static_cast<size_t>(e) * (p.K / G) + kb * (kW4Blk / G) + sg) * p.N + nw + sn8;
+        };
+        if (i0 < i1) seek();
+        // Post the copies of the next item and move on.  Pieces outside the matrices
+        // are filled with zeros.
+        auto post = [&]() {
+            if (item >= i1) return;
+            const W4Stage st = stage_at(slot);
+            const int k0 = kb * kW4Blk;
+            {
+                const int r = lane >> 2, c = lane & 3;
+                const uint32_t dst = smem_addr(st.w) + r * 64 + (swz_w<G>(c, r) << 4);  // row + 8: the same swizzle
+                if (k0 + kW4Blk <= p.K && left >= (MODE == kW4GateUp ? kW4Rows / 2 : kW4Rows)) {
+                    const uint8_t* q = qa;
+#pragma unroll
+                    for (int g = 0; g < 8; ++g, q += ld8) {
+                        if (MODE == kW4GateUp && g == 4) q = qb;
+                        cp_async16(dst + g * 512, q);
+                    }
                 } else {
-                    load_stage<MODE>(p, st, e0, n0, i, cols_s, nc0);
+                    const bool kin = k0 + c * 32 < p.K;
+#pragma unroll
+                    for (int g = 0; g < 8; ++g) {
+                        const int g8 = MODE == kW4GateUp ? g & 3 : g;
+                        const bool in = kin && g8 * 8 < left;
+                        cp_async16(dst + g * 512, in ? (MODE == kW4GateUp && g >= 4 ? qb : qa) + g8 * ld8 : p.q0, in);
+                    }
                 }
             }
-            cp_async_commit();
+            if (sg < kW4Blk / G) {
+                const bool in = k0 + sg * G < p.K && sn8 < left;
+                cp_async16(smem_addr(st.s) + sg * 128 + (sc << 4), in ? sp : p.s0, in);
+            }
+            {   // x rows, shared out among the split's warps
+                const int nc = MODE == kW4Down ? rt.seg_n[seg] : nc0;
+                const int c = lane & 15, kx = k0 + c * 8;
+                const bool kin = kx < p.K;
+                for (int r = (lane >> 4) + 2 * rw; r < nc; r += 2 * S::RW) {
+                    const int row = MODE == kW4Down ? rt.order[rt.seg_r[seg] + r] : x_row[r];
+                    cp_async16(smem_addr(st.x) + r * 256 + (swz_x<G>(c, r) << 4),
+                               kin ? p.x + static_cast<size_t>(row) * p.K + kx : p.x, kin);
+                }
+            }
+            ++item;
+            slot = slot + 1 == kW4Stages ? 0 : slot + 1;
+            ++kb;
+            if (MODE == kW4Down && kb == KB) {
+                kb = 0;
+                ++seg;
+                if (item < i1) seek();
+            } else {
+                qa += 64;
+                if (MODE == kW4GateUp) qb += 64;
+                sp += static_cast<size_t>(kW4Blk / G) * p.N;
+            }
+        };
+        auto meet = [&]() {
+            if (S::RW == 1) __syncwarp();
+            else if (S::KW == 1) __syncthreads();
+            else if (kw == 0) asm volatile("bar.sync 1, 64;" ::: "memory");
+            else asm volatile("bar.sync 2, 64;" ::: "memory");
         };
         float acc[4][NT][4];
 #pragma unroll
@@ -355,29 +471,37 @@ __global__ void __launch_bounds__(kW4Warps * 32) w4_kernel(const W4Args p) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
 #pragma unroll
-        for (int s = 0; s < kW4Stages - 1; ++s) post(i0 + s);
+        for (int s = 0; s < kW4Stages - 1; ++s) {
+            post();
+            cp_async_commit();
+        }
+        int cslot = 0, cseg = MODE == kW4Down && i0 < i1 ? i0 / KB : 0, ckb = i0 - cseg * KB;
         for (int i = i0; i < i1; ++i) {
             cp_async_wait<kW4Stages - 2>();
-            __syncwarp();
-            post(i + kW4Stages - 1);
-            const int seg = MODE == kW4Down ? i / KB : 0;
-            const int nc = MODE == kW4Down ? rt.seg_n[seg] : nc0;
-            compute_stage<NT>(p, stage_at(p, ring, (i - i0) % kW4Stages), nc, acc);
-            if (MODE == kW4Down && (i + 1 == i1 || (i + 1) % KB == 0)) {
-                // the quarter-warps in turn: a token may hold two rows of one segment
+            meet();
+            post();
+            cp_async_commit();
+            const int nc = MODE == kW4Down ? rt.seg_n[cseg] : nc0;
+            compute_stage<NT, G>(stage_at(cslot), nc, p.magic, acc);
+            cslot = cslot + 1 == kW4Stages ? 0 : cslot + 1;
+            ++ckb;
+            if (MODE == kW4Down && (i + 1 == i1 || ckb == KB)) {
+                // the segment's rows by token.  If a token holds two rows of one
+                // expert, the quarter-warps (two rows each) take turns.
                 float* mine = sums + static_cast<size_t>(warp) * T * kW4Pad;
                 const int r = lane >> 2, t = lane & 3;
-                for (int q = 0; q < 4; ++q) {
-                    if (t == q) {
+                const bool turns = rt.twice != 0;
+                for (int q = 0; q < (turns ? 4 : 1); ++q) {
+                    if (!turns || t == q) {
 #pragma unroll
                         for (int j = 0; j < NT; ++j)
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 const int col = j * 8 + 2 * t + h;
                                 if (col < nc) {
-                                    const int row = rt.order[rt.seg_r[seg] + col];
-                                    const float wt = p.w[row];
-                                    float* dst = mine + (row / p.k) * kW4Pad + r;
+                                    const int o = rt.seg_r[cseg] + col;
+                                    const float wt = rt.wt[o];
+                                    float* dst = mine + (rt.order[o] / p.k) * kW4Pad + r;
 #pragma unroll
                                     for (int m = 0; m < 4; ++m) {
                                         dst[m * 16] += wt * acc[m][j][h];
@@ -394,12 +518,15 @@ __global__ void __launch_bounds__(kW4Warps * 32) w4_kernel(const W4Args p) {
                     for (int j = 0; j < NT; ++j)
 #pragma unroll
                         for (int z = 0; z < 4; ++z) acc[m][j][z] = 0.0f;
+                ckb = 0;
+                ++cseg;
             }
         }
         cp_async_wait<0>();
         __syncthreads();  // the rings are empty
 
-        // sums over the CTA's warps, in order, into the first warp's tile
+        // sums over the splits, in order, into the first split's tiles: a warp's
+        // tile is [nc][64], the first RW tiles make the CTA's
         const int nc = MODE == kW4Down ? T : nc0;
         if (MODE != kW4Down) {
             const int r = lane >> 2, t = lane & 3;
@@ -419,36 +546,37 @@ __global__ void __launch_bounds__(kW4Warps * 32) w4_kernel(const W4Args p) {
                 }
             __syncthreads();
         }
-        for (int o = threadIdx.x; o < nc * kW4Rows; o += blockDim.x) {
-            const int at = (o >> 6) * kW4Pad + (o & 63);
-            float v = sums[at];
+        if (S::KW > 1) {
+            for (int o = threadIdx.x; o < S::RW * nc * kW4Rows; o += blockDim.x) {
+                const int at = (o >> 6) * kW4Pad + (o & 63);
+                float v = sums[at];
 #pragma unroll
-            for (int w = 1; w < kW4Warps; ++w) v += sums[w * nc * kW4Pad + at];
-            sums[at] = v;
+                for (int w = 1; w < S::KW; ++w) v += sums[w * S::RW * nc * kW4Pad + at];
+                sums[at] = v;
+            }
         }
         // sums over the cluster's CTAs, in order; each CTA stores its share
         if (csize > 1) cluster_sync();
         else __syncthreads();
-        const uint32_t sums_u = static_cast<uint32_t>(__cvta_generic_to_shared(sums));
-        for (int o = crank * blockDim.x + threadIdx.x; o < nc * kOutRows; o += csize * blockDim.x) {
-            const int col = o / kOutRows, row = o % kOutRows;
+        const uint32_t sums_u = smem_addr(sums);
+        for (int o = crank * blockDim.x + threadIdx.x; o < nc * S::kOut; o += csize * blockDim.x) {
+            const int col = o / S::kOut, row = o % S::kOut;
             const int n = n0 + row;
-            auto total = [&](int rr) {
-                const uint32_t at = sums_u + (col * kW4Pad + rr) * 4;
-                if (csize == 1) return sums[col * kW4Pad + rr];
+            auto total = [&](int g, int rr) {  // row rr of row group g's tile
+                const int at = (g * nc + col) * kW4Pad + rr;
+                if (csize == 1) return sums[at];
                 float v = 0.0f;
-                for (int c = 0; c < csize; ++c) v += ld_cluster_f32(at, c);
+                for (int c = 0; c < csize; ++c) v += ld_cluster_f32(sums_u + at * 4, c);
                 return v;
             };
             if (n < p.N) {
                 if (MODE == kW4GateUp) {
-                    const float g = total(row), u = total(row + 32);
+                    const float g = total(row >> 5, row & 31), u = total(row >> 5, (row & 31) + 32);
                     const float h = g / (1.0f + expf(-g)) * u;
-                    const int rr = rt.order[rt.seg_r[blockIdx.y] + col];
-                    p.out[static_cast<size_t>(rr) * p.N + n] = __float2bfloat16_rn(h);
+                    p.out[static_cast<size_t>(out_row[col]) * p.N + n] = __float2bfloat16_rn(h);
                 } else {
                     const int m = MODE == kW4Gemv ? pass * p.x_rows + col : col;
-                    p.out[static_cast<size_t>(m) * p.N + n] = __float2bfloat16_rn(total(row));
+                    p.out[static_cast<size_t>(m) * p.N + n] = __float2bfloat16_rn(total(row >> 6, row & 63));
                 }
             }
         }
@@ -549,38 +677,45 @@ bool w4_shape_ok(int N, int K, int group, std::string* why) {
     return true;
 }
 
-// CTAs that share a tile's inputs: doubled while the grid stays below two CTAs
-// an SM and every warp keeps two k-blocks.
-int w4_cluster(long long ctas, long long blocks, int sms) {
-    int c = 1;
-    while (c < kW4ClusterMax && ctas * c * 2 <= 2 * sms && blocks >= 2ll * kW4Warps * c * 2) c *= 2;
-    return c;
+// CTAs that share a tile's inputs: as many as fit the GPU at once (`slots` CTAs)
+// while every split keeps two k-blocks.
+int w4_cluster(long long ctas, long long blocks, int splits, long long slots) {
+    long long c = slots / ctas;
+    c = c < blocks / (2 * splits) ? c : blocks / (2 * splits);
+    return static_cast<int>(c < 1 ? 1 : c > kW4ClusterMax ? kW4ClusterMax : c);
 }
 
-SmemOptIn g_w4_opt[3][3];
-
 // `rows` tokens at most; x_rows <= 8 NT of them (or of an expert's rows) a pass.
-template <int MODE, int NT>
+template <int MODE, int NT, int G>
 int w4_launch(W4Args a, int rows, int x_rows, int dev, int sms, void* stream) {
-    constexpr int kOutRows = MODE == kW4GateUp ? 32 : 64;
-    constexpr int kSmemMost = kSmemLimit - 1024;  // the column list is static
+    using S = W4Shape<MODE, NT, G>;
+    constexpr int kSmemMost = kSmemLimit - 1024;  // the row list is static
     a.x_rows = x_rows;
-    a.stage_bytes = kW4Rows * 64 + x_rows * 256 + (kW4Blk / a.group) * 128;
-    const size_t rings = static_cast<size_t>(kW4Warps) * kW4Stages * a.stage_bytes;
+    a.magic = 0x43004300u;
+    const int rings = S::ring_bytes(x_rows);
     const int sum_rows = MODE == kW4Down ? rows : x_rows;
-    const size_t sums = (static_cast<size_t>(kW4Warps) * sum_rows * kW4Pad * 4 + 127) / 128 * 128;
-    const size_t routing = MODE == kW4Gemv ? 0 : (sizeof(W4Routing) + 127) / 128 * 128;
-    const size_t smem = routing + (MODE == kW4Down ? sums + rings : (sums > rings ? sums : rings));
+    const int sums = (kW4Warps * sum_rows * kW4Pad * 4 + 127) / 128 * 128;
+    const int routing = MODE == kW4Gemv ? 0 : static_cast<int>((sizeof(W4Routing) + 127) / 128 * 128);
+    int smem = routing > rings ? routing : rings;
+    smem = smem > sums ? smem : sums;
+    if (MODE == kW4Down) smem = routing + sums + rings;
     if (smem > kSmemMost) return api_fail(ET_ERR_UNSUPPORTED, "rows do not fit in shared memory");
-    constexpr int kNi = NT == 1 ? 0 : NT == 2 ? 1 : 2;
-    cudaError_t e = api_smem_opt_in(g_w4_opt[MODE][kNi], dev, w4_kernel<MODE, NT>, kSmemMost);
+    static SmemOptIn opt;
+    cudaError_t e = api_smem_opt_in(opt, dev, w4_kernel<MODE, NT, G>, kSmemMost);
     if (e != cudaSuccess) return api_fail_cuda(e, "cudaFuncSetAttribute(4-bit products)");
+    static const int regs = [] {
+        cudaFuncAttributes at{};
+        return cudaFuncGetAttributes(&at, w4_kernel<MODE, NT, G>) == cudaSuccess ? at.numRegs : 255;
+    }();
+    const int by_smem = kSmemSm / (smem + 1280), by_regs = 65536 / (kW4Warps * 32 * ((regs + 7) / 8 * 8));
+    const int occ = by_smem < by_regs ? by_smem : by_regs;  // CTAs an SM
     // segments of a call: each has a row, an expert has one and one more for each full pass
     const int R = rows * a.k, experts = R < a.E ? R : a.E;
     const int slots = MODE == kW4Gemv ? 1 : (experts + R / x_rows < R ? experts + R / x_rows : R);
-    const int tiles = (a.N + kOutRows - 1) / kOutRows;
+    const int tiles = (a.N + S::kOut - 1) / S::kOut;
     const long long blocks = static_cast<long long>((a.K + kW4Blk - 1) / kW4Blk) * (MODE == kW4Down ? slots : 1);
-    const int c = w4_cluster(static_cast<long long>(tiles) * (MODE == kW4GateUp ? slots : 1), blocks, sms);
+    const int c = w4_cluster(static_cast<long long>(tiles) * (MODE == kW4GateUp ? slots : 1), blocks, S::KW,
+                             static_cast<long long>(sms) * occ);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(tiles * c, MODE == kW4GateUp ? slots : 1);
     cfg.blockDim = dim3(kW4Warps * 32);
@@ -593,16 +728,23 @@ int w4_launch(W4Args a, int rows, int x_rows, int dev, int sms, void* stream) {
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, w4_kernel<MODE, NT>, a);
+    e = cudaLaunchKernelEx(&cfg, w4_kernel<MODE, NT, G>, a);
     if (e != cudaSuccess) return api_fail_cuda(e, "launch of the 4-bit product kernel");
     return ET_OK;
 }
 
-template <int MODE>
+template <int MODE, int G>
 int w4_launch_nt(const W4Args& a, int rows, int x_rows, int dev, int sms, void* stream) {
-    if (x_rows <= 8) return w4_launch<MODE, 1>(a, rows, x_rows, dev, sms, stream);
-    if (x_rows <= 16) return w4_launch<MODE, 2>(a, rows, x_rows, dev, sms, stream);
-    return w4_launch<MODE, 4>(a, rows, x_rows, dev, sms, stream);
+    if (x_rows <= 8) return w4_launch<MODE, 1, G>(a, rows, x_rows, dev, sms, stream);
+    if (x_rows <= 16) return w4_launch<MODE, 2, G>(a, rows, x_rows, dev, sms, stream);
+    return w4_launch<MODE, 4, G>(a, rows, x_rows, dev, sms, stream);
+}
+
+template <int MODE>
+int w4_launch_group(const W4Args& a, int group, int rows, int x_rows, int dev, int sms, void* stream) {
+    if (group == 32) return w4_launch_nt<MODE, 32>(a, rows, x_rows, dev, sms, stream);
+    if (group == 64) return w4_launch_nt<MODE, 64>(a, rows, x_rows, dev, sms, stream);
+    return w4_launch_nt<MODE, 128>(a, rows, x_rows, dev, sms, stream);
 }
 
 int w4_conv_check(int E, int N, int K, int group) {
@@ -719,12 +861,11 @@ int et_w4_gemv(const void* X, const void* q, const void* scale, void* Y, int M, 
         a.T_max = M_max;
         a.N = N;
         a.K = K;
-        a.group = group;
         a.E = 1;
         a.k = 1;
         a.hdr = static_cast<EtHeader*>(workspace);
         const int rows = d_M ? M_max : M;
-        return w4_launch_nt<kW4Gemv>(a, rows, rows < 32 ? rows : 32, dev, sms, stream);
+        return w4_launch_group<kW4Gemv>(a, group, rows, rows < 32 ? rows : 32, dev, sms, stream);
     });
 }
 
@@ -775,17 +916,15 @@ int et_w4_experts(const void* x, const int32_t* topk_idx, const float* topk_w, c
         a.T_max = T_max;
         a.N = F;
         a.K = H;
-        a.group = group;
         a.E = E;
         a.k = k;
         a.hdr = reinterpret_cast<EtHeader*>(ws);
         const int rows = d_T ? T_max : T, R = rows * k;
-        // a pass takes the rows an expert has on average, with room for twice as many;
-        // the down products also keep fp32 rows by token, which leaves room for 16
-        const int avg = (R + E - 1) / E;
-        const int width = avg <= 4 ? 8 : avg <= 8 ? 16 : 32;
-        const int up_rows = rows < width ? rows : width, down_rows = up_rows < 16 ? up_rows : 16;
-        if ((rc = w4_launch_nt<kW4GateUp>(a, rows, up_rows, dev, sms, stream))) return rc;
+        // a pass takes twice the rows an expert has on average: 4, 8, 16 or 32
+        const int avg2 = 2 * ((R + E - 1) / E);
+        int width = avg2 <= 4 ? 4 : avg2 <= 8 ? 8 : avg2 <= 16 ? 16 : 32;
+        width = rows < width ? rows : width;
+        if ((rc = w4_launch_group<kW4GateUp>(a, group, rows, width, dev, sms, stream))) return rc;
         W4Args b = a;
         b.x = h;
         b.q0 = static_cast<const uint8_t*>(q_down);
@@ -795,7 +934,7 @@ int et_w4_experts(const void* x, const int32_t* topk_idx, const float* topk_w, c
         b.out = static_cast<bf16*>(out);
         b.N = H;
         b.K = F;
-        return w4_launch_nt<kW4Down>(b, rows, down_rows, dev, sms, stream);
+        return w4_launch_group<kW4Down>(b, group, rows, width, dev, sms, stream);
     });
 }
 
