@@ -422,7 +422,7 @@ int et_block_norm_bwd(const void* x, const void* y, const void* gamma_post, cons
  * group, q = 8 + round-half-even(w / scale) within 0..15; a group whose scale
  * is 0 becomes zeros, one with an infinity or NaN a scale of NaN (and q = 8).
  * et_w4_dequantize gives bf16(w[n,k]) back, for batches beyond the calls
- * below (through et_moe_layer or et_splitk_gemm).  1 <= E <= 65536.
+ * below (through et_moe_layer or et_splitk_gemm).  E * N <= 2^32.
  *
  * et_w4_gemv: Y[M,N] = bf16( X w^T ), X bf16 [M_max,K], Y bf16 [M_max,N], rows
  * >= M untouched; 1 <= M_max <= 64.

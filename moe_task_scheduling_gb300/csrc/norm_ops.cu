@@ -23,7 +23,7 @@ struct NormArgs {
     const bf16* gamma_post;  // [H] or null
     const void* gate;        // bf16 [H], fp32 [T], bf16 [T, H] or null
     const bf16* gamma_pre;   // [H] or null
-    float scale, eps;
+    float scale, eps, inv_H;
     int gate_kind;
     const int32_t* d_T;
     int T_host, T_max, H;
@@ -99,24 +99,8 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[32], int& n) {
     return v;
 }
 
-// Gate values of columns [c, c + 8) of row t.
-template <bool VEC>
-__device__ __forceinline__ void gate8(const NormArgs& p, int t, int c, float* g) {
-    if (p.gate_kind == kGateNone) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = 1.0f;
-    } else if (p.gate_kind == kGateToken) {
-        const float v = static_cast<const float*>(p.gate)[t];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = v;
-    } else {
-        const bf16* row = static_cast<const bf16*>(p.gate) +
-                          (p.gate_kind == kGateFull ? static_cast<size_t>(t) * p.H : 0);
-        const Vec8 v = load8<VEC>(row, c, p.H);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = v[i];
-    }
-}
+// 1 / sqrt(sum / H + eps)
+__device__ __forceinline__ float inv_rms(float sum, float inv_H, float eps) { return rsqrtf(sum * inv_H + eps); }
 
 // V vectors of 8 columns a thread; ROW: one row a CTA, else one row a warp.
 template <int V, bool VEC, bool ROW>
@@ -132,43 +116,45 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormArgs p) {
     for (int t = blockIdx.x * rows_cta + (ROW ? 0 : threadIdx.x >> 5); t < T; t += gridDim.x * rows_cta) {
         const size_t off = static_cast<size_t>(t) * H;
         float z[V][8];
-        Vec8 yv[V];
+        Vec8 yv[V], gv[V];
         float ss = 0.0f;
+        const bool vec_gate = p.gate_kind == kGateFull || p.gate_kind == kGateChannel;
+        const bf16* grow = static_cast<const bf16*>(p.gate) + (p.gate_kind == kGateFull ? off : 0);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
+        for (int j = 0; j < V; ++j) {  // every load of the row before the first sum
             const int c = (j * width + lane) * 8;
             const Vec8 xv = load8<VEC>(p.x + off, c, H);
+            yv[j] = p.y ? load8<VEC>(p.y + off, c, H) : Vec8{};
+            gv[j] = vec_gate ? load8<VEC>(grow, c, H) : Vec8{};
 #pragma unroll
             for (int i = 0; i < 8; ++i) z[j][i] = xv[i];
-            yv[j] = p.y ? load8<VEC>(p.y + off, c, H) : Vec8{};
+        }
+        const float gtok = p.gate_kind == kGateToken ? static_cast<const float*>(p.gate)[t] : 1.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss += yv[j][i] * yv[j][i];
-        }
         float ry = 1.0f;
-        if (p.y && p.gamma_post) ry = 1.0f / sqrtf(row_sum<ROW>(ss, red, sums) / H + p.eps);
+        if (p.y && p.gamma_post) ry = inv_rms(row_sum<ROW>(ss, red, sums), p.inv_H, p.eps);
         float zz = 0.0f;
+        const float gs = p.scale * gtok;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int c = (j * width + lane) * 8;
             if (p.y && c < H) {
-                float g[8];
-                gate8<VEC>(p, t, c, g);
                 const Vec8 gp = p.gamma_post ? load8<VEC>(p.gamma_post, c, H) : Vec8{};
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float n = p.gamma_post ? yv[j][i] * ry * gp[i] : yv[j][i];
-                    z[j][i] += p.scale * g[i] * n;
+                    z[j][i] += (vec_gate ? gs * gv[j][i] : gs) * n;  // 0 past H, where y is 0
                 }
-                if (!VEC)  // columns past H hold no value (a per-token gate is not zero there)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) z[j][i] = c + i < H ? z[j][i] : 0.0f;
             }
             if (p.x_out && c < H) store8<VEC>(p.x_out + off, c, H, z[j]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) zz += z[j][i] * z[j][i];
         }
         if (p.x_hat) {
-            const float rz = 1.0f / sqrtf(row_sum<ROW>(zz, red, sums) / H + p.eps);
+            const float rz = inv_rms(row_sum<ROW>(zz, red, sums), p.inv_H, p.eps);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int c = (j * width + lane) * 8;
@@ -184,80 +170,153 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormArgs p) {
     }
 }
 
+// Two sums over the row's threads with one barrier (see row_sum).
+template <bool ROW>
+__device__ __forceinline__ float2 row_sum2(float2 v, float (*red)[32], float (*red2)[32], int& n) {
+    v.x = warp_sum(v.x);
+    v.y = warp_sum(v.y);
+    if (ROW) {
+        const int slot = n++ & 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        if (lane == 0) { red[slot][warp] = v.x; red2[slot][warp] = v.y; }
+        __syncthreads();
+        const bool in = lane < static_cast<int>(blockDim.x >> 5);
+        v.x = warp_sum(in ? red[slot][lane] : 0.0f);
+        v.y = warp_sum(in ? red2[slot][lane] : 0.0f);
+    }
+    return v;
+}
+
 // The gradient.  A row's statistics are recomputed from x and y (they are read
 // anyway).  The parameter gradients are summed over this CTA's rows in
 // registers, thread by thread for its own columns, then over CTAs by
 // norm_sum_kernel in a fixed order.
-template <int V, bool VEC, bool ROW>
-__global__ void __launch_bounds__(V > 1 ? 1024 : 512) norm_bwd_kernel(const NormArgs p) {
-    __shared__ float red[2][32];
+//
+// STAGED (whole rows a CTA, 16-byte accesses): the five input rows of the next
+// row of this CTA are copied to shared memory while the current one is worked
+// on, and each thread reads back only what it copied itself, so the copies need
+// no barrier.  Three sums a row (mean y^2; mean z^2 with the second norm's
+// projection; the first norm's projection) are three barriers.
+// MAXT: most threads, which bounds the registers (16 columns a thread take 128).
+enum NormRow { kRowX = 0, kRowY = 1, kRowDz = 2, kRowDh = 3, kRowGate = 4, kRowArrays = 5 };
+
+template <int V, bool VEC, bool ROW, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormArgs p) {
+    constexpr bool STAGED = VEC && ROW;
+    __shared__ float red[2][32], red2[2][32];
     int sums = 0;
-    extern __shared__ float acc_sm[];  // !ROW: [warps][3][256]
+    extern __shared__ __align__(16) uint8_t dyn[];  // STAGED: [2][5][H] bf16; !ROW: [warps][3][256] floats
     bool ok;
-    int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
+    const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
     const int H = p.H;
     const int width = ROW ? blockDim.x : 32;
     const int lane = ROW ? threadIdx.x : threadIdx.x & 31;
     const int rows_cta = ROW ? 1 : blockDim.x >> 5;
+    const int step = gridDim.x * rows_cta;
+    const bool post = p.y && p.gamma_post;
+    const bool full = p.gate_kind == kGateFull;
     float a_post[V][8], a_pre[V][8], a_gate[V][8];
 #pragma unroll
     for (int j = 0; j < V; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i) a_post[j][i] = a_pre[j][i] = a_gate[j][i] = 0.0f;
 
-    for (int t = blockIdx.x * rows_cta + (ROW ? 0 : threadIdx.x >> 5); t < T; t += gridDim.x * rows_cta) {
-        const size_t off = static_cast<size_t>(t) * H;
-        Vec8 xv[V], yv[V], dz[V], dh[V];
-        float ss = 0.0f;
+    auto stage = [&](int t, int buf) {
+        if (STAGED && t < T) {
+            const size_t off = static_cast<size_t>(t) * H;
+            const bf16* src[kRowArrays] = {p.x, p.y, p.d_x_out, p.d_x_hat, full ? static_cast<const bf16*>(p.gate) : nullptr};
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = (j * width + lane) * 8;
-            xv[j] = load8<VEC>(p.x + off, c, H);
-            yv[j] = p.y ? load8<VEC>(p.y + off, c, H) : Vec8{};
-            dz[j] = p.d_x_out ? load8<VEC>(p.d_x_out + off, c, H) : Vec8{};
-            dh[j] = p.d_x_hat ? load8<VEC>(p.d_x_hat + off, c, H) : Vec8{};
+            for (int j = 0; j < V; ++j) {
+                const int c = (j * width + lane) * 8;
+                if (c < H)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss += yv[j][i] * yv[j][i];
+                    for (int a = 0; a < kRowArrays; ++a)
+                        if (src[a]) cp_async16(smem_addr(dyn) + ((buf * kRowArrays + a) * H + c) * 2, src[a] + off + c);
+            }
         }
-        const bool post = p.y && p.gamma_post;
+        if (STAGED) cp_async_commit();
+    };
+    // columns [c, c + 8) of the current row of one input (zeros where it is not given)
+    auto row8 = [&](int a, const bf16* base, int t, int buf, int c) -> Vec8 {
+        if (!base) return Vec8{};
+        if (STAGED) {
+            Vec8 v{};
+            if (c < H) {
+                const uint4 q = *reinterpret_cast<const uint4*>(dyn + (static_cast<size_t>(buf * kRowArrays + a) * H + c) * 2);
+                v.u[0] = q.x; v.u[1] = q.y; v.u[2] = q.z; v.u[3] = q.w;
+            }
+            return v;
+        }
+        return load8<VEC>(base + static_cast<size_t>(t) * H, c, H);
+    };
+    // scale * gate of columns [c, c + 8)
+    auto gate_of = [&](int t, int buf, int c, float gs, float* g) {
+        if (full || p.gate_kind == kGateChannel) {
+            const Vec8 v = full ? row8(kRowGate, static_cast<const bf16*>(p.gate), t, buf, c)
+                                : load8<VEC>(static_cast<const bf16*>(p.gate), c, H);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = gs * v[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = gs;
+        }
+    };
+
+    int buf = 0;
+    const int t0 = blockIdx.x * rows_cta + (ROW ? 0 : threadIdx.x >> 5);
+    stage(t0, 0);
+    for (int t = t0; t < T; t += step, buf ^= 1) {
+        stage(t + step, buf ^ 1);  // this thread has read that buffer's last row
+        if (STAGED) cp_async_wait<1>();
+        const size_t off = static_cast<size_t>(t) * H;
+        float ss = 0.0f;
+        if (post)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const Vec8 yv = row8(kRowY, p.y, t, buf, (j * width + lane) * 8);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ss += yv[i] * yv[i];
+            }
+        const float gs = p.scale * (p.gate_kind == kGateToken ? static_cast<const float*>(p.gate)[t] : 1.0f);
         float ry = 1.0f;
-        if (post) ry = 1.0f / sqrtf(row_sum<ROW>(ss, red, sums) / H + p.eps);
+        if (post) ry = inv_rms(row_sum<ROW>(ss, red, sums), p.inv_H, p.eps);
         // z, and with it the statistics of the second norm and sum(d_x_hat gamma_pre z)
-        float z[V][8], zz = 0.0f, az = 0.0f;
+        float z[V][8];
+        float2 za = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int c = (j * width + lane) * 8;
+            const Vec8 xv = row8(kRowX, p.x, t, buf, c);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) z[j][i] = xv[j][i];
+            for (int i = 0; i < 8; ++i) z[j][i] = xv[i];
             if (c < H) {
                 if (p.y) {
                     float g[8];
-                    gate8<VEC>(p, t, c, g);
+                    gate_of(t, buf, c, gs, g);
+                    const Vec8 yv = row8(kRowY, p.y, t, buf, c);
                     const Vec8 gp = post ? load8<VEC>(p.gamma_post, c, H) : Vec8{};
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        z[j][i] += p.scale * g[i] * (post ? yv[j][i] * ry * gp[i] : yv[j][i]);
-                    if (!VEC)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) z[j][i] = c + i < H ? z[j][i] : 0.0f;
+                        z[j][i] += g[i] * (post ? yv[i] * ry * gp[i] : yv[i]);  // 0 past H, where y is 0
                 }
                 if (p.d_x_hat) {
+                    const Vec8 dh = row8(kRowDh, p.d_x_hat, t, buf, c);
                     const Vec8 gp = load8<VEC>(p.gamma_pre, c, H);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        zz += z[j][i] * z[j][i];
-                        az += dh[j][i] * gp[i] * z[j][i];
+                        za.x += z[j][i] * z[j][i];
+                        za.y += dh[i] * gp[i] * z[j][i];
                     }
                 }
             }
         }
         float rz = 0.0f, k2 = 0.0f;
         if (p.d_x_hat) {
-            rz = 1.0f / sqrtf(row_sum<ROW>(zz, red, sums) / H + p.eps);
-            k2 = row_sum<ROW>(az, red, sums) / H * rz * rz * rz;
+            za = row_sum2<ROW>(za, red, red2, sums);
+            rz = inv_rms(za.x, p.inv_H, p.eps);
+            k2 = za.y * p.inv_H * rz * rz * rz;
         }
         // d z, the parameter gradients, and sum(d n gamma_post y)
-        float by = 0.0f, dgt = 0.0f;
+        float2 bg = make_float2(0.0f, 0.0f);
         float d[V][8];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -265,58 +324,60 @@ __global__ void __launch_bounds__(V > 1 ? 1024 : 512) norm_bwd_kernel(const Norm
 #pragma unroll
             for (int i = 0; i < 8; ++i) d[j][i] = 0.0f;
             if (c < H) {
+                const Vec8 dz = row8(kRowDz, p.d_x_out, t, buf, c);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) d[j][i] = dz[j][i];
+                for (int i = 0; i < 8; ++i) d[j][i] = dz[i];
                 if (p.d_x_hat) {
+                    const Vec8 dh = row8(kRowDh, p.d_x_hat, t, buf, c);
                     const Vec8 gp = load8<VEC>(p.gamma_pre, c, H);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        d[j][i] += rz * (dh[j][i] * gp[i]) - z[j][i] * k2;
-                        a_pre[j][i] += dh[j][i] * (z[j][i] * rz);
+                        d[j][i] += rz * (dh[i] * gp[i]) - z[j][i] * k2;
+                        a_pre[j][i] += dh[i] * (z[j][i] * rz);
                     }
                 }
                 store8<VEC>(p.dx + off, c, H, d[j]);
                 if (p.y) {
                     float g[8], dgf[8];
-                    gate8<VEC>(p, t, c, g);
+                    gate_of(t, buf, c, gs, g);
+                    const Vec8 yv = row8(kRowY, p.y, t, buf, c);
                     const Vec8 gp = post ? load8<VEC>(p.gamma_post, c, H) : Vec8{};
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float u = yv[j][i] * ry;  // the normalised value
-                        const float n = post ? u * gp[i] : yv[j][i];
+                        const float u = yv[i] * ry;  // the normalised value
+                        const float n = post ? u * gp[i] : yv[i];
                         dgf[i] = p.scale * n * d[j][i];
-                        d[j][i] *= p.scale * g[i];  // d n
+                        d[j][i] *= g[i];  // d n
                         a_post[j][i] += d[j][i] * u;
                         if (post) {
                             d[j][i] *= gp[i];
-                            by += d[j][i] * yv[j][i];
+                            bg.x += d[j][i] * yv[i];
                         }
                         a_gate[j][i] += dgf[i];
-                        dgt += dgf[i];
+                        bg.y += dgf[i];
                     }
                     if (p.d_gate_full) store8<VEC>(p.d_gate_full + off, c, H, dgf);
                 }
             }
         }
         if (p.y) {
-            float k1 = 0.0f;
-            if (post) k1 = row_sum<ROW>(by, red, sums) / H * ry * ry * ry;
-            if (p.d_gate_token) {
-                dgt = row_sum<ROW>(dgt, red, sums);
-                if (lane == 0) p.d_gate_token[t] = dgt;
-            }
+            if (post || p.d_gate_token) bg = row_sum2<ROW>(bg, red, red2, sums);
+            const float k1 = post ? bg.x * p.inv_H * ry * ry * ry : 0.0f;
+            if (p.d_gate_token && lane == 0) p.d_gate_token[t] = bg.y;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int c = (j * width + lane) * 8;
                 if (c < H) {
+                    const Vec8 yv = row8(kRowY, p.y, t, buf, c);
                     float o[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = post ? ry * d[j][i] - yv[j][i] * k1 : d[j][i];
+                    for (int i = 0; i < 8; ++i) o[i] = post ? ry * d[j][i] - yv[i] * k1 : d[j][i];
                     store8<VEC>(p.dy + off, c, H, o);
                 }
             }
         }
     }
+    if (STAGED) cp_async_wait<0>();
 
     if (!ok) return;
     float* part = p.part + static_cast<size_t>(blockIdx.x) * 3 * H;
@@ -334,6 +395,7 @@ __global__ void __launch_bounds__(V > 1 ? 1024 : 512) norm_bwd_kernel(const Norm
             }
     } else {  // one row a warp (H <= 256): the CTA's warps in order
         const int warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+        float* acc_sm = reinterpret_cast<float*>(dyn);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float* a = acc_sm + warp * 768 + lane * 8 + i;
@@ -359,24 +421,24 @@ struct NormSumArgs {
     int T_max;
 };
 
-// Column sums of the partial rows: 32 columns x 8 row groups a CTA.
-__global__ void __launch_bounds__(256) norm_sum_kernel(const NormSumArgs p) {
-    __shared__ float red[8][33];
+// Column sums of the partial rows: 32 columns x 32 row groups a CTA, so that the
+// (L2-resident) loads of a column are in flight together.
+__global__ void __launch_bounds__(1024) norm_sum_kernel(const NormSumArgs p) {
+    __shared__ float red[32][33];
     if (p.d_T && (*p.d_T < 0 || *p.d_T > p.T_max)) return;
     float* out = p.out[blockIdx.y];
     if (!out) return;
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), grp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
     float s = 0.0f;
     if (c < p.H)
-        for (int g = grp; g < p.parts; g += 8) s += p.part[(static_cast<size_t>(g) * 3 + blockIdx.y) * p.H + c];
-    red[grp][threadIdx.x & 31] = s;
+#pragma unroll 10
+        for (int g = grp; g < p.parts; g += 32)
+            s += __ldcg(p.part + (static_cast<size_t>(g) * 3 + blockIdx.y) * p.H + c);
+    red[grp][lane] = s;
     __syncthreads();
-    if (grp == 0 && c < p.H) {
-        s = 0.0f;
-#pragma unroll
-        for (int g = 0; g < 8; ++g) s += red[g][threadIdx.x];
-        out[c] = s;
-    }
+    s = warp_sum(red[lane][grp]);  // warp grp: its column's 32 groups
+    if (lane == 0 && blockIdx.x * 32 + grp < p.H) out[blockIdx.x * 32 + grp] = s;
 }
 
 size_t norm_ws_bytes(int T_max, int H) {
@@ -420,12 +482,10 @@ bool norm_vec(int H, std::initializer_list<const void*> ps) {
     return true;
 }
 
-// Threads of a row: one vector of 8 columns each up to `most`, then two.
-int norm_threads(int H, int most) {
+// Threads of a row: 16 columns (two vectors) each, 8 for a row of up to 512.
+int norm_threads(int H) {
     const int vecs = (H + 7) / 8;
-    int t = (vecs + 31) / 32 * 32;
-    if (t > most) t = ((vecs + 1) / 2 + 31) / 32 * 32;
-    return t;
+    return ((vecs > 64 ? (vecs + 1) / 2 : vecs) + 31) / 32 * 32;
 }
 
 template <bool VEC>
@@ -436,27 +496,46 @@ cudaError_t launch_fwd(const NormArgs& a, int rows, int sms, void* stream) {
         grid = grid < 8 * sms ? grid : 8 * sms;
         return api_launch(norm_fwd_kernel<1, VEC, false>, grid, warps * 32, 0, stream, a);
     }
-    const int th = norm_threads(a.H, 1024);
-    const int most = sms * (2048 / th < 32 ? 2048 / th : 32);
+    const int th = norm_threads(a.H);
+    const int most = sms * (1024 / th);
     const int grid = rows < most ? rows : most;
-    if (th * 8 >= a.H) return api_launch(norm_fwd_kernel<1, VEC, true>, grid, th, 0, stream, a);
+    if (a.H <= 512) return api_launch(norm_fwd_kernel<1, VEC, true>, grid, th, 0, stream, a);
     return api_launch(norm_fwd_kernel<2, VEC, true>, grid, th, 0, stream, a);
 }
 
 // The grid is also the number of partial rows that norm_sum_kernel reads.
+template <int V, bool VEC, int MAXT>
+cudaError_t launch_bwd_rows(const NormArgs& a, int dev, int sms, int threads, int rows, int parts_max, int* parts,
+                            void* stream) {
+    static SmemOptIn opt;
+    const int smem = VEC ? 2 * kRowArrays * a.H * static_cast<int>(sizeof(bf16)) : 0;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = api_smem_opt_in(opt, dev, norm_bwd_kernel<V, VEC, true, MAXT>, kSmemLimit - 2048);
+        if (e != cudaSuccess) return e;
+    }
+    // CTAs an SM: one of more than 256 threads (128 registers each), else two
+    const int most = threads > 256 ? sms : 2 * sms;
+    *parts = rows < parts_max ? rows : parts_max;
+    *parts = *parts < most ? *parts : most;
+    return api_launch(norm_bwd_kernel<V, VEC, true, MAXT>, *parts, threads, smem, stream, a);
+}
+
 template <bool VEC>
-cudaError_t launch_bwd(const NormArgs& a, int rows, int parts_max, int* parts, void* stream) {
+cudaError_t launch_bwd(const NormArgs& a, int dev, int sms, int rows, int parts_max, int* parts, void* stream) {
     if (a.H <= 256) {
         const int warps = 8;
         const int need = (rows + warps - 1) / warps;
         *parts = need < parts_max ? need : parts_max;
-        return api_launch(norm_bwd_kernel<1, VEC, false>, *parts, warps * 32, warps * 768 * sizeof(float),
+        return api_launch(norm_bwd_kernel<1, VEC, false, 256>, *parts, warps * 32, warps * 768 * sizeof(float),
                           stream, a);
     }
-    *parts = rows < parts_max ? rows : parts_max;
-    const int th = norm_threads(a.H, 512);
-    if (th * 8 >= a.H) return api_launch(norm_bwd_kernel<1, VEC, true>, *parts, th, 0, stream, a);
-    return api_launch(norm_bwd_kernel<2, VEC, true>, *parts, th, 0, stream, a);
+    const int th = norm_threads(a.H);
+    // two staged rows of more than 11000 columns do not fit in shared memory
+    if (th > 512 || (VEC && 2 * kRowArrays * a.H * static_cast<int>(sizeof(bf16)) > kSmemLimit - 2048))
+        return launch_bwd_rows<2, false, 1024>(a, dev, sms, th, rows, parts_max, parts, stream);
+    if (a.H <= 512) return launch_bwd_rows<1, VEC, 256>(a, dev, sms, th, rows, parts_max, parts, stream);
+    if (th <= 256) return launch_bwd_rows<2, VEC, 256>(a, dev, sms, th, rows, parts_max, parts, stream);
+    return launch_bwd_rows<2, VEC, 512>(a, dev, sms, th, rows, parts_max, parts, stream);
 }
 
 }  // namespace
@@ -495,6 +574,7 @@ int et_block_norm(const void* x, const void* y, const void* gamma_post, const vo
         a.gamma_pre = static_cast<const bf16*>(gamma_pre);
         a.scale = scale;
         a.eps = eps;
+        a.inv_H = 1.0f / static_cast<float>(H);
         a.gate_kind = gate_kind;
         a.d_T = d_T;
         a.T_host = T;
@@ -544,6 +624,7 @@ int et_block_norm_bwd(const void* x, const void* y, const void* gamma_post, cons
         a.gamma_pre = static_cast<const bf16*>(gamma_pre);
         a.scale = scale;
         a.eps = eps;
+        a.inv_H = 1.0f / static_cast<float>(H);
         a.gate_kind = gate_kind;
         a.d_T = d_T;
         a.T_host = T;
@@ -563,14 +644,14 @@ int et_block_norm_bwd(const void* x, const void* y, const void* gamma_post, cons
         if (rows > 0) {
             const bool vec = norm_vec(H, {x, y, gamma_post, gate_kind == kGateToken ? nullptr : gate, gamma_pre,
                                           d_x_out, d_x_hat, dx, dy, a.d_gate_full});
-            const cudaError_t e = vec ? launch_bwd<true>(a, rows, parts_max, &parts, stream)
-                                      : launch_bwd<false>(a, rows, parts_max, &parts, stream);
+            const cudaError_t e = vec ? launch_bwd<true>(a, dev, sms, rows, parts_max, &parts, stream)
+                                      : launch_bwd<false>(a, dev, sms, rows, parts_max, &parts, stream);
             if (e != cudaSuccess) return api_fail_cuda(e, "launch of the block norm's backward kernel");
         }
         float* d_gate_channel = gate_kind == kGateChannel ? static_cast<float*>(d_gate) : nullptr;
         if (d_gamma_post || d_gamma_pre || d_gate_channel) {
             const NormSumArgs s{a.part, {d_gamma_post, d_gamma_pre, d_gate_channel}, H, parts, d_T, T_max};
-            const cudaError_t e = api_launch(norm_sum_kernel, dim3((H + 31) / 32, 3), 256, 0, stream, s);
+            const cudaError_t e = api_launch(norm_sum_kernel, dim3((H + 31) / 32, 3), 1024, 0, stream, s);
             if (e != cudaSuccess) return api_fail_cuda(e, "launch of the block norm's parameter sums");
         }
         return ET_OK;

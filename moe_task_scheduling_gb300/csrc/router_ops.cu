@@ -39,14 +39,16 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// One row a warp, expert e = lane + 32 i in register i.  The k rounds of the
-// selection also give the row's largest logit, so the softmax needs no max
-// pass.  Sums over rows: per warp in registers, per CTA in shared memory, over
-// CTAs by the last one to finish -- each in a fixed order, so that losses and
-// mean probabilities are the same bits on every run.
+// One row a warp, expert e = lane + 32 i in register i; the next row's logits are
+// loaded while the current one is worked on.  The k rounds of the selection also
+// give the row's largest logit, so the softmax needs no max pass.  Sums over
+// rows: per warp in registers (32 rows, then once more, so that long sums stay
+// short), per CTA in shared memory, over CTAs by the last one to finish -- each
+// in a fixed order, so that losses and mean probabilities are the same bits on
+// every run.  All in fp32: fp64 runs at 1/64 of it here.
 template <int EPL>
 __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_topk_kernel(const RouterArgs p) {
-    extern __shared__ float sm[];
+    extern __shared__ __align__(16) float sm[];  // [warps][E], then the last CTA's sums
     __shared__ int hist[kRouterEMax];
     __shared__ float zsum[kRouterWarpsMax];
     __shared__ int nsum[kRouterWarpsMax];
@@ -56,24 +58,34 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_topk_kernel(const
     bool ok;
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
     if (!ok) return;
+    const int t0 = blockIdx.x * nwarps + warp, step = gridDim.x * nwarps;
+    auto load = [&](int t, float (&v)[EPL], int& on) {
+        const float* L = p.logits + static_cast<size_t>(t) * E;
+        on = t < T && (!p.mask || p.mask[t] != 0);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) v[i] = t < T && lane + 32 * i < E ? L[lane + 32 * i] : -INFINITY;
+    };
+    float nv[EPL];
+    int non;
+    load(t0, nv, non);
     for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
     __syncthreads();
 
-    float accp[EPL], accz = 0.0f;
-    int accn = 0;
+    float accp[EPL], bigp[EPL], accz = 0.0f, bigz = 0.0f;
+    int accn = 0, rows32 = 0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) accp[i] = 0.0f;
+    for (int i = 0; i < EPL; ++i) accp[i] = bigp[i] = 0.0f;
 
-    for (int t = blockIdx.x * nwarps + warp; t < T; t += gridDim.x * nwarps) {
-        const float* L = p.logits + static_cast<size_t>(t) * E;
+    for (int t = t0; t < T; t += step) {
         float v[EPL];
         uint32_t key[EPL];
+        const int masked_in = non;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            const int e = lane + 32 * i;
-            v[i] = e < E ? L[e] : -INFINITY;
-            key[i] = e < E ? logit_key(v[i]) : 0u;
+            v[i] = nv[i];
+            key[i] = lane + 32 * i < E ? logit_key(v[i]) : 0u;
         }
+        load(t + step, nv, non);
         float myL = -INFINITY;
         int myE = -1;
 #pragma unroll 1
@@ -94,23 +106,27 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_topk_kernel(const
             if (lane == j) { myL = Lw; myE = static_cast<int>(e); }
         }
         const float L0 = __shfl_sync(0xffffffffu, myL, 0);
-        const bool live = (!p.mask || p.mask[t] != 0) && !(L0 == -INFINITY);
+        const bool live = masked_in && !(L0 == -INFINITY);
         const bool on = live && lane < k && !(myL == -INFINITY);
         const float ex = on ? expf(myL - L0) : 0.0f;
-        const float z = warp_sum(ex);
+        float pe[EPL], s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            pe[i] = live && lane + 32 * i < E ? expf(v[i] - L0) : 0.0f;
+            s += pe[i];
+        }
+        float z = ex;
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) {  // both sums, interleaved
+            z += __shfl_xor_sync(0xffffffffu, z, off);
+            s += __shfl_xor_sync(0xffffffffu, s, off);
+        }
         if (lane < k) {
             p.idx[static_cast<size_t>(t) * k + lane] = on ? myE : -1;
             p.w[static_cast<size_t>(t) * k + lane] = on ? ex / z : 0.0f;
         }
         if (on) atomicAdd(&hist[myE], 1);
         if (live) {
-            float pe[EPL], s = 0.0f;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                pe[i] = lane + 32 * i < E ? expf(v[i] - L0) : 0.0f;
-                s += pe[i];
-            }
-            s = warp_sum(s);
             const float inv = 1.0f / s;
             const float lse = L0 + logf(s);
 #pragma unroll
@@ -118,84 +134,113 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_topk_kernel(const
             accz += lse * lse;
             ++accn;
         }
+        if (++rows32 == 32) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) { bigp[i] += accp[i]; accp[i] = 0.0f; }
+            bigz += accz;
+            accz = 0.0f;
+            rows32 = 0;
+        }
     }
 
     // CTA sums, warps in order
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-        if (lane + 32 * i < E) sm[warp * E + lane + 32 * i] = accp[i];
-    if (lane == 0) { zsum[warp] = accz; nsum[warp] = accn; }
+        if (lane + 32 * i < E) sm[warp * E + lane + 32 * i] = bigp[i] + accp[i];
+    if (lane == 0) { zsum[warp] = bigz + accz; nsum[warp] = accn; }
     __syncthreads();
-    const int b = blockIdx.x;
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        float s = 0.0f;
-        for (int w = 0; w < nwarps; ++w) s += sm[w * E + e];
-        p.part_p[b * E + e] = s;
-        p.part_c[b * E + e] = hist[e];
-    }
-    if (threadIdx.x == 0) {
-        float s = 0.0f;
-        int n = 0;
-        for (int w = 0; w < nwarps; ++w) { s += zsum[w]; n += nsum[w]; }
-        p.part_z[b] = s;
-        p.part_n[b] = n;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        __threadfence();
-        const int n = atomicAdd(&p.hdr->exit_count, 1);
-        last = n == static_cast<int>(gridDim.x) - 1;
-        if (last) p.hdr->exit_count = 0;
-        __threadfence();
-    }
-    __syncthreads();
-    if (!last) return;
-
-    // the last CTA: sums over CTAs (fp64: the order is fixed, the length is not)
-    const int G = gridDim.x;
-    double bal = 0.0;
-    __shared__ double red[kRouterWarpsMax];
-    __shared__ int n_all;
-    __shared__ double z_all;
+    const int b = blockIdx.x, G = gridDim.x;
+    const bool one = G == 1;  // one CTA: its sums are the call's
     if (warp == 0) {
-        int n = 0;
-        double z = 0.0;
-        for (int g = lane; g < G; g += 32) {
-            n += __ldcg(p.part_n + g);
-            z += __ldcg(p.part_z + g);
+        float s = warp_sum(lane < nwarps ? zsum[lane] : 0.0f);
+        const int n = __reduce_add_sync(0xffffffffu, lane < nwarps ? nsum[lane] : 0);
+        __syncwarp();
+        if (lane == 0) {
+            if (one) { zsum[0] = s; nsum[0] = n; }
+            else { p.part_z[b] = s; p.part_n[b] = n; }
         }
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) {
-            n += __shfl_xor_sync(0xffffffffu, n, off);
-            z += __shfl_xor_sync(0xffffffffu, z, off);
-        }
-        if (lane == 0) { n_all = n; z_all = z; }
     }
-    __syncthreads();
-    const double rows = n_all > 0 ? n_all : 1;
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        double s = 0.0;
-        int c = 0;
-        for (int g = 0; g < G; ++g) {
-            s += __ldcg(p.part_p + g * E + e);
-            c += __ldcg(p.part_c + g * E + e);
+        float s = 0.0f;
+#pragma unroll 8
+        for (int w = 0; w < nwarps; ++w) s += sm[w * E + e];
+        if (one) {
+            sm[e] = s;
+        } else {
+            p.part_p[b * E + e] = s;
+            p.part_c[b * E + e] = hist[e];
         }
-        const double P = s / rows;
-        if (p.counts) p.counts[e] = c;
-        if (p.mean_prob) p.mean_prob[e] = static_cast<float>(P);
-        bal += c / (rows * k) * P;
     }
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) bal += __shfl_xor_sync(0xffffffffu, bal, off);
-    if (lane == 0) red[warp] = bal;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        double s = 0.0;
-        for (int w = 0; w < nwarps; ++w) s += red[w];
-        if (p.n_routed) *p.n_routed = n_all;
-        if (p.losses) {
-            p.losses[0] = static_cast<float>(E * s);
-            p.losses[1] = static_cast<float>(z_all / rows);
+    if (!one) {
+        if (threadIdx.x == 0) {
+            __threadfence();
+            const int n = atomicAdd(&p.hdr->exit_count, 1);
+            last = n == G - 1;
+            if (last) p.hdr->exit_count = 0;
+            __threadfence();
+        }
+        __syncthreads();
+        if (!last) return;
+        // The last CTA: sums over CTAs.  As many threads as fit share an expert's
+        // parts (thread group x expert), so that all their loads are in flight.
+        if (warp == 0) {
+            int n = 0;
+            float z = 0.0f;
+            for (int g = lane; g < G; g += 32) {
+                n += __ldcg(p.part_n + g);
+                z += __ldcg(p.part_z + g);
+            }
+            z = warp_sum(z);
+            n = __reduce_add_sync(0xffffffffu, n);
+            if (lane == 0) { zsum[0] = z; nsum[0] = n; }
+        }
+        const int groups = max(1, static_cast<int>(blockDim.x) / E);
+        int* csum = reinterpret_cast<int*>(sm + groups * E);
+        for (int o = threadIdx.x; o < groups * E; o += blockDim.x) {
+            const int e = o % E;
+            float s = 0.0f;
+            int c = 0;
+#pragma unroll 10
+            for (int g = o / E; g < G; g += groups) {
+                s += __ldcg(p.part_p + g * E + e);
+                c += __ldcg(p.part_c + g * E + e);
+            }
+            sm[o] = s;
+            csum[o] = c;
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < E; e += blockDim.x) {
+            float s = 0.0f;
+            int c = 0;
+#pragma unroll 8
+            for (int g = 0; g < groups; ++g) {
+                s += sm[g * E + e];
+                c += csum[g * E + e];
+            }
+            sm[e] = s;  // this thread's column alone reads group 0's entry
+            hist[e] = c;
+        }
+        __syncthreads();
+    }
+    // sm[e], hist[e], zsum[0], nsum[0] are the sums of the call
+    if (warp == 0) {
+        const int n = nsum[0];
+        const float rows = n > 0 ? static_cast<float>(n) : 1.0f;
+        float bal = 0.0f;
+        for (int e = lane; e < E; e += 32) {
+            const float P = sm[e] / rows;
+            if (p.counts) p.counts[e] = hist[e];
+            if (p.mean_prob) p.mean_prob[e] = P;
+            bal += static_cast<float>(hist[e]) / (rows * k) * P;
+        }
+        bal = warp_sum(bal);
+        if (lane == 0) {
+            if (p.n_routed) *p.n_routed = n;
+            if (p.losses) {
+                p.losses[0] = E * bal;
+                p.losses[1] = zsum[0] / rows;
+            }
         }
     }
 }
@@ -216,7 +261,9 @@ struct RouterBwdArgs {
 };
 
 // One row a warp; the softmax is recomputed from the logits (4 bytes an entry
-// read, 4 written: storing the probabilities would add as much again).
+// read, 4 written: storing the probabilities would add as much again).  The
+// next row's loads go out before the current row's work, and before the first
+// row's the loads of the counts, so that one memory latency is paid a warp.
 template <int EPL>
 __global__ void __launch_bounds__(256) router_bwd_kernel(const RouterBwdArgs p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
@@ -224,6 +271,24 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(const RouterBwdArgs p) 
     bool ok;
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
     if (!ok) return;
+    const int t0 = blockIdx.x * nwarps + warp, step = gridDim.x * nwarps;
+    struct Row {
+        float v[EPL], w, dw;
+        int e, on;
+    };
+    auto load = [&](int t, Row& r) {
+        const bool in = t < T, sel = in && lane < k && p.d_w;
+        const float* L = p.logits + static_cast<size_t>(t) * E;
+        const size_t o = static_cast<size_t>(t) * k + lane;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) r.v[i] = in && lane + 32 * i < E ? L[lane + 32 * i] : -INFINITY;
+        r.on = in && (!p.mask || p.mask[t] != 0);
+        r.e = sel ? p.idx[o] : -1;
+        r.w = sel ? p.w[o] : 0.0f;
+        r.dw = sel ? p.d_w[o] : 0.0f;
+    };
+    Row nx;
+    load(t0, nx);
     const int n = *p.n_routed;
     const float rows = n > 0 ? static_cast<float>(n) : 1.0f;
     const float db = p.d_losses ? p.d_losses[0] : 0.0f;
@@ -234,60 +299,55 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(const RouterBwdArgs p) 
         const int e = lane + 32 * i;
         cost[i] = e < E ? static_cast<float>(E) * (static_cast<float>(p.counts[e]) / (rows * k)) / rows : 0.0f;
     }
-    for (int t = blockIdx.x * nwarps + warp; t < T; t += gridDim.x * nwarps) {
-        const float* L = p.logits + static_cast<size_t>(t) * E;
-        float v[EPL], m = -INFINITY;
-        bool nan = false;
+    for (int t = t0; t < T; t += step) {
+        const Row c = nx;
+        load(t + step, nx);
+        float m = c.v[0];
+        bool nan = c.v[0] != c.v[0];
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const int e = lane + 32 * i;
-            v[i] = e < E ? L[e] : -INFINITY;
-            m = fmaxf(m, v[i]);
-            nan |= v[i] != v[i];
+        for (int i = 1; i < EPL; ++i) {
+            m = fmaxf(m, c.v[i]);
+            nan |= c.v[i] != c.v[i];
         }
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
         nan = __any_sync(0xffffffffu, nan);
-        const bool live = (!p.mask || p.mask[t] != 0) && (nan || !(m == -INFINITY));
+        const bool live = c.on && (nan || !(m == -INFINITY));
         float d[EPL];
         if (live) {
-            float pe[EPL], s = 0.0f, cp = 0.0f;
+            // where the index is -1 neither weight nor gradient is used
+            const float w = c.e >= 0 ? c.w : 0.0f, dw = c.e >= 0 ? c.dw : 0.0f;
+            float pe[EPL], s = 0.0f, cp = 0.0f, dot = w * dw;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
-                pe[i] = lane + 32 * i < E ? expf(v[i] - m) : 0.0f;
+                pe[i] = lane + 32 * i < E ? expf(c.v[i] - m) : 0.0f;
                 s += pe[i];
                 cp += pe[i] * cost[i];
             }
-            s = warp_sum(s);
-            cp = warp_sum(cp) / s;
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) {  // three sums, interleaved
+                s += __shfl_xor_sync(0xffffffffu, s, off);
+                cp += __shfl_xor_sync(0xffffffffu, cp, off);
+                dot += __shfl_xor_sync(0xffffffffu, dot, off);
+            }
             const float inv = 1.0f / s;
+            cp *= inv;
             const float zl = dz * (m + logf(s));
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
                 const float pr = pe[i] * inv;
                 d[i] = db * pr * (cost[i] - cp) + zl * pr;
             }
-            if (p.d_w) {
-                int e = -1;
-                float w = 0.0f, dw = 0.0f;
-                if (lane < k) {
-                    e = p.idx[static_cast<size_t>(t) * k + lane];
-                    if (e >= 0) {
-                        w = p.w[static_cast<size_t>(t) * k + lane];
-                        dw = p.d_w[static_cast<size_t>(t) * k + lane];
-                    }
-                }
-                const float dot = warp_sum(w * dw);
-                const float ds = w * (dw - dot);
-#pragma unroll 1
+            const float ds = w * (dw - dot);
+            if (p.d_w)
+#pragma unroll 4
                 for (int j = 0; j < k; ++j) {
-                    const int ej = __shfl_sync(0xffffffffu, e, j);
+                    const int ej = __shfl_sync(0xffffffffu, c.e, j);
                     const float dj = __shfl_sync(0xffffffffu, ds, j);
 #pragma unroll
                     for (int i = 0; i < EPL; ++i)
                         if (ej == lane + 32 * i) d[i] += dj;
                 }
-            }
         } else {
 #pragma unroll
             for (int i = 0; i < EPL; ++i) d[i] = 0.0f;
@@ -367,7 +427,10 @@ int et_router_topk(const float* logits, const uint8_t* token_mask, int32_t* topk
         const int warps = rows < kRouterWarpsMax ? rows : kRouterWarpsMax;
         int grid = ceil_div_i(rows, warps);
         grid = grid < kRouterParts ? grid : kRouterParts;
-        const size_t smem = sizeof(float) * warps * E;
+        // [warps][E] floats; the last CTA: max(1, threads / E) x E of a float and an int
+        const size_t sums = static_cast<size_t>(warps * 32 / E > 1 ? warps * 32 / E : 1) * E * 8;
+        const size_t rows_p = sizeof(float) * warps * E;
+        const size_t smem = rows_p > sums ? rows_p : sums;
         auto kernel = E <= 32 ? router_topk_kernel<1> : E <= 64 ? router_topk_kernel<2>
                     : E <= 128 ? router_topk_kernel<4> : router_topk_kernel<8>;
         const cudaError_t e = api_launch(kernel, grid, warps * 32, smem, stream, a);

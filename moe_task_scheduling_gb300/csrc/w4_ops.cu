@@ -588,6 +588,9 @@ __global__ void __launch_bounds__(kW4Warps * 32) w4_kernel(const W4Args p) {
 
 // ---------------------------------------------------------------- conversion
 
+constexpr int kConvRows = 8;       // rows of a CTA, one a warp: N is a multiple of 8, so they share an expert
+constexpr int kConvK = 4096;       // most inputs of a row a CTA takes
+
 struct W4ConvArgs {
     const bf16* w;
     const uint8_t* q;
@@ -595,76 +598,130 @@ struct W4ConvArgs {
     bf16* w_out;
     uint8_t* q_out;
     bf16* s_out;
-    int N, K, group;
-    long long rows;  // E * N
+    int N, K, group, chunk;  // chunk: inputs a CTA takes, a multiple of 256 (or all of K)
 };
 
-// Eight inputs a thread: 16 bytes in, 4 bytes out; the lanes of a group (4, 8 or
-// 16) share its largest magnitude by shuffles.
-__global__ void __launch_bounds__(256) w4_quantize_kernel(const W4ConvArgs p) {
-    const int per = p.K / 8;  // vectors of a row: a multiple of 4, groups never cross a row
-    const long long total = p.rows * per;
+// Eight inputs a lane and step (16 bytes), four steps in flight; the lanes of a
+// group (4, 8 or 16) share its largest magnitude by shuffles.  The scales of the
+// CTA's eight rows are collected in shared memory and stored 16 bytes a group.
+//
+// q = round-half-even(w / s) without a division: y = w * (1 / s), with a
+// reciprocal good to 2^-22, is within 2^-19 of w / s (|y| < 7.1).  w and s have 8 significant bits, so w / s
+// is either exactly half-way between two integers or at least 2^-10 away from
+// that; rounding y to a multiple of 2^-13 first brings the half-way cases back
+// and moves no other across.  Scales below 2^-126 (whose reciprocal overflows)
+// are divided by.
+__global__ void __launch_bounds__(kConvRows * 32) w4_quantize_kernel(const W4ConvArgs p) {
+    __shared__ __align__(16) __nv_bfloat16 sc[kConvK / 32][kConvRows];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const size_t row0 = static_cast<size_t>(blockIdx.x) * kConvRows, row = row0 + warp;
+    const int k0 = blockIdx.y * p.chunk, kn = min(p.chunk, p.K - k0);
     const int lanes = p.group / 8;
-    const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
-    // whole warps run to the last vector, so that every shuffle has its partners
-    const long long end = (total + 31) / 32 * 32;
-    for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < end; i += stride) {
-        const bool in = i < total;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (in) v = reinterpret_cast<const uint4*>(p.w)[i];
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-        float f[8];
-        uint32_t top = 0;  // largest magnitude as bits: NaN above infinity above all numbers
+    const uint4* src = reinterpret_cast<const uint4*>(p.w + row * p.K + k0);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.q_out + (row * p.K + k0) / 2);
+    const int vecs = kn / 8;
+    for (int base = 0; base < vecs; base += 128) {
+        uint4 v[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            f[j] = (j & 1) ? bf_hi(u[j >> 1]) : bf_lo(u[j >> 1]);
-            top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
+        for (int i = 0; i < 4; ++i) {
+            const int at = base + i * 32 + lane;
+            v[i] = at < vecs ? __ldcs(src + at) : make_uint4(0, 0, 0, 0);
         }
-        for (int off = 1; off < lanes; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-        const bool finite = top < 0x7f800000u;
-        const __nv_bfloat16 sb = finite ? __float2bfloat16_rn(__uint_as_float(top) / 7.0f)
-                                        : __float2bfloat16_rn(__uint_as_float(0x7fc00000u));
-        const float s = __bfloat162float(sb);
-        uint32_t out = 0x88888888u;  // zeros, where the scale is zero or not a number
-        if (s > 0.0f) {
-            out = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float r = fminf(fmaxf(rintf(f[j] / s), -8.0f), 7.0f);
-                out |= static_cast<uint32_t>(static_cast<int>(r) + 8) << (4 * j);
+        for (int i = 0; i < 4; ++i) {
+            const int at = base + i * 32 + lane;
+            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            // largest magnitude; NaN wins over infinity, infinity over every number
+            __nv_bfloat162 m2 = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&u[0]));
+#pragma unroll
+            for (int j = 1; j < 4; ++j)
+                m2 = __hmax2_nan(m2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&u[j])));
+            for (int off = 1; off < lanes; off <<= 1) {
+                const uint32_t o = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&m2), off);
+                m2 = __hmax2_nan(m2, *reinterpret_cast<const __nv_bfloat162*>(&o));
             }
-        }
-        if (in) {
-            reinterpret_cast<uint32_t*>(p.q_out)[i] = out;
-            if ((i & (lanes - 1)) == 0) {
-                const long long row = i / per;
-                const int g = static_cast<int>(i - row * per) / lanes;
-                const long long e = row / p.N;
-                const int n = static_cast<int>(row - e * p.N);
-                p.s_out[(e * (p.K / p.group) + g) * p.N + n] = sb;
+            const float top = __bfloat162float(__hmax_nan(__low2bfloat16(m2), __high2bfloat16(m2)));
+            const bool finite = top < __uint_as_float(0x7f800000u);
+            // bf16(top / 7): top has 8 bits, so top / 7 is a bf16 value or at least 2^-12
+            // of itself away from the middle between two; top * (1 / 7) rounds alike
+            const __nv_bfloat16 sb = __float2bfloat16_rn(finite ? top * (1.0f / 7.0f) : __uint_as_float(0x7fc00000u));
+            const float s = __bfloat162float(sb);
+            uint32_t out = 0x88888888u;  // zeros, where the scale is zero or not a number
+            if (s >= 1.17549435e-38f) {
+                float inv;
+                asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));
+                // t = 1536 + w / s in steps of 2^-13; adding 1.5 * 2^23 + 8 - 1536 leaves
+                // round-half-even(w / s) + 8 in the sum's low bits, which are added up
+                // at their places with the (known) high bits taken off at the end
+                out = 0u - 0x4b400000u * 0x11111111u;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float f = (j & 1) ? bf_hi(u[j >> 1]) : bf_lo(u[j >> 1]);
+                    const float t = __fmaf_rn(f, inv, 1536.0f);
+                    out += __float_as_uint(__fadd_rn(t, 12582920.0f - 1536.0f)) << (4 * j);
+                }
+            } else if (s > 0.0f) {
+                out = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float f = (j & 1) ? bf_hi(u[j >> 1]) : bf_lo(u[j >> 1]);
+                    const float r = fminf(fmaxf(rintf(f / s), -8.0f), 7.0f);
+                    out |= static_cast<uint32_t>(static_cast<int>(r) + 8) << (4 * j);
+                }
+            }
+            if (at < vecs) {
+                dst[at] = out;
+                if ((at & (lanes - 1)) == 0) sc[at / lanes][warp] = sb;
             }
         }
     }
+    __syncthreads();
+    const size_t e = row0 / p.N;
+    const int n0 = static_cast<int>(row0 - e * p.N), groups = p.K / p.group, g0 = k0 / p.group;
+    for (int g = threadIdx.x; g < kn / p.group; g += blockDim.x)
+        *reinterpret_cast<uint4*>(p.s_out + (e * groups + g0 + g) * p.N + n0) = *reinterpret_cast<const uint4*>(&sc[g][0]);
 }
 
-__global__ void __launch_bounds__(256) w4_dequantize_kernel(const W4ConvArgs p) {
-    const int per = p.K / 8;
-    const long long total = p.rows * per;
+// The same split.  128 + q by or-ing the nibble into bf16, minus 136, times the
+// scale: the first two are exact, the product is rounded once.
+__global__ void __launch_bounds__(kConvRows * 32) w4_dequantize_kernel(const W4ConvArgs p) {
+    __shared__ __align__(16) __nv_bfloat16 sc[kConvK / 32][kConvRows];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const size_t row0 = static_cast<size_t>(blockIdx.x) * kConvRows, row = row0 + warp;
+    const int k0 = blockIdx.y * p.chunk, kn = min(p.chunk, p.K - k0);
     const int lanes = p.group / 8;
-    const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
-    for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += stride) {
-        const uint32_t q = reinterpret_cast<const uint32_t*>(p.q)[i];
-        const long long row = i / per;
-        const int g = static_cast<int>(i - row * per) / lanes;
-        const long long e = row / p.N;
-        const int n = static_cast<int>(row - e * p.N);
-        const float s = __bfloat162float(p.s[(e * (p.K / p.group) + g) * p.N + n]);
-        uint32_t o[4];
+    const size_t e = row0 / p.N;
+    const int n0 = static_cast<int>(row0 - e * p.N), groups = p.K / p.group, g0 = k0 / p.group;
+    for (int g = threadIdx.x; g < kn / p.group; g += blockDim.x)
+        *reinterpret_cast<uint4*>(&sc[g][0]) = *reinterpret_cast<const uint4*>(p.s + (e * groups + g0 + g) * p.N + n0);
+    __syncthreads();
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + (row * p.K + k0) / 2);
+    uint4* dst = reinterpret_cast<uint4*>(p.w_out + row * p.K + k0);
+    const int vecs = kn / 8;
+    const __nv_bfloat162 off = __floats2bfloat162_rn(136.0f, 136.0f);
+    for (int base = 0; base < vecs; base += 256) {
+        uint32_t v[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            o[j] = pack_bf16(s * (static_cast<int>((q >> (8 * j)) & 15u) - 8),
-                             s * (static_cast<int>((q >> (8 * j + 4)) & 15u) - 8));
-        reinterpret_cast<uint4*>(p.w_out)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int i = 0; i < 8; ++i) {
+            const int at = base + i * 32 + lane;
+            v[i] = at < vecs ? __ldcs(src + at) : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int at = base + i * 32 + lane;
+            if (at < vecs) {
+                const __nv_bfloat162 s = __bfloat162bfloat162(sc[at / lanes][warp]);
+                uint32_t o[4];  // inputs (0,4) (1,5) (2,6) (3,7)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t b = ((v[i] >> (4 * j)) & 0x000f000fu) | 0x43004300u;
+                    const __nv_bfloat162 d = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b), off), s);
+                    o[j] = *reinterpret_cast<const uint32_t*>(&d);
+                }
+                __stcs(dst + at, make_uint4(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410),
+                                            __byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632)));
+            }
+        }
     }
 }
 
@@ -750,13 +807,17 @@ int w4_launch_group(const W4Args& a, int group, int rows, int x_rows, int dev, i
 int w4_conv_check(int E, int N, int K, int group) {
     std::string why;
     if (!w4_shape_ok(N, K, group, &why)) return api_fail(ET_ERR_UNSUPPORTED, why);
-    if (E < 1 || E > 65536) return api_fail(ET_ERR_UNSUPPORTED, "E must be in [1, 65536]");
+    if (E < 1 || static_cast<long long>(E) * N > (1ll << 32))
+        return api_fail(ET_ERR_UNSUPPORTED, "E must be positive, E * N at most 2^32");
     return ET_OK;
 }
 
-int w4_conv_grid(const W4ConvArgs& a, int sms) {
-    const long long ctas = (a.rows * (a.K / 8) + 255) / 256;
-    return static_cast<int>(ctas < 32ll * sms ? ctas : 32ll * sms);
+// Rows in the grid's x (8 a CTA), inputs in chunks of 4096 in its y -- of 1024
+// when that leaves fewer than two CTAs an SM.
+dim3 w4_conv_grid(W4ConvArgs* a, int E, int sms) {
+    const long long tiles = static_cast<long long>(E) * a->N / kConvRows;
+    a->chunk = tiles * ((a->K + kConvK - 1) / kConvK) < 2ll * sms ? 1024 : kConvK;
+    return dim3(static_cast<unsigned>(tiles), (a->K + a->chunk - 1) / a->chunk);
 }
 
 size_t w4_experts_bytes(int T_max, int F, int k) {
@@ -793,8 +854,8 @@ int et_w4_quantize(const void* w, void* q, void* scale, int E, int N, int K, int
         a.N = N;
         a.K = K;
         a.group = group;
-        a.rows = static_cast<long long>(E) * N;
-        const cudaError_t e = api_launch(w4_quantize_kernel, w4_conv_grid(a, sms), 256, 0, stream, a);
+        const dim3 grid = w4_conv_grid(&a, E, sms);
+        const cudaError_t e = api_launch(w4_quantize_kernel, grid, kConvRows * 32, 0, stream, a);
         if (e != cudaSuccess) return api_fail_cuda(e, "launch of the 4-bit quantiser");
         return ET_OK;
     });
@@ -816,8 +877,8 @@ int et_w4_dequantize(const void* q, const void* scale, void* w, int E, int N, in
         a.N = N;
         a.K = K;
         a.group = group;
-        a.rows = static_cast<long long>(E) * N;
-        const cudaError_t e = api_launch(w4_dequantize_kernel, w4_conv_grid(a, sms), 256, 0, stream, a);
+        const dim3 grid = w4_conv_grid(&a, E, sms);
+        const cudaError_t e = api_launch(w4_dequantize_kernel, grid, kConvRows * 32, 0, stream, a);
         if (e != cudaSuccess) return api_fail_cuda(e, "launch of the 4-bit expansion");
         return ET_OK;
     });

@@ -11,6 +11,8 @@ import ctypes
 import os
 from typing import Optional
 
+import torch
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libetmoe.so")
 
@@ -119,7 +121,6 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -135,7 +136,6 @@ def _opts(timeout_us=0, fault_mode=0, fault_arg=0, trace=None):
 
 def alloc_trace(records: int, device="cuda"):
     """A zeroed device buffer for `records` trace records (see et_opts.trace)."""
-    import torch
     return torch.zeros(32 + 32 * records, dtype=torch.uint8, device=device)
 
 
@@ -181,7 +181,6 @@ def et_mlp_workspace_bytes(B_max, H, F) -> int:
 
 def alloc_workspace(nbytes: int, device="cuda"):
     """A zeroed, 256-byte aligned byte buffer (torch owns the memory)."""
-    import torch
     if nbytes <= 0:
         raise ValueError("invalid workspace size (shape rejected by the library)")
     return torch.zeros(nbytes, dtype=torch.uint8, device=device)
@@ -336,53 +335,60 @@ def et_mlp_chain(x, gamma, eps, w_gate, w_up, w_down, out, *, B=None, d_B=None, 
 # contiguity and device (ValueError).  They run on the tensors' device, on
 # `stream` or else that device's current stream.
 
-def _args(device, specs):
-    """Device pointers of (name, tensor or None, dtype, shape), each checked.  All must be
-    contiguous CUDA tensors on `device`."""
-    if device.type != "cuda":
-        raise ValueError(f"tensors must be on a CUDA device, not {device}")
-    out = []
-    for name, t, dtype, shape in specs:
-        if t is None:
-            out.append(None)
-            continue
-        if t.dtype is not dtype or t.shape != shape:
-            raise ValueError(f"{name} must be {dtype} {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        if t.device != device:
-            raise ValueError(f"{name} must be on {device}, not {t.device}")
-        out.append(t.data_ptr())
-    return out
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
-def _workspace_args(workspace, device):
-    import torch
+def _arg(t, name, dtype, shape, dev):
+    """Device pointer of a contiguous CUDA tensor of this type and shape on device `dev`, or None."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be on CUDA device {dev}, not {t.device}")
+
+
+def _device_of(t, name):
+    """Index of the CUDA device that holds `t`."""
+    if t.is_cuda:
+        return t.get_device()
+    raise ValueError(f"{name} must be on a CUDA device, not {t.device}")
+
+
+def _workspace_args(workspace, dev):
     if workspace is None:
         raise ValueError("workspace must be given (alloc_workspace)")
-    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.device != device:
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+    if workspace.dtype is not _U8 or not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on CUDA device {dev}")
     return workspace.data_ptr(), workspace.numel()
 
 
-def _count_arg(d_n, device):
-    import torch
+def _count_arg(d_n, dev):
     if d_n is None or isinstance(d_n, int):
         return d_n
-    if d_n.dtype is not torch.int32 or d_n.numel() != 1 or d_n.device != device:
-        raise ValueError(f"a device count must be one int32 on {device}")
+    if d_n.dtype is not _I32 or d_n.numel() != 1 or d_n.get_device() != dev:
+        raise ValueError(f"a device count must be one int32 on CUDA device {dev}")
     return d_n.data_ptr()
 
 
-def _call(fn, device, stream, args, check):
-    """fn(*args, stream) with `device` current."""
-    import torch
-    if device.index is None or device.index == torch.cuda.current_device():
-        rc = fn(*args, _stream(stream))
+# The current stream's handle without building a Stream object (3 us of a call
+# that takes 6), where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _call(fn, dev, stream, args, check):
+    """fn(*args, stream) with device `dev` current."""
+    st = _raw_stream(dev) if stream is None else _stream(stream)
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, st)
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, _stream(stream))
-    if check:
+        with torch.cuda.device(dev):
+            rc = fn(*args, st)
+    if check and rc != ET_OK:
         _check(rc)
     return rc
 
@@ -394,114 +400,112 @@ def et_router_topk_workspace_bytes(T_max, E, k) -> int:
 def et_router_topk(logits, topk_idx, topk_w, *, token_mask=None, expert_counts=None, n_routed=None,
                    mean_prob=None, losses=None, T=None, d_T=None, workspace, stream=None, check=True):
     """Top-k of logits [T_max, E]: indices, gate weights, counts; losses[0] balance, losses[1] z."""
-    import torch
-    f32, i32 = torch.float32, torch.int32
-    (T_max, E), k, dev = logits.shape, topk_idx.shape[-1], logits.device
-    ptrs = _args(dev, (("logits", logits, f32, (T_max, E)), ("token_mask", token_mask, torch.uint8, (T_max,)),
-                       ("topk_idx", topk_idx, i32, (T_max, k)), ("topk_w", topk_w, f32, (T_max, k)),
-                       ("expert_counts", expert_counts, i32, (E,)), ("n_routed", n_routed, i32, (1,)),
-                       ("mean_prob", mean_prob, f32, (E,)), ("losses", losses, f32, (2,))))
-    return _call(load().et_router_topk, dev, stream,
-                 (*ptrs, T_max if T is None else T, _count_arg(d_T, dev), T_max, E, k,
-                  *_workspace_args(workspace, dev)), check)
+    dev = _device_of(logits, "logits")
+    T_max, E = logits.shape
+    k = topk_idx.shape[-1]
+    ws, wsb = _workspace_args(workspace, dev)
+    return _call(load().et_router_topk, dev, stream, (
+        _arg(logits, "logits", _F32, (T_max, E), dev), _arg(token_mask, "token_mask", _U8, (T_max,), dev),
+        _arg(topk_idx, "topk_idx", _I32, (T_max, k), dev), _arg(topk_w, "topk_w", _F32, (T_max, k), dev),
+        _arg(expert_counts, "expert_counts", _I32, (E,), dev), _arg(n_routed, "n_routed", _I32, (1,), dev),
+        _arg(mean_prob, "mean_prob", _F32, (E,), dev), _arg(losses, "losses", _F32, (2,), dev),
+        T_max if T is None else T, _count_arg(d_T, dev), T_max, E, k, ws, wsb), check)
 
 
 def et_router_topk_bwd(logits, topk_idx, topk_w, expert_counts, n_routed, d_logits, *, token_mask=None,
                        d_losses=None, d_topk_w=None, T=None, d_T=None, workspace, stream=None, check=True):
     """Gradient of et_router_topk's losses (d_losses [2]) and gate weights (d_topk_w [T_max, k])."""
-    import torch
-    f32, i32 = torch.float32, torch.int32
-    (T_max, E), k, dev = logits.shape, topk_idx.shape[-1], logits.device
-    ptrs = _args(dev, (("logits", logits, f32, (T_max, E)), ("token_mask", token_mask, torch.uint8, (T_max,)),
-                       ("topk_idx", topk_idx, i32, (T_max, k)), ("topk_w", topk_w, f32, (T_max, k)),
-                       ("expert_counts", expert_counts, i32, (E,)), ("n_routed", n_routed, i32, (1,)),
-                       ("d_losses", d_losses, f32, (2,)), ("d_topk_w", d_topk_w, f32, (T_max, k)),
-                       ("d_logits", d_logits, f32, (T_max, E))))
-    return _call(load().et_router_topk_bwd, dev, stream,
-                 (*ptrs, T_max if T is None else T, _count_arg(d_T, dev), T_max, E, k,
-                  *_workspace_args(workspace, dev)), check)
+    dev = _device_of(logits, "logits")
+    T_max, E = logits.shape
+    k = topk_idx.shape[-1]
+    ws, wsb = _workspace_args(workspace, dev)
+    return _call(load().et_router_topk_bwd, dev, stream, (
+        _arg(logits, "logits", _F32, (T_max, E), dev), _arg(token_mask, "token_mask", _U8, (T_max,), dev),
+        _arg(topk_idx, "topk_idx", _I32, (T_max, k), dev), _arg(topk_w, "topk_w", _F32, (T_max, k), dev),
+        _arg(expert_counts, "expert_counts", _I32, (E,), dev), _arg(n_routed, "n_routed", _I32, (1,), dev),
+        _arg(d_losses, "d_losses", _F32, (2,), dev), _arg(d_topk_w, "d_topk_w", _F32, (T_max, k), dev),
+        _arg(d_logits, "d_logits", _F32, (T_max, E), dev),
+        T_max if T is None else T, _count_arg(d_T, dev), T_max, E, k, ws, wsb), check)
 
 
 def et_block_norm_workspace_bytes(T_max, H) -> int:
     return load().et_block_norm_workspace_bytes(T_max, H)
 
 
-def _gate_kind(gate, T_max, H):
-    """(kind, dtype, shape) of a gate: bf16 [H], fp32 [T_max] or bf16 [T_max, H]."""
-    import torch
+def _gate(gate, T_max, H, dev):
+    """(kind, pointer, gradient's type and shape) of a gate: bf16 [H], fp32 [T_max] or bf16 [T_max, H]."""
     if gate is None:
-        return 0, None, None
+        return 0, None, None, None
     if gate.dim() == 2:
-        return 3, torch.bfloat16, (T_max, H)
-    return (2, torch.float32, (T_max,)) if gate.dtype is torch.float32 else (1, torch.bfloat16, (H,))
+        return 3, _arg(gate, "gate", _BF16, (T_max, H), dev), _BF16, (T_max, H)
+    if gate.dtype is _F32:
+        return 2, _arg(gate, "gate", _F32, (T_max,), dev), _F32, (T_max,)
+    return 1, _arg(gate, "gate", _BF16, (H,), dev), _F32, (H,)
 
 
 def et_block_norm(x, y, x_out, x_hat, *, gamma_post=None, gate=None, scale=1.0, gamma_pre=None, eps,
                   T=None, d_T=None, workspace, stream=None, check=True):
     """x_out = x + scale * gate * RMSNorm(y) * gamma_post and x_hat = RMSNorm(x_out) * gamma_pre."""
-    import torch
-    bf = torch.bfloat16
-    (T_max, H), dev = x.shape, x.device
-    kind, gdt, gsh = _gate_kind(gate, T_max, H)
-    rows = (T_max, H)
-    px, py, pgp, pg, pgr, po, ph = _args(dev, (
-        ("x", x, bf, rows), ("y", y, bf, rows), ("gamma_post", gamma_post, bf, (H,)), ("gate", gate, gdt, gsh),
-        ("gamma_pre", gamma_pre, bf, (H,)), ("x_out", x_out, bf, rows), ("x_hat", x_hat, bf, rows)))
-    return _call(load().et_block_norm, dev, stream,
-                 (px, py, pgp, pg, kind, scale, pgr, eps, po, ph, T_max if T is None else T,
-                  _count_arg(d_T, dev), T_max, H, *_workspace_args(workspace, dev)), check)
+    dev = _device_of(x, "x")
+    T_max, H = rows = x.shape
+    kind, pgate, _, _ = _gate(gate, T_max, H, dev)
+    ws, wsb = _workspace_args(workspace, dev)
+    return _call(load().et_block_norm, dev, stream, (
+        _arg(x, "x", _BF16, rows, dev), _arg(y, "y", _BF16, rows, dev),
+        _arg(gamma_post, "gamma_post", _BF16, (H,), dev), pgate, kind, scale,
+        _arg(gamma_pre, "gamma_pre", _BF16, (H,), dev), eps, _arg(x_out, "x_out", _BF16, rows, dev),
+        _arg(x_hat, "x_hat", _BF16, rows, dev), T_max if T is None else T, _count_arg(d_T, dev), T_max, H,
+        ws, wsb), check)
 
 
 def et_block_norm_bwd(x, y, d_x_out, d_x_hat, dx, dy, *, gamma_post=None, gate=None, scale=1.0, gamma_pre=None,
                       eps, d_gamma_post=None, d_gamma_pre=None, d_gate=None, T=None, d_T=None, workspace,
                       stream=None, check=True):
     """Gradient of et_block_norm: dx, dy and, where given, the parameters' (fp32; a full gate's bf16)."""
-    import torch
-    bf, f32 = torch.bfloat16, torch.float32
-    (T_max, H), dev = x.shape, x.device
-    kind, gdt, gsh = _gate_kind(gate, T_max, H)
-    rows = (T_max, H)
-    px, py, pgp, pg, pgr, pdo, pdh, pdx, pdy, pdgp, pdgr, pdg = _args(dev, (
-        ("x", x, bf, rows), ("y", y, bf, rows), ("gamma_post", gamma_post, bf, (H,)), ("gate", gate, gdt, gsh),
-        ("gamma_pre", gamma_pre, bf, (H,)), ("d_x_out", d_x_out, bf, rows), ("d_x_hat", d_x_hat, bf, rows),
-        ("dx", dx, bf, rows), ("dy", dy, bf, rows), ("d_gamma_post", d_gamma_post, f32, (H,)),
-        ("d_gamma_pre", d_gamma_pre, f32, (H,)),
-        ("d_gate", d_gate, bf if kind == 3 else f32, gsh)))
-    return _call(load().et_block_norm_bwd, dev, stream,
-                 (px, py, pgp, pg, kind, scale, pgr, eps, pdo, pdh, pdx, pdy, pdgp, pdgr, pdg,
-                  T_max if T is None else T, _count_arg(d_T, dev), T_max, H,
-                  *_workspace_args(workspace, dev)), check)
+    dev = _device_of(x, "x")
+    T_max, H = rows = x.shape
+    kind, pgate, gdt, gsh = _gate(gate, T_max, H, dev)
+    if d_gate is not None and gate is None:
+        raise ValueError("d_gate needs a gate")
+    ws, wsb = _workspace_args(workspace, dev)
+    return _call(load().et_block_norm_bwd, dev, stream, (
+        _arg(x, "x", _BF16, rows, dev), _arg(y, "y", _BF16, rows, dev),
+        _arg(gamma_post, "gamma_post", _BF16, (H,), dev), pgate, kind, scale,
+        _arg(gamma_pre, "gamma_pre", _BF16, (H,), dev), eps, _arg(d_x_out, "d_x_out", _BF16, rows, dev),
+        _arg(d_x_hat, "d_x_hat", _BF16, rows, dev), _arg(dx, "dx", _BF16, rows, dev),
+        _arg(dy, "dy", _BF16, rows, dev), _arg(d_gamma_post, "d_gamma_post", _F32, (H,), dev),
+        _arg(d_gamma_pre, "d_gamma_pre", _F32, (H,), dev), _arg(d_gate, "d_gate", gdt, gsh, dev),
+        T_max if T is None else T, _count_arg(d_T, dev), T_max, H, ws, wsb), check)
 
 
-def _w4_weight(q, scale, N, K, E=None):
-    """Specs of one 4-bit weight ([N, K], or E of them) and its group."""
-    import torch
-    lead = () if E is None else (E,)
-    groups = scale.shape[-2] if scale.dim() == 2 + len(lead) else 0
-    group = K // groups if groups and K % groups == 0 else 0
-    return ((q, torch.uint8, lead + (N, K // 2)), (scale, torch.bfloat16, lead + (groups, N))), group
+def _w4(q, scale, name, lead, N, K, dev):
+    """(pointer of q, pointer of scale, group) of the 4-bit weight [*lead, N, K]."""
+    groups = scale.shape[-2] if scale.dim() > 1 else 0
+    if groups < 1 or K % groups:
+        raise ValueError(f"scale of {name} must be {(*lead, 'K / group', N)} with K = {K}, not {tuple(scale.shape)}")
+    return (_arg(q, name, _U8, (*lead, N, K // 2), dev),
+            _arg(scale, f"scale of {name}", _BF16, (*lead, groups, N), dev), K // groups)
 
 
 def _w4_convert(w, q, scale):
-    import torch
-    dev = w.device
-    E = w.shape[0] if w.dim() == 3 else None
-    N, K = w.shape[-2:]
-    (sq, ss), group = _w4_weight(q, scale, N, K, E)
-    pw, pq, ps = _args(dev, (("w", w, torch.bfloat16, w.shape), ("q", *sq), ("scale", *ss)))
-    return pw, pq, ps, dev, (E or 1, N, K, group)
+    dev = _device_of(w, "w")
+    *lead, N, K = w.shape
+    if len(lead) > 1:
+        raise ValueError(f"w must be [N, K] or [E, N, K], not {tuple(w.shape)}")
+    pq, ps, group = _w4(q, scale, "q", lead, N, K, dev)
+    return dev, _arg(w, "w", _BF16, w.shape, dev), pq, ps, (lead[0] if lead else 1, N, K, group)
 
 
 def et_w4_quantize(w, q, scale, *, stream=None, check=True):
     """bf16 w [N, K] or [E, N, K] -> q uint8 [.., N, K/2] and scale bf16 [.., K/group, N]; the group
     is K / scale.shape[-2]."""
-    pw, pq, ps, dev, dims = _w4_convert(w, q, scale)
+    dev, pw, pq, ps, dims = _w4_convert(w, q, scale)
     return _call(load().et_w4_quantize, dev, stream, (pw, pq, ps, *dims), check)
 
 
 def et_w4_dequantize(q, scale, w, *, stream=None, check=True):
     """The bf16 values of a 4-bit weight (the inverse of et_w4_quantize's layout)."""
-    pw, pq, ps, dev, dims = _w4_convert(w, q, scale)
+    dev, pw, pq, ps, dims = _w4_convert(w, q, scale)
     return _call(load().et_w4_dequantize, dev, stream, (pq, ps, pw, *dims), check)
 
 
@@ -511,14 +515,14 @@ def et_w4_gemv_workspace_bytes(M_max, N, K, group) -> int:
 
 def et_w4_gemv(X, q, scale, Y, *, M=None, d_M=None, workspace, stream=None, check=True):
     """Y = X w^T for up to 64 rows, w in 4 bits (et_w4_quantize's layout)."""
-    import torch
-    (M_max, K), N, dev = X.shape, Y.shape[-1], X.device
-    (sq, ss), group = _w4_weight(q, scale, N, K)
-    ptrs = _args(dev, (("X", X, torch.bfloat16, (M_max, K)), ("q", *sq), ("scale", *ss),
-                       ("Y", Y, torch.bfloat16, (M_max, N))))
-    return _call(load().et_w4_gemv, dev, stream,
-                 (*ptrs, M_max if M is None else M, _count_arg(d_M, dev), M_max, N, K, group,
-                  *_workspace_args(workspace, dev)), check)
+    dev = _device_of(X, "X")
+    M_max, K = X.shape
+    N = Y.shape[-1]
+    pq, ps, group = _w4(q, scale, "q", (), N, K, dev)
+    ws, wsb = _workspace_args(workspace, dev)
+    return _call(load().et_w4_gemv, dev, stream, (
+        _arg(X, "X", _BF16, (M_max, K), dev), pq, ps, _arg(Y, "Y", _BF16, (M_max, N), dev),
+        M_max if M is None else M, _count_arg(d_M, dev), M_max, N, K, group, ws, wsb), check)
 
 
 def et_w4_experts_workspace_bytes(T_max, H, F, E, k, group) -> int:
@@ -528,21 +532,21 @@ def et_w4_experts_workspace_bytes(T_max, H, F, E, k, group) -> int:
 def et_w4_experts(x, topk_idx, topk_w, q_gate, s_gate, q_up, s_up, q_down, s_down, out, *, T=None, d_T=None,
                   workspace, stream=None, check=True):
     """The routed SwiGLU experts of up to 64 tokens, weights in 4 bits: gate, up [E, F, H], down [E, H, F]."""
-    import torch
-    bf = torch.bfloat16
-    (T_max, H), (E, F), k, dev = x.shape, q_gate.shape[:2], topk_idx.shape[-1], x.device
-    (gq, gs), group = _w4_weight(q_gate, s_gate, F, H, E)
-    (uq, us), gu = _w4_weight(q_up, s_up, F, H, E)
-    (dq, ds), gd = _w4_weight(q_down, s_down, H, F, E)
+    dev = _device_of(x, "x")
+    T_max, H = x.shape
+    E, F = q_gate.shape[:2]
+    k = topk_idx.shape[-1]
+    pqg, psg, group = _w4(q_gate, s_gate, "q_gate", (E,), F, H, dev)
+    pqu, psu, gu = _w4(q_up, s_up, "q_up", (E,), F, H, dev)
+    pqd, psd, gd = _w4(q_down, s_down, "q_down", (E,), H, F, dev)
     if not group == gu == gd:
         raise ValueError(f"gate, up and down must have one group size, not {group}, {gu}, {gd}")
-    ptrs = _args(dev, (("x", x, bf, (T_max, H)), ("topk_idx", topk_idx, torch.int32, (T_max, k)),
-                       ("topk_w", topk_w, torch.float32, (T_max, k)), ("q_gate", *gq), ("s_gate", *gs),
-                       ("q_up", *uq), ("s_up", *us), ("q_down", *dq), ("s_down", *ds),
-                       ("out", out, bf, (T_max, H))))
-    return _call(load().et_w4_experts, dev, stream,
-                 (*ptrs, T_max if T is None else T, _count_arg(d_T, dev), T_max, H, F, E, k, group,
-                  *_workspace_args(workspace, dev)), check)
+    ws, wsb = _workspace_args(workspace, dev)
+    return _call(load().et_w4_experts, dev, stream, (
+        _arg(x, "x", _BF16, (T_max, H), dev), _arg(topk_idx, "topk_idx", _I32, (T_max, k), dev),
+        _arg(topk_w, "topk_w", _F32, (T_max, k), dev), pqg, psg, pqu, psu, pqd, psd,
+        _arg(out, "out", _BF16, (T_max, H), dev), T_max if T is None else T, _count_arg(d_T, dev), T_max, H, F, E, k,
+        group, ws, wsb), check)
 
 
 def et_status(workspace, stream=None):

@@ -103,26 +103,25 @@ def test_binding_refuses_wrong_tensors(lib):
     ws = torch.zeros(1 << 16, dtype=torch.uint8)
     with pytest.raises(ValueError, match="CUDA device"):
         E.et_router_topk(torch.zeros(4, 8), torch.zeros(4, 2, dtype=i32), torch.zeros(4, 2), workspace=ws)
-    meta = torch.device("meta")
-    checks = E._args
-    dev = torch.device("cuda:0")
+    with pytest.raises(ValueError, match="CUDA device"):
+        E.et_w4_gemv(torch.zeros(4, 64, dtype=bf), ws, ws, torch.zeros(4, 8, dtype=bf), workspace=ws)
     for t, dt, sh, msg in ((torch.zeros(4, 8, dtype=bf), f32, (4, 8), "must be torch.float32"),
                            (torch.zeros(4, 7), f32, (4, 8), r"\(4, 8\)"),
                            (torch.zeros(8, 4).t(), f32, (4, 8), "contiguous"),
-                           (torch.zeros(4, 8, device=meta), f32, (4, 8), "must be on cuda:0")):
+                           (torch.zeros(4, 8), f32, (4, 8), "must be on CUDA device 0")):
         with pytest.raises(ValueError, match=msg):
-            checks(dev, (("logits", t, dt, sh),))
+            E._arg(t, "logits", dt, sh, 0)
+    assert E._arg(None, "gate", f32, (4,), 0) is None
     with pytest.raises(ValueError, match="workspace"):
-        E._workspace_args(None, dev)
+        E._workspace_args(None, 0)
     with pytest.raises(ValueError, match="workspace"):
-        E._workspace_args(ws, dev)
+        E._workspace_args(ws, 0)
     with pytest.raises(ValueError, match="device count"):
-        E._count_arg(torch.zeros(2, dtype=i32), dev)
-    q, s = torch.zeros(4, 64, 32, dtype=torch.uint8), torch.zeros(4, 2, 64, dtype=bf)
-    qd, sd = torch.zeros(4, 64, 32, dtype=torch.uint8), torch.zeros(4, 1, 64, dtype=bf)
-    with pytest.raises(ValueError, match="one group size"):
-        E.et_w4_experts(torch.zeros(2, 64, dtype=bf), torch.zeros(2, 2, dtype=i32), torch.zeros(2, 2), q, s, q, s,
-                        qd, sd, torch.zeros(2, 64, dtype=bf), workspace=ws)
+        E._count_arg(torch.zeros(2, dtype=i32), 0)
+    q = torch.zeros(4, 64, 32, dtype=torch.uint8)
+    for s in (torch.zeros(64, dtype=bf), torch.zeros(4, 3, 64, dtype=bf), torch.zeros(4, 0, 64, dtype=bf)):
+        with pytest.raises(ValueError, match="scale of q"):
+            E._w4(q, s, "q", (4,), 64, 64, 0)
 
 
 # ------------------------------------------------------------------ the 64-bit references

@@ -132,6 +132,27 @@ def test_quantize_special_values(cuda_lib):
     assert torch.equal(qc.cpu(), q)
     assert torch.equal(torch.isnan(sc.cpu()), torch.isnan(s)) and torch.equal(sc.cpu().nan_to_num(1.0), s.nan_to_num(1.0))
     assert int(torch.isnan(s).sum()) == 3
+    back = torch.empty(16, 128, dtype=BF, device="cuda")
+    cuda_lib.et_w4_dequantize(qc, sc, back)
+    want = ref.w4_values(q, s, torch.float32).to(BF)
+    assert torch.equal(back.cpu().nan_to_num(7.0), want.nan_to_num(7.0))
+
+
+def test_quantize_every_quotient(cuda_lib):
+    """Every pair of significands of a weight and its group's largest: each quotient that can lie near a half."""
+    top = (1 + torch.arange(128) / 128).to(BF)                        # the group's largest, times a power of two
+    val = torch.cat([(1 + torch.arange(128) / 128) * 2.0 ** -e for e in range(5)]).to(BF)
+    val = torch.cat([val, -val, torch.zeros(7 * 186 - 1280)]).view(186, 7)
+    w = torch.zeros(128, 186, 32, dtype=BF)
+    w[:, :, 0] = top[:, None] * 1.0
+    w[:, :, 1:8] = val.to(BF)
+    w[:, :, 1:8] = torch.minimum(torch.maximum(w[:, :, 1:8], -w[:, :, :1]), w[:, :, :1])
+    for scale in (1.0, 2.0 ** -100, 2.0 ** 100):
+        ws = (w.float() * scale).to(BF).reshape(128, 186 * 32)
+        q, s = ref.w4_pack(ws, 32)
+        qc, sc = torch.empty_like(q, device="cuda"), torch.empty_like(s, device="cuda")
+        cuda_lib.et_w4_quantize(ws.cuda(), qc, sc)
+        assert torch.equal(sc.cpu(), s) and torch.equal(qc.cpu(), q)
 
 
 # ------------------------------------------------------------------ experts
