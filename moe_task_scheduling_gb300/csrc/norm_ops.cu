@@ -189,22 +189,18 @@ __device__ __forceinline__ float2 row_sum2(float2 v, float (*red)[32], float (*r
 // The gradient.  A row's statistics are recomputed from x and y (they are read
 // anyway).  The parameter gradients are summed over this CTA's rows in
 // registers, thread by thread for its own columns, then over CTAs by
-// norm_sum_kernel in a fixed order.
+// norm_sum_kernel in a fixed order.  Three sums a row: mean y^2; mean z^2 with
+// the second norm's projection; the first norm's projection (with a per-token
+// gate's gradient).
 //
-// STAGED (whole rows a CTA, 16-byte accesses): the five input rows of the next
-// row of this CTA are copied to shared memory while the current one is worked
-// on, and each thread reads back only what it copied itself, so the copies need
-// no barrier.  Three sums a row (mean y^2; mean z^2 with the second norm's
-// projection; the first norm's projection) are three barriers.
-// MAXT: most threads, which bounds the registers (16 columns a thread take 128).
-enum NormRow { kRowX = 0, kRowY = 1, kRowDz = 2, kRowDh = 3, kRowGate = 4, kRowArrays = 5 };
-
+// This form serves every H, alignment and combination of the optional parts;
+// norm_bwd_staged_kernel the usual one.  MAXT: most threads, which bounds the
+// registers.
 template <int V, bool VEC, bool ROW, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormArgs p) {
-    constexpr bool STAGED = VEC && ROW;
     __shared__ float red[2][32], red2[2][32];
     int sums = 0;
-    extern __shared__ __align__(16) uint8_t dyn[];  // STAGED: [2][5][H] bf16; !ROW: [warps][3][256] floats
+    extern __shared__ __align__(16) uint8_t dyn[];  // !ROW: [warps][3][256] floats
     bool ok;
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
     const int H = p.H;
@@ -220,39 +216,14 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormArgs p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) a_post[j][i] = a_pre[j][i] = a_gate[j][i] = 0.0f;
 
-    auto stage = [&](int t, int buf) {
-        if (STAGED && t < T) {
-            const size_t off = static_cast<size_t>(t) * H;
-            const bf16* src[kRowArrays] = {p.x, p.y, p.d_x_out, p.d_x_hat, full ? static_cast<const bf16*>(p.gate) : nullptr};
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int c = (j * width + lane) * 8;
-                if (c < H)
-#pragma unroll
-                    for (int a = 0; a < kRowArrays; ++a)
-                        if (src[a]) cp_async16(smem_addr(dyn) + ((buf * kRowArrays + a) * H + c) * 2, src[a] + off + c);
-            }
-        }
-        if (STAGED) cp_async_commit();
-    };
-    // columns [c, c + 8) of the current row of one input (zeros where it is not given)
-    auto row8 = [&](int a, const bf16* base, int t, int buf, int c) -> Vec8 {
-        if (!base) return Vec8{};
-        if (STAGED) {
-            Vec8 v{};
-            if (c < H) {
-                const uint4 q = *reinterpret_cast<const uint4*>(dyn + (static_cast<size_t>(buf * kRowArrays + a) * H + c) * 2);
-                v.u[0] = q.x; v.u[1] = q.y; v.u[2] = q.z; v.u[3] = q.w;
-            }
-            return v;
-        }
-        return load8<VEC>(base + static_cast<size_t>(t) * H, c, H);
+    // columns [c, c + 8) of a row of one input (zeros where it is not given)
+    auto row8 = [&](const bf16* base, int t, int c) -> Vec8 {
+        return base ? load8<VEC>(base + static_cast<size_t>(t) * H, c, H) : Vec8{};
     };
     // scale * gate of columns [c, c + 8)
-    auto gate_of = [&](int t, int buf, int c, float gs, float* g) {
+    auto gate_of = [&](int t, int c, float gs, float* g) {
         if (full || p.gate_kind == kGateChannel) {
-            const Vec8 v = full ? row8(kRowGate, static_cast<const bf16*>(p.gate), t, buf, c)
-                                : load8<VEC>(static_cast<const bf16*>(p.gate), c, H);
+            const Vec8 v = row8(static_cast<const bf16*>(p.gate), full ? t : 0, c);
 #pragma unroll
             for (int i = 0; i < 8; ++i) g[i] = gs * v[i];
         } else {
@@ -261,18 +232,13 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormArgs p) {
         }
     };
 
-    int buf = 0;
-    const int t0 = blockIdx.x * rows_cta + (ROW ? 0 : threadIdx.x >> 5);
-    stage(t0, 0);
-    for (int t = t0; t < T; t += step, buf ^= 1) {
-        stage(t + step, buf ^ 1);  // this thread has read that buffer's last row
-        if (STAGED) cp_async_wait<1>();
+    for (int t = blockIdx.x * rows_cta + (ROW ? 0 : threadIdx.x >> 5); t < T; t += step) {
         const size_t off = static_cast<size_t>(t) * H;
         float ss = 0.0f;
         if (post)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const Vec8 yv = row8(kRowY, p.y, t, buf, (j * width + lane) * 8);
+                const Vec8 yv = row8(p.y, t, (j * width + lane) * 8);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) ss += yv[i] * yv[i];
             }
@@ -285,21 +251,21 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormArgs p) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int c = (j * width + lane) * 8;
-            const Vec8 xv = row8(kRowX, p.x, t, buf, c);
+            const Vec8 xv = row8(p.x, t, c);
 #pragma unroll
             for (int i = 0; i < 8; ++i) z[j][i] = xv[i];
             if (c < H) {
                 if (p.y) {
                     float g[8];
-                    gate_of(t, buf, c, gs, g);
-                    const Vec8 yv = row8(kRowY, p.y, t, buf, c);
+                    gate_of(t, c, gs, g);
+                    const Vec8 yv = row8(p.y, t, c);
                     const Vec8 gp = post ? load8<VEC>(p.gamma_post, c, H) : Vec8{};
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         z[j][i] += g[i] * (post ? yv[i] * ry * gp[i] : yv[i]);  // 0 past H, where y is 0
                 }
                 if (p.d_x_hat) {
-                    const Vec8 dh = row8(kRowDh, p.d_x_hat, t, buf, c);
+                    const Vec8 dh = row8(p.d_x_hat, t, c);
                     const Vec8 gp = load8<VEC>(p.gamma_pre, c, H);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -324,11 +290,11 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormArgs p) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) d[j][i] = 0.0f;
             if (c < H) {
-                const Vec8 dz = row8(kRowDz, p.d_x_out, t, buf, c);
+                const Vec8 dz = row8(p.d_x_out, t, c);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) d[j][i] = dz[i];
                 if (p.d_x_hat) {
-                    const Vec8 dh = row8(kRowDh, p.d_x_hat, t, buf, c);
+                    const Vec8 dh = row8(p.d_x_hat, t, c);
                     const Vec8 gp = load8<VEC>(p.gamma_pre, c, H);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -339,8 +305,8 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormArgs p) {
                 store8<VEC>(p.dx + off, c, H, d[j]);
                 if (p.y) {
                     float g[8], dgf[8];
-                    gate_of(t, buf, c, gs, g);
-                    const Vec8 yv = row8(kRowY, p.y, t, buf, c);
+                    gate_of(t, c, gs, g);
+                    const Vec8 yv = row8(p.y, t, c);
                     const Vec8 gp = post ? load8<VEC>(p.gamma_post, c, H) : Vec8{};
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -368,7 +334,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormArgs p) {
             for (int j = 0; j < V; ++j) {
                 const int c = (j * width + lane) * 8;
                 if (c < H) {
-                    const Vec8 yv = row8(kRowY, p.y, t, buf, c);
+                    const Vec8 yv = row8(p.y, t, c);
                     float o[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) o[i] = post ? ry * d[j][i] - yv[i] * k1 : d[j][i];
@@ -377,8 +343,6 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormArgs p) {
             }
         }
     }
-    if (STAGED) cp_async_wait<0>();
-
     if (!ok) return;
     float* part = p.part + static_cast<size_t>(blockIdx.x) * 3 * H;
     if (ROW) {
@@ -411,6 +375,175 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormArgs p) {
             part[o] = s;
         }
     }
+}
+
+// The same gradient where y, gamma_pre and both incoming gradients are given, H
+// is a multiple of 8 in (512, 8192] and every tensor is 16-byte aligned.
+//
+// Bound by HBM (T = H = 4096 with a full gate: 268 MB) if a row's latencies are
+// hidden: the input rows of this CTA's next row are copied to shared memory
+// while the current one is worked on, each thread reading back only what it
+// copied itself, so that the copies need no barrier; the parameters lie there
+// for all rows.  Sixteen columns a thread, in pairs (fp32x2 products): the three
+// sums and the addresses cost as much as the columns' arithmetic.
+//   u = y r_y, a = scale gate gamma_post, z = x + a u, e = d_x_hat gamma_pre,
+//   D = d_x_out + r_z e - z r_z^3 mean(e z),  b = a D,
+//   dx = D, dy = r_y (b - u mean(b u)).
+enum NormGate { kGScalar = 0, kGChannel = 1, kGFull = 2 };
+
+__device__ __forceinline__ float2 unpack2(uint32_t w) { return make_float2(bf_lo(w), bf_hi(w)); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+template <int GK, int MAXT>
+__global__ void __launch_bounds__(MAXT, 512 / MAXT) norm_bwd_staged_kernel(const NormArgs p) {
+    constexpr int A = GK == kGFull ? 5 : 4;  // staged rows: x, y, d_x_out, d_x_hat (, gate)
+    __shared__ float red[2][32], red2[2][32];
+    extern __shared__ __align__(16) uint8_t dyn[];  // [2][A][H] rows; gamma_post, gamma_pre (, gate) [H]
+    int sums = 0;
+    bool ok;
+    const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
+    if (!ok) return;
+    const int H = p.H, H2 = H * 2;
+    const bool post = p.gamma_post != nullptr;
+    const int c0 = threadIdx.x * 8, c1 = (blockDim.x + threadIdx.x) * 8;
+    const bool in0 = c0 < H, in1 = c1 < H;
+    uint8_t* par = dyn + 2 * A * H2;
+
+    auto stage = [&](int t, int buf) {
+        if (t < T) {
+            const size_t off = static_cast<size_t>(t) * H;
+            const bf16* src[5] = {p.x, p.y, p.d_x_out, p.d_x_hat, static_cast<const bf16*>(p.gate)};
+            const uint32_t dst = smem_addr(dyn) + buf * A * H2;
+#pragma unroll
+            for (int a = 0; a < A; ++a) {
+                if (in0) cp_async16(dst + a * H2 + c0 * 2, src[a] + off + c0);
+                if (in1) cp_async16(dst + a * H2 + c1 * 2, src[a] + off + c1);
+            }
+        }
+        cp_async_commit();
+    };
+    int buf = 0;
+    stage(blockIdx.x, 0);
+    // the parameters, 1 for a missing gamma_post
+    for (int j = 0; j < 2; ++j) {
+        const int c = j ? c1 : c0;
+        if (c < H) {
+            *reinterpret_cast<uint4*>(par + c * 2) = post ? *reinterpret_cast<const uint4*>(p.gamma_post + c)
+                : make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+            *reinterpret_cast<uint4*>(par + H2 + c * 2) = *reinterpret_cast<const uint4*>(p.gamma_pre + c);
+            if (GK == kGChannel)
+                *reinterpret_cast<uint4*>(par + 2 * H2 + c * 2) =
+                    *reinterpret_cast<const uint4*>(static_cast<const bf16*>(p.gate) + c);
+        }
+    }
+    float2 a_post[2][4], a_pre[2][4], a_gate[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a_post[j][i] = a_pre[j][i] = a_gate[j][i] = both(0.0f);
+
+    for (int t = blockIdx.x; t < T; t += gridDim.x, buf ^= 1) {
+        stage(t + gridDim.x, buf ^ 1);  // this thread has read that buffer's last row
+        cp_async_wait<1>();
+        const uint8_t* rows = dyn + buf * A * H2;
+        auto get = [&](const uint8_t* base, int j) -> uint4 {  // zeros past H
+            return (j ? in1 : in0) ? *reinterpret_cast<const uint4*>(base + (j ? c1 : c0) * 2) : make_uint4(0, 0, 0, 0);
+        };
+        auto word = [](const uint4& v, int i) -> uint32_t { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; };
+        const float gs = p.scale * (GK == kGScalar && p.gate ? static_cast<const float*>(p.gate)[t] : 1.0f);
+        float2 u[2][4], z[2][4];
+        float2 ss = both(0.0f);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint4 y = get(rows + H2, j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                u[j][i] = unpack2(word(y, i));
+                ss = __ffma2_rn(u[j][i], u[j][i], ss);
+            }
+        }
+        const float ry = post ? inv_rms(row_sum<true>(ss.x + ss.y, red, sums), p.inv_H, p.eps) : 1.0f;
+        float2 zz = both(0.0f), ez = both(0.0f);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint4 x = get(rows, j), dh = get(rows + 3 * H2, j), gp = get(par, j), gr = get(par + H2, j);
+            const uint4 g = GK == kGFull ? get(rows + 4 * H2, j) : GK == kGChannel ? get(par + 2 * H2, j) : uint4{};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                u[j][i] = __fmul2_rn(u[j][i], both(ry));
+                float2 a = __fmul2_rn(unpack2(word(gp, i)), both(gs));
+                if (GK != kGScalar) a = __fmul2_rn(a, unpack2(word(g, i)));
+                z[j][i] = __ffma2_rn(a, u[j][i], unpack2(word(x, i)));
+                const float2 e = __fmul2_rn(unpack2(word(dh, i)), unpack2(word(gr, i)));
+                zz = __ffma2_rn(z[j][i], z[j][i], zz);
+                ez = __ffma2_rn(e, z[j][i], ez);
+            }
+        }
+        const float2 za = row_sum2<true>(make_float2(zz.x + zz.y, ez.x + ez.y), red, red2, sums);
+        const float rz = inv_rms(za.x, p.inv_H, p.eps);
+        const float k2 = za.y * p.inv_H * rz * rz * rz;
+        const size_t off = static_cast<size_t>(t) * H;
+        float2 bu = both(0.0f), gt = both(0.0f);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint4 dz = get(rows + 2 * H2, j), dh = get(rows + 3 * H2, j), gp = get(par, j), gr = get(par + H2, j);
+            const uint4 g = GK == kGFull ? get(rows + 4 * H2, j) : GK == kGChannel ? get(par + 2 * H2, j) : uint4{};
+            uint32_t odx[4], odg[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 h = unpack2(word(dh, i)), gp2 = unpack2(word(gp, i));
+                const float2 e = __fmul2_rn(h, unpack2(word(gr, i)));
+                float2 D = __ffma2_rn(e, both(rz), unpack2(word(dz, i)));
+                D = __ffma2_rn(z[j][i], both(-k2), D);
+                a_pre[j][i] = __ffma2_rn(h, __fmul2_rn(z[j][i], both(rz)), a_pre[j][i]);
+                odx[i] = pack_bf16(D.x, D.y);
+                const float2 q = GK == kGScalar ? both(gs) : __fmul2_rn(unpack2(word(g, i)), both(gs));
+                const float2 tu = __fmul2_rn(D, u[j][i]);
+                a_post[j][i] = __ffma2_rn(q, tu, a_post[j][i]);
+                if (GK == kGScalar) gt = __ffma2_rn(gp2, tu, gt);
+                if (GK == kGChannel) a_gate[j][i] = __ffma2_rn(gp2, tu, a_gate[j][i]);
+                if (GK == kGFull) {
+                    const float2 dg = __fmul2_rn(__fmul2_rn(gp2, both(p.scale)), tu);
+                    odg[i] = pack_bf16(dg.x, dg.y);
+                }
+                z[j][i] = __fmul2_rn(__fmul2_rn(q, gp2), D);  // b
+                bu = __ffma2_rn(z[j][i], u[j][i], bu);
+            }
+            if (j ? in1 : in0) {
+                *reinterpret_cast<uint4*>(p.dx + off + (j ? c1 : c0)) = make_uint4(odx[0], odx[1], odx[2], odx[3]);
+                if (GK == kGFull && p.d_gate_full)
+                    *reinterpret_cast<uint4*>(p.d_gate_full + off + (j ? c1 : c0)) = make_uint4(odg[0], odg[1], odg[2], odg[3]);
+            }
+        }
+        float m = 0.0f;
+        if (post || p.d_gate_token) {
+            const float2 s = row_sum2<true>(make_float2(bu.x + bu.y, gt.x + gt.y), red, red2, sums);
+            m = post ? s.x * p.inv_H : 0.0f;
+            if (p.d_gate_token && threadIdx.x == 0) p.d_gate_token[t] = s.y * p.scale;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = __fmul2_rn(__ffma2_rn(u[j][i], both(-m), z[j][i]), both(ry));
+                o[i] = pack_bf16(v.x, v.y);
+            }
+            if (j ? in1 : in0) *reinterpret_cast<uint4*>(p.dy + off + (j ? c1 : c0)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+    cp_async_wait<0>();
+    float* part = p.part + static_cast<size_t>(blockIdx.x) * 3 * H;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (j ? in1 : in0)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float* o = part + (j ? c1 : c0) + 2 * i;  // H is a multiple of 8: 8-byte aligned
+                *reinterpret_cast<float2*>(o) = a_post[j][i];
+                *reinterpret_cast<float2*>(o + H) = a_pre[j][i];
+                if (GK == kGChannel) *reinterpret_cast<float2*>(o + 2 * H) = __fmul2_rn(a_gate[j][i], both(p.scale));
+            }
 }
 
 struct NormSumArgs {
@@ -503,23 +636,19 @@ cudaError_t launch_fwd(const NormArgs& a, int rows, int sms, void* stream) {
     return api_launch(norm_fwd_kernel<2, VEC, true>, grid, th, 0, stream, a);
 }
 
-// The grid is also the number of partial rows that norm_sum_kernel reads.
-template <int V, bool VEC, int MAXT>
-cudaError_t launch_bwd_rows(const NormArgs& a, int dev, int sms, int threads, int rows, int parts_max, int* parts,
-                            void* stream) {
+template <int GK, int MAXT>
+cudaError_t launch_bwd_staged(const NormArgs& a, int dev, int sms, int threads, int rows, int* parts, void* stream) {
     static SmemOptIn opt;
-    const int smem = VEC ? 2 * kRowArrays * a.H * static_cast<int>(sizeof(bf16)) : 0;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = api_smem_opt_in(opt, dev, norm_bwd_kernel<V, VEC, true, MAXT>, kSmemLimit - 2048);
-        if (e != cudaSuccess) return e;
-    }
-    // CTAs an SM: one of more than 256 threads (128 registers each), else two
-    const int most = threads > 256 ? sms : 2 * sms;
-    *parts = rows < parts_max ? rows : parts_max;
+    // 2 A rows and the parameters: 12 rows at most, 197 KB at H = 8192
+    const int smem = (GK == kGFull ? 12 : GK == kGChannel ? 11 : 10) * a.H * static_cast<int>(sizeof(bf16));
+    const cudaError_t e = api_smem_opt_in(opt, dev, norm_bwd_staged_kernel<GK, MAXT>, kSmemLimit - 2048);
+    if (e != cudaSuccess) return e;
+    const int most = sms * (512 / MAXT);
     *parts = *parts < most ? *parts : most;
-    return api_launch(norm_bwd_kernel<V, VEC, true, MAXT>, *parts, threads, smem, stream, a);
+    return api_launch(norm_bwd_staged_kernel<GK, MAXT>, *parts, threads, smem, stream, a);
 }
 
+// The grid is also the number of partial rows that norm_sum_kernel reads.
 template <bool VEC>
 cudaError_t launch_bwd(const NormArgs& a, int dev, int sms, int rows, int parts_max, int* parts, void* stream) {
     if (a.H <= 256) {
@@ -530,12 +659,20 @@ cudaError_t launch_bwd(const NormArgs& a, int dev, int sms, int rows, int parts_
                           stream, a);
     }
     const int th = norm_threads(a.H);
-    // two staged rows of more than 11000 columns do not fit in shared memory
-    if (th > 512 || (VEC && 2 * kRowArrays * a.H * static_cast<int>(sizeof(bf16)) > kSmemLimit - 2048))
-        return launch_bwd_rows<2, false, 1024>(a, dev, sms, th, rows, parts_max, parts, stream);
-    if (a.H <= 512) return launch_bwd_rows<1, VEC, 256>(a, dev, sms, th, rows, parts_max, parts, stream);
-    if (th <= 256) return launch_bwd_rows<2, VEC, 256>(a, dev, sms, th, rows, parts_max, parts, stream);
-    return launch_bwd_rows<2, VEC, 512>(a, dev, sms, th, rows, parts_max, parts, stream);
+    *parts = rows < parts_max ? rows : parts_max;
+    if (VEC && a.H > 512 && th <= 512 && a.y && a.gamma_pre && a.d_x_out && a.d_x_hat) {
+        if (th <= 256) {
+            if (a.gate_kind == kGateFull) return launch_bwd_staged<kGFull, 256>(a, dev, sms, th, rows, parts, stream);
+            if (a.gate_kind == kGateChannel) return launch_bwd_staged<kGChannel, 256>(a, dev, sms, th, rows, parts, stream);
+            return launch_bwd_staged<kGScalar, 256>(a, dev, sms, th, rows, parts, stream);
+        }
+        if (a.gate_kind == kGateFull) return launch_bwd_staged<kGFull, 512>(a, dev, sms, th, rows, parts, stream);
+        if (a.gate_kind == kGateChannel) return launch_bwd_staged<kGChannel, 512>(a, dev, sms, th, rows, parts, stream);
+        return launch_bwd_staged<kGScalar, 512>(a, dev, sms, th, rows, parts, stream);
+    }
+    if (a.H <= 512) return api_launch(norm_bwd_kernel<1, VEC, true, 512>, *parts, th, 0, stream, a);
+    if (th <= 512) return api_launch(norm_bwd_kernel<2, VEC, true, 512>, *parts, th, 0, stream, a);
+    return api_launch(norm_bwd_kernel<2, VEC, true, 1024>, *parts, th, 0, stream, a);
 }
 
 }  // namespace

@@ -39,6 +39,11 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+// The logit of a key (+0.0 for both zeros, a NaN for any NaN).
+__device__ __forceinline__ float key_logit(uint32_t key) {
+    return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
+}
+
 // One row a warp, expert e = lane + 32 i in register i; the next row's logits are
 // loaded while the current one is worked on.  The k rounds of the selection also
 // give the row's largest logit, so the softmax needs no max pass.  Sums over
@@ -86,25 +91,24 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_topk_kernel(const
             key[i] = lane + 32 * i < E ? logit_key(v[i]) : 0u;
         }
         load(t + step, nv, non);
-        float myL = -INFINITY;
-        int myE = -1;
+        uint32_t mykey = 0, myE = 0;
 #pragma unroll 1
         for (int j = 0; j < k; ++j) {
             uint32_t bk = key[0];
-            int bi = 0;
 #pragma unroll
-            for (int i = 1; i < EPL; ++i)
-                if (key[i] > bk) { bk = key[i]; bi = i; }
+            for (int i = 1; i < EPL; ++i) bk = max(bk, key[i]);
             const uint32_t kmax = __reduce_max_sync(0xffffffffu, bk);
-            const uint32_t e = __reduce_min_sync(
-                0xffffffffu, bk == kmax ? static_cast<uint32_t>(lane + 32 * bi) : 0xffffffffu);
-            float Lw = 0.0f;
+            uint32_t e = 0xffffffffu;  // this lane's lowest expert that holds it
+#pragma unroll
+            for (int i = EPL - 1; i >= 0; --i)
+                if (key[i] == kmax) e = static_cast<uint32_t>(lane + 32 * i);
+            e = __reduce_min_sync(0xffffffffu, e);
 #pragma unroll
             for (int i = 0; i < EPL; ++i)
-                if (static_cast<uint32_t>(lane + 32 * i) == e) { key[i] = 0u; Lw = v[i]; }
-            Lw = __shfl_sync(0xffffffffu, Lw, e & 31);
-            if (lane == j) { myL = Lw; myE = static_cast<int>(e); }
+                if (static_cast<uint32_t>(lane + 32 * i) == e) key[i] = 0u;
+            if (lane == j) { mykey = kmax; myE = e; }
         }
+        const float myL = lane < k ? key_logit(mykey) : -INFINITY;
         const float L0 = __shfl_sync(0xffffffffu, myL, 0);
         const bool live = masked_in && !(L0 == -INFINITY);
         const bool on = live && lane < k && !(myL == -INFINITY);
@@ -122,7 +126,7 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_topk_kernel(const
             s += __shfl_xor_sync(0xffffffffu, s, off);
         }
         if (lane < k) {
-            p.idx[static_cast<size_t>(t) * k + lane] = on ? myE : -1;
+            p.idx[static_cast<size_t>(t) * k + lane] = on ? static_cast<int>(myE) : -1;
             p.w[static_cast<size_t>(t) * k + lane] = on ? ex / z : 0.0f;
         }
         if (on) atomicAdd(&hist[myE], 1);
@@ -294,11 +298,9 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(const RouterBwdArgs p) 
     const float db = p.d_losses ? p.d_losses[0] : 0.0f;
     const float dz = p.d_losses ? 2.0f * p.d_losses[1] / rows : 0.0f;
     float cost[EPL];  // E f_e / n: what a unit of probability on expert e costs
+    const float per = static_cast<float>(E) / (rows * k) / rows;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        const int e = lane + 32 * i;
-        cost[i] = e < E ? static_cast<float>(E) * (static_cast<float>(p.counts[e]) / (rows * k)) / rows : 0.0f;
-    }
+    for (int i = 0; i < EPL; ++i) cost[i] = lane + 32 * i < E ? per * static_cast<float>(p.counts[lane + 32 * i]) : 0.0f;
     for (int t = t0; t < T; t += step) {
         const Row c = nx;
         load(t + step, nx);

@@ -598,7 +598,7 @@ struct W4ConvArgs {
     bf16* w_out;
     uint8_t* q_out;
     bf16* s_out;
-    int N, K, group, chunk;  // chunk: inputs a CTA takes, a multiple of 256 (or all of K)
+    int N, K, chunk;  // chunk: inputs a CTA takes, a multiple of 256 (or all of K)
 };
 
 // Eight inputs a lane and step (16 bytes), four steps in flight; the lanes of a
@@ -611,12 +611,13 @@ struct W4ConvArgs {
 // that; rounding y to a multiple of 2^-13 first brings the half-way cases back
 // and moves no other across.  Scales below 2^-126 (whose reciprocal overflows)
 // are divided by.
+template <int G>
 __global__ void __launch_bounds__(kConvRows * 32) w4_quantize_kernel(const W4ConvArgs p) {
-    __shared__ __align__(16) __nv_bfloat16 sc[kConvK / 32][kConvRows];
+    __shared__ __align__(16) __nv_bfloat16 sc[kConvK / G][kConvRows];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const size_t row0 = static_cast<size_t>(blockIdx.x) * kConvRows, row = row0 + warp;
     const int k0 = blockIdx.y * p.chunk, kn = min(p.chunk, p.K - k0);
-    const int lanes = p.group / 8;
+    constexpr int lanes = G / 8;
     const uint4* src = reinterpret_cast<const uint4*>(p.w + row * p.K + k0);
     uint32_t* dst = reinterpret_cast<uint32_t*>(p.q_out + (row * p.K + k0) / 2);
     const int vecs = kn / 8;
@@ -636,6 +637,7 @@ __global__ void __launch_bounds__(kConvRows * 32) w4_quantize_kernel(const W4Con
 #pragma unroll
             for (int j = 1; j < 4; ++j)
                 m2 = __hmax2_nan(m2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&u[j])));
+#pragma unroll
             for (int off = 1; off < lanes; off <<= 1) {
                 const uint32_t o = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&m2), off);
                 m2 = __hmax2_nan(m2, *reinterpret_cast<const __nv_bfloat162*>(&o));
@@ -677,22 +679,23 @@ __global__ void __launch_bounds__(kConvRows * 32) w4_quantize_kernel(const W4Con
     }
     __syncthreads();
     const size_t e = row0 / p.N;
-    const int n0 = static_cast<int>(row0 - e * p.N), groups = p.K / p.group, g0 = k0 / p.group;
-    for (int g = threadIdx.x; g < kn / p.group; g += blockDim.x)
+    const int n0 = static_cast<int>(row0 - e * p.N), groups = p.K / G, g0 = k0 / G;
+    for (int g = threadIdx.x; g < kn / G; g += blockDim.x)
         *reinterpret_cast<uint4*>(p.s_out + (e * groups + g0 + g) * p.N + n0) = *reinterpret_cast<const uint4*>(&sc[g][0]);
 }
 
 // The same split.  128 + q by or-ing the nibble into bf16, minus 136, times the
 // scale: the first two are exact, the product is rounded once.
+template <int G>
 __global__ void __launch_bounds__(kConvRows * 32) w4_dequantize_kernel(const W4ConvArgs p) {
-    __shared__ __align__(16) __nv_bfloat16 sc[kConvK / 32][kConvRows];
+    __shared__ __align__(16) __nv_bfloat16 sc[kConvK / G][kConvRows];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const size_t row0 = static_cast<size_t>(blockIdx.x) * kConvRows, row = row0 + warp;
     const int k0 = blockIdx.y * p.chunk, kn = min(p.chunk, p.K - k0);
-    const int lanes = p.group / 8;
+    constexpr int lanes = G / 8;
     const size_t e = row0 / p.N;
-    const int n0 = static_cast<int>(row0 - e * p.N), groups = p.K / p.group, g0 = k0 / p.group;
-    for (int g = threadIdx.x; g < kn / p.group; g += blockDim.x)
+    const int n0 = static_cast<int>(row0 - e * p.N), groups = p.K / G, g0 = k0 / G;
+    for (int g = threadIdx.x; g < kn / G; g += blockDim.x)
         *reinterpret_cast<uint4*>(&sc[g][0]) = *reinterpret_cast<const uint4*>(p.s + (e * groups + g0 + g) * p.N + n0);
     __syncthreads();
     const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + (row * p.K + k0) / 2);
@@ -853,9 +856,10 @@ int et_w4_quantize(const void* w, void* q, void* scale, int E, int N, int K, int
         a.s_out = static_cast<bf16*>(scale);
         a.N = N;
         a.K = K;
-        a.group = group;
         const dim3 grid = w4_conv_grid(&a, E, sms);
-        const cudaError_t e = api_launch(w4_quantize_kernel, grid, kConvRows * 32, 0, stream, a);
+        const cudaError_t e = api_launch(group == 32 ? w4_quantize_kernel<32> : group == 64 ? w4_quantize_kernel<64>
+                                                                   : w4_quantize_kernel<128>,
+                                          grid, kConvRows * 32, 0, stream, a);
         if (e != cudaSuccess) return api_fail_cuda(e, "launch of the 4-bit quantiser");
         return ET_OK;
     });
@@ -876,9 +880,10 @@ int et_w4_dequantize(const void* q, const void* scale, void* w, int E, int N, in
         a.w_out = static_cast<bf16*>(w);
         a.N = N;
         a.K = K;
-        a.group = group;
         const dim3 grid = w4_conv_grid(&a, E, sms);
-        const cudaError_t e = api_launch(w4_dequantize_kernel, grid, kConvRows * 32, 0, stream, a);
+        const cudaError_t e = api_launch(group == 32 ? w4_dequantize_kernel<32> : group == 64 ? w4_dequantize_kernel<64>
+                                                                     : w4_dequantize_kernel<128>,
+                                          grid, kConvRows * 32, 0, stream, a);
         if (e != cudaSuccess) return api_fail_cuda(e, "launch of the 4-bit expansion");
         return ET_OK;
     });
