@@ -49,17 +49,33 @@ cudaError_t api_smem_opt_in(SmemOptIn& st, int dev, K kernel, int bytes) {
     return e;
 }
 
-// One launch; the error is this launch's own (cudaGetLastError could return an
-// older one of the calling program).
+// One launch; cluster: CTAs a cluster; early: it may be scheduled while the
+// kernel before it drains (its kernel then waits, see grid_wait in ops_device.cuh).
+// The error is this launch's own (cudaGetLastError could return an older one of
+// the calling program).
 template <class... P, class... A>
-cudaError_t api_launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, void* stream,
-                       A&&... args) {
+cudaError_t api_launch_cluster(void (*kernel)(P...), dim3 grid, dim3 block, int cluster, bool early, size_t smem,
+                               void* stream, A&&... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = early ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+template <class... P, class... A>
+cudaError_t api_launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, void* stream, A&&... args) {
+    return api_launch_cluster(kernel, grid, block, 1, true, smem, stream, std::forward<A>(args)...);
 }
 
 }  // namespace et

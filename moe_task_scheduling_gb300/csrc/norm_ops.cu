@@ -107,6 +107,7 @@ template <int V, bool VEC, bool ROW>
 __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormArgs p) {
     __shared__ float red[2][32];
     int sums = 0;
+    grid_begin();
     bool ok;
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
     const int H = p.H;
@@ -201,6 +202,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormArgs p) {
     __shared__ float red[2][32], red2[2][32];
     int sums = 0;
     extern __shared__ __align__(16) uint8_t dyn[];  // !ROW: [warps][3][256] floats
+    grid_begin();
     bool ok;
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
     const int H = p.H;
@@ -400,6 +402,7 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) norm_bwd_staged_kernel(const
     __shared__ float red[2][32], red2[2][32];
     extern __shared__ __align__(16) uint8_t dyn[];  // [2][A][H] rows; gamma_post, gamma_pre (, gate) [H]
     int sums = 0;
+    grid_begin();
     bool ok;
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
     if (!ok) return;
@@ -558,6 +561,7 @@ struct NormSumArgs {
 // (L2-resident) loads of a column are in flight together.
 __global__ void __launch_bounds__(1024) norm_sum_kernel(const NormSumArgs p) {
     __shared__ float red[32][33];
+    grid_begin();
     if (p.d_T && (*p.d_T < 0 || *p.d_T > p.T_max)) return;
     float* out = p.out[blockIdx.y];
     if (!out) return;

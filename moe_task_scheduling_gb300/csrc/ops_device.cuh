@@ -12,6 +12,17 @@
 
 namespace et {
 
+// Most of these kernels are launched with programmatic stream serialisation: one
+// may be scheduled while the kernel before it in the stream drains, so it waits
+// for that kernel's end (and its writes) before it touches global memory, then
+// lets its own successor be scheduled.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_begin() {
+    grid_wait();
+    grid_release();
+}
+
 // Status details of these kernels (et_status), after the wait sites of et_layout.h.
 constexpr int kWhereExpertIndex = 13;  // an expert index outside [-1, E)
 

@@ -50,7 +50,8 @@ __device__ __forceinline__ float key_logit(uint32_t key) {
 // rows: per warp in registers (32 rows, then once more, so that long sums stay
 // short), per CTA in shared memory, over CTAs by the last one to finish -- each
 // in a fixed order, so that losses and mean probabilities are the same bits on
-// every run.  All in fp32: fp64 runs at 1/64 of it here.
+// every run.  All in fp32: fp64 runs at 1/64 of it here.  exp, log and the
+// quotients are the fast ones: within |L - L0| + 4 and 2 units of 2^-24.
 template <int EPL>
 __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_topk_kernel(const RouterArgs p) {
     extern __shared__ __align__(16) float sm[];  // [warps][E], then the last CTA's sums
@@ -60,6 +61,7 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_topk_kernel(const
     __shared__ int last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
     const int E = p.E, k = p.k;
+    grid_begin();
     bool ok;
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
     if (!ok) return;
@@ -91,32 +93,67 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_topk_kernel(const
             key[i] = lane + 32 * i < E ? logit_key(v[i]) : 0u;
         }
         load(t + step, nv, non);
+        // A lane's entries in descending order (neighbours change places only for a
+        // strictly larger key, so equal ones stay in the order of their experts);
+        // then each round looks at the heads alone.  i_[] is the place i of an entry.
+        int i_[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) i_[i] = i;
+        constexpr bool kSorted = EPL == 4;  // 2: nothing to gain; 8: 28 exchanges
+        if (kSorted) {
+#pragma unroll
+            for (int n = EPL - 1; n > 0; --n)
+#pragma unroll
+                for (int i = 0; i < n; ++i) {
+                    const bool up = key[i + 1] > key[i];
+                    const uint32_t ka = key[i];
+                    const int ia = i_[i];
+                    key[i] = up ? key[i + 1] : ka;
+                    i_[i] = up ? i_[i + 1] : ia;
+                    key[i + 1] = up ? ka : key[i + 1];
+                    i_[i + 1] = up ? ia : i_[i + 1];
+                }
+        }
         uint32_t mykey = 0, myE = 0;
 #pragma unroll 1
         for (int j = 0; j < k; ++j) {
             uint32_t bk = key[0];
+            if (!kSorted)
 #pragma unroll
-            for (int i = 1; i < EPL; ++i) bk = max(bk, key[i]);
+                for (int i = 1; i < EPL; ++i) bk = max(bk, key[i]);
             const uint32_t kmax = __reduce_max_sync(0xffffffffu, bk);
-            uint32_t e = 0xffffffffu;  // this lane's lowest expert that holds it
+            uint32_t mine = 0xffffffffu;  // this lane's lowest expert that holds it
+            if (kSorted) {
+                if (bk == kmax) mine = static_cast<uint32_t>(lane + 32 * i_[0]);
+            } else {
 #pragma unroll
-            for (int i = EPL - 1; i >= 0; --i)
-                if (key[i] == kmax) e = static_cast<uint32_t>(lane + 32 * i);
-            e = __reduce_min_sync(0xffffffffu, e);
+                for (int i = EPL - 1; i >= 0; --i)
+                    if (key[i] == kmax) mine = static_cast<uint32_t>(lane + 32 * i);
+            }
+            const uint32_t e = __reduce_min_sync(0xffffffffu, mine);
+            if (kSorted) {
+                const bool win = mine == e;
 #pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (static_cast<uint32_t>(lane + 32 * i) == e) key[i] = 0u;
+                for (int i = 0; i < EPL; ++i) {
+                    key[i] = win ? (i + 1 < EPL ? key[(i + 1) % EPL] : 0u) : key[i];
+                    if (i + 1 < EPL) i_[i] = win ? i_[(i + 1) % EPL] : i_[i];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if (static_cast<uint32_t>(lane + 32 * i) == e) key[i] = 0u;
+            }
             if (lane == j) { mykey = kmax; myE = e; }
         }
         const float myL = lane < k ? key_logit(mykey) : -INFINITY;
         const float L0 = __shfl_sync(0xffffffffu, myL, 0);
         const bool live = masked_in && !(L0 == -INFINITY);
         const bool on = live && lane < k && !(myL == -INFINITY);
-        const float ex = on ? expf(myL - L0) : 0.0f;
+        const float ex = on ? __expf(myL - L0) : 0.0f;
         float pe[EPL], s = 0.0f;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            pe[i] = live && lane + 32 * i < E ? expf(v[i] - L0) : 0.0f;
+            pe[i] = live && lane + 32 * i < E ? __expf(v[i] - L0) : 0.0f;
             s += pe[i];
         }
         float z = ex;
@@ -127,12 +164,12 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_topk_kernel(const
         }
         if (lane < k) {
             p.idx[static_cast<size_t>(t) * k + lane] = on ? static_cast<int>(myE) : -1;
-            p.w[static_cast<size_t>(t) * k + lane] = on ? ex / z : 0.0f;
+            p.w[static_cast<size_t>(t) * k + lane] = on ? __fdividef(ex, z) : 0.0f;
         }
         if (on) atomicAdd(&hist[myE], 1);
         if (live) {
-            const float inv = 1.0f / s;
-            const float lse = L0 + logf(s);
+            const float inv = __fdividef(1.0f, s);
+            const float lse = L0 + __logf(s);
 #pragma unroll
             for (int i = 0; i < EPL; ++i) accp[i] += pe[i] * inv;
             accz += lse * lse;
@@ -205,10 +242,17 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_topk_kernel(const
             const int e = o % E;
             float s = 0.0f;
             int c = 0;
-#pragma unroll 10
-            for (int g = o / E; g < G; g += groups) {
-                s += __ldcg(p.part_p + g * E + e);
-                c += __ldcg(p.part_c + g * E + e);
+            for (int g0 = o / E; g0 < G; g0 += 10 * groups) {
+                float v[10];
+                int n[10];
+#pragma unroll
+                for (int i = 0; i < 10; ++i) {  // twenty loads in flight
+                    const int g = g0 + i * groups;
+                    v[i] = g < G ? __ldcg(p.part_p + g * E + e) : 0.0f;
+                    n[i] = g < G ? __ldcg(p.part_c + g * E + e) : 0;
+                }
+#pragma unroll
+                for (int i = 0; i < 10; ++i) { s += v[i]; c += n[i]; }
             }
             sm[o] = s;
             csum[o] = c;
@@ -270,11 +314,17 @@ struct RouterBwdArgs {
 // row's the loads of the counts, so that one memory latency is paid a warp.
 template <int EPL>
 __global__ void __launch_bounds__(256) router_bwd_kernel(const RouterBwdArgs p) {
+    __shared__ float add_s[8][32 * EPL];  // a row's gradients through the gate weights, by expert
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
     const int E = p.E, k = p.k;
+    grid_begin();
     bool ok;
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
     if (!ok) return;
+    float* add = add_s[warp];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) add[lane + 32 * i] = 0.0f;
+    __syncwarp();
     const int t0 = blockIdx.x * nwarps + warp, step = gridDim.x * nwarps;
     struct Row {
         float v[EPL], w, dw;
@@ -322,7 +372,7 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(const RouterBwdArgs p) 
             float pe[EPL], s = 0.0f, cp = 0.0f, dot = w * dw;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
-                pe[i] = lane + 32 * i < E ? expf(c.v[i] - m) : 0.0f;
+                pe[i] = lane + 32 * i < E ? __expf(c.v[i] - m) : 0.0f;
                 s += pe[i];
                 cp += pe[i] * cost[i];
             }
@@ -332,24 +382,27 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(const RouterBwdArgs p) 
                 cp += __shfl_xor_sync(0xffffffffu, cp, off);
                 dot += __shfl_xor_sync(0xffffffffu, dot, off);
             }
-            const float inv = 1.0f / s;
+            const float inv = __fdividef(1.0f, s);
             cp *= inv;
-            const float zl = dz * (m + logf(s));
+            const float zl = dz * (m + __logf(s));
+            if (p.d_w) {
+                // an index outside [0, E) adds nothing; one that comes twice adds twice
+                const bool sel = c.e >= 0 && c.e < E;
+                if (sel) atomicAdd(add + c.e, w * (dw - dot));
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) d[i] = add[lane + 32 * i];
+                __syncwarp();
+                if (sel) add[c.e] = 0.0f;
+            } else {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) d[i] = 0.0f;
+            }
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
                 const float pr = pe[i] * inv;
-                d[i] = db * pr * (cost[i] - cp) + zl * pr;
+                d[i] += db * pr * (cost[i] - cp) + zl * pr;
             }
-            const float ds = w * (dw - dot);
-            if (p.d_w)
-#pragma unroll 4
-                for (int j = 0; j < k; ++j) {
-                    const int ej = __shfl_sync(0xffffffffu, c.e, j);
-                    const float dj = __shfl_sync(0xffffffffu, ds, j);
-#pragma unroll
-                    for (int i = 0; i < EPL; ++i)
-                        if (ej == lane + 32 * i) d[i] += dj;
-                }
         } else {
 #pragma unroll
             for (int i = 0; i < EPL; ++i) d[i] = 0.0f;

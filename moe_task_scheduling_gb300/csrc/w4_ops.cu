@@ -38,7 +38,8 @@ struct W4Args {
     const int32_t* d_T;
     int T_host, T_max, N, K, E, k;
     EtHeader* hdr;
-    int x_rows;               // rows of x a stage holds = rows of a pass or segment
+    int x_rows;               // rows of x a stage holds = most rows of a pass or segment
+    int sum_rows;             // rows of a warp's fp32 tile: x_rows, or (down) the tokens
     uint32_t magic;           // 0x43004300 (see unpack8)
 };
 
@@ -136,33 +137,44 @@ __device__ __forceinline__ void compute_stage(const W4Stage& st, int nc, uint32_
                 mma16816(off[j], neg, neg, neg, neg, b[i][j][2], b[i][j][3], off[j]);
             }
         }
+        // MC row tiles at a time: their chains of products are independent, which hides
+        // the tensor core's latency when few warps are there to do it
+        constexpr int MC = 1;
         const __nv_bfloat16* sa = reinterpret_cast<const __nv_bfloat16*>(st.s + g * 128) + r;
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            uint32_t lo[W], hi[W];
-            const uint8_t* a = st.w + (m * 16 + r) * 64 + (swz_w<G>(g * (G / 32) + (t * W >> 2), r) << 4) + ((t * W & 3) << 2);
-            ld_words<W>(a, lo);
-            ld_words<W>(a + 512, hi);
-            const float s0 = __bfloat162float(sa[m * 16]), s1 = __bfloat162float(sa[m * 16 + 8]);
-            float part[NT][4];
+        for (int m0 = 0; m0 < 4; m0 += MC) {
+            uint32_t lo[MC][W], hi[MC][W];
+            float s0[MC], s1[MC], part[MC][NT][4];
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-                uint32_t u[4], v[4];
-                unpack8(lo[i], magic, u);
-                unpack8(hi[i], magic, v);
+            for (int m = 0; m < MC; ++m) {
+                const uint8_t* a = st.w + ((m0 + m) * 16 + r) * 64 + (swz_w<G>(g * (G / 32) + (t * W >> 2), r) << 4) + ((t * W & 3) << 2);
+                ld_words<W>(a, lo[m]);
+                ld_words<W>(a + 512, hi[m]);
+                s0[m] = __bfloat162float(sa[(m0 + m) * 16]);
+                s1[m] = __bfloat162float(sa[(m0 + m) * 16 + 8]);
+            }
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+#pragma unroll
+                for (int m = 0; m < MC; ++m) {
+                    uint32_t u[4], v[4];
+                    unpack8(lo[m][i], magic, u);
+                    unpack8(hi[m][i], magic, v);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        mma16816(part[m][j], u[0], v[0], u[1], v[1], b[i][j][0], b[i][j][1], i == 0 ? off[j] : part[m][j]);
+                        mma16816(part[m][j], u[2], v[2], u[3], v[3], b[i][j][2], b[i][j][3], part[m][j]);
+                    }
+                }
+#pragma unroll
+            for (int m = 0; m < MC; ++m)
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    mma16816(part[j], u[0], v[0], u[1], v[1], b[i][j][0], b[i][j][1], i == 0 ? off[j] : part[j]);
-                    mma16816(part[j], u[2], v[2], u[3], v[3], b[i][j][2], b[i][j][3], part[j]);
+                    acc[m0 + m][j][0] += s0[m] * part[m][j][0];
+                    acc[m0 + m][j][1] += s0[m] * part[m][j][1];
+                    acc[m0 + m][j][2] += s1[m] * part[m][j][2];
+                    acc[m0 + m][j][3] += s1[m] * part[m][j][3];
                 }
-            }
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                acc[m][j][0] += s0 * part[j][0];
-                acc[m][j][1] += s0 * part[j][1];
-                acc[m][j][2] += s1 * part[j][2];
-                acc[m][j][3] += s1 * part[j][3];
-            }
         }
     }
 }
@@ -192,22 +204,91 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
 // The routed rows of a call, grouped by expert, in shared memory.  Rows r = t k + j
 // whose index is -1 are left out; an index outside [-1, E) is recorded and left out.
 struct W4Routing {
-    int16_t e[kW4RoutedMax];        // row -> expert (-1: none)
-    int16_t order[kW4RoutedMax];    // rows by expert, ascending within one
-    float wt[kW4RoutedMax];         // their gate weights
-    int16_t seg_e[kW4RoutedMax];    // segments: up to `width` rows of one expert
-    int16_t seg_r[kW4RoutedMax];
-    int16_t seg_n[kW4RoutedMax];
-    int16_t cnt[kW4Warps][kW4EMax]; // rows of an expert in a warp's share, then their first entry in `order`
-    int total[kW4Warps];
-    int n_seg;
-    int twice;                      // a token names an expert twice
+    float* wt;          // [R] gate weight of an entry of `order`
+    int16_t* order;     // [R] rows by expert, ascending within one
+    int16_t* tok;       // [R] their tokens
+    int16_t* seg_e;     // [R] segments: up to `width` rows of one expert: the expert,
+    int16_t* seg_r;     // [R] its first entry in `order`,
+    int16_t* seg_n;     // [R] its rows
+    int16_t* e;         // [R] row -> expert (-1: none)
+    int16_t* cnt;       // [4][E'] rows of an expert in a warp's share, then their first entry
+    int* shared;        // [6]: scan totals, n_seg, whether a token names an expert twice
+    int Ep;             // E rounded up to even
+    int n_seg, twice;
+
+    __host__ __device__ static int bytes(int R, int E) {
+        return (R * 16 + kW4Warps * ((E + 1) & ~1) * 2 + 24 + 127) / 128 * 128;
+    }
+    __device__ __forceinline__ void place(uint8_t* at, int R, int E) {
+        wt = reinterpret_cast<float*>(at);
+        shared = reinterpret_cast<int*>(wt + R);
+        cnt = reinterpret_cast<int16_t*>(shared + 6);
+        Ep = (E + 1) & ~1;
+        order = cnt + kW4Warps * Ep;
+        tok = order + R;
+        seg_e = tok + R;
+        seg_r = seg_e + R;
+        seg_n = seg_r + R;
+        e = seg_n + R;
+    }
 };
 static_assert(kW4Warps * 32 * 2 >= kW4EMax, "two experts a thread");
 static_assert(kW4RoutedMax <= kW4Warps * 128, "four rows a thread");
 
+// Up to 32 rows (decoding): one warp, experts in the order of their first row,
+// one barrier.  More: all warps, experts ascending.
 __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, int T, int width) {
     const int R = T * p.k, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (R <= 32) {
+        if (warp == 0) {
+            int e = lane < R ? p.idx[lane] : -1;
+            const float wt = lane < R ? p.w[lane] : 0.0f;
+            if (e < -1 || e >= p.E) {
+                record_status(p.hdr, ET_ERR_BOUNDS, kWhereExpertIndex);
+                e = -1;
+            }
+            __syncwarp();
+            const uint32_t same = __match_any_sync(0xffffffffu, e);
+            const int before = __popc(same & ((1u << lane) - 1u)), c = __popc(same);
+            const bool lead = e >= 0 && before == 0;
+            const int v = lead ? c | ((c + width - 1) / width << 16) : 0;  // rows, segments
+            int inc = v;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, inc, off);
+                if (lane >= off) inc += up;
+            }
+            const int base = inc - v;
+            const int r0 = __shfl_sync(0xffffffffu, base & 0xffff, __ffs(same) - 1);
+            bool again = false;  // an earlier row of this token with this expert
+            for (int o = 1; o < p.k; ++o) {
+                const int other = __shfl_up_sync(0xffffffffu, e, o);
+                again |= lane % p.k >= o && e >= 0 && other == e;
+            }
+            if (e >= 0) {
+                rt.order[r0 + before] = static_cast<int16_t>(lane);
+                rt.tok[r0 + before] = static_cast<int16_t>(lane / p.k);
+                rt.wt[r0 + before] = wt;
+            }
+            if (lead) {
+                int s0 = base >> 16;
+                for (int o = 0; o < c; o += width, ++s0) {
+                    rt.seg_e[s0] = static_cast<int16_t>(e);
+                    rt.seg_r[s0] = static_cast<int16_t>(r0 + o);
+                    rt.seg_n[s0] = static_cast<int16_t>(min(width, c - o));
+                }
+            }
+            again = __any_sync(0xffffffffu, again);
+            if (lane == 31) {
+                rt.shared[4] = inc >> 16;
+                rt.shared[5] = again;
+            }
+        }
+        __syncthreads();
+        rt.n_seg = rt.shared[4];
+        rt.twice = rt.shared[5];
+        return;
+    }
     const int span = (R + kW4Warps * 32 - 1) / (kW4Warps * 32) * 32;  // consecutive rows of a warp
     int e[4], at[4];
     float wt[4];
@@ -218,10 +299,11 @@ __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, in
         e[i] = in ? p.idx[r] : -1;
         wt[i] = in ? p.w[r] : 0.0f;
     }
-    for (int i = tid; i < kW4Warps * kW4EMax / 2; i += blockDim.x) reinterpret_cast<int*>(rt.cnt)[i] = 0;
-    if (tid == 0) rt.twice = 0;
+    for (int i = tid; i < kW4Warps * rt.Ep / 2; i += blockDim.x) reinterpret_cast<int*>(rt.cnt)[i] = 0;
+    if (tid == 0) rt.shared[5] = 0;
     __syncthreads();
     // a row's place among its warp's rows of that expert
+    int16_t* mine = rt.cnt + warp * rt.Ep;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (i * 32 >= span) break;
@@ -230,12 +312,13 @@ __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, in
             record_status(p.hdr, ET_ERR_BOUNDS, kWhereExpertIndex);
             e[i] = -1;
         }
+        __syncwarp();
         const uint32_t same = __match_any_sync(0xffffffffu, e[i]);
         const int before = __popc(same & ((1u << lane) - 1u));
         int have = 0;
-        if (e[i] >= 0) have = rt.cnt[warp][e[i]];
+        if (e[i] >= 0) have = mine[e[i]];
         __syncwarp();
-        if (e[i] >= 0 && before == 0) rt.cnt[warp][e[i]] = static_cast<int16_t>(have + __popc(same));
+        if (e[i] >= 0 && before == 0) mine[e[i]] = static_cast<int16_t>(have + __popc(same));
         __syncwarp();
         at[i] = have + before;
         if (r < R) rt.e[r] = static_cast<int16_t>(e[i]);
@@ -247,9 +330,9 @@ __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, in
     for (int h = 0; h < 2; ++h) {
         const int x = 2 * tid + h;
         c[h] = 0;
-        if (x < kW4EMax)
+        if (x < p.E)
 #pragma unroll
-            for (int w = 0; w < kW4Warps; ++w) c[h] += rt.cnt[w][x];
+            for (int w = 0; w < kW4Warps; ++w) c[h] += rt.cnt[w * rt.Ep + x];
         v[h] = c[h] | ((c[h] + width - 1) / width << 16);
         sum += v[h];
     }
@@ -259,18 +342,18 @@ __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, in
         const int up = __shfl_up_sync(0xffffffffu, inc, off);
         if (lane >= off) inc += up;
     }
-    if (lane == 31) rt.total[warp] = inc;
+    if (lane == 31) rt.shared[warp] = inc;
     // a token's rows against its earlier ones
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = warp * span + i * 32 + lane;
         if (i * 32 < span && r < R && e[i] >= 0)
             for (int o = r - r % p.k; o < r; ++o)
-                if (rt.e[o] == e[i]) rt.twice = 1;
+                if (rt.e[o] == e[i]) rt.shared[5] = 1;
     }
     __syncthreads();
     int base = inc - sum;
-    for (int w = 0; w < warp; ++w) base += rt.total[w];
+    for (int w = 0; w < warp; ++w) base += rt.shared[w];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int x = 2 * tid + h;
@@ -284,36 +367,44 @@ __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, in
             }
 #pragma unroll
             for (int w = 0; w < kW4Warps; ++w) {
-                const int n = rt.cnt[w][x];
-                rt.cnt[w][x] = static_cast<int16_t>(a);
+                const int n = rt.cnt[w * rt.Ep + x];
+                rt.cnt[w * rt.Ep + x] = static_cast<int16_t>(a);
                 a += n;
             }
         }
         base += v[h];
     }
-    if (tid == static_cast<int>(blockDim.x) - 1) rt.n_seg = base >> 16;
+    if (tid == static_cast<int>(blockDim.x) - 1) rt.shared[4] = base >> 16;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = warp * span + i * 32 + lane;
         if (i * 32 < span && r < R && e[i] >= 0) {
-            const int o = rt.cnt[warp][e[i]] + at[i];
+            const int o = mine[e[i]] + at[i];
             rt.order[o] = static_cast<int16_t>(r);
+            rt.tok[o] = static_cast<int16_t>(r / p.k);
             rt.wt[o] = wt[i];
         }
     }
+    rt.n_seg = rt.shared[4];
+    rt.twice = rt.shared[5];
     __syncthreads();
 }
 
-// One CTA of four warps: RW row groups x 4 / RW splits of the inputs.  The inputs
-// are split further over the CTAs of the cluster.  The RW warps of a split share
-// its x rows and meet at a named barrier once a k-block; splits run on their
-// own, each through its own ring.
-//   kW4Gemv   x rows in chunks of x_rows <= 8 NT, all of K.
-//   kW4GateUp blockIdx.y picks the segment: up to x_rows rows of one expert.
-//   kW4Down   the work is the list of (segment, k-block); a warp adds what it
-//             has for a segment, times the gate weight, to its own fp32 rows by
-//             token, and the sum over splits and CTAs is the layer's output.
+// One CTA of four warps: RW row groups x KW = 4 / RW splits of the inputs.  The
+// RW warps of a split share its x rows and meet at a named barrier once a
+// k-block; splits run on their own, each through its own ring, and the copies
+// run ahead across the units of a CTA.
+//   kW4Gemv    a unit is a tile of weight rows and up to x_rows <= 8 NT rows of x.
+//   kW4GateUp  a unit is a tile (half gate, half up) and a segment: up to x_rows
+//              rows of one expert.
+//     Both: with as many units as CTAs that fit, or more, a CTA takes units in
+//     turn and splits their inputs over its warps; with fewer, a cluster of CTAs
+//     takes one unit and splits its inputs over all their warps.
+//   kW4Down    a cluster takes a tile of the output and splits the list of
+//              (segment, k-block) over its warps; a warp adds what it has for a
+//              segment, times the gate weight, to its own fp32 rows by token, and
+//              the sum over splits and CTAs is the layer's output.
 template <int MODE, int NT, int G>
 struct W4Shape {
     static constexpr int RW = NT == 1 ? 1 : NT == 2 ? 2 : 4;  // row groups
@@ -328,164 +419,171 @@ struct W4Shape {
 template <int MODE, int NT, int G>
 __global__ void __launch_bounds__(kW4Warps * 32) w4_kernel(const W4Args p) {
     using S = W4Shape<MODE, NT, G>;
+    constexpr bool kDown = MODE == kW4Down;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int x_row[NT * 8];    // gemv and gate/up: this pass's rows of x
-    __shared__ int out_row[NT * 8];  // gate/up: the routed rows
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rw = warp % S::RW, kw = warp / S::RW;
     const int csize = static_cast<int>(cluster_size()), crank = static_cast<int>(cluster_rank());
-    const int unit = crank * S::KW + kw, units = csize * S::KW;
-    const int n0 = (blockIdx.x / csize) * S::kOut;                        // the CTA's first output
-    const int nw = n0 + rw * (MODE == kW4GateUp ? kW4Rows / 2 : kW4Rows);  // this warp's
+    const int split = crank * S::KW + kw, splits = csize * S::KW;
     const int KB = (p.K + kW4Blk - 1) / kW4Blk;
+    const int tiles = (p.N + S::kOut - 1) / S::kOut;
+    // The down kernel is scheduled while the gate/up kernel of its call drains.  That
+    // one has started after everything before it, so only h is not there yet, and
+    // waited for below: routing and the first weights come in meanwhile (T = 1,
+    // fine-grained: 17.1 -> 14.6 us).  The others start when the stream is free:
+    // early starts spread their CTAs unevenly over the SMs (M = 16, 4096 x 14336:
+    // 16.4 -> 19.9 us).
+    if (MODE == kW4GateUp) grid_release();
     bool ok;
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
-    if (!ok) return;  // the same for every CTA of the cluster
-
-    // shared memory.  gemv and gate/up: the rings, and over them (before: the
-    // routing; after: the fp32 sums).  down: [routing][fp32 sums by token][rings].
-    W4Routing& rt = *reinterpret_cast<W4Routing*>(smem);
-    uint8_t* rest = smem;
-    if (MODE == kW4Down) rest += (sizeof(W4Routing) + 127) / 128 * 128;
-    float* sums = reinterpret_cast<float*>(rest);
-    if (MODE == kW4Down) rest += (static_cast<size_t>(kW4Warps) * T * kW4Pad * 4 + 127) / 128 * 128;
-    const int sbytes = S::stage_bytes(p.x_rows);
-    uint8_t* ring = rest + kw * kW4Stages * sbytes;
-
-    int nc0 = 0, e0 = 0;
-    if (MODE != kW4Gemv) build_routing(p, rt, T, p.x_rows);
-    if (MODE == kW4GateUp) {
-        if (static_cast<int>(blockIdx.y) >= rt.n_seg) return;  // the whole cluster
-        nc0 = rt.seg_n[blockIdx.y];
-        e0 = rt.seg_e[blockIdx.y];
-        if (static_cast<int>(threadIdx.x) < nc0) {
-            const int r = rt.order[rt.seg_r[blockIdx.y] + threadIdx.x];
-            out_row[threadIdx.x] = r;
-            x_row[threadIdx.x] = r / p.k;
-        }
-        __syncthreads();  // the routing's memory becomes the rings'
+    if (!ok) {  // the same for every CTA of the cluster
+        if (kDown) grid_wait();
+        return;
     }
-    if (MODE == kW4Down) {
+
+    // shared memory: [rings][fp32 sums: a tile a warp][routing]
+    const int sbytes = S::stage_bytes(p.x_rows);
+    uint8_t* ring = smem + kw * kW4Stages * sbytes;
+    float* sums = reinterpret_cast<float*>(smem + S::ring_bytes(p.x_rows));
+    W4Routing rt;
+    if (MODE != kW4Gemv) {
+        rt.place(reinterpret_cast<uint8_t*>(sums + kW4Warps * p.sum_rows * kW4Pad), p.T_max * p.k, p.E);
+        build_routing(p, rt, T, p.x_rows);
+    }
+
+    // The units of this CTA (or cluster), and the items -- k-blocks -- of one unit
+    // that are this split's.  Down: one unit, whose items are (segment, k-block).
+    const int passes = MODE == kW4Gemv ? (T + p.x_rows - 1) / p.x_rows : 1;
+    const int n_units = kDown ? tiles : tiles * (MODE == kW4GateUp ? rt.n_seg : passes);
+    const int u0 = blockIdx.x / csize, ustep = gridDim.x / csize;
+    const int items = kDown ? rt.n_seg * KB : KB;
+    const int i0 = static_cast<int>(static_cast<unsigned>(items) * split / splits);
+    const int i1 = static_cast<int>(static_cast<unsigned>(items) * (split + 1) / splits);
+    if (kDown) {
         for (int i = threadIdx.x; i < kW4Warps * T * kW4Pad; i += blockDim.x) sums[i] = 0.0f;
         __syncthreads();
     }
+    auto tile_of = [&](int u) { return kDown ? u : MODE == kW4GateUp ? u % tiles : u / passes; };
+    auto part_of = [&](int u) { return kDown ? 0 : MODE == kW4GateUp ? u / tiles : u % passes; };  // segment or pass
+    auto rows_of = [&](int part) {
+        return MODE == kW4Gemv ? min(p.x_rows, T - part * p.x_rows) : static_cast<int>(rt.seg_n[part]);
+    };
 
-    const int passes = MODE == kW4Gemv ? (T + p.x_rows - 1) / p.x_rows : 1;
-    for (int pass = 0; pass < passes; ++pass) {
-        if (MODE == kW4Gemv) {
-            nc0 = min(p.x_rows, T - pass * p.x_rows);
-            if (static_cast<int>(threadIdx.x) < nc0) x_row[threadIdx.x] = pass * p.x_rows + threadIdx.x;
-            __syncthreads();
+    auto stage_at = [&](int slot) {
+        uint8_t* b = ring + slot * sbytes;
+        return W4Stage{b + rw * S::kWarpBytes, b + rw * S::kWarpBytes + kW4Rows * 64, b + S::RW * S::kWarpBytes};
+    };
+    // Where the copies are: the next item, its ring slot, and this lane's first piece
+    // of its weights (row nw + lane / 4, 16 bytes lane % 4) and scales.  A warp's rows
+    // are [nw, nw + 64) of one matrix, or 32 + 32 of two.
+    const size_t ld = static_cast<size_t>(p.K) / 2, ld8 = ld * 8;
+    const int sg = lane >> 3, sc = lane & 7;  // this lane's group of the k-block and its 8 rows
+    const int sn8 = MODE == kW4GateUp ? (sc & 3) * 8 : sc * 8;
+    int pu = i0 < i1 ? u0 : n_units, pi = i0, slot = 0, part = 0, kb = 0, left = 0, nc_p = 0;
+    const uint8_t *qa, *qb;
+    const bf16* sp;
+    auto seek = [&]() {  // to item pi of unit pu
+        part = kDown ? pi / KB : part_of(pu);
+        kb = kDown ? pi - part * KB : pi;
+        nc_p = rows_of(part);
+        const int e = MODE == kW4Gemv ? 0 : rt.seg_e[part];
+        const int nw = tile_of(pu) * S::kOut + rw * (MODE == kW4GateUp ? kW4Rows / 2 : kW4Rows);
+        left = p.N - nw;  // rows there are: a multiple of 8
+        const size_t at = (static_cast<size_t>(e) * p.N + nw + (lane >> 2)) * ld + static_cast<size_t>(kb) * 64 + (lane & 3) * 16;
+        qa = p.q0 + at;
+        if (MODE == kW4GateUp) qb = p.q1 + at;
+        const bf16* s = (MODE == kW4GateUp && sc >= 4) ? p.s1 : p.s0;
+        sp = s + (static_cast<size_t>(e) * (p.K / G) + kb * (kW4Blk / G) + sg) * p.N + nw + sn8;
+    };
+    if (pu < n_units) seek();
+    // Post the copies of the next item and move on.  Pieces outside the matrices are
+    // filled with zeros.
+    auto post_w = [&](const W4Stage& st, int k0) {
+        const int r = lane >> 2, c = lane & 3;
+        const uint32_t dst = smem_addr(st.w) + r * 64 + (swz_w<G>(c, r) << 4);  // row + 8: the same swizzle
+        if (k0 + kW4Blk <= p.K && left >= (MODE == kW4GateUp ? kW4Rows / 2 : kW4Rows)) {
+            const uint8_t* q = qa;
+#pragma unroll
+            for (int g = 0; g < 8; ++g, q += ld8) {
+                if (MODE == kW4GateUp && g == 4) q = qb;
+                cp_async16(dst + g * 512, q);
+            }
+        } else {
+            const bool kin = k0 + c * 32 < p.K;
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+                const int g8 = MODE == kW4GateUp ? g & 3 : g;
+                const bool in = kin && g8 * 8 < left;
+                cp_async16(dst + g * 512, in ? (MODE == kW4GateUp && g >= 4 ? qb : qa) + g8 * ld8 : p.q0, in);
+            }
         }
-        const int items = (MODE == kW4Down ? rt.n_seg : 1) * KB;
-        const int i0 = static_cast<int>(static_cast<long long>(items) * unit / units);
-        const int i1 = static_cast<int>(static_cast<long long>(items) * (unit + 1) / units);
-
-        auto stage_at = [&](int slot) {
-            uint8_t* b = ring + slot * sbytes;
-            return W4Stage{b + rw * S::kWarpBytes, b + rw * S::kWarpBytes + kW4Rows * 64, b + S::RW * S::kWarpBytes};
-        };
-        // Where the copies are: the next item to post, its ring slot, and this
-        // lane's first piece of its weights (row nw + lane / 4, 16 bytes lane % 4)
-        // and scales.  Rows [nw, nw + 64) of one matrix, or 32 + 32 of two.
-        const size_t ld = static_cast<size_t>(p.K) / 2, ld8 = ld * 8;
-        const int left = p.N - nw;  // rows there are: a multiple of 8
-        int item = i0, slot = 0, seg = MODE == kW4Down && i0 < i1 ? i0 / KB : 0, kb = i0 - seg * KB;
-        const uint8_t *qa, *qb;
-        const bf16* sp;
-        const int sg = lane >> 3, sc = lane & 7;  // this lane's group of the k-block and its 8 rows
-        const int sn8 = MODE == kW4GateUp ? (sc & 3) * 8 : sc * 8;
-        auto seek = [&]() {
-            const int e = MODE == kW4Down ? rt.seg_e[seg] : e0;
-            const size_t at = (static_cast<size_t>(e) * p.N + nw + (lane >> 2)) * ld + static_cast<size_t>(kb) * 64 + (lane & 3) * 16;
-            qa = p.q0 + at;
-            if (MODE == kW4GateUp) qb = p.q1 + at;
-            const bf16* s = (MODE == kW4GateUp && sc >= 4) ? p.s1 : p.s0;
-            sp = s + (static_cast<size_t>(e) * (p.K / G) + kb * (kW4Blk / G) + sg) * p.N + nw + sn8;
-        };
-        if (i0 < i1) seek();
-        // Post the copies of the next item and move on.  Pieces outside the matrices
-        // are filled with zeros.
-        auto post = [&]() {
-            if (item >= i1) return;
-            const W4Stage st = stage_at(slot);
-            const int k0 = kb * kW4Blk;
-            {
-                const int r = lane >> 2, c = lane & 3;
-                const uint32_t dst = smem_addr(st.w) + r * 64 + (swz_w<G>(c, r) << 4);  // row + 8: the same swizzle
-                if (k0 + kW4Blk <= p.K && left >= (MODE == kW4GateUp ? kW4Rows / 2 : kW4Rows)) {
-                    const uint8_t* q = qa;
-#pragma unroll
-                    for (int g = 0; g < 8; ++g, q += ld8) {
-                        if (MODE == kW4GateUp && g == 4) q = qb;
-                        cp_async16(dst + g * 512, q);
-                    }
-                } else {
-                    const bool kin = k0 + c * 32 < p.K;
-#pragma unroll
-                    for (int g = 0; g < 8; ++g) {
-                        const int g8 = MODE == kW4GateUp ? g & 3 : g;
-                        const bool in = kin && g8 * 8 < left;
-                        cp_async16(dst + g * 512, in ? (MODE == kW4GateUp && g >= 4 ? qb : qa) + g8 * ld8 : p.q0, in);
-                    }
-                }
-            }
-            if (sg < kW4Blk / G) {
-                const bool in = k0 + sg * G < p.K && sn8 < left;
-                cp_async16(smem_addr(st.s) + sg * 128 + (sc << 4), in ? sp : p.s0, in);
-            }
-            {   // x rows, shared out among the split's warps
-                const int nc = MODE == kW4Down ? rt.seg_n[seg] : nc0;
-                const int c = lane & 15, kx = k0 + c * 8;
-                const bool kin = kx < p.K;
-                for (int r = (lane >> 4) + 2 * rw; r < nc; r += 2 * S::RW) {
-                    const int row = MODE == kW4Down ? rt.order[rt.seg_r[seg] + r] : x_row[r];
-                    cp_async16(smem_addr(st.x) + r * 256 + (swz_x<G>(c, r) << 4),
-                               kin ? p.x + static_cast<size_t>(row) * p.K + kx : p.x, kin);
-                }
-            }
-            ++item;
+        if (sg < kW4Blk / G) {
+            const bool in = k0 + sg * G < p.K && sn8 < left;
+            cp_async16(smem_addr(st.s) + sg * 128 + (sc << 4), in ? sp : p.s0, in);
+        }
+    };
+    auto post_x = [&](const W4Stage& st, int k0) {  // shared out among the split's warps
+        const int c = lane & 15, kx = k0 + c * 8;
+        const bool kin = kx < p.K;
+        for (int r = (lane >> 4) + 2 * rw; r < nc_p; r += 2 * S::RW) {
+            const int row = MODE == kW4Gemv ? part * p.x_rows + r
+                          : kDown ? rt.order[rt.seg_r[part] + r] : rt.tok[rt.seg_r[part] + r];
+            cp_async16(smem_addr(st.x) + r * 256 + (swz_x<G>(c, r) << 4),
+                       kin ? p.x + static_cast<size_t>(row) * p.K + kx : p.x, kin);
+        }
+    };
+    auto post = [&](bool first) {
+        if (pu < n_units) post_w(stage_at(slot), kb * kW4Blk);
+        if (kDown && first) grid_wait();  // in every CTA: who waits for this kernel counts on it
+        if (pu < n_units) {
+            post_x(stage_at(slot), kb * kW4Blk);
             slot = slot + 1 == kW4Stages ? 0 : slot + 1;
-            ++kb;
-            if (MODE == kW4Down && kb == KB) {
-                kb = 0;
-                ++seg;
-                if (item < i1) seek();
+            if (++pi == i1) {
+                pi = i0;
+                pu = kDown ? n_units : pu + ustep;
+                if (pu < n_units) seek();
+            } else if (kDown && kb + 1 == KB) {
+                seek();
             } else {
+                ++kb;
                 qa += 64;
                 if (MODE == kW4GateUp) qb += 64;
                 sp += static_cast<size_t>(kW4Blk / G) * p.N;
             }
-        };
-        auto meet = [&]() {
-            if (S::RW == 1) __syncwarp();
-            else if (S::KW == 1) __syncthreads();
-            else if (kw == 0) asm volatile("bar.sync 1, 64;" ::: "memory");
-            else asm volatile("bar.sync 2, 64;" ::: "memory");
-        };
-        float acc[4][NT][4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
-#pragma unroll
-        for (int s = 0; s < kW4Stages - 1; ++s) {
-            post();
-            cp_async_commit();
         }
-        int cslot = 0, cseg = MODE == kW4Down && i0 < i1 ? i0 / KB : 0, ckb = i0 - cseg * KB;
+        cp_async_commit();
+    };
+    auto meet = [&]() {
+        if (S::RW == 1) __syncwarp();
+        else if (S::KW == 1) __syncthreads();
+        else if (kw == 0) asm volatile("bar.sync 1, 64;" ::: "memory");
+        else asm volatile("bar.sync 2, 64;" ::: "memory");
+    };
+    post(true);
+#pragma unroll
+    for (int s = 1; s < kW4Stages - 1; ++s) post(false);
+
+    int cslot = 0;
+    for (int u = u0; u < n_units; u += ustep) {
+        float acc[4][NT][4];
+        auto clear = [&]() {
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
+        };
+        clear();
+        int cpart = kDown && i0 < i1 ? i0 / KB : part_of(u), ckb = i0 - cpart * KB;  // ckb: down only
+        int nc = kDown ? (i0 < i1 ? rows_of(cpart) : 0) : rows_of(cpart);
         for (int i = i0; i < i1; ++i) {
             cp_async_wait<kW4Stages - 2>();
             meet();
-            post();
-            cp_async_commit();
-            const int nc = MODE == kW4Down ? rt.seg_n[cseg] : nc0;
+            post(false);
             compute_stage<NT, G>(stage_at(cslot), nc, p.magic, acc);
             cslot = cslot + 1 == kW4Stages ? 0 : cslot + 1;
-            ++ckb;
-            if (MODE == kW4Down && (i + 1 == i1 || ckb == KB)) {
+            if (kDown && (i + 1 == i1 || ++ckb == KB)) {
                 // the segment's rows by token.  If a token holds two rows of one
                 // expert, the quarter-warps (two rows each) take turns.
                 float* mine = sums + static_cast<size_t>(warp) * T * kW4Pad;
@@ -499,9 +597,9 @@ __global__ void __launch_bounds__(kW4Warps * 32) w4_kernel(const W4Args p) {
                             for (int h = 0; h < 2; ++h) {
                                 const int col = j * 8 + 2 * t + h;
                                 if (col < nc) {
-                                    const int o = rt.seg_r[cseg] + col;
+                                    const int o = rt.seg_r[cpart] + col;
                                     const float wt = rt.wt[o];
-                                    float* dst = mine + (rt.order[o] / p.k) * kW4Pad + r;
+                                    float* dst = mine + rt.tok[o] * kW4Pad + r;
 #pragma unroll
                                     for (int m = 0; m < 4; ++m) {
                                         dst[m * 16] += wt * acc[m][j][h];
@@ -512,23 +610,18 @@ __global__ void __launch_bounds__(kW4Warps * 32) w4_kernel(const W4Args p) {
                     }
                     __syncwarp();
                 }
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) acc[m][j][z] = 0.0f;
+                clear();
                 ckb = 0;
-                ++cseg;
+                ++cpart;
+                if (i + 1 < i1) nc = rows_of(cpart);
             }
         }
-        cp_async_wait<0>();
-        __syncthreads();  // the rings are empty
 
-        // sums over the splits, in order, into the first split's tiles: a warp's
-        // tile is [nc][64], the first RW tiles make the CTA's
-        const int nc = MODE == kW4Down ? T : nc0;
-        if (MODE != kW4Down) {
+        // sums over the splits, in order: a warp's tile is [nc][64], the first RW
+        // tiles make the CTA's
+        if (kDown) {
+            nc = T;
+        } else {
             const int r = lane >> 2, t = lane & 3;
 #pragma unroll
             for (int j = 0; j < NT; ++j)
@@ -544,38 +637,44 @@ __global__ void __launch_bounds__(kW4Warps * 32) w4_kernel(const W4Args p) {
                         }
                     }
                 }
-            __syncthreads();
         }
-        if (S::KW > 1) {
-            for (int o = threadIdx.x; o < S::RW * nc * kW4Rows; o += blockDim.x) {
-                const int at = (o >> 6) * kW4Pad + (o & 63);
-                float v = sums[at];
+        __syncthreads();
+        if (csize > 1) {
+            if (S::KW > 1) {
+                for (int o = threadIdx.x; o < S::RW * nc * kW4Rows; o += blockDim.x) {
+                    const int at = (o >> 6) * kW4Pad + (o & 63);
+                    float v = sums[at];
 #pragma unroll
-                for (int w = 1; w < S::KW; ++w) v += sums[w * S::RW * nc * kW4Pad + at];
-                sums[at] = v;
+                    for (int w = 1; w < S::KW; ++w) v += sums[w * S::RW * nc * kW4Pad + at];
+                    sums[at] = v;
+                }
             }
+            cluster_sync();
         }
-        // sums over the cluster's CTAs, in order; each CTA stores its share
-        if (csize > 1) cluster_sync();
-        else __syncthreads();
+        // then over the cluster's CTAs, in order; each CTA stores its share
         const uint32_t sums_u = smem_addr(sums);
+        const int n0 = tile_of(u) * S::kOut;
         for (int o = crank * blockDim.x + threadIdx.x; o < nc * S::kOut; o += csize * blockDim.x) {
             const int col = o / S::kOut, row = o % S::kOut;
             const int n = n0 + row;
             auto total = [&](int g, int rr) {  // row rr of row group g's tile
                 const int at = (g * nc + col) * kW4Pad + rr;
-                if (csize == 1) return sums[at];
                 float v = 0.0f;
-                for (int c = 0; c < csize; ++c) v += ld_cluster_f32(sums_u + at * 4, c);
+                if (csize == 1) {
+#pragma unroll
+                    for (int w = 0; w < S::KW; ++w) v += sums[w * S::RW * nc * kW4Pad + at];
+                } else {
+                    for (int c = 0; c < csize; ++c) v += ld_cluster_f32(sums_u + at * 4, c);
+                }
                 return v;
             };
             if (n < p.N) {
                 if (MODE == kW4GateUp) {
-                    const float g = total(row >> 5, row & 31), u = total(row >> 5, (row & 31) + 32);
-                    const float h = g / (1.0f + expf(-g)) * u;
-                    p.out[static_cast<size_t>(out_row[col]) * p.N + n] = __float2bfloat16_rn(h);
+                    const float g = total(row >> 5, row & 31), up = total(row >> 5, (row & 31) + 32);
+                    const float h = g / (1.0f + expf(-g)) * up;
+                    p.out[static_cast<size_t>(rt.order[rt.seg_r[cpart] + col]) * p.N + n] = __float2bfloat16_rn(h);
                 } else {
-                    const int m = MODE == kW4Gemv ? pass * p.x_rows + col : col;
+                    const int m = MODE == kW4Gemv ? cpart * p.x_rows + col : col;
                     p.out[static_cast<size_t>(m) * p.N + n] = __float2bfloat16_rn(total(row >> 6, row & 63));
                 }
             }
@@ -615,6 +714,7 @@ template <int G>
 __global__ void __launch_bounds__(kConvRows * 32) w4_quantize_kernel(const W4ConvArgs p) {
     __shared__ __align__(16) __nv_bfloat16 sc[kConvK / G][kConvRows];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    grid_begin();
     const size_t row0 = static_cast<size_t>(blockIdx.x) * kConvRows, row = row0 + warp;
     const int k0 = blockIdx.y * p.chunk, kn = min(p.chunk, p.K - k0);
     constexpr int lanes = G / 8;
@@ -690,6 +790,7 @@ template <int G>
 __global__ void __launch_bounds__(kConvRows * 32) w4_dequantize_kernel(const W4ConvArgs p) {
     __shared__ __align__(16) __nv_bfloat16 sc[kConvK / G][kConvRows];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    grid_begin();
     const size_t row0 = static_cast<size_t>(blockIdx.x) * kConvRows, row = row0 + warp;
     const int k0 = blockIdx.y * p.chunk, kn = min(p.chunk, p.K - k0);
     constexpr int lanes = G / 8;
@@ -737,58 +838,47 @@ bool w4_shape_ok(int N, int K, int group, std::string* why) {
     return true;
 }
 
-// CTAs that share a tile's inputs: as many as fit the GPU at once (`slots` CTAs)
-// while every split keeps two k-blocks.
-int w4_cluster(long long ctas, long long blocks, int splits, long long slots) {
-    long long c = slots / ctas;
-    c = c < blocks / (2 * splits) ? c : blocks / (2 * splits);
-    return static_cast<int>(c < 1 ? 1 : c > kW4ClusterMax ? kW4ClusterMax : c);
+// CTAs that share a unit's inputs: 8, 4 or 2 while they fit the GPU at once
+// (`fit` CTAs; clusters leave some places unused) and every split keeps two
+// k-blocks.  Powers of two only: 64 units of 7 took 18 us where 64 of 4 or 8
+// took 12 to 13, 32 of 5 26 us where 32 of 8 took 16 (some wait for a second
+// round).
+int w4_cluster(long long units, long long blocks, int splits, long long fit) {
+    for (int c = kW4ClusterMax; c > 1; c /= 2)
+        if (units * c <= (c == 8 ? fit * 85 / 100 : c == 4 ? fit * 90 / 100 : fit) && blocks >= 2ll * splits * c) return c;
+    return 1;
 }
 
 // `rows` tokens at most; x_rows <= 8 NT of them (or of an expert's rows) a pass.
 template <int MODE, int NT, int G>
 int w4_launch(W4Args a, int rows, int x_rows, int dev, int sms, void* stream) {
     using S = W4Shape<MODE, NT, G>;
-    constexpr int kSmemMost = kSmemLimit - 1024;  // the row list is static
     a.x_rows = x_rows;
+    a.sum_rows = MODE == kW4Down ? rows : x_rows;
     a.magic = 0x43004300u;
-    const int rings = S::ring_bytes(x_rows);
-    const int sum_rows = MODE == kW4Down ? rows : x_rows;
-    const int sums = (kW4Warps * sum_rows * kW4Pad * 4 + 127) / 128 * 128;
-    const int routing = MODE == kW4Gemv ? 0 : static_cast<int>((sizeof(W4Routing) + 127) / 128 * 128);
-    int smem = routing > rings ? routing : rings;
-    smem = smem > sums ? smem : sums;
-    if (MODE == kW4Down) smem = routing + sums + rings;
-    if (smem > kSmemMost) return api_fail(ET_ERR_UNSUPPORTED, "rows do not fit in shared memory");
+    // segments of a call: each has a row, an expert has one and one more for each full pass
+    const int R = rows * a.k, experts = R < a.E ? R : a.E;
+    const int segs = experts + R / x_rows < R ? experts + R / x_rows : R;
+    const long long tiles = (a.N + S::kOut - 1) / S::kOut;
+    const long long units = tiles * (MODE == kW4Down ? 1 : MODE == kW4GateUp ? segs : (rows + x_rows - 1) / x_rows);
+    const long long blocks = static_cast<long long>((a.K + kW4Blk - 1) / kW4Blk) * (MODE == kW4Down ? segs : 1);
+    const int routing = MODE == kW4Gemv ? 0 : W4Routing::bytes(a.T_max * a.k, a.E);
+    const int smem = S::ring_bytes(x_rows) + kW4Warps * a.sum_rows * kW4Pad * 4 + routing;
+    if (smem > kSmemLimit) return api_fail(ET_ERR_UNSUPPORTED, "rows do not fit in shared memory");
     static SmemOptIn opt;
-    cudaError_t e = api_smem_opt_in(opt, dev, w4_kernel<MODE, NT, G>, kSmemMost);
+    cudaError_t e = api_smem_opt_in(opt, dev, w4_kernel<MODE, NT, G>, kSmemLimit);
     if (e != cudaSuccess) return api_fail_cuda(e, "cudaFuncSetAttribute(4-bit products)");
     static const int regs = [] {
         cudaFuncAttributes at{};
         return cudaFuncGetAttributes(&at, w4_kernel<MODE, NT, G>) == cudaSuccess ? at.numRegs : 255;
     }();
-    const int by_smem = kSmemSm / (smem + 1280), by_regs = 65536 / (kW4Warps * 32 * ((regs + 7) / 8 * 8));
-    const int occ = by_smem < by_regs ? by_smem : by_regs;  // CTAs an SM
-    // segments of a call: each has a row, an expert has one and one more for each full pass
-    const int R = rows * a.k, experts = R < a.E ? R : a.E;
-    const int slots = MODE == kW4Gemv ? 1 : (experts + R / x_rows < R ? experts + R / x_rows : R);
-    const int tiles = (a.N + S::kOut - 1) / S::kOut;
-    const long long blocks = static_cast<long long>((a.K + kW4Blk - 1) / kW4Blk) * (MODE == kW4Down ? slots : 1);
-    const int c = w4_cluster(static_cast<long long>(tiles) * (MODE == kW4GateUp ? slots : 1), blocks, S::KW,
-                             static_cast<long long>(sms) * occ);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(tiles * c, MODE == kW4GateUp ? slots : 1);
-    cfg.blockDim = dim3(kW4Warps * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = c;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, w4_kernel<MODE, NT, G>, a);
+    const int threads = kW4Warps * 32;
+    const int by_smem = kSmemSm / (smem + 1024), by_regs = 65536 / (threads * ((regs + 7) / 8 * 8));
+    const long long fit = static_cast<long long>(sms) * (by_smem < by_regs ? by_smem : by_regs);  // CTAs at once
+    const int c = w4_cluster(units, blocks, S::KW, fit);
+    const long long grid = MODE != kW4Down && c == 1 && units > fit ? fit : units * c;
+    e = api_launch_cluster(w4_kernel<MODE, NT, G>, dim3(static_cast<unsigned>(grid)), threads, c,
+                           MODE == kW4Down, smem, stream, a);
     if (e != cudaSuccess) return api_fail_cuda(e, "launch of the 4-bit product kernel");
     return ET_OK;
 }
