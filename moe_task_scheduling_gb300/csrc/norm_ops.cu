@@ -551,7 +551,8 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) norm_bwd_staged_kernel(const
 
 struct NormSumArgs {
     const float* part;
-    float* out[3];  // d_gamma_post, d_gamma_pre, d_gate; null: not wanted
+    float* out[3];  // the wanted ones of d_gamma_post, d_gamma_pre, d_gate
+    int arr[3];     // which
     int H, parts;
     const int32_t* d_T;
     int T_max;
@@ -564,14 +565,14 @@ __global__ void __launch_bounds__(1024) norm_sum_kernel(const NormSumArgs p) {
     grid_begin();
     if (p.d_T && (*p.d_T < 0 || *p.d_T > p.T_max)) return;
     float* out = p.out[blockIdx.y];
-    if (!out) return;
+    const int arr = p.arr[blockIdx.y];
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float s = 0.0f;
     if (c < p.H)
 #pragma unroll 10
         for (int g = grp; g < p.parts; g += 32)
-            s += __ldcg(p.part + (static_cast<size_t>(g) * 3 + blockIdx.y) * p.H + c);
+            s += __ldcg(p.part + (static_cast<size_t>(g) * 3 + arr) * p.H + c);
     red[grp][lane] = s;
     __syncthreads();
     s = warp_sum(red[lane][grp]);  // warp grp: its column's 32 groups
@@ -790,9 +791,16 @@ int et_block_norm_bwd(const void* x, const void* y, const void* gamma_post, cons
             if (e != cudaSuccess) return api_fail_cuda(e, "launch of the block norm's backward kernel");
         }
         float* d_gate_channel = gate_kind == kGateChannel ? static_cast<float*>(d_gate) : nullptr;
-        if (d_gamma_post || d_gamma_pre || d_gate_channel) {
-            const NormSumArgs s{a.part, {d_gamma_post, d_gamma_pre, d_gate_channel}, H, parts, d_T, T_max};
-            const cudaError_t e = api_launch(norm_sum_kernel, dim3((H + 31) / 32, 3), 1024, 0, stream, s);
+        NormSumArgs s{a.part, {}, {}, H, parts, d_T, T_max};
+        float* wanted[3] = {d_gamma_post, d_gamma_pre, d_gate_channel};
+        int n = 0;
+        for (int i = 0; i < 3; ++i)
+            if (wanted[i]) {
+                s.out[n] = wanted[i];
+                s.arr[n++] = i;
+            }
+        if (n) {
+            const cudaError_t e = api_launch(norm_sum_kernel, dim3((H + 31) / 32, n), 1024, 0, stream, s);
             if (e != cudaSuccess) return api_fail_cuda(e, "launch of the block norm's parameter sums");
         }
         return ET_OK;

@@ -17,7 +17,8 @@ namespace {
 constexpr int kW4Rows = 64;        // weight rows of a warp (gate/up: 32 of each)
 constexpr int kW4Blk = 128;        // inputs of a stage: 64 bytes of a row
 constexpr int kW4Warps = 4;
-constexpr int kW4Stages = 2;
+constexpr int kW4Stages = 2;       // k-blocks of a ring: three or four gained nothing (the unpacking, not
+                                   // the memory, sets the pace) and took room from other CTAs
 constexpr int kW4RowsMax = 64;     // most rows of x (tokens)
 constexpr int kW4KMax = 8;         // experts of a token
 constexpr int kW4EMax = 256;
@@ -428,12 +429,11 @@ __global__ void __launch_bounds__(kW4Warps * 32) w4_kernel(const W4Args p) {
     const int KB = (p.K + kW4Blk - 1) / kW4Blk;
     const int tiles = (p.N + S::kOut - 1) / S::kOut;
     // The down kernel is scheduled while the gate/up kernel of its call drains.  That
-    // one has started after everything before it, so only h is not there yet, and
+    // one has waited for everything before it, so only h is not there yet, and
     // waited for below: routing and the first weights come in meanwhile (T = 1,
-    // fine-grained: 17.1 -> 14.6 us).  The others start when the stream is free:
-    // early starts spread their CTAs unevenly over the SMs (M = 16, 4096 x 14336:
-    // 16.4 -> 19.9 us).
-    if (MODE == kW4GateUp) grid_release();
+    // fine-grained: 17.1 -> 14.6 us).
+    if (!kDown) grid_wait();
+    grid_release();
     bool ok;
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
     if (!ok) {  // the same for every CTA of the cluster
@@ -838,15 +838,33 @@ bool w4_shape_ok(int N, int K, int group, std::string* why) {
     return true;
 }
 
-// CTAs that share a unit's inputs: 8, 4 or 2 while they fit the GPU at once
-// (`fit` CTAs; clusters leave some places unused) and every split keeps two
-// k-blocks.  Powers of two only: 64 units of 7 took 18 us where 64 of 4 or 8
-// took 12 to 13, 32 of 5 26 us where 32 of 8 took 16 (some wait for a second
-// round).
-int w4_cluster(long long units, long long blocks, int splits, long long fit) {
-    for (int c = kW4ClusterMax; c > 1; c /= 2)
-        if (units * c <= (c == 8 ? fit * 85 / 100 : c == 4 ? fit * 90 / 100 : fit) && blocks >= 2ll * splits * c) return c;
-    return 1;
+// How many clusters of c CTAs of a kernel fit the GPU at once when n of its CTAs
+// fit an SM (a cluster lies within one of the GPU's processor clusters, so some
+// places stay empty).  Asked for once and kept: it depends on nothing else.
+struct W4Fit {
+    int clusters[4][33] = {};  // [log2 c][n], 0: not asked yet
+};
+template <class K>
+int w4_fit(W4Fit& f, K kernel, int c, int n) {
+    const int lc = c == 8 ? 3 : c == 4 ? 2 : c == 2 ? 1 : 0;
+    n = n < 1 ? 1 : n > 32 ? 32 : n;
+    int v = __atomic_load_n(&f.clusters[lc][n], __ATOMIC_RELAXED);
+    if (v) return v;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(c * 1024);
+    cfg.blockDim = dim3(kW4Warps * 32);
+    const int smem = kSmemSm / n / 128 * 128 - 1024;
+    cfg.dynamicSmemBytes = smem < kSmemLimit ? smem : kSmemLimit;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = c;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&v, kernel, &cfg) != cudaSuccess || v < 1) v = 1;
+    __atomic_store_n(&f.clusters[lc][n], v, __ATOMIC_RELAXED);
+    return v;
 }
 
 // `rows` tokens at most; x_rows <= 8 NT of them (or of an expert's rows) a pass.
@@ -863,7 +881,7 @@ int w4_launch(W4Args a, int rows, int x_rows, int dev, int sms, void* stream) {
     const long long units = tiles * (MODE == kW4Down ? 1 : MODE == kW4GateUp ? segs : (rows + x_rows - 1) / x_rows);
     const long long blocks = static_cast<long long>((a.K + kW4Blk - 1) / kW4Blk) * (MODE == kW4Down ? segs : 1);
     const int routing = MODE == kW4Gemv ? 0 : W4Routing::bytes(a.T_max * a.k, a.E);
-    const int smem = S::ring_bytes(x_rows) + kW4Warps * a.sum_rows * kW4Pad * 4 + routing;
+    int smem = S::ring_bytes(x_rows) + kW4Warps * a.sum_rows * kW4Pad * 4 + routing;
     if (smem > kSmemLimit) return api_fail(ET_ERR_UNSUPPORTED, "rows do not fit in shared memory");
     static SmemOptIn opt;
     cudaError_t e = api_smem_opt_in(opt, dev, w4_kernel<MODE, NT, G>, kSmemLimit);
@@ -874,11 +892,30 @@ int w4_launch(W4Args a, int rows, int x_rows, int dev, int sms, void* stream) {
     }();
     const int threads = kW4Warps * 32;
     const int by_smem = kSmemSm / (smem + 1024), by_regs = 65536 / (threads * ((regs + 7) / 8 * 8));
-    const long long fit = static_cast<long long>(sms) * (by_smem < by_regs ? by_smem : by_regs);  // CTAs at once
-    const int c = w4_cluster(units, blocks, S::KW, fit);
-    const long long grid = MODE != kW4Down && c == 1 && units > fit ? fit : units * c;
-    e = api_launch_cluster(w4_kernel<MODE, NT, G>, dim3(static_cast<unsigned>(grid)), threads, c,
-                           MODE == kW4Down, smem, stream, a);
+    const int per_sm = by_smem < by_regs ? by_smem : by_regs;  // CTAs an SM
+    static W4Fit fits;
+    // CTAs that share a unit's inputs: 8, 4 or 2 if all of them fit at once and every
+    // split keeps two k-blocks
+    int c = kW4ClusterMax;
+    while (c > 1 && (blocks < 2ll * S::KW * c || units > w4_fit(fits, w4_kernel<MODE, NT, G>, c, per_sm))) c /= 2;
+    const long long fit = static_cast<long long>(sms) * per_sm;
+    const bool in_turn = MODE != kW4Down && c == 1 && units > fit;  // CTAs take several units
+    const long long grid = in_turn ? fit : units * c;
+    // Scheduled while the kernel before drains, which hides the launch (eager calls,
+    // M = 1, 4096 x 14336: 14.5 -> 12.5 us).  Its CTAs then fill the places the other
+    // kernel leaves, so no more of them may fit an SM than an even spread needs:
+    // without that limit M = 16 took 20.4 us, with it 16.3 (18.6 when launched after
+    // the other).  CTAs that take units in turn are launched after the other: they
+    // fill the GPU, and started early they lost 1 to 5 % (Mixtral-shaped, T = 4).
+    const bool early = !in_turn;
+    if (early) {
+        int n = static_cast<int>((grid + sms - 1) / sms);
+        while (n < per_sm && w4_fit(fits, w4_kernel<MODE, NT, G>, c, n) * static_cast<long long>(c) < grid) ++n;
+        const int more = kSmemSm / (n + 1) / 128 * 128 - 1024 + 128;  // n + 1 do not fit
+        smem = smem > more ? smem : more < kSmemLimit ? more : kSmemLimit;
+    }
+    e = api_launch_cluster(w4_kernel<MODE, NT, G>, dim3(static_cast<unsigned>(grid)), threads, c, early,
+                           smem, stream, a);
     if (e != cudaSuccess) return api_fail_cuda(e, "launch of the 4-bit product kernel");
     return ET_OK;
 }

@@ -8,6 +8,7 @@ there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -375,15 +376,16 @@ def _count_arg(d_n, dev):
 
 
 # The current stream's handle without building a Stream object (3 us of a call
-# that takes 6), where this torch has it.
+# that takes 8), and the current device, where this torch has them.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(fn, dev, stream, args, check):
     """fn(*args, stream) with device `dev` current."""
     st = _raw_stream(dev) if stream is None else _stream(stream)
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         rc = fn(*args, st)
     else:
         with torch.cuda.device(dev):
@@ -393,6 +395,7 @@ def _call(fn, dev, stream, args, check):
     return rc
 
 
+@functools.lru_cache(maxsize=None)
 def et_router_topk_workspace_bytes(T_max, E, k) -> int:
     return load().et_router_topk_workspace_bytes(T_max, E, k)
 
@@ -428,6 +431,7 @@ def et_router_topk_bwd(logits, topk_idx, topk_w, expert_counts, n_routed, d_logi
         T_max if T is None else T, _count_arg(d_T, dev), T_max, E, k, ws, wsb), check)
 
 
+@functools.lru_cache(maxsize=None)
 def et_block_norm_workspace_bytes(T_max, H) -> int:
     return load().et_block_norm_workspace_bytes(T_max, H)
 
@@ -509,6 +513,7 @@ def et_w4_dequantize(q, scale, w, *, stream=None, check=True):
     return _call(load().et_w4_dequantize, dev, stream, (pq, ps, pw, *dims), check)
 
 
+@functools.lru_cache(maxsize=None)
 def et_w4_gemv_workspace_bytes(M_max, N, K, group) -> int:
     return load().et_w4_gemv_workspace_bytes(M_max, N, K, group)
 
@@ -525,6 +530,7 @@ def et_w4_gemv(X, q, scale, Y, *, M=None, d_M=None, workspace, stream=None, chec
         M_max if M is None else M, _count_arg(d_M, dev), M_max, N, K, group, ws, wsb), check)
 
 
+@functools.lru_cache(maxsize=None)
 def et_w4_experts_workspace_bytes(T_max, H, F, E, k, group) -> int:
     return load().et_w4_experts_workspace_bytes(T_max, H, F, E, k, group)
 
