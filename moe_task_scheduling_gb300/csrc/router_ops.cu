@@ -394,6 +394,7 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(const RouterBwdArgs p) 
                 for (int i = 0; i < EPL; ++i) d[i] = add[lane + 32 * i];
                 __syncwarp();
                 if (sel) add[c.e] = 0.0f;
+                __syncwarp();
             } else {
 #pragma unroll
                 for (int i = 0; i < EPL; ++i) d[i] = 0.0f;

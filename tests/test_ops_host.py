@@ -124,6 +124,27 @@ def test_binding_refuses_wrong_tensors(lib):
             E._w4(q, s, "q", (4,), 64, 64, 0)
 
 
+def test_call_runs_on_the_tensors_device(monkeypatch):
+    """Tensors on a device that is not current: it is made current around the call, its stream is used."""
+    import contextlib
+    seen = []
+
+    @contextlib.contextmanager
+    def device(dev):
+        seen.append(("enter", dev))
+        yield
+        seen.append(("exit", dev))
+    monkeypatch.setattr(E, "_current_device", lambda: 0)
+    monkeypatch.setattr(E, "_raw_stream", lambda dev: 100 + dev)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    assert E._call(lambda *a: seen.append(a) or 0, 1, None, (7,), True) == 0
+    assert seen == [("enter", 1), (7, 101), ("exit", 1)]
+    seen.clear()
+    assert E._call(lambda *a: seen.append(a) or 0, 0, 55, (7,), True) == 0
+    assert seen == [(7, 55)]
+    assert E._call(lambda *a: E.ET_ERR_CUDA, 0, 55, (), False) == E.ET_ERR_CUDA
+
+
 # ------------------------------------------------------------------ the 64-bit references
 
 def _differences(f, x, g, h=1e-6):
