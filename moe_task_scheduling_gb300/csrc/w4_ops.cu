@@ -469,75 +469,93 @@ __global__ void __launch_bounds__(kW4Warps * 32) w4_kernel(const W4Args p) {
         return MODE == kW4Gemv ? min(p.x_rows, T - part * p.x_rows) : static_cast<int>(rt.seg_n[part]);
     };
 
+    // A stage of the ring: [RW warps: 64 rows of 64 bytes of weights, 128 / group rows
+    // of 64 scales][x rows of 256 bytes].
     auto stage_at = [&](int slot) {
         uint8_t* b = ring + slot * sbytes;
         return W4Stage{b + rw * S::kWarpBytes, b + rw * S::kWarpBytes + kW4Rows * 64, b + S::RW * S::kWarpBytes};
     };
-    // Where the copies are: the next item, its ring slot, and this lane's first piece
-    // of its weights (row nw + lane / 4, 16 bytes lane % 4) and scales.  A warp's rows
-    // are [nw, nw + 64) of one matrix, or 32 + 32 of two.
-    const size_t ld = static_cast<size_t>(p.K) / 2, ld8 = ld * 8;
-    const int sg = lane >> 3, sc = lane & 7;  // this lane's group of the k-block and its 8 rows
+    // Where the copies are: the next item, its ring slot, and what this lane copies --
+    // of the weights the row lane / 4 of each 8, piece lane % 4 of its 64 bytes; of
+    // the scales 8 rows of one group; of x the rows lane / 16 + 2 rw of each 2 RW,
+    // piece lane % 16.  A warp's rows are [nw, nw + 64) of one matrix, or 32 + 32 of two.
+    constexpr int kRowsW = MODE == kW4GateUp ? kW4Rows / 2 : kW4Rows;
+    constexpr int kXMost = NT * 8 / (2 * S::RW);  // x rows of a lane
+    const size_t ld8 = static_cast<size_t>(p.K) * 4;  // bytes of 8 rows
+    const int wr = lane >> 2, wc = lane & 3, sg = lane >> 3, sc = lane & 7, xc = lane & 15;
     const int sn8 = MODE == kW4GateUp ? (sc & 3) * 8 : sc * 8;
-    int pu = i0 < i1 ? u0 : n_units, pi = i0, slot = 0, part = 0, kb = 0, left = 0, nc_p = 0;
+    const uint32_t ring_u = smem_addr(ring);
+    const uint32_t w_to = ring_u + rw * S::kWarpBytes + wr * 64 + (swz_w<G>(wc, wr) << 4);  // row + 8: the same swizzle
+    const uint32_t s_to = ring_u + rw * S::kWarpBytes + kW4Rows * 64 + sg * 128 + (sc << 4);
+    const uint32_t x_to = ring_u + S::RW * S::kWarpBytes;
+    int pu = i0 < i1 ? u0 : n_units, pi = i0, kb = 0, left = 0, nc_p = 0;
+    uint32_t slot_off = 0;
+    const uint32_t ring_len = kW4Stages * sbytes;
     const uint8_t *qa, *qb;
-    const bf16* sp;
+    const bf16 *sp, *xp[kXMost];
     auto seek = [&]() {  // to item pi of unit pu
-        part = kDown ? pi / KB : part_of(pu);
+        const int part = kDown ? pi / KB : part_of(pu);
         kb = kDown ? pi - part * KB : pi;
         nc_p = rows_of(part);
         const int e = MODE == kW4Gemv ? 0 : rt.seg_e[part];
-        const int nw = tile_of(pu) * S::kOut + rw * (MODE == kW4GateUp ? kW4Rows / 2 : kW4Rows);
+        const int nw = tile_of(pu) * S::kOut + rw * kRowsW;
         left = p.N - nw;  // rows there are: a multiple of 8
-        const size_t at = (static_cast<size_t>(e) * p.N + nw + (lane >> 2)) * ld + static_cast<size_t>(kb) * 64 + (lane & 3) * 16;
+        const size_t at = ((static_cast<size_t>(e) * p.N + nw + wr) * p.K >> 1) + kb * 64 + wc * 16;
         qa = p.q0 + at;
         if (MODE == kW4GateUp) qb = p.q1 + at;
         const bf16* s = (MODE == kW4GateUp && sc >= 4) ? p.s1 : p.s0;
         sp = s + (static_cast<size_t>(e) * (p.K / G) + kb * (kW4Blk / G) + sg) * p.N + nw + sn8;
+#pragma unroll
+        for (int i = 0; i < kXMost; ++i) {
+            const int r = (lane >> 4) + 2 * rw + i * 2 * S::RW;
+            int row = 0;
+            if (r < nc_p)
+                row = MODE == kW4Gemv ? part * p.x_rows + r : kDown ? rt.order[rt.seg_r[part] + r] : rt.tok[rt.seg_r[part] + r];
+            xp[i] = p.x + static_cast<size_t>(row) * p.K + kb * kW4Blk + xc * 8;
+        }
     };
     if (pu < n_units) seek();
     // Post the copies of the next item and move on.  Pieces outside the matrices are
     // filled with zeros.
-    auto post_w = [&](const W4Stage& st, int k0) {
-        const int r = lane >> 2, c = lane & 3;
-        const uint32_t dst = smem_addr(st.w) + r * 64 + (swz_w<G>(c, r) << 4);  // row + 8: the same swizzle
-        if (k0 + kW4Blk <= p.K && left >= (MODE == kW4GateUp ? kW4Rows / 2 : kW4Rows)) {
+    auto post_w = [&]() {
+        const uint32_t dst = w_to + slot_off;
+        const int left_k = p.K - kb * kW4Blk;
+        if (left_k >= kW4Blk && left >= kRowsW) {
             const uint8_t* q = qa;
 #pragma unroll
             for (int g = 0; g < 8; ++g, q += ld8) {
                 if (MODE == kW4GateUp && g == 4) q = qb;
                 cp_async16(dst + g * 512, q);
             }
+            if (sg < kW4Blk / G) cp_async16(s_to + slot_off, sp);
         } else {
-            const bool kin = k0 + c * 32 < p.K;
+            const bool kin = wc * 32 < left_k;
 #pragma unroll
             for (int g = 0; g < 8; ++g) {
                 const int g8 = MODE == kW4GateUp ? g & 3 : g;
                 const bool in = kin && g8 * 8 < left;
                 cp_async16(dst + g * 512, in ? (MODE == kW4GateUp && g >= 4 ? qb : qa) + g8 * ld8 : p.q0, in);
             }
-        }
-        if (sg < kW4Blk / G) {
-            const bool in = k0 + sg * G < p.K && sn8 < left;
-            cp_async16(smem_addr(st.s) + sg * 128 + (sc << 4), in ? sp : p.s0, in);
+            if (sg < kW4Blk / G) {
+                const bool in = sg * G < left_k && sn8 < left;
+                cp_async16(s_to + slot_off, in ? sp : p.s0, in);
+            }
         }
     };
-    auto post_x = [&](const W4Stage& st, int k0) {  // shared out among the split's warps
-        const int c = lane & 15, kx = k0 + c * 8;
-        const bool kin = kx < p.K;
-        for (int r = (lane >> 4) + 2 * rw; r < nc_p; r += 2 * S::RW) {
-            const int row = MODE == kW4Gemv ? part * p.x_rows + r
-                          : kDown ? rt.order[rt.seg_r[part] + r] : rt.tok[rt.seg_r[part] + r];
-            cp_async16(smem_addr(st.x) + r * 256 + (swz_x<G>(c, r) << 4),
-                       kin ? p.x + static_cast<size_t>(row) * p.K + kx : p.x, kin);
+    auto post_x = [&]() {  // shared out among the split's warps
+        const bool kin = kb * kW4Blk + xc * 8 < p.K;
+#pragma unroll
+        for (int i = 0; i < kXMost; ++i) {
+            const int r = (lane >> 4) + 2 * rw + i * 2 * S::RW;
+            if (r < nc_p) cp_async16(x_to + slot_off + r * 256 + (swz_x<G>(xc, r) << 4), kin ? xp[i] : p.x, kin);
         }
     };
     auto post = [&](bool first) {
-        if (pu < n_units) post_w(stage_at(slot), kb * kW4Blk);
+        if (pu < n_units) post_w();
         if (kDown && first) grid_wait();  // in every CTA: who waits for this kernel counts on it
         if (pu < n_units) {
-            post_x(stage_at(slot), kb * kW4Blk);
-            slot = slot + 1 == kW4Stages ? 0 : slot + 1;
+            post_x();
+            slot_off = slot_off + sbytes == ring_len ? 0 : slot_off + sbytes;
             if (++pi == i1) {
                 pi = i0;
                 pu = kDown ? n_units : pu + ustep;
@@ -549,6 +567,8 @@ __global__ void __launch_bounds__(kW4Warps * 32) w4_kernel(const W4Args p) {
                 qa += 64;
                 if (MODE == kW4GateUp) qb += 64;
                 sp += static_cast<size_t>(kW4Blk / G) * p.N;
+#pragma unroll
+                for (int i = 0; i < kXMost; ++i) xp[i] += kW4Blk;
             }
         }
         cp_async_commit();
