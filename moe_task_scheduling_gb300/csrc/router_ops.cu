@@ -31,12 +31,12 @@ struct RouterArgs {
     int32_t* part_n;         // [kRouterParts]
 };
 
-// Order-preserving key of a logit: -0.0 ties with +0.0, NaN ranks above all
-// (it then shows in the weights and losses).  Every key is > 0.
+// Order-preserving key of a logit.  Adding +0 makes -0.0 tie with +0.0 and gives
+// every NaN the one positive NaN, which ranks above all (it then shows in the
+// weights and losses).  Every key is > 0.
 __device__ __forceinline__ uint32_t logit_key(float v) {
-    if (v != v) return 0xffffffffu;
-    const uint32_t b = __float_as_uint(v == 0.0f ? 0.0f : v);
-    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+    const int b = __float_as_int(__fadd_rn(v, 0.0f));
+    return static_cast<uint32_t>(b ^ ((b >> 31) | static_cast<int>(0x80000000u)));
 }
 
 // The logit of a key (+0.0 for both zeros, a NaN for any NaN).
