@@ -25,6 +25,7 @@ struct NormArgs {
     const bf16* gamma_pre;   // [H] or null
     float scale, eps, inv_H;
     int gate_kind;
+    int row_threads;         // threads of a row
     const int32_t* d_T;
     int T_host, T_max, H;
     EtHeader* hdr;
@@ -37,6 +38,7 @@ struct NormArgs {
     bf16* dy;
     bf16* d_gate_full;       // [T, H]
     float* d_gate_token;     // [T]
+    int part_of;             // which parameter gradients are wanted (bit 0 post, 1 pre, 2 gate)
     float* part;             // [kNormParts][3][H]: d_gamma_post, d_gamma_pre, d_gate per channel
 };
 
@@ -48,12 +50,55 @@ struct Vec8 {
     }
 };
 
-// Columns [c, c + 8) of a row of H.  VEC: one 16-byte access (H a multiple of 8
-// and the tensors 16-byte aligned); else element by element, for any H.
-template <bool VEC>
-__device__ __forceinline__ Vec8 load8(const bf16* row, int c, int H) {
+// The threads of a row, and how its columns fall to them.  A CTA holds one row, or
+// several with a group of threads (a multiple of a warp) each.  A thread has
+// sixteen columns in two vectors of eight.  VEC (H a multiple of 8, tensors
+// 16-byte aligned): eight neighbours, one 16-byte access; else columns a group
+// apart, so that neighbouring threads still read neighbouring elements.
+enum RowMode { kRowsWarp = 0, kRowsGroup = 1, kRowsOne = 2 };  // a row a warp (eight columns a thread
+                                                               // are enough), a group, a CTA
+template <int MODE>
+struct RowGroup {
+    int threads, group;  // kRowsGroup only
+
+    __device__ __forceinline__ explicit RowGroup(int row_threads) {
+        if (MODE == kRowsGroup) {
+            threads = row_threads;
+            group = threadIdx.x / row_threads;
+        }
+    }
+    __device__ __forceinline__ int th() const {  // threads of a row
+        return MODE == kRowsWarp ? 32 : MODE == kRowsOne ? static_cast<int>(blockDim.x) : threads;
+    }
+    __device__ __forceinline__ int groups() const {  // rows of the CTA
+        return MODE == kRowsOne ? 1 : MODE == kRowsWarp ? static_cast<int>(blockDim.x >> 5) : static_cast<int>(blockDim.x) / threads;
+    }
+    __device__ __forceinline__ int id() const {  // this thread's row of the CTA,
+        return MODE == kRowsOne ? 0 : MODE == kRowsWarp ? static_cast<int>(threadIdx.x >> 5) : group;
+    }
+    __device__ __forceinline__ int lane() const {  // and its place in it
+        return MODE == kRowsOne ? static_cast<int>(threadIdx.x)
+             : MODE == kRowsWarp ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x) - group * threads;
+    }
+    template <bool VEC>
+    __device__ __forceinline__ int col(int j, int i) const {
+        return VEC ? (j * th() + lane()) * 8 + i : (j * 8 + i) * th() + lane();
+    }
+    __device__ __forceinline__ void sync() const {
+        if (MODE == kRowsOne) __syncthreads();
+        else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(threads) : "memory");
+    }
+};
+
+constexpr int kNormCtaThreads = 256;  // of a CTA that holds several rows
+__host__ __device__ constexpr int norm_v(int mode) { return mode == kRowsWarp ? 1 : 2; }  // vectors of a thread
+
+// This thread's vector j of a row of H columns; zeros past its end.
+template <bool VEC, int MODE>
+__device__ __forceinline__ Vec8 load8(const bf16* row, const RowGroup<MODE>& g, int j, int H) {
     Vec8 v{};
     if (VEC) {
+        const int c = g.template col<VEC>(j, 0);
         if (c < H) {
             const uint4 q = *reinterpret_cast<const uint4*>(row + c);
             v.u[0] = q.x; v.u[1] = q.y; v.u[2] = q.z; v.u[3] = q.w;
@@ -61,40 +106,60 @@ __device__ __forceinline__ Vec8 load8(const bf16* row, int c, int H) {
     } else {
         const uint16_t* r = reinterpret_cast<const uint16_t*>(row);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < H) v.u[i >> 1] |= static_cast<uint32_t>(r[c + i]) << (16 * (i & 1));
+        for (int i = 0; i < 8; ++i) {
+            const int c = g.template col<VEC>(j, i);
+            if (c < H) v.u[i >> 1] |= static_cast<uint32_t>(r[c]) << (16 * (i & 1));
+        }
     }
     return v;
 }
 
-template <bool VEC>
-__device__ __forceinline__ void store8(bf16* row, int c, int H, const float* f) {
+template <bool VEC, int MODE>
+__device__ __forceinline__ void store8(bf16* row, const RowGroup<MODE>& g, int j, int H, const float* f) {
     uint32_t u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) u[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
     if (VEC) {
+        const int c = g.template col<VEC>(j, 0);
         if (c < H) *reinterpret_cast<uint4*>(row + c) = make_uint4(u[0], u[1], u[2], u[3]);
     } else {
         uint16_t* r = reinterpret_cast<uint16_t*>(row);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < H) r[c + i] = static_cast<uint16_t>(u[i >> 1] >> (16 * (i & 1)));
+        for (int i = 0; i < 8; ++i) {
+            const int c = g.template col<VEC>(j, i);
+            if (c < H) r[c] = static_cast<uint16_t>(u[i >> 1] >> (16 * (i & 1)));
+        }
     }
 }
 
-// Sum over the row's threads, the same bits in every one of them.  ROW: the
-// whole CTA holds one row; else a warp does.  Consecutive sums alternate
-// between two slots (n counts them), so one barrier a sum is enough: who has
-// passed the next sum's barrier knows that all have read this one.
-template <bool ROW>
-__device__ __forceinline__ float row_sum(float v, float (*red)[32], int& n) {
+// One or two sums over the row's threads, the same bits in every one of them.
+// Consecutive sums alternate between two slots of `red` (n counts them), so one
+// barrier a sum is enough: who has passed the next sum's barrier knows that all
+// have read this one.
+template <int MODE>
+__device__ __forceinline__ float row_sum(float v, float (*red)[32], const RowGroup<MODE>& g, int& n) {
     v = warp_sum(v);
-    if (ROW) {
-        const int slot = n++ & 1;
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (MODE != kRowsWarp) {
+        const int slot = n++ & 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int first = g.id() * (g.th() >> 5);
         if (lane == 0) red[slot][warp] = v;
-        __syncthreads();
-        v = warp_sum(lane < static_cast<int>(blockDim.x >> 5) ? red[slot][lane] : 0.0f);
+        g.sync();
+        v = warp_sum(lane < (g.th() >> 5) ? red[slot][first + lane] : 0.0f);
+    }
+    return v;
+}
+template <int MODE>
+__device__ __forceinline__ float2 row_sum2(float2 v, float (*red)[32], float (*red2)[32], const RowGroup<MODE>& g, int& n) {
+    v.x = warp_sum(v.x);
+    v.y = warp_sum(v.y);
+    if (MODE != kRowsWarp) {
+        const int slot = n++ & 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int first = g.id() * (g.th() >> 5);
+        if (lane == 0) { red[slot][warp] = v.x; red2[slot][warp] = v.y; }
+        g.sync();
+        const bool in = lane < (g.th() >> 5);
+        v.x = warp_sum(in ? red[slot][first + lane] : 0.0f);
+        v.y = warp_sum(in ? red2[slot][first + lane] : 0.0f);
     }
     return v;
 }
@@ -102,19 +167,20 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[32], int& n) {
 // 1 / sqrt(sum / H + eps)
 __device__ __forceinline__ float inv_rms(float sum, float inv_H, float eps) { return rsqrtf(sum * inv_H + eps); }
 
-// V vectors of 8 columns a thread; ROW: one row a CTA, else one row a warp.
-template <int V, bool VEC, bool ROW>
+// Bound by HBM: every load of a row goes out before its first sum, and many rows
+// are in flight on an SM (T = H = 4096 with a full gate, 168 MB: 26 us, 95 % of
+// the measured copy rate).
+template <bool VEC, int MODE>
 __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormArgs p) {
+    constexpr int V = norm_v(MODE);
     __shared__ float red[2][32];
-    int sums = 0;
+    int n_sums = 0;
+    const RowGroup<MODE> g(p.row_threads);
     grid_begin();
     bool ok;
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
     const int H = p.H;
-    const int width = ROW ? blockDim.x : 32;
-    const int lane = ROW ? threadIdx.x : threadIdx.x & 31;
-    const int rows_cta = ROW ? 1 : blockDim.x >> 5;
-    for (int t = blockIdx.x * rows_cta + (ROW ? 0 : threadIdx.x >> 5); t < T; t += gridDim.x * rows_cta) {
+    for (int t = blockIdx.x * g.groups() + g.id(); t < T; t += gridDim.x * g.groups()) {
         const size_t off = static_cast<size_t>(t) * H;
         float z[V][8];
         Vec8 yv[V], gv[V];
@@ -122,11 +188,10 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormArgs p) {
         const bool vec_gate = p.gate_kind == kGateFull || p.gate_kind == kGateChannel;
         const bf16* grow = static_cast<const bf16*>(p.gate) + (p.gate_kind == kGateFull ? off : 0);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {  // every load of the row before the first sum
-            const int c = (j * width + lane) * 8;
-            const Vec8 xv = load8<VEC>(p.x + off, c, H);
-            yv[j] = p.y ? load8<VEC>(p.y + off, c, H) : Vec8{};
-            gv[j] = vec_gate ? load8<VEC>(grow, c, H) : Vec8{};
+        for (int j = 0; j < V; ++j) {
+            const Vec8 xv = load8<VEC>(p.x + off, g, j, H);
+            yv[j] = p.y ? load8<VEC>(p.y + off, g, j, H) : Vec8{};
+            gv[j] = vec_gate ? load8<VEC>(grow, g, j, H) : Vec8{};
 #pragma unroll
             for (int i = 0; i < 8; ++i) z[j][i] = xv[i];
         }
@@ -136,80 +201,99 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormArgs p) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss += yv[j][i] * yv[j][i];
         float ry = 1.0f;
-        if (p.y && p.gamma_post) ry = inv_rms(row_sum<ROW>(ss, red, sums), p.inv_H, p.eps);
+        if (p.y && p.gamma_post) ry = inv_rms(row_sum(ss, red, g, n_sums), p.inv_H, p.eps);
         float zz = 0.0f;
         const float gs = p.scale * gtok;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int c = (j * width + lane) * 8;
-            if (p.y && c < H) {
-                const Vec8 gp = p.gamma_post ? load8<VEC>(p.gamma_post, c, H) : Vec8{};
+            if (p.y) {
+                const Vec8 gp = p.gamma_post ? load8<VEC>(p.gamma_post, g, j, H) : Vec8{};
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float n = p.gamma_post ? yv[j][i] * ry * gp[i] : yv[j][i];
                     z[j][i] += (vec_gate ? gs * gv[j][i] : gs) * n;  // 0 past H, where y is 0
                 }
             }
-            if (p.x_out && c < H) store8<VEC>(p.x_out + off, c, H, z[j]);
+            if (p.x_out) store8<VEC>(p.x_out + off, g, j, H, z[j]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) zz += z[j][i] * z[j][i];
         }
         if (p.x_hat) {
-            const float rz = inv_rms(row_sum<ROW>(zz, red, sums), p.inv_H, p.eps);
+            const float rz = inv_rms(row_sum(zz, red, g, n_sums), p.inv_H, p.eps);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const int c = (j * width + lane) * 8;
-                if (c < H) {
-                    const Vec8 gp = load8<VEC>(p.gamma_pre, c, H);
-                    float o[8];
+                const Vec8 gp = load8<VEC>(p.gamma_pre, g, j, H);
+                float o[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = z[j][i] * rz * gp[i];
-                    store8<VEC>(p.x_hat + off, c, H, o);
-                }
+                for (int i = 0; i < 8; ++i) o[i] = z[j][i] * rz * gp[i];
+                store8<VEC>(p.x_hat + off, g, j, H, o);
             }
         }
     }
 }
 
-// Two sums over the row's threads with one barrier (see row_sum).
-template <bool ROW>
-__device__ __forceinline__ float2 row_sum2(float2 v, float (*red)[32], float (*red2)[32], int& n) {
-    v.x = warp_sum(v.x);
-    v.y = warp_sum(v.y);
-    if (ROW) {
-        const int slot = n++ & 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        if (lane == 0) { red[slot][warp] = v.x; red2[slot][warp] = v.y; }
+// The parameter gradients of a CTA: its row groups' sums added up in order and
+// stored as this CTA's row of partial sums (those that are wanted).
+// get(arr, j, i): this thread's sum.
+template <bool VEC, int MODE, class F>
+__device__ __forceinline__ void store_part(const NormArgs& p, const RowGroup<MODE>& g, float* smem, F&& get) {
+    const int H = p.H;
+    float* part = p.part + static_cast<size_t>(blockIdx.x) * 3 * H;
+    float* to = MODE == kRowsOne || g.groups() == 1 ? part : smem + static_cast<size_t>(g.id()) * 3 * H;
+    if (MODE != kRowsOne) __syncthreads();  // what else lies there has been read
+#pragma unroll
+    for (int arr = 0; arr < 3; ++arr)
+        if (p.part_of >> arr & 1)
+#pragma unroll
+            for (int j = 0; j < norm_v(MODE); ++j) {
+                if (VEC) {
+                    const int c = g.template col<VEC>(j, 0);
+                    if (c < H) {
+                        float4* o = reinterpret_cast<float4*>(to + arr * H + c);
+                        o[0] = make_float4(get(arr, j, 0), get(arr, j, 1), get(arr, j, 2), get(arr, j, 3));
+                        o[1] = make_float4(get(arr, j, 4), get(arr, j, 5), get(arr, j, 6), get(arr, j, 7));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int c = g.template col<VEC>(j, i);
+                        if (c < H) to[arr * H + c] = get(arr, j, i);
+                    }
+                }
+            }
+    if (MODE != kRowsOne && g.groups() > 1) {
         __syncthreads();
-        const bool in = lane < static_cast<int>(blockDim.x >> 5);
-        v.x = warp_sum(in ? red[slot][lane] : 0.0f);
-        v.y = warp_sum(in ? red2[slot][lane] : 0.0f);
+        for (int o = threadIdx.x; o < 3 * H; o += blockDim.x) {
+            float s = 0.0f;
+            if (p.part_of >> (o / H) & 1)
+                for (int k = 0; k < g.groups(); ++k) s += smem[static_cast<size_t>(k) * 3 * H + o];
+            part[o] = s;
+        }
     }
-    return v;
 }
 
 // The gradient.  A row's statistics are recomputed from x and y (they are read
 // anyway).  The parameter gradients are summed over this CTA's rows in
-// registers, thread by thread for its own columns, then over CTAs by
-// norm_sum_kernel in a fixed order.  Three sums a row: mean y^2; mean z^2 with
-// the second norm's projection; the first norm's projection (with a per-token
-// gate's gradient).
+// registers, thread by thread for its own columns, then over its row groups and
+// over CTAs (norm_sum_kernel) in a fixed order.  Three sums a row: mean y^2;
+// mean z^2 with the second norm's projection; the first norm's projection (with
+// a per-token gate's gradient).
 //
 // This form serves every H, alignment and combination of the optional parts;
 // norm_bwd_staged_kernel the usual one.  MAXT: most threads, which bounds the
 // registers.
-template <int V, bool VEC, bool ROW, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormArgs p) {
+template <bool VEC, int MODE, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(const NormArgs p) {
+    constexpr int V = norm_v(MODE);
     __shared__ float red[2][32], red2[2][32];
-    int sums = 0;
-    extern __shared__ __align__(16) uint8_t dyn[];  // !ROW: [warps][3][256] floats
+    extern __shared__ __align__(16) uint8_t dyn[];  // [groups][3][H] floats
+    int n_sums = 0;
+    const RowGroup<MODE> g(p.row_threads);
     grid_begin();
     bool ok;
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
+    if (!ok) return;
     const int H = p.H;
-    const int width = ROW ? blockDim.x : 32;
-    const int lane = ROW ? threadIdx.x : threadIdx.x & 31;
-    const int rows_cta = ROW ? 1 : blockDim.x >> 5;
-    const int step = gridDim.x * rows_cta;
     const bool post = p.y && p.gamma_post;
     const bool full = p.gate_kind == kGateFull;
     float a_post[V][8], a_pre[V][8], a_gate[V][8];
@@ -217,170 +301,122 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormArgs p) {
     for (int j = 0; j < V; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i) a_post[j][i] = a_pre[j][i] = a_gate[j][i] = 0.0f;
-
-    // columns [c, c + 8) of a row of one input (zeros where it is not given)
-    auto row8 = [&](const bf16* base, int t, int c) -> Vec8 {
-        return base ? load8<VEC>(base + static_cast<size_t>(t) * H, c, H) : Vec8{};
-    };
-    // scale * gate of columns [c, c + 8)
-    auto gate_of = [&](int t, int c, float gs, float* g) {
-        if (full || p.gate_kind == kGateChannel) {
-            const Vec8 v = row8(static_cast<const bf16*>(p.gate), full ? t : 0, c);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] = gs * v[i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] = gs;
-        }
+    auto row8 = [&](const bf16* base, size_t off, int j) -> Vec8 {  // zeros where it is not given
+        return base ? load8<VEC>(base + off, g, j, H) : Vec8{};
     };
 
-    for (int t = blockIdx.x * rows_cta + (ROW ? 0 : threadIdx.x >> 5); t < T; t += step) {
+    for (int t = blockIdx.x * g.groups() + g.id(); t < T; t += gridDim.x * g.groups()) {
         const size_t off = static_cast<size_t>(t) * H;
-        float ss = 0.0f;
-        if (post)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const Vec8 yv = row8(p.y, t, (j * width + lane) * 8);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) ss += yv[i] * yv[i];
-            }
         const float gs = p.scale * (p.gate_kind == kGateToken ? static_cast<const float*>(p.gate)[t] : 1.0f);
+        auto gate_of = [&](int j, float* q) {  // scale * gate of vector j
+            if (full || p.gate_kind == kGateChannel) {
+                const Vec8 v = row8(static_cast<const bf16*>(p.gate), full ? off : 0, j);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) q[i] = gs * v[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) q[i] = gs;
+            }
+        };
+        Vec8 xv[V], yv[V], dz[V], dh[V];
+        float ss = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            xv[j] = row8(p.x, off, j);
+            yv[j] = row8(p.y, off, j);
+            dz[j] = row8(p.d_x_out, off, j);
+            dh[j] = row8(p.d_x_hat, off, j);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss += yv[j][i] * yv[j][i];
+        }
         float ry = 1.0f;
-        if (post) ry = inv_rms(row_sum<ROW>(ss, red, sums), p.inv_H, p.eps);
+        if (post) ry = inv_rms(row_sum(ss, red, g, n_sums), p.inv_H, p.eps);
         // z, and with it the statistics of the second norm and sum(d_x_hat gamma_pre z)
         float z[V][8];
         float2 za = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int c = (j * width + lane) * 8;
-            const Vec8 xv = row8(p.x, t, c);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) z[j][i] = xv[i];
-            if (c < H) {
-                if (p.y) {
-                    float g[8];
-                    gate_of(t, c, gs, g);
-                    const Vec8 yv = row8(p.y, t, c);
-                    const Vec8 gp = post ? load8<VEC>(p.gamma_post, c, H) : Vec8{};
+            for (int i = 0; i < 8; ++i) z[j][i] = xv[j][i];
+            if (p.y) {
+                float q[8];
+                gate_of(j, q);
+                const Vec8 gp = post ? row8(p.gamma_post, 0, j) : Vec8{};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        z[j][i] += g[i] * (post ? yv[i] * ry * gp[i] : yv[i]);  // 0 past H, where y is 0
-                }
-                if (p.d_x_hat) {
-                    const Vec8 dh = row8(p.d_x_hat, t, c);
-                    const Vec8 gp = load8<VEC>(p.gamma_pre, c, H);
+                for (int i = 0; i < 8; ++i)
+                    z[j][i] += q[i] * (post ? yv[j][i] * ry * gp[i] : yv[j][i]);  // 0 past H, where y is 0
+            }
+            if (p.d_x_hat) {
+                const Vec8 gr = row8(p.gamma_pre, 0, j);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        za.x += z[j][i] * z[j][i];
-                        za.y += dh[i] * gp[i] * z[j][i];
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    za.x += z[j][i] * z[j][i];
+                    za.y += dh[j][i] * gr[i] * z[j][i];
                 }
             }
         }
         float rz = 0.0f, k2 = 0.0f;
         if (p.d_x_hat) {
-            za = row_sum2<ROW>(za, red, red2, sums);
+            za = row_sum2(za, red, red2, g, n_sums);
             rz = inv_rms(za.x, p.inv_H, p.eps);
             k2 = za.y * p.inv_H * rz * rz * rz;
         }
         // d z, the parameter gradients, and sum(d n gamma_post y)
         float2 bg = make_float2(0.0f, 0.0f);
-        float d[V][8];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int c = (j * width + lane) * 8;
+            float d[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d[j][i] = 0.0f;
-            if (c < H) {
-                const Vec8 dz = row8(p.d_x_out, t, c);
+            for (int i = 0; i < 8; ++i) d[i] = dz[j][i];
+            if (p.d_x_hat) {
+                const Vec8 gr = row8(p.gamma_pre, 0, j);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) d[j][i] = dz[i];
-                if (p.d_x_hat) {
-                    const Vec8 dh = row8(p.d_x_hat, t, c);
-                    const Vec8 gp = load8<VEC>(p.gamma_pre, c, H);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        d[j][i] += rz * (dh[i] * gp[i]) - z[j][i] * k2;
-                        a_pre[j][i] += dh[i] * (z[j][i] * rz);
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    d[i] += rz * (dh[j][i] * gr[i]) - z[j][i] * k2;
+                    a_pre[j][i] += dh[j][i] * (z[j][i] * rz);
                 }
-                store8<VEC>(p.dx + off, c, H, d[j]);
-                if (p.y) {
-                    float g[8], dgf[8];
-                    gate_of(t, c, gs, g);
-                    const Vec8 yv = row8(p.y, t, c);
-                    const Vec8 gp = post ? load8<VEC>(p.gamma_post, c, H) : Vec8{};
+            }
+            store8<VEC>(p.dx + off, g, j, H, d);
+            if (p.y) {
+                float q[8], dgf[8];
+                gate_of(j, q);
+                const Vec8 gp = post ? row8(p.gamma_post, 0, j) : Vec8{};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float u = yv[i] * ry;  // the normalised value
-                        const float n = post ? u * gp[i] : yv[i];
-                        dgf[i] = p.scale * n * d[j][i];
-                        d[j][i] *= g[i];  // d n
-                        a_post[j][i] += d[j][i] * u;
-                        if (post) {
-                            d[j][i] *= gp[i];
-                            bg.x += d[j][i] * yv[i];
-                        }
-                        a_gate[j][i] += dgf[i];
-                        bg.y += dgf[i];
+                for (int i = 0; i < 8; ++i) {
+                    const float u = yv[j][i] * ry;  // the normalised value
+                    dgf[i] = p.scale * (post ? u * gp[i] : yv[j][i]) * d[i];
+                    d[i] *= q[i];  // d n
+                    a_post[j][i] += d[i] * u;
+                    if (post) {
+                        d[i] *= gp[i];
+                        bg.x += d[i] * yv[j][i];
                     }
-                    if (p.d_gate_full) store8<VEC>(p.d_gate_full + off, c, H, dgf);
+                    a_gate[j][i] += dgf[i];
+                    bg.y += dgf[i];
+                    z[j][i] = d[i];
                 }
+                if (p.d_gate_full) store8<VEC>(p.d_gate_full + off, g, j, H, dgf);
             }
         }
         if (p.y) {
-            if (post || p.d_gate_token) bg = row_sum2<ROW>(bg, red, red2, sums);
+            if (post || p.d_gate_token) bg = row_sum2(bg, red, red2, g, n_sums);
             const float k1 = post ? bg.x * p.inv_H * ry * ry * ry : 0.0f;
-            if (p.d_gate_token && lane == 0) p.d_gate_token[t] = bg.y;
+            if (p.d_gate_token && g.lane() == 0) p.d_gate_token[t] = bg.y;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const int c = (j * width + lane) * 8;
-                if (c < H) {
-                    const Vec8 yv = row8(p.y, t, c);
-                    float o[8];
+                float o[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = post ? ry * d[j][i] - yv[i] * k1 : d[j][i];
-                    store8<VEC>(p.dy + off, c, H, o);
-                }
+                for (int i = 0; i < 8; ++i) o[i] = post ? ry * z[j][i] - yv[j][i] * k1 : z[j][i];
+                store8<VEC>(p.dy + off, g, j, H, o);
             }
         }
     }
-    if (!ok) return;
-    float* part = p.part + static_cast<size_t>(blockIdx.x) * 3 * H;
-    if (ROW) {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int c = (j * width + lane) * 8 + i;
-                if (c < H) {
-                    part[c] = a_post[j][i];
-                    part[H + c] = a_pre[j][i];
-                    part[2 * H + c] = a_gate[j][i];
-                }
-            }
-    } else {  // one row a warp (H <= 256): the CTA's warps in order
-        const int warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-        float* acc_sm = reinterpret_cast<float*>(dyn);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float* a = acc_sm + warp * 768 + lane * 8 + i;
-            a[0] = a_post[0][i];
-            a[256] = a_pre[0][i];
-            a[512] = a_gate[0][i];
-        }
-        __syncthreads();
-        for (int o = threadIdx.x; o < 3 * H; o += blockDim.x) {
-            const int arr = o / H, c = o - arr * H;
-            float s = 0.0f;
-            for (int w = 0; w < nwarps; ++w) s += acc_sm[w * 768 + arr * 256 + c];
-            part[o] = s;
-        }
-    }
+    store_part<VEC>(p, g, reinterpret_cast<float*>(dyn),
+                    [&](int arr, int j, int i) { return arr == 0 ? a_post[j][i] : arr == 1 ? a_pre[j][i] : a_gate[j][i]; });
 }
 
 // The same gradient where y, gamma_pre and both incoming gradients are given, H
-// is a multiple of 8 in (512, 8192] and every tensor is 16-byte aligned.
+// is a multiple of 8 up to 8192 and every tensor is 16-byte aligned.
 //
 // Bound by HBM (T = H = 4096 with a full gate: 268 MB) if a row's latencies are
 // hidden: the input rows of this CTA's next row are copied to shared memory
@@ -396,27 +432,31 @@ enum NormGate { kGScalar = 0, kGChannel = 1, kGFull = 2 };
 __device__ __forceinline__ float2 unpack2(uint32_t w) { return make_float2(bf_lo(w), bf_hi(w)); }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-template <int GK, int MAXT>
+template <int GK, int MODE, int MAXT>
 __global__ void __launch_bounds__(MAXT, 512 / MAXT) norm_bwd_staged_kernel(const NormArgs p) {
+    constexpr int V = norm_v(MODE);
     constexpr int A = GK == kGFull ? 5 : 4;  // staged rows: x, y, d_x_out, d_x_hat (, gate)
     __shared__ float red[2][32], red2[2][32];
-    extern __shared__ __align__(16) uint8_t dyn[];  // [2][A][H] rows; gamma_post, gamma_pre (, gate) [H]
-    int sums = 0;
+    // [groups][2][A][H] rows; gamma_post, gamma_pre (, gate) [H]; at the end [groups][3][H] floats
+    extern __shared__ __align__(16) uint8_t dyn[];
+    int n_sums = 0;
+    const RowGroup<MODE> grp(p.row_threads);
     grid_begin();
     bool ok;
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
     if (!ok) return;
     const int H = p.H, H2 = H * 2;
     const bool post = p.gamma_post != nullptr;
-    const int c0 = threadIdx.x * 8, c1 = (blockDim.x + threadIdx.x) * 8;
-    const bool in0 = c0 < H, in1 = c1 < H;
-    uint8_t* par = dyn + 2 * A * H2;
+    const int c0 = grp.template col<true>(0, 0), c1 = grp.template col<true>(1, 0);
+    const bool in0 = c0 < H, in1 = V > 1 && c1 < H;
+    uint8_t* mine = dyn + static_cast<size_t>(grp.id()) * 2 * A * H2;
+    uint8_t* par = dyn + static_cast<size_t>(grp.groups()) * 2 * A * H2;
 
     auto stage = [&](int t, int buf) {
         if (t < T) {
             const size_t off = static_cast<size_t>(t) * H;
             const bf16* src[5] = {p.x, p.y, p.d_x_out, p.d_x_hat, static_cast<const bf16*>(p.gate)};
-            const uint32_t dst = smem_addr(dyn) + buf * A * H2;
+            const uint32_t dst = smem_addr(mine) + buf * A * H2;
 #pragma unroll
             for (int a = 0; a < A; ++a) {
                 if (in0) cp_async16(dst + a * H2 + c0 * 2, src[a] + off + c0);
@@ -426,9 +466,11 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) norm_bwd_staged_kernel(const
         cp_async_commit();
     };
     int buf = 0;
-    stage(blockIdx.x, 0);
-    // the parameters, 1 for a missing gamma_post
-    for (int j = 0; j < 2; ++j) {
+    const int t0 = blockIdx.x * grp.groups() + grp.id(), step = gridDim.x * grp.groups();
+    stage(t0, 0);
+    // the parameters, 1 for a missing gamma_post (every group copies them all for itself
+    // to read: the same values)
+    for (int j = 0; j < V; ++j) {
         const int c = j ? c1 : c0;
         if (c < H) {
             *reinterpret_cast<uint4*>(par + c * 2) = post ? *reinterpret_cast<const uint4*>(p.gamma_post + c)
@@ -439,25 +481,25 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) norm_bwd_staged_kernel(const
                     *reinterpret_cast<const uint4*>(static_cast<const bf16*>(p.gate) + c);
         }
     }
-    float2 a_post[2][4], a_pre[2][4], a_gate[2][4];
+    float2 a_post[V][4], a_pre[V][4], a_gate[V][4];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < V; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) a_post[j][i] = a_pre[j][i] = a_gate[j][i] = both(0.0f);
 
-    for (int t = blockIdx.x; t < T; t += gridDim.x, buf ^= 1) {
-        stage(t + gridDim.x, buf ^ 1);  // this thread has read that buffer's last row
+    for (int t = t0; t < T; t += step, buf ^= 1) {
+        stage(t + step, buf ^ 1);  // this thread has read that buffer's last row
         cp_async_wait<1>();
-        const uint8_t* rows = dyn + buf * A * H2;
+        const uint8_t* rows = mine + buf * A * H2;
         auto get = [&](const uint8_t* base, int j) -> uint4 {  // zeros past H
             return (j ? in1 : in0) ? *reinterpret_cast<const uint4*>(base + (j ? c1 : c0) * 2) : make_uint4(0, 0, 0, 0);
         };
         auto word = [](const uint4& v, int i) -> uint32_t { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; };
         const float gs = p.scale * (GK == kGScalar && p.gate ? static_cast<const float*>(p.gate)[t] : 1.0f);
-        float2 u[2][4], z[2][4];
+        float2 u[V][4], z[V][4];
         float2 ss = both(0.0f);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < V; ++j) {
             const uint4 y = get(rows + H2, j);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -465,10 +507,10 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) norm_bwd_staged_kernel(const
                 ss = __ffma2_rn(u[j][i], u[j][i], ss);
             }
         }
-        const float ry = post ? inv_rms(row_sum<true>(ss.x + ss.y, red, sums), p.inv_H, p.eps) : 1.0f;
+        const float ry = post ? inv_rms(row_sum(ss.x + ss.y, red, grp, n_sums), p.inv_H, p.eps) : 1.0f;
         float2 zz = both(0.0f), ez = both(0.0f);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < V; ++j) {
             const uint4 x = get(rows, j), dh = get(rows + 3 * H2, j), gp = get(par, j), gr = get(par + H2, j);
             const uint4 g = GK == kGFull ? get(rows + 4 * H2, j) : GK == kGChannel ? get(par + 2 * H2, j) : uint4{};
 #pragma unroll
@@ -482,13 +524,13 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) norm_bwd_staged_kernel(const
                 ez = __ffma2_rn(e, z[j][i], ez);
             }
         }
-        const float2 za = row_sum2<true>(make_float2(zz.x + zz.y, ez.x + ez.y), red, red2, sums);
+        const float2 za = row_sum2(make_float2(zz.x + zz.y, ez.x + ez.y), red, red2, grp, n_sums);
         const float rz = inv_rms(za.x, p.inv_H, p.eps);
         const float k2 = za.y * p.inv_H * rz * rz * rz;
         const size_t off = static_cast<size_t>(t) * H;
         float2 bu = both(0.0f), gt = both(0.0f);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < V; ++j) {
             const uint4 dz = get(rows + 2 * H2, j), dh = get(rows + 3 * H2, j), gp = get(par, j), gr = get(par + H2, j);
             const uint4 g = GK == kGFull ? get(rows + 4 * H2, j) : GK == kGChannel ? get(par + 2 * H2, j) : uint4{};
             uint32_t odx[4], odg[4];
@@ -520,12 +562,12 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) norm_bwd_staged_kernel(const
         }
         float m = 0.0f;
         if (post || p.d_gate_token) {
-            const float2 s = row_sum2<true>(make_float2(bu.x + bu.y, gt.x + gt.y), red, red2, sums);
+            const float2 s = row_sum2(make_float2(bu.x + bu.y, gt.x + gt.y), red, red2, grp, n_sums);
             m = post ? s.x * p.inv_H : 0.0f;
-            if (p.d_gate_token && threadIdx.x == 0) p.d_gate_token[t] = s.y * p.scale;
+            if (p.d_gate_token && grp.lane() == 0) p.d_gate_token[t] = s.y * p.scale;
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < V; ++j) {
             uint32_t o[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -536,17 +578,10 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) norm_bwd_staged_kernel(const
         }
     }
     cp_async_wait<0>();
-    float* part = p.part + static_cast<size_t>(blockIdx.x) * 3 * H;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-        if (j ? in1 : in0)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float* o = part + (j ? c1 : c0) + 2 * i;  // H is a multiple of 8: 8-byte aligned
-                *reinterpret_cast<float2*>(o) = a_post[j][i];
-                *reinterpret_cast<float2*>(o + H) = a_pre[j][i];
-                if (GK == kGChannel) *reinterpret_cast<float2*>(o + 2 * H) = __fmul2_rn(a_gate[j][i], both(p.scale));
-            }
+    store_part<true>(p, grp, reinterpret_cast<float*>(dyn), [&](int arr, int j, int i) {
+        const float2 v = arr == 0 ? a_post[j][i >> 1] : arr == 1 ? a_pre[j][i >> 1] : a_gate[j][i >> 1];
+        return (i & 1 ? v.y : v.x) * (arr == 2 ? p.scale : 1.0f);
+    });
 }
 
 struct NormSumArgs {
@@ -620,64 +655,79 @@ bool norm_vec(int H, std::initializer_list<const void*> ps) {
     return true;
 }
 
-// Threads of a row: 16 columns (two vectors) each, 8 for a row of up to 512.
-int norm_threads(int H) {
-    const int vecs = (H + 7) / 8;
-    return ((vecs > 64 ? (vecs + 1) / 2 : vecs) + 31) / 32 * 32;
+// Threads of a row: sixteen columns each.
+int norm_threads(int H) { return ((H + 15) / 16 + 31) / 32 * 32; }
+
+// Rows of a CTA: as many as make 256 threads.  With fewer, a small H left most of
+// an SM idle (forward and backward, T = 4096, H = 512: 62 us, with eight rows 20).
+int norm_groups(int threads, int rows) {
+    const int g = threads < kNormCtaThreads ? kNormCtaThreads / threads : 1;
+    return g < rows ? g : rows;
+}
+
+RowMode norm_mode(int H, int threads) {
+    return H <= 256 ? kRowsWarp : 2 * threads <= kNormCtaThreads ? kRowsGroup : kRowsOne;
 }
 
 template <bool VEC>
-cudaError_t launch_fwd(const NormArgs& a, int rows, int sms, void* stream) {
-    if (a.H <= 256) {
-        const int warps = rows < 8 ? rows : 8;
-        int grid = (rows + warps - 1) / warps;
-        grid = grid < 8 * sms ? grid : 8 * sms;
-        return api_launch(norm_fwd_kernel<1, VEC, false>, grid, warps * 32, 0, stream, a);
-    }
-    const int th = norm_threads(a.H);
-    const int most = sms * (1024 / th);
-    const int grid = rows < most ? rows : most;
-    if (a.H <= 512) return api_launch(norm_fwd_kernel<1, VEC, true>, grid, th, 0, stream, a);
-    return api_launch(norm_fwd_kernel<2, VEC, true>, grid, th, 0, stream, a);
+cudaError_t launch_fwd(NormArgs a, int rows, int sms, void* stream) {
+    a.row_threads = norm_threads(a.H);
+    const RowMode mode = norm_mode(a.H, a.row_threads);
+    const int groups = norm_groups(a.row_threads, rows), th = a.row_threads * groups;
+    const int need = (rows + groups - 1) / groups, most = sms * (1024 / th);
+    const int grid = need < most ? need : most;
+    return api_launch(mode == kRowsWarp ? norm_fwd_kernel<VEC, kRowsWarp> : mode == kRowsGroup ? norm_fwd_kernel<VEC, kRowsGroup>
+                                                                          : norm_fwd_kernel<VEC, kRowsOne>,
+                      grid, th, 0, stream, a);
 }
 
-template <int GK, int MAXT>
-cudaError_t launch_bwd_staged(const NormArgs& a, int dev, int sms, int threads, int rows, int* parts, void* stream) {
-    static SmemOptIn opt;
-    // 2 A rows and the parameters: 12 rows at most, 197 KB at H = 8192
-    const int smem = (GK == kGFull ? 12 : GK == kGChannel ? 11 : 10) * a.H * static_cast<int>(sizeof(bf16));
-    const cudaError_t e = api_smem_opt_in(opt, dev, norm_bwd_staged_kernel<GK, MAXT>, kSmemLimit - 2048);
+struct NormLaunch {
+    int dev, sms, rows, parts_max;
+    int* parts;
+    void* stream;
+};
+
+// The grid is also the number of partial rows that norm_sum_kernel reads: two CTAs
+// an SM of up to 256 threads (128 registers each), else one.
+template <class K>
+cudaError_t launch_bwd_rows(SmemOptIn& opt, K kernel, const NormArgs& a, const NormLaunch& l, int smem_row, int smem_cta) {
+    const cudaError_t e = api_smem_opt_in(opt, l.dev, kernel, kSmemLimit - 2048);
     if (e != cudaSuccess) return e;
-    const int most = sms * (512 / MAXT);
-    *parts = *parts < most ? *parts : most;
-    return api_launch(norm_bwd_staged_kernel<GK, MAXT>, *parts, threads, smem, stream, a);
+    const int groups = norm_groups(a.row_threads, l.rows), th = a.row_threads * groups;
+    const int need = (l.rows + groups - 1) / groups, most = th <= kNormCtaThreads ? 2 * l.sms : l.sms;
+    int n = need < l.parts_max ? need : l.parts_max;
+    *l.parts = n = n < most ? n : most;
+    // the rows of a CTA, then (at the end) its groups' sums
+    const int staged = groups * smem_row + smem_cta, merge = groups > 1 ? groups * 3 * a.H * 4 : 0;
+    return api_launch(kernel, n, th, staged > merge ? staged : merge, l.stream, a);
 }
 
-// The grid is also the number of partial rows that norm_sum_kernel reads.
+template <int GK>
+cudaError_t launch_bwd_staged(const NormArgs& a, RowMode mode, const NormLaunch& l) {
+    static SmemOptIn opt[4];
+    constexpr int A = GK == kGFull ? 5 : 4;
+    const int row = 2 * A * a.H * 2, par = (GK == kGChannel ? 3 : 2) * a.H * 2;  // 197 KB at most
+    if (mode == kRowsWarp) return launch_bwd_rows(opt[0], norm_bwd_staged_kernel<GK, kRowsWarp, 256>, a, l, row, par);
+    if (mode == kRowsGroup) return launch_bwd_rows(opt[1], norm_bwd_staged_kernel<GK, kRowsGroup, 256>, a, l, row, par);
+    if (a.row_threads <= 256) return launch_bwd_rows(opt[2], norm_bwd_staged_kernel<GK, kRowsOne, 256>, a, l, row, par);
+    return launch_bwd_rows(opt[3], norm_bwd_staged_kernel<GK, kRowsOne, 512>, a, l, row, par);
+}
+
 template <bool VEC>
-cudaError_t launch_bwd(const NormArgs& a, int dev, int sms, int rows, int parts_max, int* parts, void* stream) {
-    if (a.H <= 256) {
-        const int warps = 8;
-        const int need = (rows + warps - 1) / warps;
-        *parts = need < parts_max ? need : parts_max;
-        return api_launch(norm_bwd_kernel<1, VEC, false, 256>, *parts, warps * 32, warps * 768 * sizeof(float),
-                          stream, a);
+cudaError_t launch_bwd(NormArgs a, const NormLaunch& l) {
+    a.row_threads = norm_threads(a.H);
+    const RowMode mode = norm_mode(a.H, a.row_threads);
+    if (VEC && a.row_threads <= 512 && a.y && a.gamma_pre && a.d_x_out && a.d_x_hat) {
+        if (a.gate_kind == kGateFull) return launch_bwd_staged<kGFull>(a, mode, l);
+        if (a.gate_kind == kGateChannel) return launch_bwd_staged<kGChannel>(a, mode, l);
+        return launch_bwd_staged<kGScalar>(a, mode, l);
     }
-    const int th = norm_threads(a.H);
-    *parts = rows < parts_max ? rows : parts_max;
-    if (VEC && a.H > 512 && th <= 512 && a.y && a.gamma_pre && a.d_x_out && a.d_x_hat) {
-        if (th <= 256) {
-            if (a.gate_kind == kGateFull) return launch_bwd_staged<kGFull, 256>(a, dev, sms, th, rows, parts, stream);
-            if (a.gate_kind == kGateChannel) return launch_bwd_staged<kGChannel, 256>(a, dev, sms, th, rows, parts, stream);
-            return launch_bwd_staged<kGScalar, 256>(a, dev, sms, th, rows, parts, stream);
-        }
-        if (a.gate_kind == kGateFull) return launch_bwd_staged<kGFull, 512>(a, dev, sms, th, rows, parts, stream);
-        if (a.gate_kind == kGateChannel) return launch_bwd_staged<kGChannel, 512>(a, dev, sms, th, rows, parts, stream);
-        return launch_bwd_staged<kGScalar, 512>(a, dev, sms, th, rows, parts, stream);
-    }
-    if (a.H <= 512) return api_launch(norm_bwd_kernel<1, VEC, true, 512>, *parts, th, 0, stream, a);
-    if (th <= 512) return api_launch(norm_bwd_kernel<2, VEC, true, 512>, *parts, th, 0, stream, a);
-    return api_launch(norm_bwd_kernel<2, VEC, true, 1024>, *parts, th, 0, stream, a);
+    static SmemOptIn opt[5];
+    if (mode == kRowsWarp) return launch_bwd_rows(opt[0], norm_bwd_kernel<VEC, kRowsWarp, 256>, a, l, 0, 0);
+    if (mode == kRowsGroup) return launch_bwd_rows(opt[1], norm_bwd_kernel<VEC, kRowsGroup, 256>, a, l, 0, 0);
+    if (a.row_threads <= 256) return launch_bwd_rows(opt[2], norm_bwd_kernel<VEC, kRowsOne, 256>, a, l, 0, 0);
+    if (a.row_threads <= 512) return launch_bwd_rows(opt[3], norm_bwd_kernel<VEC, kRowsOne, 512>, a, l, 0, 0);
+    return launch_bwd_rows(opt[4], norm_bwd_kernel<VEC, kRowsOne, 1024>, a, l, 0, 0);
 }
 
 }  // namespace
@@ -780,14 +830,15 @@ int et_block_norm_bwd(const void* x, const void* y, const void* gamma_post, cons
         a.d_gate_full = gate_kind == kGateFull ? static_cast<bf16*>(d_gate) : nullptr;
         a.d_gate_token = gate_kind == kGateToken ? static_cast<float*>(d_gate) : nullptr;
         a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
+        a.part_of = (d_gamma_post ? 1 : 0) | (d_gamma_pre ? 2 : 0) | (gate_kind == kGateChannel && d_gate ? 4 : 0);
         const int parts_max = T_max < kNormParts ? T_max : kNormParts;
         const int rows = d_T ? T_max : T;
         int parts = 0;
         if (rows > 0) {
             const bool vec = norm_vec(H, {x, y, gamma_post, gate_kind == kGateToken ? nullptr : gate, gamma_pre,
                                           d_x_out, d_x_hat, dx, dy, a.d_gate_full});
-            const cudaError_t e = vec ? launch_bwd<true>(a, dev, sms, rows, parts_max, &parts, stream)
-                                      : launch_bwd<false>(a, dev, sms, rows, parts_max, &parts, stream);
+            const NormLaunch l{dev, sms, rows, parts_max, &parts, stream};
+            const cudaError_t e = vec ? launch_bwd<true>(a, l) : launch_bwd<false>(a, l);
             if (e != cudaSuccess) return api_fail_cuda(e, "launch of the block norm's backward kernel");
         }
         float* d_gate_channel = gate_kind == kGateChannel ? static_cast<float*>(d_gate) : nullptr;
