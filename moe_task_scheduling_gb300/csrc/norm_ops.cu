@@ -86,6 +86,7 @@ struct RowGroup {
     }
     __device__ __forceinline__ void sync() const {
         if (MODE == kRowsOne) __syncthreads();
+        else if (MODE == kRowsWarp) __syncwarp();
         else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(threads) : "memory");
     }
 };
@@ -415,14 +416,17 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(con
                     [&](int arr, int j, int i) { return arr == 0 ? a_post[j][i] : arr == 1 ? a_pre[j][i] : a_gate[j][i]; });
 }
 
-// The same gradient where y, gamma_pre and both incoming gradients are given, H
-// is a multiple of 8 up to 8192 and every tensor is 16-byte aligned.
+// The same gradient where y, gamma_pre and both incoming gradients are given and H
+// is at most 8192.
 //
 // Bound by HBM (T = H = 4096 with a full gate: 268 MB) if a row's latencies are
 // hidden: the input rows of this CTA's next row are copied to shared memory
 // while the current one is worked on, each thread reading back only what it
 // copied itself, so that the copies need no barrier; the parameters lie there
-// for all rows.  Sixteen columns a thread, in pairs (fp32x2 products): the three
+// for all rows.  Without VEC (see RowGroup) a row is copied by the 16-byte pieces
+// that hold it -- the first of a tensor element by element, the last cut to its
+// end, so that nothing outside is read -- and read back by element, with a
+// barrier on either side.  Sixteen columns a thread, in pairs (fp32x2 products): the three
 // sums and the addresses cost as much as the columns' arithmetic.
 //   u = y r_y, a = scale gate gamma_post, z = x + a u, e = d_x_hat gamma_pre,
 //   D = d_x_out + r_z e - z r_z^3 mean(e z),  b = a D,
@@ -432,12 +436,16 @@ enum NormGate { kGScalar = 0, kGChannel = 1, kGFull = 2 };
 __device__ __forceinline__ float2 unpack2(uint32_t w) { return make_float2(bf_lo(w), bf_hi(w)); }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-template <int GK, int MODE, int MAXT>
+// Bytes of a staged row: without VEC it starts anywhere in its first 16-byte piece.
+__host__ __device__ constexpr int norm_row_bytes(int H, bool vec) { return vec ? H * 2 : (H * 2 + 29) / 16 * 16; }
+
+template <bool VEC, int GK, int MODE, int MAXT>
 __global__ void __launch_bounds__(MAXT, 512 / MAXT) norm_bwd_staged_kernel(const NormArgs p) {
     constexpr int V = norm_v(MODE);
     constexpr int A = GK == kGFull ? 5 : 4;  // staged rows: x, y, d_x_out, d_x_hat (, gate)
     __shared__ float red[2][32], red2[2][32];
-    // [groups][2][A][H] rows; gamma_post, gamma_pre (, gate) [H]; at the end [groups][3][H] floats
+    // [groups][2][A] rows; gamma_post, gamma_pre (, gate), each thread's own 16 values
+    // together; at the end [groups][3][H] floats
     extern __shared__ __align__(16) uint8_t dyn[];
     int n_sums = 0;
     const RowGroup<MODE> grp(p.row_threads);
@@ -447,20 +455,42 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) norm_bwd_staged_kernel(const
     if (!ok) return;
     const int H = p.H, H2 = H * 2;
     const bool post = p.gamma_post != nullptr;
+    const int row_b = norm_row_bytes(H, VEC), par_b = grp.th() * V * 16;  // bytes of a staged row, of a parameter
     const int c0 = grp.template col<true>(0, 0), c1 = grp.template col<true>(1, 0);
-    const bool in0 = c0 < H, in1 = V > 1 && c1 < H;
-    uint8_t* mine = dyn + static_cast<size_t>(grp.id()) * 2 * A * H2;
-    uint8_t* par = dyn + static_cast<size_t>(grp.groups()) * 2 * A * H2;
+    const bool in0 = c0 < H, in1 = V > 1 && c1 < H;  // VEC only
+    uint8_t* mine = dyn + static_cast<size_t>(grp.id()) * 2 * A * row_b;
+    uint8_t* par = dyn + static_cast<size_t>(grp.groups()) * 2 * A * row_b + grp.lane() * 16;
 
+    auto source = [&](int a) -> const bf16* {
+        return a == 0 ? p.x : a == 1 ? p.y : a == 2 ? p.d_x_out : a == 3 ? p.d_x_hat : static_cast<const bf16*>(p.gate);
+    };
     auto stage = [&](int t, int buf) {
         if (t < T) {
             const size_t off = static_cast<size_t>(t) * H;
-            const bf16* src[5] = {p.x, p.y, p.d_x_out, p.d_x_hat, static_cast<const bf16*>(p.gate)};
-            const uint32_t dst = smem_addr(mine) + buf * A * H2;
+            const uint32_t dst = smem_addr(mine) + buf * A * row_b;
 #pragma unroll
             for (int a = 0; a < A; ++a) {
-                if (in0) cp_async16(dst + a * H2 + c0 * 2, src[a] + off + c0);
-                if (in1) cp_async16(dst + a * H2 + c1 * 2, src[a] + off + c1);
+                if (VEC) {
+                    if (in0) cp_async16(dst + a * row_b + c0 * 2, source(a) + off + c0);
+                    if (in1) cp_async16(dst + a * row_b + c1 * 2, source(a) + off + c1);
+                } else {
+                    const uint8_t* base = reinterpret_cast<const uint8_t*>(source(a));
+                    const uint8_t* row = base + off * 2;
+                    const uint8_t* first = row - (reinterpret_cast<uintptr_t>(row) & 15);
+                    const int pieces = static_cast<int>((row + H2 - first + 15) >> 4);
+                    const uint8_t* end = base + static_cast<size_t>(p.T_max) * H2;
+                    for (int k = grp.lane(); k < pieces; k += grp.th()) {
+                        const uint8_t* c = first + k * 16;
+                        if (c < base) {
+                            for (int i = 0; i < 8; ++i)
+                                if (c + 2 * i >= base && c + 2 * i < end)
+                                    *reinterpret_cast<uint16_t*>(mine + (buf * A + a) * row_b + k * 16 + 2 * i) =
+                                        *reinterpret_cast<const uint16_t*>(c + 2 * i);
+                        } else {
+                            cp_async16_part(dst + a * row_b + k * 16, c, end - c < 16 ? static_cast<int>(end - c) : 16);
+                        }
+                    }
+                }
             }
         }
         cp_async_commit();
@@ -468,18 +498,17 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) norm_bwd_staged_kernel(const
     int buf = 0;
     const int t0 = blockIdx.x * grp.groups() + grp.id(), step = gridDim.x * grp.groups();
     stage(t0, 0);
-    // the parameters, 1 for a missing gamma_post (every group copies them all for itself
-    // to read: the same values)
+    // the parameters, 1 for a missing gamma_post; every thread reads back what it wrote
+    // (the groups write the same)
+#pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int c = j ? c1 : c0;
-        if (c < H) {
-            *reinterpret_cast<uint4*>(par + c * 2) = post ? *reinterpret_cast<const uint4*>(p.gamma_post + c)
-                : make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-            *reinterpret_cast<uint4*>(par + H2 + c * 2) = *reinterpret_cast<const uint4*>(p.gamma_pre + c);
-            if (GK == kGChannel)
-                *reinterpret_cast<uint4*>(par + 2 * H2 + c * 2) =
-                    *reinterpret_cast<const uint4*>(static_cast<const bf16*>(p.gate) + c);
-        }
+        auto put = [&](int a, const bf16* src) {
+            const Vec8 v = src ? load8<VEC>(src, grp, j, H) : Vec8{{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u}};
+            *reinterpret_cast<uint4*>(par + a * par_b + j * grp.th() * 16) = make_uint4(v.u[0], v.u[1], v.u[2], v.u[3]);
+        };
+        put(0, p.gamma_post);
+        put(1, p.gamma_pre);
+        if (GK == kGChannel) put(2, static_cast<const bf16*>(p.gate));
     }
     float2 a_post[V][4], a_pre[V][4], a_gate[V][4];
 #pragma unroll
@@ -490,9 +519,32 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) norm_bwd_staged_kernel(const
     for (int t = t0; t < T; t += step, buf ^= 1) {
         stage(t + step, buf ^ 1);  // this thread has read that buffer's last row
         cp_async_wait<1>();
-        const uint8_t* rows = mine + buf * A * H2;
-        auto get = [&](const uint8_t* base, int j) -> uint4 {  // zeros past H
-            return (j ? in1 : in0) ? *reinterpret_cast<const uint4*>(base + (j ? c1 : c0) * 2) : make_uint4(0, 0, 0, 0);
+        if (!VEC) grp.sync();  // the other threads' pieces
+        const uint8_t* rows = mine + buf * A * row_b;
+        const size_t off = static_cast<size_t>(t) * H;
+        auto get = [&](int a, int j) -> uint4 {  // vector j of staged row a; zeros past H
+            if (VEC) return (j ? in1 : in0) ? *reinterpret_cast<const uint4*>(rows + a * row_b + (j ? c1 : c0) * 2) : make_uint4(0, 0, 0, 0);
+            const uint16_t* r = reinterpret_cast<const uint16_t*>(rows + a * row_b + (reinterpret_cast<uintptr_t>(source(a) + off) & 15));
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int lo = grp.template col<VEC>(j, 2 * i), hi = grp.template col<VEC>(j, 2 * i + 1);
+                w[i] = (lo < H ? r[lo] : 0u) | (hi < H ? static_cast<uint32_t>(r[hi]) << 16 : 0u);
+            }
+            return make_uint4(w[0], w[1], w[2], w[3]);
+        };
+        auto param = [&](int a, int j) -> uint4 { return *reinterpret_cast<const uint4*>(par + a * par_b + j * grp.th() * 16); };
+        auto put_row = [&](bf16* to, int j, const uint32_t (&w)[4]) {
+            if (VEC) {
+                if (j ? in1 : in0) *reinterpret_cast<uint4*>(to + off + (j ? c1 : c0)) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+                uint16_t* o = reinterpret_cast<uint16_t*>(to + off);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int c = grp.template col<VEC>(j, i);
+                    if (c < H) o[c] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+                }
+            }
         };
         auto word = [](const uint4& v, int i) -> uint32_t { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; };
         const float gs = p.scale * (GK == kGScalar && p.gate ? static_cast<const float*>(p.gate)[t] : 1.0f);
@@ -500,7 +552,7 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) norm_bwd_staged_kernel(const
         float2 ss = both(0.0f);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const uint4 y = get(rows + H2, j);
+            const uint4 y = get(1, j);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 u[j][i] = unpack2(word(y, i));
@@ -511,8 +563,8 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) norm_bwd_staged_kernel(const
         float2 zz = both(0.0f), ez = both(0.0f);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const uint4 x = get(rows, j), dh = get(rows + 3 * H2, j), gp = get(par, j), gr = get(par + H2, j);
-            const uint4 g = GK == kGFull ? get(rows + 4 * H2, j) : GK == kGChannel ? get(par + 2 * H2, j) : uint4{};
+            const uint4 x = get(0, j), dh = get(3, j), gp = param(0, j), gr = param(1, j);
+            const uint4 g = GK == kGFull ? get(4, j) : GK == kGChannel ? param(2, j) : uint4{};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 u[j][i] = __fmul2_rn(u[j][i], both(ry));
@@ -527,12 +579,11 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) norm_bwd_staged_kernel(const
         const float2 za = row_sum2(make_float2(zz.x + zz.y, ez.x + ez.y), red, red2, grp, n_sums);
         const float rz = inv_rms(za.x, p.inv_H, p.eps);
         const float k2 = za.y * p.inv_H * rz * rz * rz;
-        const size_t off = static_cast<size_t>(t) * H;
         float2 bu = both(0.0f), gt = both(0.0f);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const uint4 dz = get(rows + 2 * H2, j), dh = get(rows + 3 * H2, j), gp = get(par, j), gr = get(par + H2, j);
-            const uint4 g = GK == kGFull ? get(rows + 4 * H2, j) : GK == kGChannel ? get(par + 2 * H2, j) : uint4{};
+            const uint4 dz = get(2, j), dh = get(3, j), gp = param(0, j), gr = param(1, j);
+            const uint4 g = GK == kGFull ? get(4, j) : GK == kGChannel ? param(2, j) : uint4{};
             uint32_t odx[4], odg[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -554,11 +605,8 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) norm_bwd_staged_kernel(const
                 z[j][i] = __fmul2_rn(__fmul2_rn(q, gp2), D);  // b
                 bu = __ffma2_rn(z[j][i], u[j][i], bu);
             }
-            if (j ? in1 : in0) {
-                *reinterpret_cast<uint4*>(p.dx + off + (j ? c1 : c0)) = make_uint4(odx[0], odx[1], odx[2], odx[3]);
-                if (GK == kGFull && p.d_gate_full)
-                    *reinterpret_cast<uint4*>(p.d_gate_full + off + (j ? c1 : c0)) = make_uint4(odg[0], odg[1], odg[2], odg[3]);
-            }
+            put_row(p.dx, j, odx);
+            if (GK == kGFull && p.d_gate_full) put_row(p.d_gate_full, j, odg);
         }
         float m = 0.0f;
         if (post || p.d_gate_token) {
@@ -574,11 +622,12 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) norm_bwd_staged_kernel(const
                 const float2 v = __fmul2_rn(__ffma2_rn(u[j][i], both(-m), z[j][i]), both(ry));
                 o[i] = pack_bf16(v.x, v.y);
             }
-            if (j ? in1 : in0) *reinterpret_cast<uint4*>(p.dy + off + (j ? c1 : c0)) = make_uint4(o[0], o[1], o[2], o[3]);
+            put_row(p.dy, j, o);
         }
+        if (!VEC) grp.sync();  // this buffer is copied to again
     }
     cp_async_wait<0>();
-    store_part<true>(p, grp, reinterpret_cast<float*>(dyn), [&](int arr, int j, int i) {
+    store_part<VEC>(p, grp, reinterpret_cast<float*>(dyn), [&](int arr, int j, int i) {
         const float2 v = arr == 0 ? a_post[j][i >> 1] : arr == 1 ? a_pre[j][i >> 1] : a_gate[j][i >> 1];
         return (i & 1 ? v.y : v.x) * (arr == 2 ? p.scale : 1.0f);
     });
@@ -702,25 +751,26 @@ cudaError_t launch_bwd_rows(SmemOptIn& opt, K kernel, const NormArgs& a, const N
     return api_launch(kernel, n, th, staged > merge ? staged : merge, l.stream, a);
 }
 
-template <int GK>
+template <bool VEC, int GK>
 cudaError_t launch_bwd_staged(const NormArgs& a, RowMode mode, const NormLaunch& l) {
     static SmemOptIn opt[4];
     constexpr int A = GK == kGFull ? 5 : 4;
-    const int row = 2 * A * a.H * 2, par = (GK == kGChannel ? 3 : 2) * a.H * 2;  // 197 KB at most
-    if (mode == kRowsWarp) return launch_bwd_rows(opt[0], norm_bwd_staged_kernel<GK, kRowsWarp, 256>, a, l, row, par);
-    if (mode == kRowsGroup) return launch_bwd_rows(opt[1], norm_bwd_staged_kernel<GK, kRowsGroup, 256>, a, l, row, par);
-    if (a.row_threads <= 256) return launch_bwd_rows(opt[2], norm_bwd_staged_kernel<GK, kRowsOne, 256>, a, l, row, par);
-    return launch_bwd_rows(opt[3], norm_bwd_staged_kernel<GK, kRowsOne, 512>, a, l, row, par);
+    const int row = 2 * A * norm_row_bytes(a.H, VEC);                        // 197 KB at most,
+    const int par = (GK == kGChannel ? 3 : 2) * a.row_threads * norm_v(mode) * 16;  // with these
+    if (mode == kRowsWarp) return launch_bwd_rows(opt[0], norm_bwd_staged_kernel<VEC, GK, kRowsWarp, 256>, a, l, row, par);
+    if (mode == kRowsGroup) return launch_bwd_rows(opt[1], norm_bwd_staged_kernel<VEC, GK, kRowsGroup, 256>, a, l, row, par);
+    if (a.row_threads <= 256) return launch_bwd_rows(opt[2], norm_bwd_staged_kernel<VEC, GK, kRowsOne, 256>, a, l, row, par);
+    return launch_bwd_rows(opt[3], norm_bwd_staged_kernel<VEC, GK, kRowsOne, 512>, a, l, row, par);
 }
 
 template <bool VEC>
 cudaError_t launch_bwd(NormArgs a, const NormLaunch& l) {
     a.row_threads = norm_threads(a.H);
     const RowMode mode = norm_mode(a.H, a.row_threads);
-    if (VEC && a.row_threads <= 512 && a.y && a.gamma_pre && a.d_x_out && a.d_x_hat) {
-        if (a.gate_kind == kGateFull) return launch_bwd_staged<kGFull>(a, mode, l);
-        if (a.gate_kind == kGateChannel) return launch_bwd_staged<kGChannel>(a, mode, l);
-        return launch_bwd_staged<kGScalar>(a, mode, l);
+    if (a.row_threads <= 512 && a.y && a.gamma_pre && a.d_x_out && a.d_x_hat) {
+        if (a.gate_kind == kGateFull) return launch_bwd_staged<VEC, kGFull>(a, mode, l);
+        if (a.gate_kind == kGateChannel) return launch_bwd_staged<VEC, kGChannel>(a, mode, l);
+        return launch_bwd_staged<VEC, kGScalar>(a, mode, l);
     }
     static SmemOptIn opt[5];
     if (mode == kRowsWarp) return launch_bwd_rows(opt[0], norm_bwd_kernel<VEC, kRowsWarp, 256>, a, l, 0, 0);
