@@ -408,7 +408,7 @@ __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, in
 //              the sum over splits and CTAs is the layer's output.
 template <int MODE, int NT, int G>
 struct W4Shape {
-    static constexpr int RW = NT == 1 ? 1 : NT == 2 ? 2 : 4;  // row groups
+    static constexpr int RW = NT;             // row groups
     static constexpr int KW = kW4Warps / RW;                  // splits of the inputs
     static constexpr int kTile = RW * kW4Rows;                // weight rows of a CTA
     static constexpr int kOut = MODE == kW4GateUp ? kTile / 2 : kTile;
@@ -887,40 +887,64 @@ int w4_fit(W4Fit& f, K kernel, int c, int n) {
     return v;
 }
 
+// How a call is spread over the GPU.
+struct W4Plan {
+    long long units;
+    int c, per_sm, smem;  // CTAs that share a unit, CTAs an SM, dynamic shared memory of one
+    long long cost;       // estimated ns (kW4Gemv)
+};
+
+template <int MODE, int NT, int G>
+W4Fit& w4_fits() {
+    static W4Fit fits;
+    return fits;
+}
+
 // `rows` tokens at most; x_rows <= 8 NT of them (or of an expert's rows) a pass.
 template <int MODE, int NT, int G>
-int w4_launch(W4Args a, int rows, int x_rows, int dev, int sms, void* stream) {
+int w4_plan(const W4Args& a, int rows, int x_rows, int dev, int sms, W4Plan* pl) {
     using S = W4Shape<MODE, NT, G>;
-    a.x_rows = x_rows;
-    a.sum_rows = MODE == kW4Down ? rows : x_rows;
-    a.magic = 0x43004300u;
     // segments of a call: each has a row, an expert has one and one more for each full pass
     const int R = rows * a.k, experts = R < a.E ? R : a.E;
     const int segs = experts + R / x_rows < R ? experts + R / x_rows : R;
     const long long tiles = (a.N + S::kOut - 1) / S::kOut;
     const long long units = tiles * (MODE == kW4Down ? 1 : MODE == kW4GateUp ? segs : (rows + x_rows - 1) / x_rows);
-    const long long blocks = static_cast<long long>((a.K + kW4Blk - 1) / kW4Blk) * (MODE == kW4Down ? segs : 1);
+    const int KB = (a.K + kW4Blk - 1) / kW4Blk;
+    const long long blocks = static_cast<long long>(KB) * (MODE == kW4Down ? segs : 1);
     const int routing = MODE == kW4Gemv ? 0 : W4Routing::bytes(a.T_max * a.k, a.E);
-    int smem = S::ring_bytes(x_rows) + kW4Warps * a.sum_rows * kW4Pad * 4 + routing;
+    const int sum_rows = MODE == kW4Down ? rows : x_rows;
+    const int smem = S::ring_bytes(x_rows) + kW4Warps * sum_rows * kW4Pad * 4 + routing;
     if (smem > kSmemLimit) return api_fail(ET_ERR_UNSUPPORTED, "rows do not fit in shared memory");
     static SmemOptIn opt;
-    cudaError_t e = api_smem_opt_in(opt, dev, w4_kernel<MODE, NT, G>, kSmemLimit);
+    const cudaError_t e = api_smem_opt_in(opt, dev, w4_kernel<MODE, NT, G>, kSmemLimit);
     if (e != cudaSuccess) return api_fail_cuda(e, "cudaFuncSetAttribute(4-bit products)");
     static const int regs = [] {
         cudaFuncAttributes at{};
         return cudaFuncGetAttributes(&at, w4_kernel<MODE, NT, G>) == cudaSuccess ? at.numRegs : 255;
     }();
-    const int threads = kW4Warps * 32;
-    const int by_smem = kSmemSm / (smem + 1024), by_regs = 65536 / (threads * ((regs + 7) / 8 * 8));
-    const int per_sm = by_smem < by_regs ? by_smem : by_regs;  // CTAs an SM
-    static W4Fit fits;
-    // CTAs that share a unit's inputs: 8, 4 or 2 if all of them fit at once and every
-    // split keeps two k-blocks
+    const int by_smem = kSmemSm / (smem + 1024), by_regs = 65536 / (kW4Warps * 32 * ((regs + 7) / 8 * 8));
+    const int per_sm = by_smem < by_regs ? by_smem : by_regs;
+    // 8, 4 or 2 CTAs share a unit's inputs if all of them fit at once and every split
+    // keeps two k-blocks
     int c = kW4ClusterMax;
-    while (c > 1 && (blocks < 2ll * S::KW * c || units > w4_fit(fits, w4_kernel<MODE, NT, G>, c, per_sm))) c /= 2;
-    const long long fit = static_cast<long long>(sms) * per_sm;
-    const bool in_turn = MODE != kW4Down && c == 1 && units > fit;  // CTAs take several units
-    const long long grid = in_turn ? fit : units * c;
+    while (c > 1 && (blocks < 2ll * S::KW * c || units > w4_fit(w4_fits<MODE, NT, G>(), w4_kernel<MODE, NT, G>, c, per_sm)))
+        c /= 2;
+    // the k-blocks of a warp of the busiest SM, its CTAs taken one after the other.  On 108
+    // calls (9 to 64 rows, 768 x 2048 to 28672 x 8192) the estimate was within 10 % of the
+    // measured time in six of seven; the faster side was taken in 98, and 14 % lost at most.
+    const long long items = (units * c + sms - 1) / sms * ((KB + c * S::KW - 1) / (c * S::KW));
+    *pl = {units, c, per_sm, smem, NT == 1 ? 3600 + 480 * items : 5000 + 670 * items};
+    return ET_OK;
+}
+
+template <int MODE, int NT, int G>
+int w4_launch(W4Args a, int rows, int x_rows, const W4Plan& pl, int sms, void* stream) {
+    a.x_rows = x_rows;
+    a.sum_rows = MODE == kW4Down ? rows : x_rows;
+    a.magic = 0x43004300u;
+    const long long fit = static_cast<long long>(sms) * pl.per_sm;
+    const bool in_turn = MODE != kW4Down && pl.c == 1 && pl.units > fit;  // CTAs take several units
+    const long long grid = in_turn ? fit : pl.units * pl.c;
     // Scheduled while the kernel before drains, which hides the launch (eager calls,
     // M = 1, 4096 x 14336: 14.5 -> 12.5 us).  Its CTAs then fill the places the other
     // kernel leaves, so no more of them may fit an SM than an even spread needs:
@@ -928,30 +952,45 @@ int w4_launch(W4Args a, int rows, int x_rows, int dev, int sms, void* stream) {
     // the other).  CTAs that take units in turn are launched after the other: they
     // fill the GPU, and started early they lost 1 to 5 % (Mixtral-shaped, T = 4).
     const bool early = !in_turn;
+    int smem = pl.smem;
     if (early) {
+        W4Fit& fits = w4_fits<MODE, NT, G>();
         int n = static_cast<int>((grid + sms - 1) / sms);
-        while (n < per_sm && w4_fit(fits, w4_kernel<MODE, NT, G>, c, n) * static_cast<long long>(c) < grid) ++n;
+        while (n < pl.per_sm && w4_fit(fits, w4_kernel<MODE, NT, G>, pl.c, n) * static_cast<long long>(pl.c) < grid) ++n;
         const int more = kSmemSm / (n + 1) / 128 * 128 - 1024 + 128;  // n + 1 do not fit
         smem = smem > more ? smem : more < kSmemLimit ? more : kSmemLimit;
     }
-    e = api_launch_cluster(w4_kernel<MODE, NT, G>, dim3(static_cast<unsigned>(grid)), threads, c, early,
-                           smem, stream, a);
+    const cudaError_t e = api_launch_cluster(w4_kernel<MODE, NT, G>, dim3(static_cast<unsigned>(grid)), kW4Warps * 32,
+                                             pl.c, early, smem, stream, a);
     if (e != cudaSuccess) return api_fail_cuda(e, "launch of the 4-bit product kernel");
     return ET_OK;
 }
 
+// kW4Gemv with 9 rows or more: 8 a pass (one tile of columns in every product) or 16
+// (two), whichever is estimated to end first.  Half the passes over the weights mean
+// half the unpacking, and win where there is much to do: 28672 x 8192, M = 16 36.6 us
+// against 50.4; twice the CTAs win where an SM would stay empty: 14336 x 4096, M = 16
+// 14.8 us against 16.8, 2048 x 2048 4.3 against 5.5.  (32 a pass, a fourth of the
+// splits, lost nearly everywhere: M = 32, 4096 x 14336 38.3 us against 25.0.)
 template <int MODE, int G>
-int w4_launch_nt(const W4Args& a, int rows, int x_rows, int dev, int sms, void* stream) {
-    if (x_rows <= 8) return w4_launch<MODE, 1, G>(a, rows, x_rows, dev, sms, stream);
-    if (x_rows <= 16) return w4_launch<MODE, 2, G>(a, rows, x_rows, dev, sms, stream);
-    return w4_launch<MODE, 4, G>(a, rows, x_rows, dev, sms, stream);
+int w4_launch_rows(const W4Args& a, int rows, int x_rows, int dev, int sms, void* stream) {
+    W4Plan one{}, two{};
+    int rc = ET_OK;
+    const int one_rows = x_rows < 8 ? x_rows : 8, two_rows = x_rows < 16 ? x_rows : 16;
+    if (MODE == kW4Gemv || x_rows <= 8)
+        if ((rc = w4_plan<MODE, 1, G>(a, rows, one_rows, dev, sms, &one))) return rc;
+    if (x_rows > 8)
+        if ((rc = w4_plan<MODE, 2, G>(a, rows, two_rows, dev, sms, &two))) return rc;
+    if (x_rows <= 8 || (MODE == kW4Gemv && one.cost <= two.cost))
+        return w4_launch<MODE, 1, G>(a, rows, one_rows, one, sms, stream);
+    return w4_launch<MODE, 2, G>(a, rows, two_rows, two, sms, stream);
 }
 
 template <int MODE>
 int w4_launch_group(const W4Args& a, int group, int rows, int x_rows, int dev, int sms, void* stream) {
-    if (group == 32) return w4_launch_nt<MODE, 32>(a, rows, x_rows, dev, sms, stream);
-    if (group == 64) return w4_launch_nt<MODE, 64>(a, rows, x_rows, dev, sms, stream);
-    return w4_launch_nt<MODE, 128>(a, rows, x_rows, dev, sms, stream);
+    if (group == 32) return w4_launch_rows<MODE, 32>(a, rows, x_rows, dev, sms, stream);
+    if (group == 64) return w4_launch_rows<MODE, 64>(a, rows, x_rows, dev, sms, stream);
+    return w4_launch_rows<MODE, 128>(a, rows, x_rows, dev, sms, stream);
 }
 
 int w4_conv_check(int E, int N, int K, int group) {
@@ -1078,7 +1117,7 @@ int et_w4_gemv(const void* X, const void* q, const void* scale, void* Y, int M, 
         a.k = 1;
         a.hdr = static_cast<EtHeader*>(workspace);
         const int rows = d_M ? M_max : M;
-        return w4_launch_group<kW4Gemv>(a, group, rows, rows < 32 ? rows : 32, dev, sms, stream);
+        return w4_launch_group<kW4Gemv>(a, group, rows, rows, dev, sms, stream);
     });
 }
 
@@ -1133,9 +1172,14 @@ int et_w4_experts(const void* x, const int32_t* topk_idx, const float* topk_w, c
         a.k = k;
         a.hdr = reinterpret_cast<EtHeader*>(ws);
         const int rows = d_T ? T_max : T, R = rows * k;
-        // a pass takes twice the rows an expert has on average: 4, 8, 16 or 32
-        const int avg2 = 2 * ((R + E - 1) / E);
-        int width = avg2 <= 4 ? 4 : avg2 <= 8 ? 8 : avg2 <= 16 ? 16 : 32;
+        // Rows a pass takes, 4, 8 or 16, by the rows an expert has on average.  More save passes
+        // over experts with many, and cost shared memory (CTAs an SM) and, from 9 on, a second
+        // tile of columns in every product; long sums (H) repay that sooner.  Microseconds with
+        // 4 and 8 rows at an average of 2: E 8, 4096 x 14336 177 and 161, E 32, 2048 x 768 28 and
+        // 31; with 8 and 16 at 8: 267 and 217, 45 and 46; at 16: 485 and 360, 71 and 79.
+        const int avg = (R + E - 1) / E;
+        const bool deep = H >= 4096;
+        int width = avg <= (deep ? 1 : 2) ? 4 : avg < 8 || !deep ? 8 : 16;
         width = rows < width ? rows : width;
         if ((rc = w4_launch_group<kW4GateUp>(a, group, rows, width, dev, sms, stream))) return rc;
         W4Args b = a;
