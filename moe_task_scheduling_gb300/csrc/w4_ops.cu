@@ -929,11 +929,15 @@ int w4_plan(const W4Args& a, int rows, int x_rows, int dev, int sms, W4Plan* pl)
     int c = kW4ClusterMax;
     while (c > 1 && (blocks < 2ll * S::KW * c || units > w4_fit(w4_fits<MODE, NT, G>(), w4_kernel<MODE, NT, G>, c, per_sm)))
         c /= 2;
-    // the k-blocks of a warp of the busiest SM, its CTAs taken one after the other.  On 108
-    // calls (9 to 64 rows, 768 x 2048 to 28672 x 8192) the estimate was within 10 % of the
-    // measured time in six of seven; the faster side was taken in 98, and 14 % lost at most.
-    const long long items = (units * c + sms - 1) / sms * ((KB + c * S::KW - 1) / (c * S::KW));
-    *pl = {units, c, per_sm, smem, NT == 1 ? 3600 + 480 * items : 5000 + 670 * items};
+    // The k-blocks of a warp of the busiest SM, its CTAs taken one after the other.  On 108
+    // calls (9 to 64 rows, 768 x 2048 to 28672 x 8192) the estimate below was within 10 % of
+    // the measured time in six of seven; the faster side was taken in 98, and 14 % lost at
+    // most.  A smaller cluster that evens the SMs' shares is taken too: 4096 x 14336, M = 1
+    // with 8 CTAs (4 on some SMs, 3 on others) 11.3 us, with 4 (2 on most) 10.8.
+    const auto items = [&](int n) { return (units * n + sms - 1) / sms * ((KB + n * S::KW - 1) / (n * S::KW)); };
+    if (MODE == kW4Gemv)
+        while (c > 1 && items(c / 2) < items(c)) c /= 2;
+    *pl = {units, c, per_sm, smem, NT == 1 ? 3600 + 480 * items(c) : 5000 + 670 * items(c)};
     return ET_OK;
 }
 
