@@ -44,6 +44,10 @@
  * Supported shapes: H and F multiples of 128; 1 <= k <= min(E, 8);
  * 1 <= E <= 256; 0 <= T <= T_max.  Anything else returns ET_ERR_UNSUPPORTED
  * or ET_ERR_INVALID.  T == 0 launches nothing and leaves `out` untouched.
+ * The router, norm and 4-bit calls state their own shapes.  One workspace may
+ * serve several of those three, one call after the other, if it has the bytes
+ * of the largest; it must not serve the other calls too, whose counters would
+ * lie under their data.
  */
 #ifndef ETMOE_H
 #define ETMOE_H
@@ -332,8 +336,8 @@ int et_mlp_chain(const void* x, const void* gamma, float eps, const void* w_gate
  *
  * All of it fp32; sums over tokens run in a fixed order, so the results are
  * the same bits on every run.  With n == 0 the losses and probabilities are 0.
- * A NaN logit ranks above all others and makes the token's weights, and the
- * losses, NaN.  The losses are in logits alone: counts carries no gradient.
+ * A NaN logit ranks above all others; it makes the token's weights and the
+ * losses NaN, as +inf does.  The losses are in logits alone: counts carries no gradient.
  *
  * The gradient (et_router_topk_bwd), for d_losses fp32 [2] (NULL: 0) and
  * d_topk_w fp32 [T,k] (NULL: 0; read only where idx is not -1):
@@ -437,8 +441,9 @@ int et_block_norm_bwd(const void* x, const void* y, const void* gamma_post, cons
  * may name an expert twice.  1 <= T_max <= 64, 1 <= E <= 256, 1 <= k <=
  * min(E, 8); H and F are inputs and outputs in turn: multiples of group.
  *
- * Products are exact and summed in fp32; a group's sum of (q - 8) x is formed
- * before it is scaled and has to be finite in fp32.  The results are the same
+ * Products are exact and summed in fp32.  A group's sum is formed before it is
+ * scaled, as sum (q + 128) x - 136 sum x: the sum of 143 |x| over a group has
+ * to be finite in fp32.  The results are the same
  * bits on every run of a shape.  M, d_M, T and d_T as in et_splitk_gemm and
  * et_moe_layer.  Errors as et_moe_layer.
  * ---------------------------------------------------------------------- */

@@ -151,6 +151,31 @@ def test_other_alignment(cuda_lib, offset):
         _run_case(cuda_lib, 9, H, "full", True, True, True, 1.0, seed=7, offset=offset)
 
 
+@pytest.mark.parametrize("T,H,offset", [(4000, 33, 0), (1500, 1001, 0), (1500, 1001, 1), (1500, 1000, 3), (700, 4099, 5)])
+@pytest.mark.parametrize("gate", ["token", "channel", "full"])
+def test_many_rows_off_alignment(cuda_lib, T, H, offset, gate):
+    """Rows of odd width, or that start off a 16-byte boundary, with several for each thread group to take in turn."""
+    _run_case(cuda_lib, T, H, gate, True, True, True, 0.5, seed=H, offset=offset)
+
+
+@pytest.mark.parametrize("H", [129, 1001])
+def test_in_place_off_alignment(cuda_lib, H):
+    """dx over d_x_out and dy over y where rows share 16-byte pieces with their neighbours."""
+    T = 1200
+    d = _inputs(T, H, "full", True, True, True, 4)
+    ws = cuda_lib.alloc_workspace(cuda_lib.et_block_norm_workspace_bytes(T, H))
+    kw = dict(gamma_post=d["gamma_post"], gate=d["gate"], scale=0.7, gamma_pre=d["gamma_pre"], eps=EPS, workspace=ws)
+    res = []
+    for place in (False, True, True):
+        y2, dz2 = d["y"].clone(), d["d_x_out"].clone()
+        dx, dy = (dz2, y2) if place else (torch.empty_like(y2), torch.empty_like(y2))
+        dg, dgf = torch.empty(H, device="cuda"), torch.empty_like(y2)
+        cuda_lib.et_block_norm_bwd(d["x"], y2, dz2, d["d_x_hat"], dx, dy, d_gamma_post=dg, d_gate=dgf, **kw)
+        res.append((dx, dy, dg, dgf))
+    for got in res[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got, res[0]))
+
+
 def test_one_gradient_missing(cuda_lib):
     """No gradient into x_out, or none into x_hat."""
     T, H = 9, 320

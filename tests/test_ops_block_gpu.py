@@ -111,6 +111,38 @@ def test_decoding_block(cuda_lib):
         b.check(T)
 
 
+def test_one_workspace_for_all(cuda_lib):
+    """The router, norm and 4-bit calls may share one workspace, one call after the other."""
+    E = cuda_lib
+    b = Block(E, 12, 256, 384, 16, 4, 64, 1)
+    b.x.copy_(_rn(_gen(2), 12, 256))
+    T, H, En, k = 3000, 520, 64, 4
+    g = _gen(6)
+    x, y, dz, dh = (_rn(g, T, H) for _ in range(4))
+    gam = _rn(g, H, mean=1.0, std=0.1)
+    L = torch.randn(T, En, generator=g, device="cuda")
+    sizes = (E.et_block_norm_workspace_bytes(T, H), E.et_router_topk_workspace_bytes(T, En, k), b.wse.numel())
+
+    def step(wsn, wsr):
+        dx, dy = torch.empty_like(x), torch.empty_like(x)
+        dg = torch.empty(H, device="cuda")
+        idx, w = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+        losses = torch.empty(2, device="cuda")
+        b.run()
+        E.et_router_topk(L, idx, w, losses=losses, workspace=wsr)
+        b.run()
+        E.et_block_norm_bwd(x, y, dz, dh, dx, dy, gamma_post=gam, gamma_pre=gam, eps=EPS, d_gamma_pre=dg, workspace=wsn)
+        E.et_router_topk(L, idx, w, losses=losses, workspace=wsr)
+        return b.out.clone(), b.y.clone(), b.losses.clone(), dx, dy, dg, idx, w, losses
+
+    want = step(E.alloc_workspace(sizes[0]), E.alloc_workspace(sizes[1]))
+    one = E.alloc_workspace(max(sizes))
+    b.wsn = b.wsr = b.wse = one
+    for _ in range(3):
+        assert all(torch.equal(a, c) for a, c in zip(step(one, one), want))
+    assert E.et_status(one) == (0, 0)
+
+
 def test_two_blocks_on_two_streams(cuda_lib):
     """Two blocks at once, each with its own workspaces, give what they give alone."""
     bs = [Block(cuda_lib, 5, 128, 256, 8, 2, 32, s) for s in (11, 12)]

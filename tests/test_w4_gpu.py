@@ -62,6 +62,32 @@ def test_gemv(cuda_lib, N, K, group):
     assert (_gemv(cuda_lib, x, qc, sc)[0] == 0).all()
 
 
+@pytest.mark.parametrize("M,N,K,group", [(16, 6144, 4096, 64), (11, 6144, 4096, 128), (33, 2120, 7168, 32), (64, 2120, 7168, 128),
+                                         (50, 3000, 8192, 64)])
+def test_gemv_many_rows_of_large_weights(cuda_lib, M, N, K, group):
+    """Passes of sixteen rows, the last of them ragged."""
+    q, s = _weight((N, K), group, N + M)
+    qc, sc = _cuda(q, s)
+    x = torch.randn(M, K, generator=_gen(M)).to(BF).cuda()
+    y, ws = _gemv(cuda_lib, x, qc, sc)
+    _check_gemv(y, x, q, s)
+    assert torch.equal(y, _gemv(cuda_lib, x, qc, sc, ws=ws)[0])
+    y, _ = _gemv(cuda_lib, x, qc, sc, d_M=torch.full((1,), M - 5, dtype=torch.int32, device="cuda"), ws=ws)
+    _check_gemv(y, x, q, s, M - 5)
+
+
+@pytest.mark.parametrize("T,H,F,En,k,group", [(64, 4096, 128, 4, 1, 128), (33, 4096, 320, 6, 2, 64), (64, 4128, 96, 2, 2, 32)])
+def test_experts_with_many_rows_and_long_sums(cuda_lib, T, H, F, En, k, group):
+    """Experts with more rows than a pass of sixteen takes, and with fewer."""
+    a = _experts_inputs(T, H, F, En, k, group, T + H)
+    out, ws = _experts(cuda_lib, *a)
+    _check_experts(out, *a)
+    dT = torch.full((1,), 9, dtype=torch.int32, device="cuda")
+    out, _ = _experts(cuda_lib, *a, d_T=dT, ws=ws)
+    _check_experts(out, *a, T=9)
+    assert cuda_lib.et_status(ws) == (0, 0)
+
+
 def test_gemv_device_count(cuda_lib):
     N, K = 264, 640
     q, s = _weight((N, K), 64, 1)
