@@ -16,7 +16,8 @@ namespace {
 
 constexpr int kW4Rows = 64;        // weight rows of a warp (gate/up: 32 of each)
 constexpr int kW4Blk = 128;        // inputs of a stage: 64 bytes of a row
-constexpr int kW4Warps = 4;
+constexpr int kW4Warps = 4;        // of a CTA; the down kernel takes twice as many where that evens its spread
+constexpr int kW4WarpsMax = 8;
 constexpr int kW4Stages = 2;       // k-blocks of a ring: three or four gained nothing (the unpacking, not
                                    // the memory, sets the pace) and took room from other CTAs
 constexpr int kW4RowsMax = 64;     // most rows of x (tokens)
@@ -212,20 +213,21 @@ struct W4Routing {
     int16_t* seg_r;     // [R] its first entry in `order`,
     int16_t* seg_n;     // [R] its rows
     int16_t* e;         // [R] row -> expert (-1: none)
-    int16_t* cnt;       // [4][E'] rows of an expert in a warp's share, then their first entry
-    int* shared;        // [6]: scan totals, n_seg, whether a token names an expert twice
+    int16_t* cnt;       // [W][E'] rows of an expert in a warp's share, then their first entry
+    int* shared;        // [W + 2]: scan totals, n_seg, whether a token names an expert twice
     int Ep;             // E rounded up to even
     int n_seg, twice;
 
-    __host__ __device__ static int bytes(int R, int E) {
-        return (R * 16 + kW4Warps * ((E + 1) & ~1) * 2 + 24 + 127) / 128 * 128;
+    __host__ __device__ static int bytes(int R, int E, int W) {
+        return (R * 16 + W * ((E + 1) & ~1) * 2 + (W + 2) * 4 + 127) / 128 * 128;
     }
+    template <int W>
     __device__ __forceinline__ void place(uint8_t* at, int R, int E) {
         wt = reinterpret_cast<float*>(at);
         shared = reinterpret_cast<int*>(wt + R);
-        cnt = reinterpret_cast<int16_t*>(shared + 6);
+        cnt = reinterpret_cast<int16_t*>(shared + W + 2);
         Ep = (E + 1) & ~1;
-        order = cnt + kW4Warps * Ep;
+        order = cnt + W * Ep;
         tok = order + R;
         seg_e = tok + R;
         seg_r = seg_e + R;
@@ -238,6 +240,7 @@ static_assert(kW4RoutedMax <= kW4Warps * 128, "four rows a thread");
 
 // Up to 32 rows (decoding): one warp, experts in the order of their first row,
 // one barrier.  More: all warps, experts ascending.
+template <int W>
 __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, int T, int width) {
     const int R = T * p.k, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (R <= 32) {
@@ -281,16 +284,16 @@ __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, in
             }
             again = __any_sync(0xffffffffu, again);
             if (lane == 31) {
-                rt.shared[4] = inc >> 16;
-                rt.shared[5] = again;
+                rt.shared[W] = inc >> 16;
+                rt.shared[W + 1] = again;
             }
         }
         __syncthreads();
-        rt.n_seg = rt.shared[4];
-        rt.twice = rt.shared[5];
+        rt.n_seg = rt.shared[W];
+        rt.twice = rt.shared[W + 1];
         return;
     }
-    const int span = (R + kW4Warps * 32 - 1) / (kW4Warps * 32) * 32;  // consecutive rows of a warp
+    const int span = (R + W * 32 - 1) / (W * 32) * 32;  // consecutive rows of a warp
     int e[4], at[4];
     float wt[4];
 #pragma unroll
@@ -300,8 +303,8 @@ __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, in
         e[i] = in ? p.idx[r] : -1;
         wt[i] = in ? p.w[r] : 0.0f;
     }
-    for (int i = tid; i < kW4Warps * rt.Ep / 2; i += blockDim.x) reinterpret_cast<int*>(rt.cnt)[i] = 0;
-    if (tid == 0) rt.shared[5] = 0;
+    for (int i = tid; i < W * rt.Ep / 2; i += blockDim.x) reinterpret_cast<int*>(rt.cnt)[i] = 0;
+    if (tid == 0) rt.shared[W + 1] = 0;
     __syncthreads();
     // a row's place among its warp's rows of that expert
     int16_t* mine = rt.cnt + warp * rt.Ep;
@@ -333,7 +336,7 @@ __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, in
         c[h] = 0;
         if (x < p.E)
 #pragma unroll
-            for (int w = 0; w < kW4Warps; ++w) c[h] += rt.cnt[w * rt.Ep + x];
+            for (int w = 0; w < W; ++w) c[h] += rt.cnt[w * rt.Ep + x];
         v[h] = c[h] | ((c[h] + width - 1) / width << 16);
         sum += v[h];
     }
@@ -350,7 +353,7 @@ __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, in
         const int r = warp * span + i * 32 + lane;
         if (i * 32 < span && r < R && e[i] >= 0)
             for (int o = r - r % p.k; o < r; ++o)
-                if (rt.e[o] == e[i]) rt.shared[5] = 1;
+                if (rt.e[o] == e[i]) rt.shared[W + 1] = 1;
     }
     __syncthreads();
     int base = inc - sum;
@@ -367,7 +370,7 @@ __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, in
                 rt.seg_n[s0] = static_cast<int16_t>(min(width, c[h] - o));
             }
 #pragma unroll
-            for (int w = 0; w < kW4Warps; ++w) {
+            for (int w = 0; w < W; ++w) {
                 const int n = rt.cnt[w * rt.Ep + x];
                 rt.cnt[w * rt.Ep + x] = static_cast<int16_t>(a);
                 a += n;
@@ -375,7 +378,7 @@ __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, in
         }
         base += v[h];
     }
-    if (tid == static_cast<int>(blockDim.x) - 1) rt.shared[4] = base >> 16;
+    if (tid == static_cast<int>(blockDim.x) - 1) rt.shared[W] = base >> 16;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -387,12 +390,12 @@ __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, in
             rt.wt[o] = wt[i];
         }
     }
-    rt.n_seg = rt.shared[4];
-    rt.twice = rt.shared[5];
+    rt.n_seg = rt.shared[W];
+    rt.twice = rt.shared[W + 1];
     __syncthreads();
 }
 
-// One CTA of four warps: RW row groups x KW = 4 / RW splits of the inputs.  The
+// One CTA of W = 4 warps (or 8): RW row groups x KW = W / RW splits of the inputs.  The
 // RW warps of a split share its x rows and meet at a named barrier once a
 // k-block; splits run on their own, each through its own ring, and the copies
 // run ahead across the units of a CTA.
@@ -406,20 +409,21 @@ __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, in
 //              (segment, k-block) over its warps; a warp adds what it has for a
 //              segment, times the gate weight, to its own fp32 rows by token, and
 //              the sum over splits and CTAs is the layer's output.
-template <int MODE, int NT, int G>
+template <int MODE, int NT, int G, int W>
 struct W4Shape {
     static constexpr int RW = NT;             // row groups
-    static constexpr int KW = kW4Warps / RW;                  // splits of the inputs
+    static constexpr int KW = W / RW;                         // splits of the inputs
     static constexpr int kTile = RW * kW4Rows;                // weight rows of a CTA
     static constexpr int kOut = MODE == kW4GateUp ? kTile / 2 : kTile;
     static constexpr int kWarpBytes = kW4Rows * 64 + (kW4Blk / G) * 128;
+    static_assert(RW == 1 || (RW == 2 && KW == 2), "two named barriers");
     static __host__ __device__ int stage_bytes(int x_rows) { return RW * kWarpBytes + x_rows * 256; }
     static __host__ __device__ int ring_bytes(int x_rows) { return KW * kW4Stages * stage_bytes(x_rows); }
 };
 
-template <int MODE, int NT, int G>
-__global__ void __launch_bounds__(kW4Warps * 32) w4_kernel(const W4Args p) {
-    using S = W4Shape<MODE, NT, G>;
+template <int MODE, int NT, int G, int W>
+__global__ void __launch_bounds__(W * 32) w4_kernel(const W4Args p) {
+    using S = W4Shape<MODE, NT, G, W>;
     constexpr bool kDown = MODE == kW4Down;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -447,8 +451,8 @@ __global__ void __launch_bounds__(kW4Warps * 32) w4_kernel(const W4Args p) {
     float* sums = reinterpret_cast<float*>(smem + S::ring_bytes(p.x_rows));
     W4Routing rt;
     if (MODE != kW4Gemv) {
-        rt.place(reinterpret_cast<uint8_t*>(sums + kW4Warps * p.sum_rows * kW4Pad), p.T_max * p.k, p.E);
-        build_routing(p, rt, T, p.x_rows);
+        rt.template place<W>(reinterpret_cast<uint8_t*>(sums + W * p.sum_rows * kW4Pad), p.T_max * p.k, p.E);
+        build_routing<W>(p, rt, T, p.x_rows);
     }
 
     // The units of this CTA (or cluster), and the items -- k-blocks -- of one unit
@@ -460,7 +464,7 @@ __global__ void __launch_bounds__(kW4Warps * 32) w4_kernel(const W4Args p) {
     const int i0 = static_cast<int>(static_cast<unsigned>(items) * split / splits);
     const int i1 = static_cast<int>(static_cast<unsigned>(items) * (split + 1) / splits);
     if (kDown) {
-        for (int i = threadIdx.x; i < kW4Warps * T * kW4Pad; i += blockDim.x) sums[i] = 0.0f;
+        for (int i = threadIdx.x; i < W * T * kW4Pad; i += blockDim.x) sums[i] = 0.0f;
         __syncthreads();
     }
     auto tile_of = [&](int u) { return kDown ? u : MODE == kW4GateUp ? u % tiles : u / passes; };
@@ -575,7 +579,6 @@ __global__ void __launch_bounds__(kW4Warps * 32) w4_kernel(const W4Args p) {
     };
     auto meet = [&]() {
         if (S::RW == 1) __syncwarp();
-        else if (S::KW == 1) __syncthreads();
         else if (kw == 0) asm volatile("bar.sync 1, 64;" ::: "memory");
         else asm volatile("bar.sync 2, 64;" ::: "memory");
     };
@@ -865,14 +868,14 @@ struct W4Fit {
     int clusters[4][33] = {};  // [log2 c][n], 0: not asked yet
 };
 template <class K>
-int w4_fit(W4Fit& f, K kernel, int c, int n) {
+int w4_fit(W4Fit& f, K kernel, int threads, int c, int n) {
     const int lc = c == 8 ? 3 : c == 4 ? 2 : c == 2 ? 1 : 0;
     n = n < 1 ? 1 : n > 32 ? 32 : n;
     int v = __atomic_load_n(&f.clusters[lc][n], __ATOMIC_RELAXED);
     if (v) return v;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(c * 1024);
-    cfg.blockDim = dim3(kW4Warps * 32);
+    cfg.blockDim = dim3(threads);
     const int smem = kSmemSm / n / 128 * 128 - 1024;
     cfg.dynamicSmemBytes = smem < kSmemLimit ? smem : kSmemLimit;
     cudaLaunchAttribute at[1];
@@ -894,16 +897,16 @@ struct W4Plan {
     long long cost;       // estimated ns (kW4Gemv)
 };
 
-template <int MODE, int NT, int G>
-W4Fit& w4_fits() {
+template <int MODE, int NT, int G, int W>
+int w4_fit(int c, int n) {
     static W4Fit fits;
-    return fits;
+    return w4_fit(fits, w4_kernel<MODE, NT, G, W>, W * 32, c, n);
 }
 
 // `rows` tokens at most; x_rows <= 8 NT of them (or of an expert's rows) a pass.
-template <int MODE, int NT, int G>
+template <int MODE, int NT, int G, int W>
 int w4_plan(const W4Args& a, int rows, int x_rows, int dev, int sms, W4Plan* pl) {
-    using S = W4Shape<MODE, NT, G>;
+    using S = W4Shape<MODE, NT, G, W>;
     // segments of a call: each has a row, an expert has one and one more for each full pass
     const int R = rows * a.k, experts = R < a.E ? R : a.E;
     const int segs = experts + R / x_rows < R ? experts + R / x_rows : R;
@@ -911,24 +914,24 @@ int w4_plan(const W4Args& a, int rows, int x_rows, int dev, int sms, W4Plan* pl)
     const long long units = tiles * (MODE == kW4Down ? 1 : MODE == kW4GateUp ? segs : (rows + x_rows - 1) / x_rows);
     const int KB = (a.K + kW4Blk - 1) / kW4Blk;
     const long long blocks = static_cast<long long>(KB) * (MODE == kW4Down ? segs : 1);
-    const int routing = MODE == kW4Gemv ? 0 : W4Routing::bytes(a.T_max * a.k, a.E);
+    const int routing = MODE == kW4Gemv ? 0 : W4Routing::bytes(a.T_max * a.k, a.E, W);
     const int sum_rows = MODE == kW4Down ? rows : x_rows;
-    const int smem = S::ring_bytes(x_rows) + kW4Warps * sum_rows * kW4Pad * 4 + routing;
-    if (smem > kSmemLimit) return api_fail(ET_ERR_UNSUPPORTED, "rows do not fit in shared memory");
+    const int smem = S::ring_bytes(x_rows) + W * sum_rows * kW4Pad * 4 + routing;
+    *pl = {};
+    if (smem > kSmemLimit) return ET_OK;  // no place for it
     static SmemOptIn opt;
-    const cudaError_t e = api_smem_opt_in(opt, dev, w4_kernel<MODE, NT, G>, kSmemLimit);
+    const cudaError_t e = api_smem_opt_in(opt, dev, w4_kernel<MODE, NT, G, W>, kSmemLimit);
     if (e != cudaSuccess) return api_fail_cuda(e, "cudaFuncSetAttribute(4-bit products)");
     static const int regs = [] {
         cudaFuncAttributes at{};
-        return cudaFuncGetAttributes(&at, w4_kernel<MODE, NT, G>) == cudaSuccess ? at.numRegs : 255;
+        return cudaFuncGetAttributes(&at, w4_kernel<MODE, NT, G, W>) == cudaSuccess ? at.numRegs : 255;
     }();
-    const int by_smem = kSmemSm / (smem + 1024), by_regs = 65536 / (kW4Warps * 32 * ((regs + 7) / 8 * 8));
-    const int per_sm = by_smem < by_regs ? by_smem : by_regs;
+    const int by_smem = kSmemSm / (smem + 1024), by_regs = 65536 / (W * 32 * ((regs + 7) / 8 * 8));
+    const int per_sm = W > kW4Warps ? 1 : by_smem < by_regs ? by_smem : by_regs;
     // 8, 4 or 2 CTAs share a unit's inputs if all of them fit at once and every split
     // keeps two k-blocks
     int c = kW4ClusterMax;
-    while (c > 1 && (blocks < 2ll * S::KW * c || units > w4_fit(w4_fits<MODE, NT, G>(), w4_kernel<MODE, NT, G>, c, per_sm)))
-        c /= 2;
+    while (c > 1 && (blocks < 2ll * S::KW * c || units > w4_fit<MODE, NT, G, W>(c, per_sm))) c /= 2;
     // The k-blocks of a warp of the busiest SM, its CTAs taken one after the other.  On 108
     // calls (9 to 64 rows, 768 x 2048 to 28672 x 8192) the estimate below was within 10 % of
     // the measured time in six of seven; the faster side was taken in 98, and 14 % lost at
@@ -941,8 +944,9 @@ int w4_plan(const W4Args& a, int rows, int x_rows, int dev, int sms, W4Plan* pl)
     return ET_OK;
 }
 
-template <int MODE, int NT, int G>
+template <int MODE, int NT, int G, int W>
 int w4_launch(W4Args a, int rows, int x_rows, const W4Plan& pl, int sms, void* stream) {
+    if (!pl.per_sm) return api_fail(ET_ERR_UNSUPPORTED, "rows do not fit in shared memory");
     a.x_rows = x_rows;
     a.sum_rows = MODE == kW4Down ? rows : x_rows;
     a.magic = 0x43004300u;
@@ -958,16 +962,34 @@ int w4_launch(W4Args a, int rows, int x_rows, const W4Plan& pl, int sms, void* s
     const bool early = !in_turn;
     int smem = pl.smem;
     if (early) {
-        W4Fit& fits = w4_fits<MODE, NT, G>();
         int n = static_cast<int>((grid + sms - 1) / sms);
-        while (n < pl.per_sm && w4_fit(fits, w4_kernel<MODE, NT, G>, pl.c, n) * static_cast<long long>(pl.c) < grid) ++n;
+        while (n < pl.per_sm && w4_fit<MODE, NT, G, W>(pl.c, n) * static_cast<long long>(pl.c) < grid) ++n;
         const int more = kSmemSm / (n + 1) / 128 * 128 - 1024 + 128;  // n + 1 do not fit
         smem = smem > more ? smem : more < kSmemLimit ? more : kSmemLimit;
     }
-    const cudaError_t e = api_launch_cluster(w4_kernel<MODE, NT, G>, dim3(static_cast<unsigned>(grid)), kW4Warps * 32,
+    const cudaError_t e = api_launch_cluster(w4_kernel<MODE, NT, G, W>, dim3(static_cast<unsigned>(grid)), W * 32,
                                              pl.c, early, smem, stream, a);
     if (e != cudaSuccess) return api_fail_cuda(e, "launch of the 4-bit product kernel");
     return ET_OK;
+}
+
+template <int MODE, int NT, int G>
+int w4_launch_warps(const W4Args& a, int rows, int x_rows, const W4Plan& pl, int dev, int sms, void* stream) {
+    if constexpr (MODE == kW4Down && NT == 1) {
+        // Clusters of 8 with about two CTAs an SM become clusters of 4 with one of twice the
+        // warps.  The places the gate/up kernel leaves come free one by one, its shared memory
+        // in pieces, where 8 did not always find room: then 3 of 32 clusters ran after the
+        // others (fine-grained, T = 48: 93 us, or 108, by the tokens' experts; now 92).  Clusters
+        // of 4 did, and two tiles of columns (NT) did: T = 32, Mixtral-shaped 217 us, with 8
+        // warps 230.
+        if (pl.c == kW4ClusterMax && pl.units * pl.c * 4 >= 5ll * sms) {
+            W4Plan two{};
+            const int rc = w4_plan<MODE, NT, G, kW4WarpsMax>(a, rows, x_rows, dev, sms, &two);
+            if (rc) return rc;
+            if (two.per_sm && 2 * two.c >= pl.c) return w4_launch<MODE, NT, G, kW4WarpsMax>(a, rows, x_rows, two, sms, stream);
+        }
+    }
+    return w4_launch<MODE, NT, G, kW4Warps>(a, rows, x_rows, pl, sms, stream);
 }
 
 // kW4Gemv with 9 rows or more: 8 a pass (one tile of columns in every product) or 16
@@ -982,12 +1004,12 @@ int w4_launch_rows(const W4Args& a, int rows, int x_rows, int dev, int sms, void
     int rc = ET_OK;
     const int one_rows = x_rows < 8 ? x_rows : 8, two_rows = x_rows < 16 ? x_rows : 16;
     if (MODE == kW4Gemv || x_rows <= 8)
-        if ((rc = w4_plan<MODE, 1, G>(a, rows, one_rows, dev, sms, &one))) return rc;
+        if ((rc = w4_plan<MODE, 1, G, kW4Warps>(a, rows, one_rows, dev, sms, &one))) return rc;
     if (x_rows > 8)
-        if ((rc = w4_plan<MODE, 2, G>(a, rows, two_rows, dev, sms, &two))) return rc;
+        if ((rc = w4_plan<MODE, 2, G, kW4Warps>(a, rows, two_rows, dev, sms, &two))) return rc;
     if (x_rows <= 8 || (MODE == kW4Gemv && one.cost <= two.cost))
-        return w4_launch<MODE, 1, G>(a, rows, one_rows, one, sms, stream);
-    return w4_launch<MODE, 2, G>(a, rows, two_rows, two, sms, stream);
+        return w4_launch_warps<MODE, 1, G>(a, rows, one_rows, one, dev, sms, stream);
+    return w4_launch_warps<MODE, 2, G>(a, rows, two_rows, two, dev, sms, stream);
 }
 
 template <int MODE>
