@@ -65,7 +65,8 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_topk_kernel(const
     bool ok;
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
     if (!ok) return;
-    const int t0 = blockIdx.x * nwarps + warp, step = gridDim.x * nwarps;
+    // rows to CTAs in turn, so that the last round is spread over all of them
+    const int t0 = blockIdx.x + gridDim.x * warp, step = gridDim.x * nwarps;
     auto load = [&](int t, float (&v)[EPL], int& on) {
         const float* L = p.logits + static_cast<size_t>(t) * E;
         on = t < T && (!p.mask || p.mask[t] != 0);
