@@ -28,13 +28,15 @@ constexpr int kSmemSm = 228 * 1024;  // shared memory of an SM; each CTA takes 1
 constexpr int kW4Pad = kW4Rows + 8;  // row length of a warp's fp32 tile, padded against bank conflicts
 constexpr int kW4RoutedMax = kW4RowsMax * kW4KMax;
 
-enum W4Mode { kW4Gemv = 0, kW4GateUp = 1, kW4Down = 2 };
+enum W4Mode { kW4Gemv = 0, kW4GateUp = 1, kW4Down = 2, kW4GateUpAlone = 3, kW4DownAlone = 4 };
+__host__ __device__ constexpr bool w4_is_alone(int mode) { return mode == kW4GateUpAlone || mode == kW4DownAlone; }
 
 struct W4Args {
     const bf16* x;            // [rows, K]
     const uint8_t *q0, *q1;   // [E][N, K/2]; q1: the up projection
     const bf16 *s0, *s1;      // [E][K/group, N]
     bf16* out;                // [rows, N]
+    float* y;                 // [T k, N]: a row's own output (kW4DownAlone)
     const int32_t* idx;       // [T, k]
     const float* w;           // [T, k]
     const int32_t* d_T;
@@ -409,6 +411,10 @@ __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, in
 //              (segment, k-block) over its warps; a warp adds what it has for a
 //              segment, times the gate weight, to its own fp32 rows by token, and
 //              the sum over splits and CTAs is the layer's output.
+//   kW4GateUpAlone, kW4DownAlone
+//              a warp takes a unit (a tile and a segment) by itself, with nothing to
+//              sum and nobody to meet; down then writes a routed row's share in fp32
+//              for w4_combine_kernel.  For calls with units enough (w4_alone).
 //
 // What bounds it.  An item -- 64 weight rows x 128 inputs, 4.2 KB -- takes a
 // scheduler about 670 cycles with warps enough to fill it (257 instructions unpack
@@ -418,7 +424,7 @@ __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, in
 // bytes for every byte read would have to be written first, and its rate is not
 // needed for 8 or 16 columns.  Memory and instructions being about even, what remains
 // is launch, latency, and an uneven number of items an SM.  T = 4, Mixtral-shaped:
-// 114 us, 64 % of the copy rate; T = 32, fine-grained: 83 us, 50 %; M = 1, 4096 x
+// 112 us, 65 % of the copy rate; T = 32, fine-grained: 74 us, 56 %; M = 1, 4096 x
 // 14336: 10.8 us, 41 %, of which 3.6 are spent before and after the items.  Not
 // kept, since they gained nothing: deeper rings, several row tiles interleaved,
 // the -136 sum(x) taken apart from the chain, sums pushed to one CTA of a cluster.
@@ -427,7 +433,7 @@ struct W4Shape {
     static constexpr int RW = NT;                             // row groups
     static constexpr int KW = W / RW;                         // splits of the inputs
     static constexpr int kTile = RW * kW4Rows;                // weight rows of a CTA
-    static constexpr int kOut = MODE == kW4GateUp ? kTile / 2 : kTile;
+    static constexpr int kOut = MODE == kW4GateUp || MODE == kW4GateUpAlone ? kTile / 2 : kTile;
     static constexpr int kWarpBytes = kW4Rows * 64 + (kW4Blk / G) * 128;
     static_assert(RW == 1 || (RW == 2 && KW == 2), "two named barriers");
     static __host__ __device__ int stage_bytes(int x_rows) { return RW * kWarpBytes + x_rows * 256; }
@@ -438,23 +444,26 @@ template <int MODE, int NT, int G, int W>
 __global__ void __launch_bounds__(W * 32) w4_kernel(const W4Args p) {
     using S = W4Shape<MODE, NT, G, W>;
     constexpr bool kDown = MODE == kW4Down;
+    constexpr bool kGateUp = MODE == kW4GateUp || MODE == kW4GateUpAlone;
+    constexpr bool kAlone = w4_is_alone(MODE);
+    constexpr bool kAfter = MODE == kW4Down || MODE == kW4DownAlone;  // reads h
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rw = warp % S::RW, kw = warp / S::RW;
     const int csize = static_cast<int>(cluster_size()), crank = static_cast<int>(cluster_rank());
-    const int split = crank * S::KW + kw, splits = csize * S::KW;
+    const int split = kAlone ? 0 : crank * S::KW + kw, splits = kAlone ? 1 : csize * S::KW;
     const int KB = (p.K + kW4Blk - 1) / kW4Blk;
     const int tiles = (p.N + S::kOut - 1) / S::kOut;
     // The down kernel is scheduled while the gate/up kernel of its call drains.  That
     // one has waited for everything before it, so only h is not there yet, and
     // waited for below: routing and the first weights come in meanwhile (T = 1,
     // fine-grained: 17.1 -> 14.6 us).
-    if (!kDown) grid_wait();
+    if (!kAfter) grid_wait();
     grid_release();
     bool ok;
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
     if (!ok) {  // the same for every CTA of the cluster
-        if (kDown) grid_wait();
+        if (kAfter) grid_wait();
         return;
     }
 
@@ -464,15 +473,15 @@ __global__ void __launch_bounds__(W * 32) w4_kernel(const W4Args p) {
     float* sums = reinterpret_cast<float*>(smem + S::ring_bytes(p.x_rows));
     W4Routing rt;
     if (MODE != kW4Gemv) {
-        rt.template place<W>(reinterpret_cast<uint8_t*>(sums + W * p.sum_rows * kW4Pad), p.T_max * p.k, p.E);
+        rt.template place<W>(reinterpret_cast<uint8_t*>(sums + (kAlone ? 0 : W * p.sum_rows * kW4Pad)), p.T_max * p.k, p.E);
         build_routing<W>(p, rt, T, p.x_rows);
     }
 
     // The units of this CTA (or cluster), and the items -- k-blocks -- of one unit
     // that are this split's.  Down: one unit, whose items are (segment, k-block).
     const int passes = MODE == kW4Gemv ? (T + p.x_rows - 1) / p.x_rows : 1;
-    const int n_units = kDown ? tiles : tiles * (MODE == kW4GateUp ? rt.n_seg : passes);
-    const int u0 = blockIdx.x / csize, ustep = gridDim.x / csize;
+    const int n_units = kDown ? tiles : tiles * (MODE == kW4Gemv ? passes : rt.n_seg);
+    const int u0 = kAlone ? blockIdx.x * W + warp : blockIdx.x / csize, ustep = kAlone ? gridDim.x * W : gridDim.x / csize;
     const int items = kDown ? rt.n_seg * KB : KB;
     const int i0 = static_cast<int>(static_cast<unsigned>(items) * split / splits);
     const int i1 = static_cast<int>(static_cast<unsigned>(items) * (split + 1) / splits);
@@ -480,8 +489,8 @@ __global__ void __launch_bounds__(W * 32) w4_kernel(const W4Args p) {
         for (int i = threadIdx.x; i < W * T * kW4Pad; i += blockDim.x) sums[i] = 0.0f;
         __syncthreads();
     }
-    auto tile_of = [&](int u) { return kDown ? u : MODE == kW4GateUp ? u % tiles : u / passes; };
-    auto part_of = [&](int u) { return kDown ? 0 : MODE == kW4GateUp ? u / tiles : u % passes; };  // segment or pass
+    auto tile_of = [&](int u) { return kDown ? u : MODE == kW4Gemv ? u / passes : u % tiles; };
+    auto part_of = [&](int u) { return kDown ? 0 : MODE == kW4Gemv ? u % passes : u / tiles; };  // segment or pass
     auto rows_of = [&](int part) {
         return MODE == kW4Gemv ? min(p.x_rows, T - part * p.x_rows) : static_cast<int>(rt.seg_n[part]);
     };
@@ -496,11 +505,11 @@ __global__ void __launch_bounds__(W * 32) w4_kernel(const W4Args p) {
     // of the weights the row lane / 4 of each 8, piece lane % 4 of its 64 bytes; of
     // the scales 8 rows of one group; of x the rows lane / 16 + 2 rw of each 2 RW,
     // piece lane % 16.  A warp's rows are [nw, nw + 64) of one matrix, or 32 + 32 of two.
-    constexpr int kRowsW = MODE == kW4GateUp ? kW4Rows / 2 : kW4Rows;
+    constexpr int kRowsW = kGateUp ? kW4Rows / 2 : kW4Rows;
     constexpr int kXMost = NT * 8 / (2 * S::RW);  // x rows of a lane
     const size_t ld8 = static_cast<size_t>(p.K) * 4;  // bytes of 8 rows
     const int wr = lane >> 2, wc = lane & 3, sg = lane >> 3, sc = lane & 7, xc = lane & 15;
-    const int sn8 = MODE == kW4GateUp ? (sc & 3) * 8 : sc * 8;
+    const int sn8 = kGateUp ? (sc & 3) * 8 : sc * 8;
     const uint32_t ring_u = smem_addr(ring);
     const uint32_t w_to = ring_u + rw * S::kWarpBytes + wr * 64 + (swz_w<G>(wc, wr) << 4);  // row + 8: the same swizzle
     const uint32_t s_to = ring_u + rw * S::kWarpBytes + kW4Rows * 64 + sg * 128 + (sc << 4);
@@ -519,15 +528,15 @@ __global__ void __launch_bounds__(W * 32) w4_kernel(const W4Args p) {
         left = p.N - nw;  // rows there are: a multiple of 8
         const size_t at = ((static_cast<size_t>(e) * p.N + nw + wr) * p.K >> 1) + kb * 64 + wc * 16;
         qa = p.q0 + at;
-        if (MODE == kW4GateUp) qb = p.q1 + at;
-        const bf16* s = (MODE == kW4GateUp && sc >= 4) ? p.s1 : p.s0;
+        if (kGateUp) qb = p.q1 + at;
+        const bf16* s = (kGateUp && sc >= 4) ? p.s1 : p.s0;
         sp = s + (static_cast<size_t>(e) * (p.K / G) + kb * (kW4Blk / G) + sg) * p.N + nw + sn8;
 #pragma unroll
         for (int i = 0; i < kXMost; ++i) {
             const int r = (lane >> 4) + 2 * rw + i * 2 * S::RW;
             int row = 0;
             if (r < nc_p)
-                row = MODE == kW4Gemv ? part * p.x_rows + r : kDown ? rt.order[rt.seg_r[part] + r] : rt.tok[rt.seg_r[part] + r];
+                row = MODE == kW4Gemv ? part * p.x_rows + r : kAfter ? rt.order[rt.seg_r[part] + r] : rt.tok[rt.seg_r[part] + r];
             xp[i] = p.x + static_cast<size_t>(row) * p.K + kb * kW4Blk + xc * 8;
         }
     };
@@ -541,7 +550,7 @@ __global__ void __launch_bounds__(W * 32) w4_kernel(const W4Args p) {
             const uint8_t* q = qa;
 #pragma unroll
             for (int g = 0; g < 8; ++g, q += ld8) {
-                if (MODE == kW4GateUp && g == 4) q = qb;
+                if (kGateUp && g == 4) q = qb;
                 cp_async16(dst + g * 512, q);
             }
             if (sg < kW4Blk / G) cp_async16(s_to + slot_off, sp);
@@ -549,9 +558,9 @@ __global__ void __launch_bounds__(W * 32) w4_kernel(const W4Args p) {
             const bool kin = wc * 32 < left_k;
 #pragma unroll
             for (int g = 0; g < 8; ++g) {
-                const int g8 = MODE == kW4GateUp ? g & 3 : g;
+                const int g8 = kGateUp ? g & 3 : g;
                 const bool in = kin && g8 * 8 < left;
-                cp_async16(dst + g * 512, in ? (MODE == kW4GateUp && g >= 4 ? qb : qa) + g8 * ld8 : p.q0, in);
+                cp_async16(dst + g * 512, in ? (kGateUp && g >= 4 ? qb : qa) + g8 * ld8 : p.q0, in);
             }
             if (sg < kW4Blk / G) {
                 const bool in = sg * G < left_k && sn8 < left;
@@ -569,7 +578,7 @@ __global__ void __launch_bounds__(W * 32) w4_kernel(const W4Args p) {
     };
     auto post = [&](bool first) {
         if (pu < n_units) post_w();
-        if (kDown && first) grid_wait();  // in every CTA: who waits for this kernel counts on it
+        if (kAfter && first) grid_wait();  // in every CTA: who waits for this kernel counts on it
         if (pu < n_units) {
             post_x();
             slot_off = slot_off + sbytes == ring_len ? 0 : slot_off + sbytes;
@@ -582,7 +591,7 @@ __global__ void __launch_bounds__(W * 32) w4_kernel(const W4Args p) {
             } else {
                 ++kb;
                 qa += 64;
-                if (MODE == kW4GateUp) qb += 64;
+                if (kGateUp) qb += 64;
                 sp += static_cast<size_t>(kW4Blk / G) * p.N;
 #pragma unroll
                 for (int i = 0; i < kXMost; ++i) xp[i] += kW4Blk;
@@ -653,6 +662,30 @@ __global__ void __launch_bounds__(W * 32) w4_kernel(const W4Args p) {
             }
         }
 
+        if (kAlone) {
+            const int r = lane >> 2, t = lane & 3, n0 = tile_of(u) * S::kOut + r;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int col = 2 * t + h;
+                if (col < nc) {
+                    const int o = rt.seg_r[cpart] + col;
+                    const size_t row = static_cast<size_t>(rt.order[o]) * p.N;
+                    const float wt = kGateUp ? 0.0f : rt.wt[o];
+#pragma unroll
+                    for (int m = 0; m < (kGateUp ? 2 : 4); ++m)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const int n = n0 + m * 16 + q * 8;
+                            const float v = acc[m][0][2 * q + h];
+                            if (n >= p.N) continue;
+                            if (kGateUp) p.out[row + n] = __float2bfloat16_rn(v / (1.0f + expf(-v)) * acc[(m + 2) & 3][0][2 * q + h]);
+                            else p.y[row + n] = wt * v;
+                        }
+                }
+            }
+            continue;
+        }
+
         // sums over the splits, in order: a warp's tile is [nc][64], the first RW
         // tiles make the CTA's
         if (kDown) {
@@ -719,6 +752,32 @@ __global__ void __launch_bounds__(W * 32) w4_kernel(const W4Args p) {
         if (csize > 1) cluster_sync();
         else __syncthreads();
     }
+}
+
+struct W4CombineArgs {
+    const float* y;  // [T k, N]
+    const int32_t* idx;
+    bf16* out;
+    const int32_t* d_T;
+    int T_host, T_max, N, E, k;
+    EtHeader* hdr;
+};
+
+// out[t] = the sum of a token's rows, in order: four columns a thread.
+__global__ void __launch_bounds__(256) w4_combine_kernel(const W4CombineArgs p) {
+    grid_begin();
+    bool ok;
+    const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
+    const int t = blockIdx.y, n = (blockIdx.x * 256 + threadIdx.x) * 4;
+    if (!ok || t >= T || n >= p.N) return;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int j = 0; j < p.k; ++j) {
+        const int r = t * p.k + j, e = p.idx[r];
+        if (e < 0 || e >= p.E) continue;
+        const float4 v = *reinterpret_cast<const float4*>(p.y + static_cast<size_t>(r) * p.N + n);
+        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
+    *reinterpret_cast<uint2*>(p.out + static_cast<size_t>(t) * p.N + n) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
 }
 
 // ---------------------------------------------------------------- conversion
@@ -906,6 +965,13 @@ int w4_fit(W4Fit& f, K kernel, int threads, int c, int n) {
     return v;
 }
 
+// Most segments of R routed rows: each has a row, an expert has one and one more for
+// each full pass.
+int w4_segments(int R, int E, int width) {
+    const int experts = R < E ? R : E;
+    return experts + R / width < R ? experts + R / width : R;
+}
+
 // How a call is spread over the GPU.
 struct W4Plan {
     long long units;
@@ -923,16 +989,15 @@ int w4_fit(int c, int n) {
 template <int MODE, int NT, int G, int W>
 int w4_plan(const W4Args& a, int rows, int x_rows, int dev, int sms, W4Plan* pl) {
     using S = W4Shape<MODE, NT, G, W>;
-    // segments of a call: each has a row, an expert has one and one more for each full pass
-    const int R = rows * a.k, experts = R < a.E ? R : a.E;
-    const int segs = experts + R / x_rows < R ? experts + R / x_rows : R;
+    const int segs = w4_segments(rows * a.k, a.E, x_rows);
     const long long tiles = (a.N + S::kOut - 1) / S::kOut;
-    const long long units = tiles * (MODE == kW4Down ? 1 : MODE == kW4GateUp ? segs : (rows + x_rows - 1) / x_rows);
+    constexpr bool alone = w4_is_alone(MODE);
+    const long long units = tiles * (MODE == kW4Down ? 1 : MODE == kW4Gemv ? (rows + x_rows - 1) / x_rows : segs);
     const int KB = (a.K + kW4Blk - 1) / kW4Blk;
     const long long blocks = static_cast<long long>(KB) * (MODE == kW4Down ? segs : 1);
     const int routing = MODE == kW4Gemv ? 0 : W4Routing::bytes(a.T_max * a.k, a.E, W);
     const int sum_rows = MODE == kW4Down ? rows : x_rows;
-    const int smem = S::ring_bytes(x_rows) + W * sum_rows * kW4Pad * 4 + routing;
+    const int smem = S::ring_bytes(x_rows) + (alone ? 0 : W * sum_rows * kW4Pad * 4) + routing;
     *pl = {};
     if (smem > kSmemLimit) return ET_OK;  // no place for it
     static SmemOptIn opt;
@@ -946,7 +1011,7 @@ int w4_plan(const W4Args& a, int rows, int x_rows, int dev, int sms, W4Plan* pl)
     const int per_sm = W > kW4Warps ? 1 : by_smem < by_regs ? by_smem : by_regs;
     // 8, 4 or 2 CTAs share a unit's inputs if all of them fit at once and every split
     // keeps two k-blocks
-    int c = kW4ClusterMax;
+    int c = alone ? 1 : kW4ClusterMax;
     while (c > 1 && (blocks < 2ll * S::KW * c || units > w4_fit<MODE, NT, G, W>(c, per_sm))) c /= 2;
     // The k-blocks of a warp of the busiest SM, its CTAs taken one after the other.  On 108
     // calls (9 to 64 rows, 768 x 2048 to 28672 x 8192) the estimate below was within 10 % of
@@ -967,8 +1032,9 @@ int w4_launch(W4Args a, int rows, int x_rows, const W4Plan& pl, int sms, void* s
     a.sum_rows = MODE == kW4Down ? rows : x_rows;
     a.magic = 0x43004300u;
     const long long fit = static_cast<long long>(sms) * pl.per_sm;
-    const bool in_turn = MODE != kW4Down && pl.c == 1 && pl.units > fit;  // CTAs take several units
-    const long long grid = in_turn ? fit : pl.units * pl.c;
+    const long long units = w4_is_alone(MODE) ? (pl.units + W - 1) / W : pl.units;  // of a CTA's size
+    const bool in_turn = MODE != kW4Down && pl.c == 1 && units > fit;                // CTAs take several
+    const long long grid = in_turn ? fit : units * pl.c;
     // Scheduled while the kernel before drains, which hides the launch (eager calls,
     // M = 1, 4096 x 14336: 14.5 -> 12.5 us).  Its CTAs then fill the places the other
     // kernel leaves, so no more of them may fit an SM than an even spread needs:
@@ -995,9 +1061,9 @@ int w4_launch_warps(const W4Args& a, int rows, int x_rows, const W4Plan& pl, int
         // Clusters of 8 with about two CTAs an SM become clusters of 4 with one of twice the
         // warps.  The places the gate/up kernel leaves come free one by one, its shared memory
         // in pieces, where 8 did not always find room: then 3 of 32 clusters ran after the
-        // others (fine-grained, T = 48: 93 us, or 108, by the tokens' experts; now 92).  Clusters
-        // of 4 did, and two tiles of columns (NT) did: T = 32, Mixtral-shaped 217 us, with 8
-        // warps 230.
+        // others (fine-grained, T = 5: 31 us, or 38, by the tokens' experts; now always 31).
+        // Clusters of 4 did, and two tiles of columns (NT) did: T = 32, Mixtral-shaped 217 us,
+        // with 8 warps 230.
         if (pl.c == kW4ClusterMax && pl.units * pl.c * 4 >= 5ll * sms) {
             W4Plan two{};
             const int rc = w4_plan<MODE, NT, G, kW4WarpsMax>(a, rows, x_rows, dev, sms, &two);
@@ -1015,7 +1081,7 @@ int w4_launch_warps(const W4Args& a, int rows, int x_rows, const W4Plan& pl, int
 // 14.8 us against 16.8, 2048 x 2048 4.3 against 5.5.  (32 a pass, a fourth of the
 // splits, lost nearly everywhere: M = 32, 4096 x 14336 38.3 us against 25.0.)
 template <int MODE, int G>
-int w4_launch_rows(const W4Args& a, int rows, int x_rows, int dev, int sms, void* stream) {
+int w4_launch_split(const W4Args& a, int rows, int x_rows, int dev, int sms, void* stream) {
     W4Plan one{}, two{};
     int rc = ET_OK;
     const int one_rows = x_rows < 8 ? x_rows : 8, two_rows = x_rows < 16 ? x_rows : 16;
@@ -1026,6 +1092,17 @@ int w4_launch_rows(const W4Args& a, int rows, int x_rows, int dev, int sms, void
     if (x_rows <= 8 || (MODE == kW4Gemv && one.cost <= two.cost))
         return w4_launch_warps<MODE, 1, G>(a, rows, one_rows, one, dev, sms, stream);
     return w4_launch_warps<MODE, 2, G>(a, rows, two_rows, two, dev, sms, stream);
+}
+
+template <int MODE, int G>
+int w4_launch_rows(const W4Args& a, int rows, int x_rows, int dev, int sms, void* stream) {
+    if constexpr (w4_is_alone(MODE)) {
+        W4Plan pl{};
+        const int rc = w4_plan<MODE, 1, G, kW4Warps>(a, rows, x_rows, dev, sms, &pl);
+        return rc ? rc : w4_launch<MODE, 1, G, kW4Warps>(a, rows, x_rows, pl, sms, stream);
+    } else {
+        return w4_launch_split<MODE, G>(a, rows, x_rows, dev, sms, stream);
+    }
 }
 
 template <int MODE>
@@ -1051,8 +1128,25 @@ dim3 w4_conv_grid(W4ConvArgs* a, int E, int sms) {
     return dim3(static_cast<unsigned>(tiles), (a->K + a->chunk - 1) / a->chunk);
 }
 
-size_t w4_experts_bytes(int T_max, int F, int k) {
+// Whether a warp takes a unit alone: when there are units for `percent` of the warps
+// at work at once (four CTAs of four an SM), so that few wait for the last.  `outs`
+// outputs a unit, `tile` of them.  Microseconds of a call with shared and alone units:
+//   gate/up  T = 32, fine-grained (4608 units, 2432 warps) 83 and 78; T = 16,
+//            Mixtral-shaped (5376) 173 and 154; T = 4, E 64, 7168 x 2048 (2048) 141, 162
+//   down     T = 64, fine-grained (6144) 110 and 92; T = 8 (2048) 43 and 41, 39 and 40;
+//            T = 4 (1024) 27.4 and 27.8; T = 16, Mixtral-shaped (768) 173 and 199
+bool w4_alone(int R, int E, int width, int outs, int tile, int percent, int sms) {
+    const long long units = static_cast<long long>((outs + tile - 1) / tile) * w4_segments(R, E, width);
+    return width <= 8 && 100 * units >= percent * 16ll * sms;
+}
+
+// Workspace: header, h [T_max k, F] bf16, a routed row's share of the output [T_max k, H]
+// fp32.
+size_t w4_h_end(int T_max, int F, int k) {
     return (kHeaderBytes + sizeof(uint16_t) * static_cast<size_t>(T_max) * k * F + 255) / 256 * 256;
+}
+size_t w4_experts_bytes(int T_max, int H, int F, int k) {
+    return w4_h_end(T_max, F, k) + (sizeof(float) * static_cast<size_t>(T_max) * k * H + 255) / 256 * 256;
 }
 
 bool w4_experts_ok(int T_max, int H, int F, int E, int k, int group, std::string* why) {
@@ -1167,7 +1261,7 @@ size_t et_w4_experts_workspace_bytes(int T_max, int H, int F, int E, int k, int 
     try {
         std::string why;
         if (!w4_experts_ok(T_max, H, F, E, k, group, &why)) return 0;
-        return w4_experts_bytes(T_max, F, k);
+        return w4_experts_bytes(T_max, H, F, k);
     } catch (...) {
         return 0;
     }
@@ -1189,7 +1283,7 @@ int et_w4_experts(const void* x, const int32_t* topk_idx, const float* topk_w, c
         if (!api_aligned(topk_idx, 4) || !api_aligned(topk_w, 4) || !api_aligned(d_T, 4))
             return api_fail(ET_ERR_INVALID, "tensors must be aligned to their element size");
         if (!d_T && (T < 0 || T > T_max)) return api_fail(ET_ERR_INVALID, "T must be in [0, T_max]");
-        int rc = api_check_ws(workspace, workspace_bytes, w4_experts_bytes(T_max, F, k));
+        int rc = api_check_ws(workspace, workspace_bytes, w4_experts_bytes(T_max, H, F, k));
         if (rc) return rc;
         if (!d_T && T == 0) return ET_OK;
         int dev = 0, sms = 0;
@@ -1223,7 +1317,9 @@ int et_w4_experts(const void* x, const int32_t* topk_idx, const float* topk_w, c
         const bool deep = H >= 4096;
         int width = avg <= (deep ? 1 : 2) ? 4 : avg < 8 || !deep ? 8 : 16;
         width = rows < width ? rows : width;
-        if ((rc = w4_launch_group<kW4GateUp>(a, group, rows, width, dev, sms, stream))) return rc;
+        if (w4_alone(R, E, width, F, 32, 125, sms)) rc = w4_launch_group<kW4GateUpAlone>(a, group, rows, width, dev, sms, stream);
+        else rc = w4_launch_group<kW4GateUp>(a, group, rows, width, dev, sms, stream);
+        if (rc) return rc;
         W4Args b = a;
         b.x = h;
         b.q0 = static_cast<const uint8_t*>(q_down);
@@ -1233,7 +1329,13 @@ int et_w4_experts(const void* x, const int32_t* topk_idx, const float* topk_w, c
         b.out = static_cast<bf16*>(out);
         b.N = H;
         b.K = F;
-        return w4_launch_group<kW4Down>(b, group, rows, width, dev, sms, stream);
+        if (!w4_alone(R, E, width, H, kW4Rows, 80, sms)) return w4_launch_group<kW4Down>(b, group, rows, width, dev, sms, stream);
+        b.y = reinterpret_cast<float*>(ws + w4_h_end(T_max, F, k));
+        if ((rc = w4_launch_group<kW4DownAlone>(b, group, rows, width, dev, sms, stream))) return rc;
+        const W4CombineArgs ca{b.y, topk_idx, static_cast<bf16*>(out), d_T, T, T_max, H, E, k, a.hdr};
+        const cudaError_t e = api_launch(w4_combine_kernel, dim3((H + 1023) / 1024, rows), 256, 0, stream, ca);
+        if (e != cudaSuccess) return api_fail_cuda(e, "launch of the sum over a token's experts");
+        return ET_OK;
     });
 }
 

@@ -88,6 +88,34 @@ def test_experts_with_many_rows_and_long_sums(cuda_lib, T, H, F, En, k, group):
     assert cuda_lib.et_status(ws) == (0, 0)
 
 
+@pytest.mark.parametrize("T,H,F,En,k,group", [(64, 416, 288, 256, 8, 32), (63, 448, 320, 250, 8, 64), (40, 1024, 128, 128, 8, 128),
+                                              (64, 64, 1568, 200, 8, 32)])
+def test_experts_of_many_units(cuda_lib, T, H, F, En, k, group):
+    """So many (tile, rows of an expert) that a warp takes each alone: in both products, or in one of them; with
+    experts left out, named twice and out of range, and fewer tokens by the device count."""
+    x, idx, w, gate, up, down = _experts_inputs(T, H, F, En, k, group, T + H)
+    idx[0] = -1
+    idx[1, 3:] = idx[1, 0]
+    idx[5, 2], w[5, 2] = -1, math.nan
+    idx[6, 1], idx[7, 0] = En, -7
+    seen = torch.where((idx >= 0) & (idx < En), idx, -1)
+    out, ws = _experts(cuda_lib, x, idx, w, gate, up, down)
+    assert (out[0] == 0).all()
+    _check_experts(out, x, seen, w, gate, up, down)
+    assert torch.equal(out, _experts(cuda_lib, x, idx, w, gate, up, down, ws=ws)[0])
+    assert cuda_lib.et_status(ws)[0] == cuda_lib.ET_ERR_BOUNDS
+    cuda_lib.et_reset_status(ws)
+    dT = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for n in (5, 0, T + 1):
+        dT.fill_(n)
+        out, _ = _experts(cuda_lib, x, idx, w, gate, up, down, d_T=dT, ws=ws)
+        if n <= T:
+            _check_experts(out, x, seen, w, gate, up, down, T=n)
+            assert cuda_lib.et_status(ws) == (0, 0)
+        else:
+            assert (out == 7).all() and cuda_lib.et_status(ws)[0] == cuda_lib.ET_ERR_BOUNDS
+
+
 def test_gemv_device_count(cuda_lib):
     N, K = 264, 640
     q, s = _weight((N, K), 64, 1)
