@@ -354,8 +354,9 @@ def _arg(t, name, dtype, shape, dev):
 
 def _device_of(t, name):
     """Index of the CUDA device that holds `t`."""
-    if t.is_cuda:
-        return t.get_device()
+    dev = t.get_device()  # -1 on the CPU
+    if dev >= 0:
+        return dev
     raise ValueError(f"{name} must be on a CUDA device, not {t.device}")
 
 
@@ -484,11 +485,15 @@ def et_block_norm_bwd(x, y, d_x_out, d_x_hat, dx, dy, *, gamma_post=None, gate=N
 
 def _w4(q, scale, name, lead, N, K, dev):
     """(pointer of q, pointer of scale, group) of the 4-bit weight [*lead, N, K]."""
-    groups = scale.shape[-2] if scale.dim() > 1 else 0
+    shape = scale.shape
+    groups = shape[-2] if len(shape) > 1 else 0
     if groups < 1 or K % groups:
-        raise ValueError(f"scale of {name} must be {(*lead, 'K / group', N)} with K = {K}, not {tuple(scale.shape)}")
-    return (_arg(q, name, _U8, (*lead, N, K // 2), dev),
-            _arg(scale, f"scale of {name}", _BF16, (*lead, groups, N), dev), K // groups)
+        raise ValueError(f"scale of {name} must be {(*lead, 'K / group', N)} with K = {K}, not {tuple(shape)}")
+    shape_q, shape_s = (*lead, N, K // 2), (*lead, groups, N)
+    if q is not None and q.dtype is _U8 and scale.dtype is _BF16 and q.shape == shape_q and shape == shape_s and \
+            q.is_contiguous() and scale.is_contiguous() and q.get_device() == dev == scale.get_device():
+        return q.data_ptr(), scale.data_ptr(), K // groups
+    return _arg(q, name, _U8, shape_q, dev), _arg(scale, f"scale of {name}", _BF16, shape_s, dev), K // groups
 
 
 def _w4_convert(w, q, scale):
