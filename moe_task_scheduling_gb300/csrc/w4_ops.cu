@@ -6,6 +6,7 @@
 // q is row-major, two inputs a byte (the even one in the low half); scale is
 // bf16 with the group first, so that a tile of rows reads consecutive scales.
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/etmoe.h"
 #include "et_api.h"
@@ -414,7 +415,8 @@ __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, in
 //   kW4GateUpAlone, kW4DownAlone
 //              a warp takes a unit (a tile and a segment) by itself, with nothing to
 //              sum and nobody to meet; down then writes a routed row's share in fp32
-//              for w4_combine_kernel.  For calls with units enough (w4_alone).
+//              for w4_combine_kernel.  For calls with units enough (w4_launch_gate_up and
+//              w4_launch_down say which).
 //
 // What bounds it.  An item -- 64 weight rows x 128 inputs, 4.2 KB -- takes a
 // scheduler about 670 cycles with warps enough to fill it (257 instructions unpack
@@ -424,8 +426,8 @@ __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, in
 // bytes for every byte read would have to be written first, and its rate is not
 // needed for 8 or 16 columns.  Memory and instructions being about even, what remains
 // is launch, latency, and an uneven number of items an SM.  T = 4, Mixtral-shaped:
-// 112 us, 65 % of the copy rate; T = 32, fine-grained: 74 us, 56 %; M = 1, 4096 x
-// 14336: 10.8 us, 41 %, of which 3.6 are spent before and after the items.  Not
+// 111 us, 66 % of the copy rate; T = 32, fine-grained: 74 us, 56 %; M = 1, 4096 x
+// 14336: 10.3 us, 43 %, of which 3.4 are spent before and after the items.  Not
 // kept, since they gained nothing: deeper rings, several row tiles interleaved,
 // the -136 sum(x) taken apart from the chain, sums pushed to one CTA of a cluster.
 template <int MODE, int NT, int G, int W>
@@ -440,8 +442,12 @@ struct W4Shape {
     static __host__ __device__ int ring_bytes(int x_rows) { return KW * kW4Stages * stage_bytes(x_rows); }
 };
 
+// Three CTAs an SM: 168 registers a thread and twelve warps did more than 128 and
+// sixteen (T = 32, 64 experts of 7168 x 2048: 277 us and 289; five CTAs 313), M = 1,
+// 4096 x 14336 10.3 us and 10.8.  Without a limit two tiles of columns take 240, two
+// CTAs an SM, and T = 32, Mixtral-shaped, 270 us in place of 208.
 template <int MODE, int NT, int G, int W>
-__global__ void __launch_bounds__(W * 32) w4_kernel(const W4Args p) {
+__global__ void __launch_bounds__(W * 32, W == kW4Warps ? 3 : 1) w4_kernel(const W4Args p) {
     using S = W4Shape<MODE, NT, G, W>;
     constexpr bool kDown = MODE == kW4Down;
     constexpr bool kGateUp = MODE == kW4GateUp || MODE == kW4GateUpAlone;
@@ -1015,13 +1021,13 @@ int w4_plan(const W4Args& a, int rows, int x_rows, int dev, int sms, W4Plan* pl)
     while (c > 1 && (blocks < 2ll * S::KW * c || units > w4_fit<MODE, NT, G, W>(c, per_sm))) c /= 2;
     // The k-blocks of a warp of the busiest SM, its CTAs taken one after the other.  On 108
     // calls (9 to 64 rows, 768 x 2048 to 28672 x 8192) the estimate below was within 10 % of
-    // the measured time in six of seven; the faster side was taken in 98, and 14 % lost at
+    // the measured time in seven of eight; the faster side was taken in 104, and 7 % lost at
     // most.  A smaller cluster that evens the SMs' shares is taken too: 4096 x 14336, M = 1
     // with 8 CTAs (4 on some SMs, 3 on others) 11.3 us, with 4 (2 on most) 10.8.
     const auto items = [&](int n) { return (units * n + sms - 1) / sms * ((KB + n * S::KW - 1) / (n * S::KW)); };
     if (MODE == kW4Gemv)
         while (c > 1 && items(c / 2) < items(c)) c /= 2;
-    *pl = {units, c, per_sm, smem, NT == 1 ? 3600 + 480 * items(c) : 5000 + 670 * items(c)};
+    *pl = {units, c, per_sm, smem, NT == 1 ? 3400 + 450 * items(c) : 4800 + 640 * items(c)};
     return ET_OK;
 }
 
@@ -1056,60 +1062,95 @@ int w4_launch(W4Args a, int rows, int x_rows, const W4Plan& pl, int sms, void* s
 }
 
 template <int MODE, int NT, int G>
-int w4_launch_warps(const W4Args& a, int rows, int x_rows, const W4Plan& pl, int dev, int sms, void* stream) {
-    if constexpr (MODE == kW4Down && NT == 1) {
-        // Clusters of 8 with about two CTAs an SM become clusters of 4 with one of twice the
-        // warps.  The places the gate/up kernel leaves come free one by one, its shared memory
-        // in pieces, where 8 did not always find room: then 3 of 32 clusters ran after the
-        // others (fine-grained, T = 5: 31 us, or 38, by the tokens' experts; now always 31).
-        // Clusters of 4 did, and two tiles of columns (NT) did: T = 32, Mixtral-shaped 217 us,
-        // with 8 warps 230.
-        if (pl.c == kW4ClusterMax && pl.units * pl.c * 4 >= 5ll * sms) {
-            W4Plan two{};
-            const int rc = w4_plan<MODE, NT, G, kW4WarpsMax>(a, rows, x_rows, dev, sms, &two);
-            if (rc) return rc;
-            if (two.per_sm && 2 * two.c >= pl.c) return w4_launch<MODE, NT, G, kW4WarpsMax>(a, rows, x_rows, two, sms, stream);
-        }
-    }
-    return w4_launch<MODE, NT, G, kW4Warps>(a, rows, x_rows, pl, sms, stream);
+int w4_plan_launch(const W4Args& a, int rows, int x_rows, int dev, int sms, void* stream) {
+    W4Plan pl{};
+    const int rc = w4_plan<MODE, NT, G, kW4Warps>(a, rows, x_rows, dev, sms, &pl);
+    return rc ? rc : w4_launch<MODE, NT, G, kW4Warps>(a, rows, x_rows, pl, sms, stream);
 }
 
-// kW4Gemv with 9 rows or more: 8 a pass (one tile of columns in every product) or 16
-// (two), whichever is estimated to end first.  Half the passes over the weights mean
-// half the unpacking, and win where there is much to do: 28672 x 8192, M = 16 36.6 us
-// against 50.4; twice the CTAs win where an SM would stay empty: 14336 x 4096, M = 16
-// 14.8 us against 16.8, 2048 x 2048 4.3 against 5.5.  (32 a pass, a fourth of the
-// splits, lost nearly everywhere: M = 32, 4096 x 14336 38.3 us against 25.0.)
-template <int MODE, int G>
-int w4_launch_split(const W4Args& a, int rows, int x_rows, int dev, int sms, void* stream) {
+// With 9 rows or more: 8 a pass (one tile of columns in every product) or 16 (two),
+// whichever is estimated to end first.  Half the passes over the weights mean half the
+// unpacking, and win where there is much to do: 28672 x 8192, M = 16 36.6 us against
+// 50.4; twice the CTAs win where an SM would stay empty: 14336 x 4096, M = 16 14.8 us
+// against 16.8, 2048 x 2048 4.3 against 5.5.  (32 a pass, a fourth of the splits, lost
+// nearly everywhere: M = 32, 4096 x 14336 38.3 us against 25.0.)
+template <int G>
+int w4_launch_gemv(const W4Args& a, int rows, int dev, int sms, void* stream) {
     W4Plan one{}, two{};
-    int rc = ET_OK;
-    const int one_rows = x_rows < 8 ? x_rows : 8, two_rows = x_rows < 16 ? x_rows : 16;
-    if (MODE == kW4Gemv || x_rows <= 8)
-        if ((rc = w4_plan<MODE, 1, G, kW4Warps>(a, rows, one_rows, dev, sms, &one))) return rc;
-    if (x_rows > 8)
-        if ((rc = w4_plan<MODE, 2, G, kW4Warps>(a, rows, two_rows, dev, sms, &two))) return rc;
-    if (x_rows <= 8 || (MODE == kW4Gemv && one.cost <= two.cost))
-        return w4_launch_warps<MODE, 1, G>(a, rows, one_rows, one, dev, sms, stream);
-    return w4_launch_warps<MODE, 2, G>(a, rows, two_rows, two, dev, sms, stream);
+    const int one_rows = rows < 8 ? rows : 8, two_rows = rows < 16 ? rows : 16;
+    int rc = w4_plan<kW4Gemv, 1, G, kW4Warps>(a, rows, one_rows, dev, sms, &one);
+    if (!rc && rows > 8) rc = w4_plan<kW4Gemv, 2, G, kW4Warps>(a, rows, two_rows, dev, sms, &two);
+    if (rc) return rc;
+    if (rows <= 8 || one.cost <= two.cost) return w4_launch<kW4Gemv, 1, G, kW4Warps>(a, rows, one_rows, one, sms, stream);
+    return w4_launch<kW4Gemv, 2, G, kW4Warps>(a, rows, two_rows, two, sms, stream);
 }
 
-template <int MODE, int G>
-int w4_launch_rows(const W4Args& a, int rows, int x_rows, int dev, int sms, void* stream) {
-    if constexpr (w4_is_alone(MODE)) {
-        W4Plan pl{};
-        const int rc = w4_plan<MODE, 1, G, kW4Warps>(a, rows, x_rows, dev, sms, &pl);
-        return rc ? rc : w4_launch<MODE, 1, G, kW4Warps>(a, rows, x_rows, pl, sms, stream);
-    } else {
-        return w4_launch_split<MODE, G>(a, rows, x_rows, dev, sms, stream);
-    }
+// A warp takes a unit alone when each at work has two or three in turn: T = 32,
+// fine-grained (4608 units) 76.6 us and 73.7, T = 16, Mixtral-shaped (5376) 159 and 154;
+// with fewer some wait long for the last: T = 8, 64 experts of 7168 x 2048 (4096) 183
+// and 193, T = 16, fine-grained (3072) 58 and 61.
+template <int G>
+int w4_launch_gate_up(const W4Args& a, int rows, int width, int dev, int sms, void* stream) {
+    if (width > 8) return w4_plan_launch<kW4GateUp, 2, G>(a, rows, width, dev, sms, stream);
+    constexpr int kOut = kW4Rows / 2;
+    const long long units = static_cast<long long>((a.N + kOut - 1) / kOut) * w4_segments(rows * a.k, a.E, width);
+    if (units >= 30ll * sms) return w4_plan_launch<kW4GateUpAlone, 1, G>(a, rows, width, dev, sms, stream);
+    return w4_plan_launch<kW4GateUp, 1, G>(a, rows, width, dev, sms, stream);
 }
 
-template <int MODE>
-int w4_launch_group(const W4Args& a, int group, int rows, int x_rows, int dev, int sms, void* stream) {
-    if (group == 32) return w4_launch_rows<MODE, 32>(a, rows, x_rows, dev, sms, stream);
-    if (group == 64) return w4_launch_rows<MODE, 64>(a, rows, x_rows, dev, sms, stream);
-    return w4_launch_rows<MODE, 128>(a, rows, x_rows, dev, sms, stream);
+// Estimated ns of an item of a warp when `warps` are at work.
+long long w4_item_ns(long long warps, int sms) {
+    const long long ns = 350 * warps / (4 * sms);
+    return ns > 600 ? ns : 600;
+}
+
+// Up to 8 rows a pass, three forms.
+//   Clusters of 8 with about two CTAs an SM become clusters of 4 with one of twice the
+//   warps.  The places the gate/up kernel leaves come free one by one, its shared memory
+//   in pieces, where 8 did not always find room: then 3 of 32 clusters ran after the
+//   others (fine-grained, T = 5: 31 us, or 38, by the tokens' experts; now always 31).
+//   Clusters of 4 did, and two tiles of columns (NT) did: T = 32, Mixtral-shaped 217 us,
+//   with 8 warps 230.
+//   A warp takes a unit alone, and a second kernel sums a token's rows, where that is
+//   estimated to end first: clusters have 64 output columns each, and their fp32 rows of
+//   T tokens leave room for one CTA an SM from T = 50 on.  Estimate: items of a warp,
+//   0.1 us a token for the sums of a cluster, 2.5 us for the second kernel.  Call with
+//   clusters and alone, us: T = 64, E 64, k 4, 1024 x 512 37 and 25; T = 16, E 64, k 8,
+//   7168 x 2048 279 and 249; T = 8, fine-grained 39 and 42; T = 8, E 16, k 4, 4096 x 2048
+//   49 and 55; T = 16, Mixtral-shaped 159 and 183.  On 46 calls it took the faster, or
+//   lost 5 % at most.
+template <int G>
+int w4_launch_down(const W4Args& a, int rows, int width, int dev, int sms, void* stream) {
+    if (width > 8) return w4_plan_launch<kW4Down, 2, G>(a, rows, width, dev, sms, stream);
+    W4Plan four{}, eight{};
+    int rc = w4_plan<kW4Down, 1, G, kW4Warps>(a, rows, width, dev, sms, &four);
+    if (!rc && four.c == kW4ClusterMax && four.units * four.c * 4 >= 5ll * sms)
+        rc = w4_plan<kW4Down, 1, G, kW4WarpsMax>(a, rows, width, dev, sms, &eight);
+    if (rc) return rc;
+    const bool wide = eight.per_sm && 2 * eight.c >= four.c;
+    const W4Plan& pl = wide ? eight : four;
+    const int KB = (a.K + kW4Blk - 1) / kW4Blk, segs = w4_segments(rows * a.k, a.E, width);
+    const long long splits = pl.c * (wide ? kW4WarpsMax : kW4Warps), units = pl.units * segs;
+    const long long shared_ns = (static_cast<long long>(segs) * KB + splits - 1) / splits * w4_item_ns(pl.units * splits, sms) + 100 * rows;
+    // alone: units at work at once are rounded up to whole ones a scheduler, of three at most
+    const long long each = (units + 4 * sms - 1) / (4 * sms);
+    const long long alone_ns = KB * w4_item_ns(each <= 3 ? each * 4 * sms : units, sms) + 2500;
+    if (pl.per_sm && shared_ns <= alone_ns)
+        return wide ? w4_launch<kW4Down, 1, G, kW4WarpsMax>(a, rows, width, pl, sms, stream)
+                    : w4_launch<kW4Down, 1, G, kW4Warps>(a, rows, width, pl, sms, stream);
+    if ((rc = w4_plan_launch<kW4DownAlone, 1, G>(a, rows, width, dev, sms, stream))) return rc;
+    const W4CombineArgs ca{a.y, a.idx, a.out, a.d_T, a.T_host, a.T_max, a.N, a.E, a.k, a.hdr};
+    const cudaError_t e = api_launch(w4_combine_kernel, dim3((a.N + 1023) / 1024, rows), 256, 0, stream, ca);
+    if (e != cudaSuccess) return api_fail_cuda(e, "launch of the sum over a token's experts");
+    return ET_OK;
+}
+
+// f with the group size as a constant.
+template <class F>
+int w4_by_group(int group, F&& f) {
+    if (group == 32) return f(std::integral_constant<int, 32>{});
+    if (group == 64) return f(std::integral_constant<int, 64>{});
+    return f(std::integral_constant<int, 128>{});
 }
 
 int w4_conv_check(int E, int N, int K, int group) {
@@ -1126,18 +1167,6 @@ dim3 w4_conv_grid(W4ConvArgs* a, int E, int sms) {
     const long long tiles = static_cast<long long>(E) * a->N / kConvRows;
     a->chunk = tiles * ((a->K + kConvK - 1) / kConvK) < 2ll * sms ? 1024 : kConvK;
     return dim3(static_cast<unsigned>(tiles), (a->K + a->chunk - 1) / a->chunk);
-}
-
-// Whether a warp takes a unit alone: when there are units for `percent` of the warps
-// at work at once (four CTAs of four an SM), so that few wait for the last.  `outs`
-// outputs a unit, `tile` of them.  Microseconds of a call with shared and alone units:
-//   gate/up  T = 32, fine-grained (4608 units, 2432 warps) 83 and 78; T = 16,
-//            Mixtral-shaped (5376) 173 and 154; T = 4, E 64, 7168 x 2048 (2048) 141, 162
-//   down     T = 64, fine-grained (6144) 110 and 92; T = 8 (2048) 43 and 41, 39 and 40;
-//            T = 4 (1024) 27.4 and 27.8; T = 16, Mixtral-shaped (768) 173 and 199
-bool w4_alone(int R, int E, int width, int outs, int tile, int percent, int sms) {
-    const long long units = static_cast<long long>((outs + tile - 1) / tile) * w4_segments(R, E, width);
-    return width <= 8 && 100 * units >= percent * 16ll * sms;
 }
 
 // Workspace: header, h [T_max k, F] bf16, a routed row's share of the output [T_max k, H]
@@ -1253,7 +1282,7 @@ int et_w4_gemv(const void* X, const void* q, const void* scale, void* Y, int M, 
         a.k = 1;
         a.hdr = static_cast<EtHeader*>(workspace);
         const int rows = d_M ? M_max : M;
-        return w4_launch_group<kW4Gemv>(a, group, rows, rows, dev, sms, stream);
+        return w4_by_group(group, [&](auto g) { return w4_launch_gemv<decltype(g)::value>(a, rows, dev, sms, stream); });
     });
 }
 
@@ -1317,8 +1346,7 @@ int et_w4_experts(const void* x, const int32_t* topk_idx, const float* topk_w, c
         const bool deep = H >= 4096;
         int width = avg <= (deep ? 1 : 2) ? 4 : avg < 8 || !deep ? 8 : 16;
         width = rows < width ? rows : width;
-        if (w4_alone(R, E, width, F, 32, 125, sms)) rc = w4_launch_group<kW4GateUpAlone>(a, group, rows, width, dev, sms, stream);
-        else rc = w4_launch_group<kW4GateUp>(a, group, rows, width, dev, sms, stream);
+        rc = w4_by_group(group, [&](auto g) { return w4_launch_gate_up<decltype(g)::value>(a, rows, width, dev, sms, stream); });
         if (rc) return rc;
         W4Args b = a;
         b.x = h;
@@ -1329,13 +1357,8 @@ int et_w4_experts(const void* x, const int32_t* topk_idx, const float* topk_w, c
         b.out = static_cast<bf16*>(out);
         b.N = H;
         b.K = F;
-        if (!w4_alone(R, E, width, H, kW4Rows, 80, sms)) return w4_launch_group<kW4Down>(b, group, rows, width, dev, sms, stream);
         b.y = reinterpret_cast<float*>(ws + w4_h_end(T_max, F, k));
-        if ((rc = w4_launch_group<kW4DownAlone>(b, group, rows, width, dev, sms, stream))) return rc;
-        const W4CombineArgs ca{b.y, topk_idx, static_cast<bf16*>(out), d_T, T, T_max, H, E, k, a.hdr};
-        const cudaError_t e = api_launch(w4_combine_kernel, dim3((H + 1023) / 1024, rows), 256, 0, stream, ca);
-        if (e != cudaSuccess) return api_fail_cuda(e, "launch of the sum over a token's experts");
-        return ET_OK;
+        return w4_by_group(group, [&](auto g) { return w4_launch_down<decltype(g)::value>(b, rows, width, dev, sms, stream); });
     });
 }
 

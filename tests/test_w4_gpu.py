@@ -89,7 +89,7 @@ def test_experts_with_many_rows_and_long_sums(cuda_lib, T, H, F, En, k, group):
 
 
 @pytest.mark.parametrize("T,H,F,En,k,group", [(64, 416, 288, 256, 8, 32), (63, 448, 320, 250, 8, 64), (40, 1024, 128, 128, 8, 128),
-                                              (64, 64, 1568, 200, 8, 32)])
+                                              (64, 64, 1568, 200, 8, 32), (64, 128, 1600, 128, 8, 64), (50, 128, 3200, 60, 8, 128)])
 def test_experts_of_many_units(cuda_lib, T, H, F, En, k, group):
     """So many (tile, rows of an expert) that a warp takes each alone: in both products, or in one of them; with
     experts left out, named twice and out of range, and fewer tokens by the device count."""
