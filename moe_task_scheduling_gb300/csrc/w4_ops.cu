@@ -1046,8 +1046,12 @@ int w4_launch(W4Args a, int rows, int x_rows, const W4Plan& pl, int sms, void* s
     // kernel leaves, so no more of them may fit an SM than an even spread needs:
     // without that limit M = 16 took 20.4 us, with it 16.3 (18.6 when launched after
     // the other).  CTAs that take units in turn are launched after the other: they
-    // fill the GPU, and started early they lost 1 to 5 % (Mixtral-shaped, T = 4).
-    const bool early = !in_turn;
+    // fill the GPU, and started early they lost 1 to 5 % (Mixtral-shaped, T = 4) --
+    // except after the gate/up kernel where they are short, up to 64 items a scheduler:
+    // 32 experts of 2048 x 768, k = 4, T = 64 36.9 us and 33.8; fine-grained, T = 64 86
+    // and 80, T = 32 73.4 and 74.5; longer ones, 64 of 7168 x 2048, T = 16 245 and 252.
+    const long long per_scheduler = pl.units * ((a.K + kW4Blk - 1) / kW4Blk) / (4 * sms);
+    const bool early = !in_turn || (MODE == kW4DownAlone && per_scheduler <= 64);
     int smem = pl.smem;
     if (early) {
         int n = static_cast<int>((grid + sms - 1) / sms);
