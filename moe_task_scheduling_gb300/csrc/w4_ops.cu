@@ -769,7 +769,8 @@ struct W4CombineArgs {
     EtHeader* hdr;
 };
 
-// out[t] = the sum of a token's rows, in order: four columns a thread.
+// out[t] = the sum of a token's rows, in order: four columns a thread.  All launch and
+// latency (T = 32, H = 2048, 8 rows each, 2.1 MB: 6.8 us by itself with cold caches).
 __global__ void __launch_bounds__(256) w4_combine_kernel(const W4CombineArgs p) {
     grid_begin();
     bool ok;
@@ -780,7 +781,7 @@ __global__ void __launch_bounds__(256) w4_combine_kernel(const W4CombineArgs p) 
     for (int j = 0; j < p.k; ++j) {
         const int r = t * p.k + j, e = p.idx[r];
         if (e < 0 || e >= p.E) continue;
-        const float4 v = *reinterpret_cast<const float4*>(p.y + static_cast<size_t>(r) * p.N + n);
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(p.y + static_cast<size_t>(r) * p.N + n));
         s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
     }
     *reinterpret_cast<uint2*>(p.out + static_cast<size_t>(t) * p.N + n) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
