@@ -25,8 +25,7 @@ struct RouterArgs {
     const int32_t* d_T;
     int T_host, T_max, E, k;
     EtHeader* hdr;
-    float* part_p;           // [kRouterParts, E]
-    int32_t* part_c;         // [kRouterParts, E]
+    float2* part;            // [kRouterParts, E]: a CTA's sum of probabilities; its count, as an integer
     float* part_z;           // [kRouterParts]
     int32_t* part_n;         // [kRouterParts]
 };
@@ -53,8 +52,8 @@ __device__ __forceinline__ float key_logit(uint32_t key) {
 // every run.  All in fp32: fp64 runs at 1/64 of it here.  exp, log and the
 // quotients are the fast ones: within |L - L0| + 4 and 2 units of 2^-24.
 //
-// T = 16384, E = 128, k = 8: 16 us for 9.4 MB, which HBM would bring in 1.4.  About
-// 8 us are fixed -- the launch, the first loads, and the way through memory to the
+// T = 16384, E = 128, k = 8: 14.4 us for 9.4 MB, which HBM would bring in 1.4.  About
+// 7 us are fixed -- the launch, the first loads, and the way through memory to the
 // last CTA's sums -- and the rest is instructions: 27 rows a scheduler, 530 cycles
 // each, two warp reductions in each of the k rounds among them.  (A vote in place
 // of the second reduction, with a branch for ties: 17.5 -> 18.4 us.)
@@ -215,18 +214,16 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_topk_kernel(const
         if (one) {
             sm[e] = s;
         } else {
-            p.part_p[b * E + e] = s;
-            p.part_c[b * E + e] = hist[e];
+            p.part[b * E + e] = make_float2(s, __int_as_float(hist[e]));
         }
     }
     __syncthreads();
     if (!one) {
-        if (threadIdx.x == 0) {
-            __threadfence();
-            const int n = atomicAdd(&p.hdr->exit_count, 1);
+        if (threadIdx.x == 0) {  // after what this CTA wrote, before what the last one reads
+            int n;
+            asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(n) : "l"(&p.hdr->exit_count) : "memory");
             last = n == G - 1;
             if (last) p.hdr->exit_count = 0;
-            __threadfence();
         }
         __syncthreads();
         if (!last) return;
@@ -249,17 +246,15 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_topk_kernel(const
             const int e = o % E;
             float s = 0.0f;
             int c = 0;
-            for (int g0 = o / E; g0 < G; g0 += 10 * groups) {
-                float v[10];
-                int n[10];
+            for (int g0 = o / E; g0 < G; g0 += 19 * groups) {
+                float2 v[19];
 #pragma unroll
-                for (int i = 0; i < 10; ++i) {  // twenty loads in flight
+                for (int i = 0; i < 19; ++i) {  // all of 152 CTAs' in flight with eight groups
                     const int g = g0 + i * groups;
-                    v[i] = g < G ? __ldcg(p.part_p + g * E + e) : 0.0f;
-                    n[i] = g < G ? __ldcg(p.part_c + g * E + e) : 0;
+                    v[i] = g < G ? __ldcg(p.part + g * E + e) : make_float2(0.0f, 0.0f);
                 }
 #pragma unroll
-                for (int i = 0; i < 10; ++i) { s += v[i]; c += n[i]; }
+                for (int i = 0; i < 19; ++i) { s += v[i].x; c += __float_as_int(v[i].y); }
             }
             sm[o] = s;
             csum[o] = c;
@@ -427,16 +422,14 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(const RouterBwdArgs p) 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct RouterLayout {
-    size_t part_p, part_c, part_z, part_n, total;
+    size_t part, part_z, part_n, total;
 };
 
 RouterLayout router_layout(int E) {
     RouterLayout L{};
     size_t off = kHeaderBytes;
-    L.part_p = off;
-    off = align256(off + sizeof(float) * kRouterParts * E);
-    L.part_c = off;
-    off = align256(off + sizeof(int) * kRouterParts * E);
+    L.part = off;
+    off = align256(off + sizeof(float2) * kRouterParts * E);
     L.part_z = off;
     off = align256(off + sizeof(float) * kRouterParts);
     L.part_n = off;
@@ -486,10 +479,14 @@ int et_router_topk(const float* logits, const uint8_t* token_mask, int32_t* topk
         uint8_t* ws = static_cast<uint8_t*>(workspace);
         RouterArgs a{logits, token_mask, topk_idx, topk_w, expert_counts, n_routed, mean_prob, losses,
                      d_T, T, T_max, E, k, reinterpret_cast<EtHeader*>(ws),
-                     reinterpret_cast<float*>(ws + L.part_p), reinterpret_cast<int32_t*>(ws + L.part_c),
+                     reinterpret_cast<float2*>(ws + L.part),
                      reinterpret_cast<float*>(ws + L.part_z), reinterpret_cast<int32_t*>(ws + L.part_n)};
         const int rows = d_T ? T_max : (T > 0 ? T : 1);
-        const int warps = rows < kRouterWarpsMax ? rows : kRouterWarpsMax;
+        // One CTA up to 32 rows: nothing to sum over CTAs.  Beyond, as few warps as let the
+        // last CTA read all sums in one batch (32 warps / E groups of 19): rows share fewer SMs.
+        int warps = rows < kRouterWarpsMax ? rows : kRouterWarpsMax;
+        if (rows > kRouterWarpsMax)
+            while (warps > 8 && 4ll * rows * E <= 608ll * warps * warps) warps /= 2;
         int grid = ceil_div_i(rows, warps);
         grid = grid < kRouterParts ? grid : kRouterParts;
         // [warps][E] floats; the last CTA: max(1, threads / E) x E of a float and an int
