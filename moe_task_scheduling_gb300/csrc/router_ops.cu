@@ -43,6 +43,82 @@ __device__ __forceinline__ float key_logit(uint32_t key) {
     return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
 }
 
+// The selection on whole keys, two reductions a round (the largest key, the lowest
+// expert that has it): lane j < k gets the j-th.
+template <int EPL>
+__device__ __forceinline__ void select_whole(const float (&v)[EPL], int E, int k, int lane, uint32_t& mykey, uint32_t& myE) {
+    uint32_t key[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = lane + 32 * i < E ? logit_key(v[i]) : 0u;
+#pragma unroll 1
+    for (int j = 0; j < k; ++j) {
+        uint32_t bk = key[0];
+#pragma unroll
+        for (int i = 1; i < EPL; ++i) bk = max(bk, key[i]);
+        const uint32_t kmax = __reduce_max_sync(0xffffffffu, bk);
+        uint32_t low = 0xffffffffu;  // this lane's lowest expert that holds it
+#pragma unroll
+        for (int i = EPL - 1; i >= 0; --i)
+            if (key[i] == kmax) low = static_cast<uint32_t>(lane + 32 * i);
+        const uint32_t e = __reduce_min_sync(0xffffffffu, low);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (static_cast<uint32_t>(lane + 32 * i) == e) key[i] = 0u;
+        if (lane == j) { mykey = kmax; myE = e; }
+    }
+}
+
+template <int EPL>
+__device__ __noinline__ void select_again(const float (&v)[EPL], int E, int k, int lane, uint32_t& mykey, uint32_t& myE) {
+    select_whole<EPL>(v, E, k, lane, mykey, myE);
+}
+
+// The same where a lane has four experts or eight.  Keys are cut above kLow, with the
+// expert below, lower experts larger: one reduction a round finds both.  A lane's keys
+// are sorted, so that a round looks at the heads alone.  Round k + 1 tells whether the
+// cut decided who is chosen; if it may have, the row is selected again on whole keys.
+// T = 65536, E = 128, k = 8 37.0 -> 33.0 us, T = 16384, E = 256 25.6 -> 21.7; with one
+// or two experts a lane whole keys are faster (T = 16384, E = 8, k = 2 9.1 us and 10.4).
+template <int EPL>
+__device__ __forceinline__ void select_cut(const float (&v)[EPL], const float* logits, int E, int k, int lane,
+                                           uint32_t& mykey, uint32_t& myE) {
+    constexpr uint32_t kLow = 32 * EPL - 1, kNegInfKey = 0x007fffffu;
+    uint32_t pk[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        const uint32_t e = lane + 32 * i;
+        pk[i] = e < static_cast<uint32_t>(E) ? (logit_key(v[i]) & ~kLow) | (kLow - e) : 0u;
+    }
+#pragma unroll
+    for (int m = EPL - 1; m > 0; --m)
+#pragma unroll
+        for (int i = 0; i < m; ++i) {
+            const uint32_t hi = max(pk[i], pk[i + 1]);
+            pk[i + 1] = min(pk[i], pk[i + 1]);
+            pk[i] = hi;
+        }
+    uint32_t mine = 0;  // lane j: the j-th, 0 when there is none
+#pragma unroll 1
+    for (int j = 0; j <= k; ++j) {
+        const uint32_t top = __reduce_max_sync(0xffffffffu, pk[0]);
+        const bool win = pk[0] == top;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) pk[i] = win ? (i + 1 < EPL ? pk[(i + 1) % EPL] : 0u) : pk[i];
+        if (lane == j) mine = top;
+    }
+    myE = kLow - (mine & kLow);
+    mykey = 0;
+    if (mine) mykey = logit_key(logits[myE]);
+    // Experts with one cut key come in the order of their number: right unless a later
+    // one's whole key is larger, or the cut key goes on behind the k-th (-inf may: none
+    // of its kind is chosen).
+    const uint32_t after = __shfl_down_sync(0xffffffffu, mykey, 1);
+    const uint32_t next = __shfl_down_sync(0xffffffffu, mine, 1);
+    const bool same = ((mine ^ next) & ~kLow) == 0 && mykey != kNegInfKey;
+    const bool doubt = lane < k && same && (mykey < after || lane == k - 1);
+    if (__any_sync(0xffffffffu, doubt)) select_again<EPL>(v, E, k, lane, mykey, myE);
+}
+
 // One row a warp, expert e = lane + 32 i in register i; the next row's logits are
 // loaded while the current one is worked on.  The k rounds of the selection also
 // give the row's largest logit, so the softmax needs no max pass.  Sums over
@@ -52,11 +128,10 @@ __device__ __forceinline__ float key_logit(uint32_t key) {
 // every run.  All in fp32: fp64 runs at 1/64 of it here.  exp, log and the
 // quotients are the fast ones: within |L - L0| + 4 and 2 units of 2^-24.
 //
-// T = 16384, E = 128, k = 8: 14.4 us for 9.4 MB, which HBM would bring in 1.4.  About
+// T = 16384, E = 128, k = 8: 13.5 us for 9.4 MB, which HBM would bring in 1.4.  About
 // 7 us are fixed -- the launch, the first loads, and the way through memory to the
-// last CTA's sums -- and the rest is instructions: 27 rows a scheduler, 530 cycles
-// each, two warp reductions in each of the k rounds among them.  (A vote in place
-// of the second reduction, with a branch for ties: 17.5 -> 18.4 us.)
+// last CTA's sums -- and the rest is instructions: 27 rows a scheduler, 450 cycles
+// each, the selection most of them.
 template <int EPL>
 __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_topk_kernel(const RouterArgs p) {
     extern __shared__ __align__(16) float sm[];  // [warps][E], then the last CTA's sums
@@ -91,66 +166,13 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_topk_kernel(const
 
     for (int t = t0; t < T; t += step) {
         float v[EPL];
-        uint32_t key[EPL];
         const int masked_in = non;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            v[i] = nv[i];
-            key[i] = lane + 32 * i < E ? logit_key(v[i]) : 0u;
-        }
+        for (int i = 0; i < EPL; ++i) v[i] = nv[i];
         load(t + step, nv, non);
-        // A lane's entries in descending order (neighbours change places only for a
-        // strictly larger key, so equal ones stay in the order of their experts);
-        // then each round looks at the heads alone.  i_[] is the place i of an entry.
-        int i_[EPL];
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) i_[i] = i;
-        constexpr bool kSorted = EPL == 4;  // 2: nothing to gain; 8: 28 exchanges
-        if (kSorted) {
-#pragma unroll
-            for (int n = EPL - 1; n > 0; --n)
-#pragma unroll
-                for (int i = 0; i < n; ++i) {
-                    const bool up = key[i + 1] > key[i];
-                    const uint32_t ka = key[i];
-                    const int ia = i_[i];
-                    key[i] = up ? key[i + 1] : ka;
-                    i_[i] = up ? i_[i + 1] : ia;
-                    key[i + 1] = up ? ka : key[i + 1];
-                    i_[i + 1] = up ? ia : i_[i + 1];
-                }
-        }
         uint32_t mykey = 0, myE = 0;
-#pragma unroll 1
-        for (int j = 0; j < k; ++j) {
-            uint32_t bk = key[0];
-            if (!kSorted)
-#pragma unroll
-                for (int i = 1; i < EPL; ++i) bk = max(bk, key[i]);
-            const uint32_t kmax = __reduce_max_sync(0xffffffffu, bk);
-            uint32_t mine = 0xffffffffu;  // this lane's lowest expert that holds it
-            if (kSorted) {
-                if (bk == kmax) mine = static_cast<uint32_t>(lane + 32 * i_[0]);
-            } else {
-#pragma unroll
-                for (int i = EPL - 1; i >= 0; --i)
-                    if (key[i] == kmax) mine = static_cast<uint32_t>(lane + 32 * i);
-            }
-            const uint32_t e = __reduce_min_sync(0xffffffffu, mine);
-            if (kSorted) {
-                const bool win = mine == e;
-#pragma unroll
-                for (int i = 0; i < EPL; ++i) {
-                    key[i] = win ? (i + 1 < EPL ? key[(i + 1) % EPL] : 0u) : key[i];
-                    if (i + 1 < EPL) i_[i] = win ? i_[(i + 1) % EPL] : i_[i];
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < EPL; ++i)
-                    if (static_cast<uint32_t>(lane + 32 * i) == e) key[i] = 0u;
-            }
-            if (lane == j) { mykey = kmax; myE = e; }
-        }
+        if (EPL <= 2) select_whole<EPL>(v, E, k, lane, mykey, myE);
+        else select_cut<EPL>(v, p.logits + static_cast<size_t>(t) * E, E, k, lane, mykey, myE);
         const float myL = lane < k ? key_logit(mykey) : -INFINITY;
         const float L0 = __shfl_sync(0xffffffffu, myL, 0);
         const bool live = masked_in && !(L0 == -INFINITY);

@@ -114,6 +114,29 @@ def test_ties_and_masks(cuda_lib):
         ref.check(d, ref.router_grad(logits, 3, dl, dw, mask), 64 * U, "d_logits")
 
 
+@pytest.mark.parametrize("En,k", [(5, 3), (8, 8), (40, 8), (64, 4), (100, 8), (128, 8), (200, 7), (256, 8)])
+def test_close_and_equal_logits(cuda_lib, En, k):
+    """Logits that differ in their last bits only, equal ones among them, of either sign, at the k-th place and
+    elsewhere; logits rounded to bf16; -inf and the lowest finite values side by side."""
+    T = 600
+    g = _gen(En)
+    near = 1 + torch.randint(0, 30, (T, En), generator=g) * 2.0 ** -23
+    near[100:200] = -near[100:200]
+    near[200:300] = torch.randn(100, En, generator=g).bfloat16().float()
+    near[300:400] = torch.where(torch.rand(100, En, generator=g) < 0.5, near[300:400], torch.randn(100, En, generator=g))
+    low = torch.tensor([-math.inf, torch.finfo(torch.float32).min, -3.4e38, 0.0, -0.0, 1e-45, -1e-45])
+    near[400:500] = low[torch.randint(0, 7, (100, En), generator=g)]
+    near[500:] = torch.randint(-2, 3, (100, En), generator=g).float()
+    o, _, _, _ = _forward(cuda_lib, near, k)
+    r = ref.router(near, k)
+    assert torch.equal(o["idx"].cpu(), r["idx"].to(torch.int32))
+    assert torch.equal(o["counts"].cpu(), r["counts"].to(torch.int32)) and int(o["n"]) == r["n"]
+    # weights: each logit's distance from the largest, exp and the sum over k (as above), 0 far below
+    fin = torch.where(torch.isfinite(near), near.double(), 0.0).abs()
+    fin = torch.where(fin < 1e30, fin, 0.0)
+    ref.check(o["w"], r["w"], (8 + 2 * float(fin.max()) + k) * U * r["w"] + 1e-38, "w")
+
+
 def test_nothing_is_routed(cuda_lib):
     """All tokens masked, all logits -inf, no tokens at all: zeros, not NaN."""
     for logits, mask, T in ((torch.randn(9, 6), torch.zeros(9, dtype=torch.uint8), None),
