@@ -68,16 +68,21 @@ __device__ __forceinline__ void select_whole(const float (&v)[EPL], int E, int k
     }
 }
 
+// (key, expert), out of line: it is seldom needed.
 template <int EPL>
-__device__ __noinline__ void select_again(const float (&v)[EPL], int E, int k, int lane, uint32_t& mykey, uint32_t& myE) {
-    select_whole<EPL>(v, E, k, lane, mykey, myE);
+struct RowLogits { float v[EPL]; };
+template <int EPL>
+__device__ __noinline__ uint2 select_again(RowLogits<EPL> row, int E, int k, int lane) {
+    uint32_t key = 0, e = 0;
+    select_whole<EPL>(row.v, E, k, lane, key, e);
+    return make_uint2(key, e);
 }
 
 // The same where a lane has four experts or eight.  Keys are cut above kLow, with the
 // expert below, lower experts larger: one reduction a round finds both.  A lane's keys
 // are sorted, so that a round looks at the heads alone.  Round k + 1 tells whether the
 // cut decided who is chosen; if it may have, the row is selected again on whole keys.
-// T = 65536, E = 128, k = 8 37.0 -> 33.0 us, T = 16384, E = 256 25.6 -> 21.7; with one
+// T = 65536, E = 128, k = 8 37.0 -> 32.5 us, T = 16384, E = 256 25.6 -> 20.7; with one
 // or two experts a lane whole keys are faster (T = 16384, E = 8, k = 2 9.1 us and 10.4).
 template <int EPL>
 __device__ __forceinline__ void select_cut(const float (&v)[EPL], const float* logits, int E, int k, int lane,
@@ -116,7 +121,14 @@ __device__ __forceinline__ void select_cut(const float (&v)[EPL], const float* l
     const uint32_t next = __shfl_down_sync(0xffffffffu, mine, 1);
     const bool same = ((mine ^ next) & ~kLow) == 0 && mykey != kNegInfKey;
     const bool doubt = lane < k && same && (mykey < after || lane == k - 1);
-    if (__any_sync(0xffffffffu, doubt)) select_again<EPL>(v, E, k, lane, mykey, myE);
+    if (__any_sync(0xffffffffu, doubt)) {
+        RowLogits<EPL> row;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) row.v[i] = v[i];
+        const uint2 r = select_again<EPL>(row, E, k, lane);
+        mykey = r.x;
+        myE = r.y;
+    }
 }
 
 // One row a warp, expert e = lane + 32 i in register i; the next row's logits are
@@ -128,7 +140,7 @@ __device__ __forceinline__ void select_cut(const float (&v)[EPL], const float* l
 // every run.  All in fp32: fp64 runs at 1/64 of it here.  exp, log and the
 // quotients are the fast ones: within |L - L0| + 4 and 2 units of 2^-24.
 //
-// T = 16384, E = 128, k = 8: 13.5 us for 9.4 MB, which HBM would bring in 1.4.  About
+// T = 16384, E = 128, k = 8: 13.3 us for 9.4 MB, which HBM would bring in 1.4.  About
 // 7 us are fixed -- the launch, the first loads, and the way through memory to the
 // last CTA's sums -- and the rest is instructions: 27 rows a scheduler, 450 cycles
 // each, the selection most of them.
@@ -268,15 +280,16 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_topk_kernel(const
             const int e = o % E;
             float s = 0.0f;
             int c = 0;
-            for (int g0 = o / E; g0 < G; g0 += 19 * groups) {
-                float2 v[19];
+            constexpr int kBatch = 19;  // all of 152 CTAs' in flight with eight groups
+            for (int g0 = o / E; g0 < G; g0 += kBatch * groups) {
+                float2 v[kBatch];
 #pragma unroll
-                for (int i = 0; i < 19; ++i) {  // all of 152 CTAs' in flight with eight groups
+                for (int i = 0; i < kBatch; ++i) {
                     const int g = g0 + i * groups;
                     v[i] = g < G ? __ldcg(p.part + g * E + e) : make_float2(0.0f, 0.0f);
                 }
 #pragma unroll
-                for (int i = 0; i < 19; ++i) { s += v[i].x; c += __float_as_int(v[i].y); }
+                for (int i = 0; i < kBatch; ++i) { s += v[i].x; c += __float_as_int(v[i].y); }
             }
             sm[o] = s;
             csum[o] = c;
