@@ -1093,7 +1093,7 @@ int w4_launch_gemv(const W4Args& a, int rows, int dev, int sms, void* stream) {
 // A warp takes a unit alone when each at work has two or three in turn: T = 32,
 // fine-grained (4608 units) 76.6 us and 73.7, T = 16, Mixtral-shaped (5376) 159 and 154;
 // with fewer some wait long for the last: T = 8, 64 experts of 7168 x 2048 (4096) 183
-// and 193, T = 16, fine-grained (3072) 58 and 61.
+// and 193, T = 24, fine-grained (4224) 69 and 71.
 template <int G>
 int w4_launch_gate_up(const W4Args& a, int rows, int width, int dev, int sms, void* stream) {
     if (width > 8) return w4_plan_launch<kW4GateUp, 2, G>(a, rows, width, dev, sms, stream);
