@@ -441,11 +441,13 @@ int et_block_norm_bwd(const void* x, const void* y, const void* gamma_post, cons
  * may name an expert twice.  1 <= T_max <= 64, 1 <= E <= 256, 1 <= k <=
  * min(E, 8); H and F are inputs and outputs in turn: multiples of group.
  *
- * Products are exact and summed in fp32.  A group's sum is formed before it is
- * scaled, as sum (q + 128) x - 136 sum x: the sum of 143 |x| over a group has
- * to be finite in fp32.  The results are the same
- * bits on every run of a shape.  M, d_M, T and d_T as in et_splitk_gemm and
- * et_moe_layer.  Errors as et_moe_layer.
+ * Products (q - 8) x are exact and summed in fp32; a group's sum is scaled in
+ * fp32 when it is complete, so the sum of |(q - 8) x| over a group has to be
+ * finite in fp32.  An input whose weight is 0 adds nothing, whatever its size.
+ * The error of a sum before its rounding to bf16 is at most
+ * 2^-23 (K + K / group + 16) sum |w x|.  The results are the same bits on every
+ * run of a shape.  M, d_M, T and d_T as in et_splitk_gemm and et_moe_layer.
+ * Errors as et_moe_layer.
  * ---------------------------------------------------------------------- */
 int et_w4_quantize(const void* w, void* q, void* scale, int E, int N, int K, int group,
                    void* stream);

@@ -48,16 +48,22 @@ struct W4Args {
     uint32_t magic;           // 0x43004300 (see unpack8)
 };
 
-// Eight 4-bit values -> four packed pairs of 128 + q in bf16, pairs (0,4) (1,5)
+// Eight 4-bit values -> four packed pairs of q - 8 in bf16, pairs (0,4) (1,5)
 // (2,6) (3,7).  0x4300 is 128.0 with a unit of 1 in its last place, so or-ing a
-// nibble in gives 128 + q exactly; the 136 too many of each value are taken off
-// once a group, by starting its sum at -136 sum(x).  `magic` (0x43004300) comes
-// from a kernel parameter, because a second constant known to the compiler
-// makes and-or two operations instead of one.
+// nibble in gives 128 + q exactly, and taking 136 off is exact too: what is
+// multiplied is the weight itself, so a large x whose weight is 0 adds nothing.
+// (Summing (128 + q) x and taking 136 sum(x) off saved 4 % of the time -- T = 4,
+// Mixtral-shaped, 111 us in place of 116 -- and left the rounding of 136 |x| in the
+// sum.  A packed subtraction in place of the fma: 117.)  `magic` (0x43004300) comes
+// from a kernel parameter, because a second constant known to the compiler makes
+// and-or two operations instead of one.
 __device__ __forceinline__ void unpack8(uint32_t v, uint32_t magic, uint32_t (&o)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(o[i]) : "r"(v >> (4 * i)), "r"(magic));
+    for (int i = 0; i < 4; ++i) {
+        uint32_t b;
+        asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(b) : "r"(v >> (4 * i)), "r"(magic));
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(o[i]) : "r"(b), "r"(0x3f803f80u), "r"(0xc308c308u));  // b * 1 - 136
+    }
 }
 
 // d = a b + c
@@ -105,22 +111,17 @@ __device__ __forceinline__ void ld_words(const uint8_t* a, uint32_t (&v)[W]) {
 }
 
 // One k-block: acc += scale * sum((q - 8) x) over each group, the products exact,
-// summed in fp32 by the tensor core, the scale applied in fp32 after it.  The
-// sum starts at -136 sum(x), a product of x with a matrix of -136 (exact in
-// bf16), and adds (128 + q) x: 30 times the magnitude of (q - 8) x, which costs
-// 5 of the fp32 sum's 24 bits and leaves 10 more than the bf16 result keeps.
+// summed in fp32 by the tensor core, the scale applied in fp32 after it.
 template <int NT, int G>
 __device__ __forceinline__ void compute_stage(const W4Stage& st, int nc, uint32_t magic,
                                               float (&acc)[4][NT][4]) {
     constexpr int W = G / 32;  // words of a lane and row in a group
     const int lane = threadIdx.x & 31;
     const int r = lane >> 2, t = lane & 3;
-    const uint32_t neg = 0xc308c308u;  // -136, twice
-    const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int g = 0; g < kW4Blk / G; ++g) {
         uint32_t b[W][NT][4];
-        float off[NT][4];
 #pragma unroll
         for (int i = 0; i < W; ++i)
 #pragma unroll
@@ -132,16 +133,6 @@ __device__ __forceinline__ void compute_stage(const W4Stage& st, int nc, uint32_
                 b[i][j][2] = __byte_perm(v.y, v.w, 0x5410);
                 b[i][j][3] = __byte_perm(v.y, v.w, 0x7632);
             }
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            mma16816(off[j], neg, neg, neg, neg, b[0][j][0], b[0][j][1], zero);
-            mma16816(off[j], neg, neg, neg, neg, b[0][j][2], b[0][j][3], off[j]);
-#pragma unroll
-            for (int i = 1; i < W; ++i) {
-                mma16816(off[j], neg, neg, neg, neg, b[i][j][0], b[i][j][1], off[j]);
-                mma16816(off[j], neg, neg, neg, neg, b[i][j][2], b[i][j][3], off[j]);
-            }
-        }
         // MC row tiles at a time: their chains of products are independent, which hides
         // the tensor core's latency when few warps are there to do it
         constexpr int MC = 1;
@@ -167,7 +158,7 @@ __device__ __forceinline__ void compute_stage(const W4Stage& st, int nc, uint32_
                     unpack8(hi[m][i], magic, v);
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
-                        mma16816(part[m][j], u[0], v[0], u[1], v[1], b[i][j][0], b[i][j][1], i == 0 ? off[j] : part[m][j]);
+                        mma16816(part[m][j], u[0], v[0], u[1], v[1], b[i][j][0], b[i][j][1], i == 0 ? zero : part[m][j]);
                         mma16816(part[m][j], u[2], v[2], u[3], v[3], b[i][j][2], b[i][j][3], part[m][j]);
                     }
                 }
@@ -429,7 +420,7 @@ __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, in
 // 111 us, 66 % of the copy rate; T = 32, fine-grained: 74 us, 56 %; M = 1, 4096 x
 // 14336: 10.3 us, 43 %, of which 3.4 are spent before and after the items.  Not
 // kept, since they gained nothing: deeper rings, several row tiles interleaved,
-// the -136 sum(x) taken apart from the chain, sums pushed to one CTA of a cluster.
+// sums pushed to one CTA of a cluster.
 template <int MODE, int NT, int G, int W>
 struct W4Shape {
     static constexpr int RW = NT;                             // row groups
