@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from tests import ref_ops as ref
+from tests import ref_w4
 from tests.test_w4_gpu import _cuda, _experts, _experts_inputs, _gemv, _gen
 
 pytestmark = pytest.mark.gpu
@@ -60,3 +61,14 @@ def test_experts_large_inputs_of_zero_weights(cuda_lib, T, H, F, En, k, group):
     got, _ = _experts(cuda_lib, x, idx, w, gate, up, down, ws=ws)
     assert torch.isfinite(want).all() and float(want.abs().max()) > 0
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("T,H,F,En,k,group", ref_w4.SIZES)
+def test_experts_of_exact_products(cuda_lib, T, H, F, En, k, group):
+    """Gate and up products are exact here, which leaves a bound small enough to show one lost row or 32 lost inputs."""
+    a = ref_w4.inputs(T, H, F, En, k, group, T + H)
+    out, ws = _experts(cuda_lib, *a)
+    want, bound = ref_w4.experts(*a)
+    ref.check(out, want, ref_w4.tolerance(want, bound), "out")
+    assert torch.equal(out, _experts(cuda_lib, *a, ws=ws)[0])
+    assert cuda_lib.et_status(ws) == (0, 0)
