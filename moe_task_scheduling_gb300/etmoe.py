@@ -12,8 +12,6 @@ import functools
 import os
 from typing import Optional
 
-import torch
-
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libetmoe.so")
 
@@ -122,6 +120,7 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        import torch
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -137,6 +136,7 @@ def _opts(timeout_us=0, fault_mode=0, fault_arg=0, trace=None):
 
 def alloc_trace(records: int, device="cuda"):
     """A zeroed device buffer for `records` trace records (see et_opts.trace)."""
+    import torch
     return torch.zeros(32 + 32 * records, dtype=torch.uint8, device=device)
 
 
@@ -182,6 +182,7 @@ def et_mlp_workspace_bytes(B_max, H, F) -> int:
 
 def alloc_workspace(nbytes: int, device="cuda"):
     """A zeroed, 256-byte aligned byte buffer (torch owns the memory)."""
+    import torch
     if nbytes <= 0:
         raise ValueError("invalid workspace size (shape rejected by the library)")
     return torch.zeros(nbytes, dtype=torch.uint8, device=device)
@@ -336,7 +337,18 @@ def et_mlp_chain(x, gamma, eps, w_gate, w_up, w_down, out, *, B=None, d_B=None, 
 # contiguity and device (ValueError).  They run on the tensors' device, on
 # `stream` or else that device's current stream.
 
-_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+torch = None  # imported by the first of these calls: the library opens without it
+
+
+def _bind_torch():
+    """Names that every call needs, and the current stream's handle without building a Stream object
+    (3 us of a call that takes 8) and the current device, where this torch has them."""
+    global torch, _BF16, _F32, _I32, _U8, _raw_stream, _current_device
+    import torch as t
+    _BF16, _F32, _I32, _U8 = t.bfloat16, t.float32, t.int32, t.uint8
+    _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or (lambda dev: t.cuda.current_stream(dev).cuda_stream)
+    _current_device = getattr(t._C, "_cuda_getDevice", None) or t.cuda.current_device
+    torch = t  # last: another thread that sees it finds the rest
 
 
 def _arg(t, name, dtype, shape, dev):
@@ -353,7 +365,9 @@ def _arg(t, name, dtype, shape, dev):
 
 
 def _device_of(t, name):
-    """Index of the CUDA device that holds `t`."""
+    """Index of the CUDA device that holds `t`: the first step of each of these calls."""
+    if torch is None:
+        _bind_torch()
     dev = t.get_device()  # -1 on the CPU
     if dev >= 0:
         return dev
@@ -374,13 +388,6 @@ def _count_arg(d_n, dev):
     if d_n.dtype is not _I32 or d_n.numel() != 1 or d_n.get_device() != dev:
         raise ValueError(f"a device count must be one int32 on CUDA device {dev}")
     return d_n.data_ptr()
-
-
-# The current stream's handle without building a Stream object (3 us of a call
-# that takes 8), and the current device, where this torch has them.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(fn, dev, stream, args, check):
