@@ -382,6 +382,29 @@ def _workspace_args(workspace, dev):
     return workspace.data_ptr(), workspace.numel()
 
 
+# The C calls take sizes and counts as 32-bit integers, and ctypes would cut a larger one to its low half.
+_INT_MAX = (1 << 31) - 1
+
+
+def _fits(sizes):
+    """Refuses sizes (or-ed together) of more than 31 bits."""
+    if sizes > _INT_MAX:
+        raise ValueError("sizes must be below 2^31")
+
+
+def _rows(n, n_max):
+    """The host's count of rows: all of them where it is not given."""
+    if n is None:
+        return n_max
+    if not -_INT_MAX <= n <= _INT_MAX:
+        raise ValueError(f"a count of rows must be in [0, {n_max}], not {n}")
+    return n
+
+
+def _workspace_bytes(fn, *sizes):
+    return fn(*sizes) if max(sizes) <= _INT_MAX and min(sizes) >= 0 else 0
+
+
 def _count_arg(d_n, dev):
     if d_n is None or isinstance(d_n, int):
         return d_n
@@ -405,7 +428,7 @@ def _call(fn, dev, stream, args, check):
 
 @functools.lru_cache(maxsize=None)
 def et_router_topk_workspace_bytes(T_max, E, k) -> int:
-    return load().et_router_topk_workspace_bytes(T_max, E, k)
+    return _workspace_bytes(load().et_router_topk_workspace_bytes, T_max, E, k)
 
 
 def et_router_topk(logits, topk_idx, topk_w, *, token_mask=None, expert_counts=None, n_routed=None,
@@ -414,13 +437,14 @@ def et_router_topk(logits, topk_idx, topk_w, *, token_mask=None, expert_counts=N
     dev = _device_of(logits, "logits")
     T_max, E = logits.shape
     k = topk_idx.shape[-1]
+    _fits(T_max | E | k)
     ws, wsb = _workspace_args(workspace, dev)
     return _call(load().et_router_topk, dev, stream, (
         _arg(logits, "logits", _F32, (T_max, E), dev), _arg(token_mask, "token_mask", _U8, (T_max,), dev),
         _arg(topk_idx, "topk_idx", _I32, (T_max, k), dev), _arg(topk_w, "topk_w", _F32, (T_max, k), dev),
         _arg(expert_counts, "expert_counts", _I32, (E,), dev), _arg(n_routed, "n_routed", _I32, (1,), dev),
         _arg(mean_prob, "mean_prob", _F32, (E,), dev), _arg(losses, "losses", _F32, (2,), dev),
-        T_max if T is None else T, _count_arg(d_T, dev), T_max, E, k, ws, wsb), check)
+        _rows(T, T_max), _count_arg(d_T, dev), T_max, E, k, ws, wsb), check)
 
 
 def et_router_topk_bwd(logits, topk_idx, topk_w, expert_counts, n_routed, d_logits, *, token_mask=None,
@@ -429,6 +453,7 @@ def et_router_topk_bwd(logits, topk_idx, topk_w, expert_counts, n_routed, d_logi
     dev = _device_of(logits, "logits")
     T_max, E = logits.shape
     k = topk_idx.shape[-1]
+    _fits(T_max | E | k)
     ws, wsb = _workspace_args(workspace, dev)
     return _call(load().et_router_topk_bwd, dev, stream, (
         _arg(logits, "logits", _F32, (T_max, E), dev), _arg(token_mask, "token_mask", _U8, (T_max,), dev),
@@ -436,12 +461,12 @@ def et_router_topk_bwd(logits, topk_idx, topk_w, expert_counts, n_routed, d_logi
         _arg(expert_counts, "expert_counts", _I32, (E,), dev), _arg(n_routed, "n_routed", _I32, (1,), dev),
         _arg(d_losses, "d_losses", _F32, (2,), dev), _arg(d_topk_w, "d_topk_w", _F32, (T_max, k), dev),
         _arg(d_logits, "d_logits", _F32, (T_max, E), dev),
-        T_max if T is None else T, _count_arg(d_T, dev), T_max, E, k, ws, wsb), check)
+        _rows(T, T_max), _count_arg(d_T, dev), T_max, E, k, ws, wsb), check)
 
 
 @functools.lru_cache(maxsize=None)
 def et_block_norm_workspace_bytes(T_max, H) -> int:
-    return load().et_block_norm_workspace_bytes(T_max, H)
+    return _workspace_bytes(load().et_block_norm_workspace_bytes, T_max, H)
 
 
 def _gate(gate, T_max, H, dev):
@@ -460,13 +485,14 @@ def et_block_norm(x, y, x_out, x_hat, *, gamma_post=None, gate=None, scale=1.0, 
     """x_out = x + scale * gate * RMSNorm(y) * gamma_post and x_hat = RMSNorm(x_out) * gamma_pre."""
     dev = _device_of(x, "x")
     T_max, H = rows = x.shape
+    _fits(T_max | H)
     kind, pgate, _, _ = _gate(gate, T_max, H, dev)
     ws, wsb = _workspace_args(workspace, dev)
     return _call(load().et_block_norm, dev, stream, (
         _arg(x, "x", _BF16, rows, dev), _arg(y, "y", _BF16, rows, dev),
         _arg(gamma_post, "gamma_post", _BF16, (H,), dev), pgate, kind, scale,
         _arg(gamma_pre, "gamma_pre", _BF16, (H,), dev), eps, _arg(x_out, "x_out", _BF16, rows, dev),
-        _arg(x_hat, "x_hat", _BF16, rows, dev), T_max if T is None else T, _count_arg(d_T, dev), T_max, H,
+        _arg(x_hat, "x_hat", _BF16, rows, dev), _rows(T, T_max), _count_arg(d_T, dev), T_max, H,
         ws, wsb), check)
 
 
@@ -476,6 +502,7 @@ def et_block_norm_bwd(x, y, d_x_out, d_x_hat, dx, dy, *, gamma_post=None, gate=N
     """Gradient of et_block_norm: dx, dy and, where given, the parameters' (fp32; a full gate's bf16)."""
     dev = _device_of(x, "x")
     T_max, H = rows = x.shape
+    _fits(T_max | H)
     kind, pgate, gdt, gsh = _gate(gate, T_max, H, dev)
     if d_gate is not None and gate is None:
         raise ValueError("d_gate needs a gate")
@@ -487,7 +514,7 @@ def et_block_norm_bwd(x, y, d_x_out, d_x_hat, dx, dy, *, gamma_post=None, gate=N
         _arg(d_x_hat, "d_x_hat", _BF16, rows, dev), _arg(dx, "dx", _BF16, rows, dev),
         _arg(dy, "dy", _BF16, rows, dev), _arg(d_gamma_post, "d_gamma_post", _F32, (H,), dev),
         _arg(d_gamma_pre, "d_gamma_pre", _F32, (H,), dev), _arg(d_gate, "d_gate", gdt, gsh, dev),
-        T_max if T is None else T, _count_arg(d_T, dev), T_max, H, ws, wsb), check)
+        _rows(T, T_max), _count_arg(d_T, dev), T_max, H, ws, wsb), check)
 
 
 def _w4(q, scale, name, lead, N, K, dev):
@@ -508,6 +535,7 @@ def _w4_convert(w, q, scale):
     *lead, N, K = w.shape
     if len(lead) > 1:
         raise ValueError(f"w must be [N, K] or [E, N, K], not {tuple(w.shape)}")
+    _fits(N | K | (lead[0] if lead else 1))
     pq, ps, group = _w4(q, scale, "q", lead, N, K, dev)
     return dev, _arg(w, "w", _BF16, w.shape, dev), pq, ps, (lead[0] if lead else 1, N, K, group)
 
@@ -527,7 +555,7 @@ def et_w4_dequantize(q, scale, w, *, stream=None, check=True):
 
 @functools.lru_cache(maxsize=None)
 def et_w4_gemv_workspace_bytes(M_max, N, K, group) -> int:
-    return load().et_w4_gemv_workspace_bytes(M_max, N, K, group)
+    return _workspace_bytes(load().et_w4_gemv_workspace_bytes, M_max, N, K, group)
 
 
 def et_w4_gemv(X, q, scale, Y, *, M=None, d_M=None, workspace, stream=None, check=True):
@@ -535,16 +563,17 @@ def et_w4_gemv(X, q, scale, Y, *, M=None, d_M=None, workspace, stream=None, chec
     dev = _device_of(X, "X")
     M_max, K = X.shape
     N = Y.shape[-1]
+    _fits(M_max | N | K)
     pq, ps, group = _w4(q, scale, "q", (), N, K, dev)
     ws, wsb = _workspace_args(workspace, dev)
     return _call(load().et_w4_gemv, dev, stream, (
         _arg(X, "X", _BF16, (M_max, K), dev), pq, ps, _arg(Y, "Y", _BF16, (M_max, N), dev),
-        M_max if M is None else M, _count_arg(d_M, dev), M_max, N, K, group, ws, wsb), check)
+        _rows(M, M_max), _count_arg(d_M, dev), M_max, N, K, group, ws, wsb), check)
 
 
 @functools.lru_cache(maxsize=None)
 def et_w4_experts_workspace_bytes(T_max, H, F, E, k, group) -> int:
-    return load().et_w4_experts_workspace_bytes(T_max, H, F, E, k, group)
+    return _workspace_bytes(load().et_w4_experts_workspace_bytes, T_max, H, F, E, k, group)
 
 
 def et_w4_experts(x, topk_idx, topk_w, q_gate, s_gate, q_up, s_up, q_down, s_down, out, *, T=None, d_T=None,
@@ -554,6 +583,7 @@ def et_w4_experts(x, topk_idx, topk_w, q_gate, s_gate, q_up, s_up, q_down, s_dow
     T_max, H = x.shape
     E, F = q_gate.shape[:2]
     k = topk_idx.shape[-1]
+    _fits(T_max | H | F | E | k)
     pqg, psg, group = _w4(q_gate, s_gate, "q_gate", (E,), F, H, dev)
     pqu, psu, gu = _w4(q_up, s_up, "q_up", (E,), F, H, dev)
     pqd, psd, gd = _w4(q_down, s_down, "q_down", (E,), H, F, dev)
@@ -563,7 +593,7 @@ def et_w4_experts(x, topk_idx, topk_w, q_gate, s_gate, q_up, s_up, q_down, s_dow
     return _call(load().et_w4_experts, dev, stream, (
         _arg(x, "x", _BF16, (T_max, H), dev), _arg(topk_idx, "topk_idx", _I32, (T_max, k), dev),
         _arg(topk_w, "topk_w", _F32, (T_max, k), dev), pqg, psg, pqu, psu, pqd, psd,
-        _arg(out, "out", _BF16, (T_max, H), dev), T_max if T is None else T, _count_arg(d_T, dev), T_max, H, F, E, k,
+        _arg(out, "out", _BF16, (T_max, H), dev), _rows(T, T_max), _count_arg(d_T, dev), T_max, H, F, E, k,
         group, ws, wsb), check)
 
 
