@@ -49,6 +49,26 @@ cudaError_t api_smem_opt_in(SmemOptIn& st, int dev, K kernel, int bytes) {
     return e;
 }
 
+// N numbers that queries of the runtime give for a kernel, kept for each device:
+// another device may have other SMs and other places for clusters.  A query that
+// fails is not kept, its error goes to the caller.
+template <int N>
+struct DeviceNumbers {
+    int kept[kApiMaxDevices][N] = {};  // the number + 1; 0: not asked yet
+    template <class Q>
+    cudaError_t get(int dev, int at, int* value, Q&& query) {
+        const int k = __atomic_load_n(&kept[dev][at], __ATOMIC_RELAXED);
+        if (k) {
+            *value = k - 1;
+            return cudaSuccess;
+        }
+        *value = 0;
+        const cudaError_t e = query(value);
+        if (e == cudaSuccess) __atomic_store_n(&kept[dev][at], *value + 1, __ATOMIC_RELAXED);
+        return e;
+    }
+};
+
 // One launch; cluster: CTAs a cluster; early: it may be scheduled while the
 // kernel before it drains (its kernel then waits, see grid_wait in ops_device.cuh).
 // The error is this launch's own (cudaGetLastError could return an older one of

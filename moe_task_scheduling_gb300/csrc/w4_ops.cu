@@ -936,16 +936,10 @@ bool w4_shape_ok(int N, int K, int group, std::string* why) {
 
 // How many clusters of c CTAs of a kernel fit the GPU at once when n of its CTAs
 // fit an SM (a cluster lies within one of the GPU's processor clusters, so some
-// places stay empty).  Asked for once and kept: it depends on nothing else.
-struct W4Fit {
-    int clusters[4][33] = {};  // [log2 c][n], 0: not asked yet
-};
+// places stay empty).
+constexpr int kW4FitMax = 32;  // most CTAs an SM
 template <class K>
-int w4_fit(W4Fit& f, K kernel, int threads, int c, int n) {
-    const int lc = c == 8 ? 3 : c == 4 ? 2 : c == 2 ? 1 : 0;
-    n = n < 1 ? 1 : n > 32 ? 32 : n;
-    int v = __atomic_load_n(&f.clusters[lc][n], __ATOMIC_RELAXED);
-    if (v) return v;
+cudaError_t w4_query_clusters(K kernel, int threads, int c, int n, int* clusters) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(c * 1024);
     cfg.blockDim = dim3(threads);
@@ -958,9 +952,7 @@ int w4_fit(W4Fit& f, K kernel, int threads, int c, int n) {
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&v, kernel, &cfg) != cudaSuccess || v < 1) v = 1;
-    __atomic_store_n(&f.clusters[lc][n], v, __ATOMIC_RELAXED);
-    return v;
+    return cudaOccupancyMaxActiveClusters(clusters, kernel, &cfg);
 }
 
 // Most segments of R routed rows: each has a row, an expert has one and one more for
@@ -977,10 +969,18 @@ struct W4Plan {
     long long cost;       // estimated ns (kW4Gemv)
 };
 
+// The clusters that fit device `dev`; 0 and an error in *err if the query failed.
 template <int MODE, int NT, int G, int W>
-int w4_fit(int c, int n) {
-    static W4Fit fits;
-    return w4_fit(fits, w4_kernel<MODE, NT, G, W>, W * 32, c, n);
+int w4_fit(int dev, int c, int n, cudaError_t* err) {
+    static DeviceNumbers<4 * kW4FitMax> fits;
+    n = n < 1 ? 1 : n > kW4FitMax ? kW4FitMax : n;
+    const int lc = c == 8 ? 3 : c == 4 ? 2 : c == 2 ? 1 : 0;
+    int v = 0;
+    const cudaError_t e = fits.get(dev, lc * kW4FitMax + n - 1, &v, [&](int* out) {
+        return w4_query_clusters(w4_kernel<MODE, NT, G, W>, W * 32, c, n, out);
+    });
+    if (e != cudaSuccess) *err = e;
+    return e == cudaSuccess ? v : 0;
 }
 
 // `rows` tokens at most; x_rows <= 8 NT of them (or of an expert's rows) a pass.
@@ -1001,16 +1001,22 @@ int w4_plan(const W4Args& a, int rows, int x_rows, int dev, int sms, W4Plan* pl)
     static SmemOptIn opt;
     const cudaError_t e = api_smem_opt_in(opt, dev, w4_kernel<MODE, NT, G, W>, kSmemLimit);
     if (e != cudaSuccess) return api_fail_cuda(e, "cudaFuncSetAttribute(4-bit products)");
-    static const int regs = [] {
+    static DeviceNumbers<1> kept_regs;
+    int regs = 0;
+    cudaError_t err = kept_regs.get(dev, 0, &regs, [](int* out) {
         cudaFuncAttributes at{};
-        return cudaFuncGetAttributes(&at, w4_kernel<MODE, NT, G, W>) == cudaSuccess ? at.numRegs : 255;
-    }();
+        const cudaError_t q = cudaFuncGetAttributes(&at, w4_kernel<MODE, NT, G, W>);
+        *out = at.numRegs;
+        return q;
+    });
+    if (err != cudaSuccess) return api_fail_cuda(err, "cudaFuncGetAttributes(4-bit products)");
     const int by_smem = kSmemSm / (smem + 1024), by_regs = 65536 / (W * 32 * ((regs + 7) / 8 * 8));
     const int per_sm = W > kW4Warps ? 1 : by_smem < by_regs ? by_smem : by_regs;
     // 8, 4 or 2 CTAs share a unit's inputs if all of them fit at once and every split
     // keeps two k-blocks
     int c = alone ? 1 : kW4ClusterMax;
-    while (c > 1 && (blocks < 2ll * S::KW * c || units > w4_fit<MODE, NT, G, W>(c, per_sm))) c /= 2;
+    while (c > 1 && (blocks < 2ll * S::KW * c || units > w4_fit<MODE, NT, G, W>(dev, c, per_sm, &err))) c /= 2;
+    if (err != cudaSuccess) return api_fail_cuda(err, "cudaOccupancyMaxActiveClusters(4-bit products)");
     // The k-blocks of a warp of the busiest SM, its CTAs taken one after the other.  On 108
     // calls (9 to 64 rows, 768 x 2048 to 28672 x 8192) the estimate below was within 10 % of
     // the measured time in seven of eight; the faster side was taken in 104, and 7 % lost at
@@ -1024,7 +1030,7 @@ int w4_plan(const W4Args& a, int rows, int x_rows, int dev, int sms, W4Plan* pl)
 }
 
 template <int MODE, int NT, int G, int W>
-int w4_launch(W4Args a, int rows, int x_rows, const W4Plan& pl, int sms, void* stream) {
+int w4_launch(W4Args a, int rows, int x_rows, const W4Plan& pl, int dev, int sms, void* stream) {
     if (!pl.per_sm) return api_fail(ET_ERR_UNSUPPORTED, "rows do not fit in shared memory");
     a.x_rows = x_rows;
     a.sum_rows = MODE == kW4Down ? rows : x_rows;
@@ -1047,7 +1053,9 @@ int w4_launch(W4Args a, int rows, int x_rows, const W4Plan& pl, int sms, void* s
     int smem = pl.smem;
     if (early) {
         int n = static_cast<int>((grid + sms - 1) / sms);
-        while (n < pl.per_sm && w4_fit<MODE, NT, G, W>(pl.c, n) * static_cast<long long>(pl.c) < grid) ++n;
+        cudaError_t err = cudaSuccess;
+        while (n < pl.per_sm && w4_fit<MODE, NT, G, W>(dev, pl.c, n, &err) * static_cast<long long>(pl.c) < grid) ++n;
+        if (err != cudaSuccess) return api_fail_cuda(err, "cudaOccupancyMaxActiveClusters(4-bit products)");
         const int more = kSmemSm / (n + 1) / 128 * 128 - 1024 + 128;  // n + 1 do not fit
         smem = smem > more ? smem : more < kSmemLimit ? more : kSmemLimit;
     }
@@ -1061,7 +1069,7 @@ template <int MODE, int NT, int G>
 int w4_plan_launch(const W4Args& a, int rows, int x_rows, int dev, int sms, void* stream) {
     W4Plan pl{};
     const int rc = w4_plan<MODE, NT, G, kW4Warps>(a, rows, x_rows, dev, sms, &pl);
-    return rc ? rc : w4_launch<MODE, NT, G, kW4Warps>(a, rows, x_rows, pl, sms, stream);
+    return rc ? rc : w4_launch<MODE, NT, G, kW4Warps>(a, rows, x_rows, pl, dev, sms, stream);
 }
 
 // With 9 rows or more: 8 a pass (one tile of columns in every product) or 16 (two),
@@ -1077,8 +1085,8 @@ int w4_launch_gemv(const W4Args& a, int rows, int dev, int sms, void* stream) {
     int rc = w4_plan<kW4Gemv, 1, G, kW4Warps>(a, rows, one_rows, dev, sms, &one);
     if (!rc && rows > 8) rc = w4_plan<kW4Gemv, 2, G, kW4Warps>(a, rows, two_rows, dev, sms, &two);
     if (rc) return rc;
-    if (rows <= 8 || one.cost <= two.cost) return w4_launch<kW4Gemv, 1, G, kW4Warps>(a, rows, one_rows, one, sms, stream);
-    return w4_launch<kW4Gemv, 2, G, kW4Warps>(a, rows, two_rows, two, sms, stream);
+    if (rows <= 8 || one.cost <= two.cost) return w4_launch<kW4Gemv, 1, G, kW4Warps>(a, rows, one_rows, one, dev, sms, stream);
+    return w4_launch<kW4Gemv, 2, G, kW4Warps>(a, rows, two_rows, two, dev, sms, stream);
 }
 
 // A warp takes a unit alone when each at work has two or three in turn: T = 32,
@@ -1132,8 +1140,8 @@ int w4_launch_down(const W4Args& a, int rows, int width, int dev, int sms, void*
     const long long each = (units + 4 * sms - 1) / (4 * sms);
     const long long alone_ns = KB * w4_item_ns(each <= 3 ? each * 4 * sms : units, sms) + 2500;
     if (pl.per_sm && shared_ns <= alone_ns)
-        return wide ? w4_launch<kW4Down, 1, G, kW4WarpsMax>(a, rows, width, pl, sms, stream)
-                    : w4_launch<kW4Down, 1, G, kW4Warps>(a, rows, width, pl, sms, stream);
+        return wide ? w4_launch<kW4Down, 1, G, kW4WarpsMax>(a, rows, width, pl, dev, sms, stream)
+                    : w4_launch<kW4Down, 1, G, kW4Warps>(a, rows, width, pl, dev, sms, stream);
     if ((rc = w4_plan_launch<kW4DownAlone, 1, G>(a, rows, width, dev, sms, stream))) return rc;
     const W4CombineArgs ca{a.y, a.idx, a.out, a.d_T, a.T_host, a.T_max, a.N, a.E, a.k, a.hdr};
     const cudaError_t e = api_launch(w4_combine_kernel, dim3((a.N + 1023) / 1024, rows), 256, 0, stream, ca);
