@@ -16,6 +16,7 @@ enum GateKind { kGateNone = 0, kGateChannel = 1, kGateToken = 2, kGateFull = 3 }
 
 constexpr int kNormHMax = 16384;
 constexpr int kNormParts = 304;  // most CTAs of the backward kernel = rows of partial sums
+constexpr int kNormChain = 256;  // most rows that a thread adds up where parameter gradients are wanted
 
 struct NormArgs {
     const bf16* x;           // [T, H]
@@ -38,6 +39,7 @@ struct NormArgs {
     bf16* dy;
     bf16* d_gate_full;       // [T, H]
     float* d_gate_token;     // [T]
+    int row0, row_end;       // the rows of this launch
     int part_of;             // which parameter gradients are wanted (bit 0 post, 1 pre, 2 gate)
     float* part;             // [kNormParts][3][H]: d_gamma_post, d_gamma_pre, d_gate per channel
 };
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(con
     const RowGroup<MODE> g(p.row_threads);
     grid_begin();
     bool ok;
-    const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
+    const int T = min(row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok), p.row_end);
     if (!ok) return;
     const int H = p.H;
     const bool post = p.y && p.gamma_post;
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(con
         return base ? load8<VEC>(base + off, g, j, H) : Vec8{};
     };
 
-    for (int t = blockIdx.x * g.groups() + g.id(); t < T; t += gridDim.x * g.groups()) {
+    for (int t = p.row0 + blockIdx.x * g.groups() + g.id(); t < T; t += gridDim.x * g.groups()) {
         const size_t off = static_cast<size_t>(t) * H;
         const float gs = p.scale * (p.gate_kind == kGateToken ? static_cast<const float*>(p.gate)[t] : 1.0f);
         auto gate_of = [&](int j, float* q) {  // scale * gate of vector j
@@ -453,7 +455,7 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) norm_bwd_staged_kernel(const
     const RowGroup<MODE> grp(p.row_threads);
     grid_begin();
     bool ok;
-    const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
+    const int T = min(row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok), p.row_end);
     if (!ok) return;
     const int H = p.H, H2 = H * 2;
     const bool post = p.gamma_post != nullptr;
@@ -498,7 +500,7 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) norm_bwd_staged_kernel(const
         cp_async_commit();
     };
     int buf = 0;
-    const int t0 = blockIdx.x * grp.groups() + grp.id(), step = gridDim.x * grp.groups();
+    const int t0 = p.row0 + blockIdx.x * grp.groups() + grp.id(), step = gridDim.x * grp.groups();
     stage(t0, 0);
     // the parameters, 1 for a missing gamma_post; every thread reads back what it wrote
     // (the groups write the same)
@@ -642,6 +644,7 @@ struct NormSumArgs {
     int H, parts;
     const int32_t* d_T;
     int T_max;
+    bool add;       // to what an earlier launch of the call has put there
 };
 
 // Column sums of the partial rows: 32 columns x 32 row groups a CTA, so that the
@@ -665,7 +668,10 @@ __global__ void __launch_bounds__(1024) norm_sum_kernel(const NormSumArgs p) {
     red[grp][lane] = s;
     __syncthreads();
     s = warp_sum(red[lane][grp]);  // warp grp: its column's 32 groups
-    if (lane == 0 && blockIdx.x * 32 + grp < p.H) out[blockIdx.x * 32 + grp] = s;
+    if (lane == 0 && blockIdx.x * 32 + grp < p.H) {
+        float* o = out + blockIdx.x * 32 + grp;
+        *o = p.add ? *o + s : s;
+    }
 }
 
 size_t norm_ws_bytes(int T_max, int H) {
@@ -888,26 +894,37 @@ int et_block_norm_bwd(const void* x, const void* y, const void* gamma_post, cons
         a.part_of = (d_gamma_post ? 1 : 0) | (d_gamma_pre ? 2 : 0) | (gate_kind == kGateChannel && d_gate ? 4 : 0);
         const int parts_max = T_max < kNormParts ? T_max : kNormParts;
         const int rows = d_T ? T_max : T;
-        int parts = 0;
-        if (rows > 0) {
-            const bool vec = norm_vec(H, {x, y, gamma_post, gate_kind == kGateToken ? nullptr : gate, gamma_pre,
-                                          d_x_out, d_x_hat, dx, dy, a.d_gate_full});
-            const NormLaunch l{dev, sms, rows, parts_max, &parts, stream};
-            const cudaError_t e = vec ? launch_bwd<true>(a, l) : launch_bwd<false>(a, l);
-            if (e != cudaSuccess) return api_fail_cuda(e, "launch of the block norm's backward kernel");
-        }
-        float* d_gate_channel = gate_kind == kGateChannel ? static_cast<float*>(d_gate) : nullptr;
-        NormSumArgs s{a.part, {}, {}, H, parts, d_T, T_max};
-        float* wanted[3] = {d_gamma_post, d_gamma_pre, d_gate_channel};
+        const bool vec = norm_vec(H, {x, y, gamma_post, gate_kind == kGateToken ? nullptr : gate, gamma_pre,
+                                      d_x_out, d_x_hat, dx, dy, a.d_gate_full});
+        NormSumArgs s{a.part, {}, {}, H, 0, d_T, T_max, false};
+        float* wanted[3] = {d_gamma_post, d_gamma_pre, gate_kind == kGateChannel ? static_cast<float*>(d_gate) : nullptr};
         int n = 0;
         for (int i = 0; i < 3; ++i)
             if (wanted[i]) {
                 s.out[n] = wanted[i];
                 s.arr[n++] = i;
             }
-        if (n) {
-            const cudaError_t e = api_launch(norm_sum_kernel, dim3((H + 31) / 32, n), 1024, 0, stream, s);
-            if (e != cudaSuccess) return api_fail_cuda(e, "launch of the block norm's parameter sums");
+        // Parameter gradients: launches of as many rows as leave no thread with more than
+        // kNormChain to add up, each adding its sums to the ones before.  One chain for all
+        // rows would lose up to 2^-24 of the sum with each (500000 equal rows of H = 2056:
+        // off by 400 x 2^-24).  A launch takes 0.5 ms or more then, its sums 0.01.
+        const int groups = norm_groups(norm_threads(H), rows);
+        const int ctas = norm_threads(H) * groups <= kNormCtaThreads ? kNormParts : kNormParts / 2;
+        const int most = n ? kNormChain * ctas * groups : rows;
+        for (int row0 = 0; row0 < rows || row0 == 0; row0 += most) {
+            a.row0 = row0;
+            a.row_end = rows - row0 < most ? rows : row0 + most;
+            s.add = row0 > 0;
+            if (rows > 0) {
+                const NormLaunch l{dev, sms, a.row_end - row0, parts_max, &s.parts, stream};
+                const cudaError_t e = vec ? launch_bwd<true>(a, l) : launch_bwd<false>(a, l);
+                if (e != cudaSuccess) return api_fail_cuda(e, "launch of the block norm's backward kernel");
+            }
+            if (n) {
+                const cudaError_t e = api_launch(norm_sum_kernel, dim3((H + 31) / 32, n), 1024, 0, stream, s);
+                if (e != cudaSuccess) return api_fail_cuda(e, "launch of the block norm's parameter sums");
+            }
+            if (rows == 0) break;
         }
         return ET_OK;
     });
