@@ -69,7 +69,9 @@ struct EtHeader {
     int32_t gu_split;       // K chunks of a gate/up tile chosen this call
     int32_t ev_sdone;       // shared-expert output tiles complete (fused block)
     int32_t q_wide;         // the down tiles are 256 columns wide this call
-    int32_t reserved[48];
+    int32_t w4_ready;       // 4-bit experts: what came before the gate/up kernel is complete
+    int32_t w4_seen;        // CTAs of the down kernel that have looked at w4_ready
+    int32_t reserved[46];
 };
 static_assert(sizeof(EtHeader) == 256, "header is 256 bytes");
 

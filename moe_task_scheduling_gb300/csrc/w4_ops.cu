@@ -451,16 +451,36 @@ __global__ void __launch_bounds__(W * 32, W == kW4Warps ? 3 : 1) w4_kernel(const
     const int split = kAlone ? 0 : crank * S::KW + kw, splits = kAlone ? 1 : csize * S::KW;
     const int KB = (p.K + kW4Blk - 1) / kW4Blk;
     const int tiles = (p.N + S::kOut - 1) / S::kOut;
-    // The down kernel is scheduled while the gate/up kernel of its call drains.  That
-    // one has waited for everything before it, so only h is not there yet, and
-    // waited for below: routing and the first weights come in meanwhile (T = 1,
-    // fine-grained: 17.1 -> 14.6 us).
+    // The down kernel is scheduled while the gate/up kernel of its call drains.  Routing
+    // and the first weights come in meanwhile, under a flag that gate/up releases when it
+    // has waited for everything before it: who acquires it may read all of that.  Only h
+    // is not there yet, and waited for below.  A CTA that finds no flag waits for gate/up
+    // itself.  Waiting for gate/up first took T = 1, fine-grained, from 14.7 to 15.4 us,
+    // T = 8 from 40.0 to 43.3; reading without the flag, which no rule of the memory model
+    // covers, 14.3 and 40.0.
     if (!kAfter) grid_wait();
-    grid_release();
+    if (kGateUp && blockIdx.x == 0 && threadIdx.x == 0)
+        asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(&p.hdr->w4_ready) : "memory");
+    if (!kGateUp || blockIdx.x > 0 || threadIdx.x == 0) grid_release();  // after the flag
+    int seen = 0;
+    if (kAfter) {
+        if (threadIdx.x == 0) {
+            int ready;
+            asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(ready) : "l"(&p.hdr->w4_ready) : "memory");
+            if (!ready) grid_wait();
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) seen = atomicAdd(&p.hdr->w4_seen, 1);
+    }
+    // The last CTA to look takes the flag back for the next call.
+    auto wait_h = [&]() {
+        grid_wait();
+        if (threadIdx.x == 0 && seen == static_cast<int>(gridDim.x) - 1) p.hdr->w4_ready = p.hdr->w4_seen = 0;
+    };
     bool ok;
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
     if (!ok) {  // the same for every CTA of the cluster
-        if (kAfter) grid_wait();
+        if (kAfter) wait_h();
         return;
     }
 
@@ -575,7 +595,7 @@ __global__ void __launch_bounds__(W * 32, W == kW4Warps ? 3 : 1) w4_kernel(const
     };
     auto post = [&](bool first) {
         if (pu < n_units) post_w();
-        if (kAfter && first) grid_wait();  // in every CTA: who waits for this kernel counts on it
+        if (kAfter && first) wait_h();  // in every CTA: who waits for this kernel counts on it
         if (pu < n_units) {
             post_x();
             slot_off = slot_off + sbytes == ring_len ? 0 : slot_off + sbytes;
