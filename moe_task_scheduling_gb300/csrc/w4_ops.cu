@@ -19,8 +19,8 @@ constexpr int kW4Rows = 64;        // weight rows of a warp (gate/up: 32 of each
 constexpr int kW4Blk = 128;        // inputs of a stage: 64 bytes of a row
 constexpr int kW4Warps = 4;        // of a CTA; the down kernel takes twice as many where that evens its spread
 constexpr int kW4WarpsMax = 8;
-constexpr int kW4Stages = 2;       // k-blocks of a ring: three or four gained nothing (the unpacking, not
-                                   // the memory, sets the pace) and took room from other CTAs
+constexpr int kW4Stages = 2;       // k-blocks of a ring, one computed and one copied: three or four gained nothing (the
+                                   // unpacking, not the memory, sets the pace) and took room from other CTAs
 constexpr int kW4RowsMax = 64;     // most rows of x (tokens)
 constexpr int kW4KMax = 8;         // experts of a token
 constexpr int kW4EMax = 256;
@@ -133,44 +133,33 @@ __device__ __forceinline__ void compute_stage(const W4Stage& st, int nc, uint32_
                 b[i][j][2] = __byte_perm(v.y, v.w, 0x5410);
                 b[i][j][3] = __byte_perm(v.y, v.w, 0x7632);
             }
-        // MC row tiles at a time: their chains of products are independent, which hides
-        // the tensor core's latency when few warps are there to do it
-        constexpr int MC = 1;
         const __nv_bfloat16* sa = reinterpret_cast<const __nv_bfloat16*>(st.s + g * 128) + r;
 #pragma unroll
-        for (int m0 = 0; m0 < 4; m0 += MC) {
-            uint32_t lo[MC][W], hi[MC][W];
-            float s0[MC], s1[MC], part[MC][NT][4];
+        for (int m = 0; m < 4; ++m) {
+            uint32_t lo[W], hi[W];
+            float part[NT][4];
+            const uint8_t* a = st.w + (m * 16 + r) * 64 + (swz_w<G>(g * (G / 32) + (t * W >> 2), r) << 4) + ((t * W & 3) << 2);
+            ld_words<W>(a, lo);
+            ld_words<W>(a + 512, hi);
+            const float s0 = __bfloat162float(sa[m * 16]), s1 = __bfloat162float(sa[m * 16 + 8]);
 #pragma unroll
-            for (int m = 0; m < MC; ++m) {
-                const uint8_t* a = st.w + ((m0 + m) * 16 + r) * 64 + (swz_w<G>(g * (G / 32) + (t * W >> 2), r) << 4) + ((t * W & 3) << 2);
-                ld_words<W>(a, lo[m]);
-                ld_words<W>(a + 512, hi[m]);
-                s0[m] = __bfloat162float(sa[(m0 + m) * 16]);
-                s1[m] = __bfloat162float(sa[(m0 + m) * 16 + 8]);
-            }
-#pragma unroll
-            for (int i = 0; i < W; ++i)
-#pragma unroll
-                for (int m = 0; m < MC; ++m) {
-                    uint32_t u[4], v[4];
-                    unpack8(lo[m][i], magic, u);
-                    unpack8(hi[m][i], magic, v);
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        mma16816(part[m][j], u[0], v[0], u[1], v[1], b[i][j][0], b[i][j][1], i == 0 ? zero : part[m][j]);
-                        mma16816(part[m][j], u[2], v[2], u[3], v[3], b[i][j][2], b[i][j][3], part[m][j]);
-                    }
-                }
-#pragma unroll
-            for (int m = 0; m < MC; ++m)
+            for (int i = 0; i < W; ++i) {
+                uint32_t u[4], v[4];
+                unpack8(lo[i], magic, u);
+                unpack8(hi[i], magic, v);
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    acc[m0 + m][j][0] += s0[m] * part[m][j][0];
-                    acc[m0 + m][j][1] += s0[m] * part[m][j][1];
-                    acc[m0 + m][j][2] += s1[m] * part[m][j][2];
-                    acc[m0 + m][j][3] += s1[m] * part[m][j][3];
+                    mma16816(part[j], u[0], v[0], u[1], v[1], b[i][j][0], b[i][j][1], i == 0 ? zero : part[j]);
+                    mma16816(part[j], u[2], v[2], u[3], v[3], b[i][j][2], b[i][j][3], part[j]);
                 }
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                acc[m][j][0] += s0 * part[j][0];
+                acc[m][j][1] += s0 * part[j][1];
+                acc[m][j][2] += s1 * part[j][2];
+                acc[m][j][3] += s1 * part[j][3];
+            }
         }
     }
 }
@@ -622,8 +611,6 @@ __global__ void __launch_bounds__(W * 32, W == kW4Warps ? 3 : 1) w4_kernel(const
         else asm volatile("bar.sync 2, 64;" ::: "memory");
     };
     post(true);
-#pragma unroll
-    for (int s = 1; s < kW4Stages - 1; ++s) post(false);
 
     int cslot = 0;
     for (int u = u0; u < n_units; u += ustep) {
@@ -640,7 +627,7 @@ __global__ void __launch_bounds__(W * 32, W == kW4Warps ? 3 : 1) w4_kernel(const
         int cpart = kDown && i0 < i1 ? i0 / KB : part_of(u), ckb = i0 - cpart * KB;  // ckb: down only
         int nc = kDown ? (i0 < i1 ? rows_of(cpart) : 0) : rows_of(cpart);
         for (int i = i0; i < i1; ++i) {
-            cp_async_wait<kW4Stages - 2>();
+            cp_async_wait<0>();  // the item's: the next one's are posted below
             meet();
             post(false);
             compute_stage<NT, G>(stage_at(cslot), nc, p.magic, acc);
