@@ -398,18 +398,18 @@ __device__ __forceinline__ void build_routing(const W4Args& p, W4Routing& rt, in
 //              for w4_combine_kernel.  For calls with units enough (w4_launch_gate_up and
 //              w4_launch_down say which).
 //
-// What bounds it.  An item -- 64 weight rows x 128 inputs, 4.2 KB -- takes a
-// scheduler about 670 cycles with warps enough to fill it (257 instructions unpack
-// it, 40 are products, the rest copy and address), and HBM 730 (its share of the
-// measured copy rate).  The products are mma.sync, whose operands are registers: a
-// tcgen05 product takes the weights from shared memory or TMEM, where their four
-// bytes for every byte read would have to be written first, and its rate is not
-// needed for 8 or 16 columns.  Memory and instructions being about even, what remains
-// is launch, latency, and an uneven number of items an SM.  T = 4, Mixtral-shaped:
-// 111 us, 66 % of the copy rate; T = 32, fine-grained: 74 us, 56 %; M = 1, 4096 x
-// 14336: 10.3 us, 43 %, of which 3.4 are spent before and after the items.  Not
-// kept, since they gained nothing: deeper rings, several row tiles interleaved,
-// sums pushed to one CTA of a cluster.
+// What bounds it.  An item -- 64 weight rows x 128 inputs, 4.2 KB -- is about 600
+// instructions of a warp (352 unpack it, 32 are products, the rest copy, scale and
+// address), and a scheduler's share of the measured copy rate brings it in 730 cycles.  The
+// products are mma.sync, whose operands are registers: a tcgen05 product takes the
+// weights from shared memory or TMEM, where their four bytes for every byte read would
+// have to be written first, and its rate is not needed for 8 or 16 columns.  Memory and
+// instructions being about even (issue slots busy 55 %, HBM 4.5 TB/s in a long gate/up
+// product), what remains is launch, latency, and an uneven number of items an SM.  T = 4,
+// Mixtral-shaped: 116 us, 63 % of the copy rate; T = 32, fine-grained: 72 us, 57 %;
+// M = 1, 4096 x 14336: 10.7 us, 42 %, of which 3.4 are spent before and after the items.
+// Not kept, since they gained nothing: deeper rings, several row tiles interleaved, sums
+// pushed to one CTA of a cluster.
 template <int MODE, int NT, int G, int W>
 struct W4Shape {
     static constexpr int RW = NT;                             // row groups
@@ -422,10 +422,9 @@ struct W4Shape {
     static __host__ __device__ int ring_bytes(int x_rows) { return KW * kW4Stages * stage_bytes(x_rows); }
 };
 
-// Three CTAs an SM: 168 registers a thread and twelve warps did more than 128 and
-// sixteen (T = 32, 64 experts of 7168 x 2048: 277 us and 289; five CTAs 313), M = 1,
-// 4096 x 14336 10.3 us and 10.8.  Without a limit two tiles of columns take 240, two
-// CTAs an SM, and T = 32, Mixtral-shaped, 270 us in place of 208.
+// Three CTAs an SM: 168 registers a thread and twelve warps.  With 128 and sixteen, or
+// no limit: T = 32, 64 experts of 7168 x 2048 288 us, 296, 293; T = 32, Mixtral-shaped
+// 206, 223, 218; M = 16, 28672 x 8192 37.1, 39.4, 36.9; M = 1, 4096 x 14336 10.7, 10.7, 11.2.
 template <int MODE, int NT, int G, int W>
 __global__ void __launch_bounds__(W * 32, W == kW4Warps ? 3 : 1) w4_kernel(const W4Args p) {
     using S = W4Shape<MODE, NT, G, W>;
@@ -1024,14 +1023,17 @@ int w4_plan(const W4Args& a, int rows, int x_rows, int dev, int sms, W4Plan* pl)
     int c = alone ? 1 : kW4ClusterMax;
     while (c > 1 && (blocks < 2ll * S::KW * c || units > w4_fit<MODE, NT, G, W>(dev, c, per_sm, &err))) c /= 2;
     if (err != cudaSuccess) return api_fail_cuda(err, "cudaOccupancyMaxActiveClusters(4-bit products)");
-    // The k-blocks of a warp of the busiest SM, its CTAs taken one after the other.  On 108
-    // calls (9 to 64 rows, 768 x 2048 to 28672 x 8192) the estimate below was within 10 % of
-    // the measured time in seven of eight; the faster side was taken in 104, and 7 % lost at
-    // most.  A smaller cluster that evens the SMs' shares is taken too: 4096 x 14336, M = 1
-    // with 8 CTAs (4 on some SMs, 3 on others) 11.3 us, with 4 (2 on most) 10.8.
+    // The k-blocks of a warp of the busiest SM, its CTAs taken one after the other, and
+    // from them the time (W4Plan::cost), which decides between 8 and 16 rows a pass.  On 120
+    // calls (9 to 64 rows, 768 x 768 to 28672 x 16384) the faster side was taken in 112;
+    // the others lost 9 % on average, 23 % at most (M = 9, 2032 x 14976).
     const auto items = [&](int n) { return (units * n + sms - 1) / sms * ((KB + n * S::KW - 1) / (n * S::KW)); };
-    if (MODE == kW4Gemv)
-        while (c > 1 && items(c / 2) < items(c)) c /= 2;
+    // One CTA a unit in place of two where one apiece finds an SM to itself and its warps
+    // have few k-blocks: M = 25, 2368 x 2432 (148 units) 5.0 us in place of 5.7, M = 3, 7576 x
+    // 2560 5.0 and 5.4.  With many, or larger clusters, the CTAs that an SM lacks cost more
+    // than an even share gains: M = 3, 8424 x 15872 24.3 us with one, 19.4 with two; M = 1,
+    // 2432 x 14336 10.1 with four, 9.1 with eight.
+    if (MODE == kW4Gemv && c == 2 && units <= sms && KB <= 8 * S::KW && items(1) < items(2)) c = 1;
     *pl = {units, c, per_sm, smem, NT == 1 ? 3400 + 450 * items(c) : 4800 + 640 * items(c)};
     return ET_OK;
 }
@@ -1046,15 +1048,16 @@ int w4_launch(W4Args a, int rows, int x_rows, const W4Plan& pl, int dev, int sms
     const long long units = w4_is_alone(MODE) ? (pl.units + W - 1) / W : pl.units;  // of a CTA's size
     const bool in_turn = MODE != kW4Down && pl.c == 1 && units > fit;                // CTAs take several
     const long long grid = in_turn ? fit : units * pl.c;
-    // Scheduled while the kernel before drains, which hides the launch (eager calls,
-    // M = 1, 4096 x 14336: 14.5 -> 12.5 us).  Its CTAs then fill the places the other
-    // kernel leaves, so no more of them may fit an SM than an even spread needs:
-    // without that limit M = 16 took 20.4 us, with it 16.3 (18.6 when launched after
-    // the other).  CTAs that take units in turn are launched after the other: they
-    // fill the GPU, and started early they lost 1 to 5 % (Mixtral-shaped, T = 4) --
-    // except after the gate/up kernel where they are short, up to 64 items a scheduler:
-    // 32 experts of 2048 x 768, k = 4, T = 64 36.9 us and 33.8; fine-grained, T = 64 86
-    // and 80, T = 32 73.4 and 74.5; longer ones, 64 of 7168 x 2048, T = 16 245 and 252.
+    // Scheduled while the kernel before drains, which hides the launch (M = 1, 4096 x 14336
+    // 11.0 -> 10.8 us in a graph).  Its CTAs then fill the places the other kernel leaves, so
+    // no more of them may fit an SM than an even spread needs: without that limit M = 1
+    // took 13.7 us.  CTAs that take units in turn are launched after the other: they fill
+    // the GPU, and started early they lost up to 12 % (T = 16, 16 experts of 4096 x 2048,
+    // k = 4, 55.1 us and 61.8; T = 64, fine-grained, 83.7 and 87.9; T = 4, Mixtral-shaped, the
+    // same) and gained 5 at most (T = 32, 256 experts of 1024 x 512, 46.6 and 44.3) -- except
+    // after the gate/up kernel where they are short, up to 64 items a scheduler: 32 experts
+    // of 2048 x 768, k = 4, T = 64 37.7 us and 34.8; fine-grained, T = 64 88.3 and 83.7; longer
+    // ones, 64 of 7168 x 2048, T = 16 255.6 and 262.5, T = 32 288.3 and 285.6.
     const long long per_scheduler = pl.units * ((a.K + kW4Blk - 1) / kW4Blk) / (4 * sms);
     const bool early = !in_turn || (MODE == kW4DownAlone && per_scheduler <= 64);
     int smem = pl.smem;
@@ -1080,11 +1083,11 @@ int w4_plan_launch(const W4Args& a, int rows, int x_rows, int dev, int sms, void
 }
 
 // With 9 rows or more: 8 a pass (one tile of columns in every product) or 16 (two),
-// whichever is estimated to end first.  Half the passes over the weights mean half the
-// unpacking, and win where there is much to do: 28672 x 8192, M = 16 36.6 us against
-// 50.4; twice the CTAs win where an SM would stay empty: 14336 x 4096, M = 16 14.8 us
-// against 16.8, 2048 x 2048 4.3 against 5.5.  (32 a pass, a fourth of the splits, lost
-// nearly everywhere: M = 32, 4096 x 14336 38.3 us against 25.0.)
+// whichever is estimated to end first (w4_plan).  Half the passes over the weights mean
+// half the unpacking, and win where there is much to do: 28672 x 8192, M = 16 37.2 us
+// against 49.6; twice the CTAs win where an SM would stay empty: 14336 x 4096, M = 16
+// 15.2 us against 17.1, 2048 x 2048 4.2 against 5.6.  (32 a pass, a fourth of the splits,
+// lost nearly everywhere.)
 template <int G>
 int w4_launch_gemv(const W4Args& a, int rows, int dev, int sms, void* stream) {
     W4Plan one{}, two{};
@@ -1096,10 +1099,12 @@ int w4_launch_gemv(const W4Args& a, int rows, int dev, int sms, void* stream) {
     return w4_launch<kW4Gemv, 2, G, kW4Warps>(a, rows, two_rows, two, dev, sms, stream);
 }
 
-// A warp takes a unit alone when each at work has two or three in turn: T = 32,
-// fine-grained (4608 units) 76.6 us and 73.7, T = 16, Mixtral-shaped (5376) 159 and 154;
-// with fewer some wait long for the last: T = 8, 64 experts of 7168 x 2048 (4096) 183
-// and 193, T = 24, fine-grained (4224) 69 and 71.
+// A warp takes a unit alone when each at work has two or three in turn: T = 16,
+// Mixtral-shaped (5376 units), in clusters and alone, 165.9 us and 159.6, T = 32, 64 experts of
+// 7168 x 2048 297 and 289, T = 64, 8 of 3200 x 6400 147 and 138; with fewer some wait long
+// for the last: T = 8, 64 of 7168 x 2048 (4096) 191.6 and 198.2, T = 16, 16 of 4096 x 2048
+// 55.1 and 70.5.  On 43 calls it took the faster or lost 6 % at most, but for two: T = 32,
+// 256 of 1024 x 512 46.6 and 42.8, T = 64, 4 of 1024 x 4096 48.0 and 44.2.
 template <int G>
 int w4_launch_gate_up(const W4Args& a, int rows, int width, int dev, int sms, void* stream) {
     if (width > 8) return w4_plan_launch<kW4GateUp, 2, G>(a, rows, width, dev, sms, stream);
@@ -1119,17 +1124,16 @@ long long w4_item_ns(long long warps, int sms) {
 //   Clusters of 8 with about two CTAs an SM become clusters of 4 with one of twice the
 //   warps.  The places the gate/up kernel leaves come free one by one, its shared memory
 //   in pieces, where 8 did not always find room: then 3 of 32 clusters ran after the
-//   others (fine-grained, T = 5: 31 us, or 38, by the tokens' experts; now always 31).
-//   Clusters of 4 did, and two tiles of columns (NT) did: T = 32, Mixtral-shaped 217 us,
-//   with 8 warps 230.
+//   others (fine-grained, T = 5: 34.6 us, now 31.2; T = 8 42.7, now 40.5).  Clusters of 4
+//   did, and two tiles of columns (NT) did.
 //   A warp takes a unit alone, and a second kernel sums a token's rows, where that is
 //   estimated to end first: clusters have 64 output columns each, and their fp32 rows of
 //   T tokens leave room for one CTA an SM from T = 50 on.  Estimate: items of a warp,
 //   0.1 us a token for the sums of a cluster, 2.5 us for the second kernel.  Call with
-//   clusters and alone, us: T = 64, E 64, k 4, 1024 x 512 37 and 25; T = 16, E 64, k 8,
-//   7168 x 2048 279 and 249; T = 8, fine-grained 39 and 42; T = 8, E 16, k 4, 4096 x 2048
-//   49 and 55; T = 16, Mixtral-shaped 159 and 183.  On 46 calls it took the faster, or
-//   lost 5 % at most.
+//   clusters and alone, us: T = 64, E 64, k 4, 1024 x 512 38 and 26; T = 16, E 64, k 8,
+//   7168 x 2048 283 and 256; T = 8, fine-grained 40.5 and 41.6; T = 8, E 16, k 4, 4096 x 2048
+//   51 and 57; T = 16, Mixtral-shaped 160 and 209.  On 43 calls it took the faster or lost
+//   8 % at most (T = 20, fine-grained, 67.3 and 62.4).
 template <int G>
 int w4_launch_down(const W4Args& a, int rows, int width, int dev, int sms, void* stream) {
     if (width > 8) return w4_plan_launch<kW4Down, 2, G>(a, rows, width, dev, sms, stream);
