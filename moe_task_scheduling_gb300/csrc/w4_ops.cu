@@ -1355,11 +1355,13 @@ int et_w4_experts(const void* x, const int32_t* topk_idx, const float* topk_w, c
         // Rows a pass takes, 4, 8 or 16, by the rows an expert has on average.  More save passes
         // over experts with many, and cost shared memory (CTAs an SM) and, from 9 on, a second
         // tile of columns in every product; long sums (H) repay that sooner.  Microseconds with
-        // 4 and 8 rows at an average of 2: E 8, 4096 x 14336 177 and 161, E 32, 2048 x 768 28 and
-        // 31; with 8 and 16 at 8: 267 and 217, 45 and 46; at 16: 485 and 360, 71 and 79.
+        // 4 and 8 rows at an average of 1: fine-grained, T = 5 31.2 and 32.4; of 2: T = 32 77.1
+        // and 72.3, E 8, 4096 x 14336 164 and 154, 30 other calls 0 to 18 % apart, 8 never the slower by
+        // more than 1; with 8 and 16 at 8: 246 and 206, E 32, 2048 x 768 34.8 and 53.8; at 16: 397
+        // and 339, E 8, 2048 x 768 21.7 and 31.7 (but E 4, 1024 x 4096 at 32: 48.0 and 43.6).
         const int avg = (R + E - 1) / E;
         const bool deep = H >= 4096;
-        int width = avg <= (deep ? 1 : 2) ? 4 : avg < 8 || !deep ? 8 : 16;
+        int width = avg <= 1 ? 4 : avg < 8 || !deep ? 8 : 16;
         width = rows < width ? rows : width;
         rc = w4_by_group(group, [&](auto g) { return w4_launch_gate_up<decltype(g)::value>(a, rows, width, dev, sms, stream); });
         if (rc) return rc;
