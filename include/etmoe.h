@@ -335,10 +335,11 @@ int et_mlp_chain(const void* x, const void* gamma, float eps, const void* w_gate
  *   losses[1] = (1/n) sum_t log(sum_e exp logits[t,e])^2       (z)
  *
  * All of it fp32; sums over tokens run in a fixed order, so the results are
- * the same bits on every run.  A probability or weight is off by a factor of
- * at most 1 +- (16 + E + 4 |L - L0|) 2^-24 (L0: the token's largest logit), a
- * token's log(sum exp) by 2^-21.4 + (8 |lse| + 2 |L0| + E) 2^-24.  With n == 0
- * the losses and probabilities are 0.
+ * the same bits on every run.  With L0 the token's largest logit, a weight is
+ * off by a factor of at most 1 +- (6 + k + |L - L0|) 2^-24, a probability by
+ * 1 +- (16 + E + 4 |L - L0|) 2^-24, and a token's log(sum exp) by
+ * 2^-21.4 + (8 |lse| + 2 |L0| + E) 2^-24.  With n == 0 the losses and
+ * probabilities are 0.
  * A NaN logit ranks above all others; it makes the token's weights and the
  * losses NaN, as +inf does.  The losses are in logits alone: counts carries no gradient.
  *

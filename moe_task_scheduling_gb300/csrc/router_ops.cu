@@ -137,14 +137,16 @@ __device__ __forceinline__ void select_cut(const float (&v)[EPL], const float* l
 // rows: per warp in registers (32 rows, then once more, so that long sums stay
 // short), per CTA in shared memory, over CTAs by the last one to finish -- each
 // in a fixed order, so that losses and mean probabilities are the same bits on
-// every run.  All in fp32: fp64 runs at 1/64 of it here.  exp, log and the
-// quotients are the fast ones: exp within 2 + 1.2 |L - L0| ulp (rounding L - L0
-// moves it by half of |L - L0| ulp already), a quotient within 2 ulp, log(s) within
-// 2^-21.4 for s <= 2 and 3 ulp above.  logf in place of the fast log took T = 65536,
-// E = 128 from 32.3 to 33.5 us, and with the gradient E = 16 from 32.0 to 35.0; expf
-// and true quotients as well 35.0 and 36.0.
+// every run.  All in fp32: fp64 runs at 1/64 of it here.  The gate weights, which a
+// program uses as they are, take expf and a true quotient (T = 65536, E = 128 32.4 us ->
+// 34.0; the fast ones moved a weight of e^-60 by 40 x 2^-24).  The probabilities and the
+// losses, averaged over tokens, take the fast ones: exp within 2 + 1.2 |L - L0| ulp
+// (rounding L - L0 moves it by half of |L - L0| ulp already), a quotient within 2 ulp,
+// log(s) within 2^-21.4 for s <= 2 and 3 ulp above.  With expf, logf and true quotients
+// there too the means and losses were as far from 64 bits as before (5 x 10^-8; the order
+// of the sums), for 35.1 us, and with the gradient T = 65536, E = 16 36.2 in place of 31.6.
 //
-// T = 16384, E = 128, k = 8: 13.3 us for 9.4 MB, which HBM would bring in 1.4.  About
+// T = 16384, E = 128, k = 8: 13.8 us for 9.4 MB, which HBM would bring in 1.4.  About
 // 7 us are fixed -- the launch, the first loads, and the way through memory to the
 // last CTA's sums -- and the rest is instructions: 27 rows a scheduler, 450 cycles
 // each, the selection most of them.
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_topk_kernel(const
         const float L0 = __shfl_sync(0xffffffffu, myL, 0);
         const bool live = masked_in && !(L0 == -INFINITY);
         const bool on = live && lane < k && !(myL == -INFINITY);
-        const float ex = on ? __expf(myL - L0) : 0.0f;
+        const float ex = on ? expf(myL - L0) : 0.0f;
         float pe[EPL], s = 0.0f;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
@@ -208,7 +210,7 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_topk_kernel(const
         }
         if (lane < k) {
             p.idx[static_cast<size_t>(t) * k + lane] = on ? static_cast<int>(myE) : -1;
-            p.w[static_cast<size_t>(t) * k + lane] = on ? __fdividef(ex, z) : 0.0f;
+            p.w[static_cast<size_t>(t) * k + lane] = on ? ex / z : 0.0f;
         }
         if (on) atomicAdd(&hist[myE], 1);
         if (live) {

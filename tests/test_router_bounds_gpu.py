@@ -1,4 +1,5 @@
-"""et_router_topk's stated error bounds where they are tight: the logarithm near zero."""
+"""et_router_topk's stated error bounds where they are tight: the logarithm near zero, weights far
+below the largest."""
 import pytest
 import torch
 
@@ -26,3 +27,17 @@ def test_logarithm_near_zero(cuda_lib):
     lse_err = 2 ** -21.4 + (1.0 * U + e) + 2 * U * lse
     p_rel = (4 + 2.4 * d.double()[:, None] * torch.tensor([0.0, 1.0]) + 2 + 4 + 4) * U + e
     ref.check(got, lse * p, p * lse_err + lse * p * p_rel + 1e-38, "d_logits")
+
+
+@pytest.mark.parametrize("En", [2, 40, 100])
+def test_weights_far_below_the_largest(cuda_lib, En):
+    """Rows (0, -d, -inf ...): the second weight runs from 1/2 down to e^-80.  L - L0 is exact here; exp is off by 1 ulp,
+    the sum by half a step and the exp in it, the quotient by half a step."""
+    T = 8192
+    d = torch.linspace(0, 80, T)
+    logits = torch.full((T, En), -float("inf"))
+    logits[:, 0], logits[:, 1] = 0, -d
+    o, _, _, _ = _forward(cuda_lib, logits, 2)
+    want = torch.softmax(logits[:, :2].double(), -1)
+    exp = torch.tensor([0.0, 2.0]) + 2 * torch.exp(-d.double()[:, None])
+    ref.check(o["w"], want, (exp + 2) * U * want, "w")
