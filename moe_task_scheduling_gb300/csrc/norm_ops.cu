@@ -649,8 +649,8 @@ struct NormSumArgs {
 
 // Column sums of the partial rows: 32 columns x 32 row groups a CTA, so that the
 // (L2-resident) loads of a column are in flight together.  Two sums of 304 rows of
-// 4096: 10 MB, 9.5 us with cold caches.  Half as many rows, from CTAs of 512
-// threads with two rows each, cost more there than they saved here (forward,
+// 4096: 10 MB, 10.7 to 11.4 us by itself with cold caches.  Half as many rows, from CTAs
+// of 512 threads with two rows each, cost more there than they saved here (forward,
 // backward and this, T = H = 4096: 83 us, then 93).
 __global__ void __launch_bounds__(1024) norm_sum_kernel(const NormSumArgs p) {
     __shared__ float red[32][33];

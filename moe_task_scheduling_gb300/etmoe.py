@@ -559,7 +559,8 @@ def et_w4_gemv_workspace_bytes(M_max, N, K, group) -> int:
 
 
 def et_w4_gemv(X, q, scale, Y, *, M=None, d_M=None, workspace, stream=None, check=True):
-    """Y = X w^T for up to 64 rows, w in 4 bits (et_w4_quantize's layout)."""
+    """Y = X w^T for up to 64 rows, w in 4 bits (et_w4_quantize's layout).  Beyond 32 rows et_splitk_gemm
+    on the bf16 weight (et_w4_dequantize) is about as fast or faster."""
     dev = _device_of(X, "X")
     M_max, K = X.shape
     N = Y.shape[-1]
