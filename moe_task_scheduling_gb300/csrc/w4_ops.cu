@@ -1359,6 +1359,8 @@ int et_w4_experts(const void* x, const int32_t* topk_idx, const float* topk_w, c
         // and 72.3, E 8, 4096 x 14336 164 and 154, 30 other calls 0 to 18 % apart, 8 never the slower by
         // more than 1; with 8 and 16 at 8: 246 and 206, E 32, 2048 x 768 34.8 and 53.8; at 16: 397
         // and 339, E 8, 2048 x 768 21.7 and 31.7 (but E 4, 1024 x 4096 at 32: 48.0 and 43.6).
+        // In between the two come near: E 16, 3584 x 2560 at 8 82.8 and 81.0, 83 and 92 with
+        // k = 2; E 8, 3200 x 6400 at 16 138 and 142.
         const int avg = (R + E - 1) / E;
         const bool deep = H >= 4096;
         int width = avg <= 1 ? 4 : avg < 8 || !deep ? 8 : 16;
