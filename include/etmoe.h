@@ -415,6 +415,178 @@ int et_block_norm_bwd(const void* x, const void* y, const void* gamma_post, cons
                       size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * The router with groups of experts (the source paper has no counterpart;
+ * et_router_topk's sibling for models whose choice is by score and bias):
+ *
+ *   s[t,e] = 1 / (1 + exp -logits[t,e])  (ET_SCORE_SIGMOID) or
+ *            softmax(logits[t,:])[e]     (ET_SCORE_SOFTMAX);
+ *   c[t,e] = s[t,e] + bias[e]  (bias NULL: 0), -inf where the logit is;
+ *   an expert is available to a token when c is above -inf (a bias of -inf
+ *   takes an expert out);
+ *   the E experts are n_groups groups of neighbours; a group's score is the
+ *   sum of its (up to) group_best best available c; the k_groups best groups
+ *   take part (ties: the lower group);
+ *   idx[t,:] = the k experts of these with the largest c, ties to the lower
+ *              index, -1 where there are not so many, and for a token that is
+ *              not routed (token_mask[t] == 0, or no expert available);
+ *   w[t,j]   = scale s[t,idx] / sum_i s[t,idx_i]  with renorm, else
+ *              scale s[t,idx]; 0 where idx is -1;
+ *   counts, n as in et_router_topk; mean_prob[e] = (1/n) sum_t p[t,e],
+ *   p = s / sum_e s over all experts, chosen or not; routed t;
+ *   loss[0]  = E sum_e counts[e] / (n k) * mean_prob[e].
+ *
+ * The bias enters the choice alone: weights, losses and gradients do not see
+ * it (a program moves it by the counts, for balance).  The choice is that of
+ * exact arithmetic: rows where the fp32 values of two candidates are closer
+ * than their errors are chosen again in 64 bits (a few times the time of a
+ * row; logits that are all equal come there in every row).  Values that are
+ * equal in 64 bits tie.  With x0 the row's largest logit (with renorm, the
+ * largest chosen one), a weight is off by a factor of at most
+ * 1 +- (20 + E + |x - x0|) 2^-24, a p by 1 +- (48 + E + 4 |x - x0| + 5 |x|) 2^-24.
+ * Scores below 2^-126 may be 0.  Sums over tokens run in a fixed order.
+ * A NaN logit, and with softmax one of +inf, makes its token's softmax weights,
+ * or the sigmoid weights it takes part in, and the loss NaN.
+ *
+ * The gradient (et_router_groups_bwd), d_loss fp32 [1] (NULL: 0) and d_topk_w
+ * fp32 [T,k] (NULL: 0; read only where idx is not -1), with W_j = w_j d_w_j and
+ * q = 1 - s (sigmoid) or 1 (softmax):
+ *   d_logits[t,e] = q_e (d_loss p_e (C_e - sum_f C_f p_f)
+ *                        + sum_{j: idx_j = e} (W_j - r_j)) - u p_e,
+ *   C_e = E counts[e] / (n^2 k);  r_j = w_j sum_i W_i / scale with renorm, else 0;
+ *   u = sum_i W_i for softmax scores without renorm, else 0.
+ * topk_idx, topk_w, expert_counts and n_routed are the forward's outputs; 0 for
+ * a token with no index.
+ *
+ * logits fp32 [T_max,E]; bias fp32 [E] or NULL; the other tensors as in
+ * et_router_topk, loss and d_loss fp32 [1].  1 <= n_groups <= 32, a divisor of
+ * E; 1 <= k_groups <= n_groups; group_best 1 or 2; k <= min(8, k_groups
+ * E / n_groups); renorm 0 or 1; scale finite.  Rows >= T are neither read nor
+ * written; T == 0 still writes counts, n, probabilities and loss (all 0).
+ * Workspace and errors as in et_router_topk.
+ * ---------------------------------------------------------------------- */
+enum et_score { ET_SCORE_SOFTMAX = 0, ET_SCORE_SIGMOID = 1 };
+
+size_t et_router_groups_workspace_bytes(int T_max, int E, int k);
+
+int et_router_groups(const float* logits, const float* bias, const uint8_t* token_mask,
+                     int score, int n_groups, int k_groups, int group_best, int renorm,
+                     float scale, int32_t* topk_idx, float* topk_w, int32_t* expert_counts,
+                     int32_t* n_routed, float* mean_prob, float* loss, int T,
+                     const int32_t* d_T, int T_max, int E, int k, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+int et_router_groups_bwd(const float* logits, const uint8_t* token_mask, int score, int renorm,
+                         float scale, const int32_t* topk_idx, const float* topk_w,
+                         const int32_t* expert_counts, const int32_t* n_routed,
+                         const float* d_loss, const float* d_topk_w, float* d_logits, int T,
+                         const int32_t* d_T, int T_max, int E, int k, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Dropout whose mask is never stored (the source paper has no counterpart):
+ *
+ *   out[t,h] = bf16( x[t,h] + (kept ? y[t,h] / (1 - thr / 2^16) : 0) )
+ *
+ * (x NULL: without it).  thr = p 2^16 rounded to nearest even, p in [0, 65535 /
+ * 65536]; an element is kept when its 16 random bits are at least thr.  They
+ * come from Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random
+ * numbers: as easy as 1, 2, 3", SC 2011) with the key (seed low, seed high) and
+ * the counter (h / 8, t, offset low, offset high): element h has the low (even
+ * h) or high half of word h % 8 / 2.  A dropped element adds 0 whatever it is.
+ * The same call on d_out, without x, is the gradient of y.  d_rng, if not NULL,
+ * is a device uint64 [2] {seed, offset} that is read at run time in place of
+ * seed and offset: a captured graph then draws anew at every replay.
+ *
+ * x, y, out bf16 [T_max,H]; out may be x or y.  1 <= T_max <= 2^24, 1 <= H <=
+ * 2^18 (H a multiple of 8 with 16-byte aligned tensors uses 16-byte accesses;
+ * otherwise element by element, with T_max ceil(H / 2048) < 2^31).  Rows >= T
+ * are neither read nor written.  The workspace holds the status.  Errors as
+ * et_moe_layer.
+ * ---------------------------------------------------------------------- */
+size_t et_dropout_workspace_bytes(int T_max, int H);
+
+int et_dropout(const void* x, const void* y, void* out, float p, uint64_t seed, uint64_t offset,
+               const uint64_t* d_rng, int T, const int32_t* d_T, int T_max, int H,
+               void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A block's residual with dropout and the layer norm before the next block, in
+ * one pass (the source paper has no counterpart; et_block_norm is the same for
+ * RMS norms):
+ *
+ *   z = x + dropout(y)                  (x without y)
+ *   n = (z - mean z) / sqrt(mean (z - mean z)^2 + eps)
+ *   x_out = bf16(z),   x_hat = bf16( n * gamma + beta )
+ *
+ * computed in fp32 with one rounding for each output; dropout, p, seed, offset
+ * and d_rng as in et_dropout, with its mask (p 0: all is kept; p > 0 needs y).
+ * gamma NULL is 1, beta NULL is 0; y and x_out may be NULL.
+ *
+ * et_layer_norm_bwd: with d_x_hat and d_x_out (NULL: no gradient flows there)
+ * bf16 [T_max,H]; a = d_x_hat gamma, r = 1 / sqrt(var + eps):
+ *   dx = bf16(D),  D = d_x_out + r (a - mean a - n mean(a n));
+ *   dy = bf16( dropout(D) )             (NULL: not wanted)
+ *   d_gamma = sum_t d_x_hat n,  d_beta = sum_t d_x_hat   fp32 [H] or NULL.
+ * z, n and the mask are made again from x, y and the seed.  d_gamma and d_beta
+ * are overwritten, not added to; they are summed in a fixed order (the same
+ * bits on every run) and are 0 when T == 0.
+ *
+ * x, y, x_out, x_hat, dx, dy bf16 [T_max,H]; gamma, beta bf16 [H]; eps > 0; 1 <=
+ * H <= 16384 (multiples of 8 with 16-byte aligned tensors use 16-byte accesses;
+ * any other H or alignment is served element by element); 1 <= T_max <= 2^24.
+ * x_out may be x, dx may be d_x_out, dy may be y.  Sums of a row are fp32: they
+ * must stay below 3e38, and a mean far above the deviation from it costs their
+ * relative precision, as in any fp32 norm.  Workspace:
+ * et_layer_norm_workspace_bytes; the forward needs its first 256 bytes only.
+ * Errors as et_moe_layer.
+ * ---------------------------------------------------------------------- */
+size_t et_layer_norm_workspace_bytes(int T_max, int H);
+
+int et_layer_norm(const void* x, const void* y, const void* gamma, const void* beta, float eps,
+                  float p, uint64_t seed, uint64_t offset, const uint64_t* d_rng, void* x_out,
+                  void* x_hat, int T, const int32_t* d_T, int T_max, int H, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+int et_layer_norm_bwd(const void* x, const void* y, const void* gamma, float eps, float p,
+                      uint64_t seed, uint64_t offset, const uint64_t* d_rng,
+                      const void* d_x_out, const void* d_x_hat, void* dx, void* dy,
+                      float* d_gamma, float* d_beta, int T, const int32_t* d_T, int T_max,
+                      int H, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Products of 8-bit integers with a scale for each token and each channel (the
+ * source paper has no counterpart).
+ *
+ * et_i8_quantize: rows of bf16 [M_max,K] to int8 and fp32 scales [M_max]:
+ *   scale[m] = max_k |x[m,k]| / 127,  q[m,k] = round-half-even(x / scale)
+ * within -127..127, both quotients fp32; a row of zeros has scale 0 and q 0, one
+ * with an infinity or NaN a scale of NaN and q 0.  Tokens and the channels of a
+ * weight [N,K] alike.
+ *
+ * et_i8_gemm: Y[m,n] = bf16( (s_x[m] s_w[n]) sum_k x_q[m,k] w_q[n,k] ), x_q int8
+ * [M_max,K], w_q int8 [N,K], s_x fp32 [M_max], s_w fp32 [N], Y bf16 [M_max,N],
+ * from one token to many.  The sum over k is exact while its partial sums stay
+ * within 2^24 (always for K <= 1024), and off by at most 2^-22 sum |x_q w_q|
+ * beyond; every value of int8 is served, -128 too.  The results are the same
+ * bits on every run of a shape.
+ *
+ * K is a multiple of 16 up to 65536, 1 <= N <= 2^20, 1 <= M_max <= 2^20; x_q, w_q
+ * and q 16-byte aligned, x and Y 2-byte, scales 4-byte.  Rows >= M are neither read nor written.  M and d_M as in
+ * et_splitk_gemm.  et_i8_quantize needs 256 bytes of workspace (for its status);
+ * one workspace may serve both calls.  Errors as et_moe_layer.
+ * ---------------------------------------------------------------------- */
+size_t et_i8_quantize_workspace_bytes(int M_max, int K);
+
+int et_i8_quantize(const void* x, void* q, float* scale, int M, const int32_t* d_M, int M_max,
+                   int K, void* workspace, size_t workspace_bytes, void* stream);
+
+size_t et_i8_gemm_workspace_bytes(int M_max, int N, int K);
+
+int et_i8_gemm(const void* x_q, const float* s_x, const void* w_q, const float* s_w, void* Y,
+               int M, const int32_t* d_M, int M_max, int N, int K, void* workspace,
+               size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Products with 4-bit weights, for decoding (the source paper has no
  * counterpart; the small batches of et_splitk_gemm and et_moe_layer are bound
  * by the bytes of their bf16 weights, which these hold in a quarter).

@@ -1,0 +1,265 @@
+// i8_ops.cu -- rows of bf16 to int8 with a scale each, and products of int8
+// tokens and weights with a scale for each token and channel.
+#include <cmath>
+
+#include "../../include/etmoe.h"
+#include "et_api.h"
+#include "row_ops.cuh"
+
+namespace et {
+namespace {
+
+constexpr int kI8KMax = 65536;
+constexpr int kI8Max = 1 << 20;  // rows and channels
+
+// ---------------------------------------------------------------- quantiser
+
+struct I8QuantArgs {
+    const bf16* x;   // [M, K]
+    int8_t* q;       // [M, K]
+    float* scale;    // [M]
+    int row_threads;
+    const int32_t* d_M;
+    int M_host, M_max, K;
+    EtHeader* hdr;
+};
+
+// q of eight values, packed in two words.
+template <class F>
+__device__ __forceinline__ uint2 quantize8(const F& v, float s, bool live) {
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int q = live ? max(-127, min(127, __float2int_rn(__fdiv_rn(v[i], s)))) : 0;
+        b[i] = static_cast<uint32_t>(q) & 0xffu;
+    }
+    return make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
+}
+
+// A row's largest magnitude, then its values: a row of up to sixteen columns a thread
+// (16384) stays in registers, a longer one is read again (from the caches).
+template <bool VEC, int MODE>
+__global__ void __launch_bounds__(1024) i8_quantize_kernel(const I8QuantArgs p) {
+    constexpr int V = norm_v(MODE);
+    __shared__ uint32_t red[2][32];
+    int n = 0;
+    const RowGroup<MODE> g(p.row_threads);
+    grid_begin();
+    bool ok;
+    const int M = row_count(p.d_M, p.M_host, p.M_max, p.hdr, &ok);
+    const int K = p.K, span = g.th() * 8 * V;
+    for (int m = blockIdx.x * g.groups() + g.id(); m < M; m += gridDim.x * g.groups()) {
+        const bf16* row = p.x + static_cast<size_t>(m) * K;
+        Vec8 v[V];
+        uint32_t top = 0;  // as the bits of |x|, which order as their values do, NaN above infinity
+        for (int c0 = 0; c0 < K; c0 += span)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                v[j] = load8<VEC>(row + c0, g, j, K - c0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    top = max(top, max(v[j].u[i] << 16 & 0x7fff0000u, v[j].u[i] & 0x7fff0000u));
+            }
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (MODE != kRowsWarp) {
+            const int slot = n++ & 1, lane = threadIdx.x & 31, first = g.id() * (g.th() >> 5);
+            if (lane == 0) red[slot][threadIdx.x >> 5] = top;
+            g.sync();
+            top = __reduce_max_sync(0xffffffffu, lane < (g.th() >> 5) ? red[slot][first + lane] : 0u);
+        }
+        const bool finite = top < 0x7f800000u, live = finite && top != 0;
+        const float s = finite ? __fdiv_rn(__uint_as_float(top), 127.0f) : __int_as_float(0x7fffffff);
+        if (g.lane() == 0) p.scale[m] = s;
+        int8_t* out = p.q + static_cast<size_t>(m) * K;
+        for (int c0 = 0; c0 < K; c0 += span)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                if (K > span) v[j] = load8<VEC>(row + c0, g, j, K - c0);
+                const uint2 q = quantize8(v[j], s, live);
+                if (VEC) {
+                    const int c = c0 + g.template col<VEC>(j, 0);
+                    if (c < K) *reinterpret_cast<uint2*>(out + c) = q;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int c = c0 + g.template col<VEC>(j, i);
+                        if (c < K) out[c] = static_cast<int8_t>((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+                    }
+                }
+            }
+    }
+}
+
+// ---------------------------------------------------------------- products of few rows
+
+struct I8GemmArgs {
+    const int8_t* x;   // [M, K]
+    const float* sx;   // [M]
+    const int8_t* w;   // [N, K]
+    const float* sw;   // [N]
+    bf16* y;           // [M, N]
+    const int32_t* d_M;
+    int M_host, M_max, N, K;
+    EtHeader* hdr;
+};
+
+constexpr int kGemvWarps = 8;
+constexpr int kGemvRows = 4;  // channels of a CTA
+
+// MR tokens times four channels a CTA, whose warps take 512-byte pieces of K in turn:
+// dp4a on 16-byte loads, sums exact in int32.  The weights come once from memory, the
+// tokens from L1.
+template <int MR>
+__global__ void __launch_bounds__(kGemvWarps * 32) i8_gemv_kernel(const I8GemmArgs p) {
+    __shared__ int red[kGemvWarps][kGemvRows * MR];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    grid_begin();
+    bool ok;
+    const int M = row_count(p.d_M, p.M_host, p.M_max, p.hdr, &ok);
+    const int m0 = blockIdx.y * MR, n0 = blockIdx.x * kGemvRows;
+    if (m0 >= M) return;
+    const int K = p.K;
+    int acc[kGemvRows][MR];
+#pragma unroll
+    for (int r = 0; r < kGemvRows; ++r)
+#pragma unroll
+        for (int m = 0; m < MR; ++m) acc[r][m] = 0;
+    const int8_t* w[kGemvRows];
+    const int8_t* x[MR];
+#pragma unroll
+    for (int r = 0; r < kGemvRows; ++r) w[r] = p.w + static_cast<size_t>(min(n0 + r, p.N - 1)) * K;
+#pragma unroll
+    for (int m = 0; m < MR; ++m) x[m] = p.x + static_cast<size_t>(min(m0 + m, M - 1)) * K;
+#pragma unroll 2
+    for (int c = (warp * 32 + lane) * 16; c < K; c += kGemvWarps * 512) {
+        int4 wv[kGemvRows], xv[MR];
+#pragma unroll
+        for (int r = 0; r < kGemvRows; ++r) wv[r] = __ldcs(reinterpret_cast<const int4*>(w[r] + c));
+#pragma unroll
+        for (int m = 0; m < MR; ++m) xv[m] = *reinterpret_cast<const int4*>(x[m] + c);
+#pragma unroll
+        for (int r = 0; r < kGemvRows; ++r)
+#pragma unroll
+            for (int m = 0; m < MR; ++m) {
+                int a = acc[r][m];
+                a = __dp4a(wv[r].x, xv[m].x, a);
+                a = __dp4a(wv[r].y, xv[m].y, a);
+                a = __dp4a(wv[r].z, xv[m].z, a);
+                acc[r][m] = __dp4a(wv[r].w, xv[m].w, a);
+            }
+    }
+#pragma unroll
+    for (int r = 0; r < kGemvRows; ++r)
+#pragma unroll
+        for (int m = 0; m < MR; ++m) {
+            const int s = __reduce_add_sync(0xffffffffu, acc[r][m]);
+            if (lane == 0) red[warp][m * kGemvRows + r] = s;
+        }
+    __syncthreads();
+    const int o = threadIdx.x;
+    if (o < kGemvRows * MR) {
+        int s = 0;
+#pragma unroll
+        for (int v = 0; v < kGemvWarps; ++v) s += red[v][o];
+        const int m = m0 + o / kGemvRows, n = n0 + o % kGemvRows;
+        if (m < M && n < p.N)
+            p.y[static_cast<size_t>(m) * p.N + n] = __float2bfloat16_rn(static_cast<float>(s) * (p.sx[m] * p.sw[n]));
+    }
+}
+
+bool i8_shape_ok(int M_max, int N, int K, std::string* why) {
+    if (M_max < 1 || M_max > kI8Max || N < 1 || N > kI8Max) { *why = "M_max and N must be in [1, 2^20]"; return false; }
+    if (K < 16 || K > kI8KMax || K % 16) { *why = "K must be a multiple of 16 in [16, 65536]"; return false; }
+    return true;
+}
+
+int i8_check_rows(int M, const int32_t* d_M, int M_max) {
+    if (!api_aligned(d_M, 4)) return api_fail(ET_ERR_INVALID, "tensors must be aligned to their element size");
+    if (!d_M && (M < 0 || M > M_max)) return api_fail(ET_ERR_INVALID, "M must be in [0, M_max]");
+    return ET_OK;
+}
+
+template <bool VEC>
+cudaError_t launch_i8_quantize(I8QuantArgs a, int rows, int sms, void* stream) {
+    const int cols = a.K < kNormHMax ? a.K : kNormHMax;
+    a.row_threads = norm_threads(cols);
+    const RowMode mode = norm_mode(cols, a.row_threads);
+    const int groups = norm_groups(a.row_threads, rows), th = a.row_threads * groups;
+    const int need = (rows + groups - 1) / groups, most = sms * (2048 / th);
+    return api_launch(mode == kRowsWarp ? i8_quantize_kernel<VEC, kRowsWarp> : mode == kRowsGroup ? i8_quantize_kernel<VEC, kRowsGroup>
+                                                                             : i8_quantize_kernel<VEC, kRowsOne>,
+                      need < most ? need : most, th, 0, stream, a);
+}
+
+}  // namespace
+}  // namespace et
+
+using namespace et;
+
+extern "C" {
+
+size_t et_i8_quantize_workspace_bytes(int M_max, int K) {
+    std::string why;
+    return i8_shape_ok(M_max, 1, K, &why) ? kHeaderBytes : 0;
+}
+
+int et_i8_quantize(const void* x, void* q, float* scale, int M, const int32_t* d_M, int M_max, int K, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+    return api_entry([&]() -> int {
+        std::string why;
+        if (!i8_shape_ok(M_max, 1, K, &why)) return api_fail(ET_ERR_UNSUPPORTED, why);
+        if (!x || !q || !scale) return api_fail(ET_ERR_INVALID, "x, q and scale must be non-NULL");
+        if (!api_aligned(q, 16)) return api_fail(ET_ERR_INVALID, "q must be 16-byte aligned");
+        if (!api_aligned(x, 2) || !api_aligned(scale, 4))
+            return api_fail(ET_ERR_INVALID, "tensors must be aligned to their element size");
+        int rc = i8_check_rows(M, d_M, M_max);
+        if (rc) return rc;
+        if ((rc = api_check_ws(workspace, workspace_bytes, kHeaderBytes))) return rc;
+        if (!d_M && M == 0) return ET_OK;
+        int dev = 0, sms = 0;
+        if ((rc = api_device(&dev, &sms))) return rc;
+        const I8QuantArgs a{static_cast<const bf16*>(x), static_cast<int8_t*>(q), scale, 0, d_M, M, M_max, K,
+                            static_cast<EtHeader*>(workspace)};
+        const int rows = d_M ? M_max : M;
+        const cudaError_t e = api_aligned(x, 16) ? launch_i8_quantize<true>(a, rows, sms, stream)
+                                                 : launch_i8_quantize<false>(a, rows, sms, stream);
+        if (e != cudaSuccess) return api_fail_cuda(e, "launch of the int8 quantiser");
+        return ET_OK;
+    });
+}
+
+size_t et_i8_gemm_workspace_bytes(int M_max, int N, int K) {
+    std::string why;
+    return i8_shape_ok(M_max, N, K, &why) ? kHeaderBytes : 0;
+}
+
+int et_i8_gemm(const void* x_q, const float* s_x, const void* w_q, const float* s_w, void* Y, int M, const int32_t* d_M,
+               int M_max, int N, int K, void* workspace, size_t workspace_bytes, void* stream) {
+    return api_entry([&]() -> int {
+        std::string why;
+        if (!i8_shape_ok(M_max, N, K, &why)) return api_fail(ET_ERR_UNSUPPORTED, why);
+        if (!x_q || !s_x || !w_q || !s_w || !Y) return api_fail(ET_ERR_INVALID, "x_q, s_x, w_q, s_w and Y must be non-NULL");
+        if (!api_aligned(x_q, 16) || !api_aligned(w_q, 16)) return api_fail(ET_ERR_INVALID, "x_q and w_q must be 16-byte aligned");
+        if (!api_aligned(s_x, 4) || !api_aligned(s_w, 4) || !api_aligned(Y, 2))
+            return api_fail(ET_ERR_INVALID, "tensors must be aligned to their element size");
+        int rc = i8_check_rows(M, d_M, M_max);
+        if (rc) return rc;
+        if ((rc = api_check_ws(workspace, workspace_bytes, et_i8_gemm_workspace_bytes(M_max, N, K)))) return rc;
+        if (!d_M && M == 0) return ET_OK;
+        int dev = 0, sms = 0;
+        if ((rc = api_device(&dev, &sms))) return rc;
+        const I8GemmArgs a{static_cast<const int8_t*>(x_q), s_x, static_cast<const int8_t*>(w_q), s_w, static_cast<bf16*>(Y),
+                           d_M, M, M_max, N, K, static_cast<EtHeader*>(workspace)};
+        const int rows = d_M ? M_max : M;
+        const int mr = rows == 1 ? 1 : rows == 2 ? 2 : rows <= 4 ? 4 : 8;
+        auto kernel = mr == 1 ? i8_gemv_kernel<1> : mr == 2 ? i8_gemv_kernel<2> : mr == 4 ? i8_gemv_kernel<4> : i8_gemv_kernel<8>;
+        const long long gy = (static_cast<long long>(rows) + mr - 1) / mr;
+        if (gy > 65535) return api_fail(ET_ERR_UNSUPPORTED, "too many rows");
+        const cudaError_t e = api_launch(kernel, dim3((N + kGemvRows - 1) / kGemvRows, static_cast<unsigned>(gy)),
+                                         kGemvWarps * 32, 0, stream, a);
+        if (e != cudaSuccess) return api_fail_cuda(e, "launch of the int8 product");
+        return ET_OK;
+    });
+}
+
+}  // extern "C"

@@ -1,0 +1,629 @@
+// router_groups.cu -- the router with scores by softmax or sigmoid, a bias that
+// only the choice sees, and groups of experts of which the best take part; its
+// balance loss, and the gradient.
+#include <cmath>
+
+#include "../../include/etmoe.h"
+#include "router_sums.cuh"
+
+namespace et {
+namespace {
+
+constexpr int kGroupsMax = 32;
+
+struct GroupArgs {
+    const float* logits;     // [T, E]
+    const float* bias;       // [E] or null
+    const uint8_t* mask;     // [T] or null
+    int32_t* idx;            // [T, k]
+    float* w;                // [T, k]
+    const int32_t* d_T;
+    int T_host, T_max, E, k;
+    int G, kg, best;         // groups, how many take part, whose `best` experts rank them
+    int gs;                  // experts a group
+    int lanes;               // lanes that hold a group where that is a power of two, else 0
+    int sigmoid, renorm;
+    float scale;
+    RouterSums sums;
+};
+
+__device__ __forceinline__ double key_value(unsigned long long key) {
+    return __longlong_as_double(static_cast<long long>(key >> 63 ? key ^ 0x8000000000000000ull : ~key));
+}
+
+// logit_key of a 64-bit value; NaN above all, > 0 everywhere.
+__device__ __forceinline__ unsigned long long value_key(double v) {
+    if (v != v) return ~0ull;
+    const long long b = __double_as_longlong(v + 0.0);
+    return static_cast<unsigned long long>(b) ^ (static_cast<unsigned long long>(b >> 63) | 0x8000000000000000ull);
+}
+
+// The whole choice in 64 bits, for the rows where 32 cannot tell.  Lane `lane` has the
+// logits of experts lane * EPL + i.  Returns lane j's expert, the j-th, or -1.
+// Out of line and in plain loops: one row in some hundreds comes here.
+template <int EPL>
+struct LaneLogits { float v[EPL]; };
+template <int EPL>
+__device__ __noinline__ int choose64(LaneLogits<EPL> row, const float* bias, int E, int k, int G, int kg, int best, int gs,
+                                     int sigmoid, int lane) {
+    constexpr uint32_t kAll = 0xffffffffu;
+    unsigned long long key[EPL];  // of score + bias; 0: not available
+    double m = 0.0, Z = 1.0;
+    if (!sigmoid) {
+        float top = row.v[0];
+#pragma unroll
+        for (int i = 1; i < EPL; ++i) top = fmaxf(top, row.v[i]);
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
+        m = top;
+        Z = 0.0;
+#pragma unroll 1
+        for (int i = 0; i < EPL; ++i) Z += exp(static_cast<double>(row.v[i]) - m);  // 0 past E
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) Z += __shfl_xor_sync(kAll, Z, off);
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        const int e = lane * EPL + i;
+        const double x = row.v[i];
+        key[i] = 0;
+        if (e < E && !(row.v[i] == -INFINITY)) {
+            const double s = sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - m) / Z;
+            const double c = bias ? s + static_cast<double>(bias[e]) : s;
+            if (!(c == -INFINITY)) key[i] = value_key(c);
+        }
+    }
+    if (kg < G) {
+        double score = -INFINITY;  // lane g: of group g
+#pragma unroll 1
+        for (int g = 0; g < G; ++g) {
+            unsigned long long hi = 0, lo = 0;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const int e = lane * EPL + i;
+                if (e >= g * gs && e < g * gs + gs) {
+                    lo = max(lo, min(hi, key[i]));
+                    hi = max(hi, key[i]);
+                }
+            }
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) {
+                const unsigned long long h = __shfl_xor_sync(kAll, hi, off), l = __shfl_xor_sync(kAll, lo, off);
+                lo = max(max(lo, l), min(hi, h));
+                hi = max(hi, h);
+            }
+            double s = hi ? key_value(hi) : -INFINITY;
+            if (best > 1 && lo) s += key_value(lo);
+            if (lane == g) score = s;
+        }
+        const unsigned long long mine = value_key(score);
+        int rank = 0;
+#pragma unroll 1
+        for (int g = 0; g < G; ++g) {
+            const unsigned long long other = __shfl_sync(kAll, mine, g);
+            rank += other > mine || (other == mine && g < lane);
+        }
+        const uint32_t in = __ballot_sync(kAll, lane < G && rank < kg);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const int e = lane * EPL + i;
+            if (e >= E || !(in >> (e / gs) & 1)) key[i] = 0;
+        }
+    }
+    int mineE = -1;
+#pragma unroll 1
+    for (int j = 0; j < k; ++j) {
+        unsigned long long hi = 0;
+        int at = E;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (key[i] > hi) {
+                hi = key[i];
+                at = lane * EPL + i;
+            }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) {
+            const unsigned long long h = __shfl_xor_sync(kAll, hi, off);
+            const int a = __shfl_xor_sync(kAll, at, off);
+            if (h > hi || (h == hi && a < at)) {
+                hi = h;
+                at = a;
+            }
+        }
+        if (hi && lane == j) mineE = at;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (lane * EPL + i == at) key[i] = 0;
+    }
+    return mineE;
+}
+
+// The float of a key as logit_key made it, -inf for 0.
+__device__ __forceinline__ float key_or_none(uint32_t key) { return key ? key_logit(key) : -INFINITY; }
+
+// One row a warp, experts lane * EPL + i in register i, so that a group is a few
+// neighbouring lanes.  The choice runs on 32-bit values: without a bias on the logits,
+// which order as the scores do and are exact; with one on score + bias, whose error has a
+// bound.  Where two neighbours in the order, or the last group that takes part and
+// the next, are no farther apart than both errors, the row is chosen again in 64 bits.
+template <int EPL>
+__global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(const GroupArgs p) {
+    constexpr uint32_t kAll = 0xffffffffu;
+    constexpr float kU = 1.0f / (1 << 24);
+    extern __shared__ __align__(16) float sm[];  // [warps][E], then the last CTA's sums
+    __shared__ RouterShared sh;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+    const int E = p.E, k = p.k;
+    grid_begin();
+    bool ok;
+    const int T = row_count(p.d_T, p.T_host, p.T_max, p.sums.hdr, &ok);
+    if (!ok) return;
+    const int t0 = blockIdx.x + gridDim.x * warp, step = gridDim.x * nwarps;
+    auto load = [&](int t, float (&v)[EPL], int& on) {
+        const float* L = p.logits + static_cast<size_t>(t) * E;
+        on = t < T && (!p.mask || p.mask[t] != 0);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) v[i] = t < T && lane * EPL + i < E ? L[lane * EPL + i] : -INFINITY;
+    };
+    float nv[EPL], bias[EPL];
+    int non;
+    load(t0, nv, non);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) bias[i] = p.bias && lane * EPL + i < E ? p.bias[lane * EPL + i] : 0.0f;
+    for (int e = threadIdx.x; e < E; e += blockDim.x) sh.hist[e] = 0;
+    __syncthreads();
+
+    float accp[EPL], bigp[EPL];
+    int accn = 0, rows32 = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) accp[i] = bigp[i] = 0.0f;
+
+    for (int t = t0; t < T; t += step) {
+        float v[EPL];
+        const int masked_in = non;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) v[i] = nv[i];
+        load(t + step, nv, non);
+
+        // scores s, their sum S
+        float s[EPL], S = 0.0f, top = v[0];
+#pragma unroll
+        for (int i = 1; i < EPL; ++i) top = fmaxf(top, v[i]);
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            s[i] = p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-v[i])) : __expf(v[i] - top);
+            if (v[i] == -INFINITY) s[i] = 0.0f;
+            S += s[i];
+        }
+        S = warp_sum(S);
+        const float inv = __fdividef(1.0f, S);
+        float smax = 1.0f;  // no score is larger
+        if (!p.sigmoid) {
+            smax = inv;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) s[i] *= inv;
+        }
+        // How far a score can be off: sigmoid 6.3 x 2^-24 (exp within 2 + 1.2 |x| ulp, times
+        // the slope e^x / (1 + e^x)^2 <= 1/4; an add; a quotient within 2 ulp), softmax 40 x
+        // 2^-24 of the largest (its sum's terms are off by 8.5 ulp on average at most, as
+        // their mean |x - top| is below log 256).
+        const float err = (p.sigmoid ? 10.0f : 48.0f * smax) * kU;
+
+        uint32_t key[EPL];  // 0: not available
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const float c = p.bias ? __fadd_rn(s[i], bias[i]) : v[i];
+            const bool there = lane * EPL + i < E && !(v[i] == -INFINITY) && !(c == -INFINITY);
+            key[i] = there ? logit_key(c) : 0u;
+        }
+        bool doubt = false;
+        if (p.kg < p.G) {
+            // a group's best two values of score + bias
+            float score = -INFINITY;  // lane g: of group g
+            float mag = 0.0f;
+            auto group_score = [&](float hi, float lo, bool has_lo) { return hi + (p.best > 1 && has_lo ? lo : 0.0f); };
+            if (p.lanes) {
+                uint32_t hi = 0, lo = 0;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) {
+                    const uint32_t c = p.bias ? key[i] : key[i] ? logit_key(s[i]) : 0u;
+                    lo = max(lo, min(hi, c));
+                    hi = max(hi, c);
+                }
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const uint32_t h = __shfl_xor_sync(kAll, hi, off), l = __shfl_xor_sync(kAll, lo, off);
+                    if (off < p.lanes) {
+                        lo = max(max(lo, l), min(hi, h));
+                        hi = max(hi, h);
+                    }
+                }
+                const int from = min(lane * p.lanes, 31);
+                hi = __shfl_sync(kAll, hi, from);
+                lo = __shfl_sync(kAll, lo, from);
+                if (lane < p.G) {
+                    score = group_score(key_or_none(hi), key_or_none(lo), lo != 0);
+                    mag = fabsf(key_or_none(hi)) + fabsf(lo ? key_logit(lo) : 0.0f);
+                }
+            } else {
+#pragma unroll 1
+                for (int g = 0; g < p.G; ++g) {
+                    uint32_t hi = 0, lo = 0;
+#pragma unroll
+                    for (int i = 0; i < EPL; ++i) {
+                        const int e = lane * EPL + i;
+                        const bool in = e >= g * p.gs && e < g * p.gs + p.gs && key[i];
+                        const uint32_t c = !in ? 0u : p.bias ? key[i] : logit_key(s[i]);
+                        lo = max(lo, min(hi, c));
+                        hi = max(hi, c);
+                    }
+                    const uint32_t H = __reduce_max_sync(kAll, hi);
+                    // its holder's second best (the first holder's, where several hold it)
+                    const uint32_t who = __ballot_sync(kAll, hi == H);
+                    const bool first = lane == __ffs(who) - 1;
+                    const uint32_t L = __reduce_max_sync(kAll, first ? lo : hi);
+                    if (lane == g) {
+                        score = group_score(key_or_none(H), key_or_none(L), L != 0);
+                        mag = fabsf(key_or_none(H)) + fabsf(L ? key_logit(L) : 0.0f);
+                    }
+                }
+            }
+            const uint32_t mine = logit_key(score);
+            int rank = 0;
+#pragma unroll 4
+            for (int g = 0; g < p.G; ++g) {
+                const uint32_t other = __shfl_sync(kAll, mine, g);
+                rank += other > mine || (other == mine && g < lane);
+            }
+            const uint32_t in = __ballot_sync(kAll, lane < p.G && rank < p.kg);
+            // the last that takes part and the next: apart by more than any two may be off
+            const uint32_t last_in = __ballot_sync(kAll, lane < p.G && rank == p.kg - 1);
+            const uint32_t next = __ballot_sync(kAll, lane < p.G && rank == p.kg);
+            const float off_by = 2.0f * err + 2.0f * kU * mag;
+            const float a = __shfl_sync(kAll, score, __ffs(last_in) - 1), b = __shfl_sync(kAll, score, __ffs(next) - 1);
+            const float tol = 2.0f * __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(off_by)));
+            doubt = !(a - b > tol) && !(b == -INFINITY);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const int e = lane * EPL + i;
+                const int g = p.lanes ? lane / p.lanes : e / p.gs;
+                if (!(in >> (g & 31) & 1)) key[i] = 0u;
+            }
+        }
+        // the best k, and with a bias the next one too; lane j: the j-th
+        auto next_best = [&](uint32_t& kmax, int& e) {
+            uint32_t bk = key[0];
+#pragma unroll
+            for (int i = 1; i < EPL; ++i) bk = max(bk, key[i]);
+            kmax = __reduce_max_sync(kAll, bk);
+            uint32_t low = 0xffffffffu;
+#pragma unroll
+            for (int i = EPL - 1; i >= 0; --i)
+                if (key[i] == kmax) low = static_cast<uint32_t>(lane * EPL + i);
+            e = static_cast<int>(__reduce_min_sync(kAll, low));
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                if (lane * EPL + i == e) key[i] = 0u;
+        };
+        uint32_t mykey = 0;
+        int myE = 0;
+        const int rounds = p.bias ? k + 1 : k;
+#pragma unroll 1
+        for (int j = 0; j < rounds; ++j) {
+            uint32_t kmax;
+            int e;
+            next_best(kmax, e);
+            if (lane == j) {
+                mykey = kmax;
+                myE = e;
+            }
+        }
+        const float* row = p.logits + static_cast<size_t>(t) * E;
+        bool on = lane < k && mykey != 0;
+        float myL = mykey ? row[myE] : -INFINITY;
+        if (p.bias) {
+            const float c = key_or_none(mykey), b = mykey ? p.bias[myE] : 0.0f;
+            const float cn = __shfl_down_sync(kAll, c, 1), bn = __shfl_down_sync(kAll, b, 1), Ln = __shfl_down_sync(kAll, myL, 1);
+            const bool there = __shfl_down_sync(kAll, mykey, 1) != 0;
+            const bool equal = b == bn && myL == Ln;  // a true tie, in the order of the experts already
+            const float tol = 2.0f * err + kU * (fabsf(c) + fabsf(cn));
+            doubt |= __any_sync(kAll, on && there && !equal && !(c - cn > tol));
+            // after a true tie across the k-th place, whoever comes next must be apart from it, too
+            bool tie = __ballot_sync(kAll, on && there && equal) >> (k - 1) & 1;
+            while (tie && !doubt) {
+                uint32_t kmax;
+                int e;
+                next_best(kmax, e);
+                const float Lk = __shfl_sync(kAll, myL, k - 1), bk = __shfl_sync(kAll, b, k - 1);
+                const float ck = __shfl_sync(kAll, c, k - 1), tk = __shfl_sync(kAll, tol, k - 1);
+                const bool same = kmax && row[e] == Lk && p.bias[e] == bk;
+                doubt = kmax && !same && !(ck - key_or_none(kmax) > tk);
+                tie = same;
+            }
+        }
+        if (doubt) {
+            LaneLogits<EPL> lr;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) lr.v[i] = v[i];
+            myE = choose64<EPL>(lr, p.bias, E, k, p.G, p.kg, p.best, p.gs, p.sigmoid, lane);
+            on = lane < k && myE >= 0;
+            myL = on ? row[myE] : -INFINITY;
+        }
+        const bool any = __any_sync(kAll, on), live = masked_in && any;
+        on = on && live;
+
+        // the weights, to full precision: by ratios of e^L where all scores are tiny
+        float Lm = on ? myL : -INFINITY;
+#pragma unroll
+        for (int off = 4; off >= 1; off >>= 1) Lm = fmaxf(Lm, __shfl_xor_sync(kAll, Lm, off));
+        Lm = __shfl_sync(kAll, Lm, 0);
+        float x = 0.0f;
+        if (on) {
+            if (p.renorm) x = !p.sigmoid || Lm < -60.0f ? expf(myL - Lm) : 1.0f / (1.0f + expf(-myL));
+            else x = p.sigmoid ? 1.0f / (1.0f + expf(-myL)) : expf(myL - top);
+            if (!p.sigmoid && S != S) x = S;  // a NaN or infinite logit shows, chosen or not
+        }
+        float z = 0.0f;
+        if (p.renorm) {
+            z = x;
+#pragma unroll
+            for (int off = 4; off >= 1; off >>= 1) z += __shfl_xor_sync(kAll, z, off);
+        } else if (!p.sigmoid) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) z += v[i] == -INFINITY ? 0.0f : expf(v[i] - top);
+            z = warp_sum(z);
+        } else {
+            z = 1.0f;
+        }
+        if (lane < k) {
+            p.idx[static_cast<size_t>(t) * k + lane] = on ? myE : -1;
+            p.w[static_cast<size_t>(t) * k + lane] = on ? p.scale * (x / z) : 0.0f;
+        }
+        if (on) atomicAdd(&sh.hist[myE], 1);
+        if (live) {
+            if (p.sigmoid && top < -60.0f) {  // scores as small as that: their ratios
+                float q = 0.0f;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) {
+                    s[i] = v[i] == -INFINITY ? 0.0f : __expf(v[i] - top);
+                    q += s[i];
+                }
+                q = __fdividef(1.0f, warp_sum(q));
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) accp[i] += s[i] * q;
+            } else {
+                const float q = p.sigmoid ? inv : 1.0f;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) accp[i] += s[i] * q;
+            }
+            ++accn;
+        }
+        if (++rows32 == 32) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) { bigp[i] += accp[i]; accp[i] = 0.0f; }
+            rows32 = 0;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+        if (lane * EPL + i < E) sm[warp * E + lane * EPL + i] = bigp[i] + accp[i];
+    router_sums(p.sums, sm, sh, E, k, 0.0f, accn);
+}
+
+struct GroupBwdArgs {
+    const float* logits;
+    const uint8_t* mask;
+    const int32_t* idx;
+    const float* w;
+    const int32_t* counts;
+    const int32_t* n_routed;
+    const float* d_loss;    // [1] or null
+    const float* d_w;       // [T, k] or null
+    float* d_logits;
+    const int32_t* d_T;
+    int T_host, T_max, E, k;
+    int sigmoid, renorm;
+    float inv_scale;        // 0 where scale is
+    EtHeader* hdr;
+};
+
+// One row a warp; scores are made again from the logits.  With q = 1 - s (sigmoid) or 1
+// (softmax), p = s / sum s and W_j = w_j d_w_j:
+//   d_L[e] = q_e (d_loss p_e (C_e - sum C p) + sum_{j: idx_j = e} (W_j - r_j)) - u p_e,
+//   r_j = w_j sum W / scale with renorm; u = sum W for softmax without; else 0.
+// A token is routed if it has an index that is not -1.
+template <int EPL>
+__global__ void __launch_bounds__(256) router_groups_bwd_kernel(const GroupBwdArgs p) {
+    constexpr uint32_t kAll = 0xffffffffu;
+    __shared__ float add_s[8][32 * EPL];  // a row's gradients through the gate weights, by expert
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+    const int E = p.E, k = p.k;
+    grid_begin();
+    bool ok;
+    const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
+    if (!ok) return;
+    float* add = add_s[warp];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) add[lane + 32 * i] = 0.0f;
+    __syncwarp();
+    const int t0 = blockIdx.x * nwarps + warp, step = gridDim.x * nwarps;
+    struct Row {
+        float v[EPL], w, dw;
+        int e, on;
+    };
+    auto load = [&](int t, Row& r) {
+        const bool in = t < T, sel = in && lane < k;
+        const float* L = p.logits + static_cast<size_t>(t) * E;
+        const size_t o = static_cast<size_t>(t) * k + lane;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) r.v[i] = in && lane + 32 * i < E ? L[lane + 32 * i] : -INFINITY;
+        r.on = in && (!p.mask || p.mask[t] != 0);
+        r.e = sel ? p.idx[o] : -1;
+        r.w = sel ? p.w[o] : 0.0f;
+        r.dw = sel && p.d_w ? p.d_w[o] : 0.0f;
+    };
+    Row nx;
+    load(t0, nx);
+    const int n = *p.n_routed;
+    const float rows = n > 0 ? static_cast<float>(n) : 1.0f;
+    const float dl = p.d_loss ? *p.d_loss : 0.0f;
+    float cost[EPL];  // E counts / (n^2 k): what a unit of p on expert e costs
+    const float per = static_cast<float>(E) / (rows * k) / rows;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) cost[i] = lane + 32 * i < E ? per * static_cast<float>(p.counts[lane + 32 * i]) : 0.0f;
+    for (int t = t0; t < T; t += step) {
+        const Row c = nx;
+        load(t + step, nx);
+        float top = c.v[0];
+#pragma unroll
+        for (int i = 1; i < EPL; ++i) top = fmaxf(top, c.v[i]);
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
+        const bool sel = c.e >= 0 && c.e < E;
+        const bool any = __any_sync(kAll, c.e >= 0), live = c.on && any;
+        float d[EPL];
+        if (live) {
+            const float W = c.e >= 0 ? c.w * c.dw : 0.0f;
+            const bool ratio = !p.sigmoid || top < -60.0f;  // scores as ratios of e^L
+            float s[EPL], q[EPL], S = 0.0f, cp = 0.0f, sum = W;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const bool there = !(c.v[i] == -INFINITY);
+                const float e = __expf(-fabsf(c.v[i]));  // sigmoid of either sign without overflow
+                const float h = __fdividef(1.0f, 1.0f + e);
+                const float lo = e * h;
+                s[i] = !there ? 0.0f : ratio ? __expf(c.v[i] - top) : c.v[i] < 0.0f ? lo : h;
+                q[i] = !p.sigmoid ? 1.0f : c.v[i] < 0.0f ? h : lo;
+                if (c.v[i] != c.v[i]) s[i] = q[i] = c.v[i];
+                S += s[i];
+                cp += s[i] * cost[i];
+            }
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) {  // three sums, interleaved
+                S += __shfl_xor_sync(kAll, S, off);
+                cp += __shfl_xor_sync(kAll, cp, off);
+                sum += __shfl_xor_sync(kAll, sum, off);
+            }
+            const float inv = __fdividef(1.0f, S);
+            cp *= inv;
+            const float u = !p.renorm && !p.sigmoid ? sum : 0.0f;
+            if (p.d_w) {
+                // an index outside [0, E) adds nothing; one that comes twice adds twice
+                if (sel) atomicAdd(add + c.e, p.renorm ? W - c.w * p.inv_scale * sum : W);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) d[i] = add[lane + 32 * i];
+                __syncwarp();
+                if (sel) add[c.e] = 0.0f;
+                __syncwarp();
+            } else {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) d[i] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const float pr = s[i] * inv;
+                d[i] = q[i] * (dl * pr * (cost[i] - cp) + d[i]) - u * pr;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) d[i] = 0.0f;
+        }
+        float* out = p.d_logits + static_cast<size_t>(t) * E;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (lane + 32 * i < E) out[lane + 32 * i] = d[i];
+    }
+}
+
+int groups_check(int T, const int32_t* d_T, int T_max, int E, int k, int score, float scale) {
+    std::string why;
+    if (!router_shape_ok(T_max, E, k, &why)) return api_fail(ET_ERR_UNSUPPORTED, why);
+    if (score != ET_SCORE_SOFTMAX && score != ET_SCORE_SIGMOID)
+        return api_fail(ET_ERR_INVALID, "score must be ET_SCORE_SOFTMAX or ET_SCORE_SIGMOID");
+    if (!std::isfinite(scale)) return api_fail(ET_ERR_INVALID, "scale must be finite");
+    if (!d_T && (T < 0 || T > T_max)) return api_fail(ET_ERR_INVALID, "T must be in [0, T_max]");
+    return ET_OK;
+}
+
+}  // namespace
+}  // namespace et
+
+using namespace et;
+
+extern "C" {
+
+size_t et_router_groups_workspace_bytes(int T_max, int E, int k) {
+    std::string why;
+    return router_shape_ok(T_max, E, k, &why) ? router_layout(E).total : 0;
+}
+
+int et_router_groups(const float* logits, const float* bias, const uint8_t* token_mask, int score, int n_groups, int k_groups,
+                     int group_best, int renorm, float scale, int32_t* topk_idx, float* topk_w, int32_t* expert_counts,
+                     int32_t* n_routed, float* mean_prob, float* loss, int T, const int32_t* d_T, int T_max, int E, int k,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+    return api_entry([&]() -> int {
+        int rc = groups_check(T, d_T, T_max, E, k, score, scale);
+        if (rc) return rc;
+        if (n_groups < 1 || n_groups > kGroupsMax || E % n_groups)
+            return api_fail(ET_ERR_UNSUPPORTED, "n_groups must be in [1, 32] and divide E");
+        if (k_groups < 1 || k_groups > n_groups || k > E / n_groups * k_groups)
+            return api_fail(ET_ERR_UNSUPPORTED, "k_groups must be in [1, n_groups] and its experts at least k");
+        if (group_best < 1 || group_best > 2) return api_fail(ET_ERR_UNSUPPORTED, "group_best must be 1 or 2");
+        if (!logits || !topk_idx || !topk_w)
+            return api_fail(ET_ERR_INVALID, "logits, topk_idx and topk_w must be non-NULL");
+        const void* need4[] = {logits, bias, topk_idx, topk_w, expert_counts, n_routed, mean_prob, loss, d_T};
+        for (const void* q : need4)
+            if (!api_aligned(q, 4)) return api_fail(ET_ERR_INVALID, "tensors must be aligned to their element size");
+        const RouterLayout L = router_layout(E);
+        if ((rc = api_check_ws(workspace, workspace_bytes, L.total))) return rc;
+        int dev = 0, sms = 0;
+        if ((rc = api_device(&dev, &sms))) return rc;
+        const int epl = E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : 8, gs = E / n_groups;
+        const int lanes = gs % epl ? 0 : gs / epl;
+        const GroupArgs a{logits, bias, token_mask, topk_idx, topk_w, d_T, T, T_max, E, k, n_groups, k_groups, group_best, gs,
+                          lanes & (lanes - 1) ? 0 : lanes, score == ET_SCORE_SIGMOID, renorm != 0, scale,
+                          router_sums_args(workspace, L, expert_counts, n_routed, mean_prob, loss, false)};
+        const RouterGrid g = router_grid(d_T ? T_max : T > 0 ? T : 1, E);
+        auto kernel = epl == 1 ? router_groups_kernel<1> : epl == 2 ? router_groups_kernel<2>
+                    : epl == 4 ? router_groups_kernel<4> : router_groups_kernel<8>;
+        const cudaError_t e = api_launch(kernel, g.ctas, g.warps * 32, g.smem, stream, a);
+        if (e != cudaSuccess) return api_fail_cuda(e, "launch of the grouped router kernel");
+        return ET_OK;
+    });
+}
+
+int et_router_groups_bwd(const float* logits, const uint8_t* token_mask, int score, int renorm, float scale,
+                         const int32_t* topk_idx, const float* topk_w, const int32_t* expert_counts, const int32_t* n_routed,
+                         const float* d_loss, const float* d_topk_w, float* d_logits, int T, const int32_t* d_T, int T_max,
+                         int E, int k, void* workspace, size_t workspace_bytes, void* stream) {
+    return api_entry([&]() -> int {
+        int rc = groups_check(T, d_T, T_max, E, k, score, scale);
+        if (rc) return rc;
+        if (!logits || !topk_idx || !topk_w || !expert_counts || !n_routed || !d_logits)
+            return api_fail(ET_ERR_INVALID, "logits, topk_idx, topk_w, expert_counts, n_routed and d_logits "
+                                            "must be non-NULL");
+        const void* need4[] = {logits, topk_idx, topk_w, expert_counts, n_routed, d_loss, d_topk_w, d_logits, d_T};
+        for (const void* q : need4)
+            if (!api_aligned(q, 4)) return api_fail(ET_ERR_INVALID, "tensors must be aligned to their element size");
+        if ((rc = api_check_ws(workspace, workspace_bytes, kHeaderBytes))) return rc;
+        if (!d_T && T == 0) return ET_OK;
+        int dev = 0, sms = 0;
+        if ((rc = api_device(&dev, &sms))) return rc;
+        const GroupBwdArgs a{logits, token_mask, topk_idx, topk_w, expert_counts, n_routed, d_loss, d_topk_w, d_logits, d_T,
+                             T, T_max, E, k, score == ET_SCORE_SIGMOID, renorm != 0, scale != 0.0f ? 1.0f / scale : 0.0f,
+                             static_cast<EtHeader*>(workspace)};
+        const int rows = d_T ? T_max : T;
+        int grid = ceil_div_i(rows, 8);
+        grid = grid < 8 * sms ? grid : 8 * sms;
+        auto kernel = E <= 32 ? router_groups_bwd_kernel<1> : E <= 64 ? router_groups_bwd_kernel<2>
+                    : E <= 128 ? router_groups_bwd_kernel<4> : router_groups_bwd_kernel<8>;
+        const cudaError_t e = api_launch(kernel, grid, 256, 0, stream, a);
+        if (e != cudaSuccess) return api_fail_cuda(e, "launch of the grouped router's backward kernel");
+        return ET_OK;
+    });
+}
+
+}  // extern "C"

@@ -18,6 +18,8 @@ LIB_PATH = os.path.join(HERE, "_build", "libetmoe.so")
 ET_OK, ET_ERR_INVALID, ET_ERR_WORKSPACE, ET_ERR_UNSUPPORTED, ET_ERR_CUDA, ET_ERR_TIMEOUT, \
     ET_ERR_BOUNDS = range(7)
 
+ET_SCORE_SOFTMAX, ET_SCORE_SIGMOID = range(2)
+
 STATUS_NAMES = {0: "ET_OK", 1: "ET_ERR_INVALID", 2: "ET_ERR_WORKSPACE", 3: "ET_ERR_UNSUPPORTED",
                 4: "ET_ERR_CUDA", 5: "ET_ERR_TIMEOUT", 6: "ET_ERR_BOUNDS"}
 
@@ -49,6 +51,8 @@ _lib = None
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
+_f = ctypes.c_float
+_u64 = ctypes.c_uint64
 
 _SIGNATURES = {
     "et_version": (_i, []),
@@ -83,6 +87,18 @@ _SIGNATURES = {
     "et_w4_gemv": (_i, [_vp] * 4 + [_i, _vp] + [_i] * 4 + [_vp, _sz, _vp]),
     "et_w4_experts_workspace_bytes": (_sz, [_i] * 6),
     "et_w4_experts": (_i, [_vp] * 10 + [_i, _vp] + [_i] * 6 + [_vp, _sz, _vp]),
+    "et_router_groups_workspace_bytes": (_sz, [_i, _i, _i]),
+    "et_router_groups": (_i, [_vp] * 3 + [_i] * 5 + [_f] + [_vp] * 6 + [_i, _vp] + [_i] * 3 + [_vp, _sz, _vp]),
+    "et_router_groups_bwd": (_i, [_vp, _vp, _i, _i, _f] + [_vp] * 7 + [_i, _vp] + [_i] * 3 + [_vp, _sz, _vp]),
+    "et_dropout_workspace_bytes": (_sz, [_i, _i]),
+    "et_dropout": (_i, [_vp] * 3 + [_f, _u64, _u64, _vp, _i, _vp, _i, _i, _vp, _sz, _vp]),
+    "et_layer_norm_workspace_bytes": (_sz, [_i, _i]),
+    "et_layer_norm": (_i, [_vp] * 4 + [_f, _f, _u64, _u64] + [_vp] * 3 + [_i, _vp, _i, _i, _vp, _sz, _vp]),
+    "et_layer_norm_bwd": (_i, [_vp] * 3 + [_f, _f, _u64, _u64] + [_vp] * 7 + [_i, _vp, _i, _i, _vp, _sz, _vp]),
+    "et_i8_quantize_workspace_bytes": (_sz, [_i, _i]),
+    "et_i8_quantize": (_i, [_vp] * 3 + [_i, _vp, _i, _i, _vp, _sz, _vp]),
+    "et_i8_gemm_workspace_bytes": (_sz, [_i] * 3),
+    "et_i8_gemm": (_i, [_vp] * 5 + [_i, _vp] + [_i] * 3 + [_vp, _sz, _vp]),
     "et_status": (_i, [_vp, _vp, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)]),
     "et_reset_status": (_i, [_vp, _vp]),
 }
@@ -331,7 +347,7 @@ def et_mlp_chain(x, gamma, eps, w_gate, w_up, w_down, out, *, B=None, d_B=None, 
     return rc
 
 
-# ------------------------------------------------------------------ router, norms, 4-bit weights
+# ------------------------------------------------------------------ router, norms, dropout, 4-bit and 8-bit products
 #
 # These calls check what the C ABI cannot see: each tensor's type, shape,
 # contiguity and device (ValueError).  They run on the tensors' device, on
@@ -343,9 +359,9 @@ torch = None  # imported by the first of these calls: the library opens without 
 def _bind_torch():
     """Names that every call needs, and the current stream's handle without building a Stream object
     (3 us of a call that takes 8) and the current device, where this torch has them."""
-    global torch, _BF16, _F32, _I32, _U8, _raw_stream, _current_device
+    global torch, _BF16, _F32, _I32, _U8, _I8, _raw_stream, _current_device
     import torch as t
-    _BF16, _F32, _I32, _U8 = t.bfloat16, t.float32, t.int32, t.uint8
+    _BF16, _F32, _I32, _U8, _I8 = t.bfloat16, t.float32, t.int32, t.uint8, t.int8
     _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or (lambda dev: t.cuda.current_stream(dev).cuda_stream)
     _current_device = getattr(t._C, "_cuda_getDevice", None) or t.cuda.current_device
     torch = t  # last: another thread that sees it finds the rest
@@ -596,6 +612,143 @@ def et_w4_experts(x, topk_idx, topk_w, q_gate, s_gate, q_up, s_up, q_down, s_dow
         _arg(topk_w, "topk_w", _F32, (T_max, k), dev), pqg, psg, pqu, psu, pqd, psd,
         _arg(out, "out", _BF16, (T_max, H), dev), _rows(T, T_max), _count_arg(d_T, dev), T_max, H, F, E, k,
         group, ws, wsb), check)
+
+
+@functools.lru_cache(maxsize=None)
+def et_router_groups_workspace_bytes(T_max, E, k) -> int:
+    return _workspace_bytes(load().et_router_groups_workspace_bytes, T_max, E, k)
+
+
+def et_router_groups(logits, topk_idx, topk_w, *, score, n_groups=1, k_groups=1, group_best=2, bias=None, renorm=True,
+                     scale=1.0, token_mask=None, expert_counts=None, n_routed=None, mean_prob=None, loss=None, T=None,
+                     d_T=None, workspace, stream=None, check=True):
+    """Top-k by score (ET_SCORE_SOFTMAX or ET_SCORE_SIGMOID of logits [T_max, E]) + bias within the k_groups best of
+    n_groups groups: indices, gate weights, counts, balance loss."""
+    dev = _device_of(logits, "logits")
+    T_max, E = logits.shape
+    k = topk_idx.shape[-1]
+    _fits(T_max | E | k | n_groups | k_groups | group_best)
+    ws, wsb = _workspace_args(workspace, dev)
+    return _call(load().et_router_groups, dev, stream, (
+        _arg(logits, "logits", _F32, (T_max, E), dev), _arg(bias, "bias", _F32, (E,), dev),
+        _arg(token_mask, "token_mask", _U8, (T_max,), dev), score, n_groups, k_groups, group_best, 1 if renorm else 0, scale,
+        _arg(topk_idx, "topk_idx", _I32, (T_max, k), dev), _arg(topk_w, "topk_w", _F32, (T_max, k), dev),
+        _arg(expert_counts, "expert_counts", _I32, (E,), dev), _arg(n_routed, "n_routed", _I32, (1,), dev),
+        _arg(mean_prob, "mean_prob", _F32, (E,), dev), _arg(loss, "loss", _F32, (1,), dev),
+        _rows(T, T_max), _count_arg(d_T, dev), T_max, E, k, ws, wsb), check)
+
+
+def et_router_groups_bwd(logits, topk_idx, topk_w, expert_counts, n_routed, d_logits, *, score, renorm=True, scale=1.0,
+                         token_mask=None, d_loss=None, d_topk_w=None, T=None, d_T=None, workspace, stream=None, check=True):
+    """Gradient of et_router_groups's loss (d_loss [1]) and gate weights (d_topk_w [T_max, k])."""
+    dev = _device_of(logits, "logits")
+    T_max, E = logits.shape
+    k = topk_idx.shape[-1]
+    _fits(T_max | E | k)
+    ws, wsb = _workspace_args(workspace, dev)
+    return _call(load().et_router_groups_bwd, dev, stream, (
+        _arg(logits, "logits", _F32, (T_max, E), dev), _arg(token_mask, "token_mask", _U8, (T_max,), dev),
+        score, 1 if renorm else 0, scale,
+        _arg(topk_idx, "topk_idx", _I32, (T_max, k), dev), _arg(topk_w, "topk_w", _F32, (T_max, k), dev),
+        _arg(expert_counts, "expert_counts", _I32, (E,), dev), _arg(n_routed, "n_routed", _I32, (1,), dev),
+        _arg(d_loss, "d_loss", _F32, (1,), dev), _arg(d_topk_w, "d_topk_w", _F32, (T_max, k), dev),
+        _arg(d_logits, "d_logits", _F32, (T_max, E), dev),
+        _rows(T, T_max), _count_arg(d_T, dev), T_max, E, k, ws, wsb), check)
+
+
+def _rng_args(p, seed, offset, d_rng, dev):
+    """p, seed, offset and the pointer of a device {seed, offset} (int64 or uint64 [2])."""
+    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+        raise ValueError("seed and offset must be in [0, 2^64)")
+    if d_rng is None or isinstance(d_rng, int):
+        return p, seed, offset, d_rng
+    if d_rng.dtype not in (torch.int64, torch.uint64) or d_rng.shape != (2,) or not d_rng.is_contiguous() or d_rng.get_device() != dev:
+        raise ValueError(f"d_rng must be two int64 or uint64 on CUDA device {dev}")
+    return p, seed, offset, d_rng.data_ptr()
+
+
+@functools.lru_cache(maxsize=None)
+def et_dropout_workspace_bytes(T_max, H) -> int:
+    return _workspace_bytes(load().et_dropout_workspace_bytes, T_max, H)
+
+
+def et_dropout(x, y, out, *, p, seed=0, offset=0, d_rng=None, T=None, d_T=None, workspace, stream=None, check=True):
+    """out = x + dropout(y) (x None: without it); on the gradient of out, with x None, the gradient of y."""
+    dev = _device_of(y, "y")
+    T_max, H = rows = y.shape
+    _fits(T_max | H)
+    ws, wsb = _workspace_args(workspace, dev)
+    return _call(load().et_dropout, dev, stream, (
+        _arg(x, "x", _BF16, rows, dev), _arg(y, "y", _BF16, rows, dev), _arg(out, "out", _BF16, rows, dev),
+        *_rng_args(p, seed, offset, d_rng, dev), _rows(T, T_max), _count_arg(d_T, dev), T_max, H, ws, wsb), check)
+
+
+@functools.lru_cache(maxsize=None)
+def et_layer_norm_workspace_bytes(T_max, H) -> int:
+    return _workspace_bytes(load().et_layer_norm_workspace_bytes, T_max, H)
+
+
+def et_layer_norm(x, y, x_out, x_hat, *, gamma=None, beta=None, eps, p=0.0, seed=0, offset=0, d_rng=None, T=None, d_T=None,
+                  workspace, stream=None, check=True):
+    """x_out = x + dropout(y) and x_hat = LayerNorm(x_out) * gamma + beta (y, x_out, gamma, beta may be None)."""
+    dev = _device_of(x, "x")
+    T_max, H = rows = x.shape
+    _fits(T_max | H)
+    ws, wsb = _workspace_args(workspace, dev)
+    return _call(load().et_layer_norm, dev, stream, (
+        _arg(x, "x", _BF16, rows, dev), _arg(y, "y", _BF16, rows, dev), _arg(gamma, "gamma", _BF16, (H,), dev),
+        _arg(beta, "beta", _BF16, (H,), dev), eps, *_rng_args(p, seed, offset, d_rng, dev),
+        _arg(x_out, "x_out", _BF16, rows, dev), _arg(x_hat, "x_hat", _BF16, rows, dev), _rows(T, T_max),
+        _count_arg(d_T, dev), T_max, H, ws, wsb), check)
+
+
+def et_layer_norm_bwd(x, y, d_x_out, d_x_hat, dx, dy, *, gamma=None, eps, p=0.0, seed=0, offset=0, d_rng=None, d_gamma=None,
+                      d_beta=None, T=None, d_T=None, workspace, stream=None, check=True):
+    """Gradient of et_layer_norm: dx, dy (may be None) and, where given, d_gamma and d_beta (fp32)."""
+    dev = _device_of(x, "x")
+    T_max, H = rows = x.shape
+    _fits(T_max | H)
+    ws, wsb = _workspace_args(workspace, dev)
+    return _call(load().et_layer_norm_bwd, dev, stream, (
+        _arg(x, "x", _BF16, rows, dev), _arg(y, "y", _BF16, rows, dev), _arg(gamma, "gamma", _BF16, (H,), dev), eps,
+        *_rng_args(p, seed, offset, d_rng, dev), _arg(d_x_out, "d_x_out", _BF16, rows, dev),
+        _arg(d_x_hat, "d_x_hat", _BF16, rows, dev), _arg(dx, "dx", _BF16, rows, dev), _arg(dy, "dy", _BF16, rows, dev),
+        _arg(d_gamma, "d_gamma", _F32, (H,), dev), _arg(d_beta, "d_beta", _F32, (H,), dev), _rows(T, T_max),
+        _count_arg(d_T, dev), T_max, H, ws, wsb), check)
+
+
+@functools.lru_cache(maxsize=None)
+def et_i8_quantize_workspace_bytes(M_max, K) -> int:
+    return _workspace_bytes(load().et_i8_quantize_workspace_bytes, M_max, K)
+
+
+def et_i8_quantize(x, q, scale, *, M=None, d_M=None, workspace, stream=None, check=True):
+    """bf16 rows x [M_max, K] -> int8 q and fp32 scale [M_max], one for each row (a token, or a weight's channel)."""
+    dev = _device_of(x, "x")
+    M_max, K = x.shape
+    _fits(M_max | K)
+    ws, wsb = _workspace_args(workspace, dev)
+    return _call(load().et_i8_quantize, dev, stream, (
+        _arg(x, "x", _BF16, (M_max, K), dev), _arg(q, "q", _I8, (M_max, K), dev), _arg(scale, "scale", _F32, (M_max,), dev),
+        _rows(M, M_max), _count_arg(d_M, dev), M_max, K, ws, wsb), check)
+
+
+@functools.lru_cache(maxsize=None)
+def et_i8_gemm_workspace_bytes(M_max, N, K) -> int:
+    return _workspace_bytes(load().et_i8_gemm_workspace_bytes, M_max, N, K)
+
+
+def et_i8_gemm(x_q, s_x, w_q, s_w, Y, *, M=None, d_M=None, workspace, stream=None, check=True):
+    """Y = (s_x s_w^T) * (x_q w_q^T) for int8 x_q [M_max, K] and w_q [N, K] with their fp32 scales."""
+    dev = _device_of(x_q, "x_q")
+    M_max, K = x_q.shape
+    N = Y.shape[-1]
+    _fits(M_max | N | K)
+    ws, wsb = _workspace_args(workspace, dev)
+    return _call(load().et_i8_gemm, dev, stream, (
+        _arg(x_q, "x_q", _I8, (M_max, K), dev), _arg(s_x, "s_x", _F32, (M_max,), dev), _arg(w_q, "w_q", _I8, (N, K), dev),
+        _arg(s_w, "s_w", _F32, (N,), dev), _arg(Y, "Y", _BF16, (M_max, N), dev), _rows(M, M_max), _count_arg(d_M, dev),
+        M_max, N, K, ws, wsb), check)
 
 
 def et_status(workspace, stream=None):
