@@ -317,6 +317,20 @@ int api_check_ws(const void* ws, size_t have, size_t need) {
     return check_ws(const_cast<void*>(ws), have, need);
 }
 
+int api_map128(CUtensorMap* m, const void* base, int elem_bytes, uint64_t rows, uint64_t cols, uint32_t box_rows, const char* what) {
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {cols * elem_bytes};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elem_bytes), box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    const CUresult r = g_encode(m, elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                                const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(ET_ERR_CUDA, std::string("cuTensorMapEncodeTiled failed for ") + what + " (code " +
+                                     std::to_string(static_cast<int>(r)) + ")");
+    return ET_OK;
+}
+
 }  // namespace et
 
 extern "C" {

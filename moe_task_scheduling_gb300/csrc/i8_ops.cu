@@ -4,6 +4,7 @@
 
 #include "../../include/etmoe.h"
 #include "et_api.h"
+#include "i8_gemm.h"
 #include "row_ops.cuh"
 
 namespace et {
@@ -105,6 +106,7 @@ struct I8GemmArgs {
 
 constexpr int kGemvWarps = 8;
 constexpr int kGemvRows = 4;  // channels of a CTA
+constexpr int kGemvTokens = 4;  // most tokens of a call that takes this form
 
 // MR tokens times four channels a CTA, whose warps take 512-byte pieces of K in turn:
 // dp4a on 16-byte loads, sums exact in int32.  The weights come once from memory, the
@@ -179,6 +181,49 @@ int i8_check_rows(int M, const int32_t* d_M, int M_max) {
     return ET_OK;
 }
 
+// How a product of M rows runs, and what it needs of the workspace.
+struct I8Plan {
+    bool pair;
+    int tn, mt, nt, kblocks, grid, share;
+    size_t count, x16, part, total;
+};
+
+int ceil_div_l(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
+
+I8Plan i8_plan(int M, int N, int K) {
+    I8Plan p{};
+    p.total = kHeaderBytes;
+    if (M <= kGemvTokens) return p;
+    p.kblocks = ceil_div_l(K, kI8KBlock);
+    p.mt = ceil_div_l(M, kI8TokensMax);
+    p.pair = static_cast<long long>(p.mt) * ceil_div_l(N, 256) >= kI8Sms / 2;
+    p.tn = ceil_div_l(ceil_div_l(M, p.mt), 32) * 32;
+    if (M <= 16) p.tn = 16;
+    p.nt = ceil_div_l(N, p.pair ? 256 : 128);
+    const int most = p.pair ? kI8Sms / 2 : kI8Sms;
+    const long long tiles = static_cast<long long>(p.mt) * p.nt, blocks = tiles * p.kblocks;
+    // whole tiles where their last round leaves few CTAs idle; else even shares of all
+    // k-blocks, four or more a CTA
+    p.share = 10 * tiles < 8ll * ceil_div_l(tiles, most) * most;
+    p.grid = most;
+    if (p.share && blocks < 4ll * most) p.grid = blocks < 4 ? 1 : static_cast<int>(blocks / 4);
+    // Regions that M alone sizes and that grow with it, so that a call with fewer rows than
+    // M_max finds room.  Shared tiles: fewer than 4 x 152, as more fill their rounds; parts: two
+    // a CTA, at most 152 x 128 channels x (M, 256 at most).
+    p.count = 1024;
+    p.part = 4096;
+    const size_t widest = ceil_div_l(M < kI8TokensMax ? M : kI8TokensMax, 32) * 32;
+    p.x16 = p.part + 2ull * kI8Sms * 128 * sizeof(float) * widest;
+    p.total = (p.x16 + 2ull * M * K + 255) / 256 * 256;
+    return p;
+}
+
+// Tokens that are held as fp16 at a time: at K = 4096 they stay in L2 with their weights,
+// and the workspace of a long batch stays small.
+constexpr int kI8RowsPass = 8192;
+
+size_t i8_ws_bytes(int M_max, int N, int K) { return i8_plan(M_max < kI8RowsPass ? M_max : kI8RowsPass, N, K).total; }
+
 template <bool VEC>
 cudaError_t launch_i8_quantize(I8QuantArgs a, int rows, int sms, void* stream) {
     const int cols = a.K < kNormHMax ? a.K : kNormHMax;
@@ -230,7 +275,7 @@ int et_i8_quantize(const void* x, void* q, float* scale, int M, const int32_t* d
 
 size_t et_i8_gemm_workspace_bytes(int M_max, int N, int K) {
     std::string why;
-    return i8_shape_ok(M_max, N, K, &why) ? kHeaderBytes : 0;
+    return i8_shape_ok(M_max, N, K, &why) ? i8_ws_bytes(M_max, N, K) : 0;
 }
 
 int et_i8_gemm(const void* x_q, const float* s_x, const void* w_q, const float* s_w, void* Y, int M, const int32_t* d_M,
@@ -244,20 +289,50 @@ int et_i8_gemm(const void* x_q, const float* s_x, const void* w_q, const float* 
             return api_fail(ET_ERR_INVALID, "tensors must be aligned to their element size");
         int rc = i8_check_rows(M, d_M, M_max);
         if (rc) return rc;
-        if ((rc = api_check_ws(workspace, workspace_bytes, et_i8_gemm_workspace_bytes(M_max, N, K)))) return rc;
+        if ((rc = api_check_ws(workspace, workspace_bytes, i8_ws_bytes(M_max, N, K)))) return rc;
         if (!d_M && M == 0) return ET_OK;
         int dev = 0, sms = 0;
         if ((rc = api_device(&dev, &sms))) return rc;
-        const I8GemmArgs a{static_cast<const int8_t*>(x_q), s_x, static_cast<const int8_t*>(w_q), s_w, static_cast<bf16*>(Y),
-                           d_M, M, M_max, N, K, static_cast<EtHeader*>(workspace)};
-        const int rows = d_M ? M_max : M;
-        const int mr = rows == 1 ? 1 : rows == 2 ? 2 : rows <= 4 ? 4 : 8;
-        auto kernel = mr == 1 ? i8_gemv_kernel<1> : mr == 2 ? i8_gemv_kernel<2> : mr == 4 ? i8_gemv_kernel<4> : i8_gemv_kernel<8>;
-        const long long gy = (static_cast<long long>(rows) + mr - 1) / mr;
-        if (gy > 65535) return api_fail(ET_ERR_UNSUPPORTED, "too many rows");
-        const cudaError_t e = api_launch(kernel, dim3((N + kGemvRows - 1) / kGemvRows, static_cast<unsigned>(gy)),
-                                         kGemvWarps * 32, 0, stream, a);
-        if (e != cudaSuccess) return api_fail_cuda(e, "launch of the int8 product");
+        const int all = d_M ? M_max : M;
+        uint8_t* ws = static_cast<uint8_t*>(workspace);
+        EtHeader* hdr = reinterpret_cast<EtHeader*>(ws);
+        const int8_t* x = static_cast<const int8_t*>(x_q);
+        bf16* y = static_cast<bf16*>(Y);
+        if (all <= kGemvTokens) {
+            const I8GemmArgs a{x, s_x, static_cast<const int8_t*>(w_q), s_w, y, d_M, M, all, N, K, hdr};
+            auto kernel = all == 1 ? i8_gemv_kernel<1> : all == 2 ? i8_gemv_kernel<2> : i8_gemv_kernel<4>;
+            const cudaError_t e = api_launch(kernel, dim3((N + kGemvRows - 1) / kGemvRows), kGemvWarps * 32, 0, stream, a);
+            if (e != cudaSuccess) return api_fail_cuda(e, "launch of the int8 product");
+            return ET_OK;
+        }
+        CUtensorMap mw, mx;
+        if ((rc = api_map128(&mw, w_q, 1, N, K, 128, "w_q"))) return rc;
+        for (int m0 = 0; m0 < all; m0 += kI8RowsPass) {
+            const int rows = all - m0 < kI8RowsPass ? all - m0 : kI8RowsPass;
+            const I8Plan pl = i8_plan(rows, N, K);
+            I8TcArgs a{};
+            a.sx = s_x + m0;
+            a.sw = s_w;
+            a.y = y + static_cast<size_t>(m0) * N;
+            a.rows = {d_M, m0, rows, all};
+            a.N = N;
+            a.hdr = hdr;
+            a.tile_count = reinterpret_cast<int32_t*>(ws + pl.count);
+            a.part = reinterpret_cast<float*>(ws + pl.part);
+            a.tn = pl.tn;
+            a.nt = pl.nt;
+            a.kblocks = pl.kblocks;
+            a.grid = pl.grid;
+            a.share = pl.share;
+            i8_tc_stages(pl.pair, pl.tn, &a.stages_w, &a.stages_x);
+            a.timeout_ns = 200000000ull;
+            if ((rc = api_map128(&mx, ws + pl.x16, 2, rows, K, pl.tn / (pl.pair ? 2 : 1), "x_q as fp16"))) return rc;
+            const I8ExpandArgs e16{x + static_cast<size_t>(m0) * K, ws + pl.x16, a.rows, K, hdr, a.tile_count,
+                                   pl.share ? pl.mt * pl.nt * (pl.pair ? 2 : 1) : 0};
+            cudaError_t e = launch_i8_expand(e16, sms, stream);
+            if (e == cudaSuccess) e = launch_i8_tc(a, &mw, &mx, pl.pair, dev, stream);
+            if (e != cudaSuccess) return api_fail_cuda(e, "launch of the int8 product");
+        }
         return ET_OK;
     });
 }

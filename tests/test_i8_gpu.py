@@ -94,7 +94,7 @@ GEMM = [(1, 1, 16), (1, 8, 32), (1, 4096, 14336), (2, 5, 48), (2, 1000, 1024), (
         (8, 128, 128), (8, 2000, 4096), (9, 64, 112), (12, 700, 2048), (16, 128, 1024), (16, 1024, 4096), (17, 257, 272), (31, 500, 768),
         (32, 384, 2064), (33, 1000, 144), (48, 96, 16384), (64, 512, 4096), (65, 130, 400), (100, 1000, 2048), (127, 129, 1040),
         (128, 256, 512), (129, 384, 640), (200, 1000, 2064), (255, 300, 256), (256, 1024, 1024), (257, 257, 272), (300, 2000, 528),
-        (512, 512, 2048), (777, 1111, 1008), (1000, 136, 4096), (1500, 2048, 512), (2049, 770, 784)]
+        (512, 512, 2048), (777, 1111, 1008), (1000, 136, 4096), (1500, 2048, 512), (2049, 770, 784), (2500, 2050, 272), (1111, 5000, 528), (4800, 2048, 80), (600, 6500, 1040), (8200, 1000, 144)]
 
 
 @pytest.mark.parametrize("M,N,K", GEMM)
