@@ -8,13 +8,14 @@
 // converter warps turn each 128 x 128 block into fp16 in TMEM, where the MMA takes its
 // A operand from, so that shared memory carries a weight once, as one byte.
 //
-// Roles (480 threads):
+// Roles (608 threads):
 //   warp 0        weights: TMA, int8 blocks of 128 channels x 128 k
 //   warp 1        one thread issues tcgen05.mma, D[channel, token] += W X^T
 //   warps 2..9    converters: shared memory -> registers -> fp16 -> TMEM; a thread has
 //                 half a row
-//   warps 10..13  epilogue: TMEM -> scales -> bf16, or a part's sums to the workspace
-//   warp 14       tokens: TMA, fp16 blocks of tn tokens x 128 k
+//   warps 10..17  epilogue: TMEM -> scales -> bf16, or a part's sums to the workspace; four
+//                 take the even 16-token chunks, four the odd ones
+//   warp 18       tokens: TMA, fp16 blocks of tn tokens x 128 k
 // With CG = 2 a pair of CTAs takes 256 channels: each loads and converts its own 128,
 // loads half the tokens, and the pair's MMA reads both halves, which halves the
 // traffic of the tokens into shared memory.
@@ -32,8 +33,8 @@
 namespace et {
 namespace {
 
-constexpr int kI8Threads = 480;
-constexpr int kConvWarp0 = 2, kConvWarps = 8, kEpiWarpI8 = 10, kEpiWarps = 4, kTokenWarp = 14;
+constexpr int kI8Threads = 608;
+constexpr int kConvWarp0 = 2, kConvWarps = 8, kEpiWarpI8 = 10, kEpiWarps = 8, kTokenWarp = 18;
 constexpr int kAStages = 4;          // TMEM blocks of converted weights, 64 columns each
 constexpr int kACol = 256;           // the accumulators are columns 0 .. 255
 constexpr int kWBytes = 128 * kI8KBlock;
@@ -48,7 +49,7 @@ struct I8Ctl {
     uint32_t tmem_base;
     int32_t go[2];                   // the epilogue's: the accumulator is complete (0: an abort),
     int32_t last;                    // this part was the tile's last
-    float sx[2][kI8TokensMax];
+    alignas(16) float sx[2][kI8TokensMax];
 };
 
 // ---------------------------------------------------------------- PTX that et_device.cuh has for one CTA
@@ -60,36 +61,20 @@ __device__ __forceinline__ uint32_t leader_addr(const void* p) {  // of this var
     return a;
 }
 
+// (Without .cluster scope, which would make every arrival wait for this SM's stores and
+// every wait drop its L1: what the barriers order is in TMEM and in the async proxy.)
 template <int CG>
 __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
-    if (CG == 1) {
-        mbar_arrive(bar);
-    } else {
-        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_addr<2>(bar)) : "memory");
-    }
+    if (CG == 1) mbar_arrive(bar);
+    else asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(leader_addr<2>(bar)) : "memory");
 }
 
-template <int CG>
-__device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
-    if (CG == 1) return mbar_try_wait(bar, parity);
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// mbar_wait (bounded), of either kind.
-template <int CG>
+// mbar_wait (bounded) that polls for longer before it sleeps.
 __device__ __forceinline__ bool wait(const WaitCtx& c, uint64_t* bar, uint32_t parity, int where) {
-    if (try_wait<CG>(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t it = 1;; ++it) {
-        if (try_wait<CG>(bar, parity)) return true;
+        if (mbar_try_wait(bar, parity)) return true;
         if (it > 1024) __nanosleep(64);
         if ((it & 63u) == 0) {
             if (aborted(c)) return false;
@@ -134,6 +119,13 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
                      "h"(static_cast<uint16_t>(3))
                      : "memory");
+}
+
+// True in one lane of a converged warp, the same every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
 }
 
 template <int CG>
@@ -183,6 +175,20 @@ __device__ __forceinline__ void int8_to_half(uint32_t w, uint32_t& lo, uint32_t&
     const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off), y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
     lo = *reinterpret_cast<const uint32_t*>(&x);
     hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+// A thread's values of up to 16 tokens, a row of `to` each.  The whole sixteen go out
+// without a branch between them.
+template <class V>
+__device__ __forceinline__ void store16(V* to, size_t row, const V (&v)[16], int left) {
+    if (left >= 16) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) to[c * row] = v[c];
+    } else {
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+            if (c < left) to[c * row] = v[c];
+    }
 }
 
 // ---------------------------------------------------------------- work
@@ -278,7 +284,7 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
     grid_release();
 
     const WaitCtx wc{p.hdr, p.timeout_ns};
-    const uint32_t tmem = ctl->tmem_base;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
     if (p.rows.d_M) grid_wait();
     const int M = pass_rows(p.rows, p.hdr);
     const int mt = ceil_div(M, p.tn), tiles = mt * p.nt;  // tile = n tile * mt + m tile
@@ -297,7 +303,7 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
                 const int n0 = (w.tile / mt) * 128 * CG + static_cast<int>(rank) * 128;
                 for (int kb = w.kb0; kb < w.kb1; ++kb) {
                     const uint32_t s = posted_w % p.stages_w;
-                    if (!(ok = wait<1>(wc, &ctl->empty_w[s], ((posted_w / p.stages_w) & 1u) ^ 1u, kWhereEmpty))) break;
+                    if (!(ok = wait(wc, &ctl->empty_w[s], ((posted_w / p.stages_w) & 1u) ^ 1u, kWhereEmpty))) break;
                     mbar_arrive_expect_tx(&ctl->full_w[s], kWBytes);
                     tma_load_2d(ring_w + s * kWBytes, &tm_w, &ctl->full_w[s], kb * kI8KBlock, n0, pol);
                     ++posted_w;
@@ -317,7 +323,7 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
                 const int m0 = (w.tile % mt) * p.tn + static_cast<int>(rank) * xrows;
                 for (int kb = w.kb0; kb < w.kb1; ++kb) {
                     const uint32_t s = posted_x % p.stages_x;
-                    if (!(ok = wait<CG>(wc, &ctl->empty_x[s], ((posted_x / p.stages_x) & 1u) ^ 1u, kWhereEmpty))) break;
+                    if (!(ok = wait(wc, &ctl->empty_x[s], ((posted_x / p.stages_x) & 1u) ^ 1u, kWhereEmpty))) break;
                     if (rank == 0) mbar_arrive_expect_tx(&ctl->full_x[s], xbytes * CG);
                     const uint32_t bar = leader_addr<CG>(&ctl->full_x[s]), dst = smem_u32(ring_x + s * xbytes);
                     tma_tokens<CG>(dst, &tm_x, bar, kb * kI8KBlock, m0);
@@ -331,34 +337,43 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        // The whole warp walks the work and one elected lane issues: descriptors and addresses
+        // are then uniform, which an MMA takes 37 cycles to issue with; from a branch on the
+        // lane it took 100, more than a tile of few tokens computes for.
+        if (rank == 0) {
             // D fp32, A and B fp16, both K-major
             const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(p.tn >> 3) << 17) | (static_cast<uint32_t>(128 * CG >> 4) << 24);
-            uint32_t it = 0, acc = 0;
+            uint32_t acc = 0, kx = 0, px = 0, ka = 0, pa = 0;  // ring places and their phases
             bool ok = true;
             while (ok && work.next(w)) {
-                const uint32_t slot = acc % slots;
-                if (!(ok = wait<CG>(wc, &ctl->acc_empty[slot], ((acc / slots) & 1u) ^ 1u, kWhereAcc))) break;
+                const uint32_t slot = slots == 1 ? 0 : acc & 1, turn = slots == 1 ? acc : acc >> 1;
+                ok = wait(wc, &ctl->acc_empty[slot], (turn & 1u) ^ 1u, kWhereAcc);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 const uint32_t d = tmem + slot * 128;
-                for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-                    const uint32_t sx = it % p.stages_x, sa = it % kAStages;
-                    if (!(ok = wait<CG>(wc, &ctl->full_x[sx], (it / p.stages_x) & 1u, kWhereFull) &&
-                               wait<CG>(wc, &ctl->full_a[sa], (it / kAStages) & 1u, kWhereFull)))
-                        break;
+                for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                    ok = wait(wc, &ctl->full_x[kx], px, kWhereFull) && wait(wc, &ctl->full_a[ka], pa, kWhereFull);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     tc_fence_after();
-                    const uint32_t b = smem_u32(ring_x + sx * xbytes);
+                    const uint64_t b0 = sdesc_sw128(smem_u32(ring_x + kx * xbytes)), b1 = b0 + (xrows * 128 >> 4);
+                    const uint32_t a = tmem + kACol + ka * 64;
+                    if (elect_one()) {
+                        mma_f16<CG>(d, a, b0, idesc, kb > w.kb0 ? 1u : 0u);
 #pragma unroll
-                    for (int k = 0; k < kI8KBlock / 16; ++k)
-                        mma_f16<CG>(d, tmem + kACol + sa * 64 + k * 8, sdesc_sw128(b + (k >> 2) * xrows * 128 + (k & 3) * 32), idesc,
-                                    kb > w.kb0 || k > 0 ? 1u : 0u);
-                    commit<CG>(&ctl->empty_x[sx]);
-                    commit<CG>(&ctl->empty_a[sa]);
+                        for (int k = 1; k < kI8KBlock / 16; ++k)  // 16 k are 32 bytes of a row of 64 k
+                            mma_f16<CG>(d, a + k * 8, (k < 4 ? b0 : b1) + (k & 3) * 2, idesc, 1u);
+                        commit<CG>(&ctl->empty_x[kx]);
+                        commit<CG>(&ctl->empty_a[ka]);
+                    }
+                    __syncwarp();
+                    if (++kx == static_cast<uint32_t>(p.stages_x)) { kx = 0; px ^= 1u; }
+                    if (++ka == kAStages) { ka = 0; pa ^= 1u; }
                 }
                 if (!ok) break;
-                commit<CG>(&ctl->acc_full[slot]);
+                if (elect_one()) commit<CG>(&ctl->acc_full[slot]);
+                __syncwarp();
                 ++acc;
             }
-            commit<CG>(&ctl->drain);  // every arrival above has come when this one has
+            if (elect_one()) commit<CG>(&ctl->drain);  // every arrival above has come when this one has
         }
         __syncwarp();
     } else if (warp < kEpiWarpI8) {
@@ -370,7 +385,7 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
         while (ok && work.next(w)) {
             for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                 const uint32_t sw = it % p.stages_w, sa = it % kAStages;
-                ok = wait<1>(wc, &ctl->full_w[sw], (it / p.stages_w) & 1u, kWhereFull);
+                ok = wait(wc, &ctl->full_w[sw], (it / p.stages_w) & 1u, kWhereFull);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 const uint32_t src = smem_u32(ring_w + sw * kWBytes) + row;
                 uint4 v[4];
@@ -386,7 +401,7 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->empty_w[sw]);
-                ok = wait<CG>(wc, &ctl->empty_a[sa], ((it / kAStages) & 1u) ^ 1u, kWhereEmpty);
+                ok = wait(wc, &ctl->empty_a[sa], ((it / kAStages) & 1u) ^ 1u, kWhereEmpty);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 tc_fence_after();
                 tmem_st32(a0 + sa * 64, h);
@@ -397,7 +412,7 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
             }
         }
     } else {
-        const int q = warp & 3, et = threadIdx.x - kEpiWarpI8 * 32, row = q * 32 + lane;
+        const int q = warp & 3, odd = (warp - kEpiWarpI8) >> 2, et = threadIdx.x - kEpiWarpI8 * 32, row = q * 32 + lane;
         constexpr int kChannels = 128 * CG;
         grid_wait();
         uint32_t acc = 0;
@@ -411,7 +426,7 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
             const float sw = n < p.N ? p.sw[n] : 0.0f;
             // one thread waits for all four warps: a named barrier is not bounded, so they must
             // never part
-            if (et == 0) ctl->go[acc & 1] = wait<CG>(wc, &ctl->acc_full[slot], (acc / slots) & 1u, kWhereAcc);
+            if (et == 0) ctl->go[acc & 1] = wait(wc, &ctl->acc_full[slot], (acc / slots) & 1u, kWhereAcc);
             named_bar_sync(kEpiBar, kEpiWarps * 32);
             if (!(ok = ctl->go[acc & 1] != 0)) break;
             tc_fence_after();
@@ -420,15 +435,24 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
             float* mine = p.part + ((static_cast<size_t>(cta) * 2 + (w.kb0 == 0)) * p.tn) * kChannels + rank * 128 + row;
             bf16* y = p.y + static_cast<size_t>(m0) * p.N + n;
             const uint32_t d = tmem + slot * 128 + (static_cast<uint32_t>(q * 32) << 16);
-            for (int c0 = 0; c0 < rows; c0 += 16) {
+            for (int c0 = odd * 16; c0 < rows; c0 += 32) {
                 float v[16];
                 tmem_ld16(d + c0, v);
                 tmem_ld_wait();
+                const int left = rows - c0;
+                if (part) {
+                    store16(mine + static_cast<size_t>(c0) * kChannels, kChannels, v, left);
+                } else if (n < p.N) {
+                    bf16 o[16];
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    if (c0 + c >= rows) break;
-                    if (part) mine[static_cast<size_t>(c0 + c) * kChannels] = v[c];
-                    else if (n < p.N) y[static_cast<size_t>(c0 + c) * p.N] = __float2bfloat16_rn(v[c] * (sx[c0 + c] * sw));
+                    for (int c = 0; c < 16; c += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(sx + c0 + c);
+                        o[c] = __float2bfloat16_rn(v[c] * (f.x * sw));
+                        o[c + 1] = __float2bfloat16_rn(v[c + 1] * (f.y * sw));
+                        o[c + 2] = __float2bfloat16_rn(v[c + 2] * (f.z * sw));
+                        o[c + 3] = __float2bfloat16_rn(v[c + 3] * (f.w * sw));
+                    }
+                    store16(y + static_cast<size_t>(c0) * p.N, p.N, o, left);
                 }
             }
             tc_fence_before();
@@ -449,13 +473,28 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
                 if (ctl->last) {
                     __threadfence();
                     const float* from = p.part + rank * 128 + row;
-                    for (int c = 0; c < rows; ++c) {
-                        float s = 0.0f;
-                        for (int b = b0; b <= b1; ++b) {
-                            const int begins = work.first(b) <= t0;
-                            s += __ldcg(from + ((static_cast<size_t>(b) * 2 + begins) * p.tn + c) * kChannels);
+                    for (int c0 = odd * 8; c0 < rows; c0 += 16) {
+                        float s[8];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) s[c] = 0.0f;
+                        for (int b = b0; b <= b1; b += 4) {  // in the order of k, four parts' loads in flight
+                            float v[4][8];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int begins = work.first(b + i) <= t0;
+                                const float* f = from + ((static_cast<size_t>(b + i) * 2 + begins) * p.tn + c0) * kChannels;
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) v[i][c] = b + i <= b1 ? __ldcg(f + c * kChannels) : 0.0f;
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) s[c] += v[i][c];
                         }
-                        if (n < p.N) y[static_cast<size_t>(c) * p.N] = __float2bfloat16_rn(s * (sx[c] * sw));
+                        if (n < p.N)
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                if (c0 + c < rows) y[static_cast<size_t>(c0 + c) * p.N] = __float2bfloat16_rn(s[c] * (sx[c0 + c] * sw));
                     }
                 }
                 named_bar_sync(kEpiBar, kEpiWarps * 32);  // `last` is written again
