@@ -105,67 +105,101 @@ struct I8GemmArgs {
 };
 
 constexpr int kGemvWarps = 8;
-constexpr int kGemvRows = 4;  // channels of a CTA
-constexpr int kGemvTokens = 4;  // most tokens of a call that takes this form
+constexpr int kGemvRows = 16;   // channels of a CTA
+constexpr int kGemvTokens = 16; // most tokens of a call that takes this form
+constexpr int kGemvAhead = 3;   // 128-byte pieces of K that a warp has on their way
 
-// MR tokens times four channels a CTA, whose warps take 512-byte pieces of K in turn:
-// dp4a on 16-byte loads, sums exact in int32.  The weights come once from memory, the
-// tokens from L1.
-template <int MR>
-__global__ void __launch_bounds__(kGemvWarps * 32) i8_gemv_kernel(const I8GemmArgs p) {
-    __shared__ int red[kGemvWarps][kGemvRows * MR];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ int4 load_weights(const int8_t* p) {  // streamed: the tokens keep L1
+    int4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+// c += A B, A 16 channels x 32 k, B 32 k x 8 tokens: exact in int32.
+__device__ __forceinline__ void mma_s8(int (&c)[4], int a0, int a1, int a2, int a3, int b0, int b1) {
+    asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Up to 8 MT tokens times 16 channels a CTA, whose warps take 128-byte pieces of K in
+// turn.  A thread's 16-byte loads are its fragments as they are: the order of k within a
+// piece is the same for both operands, and no other order matters to an exact sum.  An
+// integer MMA takes 16 cycles of an SM here, 32 bytes of weights a cycle for 8 tokens,
+// where HBM brings 23.
+template <int MT>
+__global__ void __launch_bounds__(kGemvWarps * 32, 2) i8_gemv_kernel(const I8GemmArgs p) {
+    __shared__ int red[kGemvWarps][MT * 8][kGemvRows + 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+    const int n0 = blockIdx.x * kGemvRows, K = p.K;
+    const int8_t* w0 = p.w + static_cast<size_t>(min(n0 + g, p.N - 1)) * K;
+    const int8_t* w1 = p.w + static_cast<size_t>(min(n0 + g + 8, p.N - 1)) * K;
+    const int k0 = warp * 128 + q * 16;
+    // Nothing is read before what comes before has ended, but the first pieces may be on
+    // their way to L2 by then.
+#pragma unroll
+    for (int i = 0; i < kGemvAhead; ++i) {
+        const int k = k0 + i * kGemvWarps * 128;
+        if (k < K) {
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(w0 + k));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(w1 + k));
+        }
+    }
     grid_begin();
     bool ok;
     const int M = row_count(p.d_M, p.M_host, p.M_max, p.hdr, &ok);
-    const int m0 = blockIdx.y * MR, n0 = blockIdx.x * kGemvRows;
-    if (m0 >= M) return;
-    const int K = p.K;
-    int acc[kGemvRows][MR];
+    if (M < 1) return;
+    const int8_t* x[MT];
 #pragma unroll
-    for (int r = 0; r < kGemvRows; ++r)
+    for (int m = 0; m < MT; ++m) x[m] = p.x + static_cast<size_t>(min(m * 8 + g, M - 1)) * K;
+    int acc[MT][4];
 #pragma unroll
-        for (int m = 0; m < MR; ++m) acc[r][m] = 0;
-    const int8_t* w[kGemvRows];
-    const int8_t* x[MR];
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int r = 0; r < kGemvRows; ++r) w[r] = p.w + static_cast<size_t>(min(n0 + r, p.N - 1)) * K;
+        for (int i = 0; i < 4; ++i) acc[m][i] = 0;
+    const int4 zero = make_int4(0, 0, 0, 0);
+    int4 wv[kGemvAhead][4];  // rows g and g + 8, bytes k and k + 64
+    auto fetch = [&](int4 (&v)[4], int k) {
+        v[0] = k < K ? load_weights(w0 + k) : zero;
+        v[1] = k < K ? load_weights(w1 + k) : zero;
+        v[2] = k + 64 < K ? load_weights(w0 + k + 64) : zero;
+        v[3] = k + 64 < K ? load_weights(w1 + k + 64) : zero;
+    };
 #pragma unroll
-    for (int m = 0; m < MR; ++m) x[m] = p.x + static_cast<size_t>(min(m0 + m, M - 1)) * K;
-#pragma unroll 2
-    for (int c = (warp * 32 + lane) * 16; c < K; c += kGemvWarps * 512) {
-        int4 wv[kGemvRows], xv[MR];
+    for (int i = 0; i < kGemvAhead; ++i) fetch(wv[i], k0 + i * kGemvWarps * 128);
+    for (int kk = k0; kk - q * 16 < K; kk += kGemvAhead * kGemvWarps * 128) {
 #pragma unroll
-        for (int r = 0; r < kGemvRows; ++r) wv[r] = __ldcs(reinterpret_cast<const int4*>(w[r] + c));
+        for (int i = 0; i < kGemvAhead; ++i) {
+            const int k = kk + i * kGemvWarps * 128;
+            if (k - q * 16 >= K) break;
+            int4 xv[MT][2];
 #pragma unroll
-        for (int m = 0; m < MR; ++m) xv[m] = *reinterpret_cast<const int4*>(x[m] + c);
-#pragma unroll
-        for (int r = 0; r < kGemvRows; ++r)
-#pragma unroll
-            for (int m = 0; m < MR; ++m) {
-                int a = acc[r][m];
-                a = __dp4a(wv[r].x, xv[m].x, a);
-                a = __dp4a(wv[r].y, xv[m].y, a);
-                a = __dp4a(wv[r].z, xv[m].z, a);
-                acc[r][m] = __dp4a(wv[r].w, xv[m].w, a);
+            for (int m = 0; m < MT; ++m) {
+                xv[m][0] = k < K ? *reinterpret_cast<const int4*>(x[m] + k) : zero;
+                xv[m][1] = k + 64 < K ? *reinterpret_cast<const int4*>(x[m] + k + 64) : zero;
             }
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    mma_s8(acc[m], wv[i][2 * h].x, wv[i][2 * h + 1].x, wv[i][2 * h].y, wv[i][2 * h + 1].y, xv[m][h].x, xv[m][h].y);
+                    mma_s8(acc[m], wv[i][2 * h].z, wv[i][2 * h + 1].z, wv[i][2 * h].w, wv[i][2 * h + 1].w, xv[m][h].z, xv[m][h].w);
+                }
+            fetch(wv[i], k + kGemvAhead * kGemvWarps * 128);
+        }
     }
 #pragma unroll
-    for (int r = 0; r < kGemvRows; ++r)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int m = 0; m < MR; ++m) {
-            const int s = __reduce_add_sync(0xffffffffu, acc[r][m]);
-            if (lane == 0) red[warp][m * kGemvRows + r] = s;
-        }
+        for (int i = 0; i < 4; ++i) red[warp][m * 8 + 2 * q + (i & 1)][g + (i >> 1) * 8] = acc[m][i];
     __syncthreads();
-    const int o = threadIdx.x;
-    if (o < kGemvRows * MR) {
+    for (int o = threadIdx.x; o < MT * 8 * kGemvRows; o += kGemvWarps * 32) {
+        const int m = o / kGemvRows, r = o % kGemvRows;
         int s = 0;
 #pragma unroll
-        for (int v = 0; v < kGemvWarps; ++v) s += red[v][o];
-        const int m = m0 + o / kGemvRows, n = n0 + o % kGemvRows;
-        if (m < M && n < p.N)
-            p.y[static_cast<size_t>(m) * p.N + n] = __float2bfloat16_rn(static_cast<float>(s) * (p.sx[m] * p.sw[n]));
+        for (int v = 0; v < kGemvWarps; ++v) s += red[v][m][r];
+        if (m < M && n0 + r < p.N)
+            p.y[static_cast<size_t>(m) * p.N + n0 + r] = __float2bfloat16_rn(static_cast<float>(s) * (p.sx[m] * p.sw[n0 + r]));
     }
 }
 
@@ -181,7 +215,7 @@ int i8_check_rows(int M, const int32_t* d_M, int M_max) {
     return ET_OK;
 }
 
-// How a product of M rows runs, and what it needs of the workspace.
+// How a pass of M rows runs on the tensor cores, and what it needs of the workspace.
 struct I8Plan {
     bool pair;
     int tn, mt, nt, kblocks, grid, share;
@@ -192,8 +226,6 @@ int ceil_div_l(long long a, long long b) { return static_cast<int>((a + b - 1) /
 
 I8Plan i8_plan(int M, int N, int K) {
     I8Plan p{};
-    p.total = kHeaderBytes;
-    if (M <= kGemvTokens) return p;
     p.kblocks = ceil_div_l(K, kI8KBlock);
     p.mt = ceil_div_l(M, kI8TokensMax);
     p.pair = static_cast<long long>(p.mt) * ceil_div_l(N, 256) >= kI8Sms / 2;
@@ -222,7 +254,9 @@ I8Plan i8_plan(int M, int N, int K) {
 // and the workspace of a long batch stays small.
 constexpr int kI8RowsPass = 8192;
 
-size_t i8_ws_bytes(int M_max, int N, int K) { return i8_plan(M_max < kI8RowsPass ? M_max : kI8RowsPass, N, K).total; }
+size_t i8_ws_bytes(int M_max, int N, int K) {
+    return M_max <= kGemvTokens ? kHeaderBytes : i8_plan(M_max < kI8RowsPass ? M_max : kI8RowsPass, N, K).total;
+}
 
 template <bool VEC>
 cudaError_t launch_i8_quantize(I8QuantArgs a, int rows, int sms, void* stream) {
@@ -300,7 +334,7 @@ int et_i8_gemm(const void* x_q, const float* s_x, const void* w_q, const float* 
         bf16* y = static_cast<bf16*>(Y);
         if (all <= kGemvTokens) {
             const I8GemmArgs a{x, s_x, static_cast<const int8_t*>(w_q), s_w, y, d_M, M, all, N, K, hdr};
-            auto kernel = all == 1 ? i8_gemv_kernel<1> : all == 2 ? i8_gemv_kernel<2> : i8_gemv_kernel<4>;
+            auto kernel = all <= 8 ? i8_gemv_kernel<1> : i8_gemv_kernel<2>;
             const cudaError_t e = api_launch(kernel, dim3((N + kGemvRows - 1) / kGemvRows), kGemvWarps * 32, 0, stream, a);
             if (e != cudaSuccess) return api_fail_cuda(e, "launch of the int8 product");
             return ET_OK;
