@@ -22,19 +22,18 @@ struct I8Rows {
 };
 
 struct I8TcArgs {
+    const int8_t* x;     // [M, K] (a pair takes its tokens from the map of their fp16 form)
     const float* sx;     // [M]
     const float* sw;     // [N]
     bf16* y;             // [M, N]
     I8Rows rows;
-    int N;
+    int N, K;
     EtHeader* hdr;
-    int32_t* tile_count; // [tiles]: parts of a shared tile that are stored (zeroed by the call's first kernel)
-    float* part;         // [grid][2][tn][channels]: parts of shared tiles
     int tn;              // tokens of a tile
     int nt;              // tiles over N
     int kblocks;
-    int grid;            // CTAs (pairs) that share the work
-    int share;           // tiles are cut anywhere along K so that all have the same work
+    int grid;            // CTAs, pairs or clusters that take tiles in turn (a cluster: one)
+    int split;           // CTAs of a cluster that share a tile (1: none)
     int stages_w, stages_x;
     uint64_t timeout_ns;
 };
@@ -45,8 +44,6 @@ struct I8ExpandArgs {
     I8Rows rows;
     int K;
     EtHeader* hdr;
-    int32_t* tile_count;
-    int tiles;           // counters to zero
 };
 
 // `pair`: CTA pairs of 256 channels.  i8_tc_stages: stages of either ring; returns the bytes of

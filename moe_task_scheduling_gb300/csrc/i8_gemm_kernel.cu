@@ -2,28 +2,28 @@
 //
 // GB300's integer tensor rate is far below its 16-bit rate, but every int8 value is
 // an fp16 value and a product of two of them is exact in fp32: the products run as
-// tcgen05 kind::f16 with fp32 sums, exact while those stay within 2^24.  The tokens
-// are written as fp16 once a call (i8_expand_kernel; they are few or the product is
-// long).  The weights, which are the traffic of a small batch, stay int8 up to the SM:
-// converter warps turn each 128 x 128 block into fp16 in TMEM, where the MMA takes its
-// A operand from, so that shared memory carries a weight once, as one byte.
+// tcgen05 kind::f16 with fp32 sums, exact while those stay within 2^24.  The weights,
+// which are the traffic of a small batch, stay int8 up to the SM: converter warps turn
+// each block of 128 channels x 128 k into fp16 in TMEM, where the MMA takes its A operand
+// from, so that shared memory carries a weight once, as one byte.
 //
 // Roles (608 threads):
 //   warp 0        weights: TMA, int8 blocks of 128 channels x 128 k
-//   warp 1        one thread issues tcgen05.mma, D[channel, token] += W X^T
-//   warps 2..9    converters: shared memory -> registers -> fp16 -> TMEM; a thread has
-//                 half a row
-//   warps 10..17  epilogue: TMEM -> scales -> bf16, or a part's sums to the workspace; four
-//                 take the even 16-token chunks, four the odd ones
-//   warp 18       tokens: TMA, fp16 blocks of tn tokens x 128 k
-// With CG = 2 a pair of CTAs takes 256 channels: each loads and converts its own 128,
-// loads half the tokens, and the pair's MMA reads both halves, which halves the
-// traffic of the tokens into shared memory.
+//   warp 1        one elected thread issues tcgen05.mma, D[channel, token] += W X^T
+//   warps 2..9    converters: shared memory -> registers -> fp16 -> TMEM, a thread a row;
+//                 four warps take the even blocks, four the odd ones
+//   warps 10..17  tokens of one CTA's tile: int8 from memory -> fp16 in shared memory;
+//                 and the epilogue: TMEM -> scales -> bf16
+//   warp 18       tokens of a pair: TMA, fp16 blocks
+// A pair of CTAs (CG = 2) takes 256 channels: each loads and converts its own 128 and
+// loads half the tokens, and the pair's MMA reads both halves, which halves the traffic of
+// the tokens into shared memory.  Its tokens come as fp16, written once a call by
+// i8_expand_kernel: with a batch that long they are read by many pairs.
 //
-// Work: tiles of 128 CG channels x tn tokens.  With many tiles a CTA takes whole ones in
-// turn; with few (share) the k-blocks of all tiles are one list, cut into even ranges,
-// and a tile that several CTAs have a part of is summed in the order of k by the one
-// that stores its part last: the same bits on every run.  Every wait is bounded.
+// Work: tiles of 128 CG channels x tn tokens, whole ones in turn.  Where tiles are few a
+// cluster of `split` CTAs takes one, each its share of k; their sums meet in shared
+// memory over the cluster and are added in the order of k: the same bits on every run.
+// Every wait is bounded.
 #include <cuda_fp16.h>
 
 #include "et_device.cuh"
@@ -39,6 +39,7 @@ constexpr int kAStages = 4;          // TMEM blocks of converted weights, 64 col
 constexpr int kACol = 256;           // the accumulators are columns 0 .. 255
 constexpr int kWBytes = 128 * kI8KBlock;
 constexpr int kEpiBar = 1;           // named barrier of the epilogue warps
+constexpr int kEpiThreads = kEpiWarps * 32;
 
 struct I8Ctl {
     uint64_t full_w[kI8MaxStages], empty_w[kI8MaxStages];
@@ -47,8 +48,7 @@ struct I8Ctl {
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drain;
     uint32_t tmem_base;
-    int32_t go[2];                   // the epilogue's: the accumulator is complete (0: an abort),
-    int32_t last;                    // this part was the tile's last
+    int32_t go[2];                   // the epilogue's: the accumulator is complete (0: an abort)
     alignas(16) float sx[2][kI8TokensMax];
 };
 
@@ -164,6 +164,9 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+__device__ __forceinline__ void sts_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Four int8 of a word as two pairs of fp16, exact: with the sign bits turned over a byte is
@@ -204,67 +207,98 @@ __device__ __forceinline__ int pass_rows(const I8Rows& r, EtHeader* hdr) {
     return max(0, min(r.count, M - r.first));
 }
 
-// A CTA's (pair's) next piece: k-blocks [kb0, kb1) of a tile.
-struct Piece {
-    int tile, kb0, kb1;
-};
-
+// A CTA's (pair's) pieces: k-blocks [kb0, kb1) of a tile.
 struct Work {
-    long long total, at, end;  // share: of the list of all tiles' k-blocks
-    int grid;                  // CTAs that have some of it (the device's M may leave less than one each)
-    int tile, tiles, step;
-    int kblocks, share;
+    int tile, kb0, kb1;
+    int at, tiles, step;
 
-    // The list's first k-block of CTA b.
-    __device__ __forceinline__ long long first(int b) const { return total * b / grid; }
-    // The CTA that has k-block x of the list.
-    __device__ __forceinline__ int owner(long long x) const { return static_cast<int>(((x + 1) * grid - 1) / total); }
-    __device__ __forceinline__ Work(const I8TcArgs& p, int tiles_, int b) : tiles(tiles_), kblocks(p.kblocks), share(p.share) {
-        total = static_cast<long long>(tiles) * kblocks;
-        grid = total < p.grid ? static_cast<int>(total) : p.grid;
-        at = b < grid ? first(b) : 0;
-        end = b < grid ? first(b + 1) : 0;
-        tile = b;
-        step = p.grid;
+    __device__ __forceinline__ Work(const I8TcArgs& p, int tiles_, int cta) : tiles(tiles_) {
+        const int part = cta % p.split;
+        at = cta / p.split;
+        step = p.split > 1 ? tiles_ : p.grid;  // a cluster has one tile
+        kb0 = p.kblocks * part / p.split;
+        kb1 = p.kblocks * (part + 1) / p.split;
     }
-    __device__ __forceinline__ bool next(Piece& w) {
-        if (share) {
-            if (at >= end) return false;
-            w.tile = static_cast<int>(at / kblocks);
-            w.kb0 = static_cast<int>(at - static_cast<long long>(w.tile) * kblocks);
-            const long long n = end - at;
-            w.kb1 = n < kblocks - w.kb0 ? w.kb0 + static_cast<int>(n) : kblocks;
-            at += w.kb1 - w.kb0;
-            return true;
-        }
-        if (tile >= tiles) return false;
-        w = {tile, 0, kblocks};
-        tile += step;
+    __device__ __forceinline__ bool next() {
+        if (at >= tiles) return false;
+        tile = at;
+        at += step;
         return true;
     }
 };
+
+// The tokens of a tile's k-blocks, by the 256 threads of the epilogue: int8 from memory (a
+// row of 128 bytes by eight neighbouring threads), as fp16 into the swizzled blocks of 64 k
+// that the MMA reads.  C: 16-byte chunks of a thread in a block; AHEAD: blocks that are on
+// their way from L2 in registers, which takes longer than the MMAs of a block of few tokens.
+template <int C, int AHEAD>
+__device__ __forceinline__ bool load_tokens(const I8TcArgs& p, I8Ctl* ctl, uint8_t* ring, const WaitCtx& wc, int m0, int rows,
+                                            int kb0, int kb1, int et, int lane, uint32_t& s, uint32_t& phase) {
+    const int chunk = et & 7, row0 = et >> 3, xbytes = p.tn * 256;
+    const int8_t* x = p.x + static_cast<size_t>(m0) * p.K + chunk * 16;
+    uint4 v[AHEAD][C];
+    auto fetch = [&](uint4 (&to)[C], int kb) {
+        const int k = kb * kI8KBlock;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int r = row0 + i * (kEpiThreads / 8);
+            to[i] = make_uint4(0, 0, 0, 0);
+            if (kb < kb1 && r < rows && k + chunk * 16 < p.K) to[i] = *reinterpret_cast<const uint4*>(x + static_cast<size_t>(r) * p.K + k);
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) fetch(v[j], kb0 + j);
+    for (int kb = kb0; kb < kb1; kb += AHEAD) {
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            if (kb + j >= kb1) break;
+            const bool ok = wait(wc, &ctl->empty_x[s], phase ^ 1u, kWhereEmpty);
+            if (!__all_sync(0xffffffffu, ok)) return false;
+            const uint32_t dst = smem_u32(ring + s * xbytes) + (chunk >> 2) * p.tn * 128;
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int r = row0 + i * (kEpiThreads / 8);
+                if (r < p.tn) {
+                    uint32_t h[8];
+                    int8_to_half(v[j][i].x, h[0], h[1]);
+                    int8_to_half(v[j][i].y, h[2], h[3]);
+                    int8_to_half(v[j][i].z, h[4], h[5]);
+                    int8_to_half(v[j][i].w, h[6], h[7]);
+                    const uint32_t at = dst + r * 128, c = (chunk & 3) * 2;
+                    sts_v4(at + ((c ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+                    sts_v4(at + (((c + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
+                }
+            }
+            fetch(v[j], kb + j + AHEAD);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->full_x[s]);
+            if (++s == static_cast<uint32_t>(p.stages_x)) { s = 0; phase ^= 1u; }
+        }
+    }
+    return true;
+}
 
 template <int CG>
 __global__ void __launch_bounds__(kI8Threads, 1)
 i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ I8TcArgs p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const int xrows = p.tn / CG, xbytes = xrows * 256;  // a stage of tokens: two boxes of 64 k
+    const int xrows = p.tn / CG, xbytes = xrows * 256;  // a stage of tokens: two blocks of 64 k
     uint8_t* ring_w = base;
     uint8_t* ring_x = base + p.stages_w * kWBytes;
     I8Ctl* ctl = reinterpret_cast<I8Ctl*>(ring_x + p.stages_x * xbytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 ? cluster_rank() : 0;
-    const int cta = blockIdx.x / CG;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kI8MaxStages; ++i) {
             mbar_init(&ctl->full_w[i], 1);
-            mbar_init(&ctl->empty_w[i], kConvWarps);
-            mbar_init(&ctl->full_x[i], 1);
+            mbar_init(&ctl->empty_w[i], kConvWarps / 2);
+            mbar_init(&ctl->full_x[i], CG == 1 ? kEpiWarps : 1);
             mbar_init(&ctl->empty_x[i], 1);
         }
         for (int i = 0; i < kAStages; ++i) {
-            mbar_init(&ctl->full_a[i], kConvWarps * CG);
+            mbar_init(&ctl->full_a[i], kConvWarps / 2 * CG);
             mbar_init(&ctl->empty_a[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -274,7 +308,7 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
         mbar_init(&ctl->drain, 1);
         fence_mbar_init();
         tma_prefetch_map(&tm_w);
-        tma_prefetch_map(&tm_x);
+        if (CG == 2) tma_prefetch_map(&tm_x);
     }
     if (warp == 1) tmem_take<CG>(&ctl->tmem_base);
     tc_fence_before();
@@ -289,50 +323,60 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
     const int M = pass_rows(p.rows, p.hdr);
     const int mt = ceil_div(M, p.tn), tiles = mt * p.nt;  // tile = n tile * mt + m tile
     const int slots = p.tn > 128 ? 1 : 2;                 // accumulators
-    uint32_t posted_w = 0, posted_x = 0;
-    Work work(p, tiles, cta);
-    Piece w;
+    Work w(p, tiles, blockIdx.x / CG);
 
     if (warp == 0) {
         if (lane == 0) {
-            // May start before what comes before this kernel ends: that is the call's own
-            // first kernel, which lets this one start only when all before it has ended.
             const uint64_t pol = policy_evict_first();
+            if (CG == 1) {
+                // Nothing is read before what comes before this kernel has ended, but the first
+                // blocks may be on their way to L2 by then.
+                Work f = w;
+                if (f.next())
+                    for (int kb = f.kb0; kb < f.kb1 && kb < f.kb0 + p.stages_w; ++kb)
+                        tma_prefetch_l2(&tm_w, kb * kI8KBlock, (f.tile / mt) * 128);
+                grid_wait();
+                fence_proxy_async_global();
+            }
+            // (A pair's kernel comes behind the call's own first kernel, which lets it start only
+            // when all before that one has ended: its weights need no wait.)
+            uint32_t s = 0, phase = 0, posted = 0;
             bool ok = true;
-            while (ok && work.next(w)) {
+            while (ok && w.next()) {
                 const int n0 = (w.tile / mt) * 128 * CG + static_cast<int>(rank) * 128;
                 for (int kb = w.kb0; kb < w.kb1; ++kb) {
-                    const uint32_t s = posted_w % p.stages_w;
-                    if (!(ok = wait(wc, &ctl->empty_w[s], ((posted_w / p.stages_w) & 1u) ^ 1u, kWhereEmpty))) break;
+                    if (!(ok = wait(wc, &ctl->empty_w[s], phase ^ 1u, kWhereEmpty))) break;
                     mbar_arrive_expect_tx(&ctl->full_w[s], kWBytes);
                     tma_load_2d(ring_w + s * kWBytes, &tm_w, &ctl->full_w[s], kb * kI8KBlock, n0, pol);
-                    ++posted_w;
+                    ++posted;
+                    if (++s == static_cast<uint32_t>(p.stages_w)) { s = 0; phase ^= 1u; }
                 }
             }
             if (!ok)  // unwinding: let the copies land
-                for (uint32_t i = posted_w > static_cast<uint32_t>(p.stages_w) ? posted_w - p.stages_w : 0; i < posted_w; ++i)
+                for (uint32_t i = posted > static_cast<uint32_t>(p.stages_w) ? posted - p.stages_w : 0; i < posted; ++i)
                     mbar_drain(&ctl->full_w[i % p.stages_w], (i / p.stages_w) & 1u, 1000000ull);
         }
         __syncwarp();
     } else if (warp == kTokenWarp) {
-        if (lane == 0) {
+        if (CG == 2 && lane == 0) {
             grid_wait();
             fence_proxy_async_global();  // the first kernel's stores, read by TMA
+            uint32_t s = 0, phase = 0, posted = 0;
             bool ok = true;
-            while (ok && work.next(w)) {
+            while (ok && w.next()) {
                 const int m0 = (w.tile % mt) * p.tn + static_cast<int>(rank) * xrows;
                 for (int kb = w.kb0; kb < w.kb1; ++kb) {
-                    const uint32_t s = posted_x % p.stages_x;
-                    if (!(ok = wait(wc, &ctl->empty_x[s], ((posted_x / p.stages_x) & 1u) ^ 1u, kWhereEmpty))) break;
+                    if (!(ok = wait(wc, &ctl->empty_x[s], phase ^ 1u, kWhereEmpty))) break;
                     if (rank == 0) mbar_arrive_expect_tx(&ctl->full_x[s], xbytes * CG);
                     const uint32_t bar = leader_addr<CG>(&ctl->full_x[s]), dst = smem_u32(ring_x + s * xbytes);
                     tma_tokens<CG>(dst, &tm_x, bar, kb * kI8KBlock, m0);
                     tma_tokens<CG>(dst + xrows * 128, &tm_x, bar, kb * kI8KBlock + 64, m0);
-                    ++posted_x;
+                    ++posted;
+                    if (++s == static_cast<uint32_t>(p.stages_x)) { s = 0; phase ^= 1u; }
                 }
             }
             if (!ok && rank == 0)
-                for (uint32_t i = posted_x > static_cast<uint32_t>(p.stages_x) ? posted_x - p.stages_x : 0; i < posted_x; ++i)
+                for (uint32_t i = posted > static_cast<uint32_t>(p.stages_x) ? posted - p.stages_x : 0; i < posted; ++i)
                     mbar_drain(&ctl->full_x[i % p.stages_x], (i / p.stages_x) & 1u, 1000000ull);
         }
         __syncwarp();
@@ -345,7 +389,7 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
             const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(p.tn >> 3) << 17) | (static_cast<uint32_t>(128 * CG >> 4) << 24);
             uint32_t acc = 0, kx = 0, px = 0, ka = 0, pa = 0;  // ring places and their phases
             bool ok = true;
-            while (ok && work.next(w)) {
+            while (ok && w.next()) {
                 const uint32_t slot = slots == 1 ? 0 : acc & 1, turn = slots == 1 ? acc : acc >> 1;
                 ok = wait(wc, &ctl->acc_empty[slot], (turn & 1u) ^ 1u, kWhereAcc);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -377,72 +421,85 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
         }
         __syncwarp();
     } else if (warp < kEpiWarpI8) {
-        const int q = warp & 3, half = (warp - kConvWarp0) >> 2, r = q * 32 + lane;
+        const int q = warp & 3, group = (warp - kConvWarp0) >> 2, r = q * 32 + lane;
         const uint32_t row = static_cast<uint32_t>(r) * 128, x7 = r & 7;
-        const uint32_t a0 = tmem + kACol + half * 32 + (static_cast<uint32_t>(q * 32) << 16);
-        uint32_t it = 0;
+        const uint32_t a0 = tmem + kACol + (static_cast<uint32_t>(q * 32) << 16);
+        uint32_t it = 0, s = 0, phase = 0;
         bool ok = true;
-        while (ok && work.next(w)) {
+        while (ok && w.next()) {
             for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-                const uint32_t sw = it % p.stages_w, sa = it % kAStages;
-                ok = wait(wc, &ctl->full_w[sw], (it / p.stages_w) & 1u, kWhereFull);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                const uint32_t src = smem_u32(ring_w + sw * kWBytes) + row;
-                uint4 v[4];
+                if ((it & 1u) == static_cast<uint32_t>(group)) {
+                    const uint32_t sa = it % kAStages;
+                    ok = wait(wc, &ctl->full_w[s], phase, kWhereFull);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    const uint32_t src = smem_u32(ring_w + s * kWBytes) + row;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) v[c] = lds_v4(src + (((half * 4 + c) ^ x7) << 4));
-                uint32_t h[32];
+                    for (int half = 0; half < 2; ++half) {
+                        uint4 v[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    int8_to_half(v[c].x, h[c * 8 + 0], h[c * 8 + 1]);
-                    int8_to_half(v[c].y, h[c * 8 + 2], h[c * 8 + 3]);
-                    int8_to_half(v[c].z, h[c * 8 + 4], h[c * 8 + 5]);
-                    int8_to_half(v[c].w, h[c * 8 + 6], h[c * 8 + 7]);
+                        for (int c = 0; c < 4; ++c) v[c] = lds_v4(src + (((half * 4 + c) ^ x7) << 4));
+                        uint32_t h[32];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            int8_to_half(v[c].x, h[c * 8 + 0], h[c * 8 + 1]);
+                            int8_to_half(v[c].y, h[c * 8 + 2], h[c * 8 + 3]);
+                            int8_to_half(v[c].z, h[c * 8 + 4], h[c * 8 + 5]);
+                            int8_to_half(v[c].w, h[c * 8 + 6], h[c * 8 + 7]);
+                        }
+                        if (!half) {
+                            ok = wait(wc, &ctl->empty_a[sa], ((it / kAStages) & 1u) ^ 1u, kWhereEmpty);
+                            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                            tc_fence_after();
+                        }
+                        tmem_st32(a0 + sa * 64 + half * 32, h);
+                    }
+                    if (!ok) break;
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    // Both only now.  An arrival on empty_w right after the loads came before them: they
+                    // queue behind the first store to TMEM, and the next block was in their place.
+                    if (lane == 0) {
+                        mbar_arrive(&ctl->empty_w[s]);
+                        arrive_leader<CG>(&ctl->full_a[sa]);
+                    }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->empty_w[sw]);
-                ok = wait(wc, &ctl->empty_a[sa], ((it / kAStages) & 1u) ^ 1u, kWhereEmpty);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                tc_fence_after();
-                tmem_st32(a0 + sa * 64, h);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_leader<CG>(&ctl->full_a[sa]);
+                if (++s == static_cast<uint32_t>(p.stages_w)) { s = 0; phase ^= 1u; }
             }
         }
     } else {
         const int q = warp & 3, odd = (warp - kEpiWarpI8) >> 2, et = threadIdx.x - kEpiWarpI8 * 32, row = q * 32 + lane;
-        constexpr int kChannels = 128 * CG;
         grid_wait();
-        uint32_t acc = 0;
+        uint32_t acc = 0, s = 0, phase = 0;
         bool ok = true;
-        while (ok && work.next(w)) {
-            const uint32_t slot = acc % slots;
-            const int m0 = (w.tile % mt) * p.tn, n = (w.tile / mt) * kChannels + static_cast<int>(rank) * 128 + row;
+        while (ok && w.next()) {
+            const uint32_t slot = slots == 1 ? 0 : acc & 1, turn = slots == 1 ? acc : acc >> 1;
+            const int m0 = (w.tile % mt) * p.tn, n = (w.tile / mt) * 128 * CG + static_cast<int>(rank) * 128 + row;
             const int rows = min(p.tn, M - m0);
             float* sx = ctl->sx[acc & 1];
-            for (int m = et; m < rows; m += kEpiWarps * 32) sx[m] = p.sx[m0 + m];
+            for (int m = et; m < rows; m += kEpiThreads) sx[m] = p.sx[m0 + m];
             const float sw = n < p.N ? p.sw[n] : 0.0f;
-            // one thread waits for all four warps: a named barrier is not bounded, so they must
-            // never part
-            if (et == 0) ctl->go[acc & 1] = wait(wc, &ctl->acc_full[slot], (acc / slots) & 1u, kWhereAcc);
-            named_bar_sync(kEpiBar, kEpiWarps * 32);
+            if (CG == 1) {
+                if (p.tn <= 32) ok = load_tokens<1, 6>(p, ctl, ring_x, wc, m0, rows, w.kb0, w.kb1, et, lane, s, phase);
+                else if (p.tn <= 64) ok = load_tokens<2, 4>(p, ctl, ring_x, wc, m0, rows, w.kb0, w.kb1, et, lane, s, phase);
+                else if (p.tn <= 128) ok = load_tokens<4, 2>(p, ctl, ring_x, wc, m0, rows, w.kb0, w.kb1, et, lane, s, phase);
+                else ok = load_tokens<8, 1>(p, ctl, ring_x, wc, m0, rows, w.kb0, w.kb1, et, lane, s, phase);
+            }
+            // One thread waits for all eight warps: a named barrier is not bounded, so they must
+            // never part.
+            if (et == 0) ctl->go[acc & 1] = wait(wc, &ctl->acc_full[slot], turn & 1u, kWhereAcc);
+            named_bar_sync(kEpiBar, kEpiThreads);
             if (!(ok = ctl->go[acc & 1] != 0)) break;
             tc_fence_after();
-            const bool part = w.kb1 - w.kb0 != p.kblocks;
-            // a part that begins its tile, or the CTA's range: one of each at most
-            float* mine = p.part + ((static_cast<size_t>(cta) * 2 + (w.kb0 == 0)) * p.tn) * kChannels + rank * 128 + row;
+            ++acc;
+            if (p.split > 1) break;  // the cluster's sums come first
             bf16* y = p.y + static_cast<size_t>(m0) * p.N + n;
             const uint32_t d = tmem + slot * 128 + (static_cast<uint32_t>(q * 32) << 16);
             for (int c0 = odd * 16; c0 < rows; c0 += 32) {
                 float v[16];
                 tmem_ld16(d + c0, v);
                 tmem_ld_wait();
-                const int left = rows - c0;
-                if (part) {
-                    store16(mine + static_cast<size_t>(c0) * kChannels, kChannels, v, left);
-                } else if (n < p.N) {
+                if (n < p.N) {
                     bf16 o[16];
 #pragma unroll
                     for (int c = 0; c < 16; c += 4) {
@@ -452,64 +509,66 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
                         o[c + 2] = __float2bfloat16_rn(v[c + 2] * (f.z * sw));
                         o[c + 3] = __float2bfloat16_rn(v[c + 3] * (f.w * sw));
                     }
-                    store16(y + static_cast<size_t>(c0) * p.N, p.N, o, left);
+                    store16(y + static_cast<size_t>(c0) * p.N, p.N, o, rows - c0);
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_leader<CG>(&ctl->acc_empty[slot]);
-            ++acc;
-            if (part) {
-                const long long t0 = static_cast<long long>(w.tile) * p.kblocks;
-                const int b0 = work.owner(t0), b1 = work.owner(t0 + p.kblocks - 1);
-                // both CTAs of a pair count their own half of the channels
-                int* count = p.tile_count + w.tile * CG + rank;
-                named_bar_sync(kEpiBar, kEpiWarps * 32);
-                if (et == 0) {
-                    __threadfence();
-                    ctl->last = atom_acq_rel_add(count, 1) == b1 - b0;
-                }
-                named_bar_sync(kEpiBar, kEpiWarps * 32);
-                if (ctl->last) {
-                    __threadfence();
-                    const float* from = p.part + rank * 128 + row;
-                    for (int c0 = odd * 8; c0 < rows; c0 += 16) {
-                        float s[8];
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) s[c] = 0.0f;
-                        for (int b = b0; b <= b1; b += 4) {  // in the order of k, four parts' loads in flight
-                            float v[4][8];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int begins = work.first(b + i) <= t0;
-                                const float* f = from + ((static_cast<size_t>(b + i) * 2 + begins) * p.tn + c0) * kChannels;
-#pragma unroll
-                                for (int c = 0; c < 8; ++c) v[i][c] = b + i <= b1 ? __ldcg(f + c * kChannels) : 0.0f;
-                            }
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                                for (int c = 0; c < 8; ++c) s[c] += v[i][c];
-                        }
-                        if (n < p.N)
-#pragma unroll
-                            for (int c = 0; c < 8; ++c)
-                                if (c0 + c < rows) y[static_cast<size_t>(c0 + c) * p.N] = __float2bfloat16_rn(s[c] * (sx[c0 + c] * sw));
-                    }
-                }
-                named_bar_sync(kEpiBar, kEpiWarps * 32);  // `last` is written again
-            }
         }
     }
 
     __syncthreads();
-    // the pair's commits have arrived here, and no CTA goes while the other may still reach into it
-    if (threadIdx.x == 32 && (CG == 2 || rank == 0)) (void)mbar_drain(&ctl->drain, 0, 2000000ull);
+    // the commits have arrived here, and no CTA goes while the pair's other may reach into it
+    if (threadIdx.x == 32) (void)mbar_drain(&ctl->drain, 0, 2000000ull);
     tc_fence_before();
     __syncthreads();
     if (CG == 2) cluster_sync();
     tc_fence_after();
+    if (CG == 1 && p.split > 1) {
+        // CTA r of the cluster sums tokens [r tn / split, (r + 1) tn / split) of the tile; what
+        // the others have of them comes into its rings, which nothing uses any more.
+        cluster_sync();
+        const int tile = blockIdx.x / p.split, mine = cluster_rank(), each = p.tn / p.split;
+        const bool have = tile < tiles && !aborted(wc);
+        if (have && warp < 16) {
+            const uint32_t row = (warp & 3) * 32 + lane;
+            const uint32_t to = smem_u32(base) + (static_cast<uint32_t>(mine) * each * 128 + row) * 4;
+            for (int c0 = (warp >> 2) * 16; c0 < p.tn; c0 += 64) {
+                float v[16];
+                tmem_ld16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    const int at = (c0 + c) / each;
+                    uint32_t dst;
+                    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(to + (c0 + c - at * each) * 512), "r"(at));
+                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(v[c]) : "memory");
+                }
+            }
+        }
+        tc_fence_before();
+        cluster_sync();
+        tc_fence_after();
+        if (have) {
+            const int m0 = (tile % mt) * p.tn, n0 = (tile / mt) * 128, rows = min(p.tn, M - m0);
+            const float* part = reinterpret_cast<const float*>(base);
+            for (int o = threadIdx.x; o < each * 128; o += kI8Threads) {
+                const int c = mine * each + o / 128, n = n0 + o % 128;
+                if (c >= rows || n >= p.N) continue;
+                float sum = 0.0f;
+#pragma unroll 4
+                for (int b = 0; b < p.split; ++b) sum += part[b * each * 128 + o];  // in the order of k
+                p.y[static_cast<size_t>(m0 + c) * p.N + n] = __float2bfloat16_rn(sum * (ctl->sx[0][c] * p.sw[n]));
+            }
+        }
+    }
     if (warp == 1) tmem_free<CG>(tmem);
+    // the last CTA out takes an abort back, so that the next call waits for its own events
+    if (threadIdx.x == 0 && atomicAdd(&p.hdr->exit_count, 1) == static_cast<int>(gridDim.x) - 1) {
+        p.hdr->exit_count = 0;
+        p.hdr->abort = 0;
+    }
 }
 
 __global__ void __launch_bounds__(256) i8_expand_kernel(const I8ExpandArgs p) {
@@ -518,10 +577,7 @@ __global__ void __launch_bounds__(256) i8_expand_kernel(const I8ExpandArgs p) {
     grid_wait();
     grid_release();
     const int at = blockIdx.x * blockDim.x + threadIdx.x, step = gridDim.x * blockDim.x;
-    for (int i = at; i < p.tiles; i += step) p.tile_count[i] = 0;
-    if (at == 0) p.hdr->abort = 0;
-    const int M = pass_rows(p.rows, p.hdr);
-    const long long n = static_cast<long long>(M) * p.K / 16;
+    const long long n = static_cast<long long>(pass_rows(p.rows, p.hdr)) * p.K / 16;
     const uint4* x = reinterpret_cast<const uint4*>(p.x);
     uint4* out = static_cast<uint4*>(p.x16);
     for (long long i = at; i < n; i += step) {
@@ -541,17 +597,20 @@ constexpr int kCtlBytes = (static_cast<int>(sizeof(I8Ctl)) + 127) / 128 * 128;
 }  // namespace
 
 // Weights first: a few 16 KB blocks more in flight matter to a small batch, whose
-// tokens need little; never less than two stages of either.
+// tokens need little; never less than two stages of either.  An even number of them, so that
+// a stage is always the same converters': who sees only every other use of a barrier could
+// take a phase that has not come for the one before it.
 int i8_tc_stages(bool pair, int tn, int* w, int* x) {
     const int xbytes = tn / (pair ? 2 : 1) * 256, room = kSmemLimit - 1024 - kCtlBytes;
     *x = xbytes > 32768 ? 2 : xbytes > 16384 ? 4 : xbytes > 8192 ? 5 : 8;
     *w = (room - *x * xbytes) / kWBytes;
     if (*w > kI8MaxStages) *w = kI8MaxStages;
+    *w &= ~1;
     return 1024 + kCtlBytes + *w * kWBytes + *x * xbytes;
 }
 
 cudaError_t launch_i8_tc(const I8TcArgs& a, const CUtensorMap* map_w, const CUtensorMap* map_x, bool pair, int dev, void* stream) {
-    static bool done[2][64] = {};
+    static bool done[2][64] = {};  // (as SmemOptIn)
     int w, x;
     const int smem = i8_tc_stages(pair, a.tn, &w, &x);
     auto kernel = pair ? i8_tc_kernel<2> : i8_tc_kernel<1>;
@@ -561,13 +620,13 @@ cudaError_t launch_i8_tc(const I8TcArgs& a, const CUtensorMap* map_w, const CUte
         __atomic_store_n(&done[pair][dev], true, __ATOMIC_RELEASE);
     }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(a.grid * (pair ? 2 : 1));
+    cfg.gridDim = dim3(pair ? 2 * a.grid : a.split > 1 ? a.grid * a.split : a.grid);
     cfg.blockDim = dim3(kI8Threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = pair ? 2 : 1;
+    at[0].val.clusterDim.x = pair ? 2 : a.split;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[1].val.programmaticStreamSerializationAllowed = 1;

@@ -25,15 +25,25 @@ struct I8QuantArgs {
     EtHeader* hdr;
 };
 
-// q of eight values, packed in two words.
+// q of eight values, packed in two words; r = 1 / s, within 1 ulp of it.  v r is within 3 ulp
+// of v / s (|v / s| <= 127: 2^-15), so both round to the same integer unless v r is closer to
+// a half than that; there the quotient itself decides.
 template <class F>
-__device__ __forceinline__ uint2 quantize8(const F& v, float s, bool live) {
+__device__ __forceinline__ uint2 quantize8(const F& v, float s, float r, bool live) {
     uint32_t b[8];
+    bool near = false;
+    float t[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int q = live ? max(-127, min(127, __float2int_rn(__fdiv_rn(v[i], s)))) : 0;
-        b[i] = static_cast<uint32_t>(q) & 0xffu;
+        t[i] = live ? v[i] * r : 0.0f;
+        near |= !(fabsf(fabsf(t[i] - truncf(t[i])) - 0.5f) > 6.2e-5f);  // a NaN counts
     }
+    if (near) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = __fdiv_rn(v[i], s);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = static_cast<uint32_t>(max(-127, min(127, __float2int_rn(t[i])))) & 0xffu;
     return make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
 }
 
@@ -70,13 +80,15 @@ __global__ void __launch_bounds__(1024) i8_quantize_kernel(const I8QuantArgs p) 
         }
         const bool finite = top < 0x7f800000u, live = finite && top != 0;
         const float s = finite ? __fdiv_rn(__uint_as_float(top), 127.0f) : __int_as_float(0x7fffffff);
+        // scales as small as that have no finite reciprocal: every quotient is taken
+        const float r = s >= 1e-37f ? __frcp_rn(s) : __int_as_float(0x7fffffff);
         if (g.lane() == 0) p.scale[m] = s;
         int8_t* out = p.q + static_cast<size_t>(m) * K;
         for (int c0 = 0; c0 < K; c0 += span)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 if (K > span) v[j] = load8<VEC>(row + c0, g, j, K - c0);
-                const uint2 q = quantize8(v[j], s, live);
+                const uint2 q = quantize8(v[j], s, r, live);
                 if (VEC) {
                     const int c = c0 + g.template col<VEC>(j, 0);
                     if (c < K) *reinterpret_cast<uint2*>(out + c) = q;
@@ -215,47 +227,65 @@ int i8_check_rows(int M, const int32_t* d_M, int M_max) {
     return ET_OK;
 }
 
-// How a pass of M rows runs on the tensor cores, and what it needs of the workspace.
+// How a pass of M rows runs on the tensor cores.
 struct I8Plan {
     bool pair;
-    int tn, mt, nt, kblocks, grid, share;
-    size_t count, x16, part, total;
+    int tn, nt, kblocks, grid, split;
 };
 
 int ceil_div_l(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
-I8Plan i8_plan(int M, int N, int K) {
-    I8Plan p{};
-    p.kblocks = ceil_div_l(K, kI8KBlock);
-    p.mt = ceil_div_l(M, kI8TokensMax);
-    p.pair = static_cast<long long>(p.mt) * ceil_div_l(N, 256) >= kI8Sms / 2;
-    p.tn = ceil_div_l(ceil_div_l(M, p.mt), 32) * 32;
-    if (M <= 16) p.tn = 16;
-    p.nt = ceil_div_l(N, p.pair ? 256 : 128);
-    const int most = p.pair ? kI8Sms / 2 : kI8Sms;
-    const long long tiles = static_cast<long long>(p.mt) * p.nt, blocks = tiles * p.kblocks;
-    // whole tiles where their last round leaves few CTAs idle; else even shares of all
-    // k-blocks, four or more a CTA
-    p.share = 10 * tiles < 8ll * ceil_div_l(tiles, most) * most;
-    p.grid = most;
-    if (p.share && blocks < 4ll * most) p.grid = blocks < 4 ? 1 : static_cast<int>(blocks / 4);
-    // Regions that M alone sizes and that grow with it, so that a call with fewer rows than
-    // M_max finds room.  Shared tiles: fewer than 4 x 152, as more fill their rounds; parts: two
-    // a CTA, at most 152 x 128 channels x (M, 256 at most).
-    p.count = 1024;
-    p.part = 4096;
-    const size_t widest = ceil_div_l(M < kI8TokensMax ? M : kI8TokensMax, 32) * 32;
-    p.x16 = p.part + 2ull * kI8Sms * 128 * sizeof(float) * widest;
-    p.total = (p.x16 + 2ull * M * K + 255) / 256 * 256;
-    return p;
+// Estimated cycles of a pass in one form (comment above i8_plan).
+double i8_cost(int M, int N, const I8Plan& p) {
+    const int mt = ceil_div_l(M, p.tn), most = p.pair ? kI8Sms / 2 : kI8Sms;
+    const double tiles = static_cast<double>(mt) * p.nt, units = tiles * p.split;
+    const double waves = units <= most ? 1.0 : static_cast<double>(ceil_div_l(static_cast<long long>(tiles), most));
+    const double active = (units < most ? units : most) * (p.pair ? 2 : 1);
+    double stage = 4.0 * p.tn;                                   // the MMAs
+    auto at_least = [&](double v) { if (v > stage) stage = v; };
+    at_least(450.0);                                             // their issue, the conversion
+    at_least((16384.0 + 128.0 * p.tn) / 44.0);                   // what an SM gets from L2
+    if (waves == 1.0) at_least(16384.0 * active / 3500.0);       // what HBM brings
+    if (!p.pair) at_least(p.tn > 128 ? 1500.0 : p.tn > 64 ? 900.0 : p.tn > 32 ? 520.0 : 450.0);  // the tokens' conversion
+    const double blocks = ceil_div_l(p.kblocks, p.split);
+    const double tile = blocks * stage + (p.tn > 128 || waves == 1.0 ? 9.0 * p.tn : 200.0) + (p.split > 1 ? 2500.0 + 6.0 * p.tn : 0.0);
+    return waves * tile + (p.pair ? 6000.0 + 3.0 * M * p.kblocks * kI8KBlock / 3000.0 : 0.0);
 }
 
-// Tokens that are held as fp16 at a time: at K = 4096 they stay in L2 with their weights,
-// and the workspace of a long batch stays small.
+I8Plan i8_plan(int M, int N, int K) {
+    I8Plan best{};
+    double cost = 0.0;
+    for (int pair = 0; pair < 2; ++pair)
+        for (int tn = 32; tn <= kI8TokensMax; tn += 32) {
+            I8Plan p{};
+            p.pair = pair != 0;
+            p.kblocks = ceil_div_l(K, kI8KBlock);
+            p.nt = ceil_div_l(N, pair ? 256 : 128);
+            const int mt = ceil_div_l(M, tn);
+            p.tn = ceil_div_l(ceil_div_l(M, mt), 32) * 32;
+            const long long tiles = static_cast<long long>(mt) * p.nt;
+            const int most = pair ? kI8Sms / 2 : kI8Sms;
+            p.grid = tiles < most ? static_cast<int>(tiles) : most;
+            for (p.split = 1; p.split <= (pair ? 1 : 8); p.split *= 2) {
+                if (p.split > 1 && (p.split * tiles > most || p.split > p.kblocks)) break;
+                const double c = i8_cost(M, N, p);
+                if (!best.tn || c < cost) {
+                    best = p;
+                    cost = c;
+                }
+            }
+            if (tn >= M) break;
+        }
+    return best;
+}
+
+// Tokens that a call holds as fp16 at a time: at K = 4096 they stay in L2 with their
+// weights, and the workspace of a long batch stays small.
 constexpr int kI8RowsPass = 8192;
 
-size_t i8_ws_bytes(int M_max, int N, int K) {
-    return M_max <= kGemvTokens ? kHeaderBytes : i8_plan(M_max < kI8RowsPass ? M_max : kI8RowsPass, N, K).total;
+size_t i8_ws_bytes(int M_max, int K) {
+    const size_t rows = M_max <= kGemvTokens ? 0 : M_max < kI8RowsPass ? M_max : kI8RowsPass;
+    return (kHeaderBytes + 2 * rows * K + 255) / 256 * 256;
 }
 
 template <bool VEC>
@@ -309,7 +339,7 @@ int et_i8_quantize(const void* x, void* q, float* scale, int M, const int32_t* d
 
 size_t et_i8_gemm_workspace_bytes(int M_max, int N, int K) {
     std::string why;
-    return i8_shape_ok(M_max, N, K, &why) ? i8_ws_bytes(M_max, N, K) : 0;
+    return i8_shape_ok(M_max, N, K, &why) ? i8_ws_bytes(M_max, K) : 0;
 }
 
 int et_i8_gemm(const void* x_q, const float* s_x, const void* w_q, const float* s_w, void* Y, int M, const int32_t* d_M,
@@ -323,7 +353,7 @@ int et_i8_gemm(const void* x_q, const float* s_x, const void* w_q, const float* 
             return api_fail(ET_ERR_INVALID, "tensors must be aligned to their element size");
         int rc = i8_check_rows(M, d_M, M_max);
         if (rc) return rc;
-        if ((rc = api_check_ws(workspace, workspace_bytes, i8_ws_bytes(M_max, N, K)))) return rc;
+        if ((rc = api_check_ws(workspace, workspace_bytes, i8_ws_bytes(M_max, K)))) return rc;
         if (!d_M && M == 0) return ET_OK;
         int dev = 0, sms = 0;
         if ((rc = api_device(&dev, &sms))) return rc;
@@ -339,31 +369,34 @@ int et_i8_gemm(const void* x_q, const float* s_x, const void* w_q, const float* 
             if (e != cudaSuccess) return api_fail_cuda(e, "launch of the int8 product");
             return ET_OK;
         }
-        CUtensorMap mw, mx;
+        CUtensorMap mw;
         if ((rc = api_map128(&mw, w_q, 1, N, K, 128, "w_q"))) return rc;
         for (int m0 = 0; m0 < all; m0 += kI8RowsPass) {
             const int rows = all - m0 < kI8RowsPass ? all - m0 : kI8RowsPass;
             const I8Plan pl = i8_plan(rows, N, K);
             I8TcArgs a{};
+            a.x = x + static_cast<size_t>(m0) * K;
             a.sx = s_x + m0;
             a.sw = s_w;
             a.y = y + static_cast<size_t>(m0) * N;
             a.rows = {d_M, m0, rows, all};
             a.N = N;
+            a.K = K;
             a.hdr = hdr;
-            a.tile_count = reinterpret_cast<int32_t*>(ws + pl.count);
-            a.part = reinterpret_cast<float*>(ws + pl.part);
             a.tn = pl.tn;
             a.nt = pl.nt;
             a.kblocks = pl.kblocks;
             a.grid = pl.grid;
-            a.share = pl.share;
+            a.split = pl.split;
             i8_tc_stages(pl.pair, pl.tn, &a.stages_w, &a.stages_x);
             a.timeout_ns = 200000000ull;
-            if ((rc = api_map128(&mx, ws + pl.x16, 2, rows, K, pl.tn / (pl.pair ? 2 : 1), "x_q as fp16"))) return rc;
-            const I8ExpandArgs e16{x + static_cast<size_t>(m0) * K, ws + pl.x16, a.rows, K, hdr, a.tile_count,
-                                   pl.share ? pl.mt * pl.nt * (pl.pair ? 2 : 1) : 0};
-            cudaError_t e = launch_i8_expand(e16, sms, stream);
+            cudaError_t e = cudaSuccess;
+            CUtensorMap mx = mw;
+            if (pl.pair) {
+                void* x16 = ws + kHeaderBytes;
+                if ((rc = api_map128(&mx, x16, 2, rows, K, pl.tn / 2, "x_q as fp16"))) return rc;
+                e = launch_i8_expand({a.x, x16, a.rows, K, hdr}, sms, stream);
+            }
             if (e == cudaSuccess) e = launch_i8_tc(a, &mw, &mx, pl.pair, dev, stream);
             if (e != cudaSuccess) return api_fail_cuda(e, "launch of the int8 product");
         }
