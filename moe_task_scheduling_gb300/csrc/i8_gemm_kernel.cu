@@ -21,7 +21,7 @@
 // i8_expand_kernel: with a batch that long they are read by many pairs.
 //
 // Work: tiles of 128 CG channels x tn tokens, whole ones in turn.  Where tiles are few a
-// cluster of `split` CTAs takes one, each its share of k; their sums meet in shared
+// cluster of `split` CTAs or pairs takes one, each its share of k; their sums meet in shared
 // memory over the cluster and are added in the order of k: the same bits on every run.
 // Every wait is bounded.
 #include <cuda_fp16.h>
@@ -55,18 +55,18 @@ struct I8Ctl {
 // ---------------------------------------------------------------- PTX that et_device.cuh has for one CTA
 
 template <int CG>
-__device__ __forceinline__ uint32_t leader_addr(const void* p) {  // of this variable in the pair's first CTA
+__device__ __forceinline__ uint32_t leader_addr(const void* p, uint32_t cta) {  // of this variable in the pair's first CTA
     uint32_t a = smem_u32(p);
-    if (CG == 2) asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
+    if (CG == 2) asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(cta & ~1u));
     return a;
 }
 
 // (Without .cluster scope, which would make every arrival wait for this SM's stores and
 // every wait drop its L1: what the barriers order is in TMEM and in the async proxy.)
 template <int CG>
-__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+__device__ __forceinline__ void arrive_leader(uint64_t* bar, uint32_t cta) {
     if (CG == 1) mbar_arrive(bar);
-    else asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(leader_addr<2>(bar)) : "memory");
+    else asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(leader_addr<2>(bar, cta)) : "memory");
 }
 
 // mbar_wait (bounded) that polls for longer before it sleeps.
@@ -112,12 +112,12 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a, uint64_t bdesc, 
 
 // Arrive on `bar` (of both CTAs of a pair) once every MMA issued so far is done.
 template <int CG>
-__device__ __forceinline__ void commit(uint64_t* bar) {
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t cta) {
     if (CG == 1)
         tc_commit(bar);
     else
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
-                     "h"(static_cast<uint16_t>(3))
+                     "h"(static_cast<uint16_t>(3u << (cta & ~1u)))
                      : "memory");
 }
 
@@ -289,7 +289,7 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
     uint8_t* ring_x = base + p.stages_w * kWBytes;
     I8Ctl* ctl = reinterpret_cast<I8Ctl*>(ring_x + p.stages_x * xbytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+    const uint32_t crank = cluster_rank(), rank = CG == 2 ? crank & 1u : 0;  // in the cluster, in the pair
     if (threadIdx.x == 0) {
         for (int i = 0; i < kI8MaxStages; ++i) {
             mbar_init(&ctl->full_w[i], 1);
@@ -368,7 +368,7 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
                 for (int kb = w.kb0; kb < w.kb1; ++kb) {
                     if (!(ok = wait(wc, &ctl->empty_x[s], phase ^ 1u, kWhereEmpty))) break;
                     if (rank == 0) mbar_arrive_expect_tx(&ctl->full_x[s], xbytes * CG);
-                    const uint32_t bar = leader_addr<CG>(&ctl->full_x[s]), dst = smem_u32(ring_x + s * xbytes);
+                    const uint32_t bar = leader_addr<CG>(&ctl->full_x[s], crank), dst = smem_u32(ring_x + s * xbytes);
                     tma_tokens<CG>(dst, &tm_x, bar, kb * kI8KBlock, m0);
                     tma_tokens<CG>(dst + xrows * 128, &tm_x, bar, kb * kI8KBlock + 64, m0);
                     ++posted;
@@ -405,19 +405,19 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
 #pragma unroll
                         for (int k = 1; k < kI8KBlock / 16; ++k)  // 16 k are 32 bytes of a row of 64 k
                             mma_f16<CG>(d, a + k * 8, (k < 4 ? b0 : b1) + (k & 3) * 2, idesc, 1u);
-                        commit<CG>(&ctl->empty_x[kx]);
-                        commit<CG>(&ctl->empty_a[ka]);
+                        commit<CG>(&ctl->empty_x[kx], crank);
+                        commit<CG>(&ctl->empty_a[ka], crank);
                     }
                     __syncwarp();
                     if (++kx == static_cast<uint32_t>(p.stages_x)) { kx = 0; px ^= 1u; }
                     if (++ka == kAStages) { ka = 0; pa ^= 1u; }
                 }
                 if (!ok) break;
-                if (elect_one()) commit<CG>(&ctl->acc_full[slot]);
+                if (elect_one()) commit<CG>(&ctl->acc_full[slot], crank);
                 __syncwarp();
                 ++acc;
             }
-            if (elect_one()) commit<CG>(&ctl->drain);  // every arrival above has come when this one has
+            if (elect_one()) commit<CG>(&ctl->drain, crank);  // every arrival above has come when this one has
         }
         __syncwarp();
     } else if (warp < kEpiWarpI8) {
@@ -461,7 +461,7 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
                     // queue behind the first store to TMEM, and the next block was in their place.
                     if (lane == 0) {
                         mbar_arrive(&ctl->empty_w[s]);
-                        arrive_leader<CG>(&ctl->full_a[sa]);
+                        arrive_leader<CG>(&ctl->full_a[sa], crank);
                     }
                 }
                 if (++s == static_cast<uint32_t>(p.stages_w)) { s = 0; phase ^= 1u; }
@@ -514,7 +514,7 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_leader<CG>(&ctl->acc_empty[slot]);
+            if (lane == 0) arrive_leader<CG>(&ctl->acc_empty[slot], crank);
         }
     }
 
@@ -523,13 +523,13 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
     if (threadIdx.x == 32) (void)mbar_drain(&ctl->drain, 0, 2000000ull);
     tc_fence_before();
     __syncthreads();
-    if (CG == 2) cluster_sync();
+    if (CG == 2 && p.split == 1) cluster_sync();
     tc_fence_after();
-    if (CG == 1 && p.split > 1) {
-        // CTA r of the cluster sums tokens [r tn / split, (r + 1) tn / split) of the tile; what
+    if (p.split > 1) {
+        // Part r of the cluster sums tokens [r tn / split, (r + 1) tn / split) of the tile; what
         // the others have of them comes into its rings, which nothing uses any more.
         cluster_sync();
-        const int tile = blockIdx.x / p.split, mine = cluster_rank(), each = p.tn / p.split;
+        const int tile = blockIdx.x / (CG * p.split), mine = crank / CG, each = p.tn / p.split;
         const bool have = tile < tiles && !aborted(wc);
         if (have && warp < 16) {
             const uint32_t row = (warp & 3) * 32 + lane;
@@ -538,12 +538,13 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
                 float v[16];
                 tmem_ld16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0, v);
                 tmem_ld_wait();
+                int at = c0 / each, c = c0 - at * each;
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    const int at = (c0 + c) / each;
+                for (int i = 0; i < 16; ++i) {
                     uint32_t dst;
-                    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(to + (c0 + c - at * each) * 512), "r"(at));
-                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(v[c]) : "memory");
+                    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(to + c * 512), "r"(at * CG + rank));
+                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(v[i]) : "memory");
+                    if (++c == each) { c = 0; ++at; }
                 }
             }
         }
@@ -551,7 +552,7 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
         cluster_sync();
         tc_fence_after();
         if (have) {
-            const int m0 = (tile % mt) * p.tn, n0 = (tile / mt) * 128, rows = min(p.tn, M - m0);
+            const int m0 = (tile % mt) * p.tn, n0 = (tile / mt) * 128 * CG + static_cast<int>(rank) * 128, rows = min(p.tn, M - m0);
             const float* part = reinterpret_cast<const float*>(base);
             for (int o = threadIdx.x; o < each * 128; o += kI8Threads) {
                 const int c = mine * each + o / 128, n = n0 + o % 128;
@@ -620,13 +621,13 @@ cudaError_t launch_i8_tc(const I8TcArgs& a, const CUtensorMap* map_w, const CUte
         __atomic_store_n(&done[pair][dev], true, __ATOMIC_RELEASE);
     }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(pair ? 2 * a.grid : a.split > 1 ? a.grid * a.split : a.grid);
+    cfg.gridDim = dim3(a.grid * a.split * (pair ? 2 : 1));
     cfg.blockDim = dim3(kI8Threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = pair ? 2 : a.split;
+    at[0].val.clusterDim.x = a.split * (pair ? 2 : 1);
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[1].val.programmaticStreamSerializationAllowed = 1;

@@ -235,21 +235,24 @@ struct I8Plan {
 
 int ceil_div_l(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
-// Estimated cycles of a pass in one form (comment above i8_plan).
-double i8_cost(int M, int N, const I8Plan& p) {
-    const int mt = ceil_div_l(M, p.tn), most = p.pair ? kI8Sms / 2 : kI8Sms;
-    const double tiles = static_cast<double>(mt) * p.nt, units = tiles * p.split;
-    const double waves = units <= most ? 1.0 : static_cast<double>(ceil_div_l(static_cast<long long>(tiles), most));
-    const double active = (units < most ? units : most) * (p.pair ? 2 : 1);
-    double stage = 4.0 * p.tn;                                   // the MMAs
-    auto at_least = [&](double v) { if (v > stage) stage = v; };
-    at_least(450.0);                                             // their issue, the conversion
-    at_least((16384.0 + 128.0 * p.tn) / 44.0);                   // what an SM gets from L2
-    if (waves == 1.0) at_least(16384.0 * active / 3500.0);       // what HBM brings
-    if (!p.pair) at_least(p.tn > 128 ? 1500.0 : p.tn > 64 ? 900.0 : p.tn > 32 ? 520.0 : 450.0);  // the tokens' conversion
-    const double blocks = ceil_div_l(p.kblocks, p.split);
-    const double tile = blocks * stage + (p.tn > 128 || waves == 1.0 ? 9.0 * p.tn : 200.0) + (p.split > 1 ? 2500.0 + 6.0 * p.tn : 0.0);
-    return waves * tile + (p.pair ? 6000.0 + 3.0 * M * p.kblocks * kI8KBlock / 3000.0 : 0.0);
+// Estimated cycles of a pass in one form, without what all forms have.  Numbers: measured
+// over the forms of some twenty shapes; a block is 128 x 128 weights and the tile's tokens.
+double i8_cost(int M, const I8Plan& p) {
+    const long long tiles = static_cast<long long>(ceil_div_l(M, p.tn)) * p.nt, units = tiles * p.split;
+    const int most = p.pair ? kI8Sms / 2 : kI8Sms;
+    const double waves = p.split > 1 ? 1.0 : static_cast<double>(ceil_div_l(tiles, most));
+    const double ctas = static_cast<double>(units < most ? units : most) * (p.pair ? 2 : 1);
+    double block = 4.0 * p.tn;                                        // the MMAs,
+    auto at_least = [&](double v) { if (v > block) block = v; };
+    at_least(waves > 1.0 ? 600.0 : 560.0);                            // the weights' conversion,
+    at_least((16384.0 + 128.0 * p.tn) / 50.0);                        // what an SM gets from L2,
+    if (waves == 1.0) at_least(16384.0 * ctas / 3500.0);              // what HBM brings,
+    if (!p.pair) at_least(p.tn > 128 ? 1900.0 : p.tn > 64 ? 1090.0 : p.tn > 32 ? 700.0 : 560.0);  // the tokens' conversion
+    double tile = ceil_div_l(p.kblocks, p.split) * block;
+    tile += p.tn > 128 || waves == 1.0 ? 9.0 * p.tn : 200.0;          // the epilogue, where nothing runs beside it
+    const int cluster = p.split * (p.pair ? 2 : 1);
+    if (p.split > 1) tile += 3000.0 + 10.0 * p.tn + (cluster == 8 ? 9000.0 : 0.0);  // clusters of 8 find few places
+    return waves * tile + (p.pair ? 1500.0 + 3.0 * M * p.kblocks * kI8KBlock / 2600.0 : 0.0);
 }
 
 I8Plan i8_plan(int M, int N, int K) {
@@ -266,9 +269,9 @@ I8Plan i8_plan(int M, int N, int K) {
             const long long tiles = static_cast<long long>(mt) * p.nt;
             const int most = pair ? kI8Sms / 2 : kI8Sms;
             p.grid = tiles < most ? static_cast<int>(tiles) : most;
-            for (p.split = 1; p.split <= (pair ? 1 : 8); p.split *= 2) {
+            for (p.split = 1; p.split <= (pair ? 4 : 8); p.split *= 2) {
                 if (p.split > 1 && (p.split * tiles > most || p.split > p.kblocks)) break;
-                const double c = i8_cost(M, N, p);
+                const double c = i8_cost(M, p);
                 if (!best.tn || c < cost) {
                     best = p;
                     cost = c;
