@@ -25,32 +25,40 @@ struct I8QuantArgs {
     EtHeader* hdr;
 };
 
-// q of eight values, packed in two words; r = 1 / s, within 1 ulp of it.  v r is within 3 ulp
-// of v / s (|v / s| <= 127: 2^-15), so both round to the same integer unless v r is closer to
-// a half than that; there the quotient itself decides.
-template <class F>
-__device__ __forceinline__ uint2 quantize8(const F& v, float s, float r, bool live) {
-    uint32_t b[8];
-    bool near = false;
-    float t[8];
+// q of eight values, packed in two words; r = 1 / s, rounded.  v r is within 3 x 2^-24 of
+// v / s, 2^-15 at most, so both round to the same integer unless v r is closer to a half
+// than that; there, and where r is no use, the quotient itself decides.  Adding 1.5 x 2^23
+// rounds (half to even) and leaves the integer in the low bits.
+__device__ __forceinline__ uint2 quantize8(const Vec8& v, float s, float r, bool use_r) {
+    constexpr float kMagic = 12582912.0f;
+    float2 t[4];
+    float far = 0.0f;  // the largest distance from an integer
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        t[i] = live ? v[i] * r : 0.0f;
-        near |= !(fabsf(fabsf(t[i] - truncf(t[i])) - 0.5f) > 6.2e-5f);  // a NaN counts
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = __fmul2_rn(unpack2(v.u[i]), both(r));
+        t[i] = __fadd2_rn(x, both(kMagic));
+        const float2 d = __ffma2_rn(__fadd2_rn(t[i], both(-kMagic)), both(-1.0f), x);
+        far = fmaxf(far, fmaxf(fabsf(d.x), fabsf(d.y)));
     }
-    if (near) {
+    if (!use_r || far > 0.5f - 6.2e-5f) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = __fdiv_rn(v[i], s);
+        for (int i = 0; i < 4; ++i) {
+            const float2 x = unpack2(v.u[i]);
+            t[i].x = fmaxf(-127.0f, fminf(127.0f, __fdiv_rn(x.x, s))) + kMagic;
+            t[i].y = fmaxf(-127.0f, fminf(127.0f, __fdiv_rn(x.y, s))) + kMagic;
+        }
     }
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = static_cast<uint32_t>(max(-127, min(127, __float2int_rn(t[i])))) & 0xffu;
-    return make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
+    for (int i = 0; i < 4; ++i) w[i] = __byte_perm(__float_as_uint(t[i].x), __float_as_uint(t[i].y), 0x0040);
+    return make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
 }
 
 // A row's largest magnitude, then its values: a row of up to sixteen columns a thread
-// (16384) stays in registers, a longer one is read again (from the caches).
+// (16384) stays in registers, and the next one is on its way meanwhile; a longer one is
+// read again (from the caches).
 template <bool VEC, int MODE>
-__global__ void __launch_bounds__(1024) i8_quantize_kernel(const I8QuantArgs p) {
+__global__ void __launch_bounds__(MODE == kRowsOne ? 1024 : 256) i8_quantize_kernel(const I8QuantArgs p) {
     constexpr int V = norm_v(MODE);
     __shared__ uint32_t red[2][32];
     int n = 0;
@@ -58,19 +66,37 @@ __global__ void __launch_bounds__(1024) i8_quantize_kernel(const I8QuantArgs p) 
     grid_begin();
     bool ok;
     const int M = row_count(p.d_M, p.M_host, p.M_max, p.hdr, &ok);
-    const int K = p.K, span = g.th() * 8 * V;
-    for (int m = blockIdx.x * g.groups() + g.id(); m < M; m += gridDim.x * g.groups()) {
-        const bf16* row = p.x + static_cast<size_t>(m) * K;
-        Vec8 v[V];
-        uint32_t top = 0;  // as the bits of |x|, which order as their values do, NaN above infinity
-        for (int c0 = 0; c0 < K; c0 += span)
+    const int K = p.K, span = g.th() * 8 * V, step = gridDim.x * g.groups();
+    const bool whole = K <= span;
+    Vec8 v[V], next[V];
+    auto fetch = [&](int m) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                v[j] = load8<VEC>(row + c0, g, j, K - c0);
+        for (int j = 0; j < V; ++j) next[j] = m < M ? load8<VEC>(p.x + static_cast<size_t>(m) * K, g, j, K) : Vec8{};
+    };
+    int m = blockIdx.x * g.groups() + g.id();
+    if (whole) fetch(m);
+    for (; m < M; m += step) {
+        const bf16* row = p.x + static_cast<size_t>(m) * K;
+        uint32_t top = 0;  // as the bits of |x|, which order as their values do, NaN above infinity
+        auto look = [&]() {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     top = max(top, max(v[j].u[i] << 16 & 0x7fff0000u, v[j].u[i] & 0x7fff0000u));
+        };
+        if (whole) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] = next[j];
+            fetch(m + step);
+            look();
+        } else {
+            for (int c0 = 0; c0 < K; c0 += span) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) v[j] = load8<VEC>(row + c0, g, j, K - c0);
+                look();
             }
+        }
         top = __reduce_max_sync(0xffffffffu, top);
         if (MODE != kRowsWarp) {
             const int slot = n++ & 1, lane = threadIdx.x & 31, first = g.id() * (g.th() >> 5);
@@ -80,15 +106,16 @@ __global__ void __launch_bounds__(1024) i8_quantize_kernel(const I8QuantArgs p) 
         }
         const bool finite = top < 0x7f800000u, live = finite && top != 0;
         const float s = finite ? __fdiv_rn(__uint_as_float(top), 127.0f) : __int_as_float(0x7fffffff);
-        // scales as small as that have no finite reciprocal: every quotient is taken
-        const float r = s >= 1e-37f ? __frcp_rn(s) : __int_as_float(0x7fffffff);
+        const bool use_r = s >= 1e-37f;  // a smaller scale has no finite reciprocal
+        const float r = use_r ? __frcp_rn(s) : 0.0f;
         if (g.lane() == 0) p.scale[m] = s;
         int8_t* out = p.q + static_cast<size_t>(m) * K;
         for (int c0 = 0; c0 < K; c0 += span)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                if (K > span) v[j] = load8<VEC>(row + c0, g, j, K - c0);
-                const uint2 q = quantize8(v[j], s, r, live);
+                if (!whole) v[j] = load8<VEC>(row + c0, g, j, K - c0);
+                uint2 q = make_uint2(0, 0);
+                if (live) q = quantize8(v[j], s, r, use_r);
                 if (VEC) {
                     const int c = c0 + g.template col<VEC>(j, 0);
                     if (c < K) *reinterpret_cast<uint2*>(out + c) = q;

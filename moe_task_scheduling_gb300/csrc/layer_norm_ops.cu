@@ -60,18 +60,25 @@ __device__ __forceinline__ uint4 drop_bits(const DropKey& k, uint32_t h8, uint32
     return make_uint4(a, b, c, d);
 }
 
-// Bit i: element i of the eight is kept.
-__device__ __forceinline__ uint32_t drop_keep8(const DropKey& k, uint32_t thr, uint32_t h8, uint32_t t) {
+// What is dropped of eight packed bf16: ones over the elements whose 16 bits are below thr
+// (a byte permutation spreads the sign of bits - thr).
+struct Mask8 { uint32_t u[4]; };
+__device__ __forceinline__ Mask8 drop_mask8(const DropKey& k, uint32_t thr, uint32_t h8, uint32_t t) {
     const uint4 w = drop_bits(k, h8, t);
-    const uint32_t hi = thr << 16;
-    uint32_t m = 0;
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    Mask8 m;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        m |= (u[i] << 16 >= hi ? 1u : 0u) << (2 * i);
-        m |= (u[i] >= hi ? 1u : 0u) << (2 * i + 1);
-    }
+    for (int i = 0; i < 4; ++i)
+        asm("prmt.b32 %0, %1, %2, 0xffbb;" : "=r"(m.u[i]) : "r"((u[i] & 0xffffu) - thr), "r"((u[i] >> 16) - thr));
     return m;
+}
+
+// Bit i: element i of the eight is dropped.
+__device__ __forceinline__ uint32_t mask_bits(const Mask8& m) {
+    uint32_t b = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b |= (m.u[i] & 1u) << (2 * i) | (m.u[i] >> 31) << (2 * i + 1);
+    return b;
 }
 
 // ---------------------------------------------------------------- dropout by itself
@@ -122,18 +129,14 @@ __global__ void __launch_bounds__(kDropThreads) dropout_vec_kernel(const Dropout
             const int i = i0 + u * kDropThreads;
             if (i >= n) break;
             const uint32_t row = H8 > 1 ? __umulhi(i, p.magic) : i;
-            const uint32_t keep = p.drop.thr ? drop_keep8(key, p.drop.thr, i - row * H8, t0 + row) : 0xffu;
+            const Mask8 m = p.drop.thr ? drop_mask8(key, p.drop.thr, i - row * H8, t0 + row) : Mask8{};
             const uint32_t yw[4] = {yv[u].x, yv[u].y, yv[u].z, yv[u].w}, xw[4] = {xv[u].x, xv[u].y, xv[u].z, xv[u].w};
             uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                float lo = keep >> (2 * j) & 1 ? bf_lo(yw[j]) * p.drop.mul : 0.0f;
-                float hi = keep >> (2 * j + 1) & 1 ? bf_hi(yw[j]) * p.drop.mul : 0.0f;
-                if (x) {
-                    lo += bf_lo(xw[j]);
-                    hi += bf_hi(xw[j]);
-                }
-                o[j] = pack_bf16(lo, hi);
+                float2 v = __fmul2_rn(unpack2(yw[j] & ~m.u[j]), both(p.drop.mul));
+                if (x) v = __fadd2_rn(v, unpack2(xw[j]));
+                o[j] = pack_bf16(v.x, v.y);
             }
             out[i] = make_uint4(o[0], o[1], o[2], o[3]);
         }
@@ -143,7 +146,7 @@ __global__ void __launch_bounds__(kDropThreads) dropout_vec_kernel(const Dropout
 // Any H and alignment: a CTA takes 2048 columns of a row, draws their mask into
 // shared memory, then neighbouring threads take neighbouring elements.
 __global__ void __launch_bounds__(kDropThreads) dropout_any_kernel(const DropoutArgs p) {
-    __shared__ uint8_t keep[kDropCols / 8];
+    __shared__ uint8_t dropped[kDropCols / 8];
     grid_begin();
     bool ok;
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
@@ -153,7 +156,7 @@ __global__ void __launch_bounds__(kDropThreads) dropout_any_kernel(const Dropout
     const int n = min(kDropCols, p.H - c0);
     const DropKey key(p.drop);
     static_assert(kDropCols / 8 == kDropThreads, "a thread draws eight elements");
-    keep[threadIdx.x] = p.drop.thr ? drop_keep8(key, p.drop.thr, c0 / 8 + threadIdx.x, t) : 0xffu;
+    dropped[threadIdx.x] = p.drop.thr ? mask_bits(drop_mask8(key, p.drop.thr, c0 / 8 + threadIdx.x, t)) : 0u;
     __syncthreads();
     const size_t off = static_cast<size_t>(t) * p.H + c0;
     bf16 yv[8], xv[8];
@@ -170,7 +173,7 @@ __global__ void __launch_bounds__(kDropThreads) dropout_any_kernel(const Dropout
     for (int i = 0; i < 8; ++i) {
         const int c = threadIdx.x + i * kDropThreads;
         if (c < n) {
-            float v = keep[c >> 3] >> (c & 7) & 1 ? __bfloat162float(yv[i]) * p.drop.mul : 0.0f;
+            float v = dropped[c >> 3] >> (c & 7) & 1 ? 0.0f : __bfloat162float(yv[i]) * p.drop.mul;
             if (p.x) v += __bfloat162float(xv[i]);
             p.out[off + c] = __float2bfloat16_rn(v);
         }
@@ -202,54 +205,63 @@ struct LnArgs {
     float* part;          // [CTAs][2][H]
 };
 
-// N sums over the row's threads at once, as row_sum.
-template <int N, int MODE>
+// N sums over the row's threads at once, as row_sum; the warps' sums (eight at most, or in
+// a warp's lanes) are added in their order.
+template <int N, int MODE, int MAXT>
 __device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[N][32], const RowGroup<MODE>& g, int& n) {
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1)
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
     if (MODE != kRowsWarp) {
-        const int slot = n++ & 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        const int first = g.id() * (g.th() >> 5);
+        const int slot = n++ & 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = g.th() >> 5;
+        const int first = g.id() * warps;
         if (lane == 0)
 #pragma unroll
             for (int i = 0; i < N; ++i) red[slot][i][warp] = v[i];
         g.sync();
-        const bool in = lane < (g.th() >> 5);
+        if (MAXT <= 256) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = in ? red[slot][i][first + lane] : 0.0f;
+            for (int i = 0; i < N; ++i) v[i] = 0.0f;
 #pragma unroll
-        for (int off = 16; off >= 1; off >>= 1)
+            for (int w = 0; w < 8; ++w)
+                if (w < warps)
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+                    for (int i = 0; i < N; ++i) v[i] += red[slot][i][first + w];
+        } else {
+            const bool in = lane < warps;
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = in ? red[slot][i][first + lane] : 0.0f;
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1)
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+        }
     }
 }
 
-// The mask of this thread's columns, bit i of element i of vector j.  VEC: drawn here.
-// Else the row's threads draw the row's mask into `bytes` first (8 columns a byte).
+// The mask of this thread's columns.  VEC: drawn here.  Else the row's threads draw the
+// row's mask into `bytes` first (8 columns a byte).
 template <bool VEC, int MODE>
-__device__ __forceinline__ void row_keep(uint32_t (&keep)[norm_v(MODE)], const DropArgs& d, const DropKey& key,
+__device__ __forceinline__ void row_mask(Mask8 (&m)[norm_v(MODE)], const DropArgs& d, const DropKey& key,
                                          const RowGroup<MODE>& g, uint8_t* bytes, int t, int H) {
 #pragma unroll
-    for (int j = 0; j < norm_v(MODE); ++j) keep[j] = 0xffu;
+    for (int j = 0; j < norm_v(MODE); ++j) m[j] = Mask8{};
     if (!d.thr) return;
     if (VEC) {
 #pragma unroll
-        for (int j = 0; j < norm_v(MODE); ++j) keep[j] = drop_keep8(key, d.thr, g.template col<true>(j, 0) >> 3, t);
+        for (int j = 0; j < norm_v(MODE); ++j) m[j] = drop_mask8(key, d.thr, g.template col<true>(j, 0) >> 3, t);
     } else {
         g.sync();  // the last row's mask has been read
-        for (int q = g.lane(); q < (H + 7) >> 3; q += g.th()) bytes[q] = drop_keep8(key, d.thr, q, t);
+        for (int q = g.lane(); q < (H + 7) >> 3; q += g.th()) bytes[q] = mask_bits(drop_mask8(key, d.thr, q, t));
         g.sync();
 #pragma unroll
-        for (int j = 0; j < norm_v(MODE); ++j) {
-            keep[j] = 0;
+        for (int j = 0; j < norm_v(MODE); ++j)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int c = g.template col<false>(j, i);
-                if (c < H) keep[j] |= (bytes[c >> 3] >> (c & 7) & 1u) << i;
+                if (c < H && (bytes[c >> 3] >> (c & 7) & 1)) m[j].u[i >> 1] |= i & 1 ? 0xffff0000u : 0xffffu;
             }
-        }
     }
 }
 
@@ -257,8 +269,8 @@ __host__ __device__ constexpr int ln_mask_bytes(int H) { return (H + 7) / 8; }
 
 // The mean first, then the squares of the distances from it: one pass over memory,
 // two sums over the row's threads.
-template <bool VEC, int MODE>
-__global__ void __launch_bounds__(1024) ln_fwd_kernel(const LnArgs p) {
+template <bool VEC, int MODE, int MAXT>
+__global__ void __launch_bounds__(MAXT) ln_fwd_kernel(const LnArgs p) {
     constexpr int V = norm_v(MODE);
     __shared__ float red[2][1][32];
     extern __shared__ uint8_t masks[];  // without VEC: [groups][H / 8]
@@ -272,53 +284,59 @@ __global__ void __launch_bounds__(1024) ln_fwd_kernel(const LnArgs p) {
     uint8_t* bytes = masks + g.id() * ln_mask_bytes(H);
     for (int t = blockIdx.x * g.groups() + g.id(); t < T; t += gridDim.x * g.groups()) {
         const size_t off = static_cast<size_t>(t) * H;
-        float z[V][8];
-        Vec8 yv[V];
+        Vec8 xv[V], yv[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const Vec8 xv = load8<VEC>(p.x + off, g, j, H);
+            xv[j] = load8<VEC>(p.x + off, g, j, H);
             yv[j] = p.y ? load8<VEC>(p.y + off, g, j, H) : Vec8{};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) z[j][i] = xv[i];
         }
+        float2 z[V][4], s2 = both(0.0f);
         if (p.y) {
-            uint32_t keep[V];
-            row_keep<VEC>(keep, p.drop, key, g, bytes, t, H);
+            Mask8 m[V];
+            row_mask<VEC>(m, p.drop, key, g, bytes, t, H);  // while the loads are on their way
 #pragma unroll
             for (int j = 0; j < V; ++j)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) z[j][i] += keep[j] >> i & 1 ? yv[j][i] * p.drop.mul : 0.0f;
+                for (int i = 0; i < 4; ++i) z[j][i] = __ffma2_rn(unpack2(yv[j].u[i] & ~m[j].u[i]), both(p.drop.mul), unpack2(xv[j].u[i]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[j][i] = unpack2(xv[j].u[i]);
         }
-        float s[1] = {0.0f};
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            if (p.x_out) store8<VEC>(p.x_out + off, g, j, H, z[j]);
+            if (p.x_out) store8<VEC>(p.x_out + off, g, j, H, &z[j][0].x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[0] += z[j][i];  // 0 past H
+            for (int i = 0; i < 4; ++i) s2 = __fadd2_rn(s2, z[j][i]);  // 0 past H
         }
-        row_sums(s, red, g, n_sums);
+        float s[1] = {s2.x + s2.y};
+        row_sums<1, MODE, MAXT>(s, red, g, n_sums);
         const float mean = __fdiv_rn(s[0], static_cast<float>(H));  // exact for a row of equal values: no deviation is made up
-        s[0] = 0.0f;
+        s2 = both(0.0f);
 #pragma unroll
         for (int j = 0; j < V; ++j)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                z[j][i] = g.template col<VEC>(j, i) < H ? z[j][i] - mean : 0.0f;
-                s[0] += z[j][i] * z[j][i];
+            for (int i = 0; i < 4; ++i) {
+                z[j][i] = __fadd2_rn(z[j][i], both(-mean));
+                if (VEC) {
+                    if (g.template col<VEC>(j, 0) >= H) z[j][i] = both(0.0f);
+                } else {
+                    if (g.template col<VEC>(j, 2 * i) >= H) z[j][i].x = 0.0f;
+                    if (g.template col<VEC>(j, 2 * i + 1) >= H) z[j][i].y = 0.0f;
+                }
+                s2 = __ffma2_rn(z[j][i], z[j][i], s2);
             }
-        row_sums(s, red, g, n_sums);
+        s[0] = s2.x + s2.y;
+        row_sums<1, MODE, MAXT>(s, red, g, n_sums);
         const float r = rsqrtf(s[0] * p.inv_H + p.eps);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const Vec8 gv = p.gamma ? load8<VEC>(p.gamma, g, j, H) : Vec8{};
-            const Vec8 bv = p.beta ? load8<VEC>(p.beta, g, j, H) : Vec8{};
-            float o[8];
+            const Vec8 one{{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u}};
+            const Vec8 gv = p.gamma ? load8<VEC>(p.gamma, g, j, H) : one, bv = p.beta ? load8<VEC>(p.beta, g, j, H) : Vec8{};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                o[i] = z[j][i] * r;
-                o[i] = p.gamma ? o[i] * gv[i] + bv[i] : o[i] + bv[i];
-            }
-            store8<VEC>(p.x_hat + off, g, j, H, o);
+            for (int i = 0; i < 4; ++i) z[j][i] = __ffma2_rn(__fmul2_rn(z[j][i], both(r)), unpack2(gv.u[i]), unpack2(bv.u[i]));
+            store8<VEC>(p.x_hat + off, g, j, H, &z[j][0].x);
         }
     }
 }
@@ -363,19 +381,19 @@ __global__ void __launch_bounds__(MAXT, MAXT > 512 ? 1 : 512 / MAXT) ln_bwd_kern
     par += grp.lane() * 16;
     const DropKey key(p.drop);
 
-    auto source = [&](int a) -> const bf16* {
-        return a == 0 ? p.x : a == 1 ? p.d_x_hat : a == 2 && ny ? p.y : p.d_x_out;
-    };
+    const bf16* const src[4] = {p.x, p.d_x_hat, ny ? p.y : p.d_x_out, p.d_x_out};
     auto stage = [&](int t, int buf) {
         if (t < T) {
             const size_t off = static_cast<size_t>(t) * H;
             const uint32_t dst = smem_addr(mine) + buf * A * row_b;
-            for (int a = 0; a < A; ++a) {
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                if (a >= A) break;
                 if (VEC) {
-                    if (in0) cp_async16(dst + a * row_b + c0 * 2, source(a) + off + c0);
-                    if (in1) cp_async16(dst + a * row_b + c1 * 2, source(a) + off + c1);
+                    if (in0) cp_async16(dst + a * row_b + c0 * 2, src[a] + off + c0);
+                    if (in1) cp_async16(dst + a * row_b + c1 * 2, src[a] + off + c1);
                 } else {
-                    const uint8_t* base = reinterpret_cast<const uint8_t*>(source(a));
+                    const uint8_t* base = reinterpret_cast<const uint8_t*>(src[a]);
                     const uint8_t* row = base + off * 2;
                     const uint8_t* first = row - (reinterpret_cast<uintptr_t>(row) & 15);
                     const int pieces = static_cast<int>((row + H2 - first + 15) >> 4);
@@ -460,7 +478,7 @@ __global__ void __launch_bounds__(MAXT, MAXT > 512 ? 1 : 512 / MAXT) ln_bwd_kern
             const size_t off = static_cast<size_t>(t) * H;
             auto get = [&](int a, int j) -> uint4 {  // vector j of staged row a; zeros past H
                 if (VEC) return (j ? in1 : in0) ? *reinterpret_cast<const uint4*>(rows + a * row_b + (j ? c1 : c0) * 2) : make_uint4(0, 0, 0, 0);
-                const uint16_t* r = reinterpret_cast<const uint16_t*>(rows + a * row_b + (reinterpret_cast<uintptr_t>(source(a) + off) & 15));
+                const uint16_t* r = reinterpret_cast<const uint16_t*>(rows + a * row_b + (reinterpret_cast<uintptr_t>(src[a] + off) & 15));
                 uint32_t w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -482,33 +500,36 @@ __global__ void __launch_bounds__(MAXT, MAXT > 512 ? 1 : 512 / MAXT) ln_bwd_kern
                 }
             };
             auto word = [](const uint4& v, int i) -> uint32_t { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; };
-            uint32_t keep[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) keep[j] = 0xffu;
-            if (ny) row_keep<VEC>(keep, p.drop, key, grp, bytes, t, H);
-            float2 z[V][4];
-            float2 s = both(0.0f);
+            Mask8 m[V];
+            float2 z[V][4], s2 = both(0.0f);
+            if (ny) row_mask<VEC>(m, p.drop, key, grp, bytes, t, H);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const uint4 x = get(0, j), y = ny ? get(2, j) : make_uint4(0, 0, 0, 0);
+                const uint4 x = get(0, j);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    z[j][i] = unpack2(word(x, i));
-                    if (ny) {
-                        const float2 v = __fmul2_rn(unpack2(word(y, i)), both(p.drop.mul));
-                        z[j][i].x += keep[j] >> (2 * i) & 1 ? v.x : 0.0f;
-                        z[j][i].y += keep[j] >> (2 * i + 1) & 1 ? v.y : 0.0f;
-                    }
-                    s = __fadd2_rn(s, z[j][i]);
+                for (int i = 0; i < 4; ++i) z[j][i] = unpack2(word(x, i));
+            }
+            if (ny) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const uint4 y = get(2, j);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) z[j][i] = __ffma2_rn(unpack2(word(y, i) & ~m[j].u[i]), both(p.drop.mul), z[j][i]);
                 }
             }
-            float s1[1] = {s.x + s.y};
-            row_sums(s1, red1, grp, n1);
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s2 = __fadd2_rn(s2, z[j][i]);
+            float s1[1] = {s2.x + s2.y};
+            row_sums<1, MODE, MAXT>(s1, red1, grp, n1);
             const float mean = __fdiv_rn(s1[0], static_cast<float>(H));
             float2 dd = both(0.0f), sa = both(0.0f), sad = both(0.0f);
+            uint4 dh[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const uint4 dh = get(1, j), gm = *reinterpret_cast<const uint4*>(par + j * grp.th() * 16);
+                dh[j] = get(1, j);
+                const uint4 gm = *reinterpret_cast<const uint4*>(par + j * grp.th() * 16);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     z[j][i] = __fadd2_rn(z[j][i], both(-mean));
@@ -518,36 +539,41 @@ __global__ void __launch_bounds__(MAXT, MAXT > 512 ? 1 : 512 / MAXT) ln_bwd_kern
                         if (grp.template col<VEC>(j, 2 * i) >= H) z[j][i].x = 0.0f;
                         if (grp.template col<VEC>(j, 2 * i + 1) >= H) z[j][i].y = 0.0f;
                     }
-                    const float2 a = __fmul2_rn(unpack2(word(dh, i)), unpack2(word(gm, i)));
+                    const float2 a = __fmul2_rn(unpack2(word(dh[j], i)), unpack2(word(gm, i)));
                     dd = __ffma2_rn(z[j][i], z[j][i], dd);
                     sa = __fadd2_rn(sa, a);
                     sad = __ffma2_rn(a, z[j][i], sad);
                 }
             }
             float s3[3] = {dd.x + dd.y, sa.x + sa.y, sad.x + sad.y};
-            row_sums(s3, red3, grp, n3);
+            row_sums<3, MODE, MAXT>(s3, red3, grp, n3);
             const float r = rsqrtf(s3[0] * p.inv_H + p.eps);
-            const float ra = -r * (s3[1] * p.inv_H), k = -r * r * r * (s3[2] * p.inv_H);
+            const float ra = -r * (s3[1] * p.inv_H), k = -r * r * (s3[2] * p.inv_H);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const uint4 dh = get(1, j), gm = *reinterpret_cast<const uint4*>(par + j * grp.th() * 16);
+                const uint4 gm = *reinterpret_cast<const uint4*>(par + j * grp.th() * 16);
                 const uint4 dz = nd ? get(2 + ny, j) : make_uint4(0, 0, 0, 0);
-                uint32_t odx[4], ody[4];
+                uint32_t odx[4];
+                float2 D[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 h = unpack2(word(dh, i));
-                    const float2 a = __fmul2_rn(h, unpack2(word(gm, i)));
-                    float2 D = __fadd2_rn(unpack2(word(dz, i)), both(ra));
-                    D = __ffma2_rn(a, both(r), D);
-                    D = __ffma2_rn(z[j][i], both(k), D);
-                    a_g[j][i] = __ffma2_rn(h, __fmul2_rn(z[j][i], both(r)), a_g[j][i]);
+                    const float2 h = unpack2(word(dh[j], i)), n = __fmul2_rn(z[j][i], both(r));
+                    D[i] = __fadd2_rn(unpack2(word(dz, i)), both(ra));
+                    D[i] = __ffma2_rn(__fmul2_rn(h, unpack2(word(gm, i))), both(r), D[i]);
+                    D[i] = __ffma2_rn(n, both(k), D[i]);
+                    a_g[j][i] = __ffma2_rn(h, n, a_g[j][i]);
                     a_b[j][i] = __fadd2_rn(a_b[j][i], h);
-                    odx[i] = pack_bf16(D.x, D.y);
-                    const float2 q = __fmul2_rn(D, both(p.drop.mul));
-                    ody[i] = pack_bf16(keep[j] >> (2 * i) & 1 ? q.x : 0.0f, keep[j] >> (2 * i + 1) & 1 ? q.y : 0.0f);
+                    odx[i] = pack_bf16(D[i].x, D[i].y);
                 }
                 put_row(p.dx, j, odx);
-                if (p.dy) put_row(p.dy, j, ody);
+                if (p.dy) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        D[i] = __fmul2_rn(D[i], both(p.drop.mul));
+                        odx[i] = pack_bf16(D[i].x, D[i].y) & ~m[j].u[i];
+                    }
+                    put_row(p.dy, j, odx);
+                }
             }
         }
         if (!VEC) grp.sync();  // this buffer and the mask's bytes are written again
@@ -644,9 +670,9 @@ cudaError_t launch_ln_fwd(LnArgs a, int rows, int sms, void* stream) {
     const int need = (rows + groups - 1) / groups, most = sms * (1024 / th);
     const int grid = need < most ? need : most;
     const int smem = !VEC && a.drop.thr ? groups * ln_mask_bytes(a.H) : 0;
-    return api_launch(mode == kRowsWarp ? ln_fwd_kernel<VEC, kRowsWarp> : mode == kRowsGroup ? ln_fwd_kernel<VEC, kRowsGroup>
-                                                                        : ln_fwd_kernel<VEC, kRowsOne>,
-                      grid, th, smem, stream, a);
+    auto kernel = mode == kRowsWarp ? ln_fwd_kernel<VEC, kRowsWarp, 256> : mode == kRowsGroup ? ln_fwd_kernel<VEC, kRowsGroup, 256>
+                : th <= 256 ? ln_fwd_kernel<VEC, kRowsOne, 256> : ln_fwd_kernel<VEC, kRowsOne, 1024>;
+    return api_launch(kernel, grid, th, smem, stream, a);
 }
 
 struct LnLaunch {
