@@ -266,6 +266,8 @@ __device__ __forceinline__ void row_mask(Mask8 (&m)[norm_v(MODE)], const DropArg
 }
 
 __host__ __device__ constexpr int ln_mask_bytes(int H) { return (H + 7) / 8; }
+// Bytes of a staged row; with VEC whole vectors of all its threads (threads V).
+__host__ __device__ constexpr int ln_row_bytes(int H, bool vec, int vectors) { return vec ? vectors * 16 : norm_row_bytes(H, false); }
 
 // The mean first, then the squares of the distances from it: one pass over memory,
 // two sums over the row's threads.
@@ -316,16 +318,17 @@ __global__ void __launch_bounds__(MAXT) ln_fwd_kernel(const LnArgs p) {
         s2 = both(0.0f);
 #pragma unroll
         for (int j = 0; j < V; ++j)
+            {
+            const float mj = VEC && g.template col<VEC>(j, 0) >= H ? 0.0f : mean;  // 0 behind H, as z
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                z[j][i] = __fadd2_rn(z[j][i], both(-mean));
-                if (VEC) {
-                    if (g.template col<VEC>(j, 0) >= H) z[j][i] = both(0.0f);
-                } else {
+                z[j][i] = __fadd2_rn(z[j][i], both(-mj));
+                if (!VEC) {
                     if (g.template col<VEC>(j, 2 * i) >= H) z[j][i].x = 0.0f;
                     if (g.template col<VEC>(j, 2 * i + 1) >= H) z[j][i].y = 0.0f;
                 }
                 s2 = __ffma2_rn(z[j][i], z[j][i], s2);
+            }
             }
         s[0] = s2.x + s2.y;
         row_sums<1, MODE, MAXT>(s, red, g, n_sums);
@@ -370,7 +373,7 @@ __global__ void __launch_bounds__(MAXT, MAXT > 512 ? 1 : 512 / MAXT) ln_bwd_kern
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
     if (!ok) return;
     const int H = p.H, H2 = H * 2, groups = grp.groups(), bufs = p.bufs;
-    const int row_b = norm_row_bytes(H, VEC), par_b = grp.th() * V * 16;
+    const int row_b = ln_row_bytes(H, VEC, grp.th() * V), par_b = grp.th() * V * 16;
     const int ny = p.y ? 1 : 0, nd = p.d_x_out ? 1 : 0, A = 2 + ny + nd;  // staged: x, d_x_hat, y, d_x_out
     const int c0 = grp.template col<true>(0, 0), c1 = grp.template col<true>(1, 0);
     const bool in0 = c0 < H, in1 = V > 1 && c1 < H;  // VEC only
@@ -416,6 +419,11 @@ __global__ void __launch_bounds__(MAXT, MAXT > 512 ? 1 : 512 / MAXT) ln_bwd_kern
     };
     int buf = 0;
     const int step = gridDim.x * groups, t0 = blockIdx.x * groups;
+    if (VEC)  // what a thread has behind H stays zero
+        for (int a = 0; a < bufs * A; ++a) {
+            if (!in0) *reinterpret_cast<uint4*>(mine + a * row_b + c0 * 2) = make_uint4(0, 0, 0, 0);
+            if (V > 1 && !in1) *reinterpret_cast<uint4*>(mine + a * row_b + c1 * 2) = make_uint4(0, 0, 0, 0);
+        }
     if (bufs == 2) stage(t0 + grp.id(), 0);
 #pragma unroll
     for (int j = 0; j < V; ++j) {  // every thread reads back what it wrote (the groups write the same)
@@ -438,13 +446,29 @@ __global__ void __launch_bounds__(MAXT, MAXT > 512 ? 1 : 512 / MAXT) ln_bwd_kern
         for (int arr = 0; arr < 2; ++arr)
             if (p.want >> arr & 1)
 #pragma unroll
-                for (int j = 0; j < V; ++j)
+                for (int j = 0; j < V; ++j) {
+                    if (VEC) {
+                        float4* o = reinterpret_cast<float4*>(to + arr * H + (j ? c1 : c0));
+                        if (j ? in1 : in0)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 v = arr ? a_b[j][i >> 1] : a_g[j][i >> 1];
-                        const int c = grp.template col<VEC>(j, i);
-                        if (c < H) to[arr * H + c] = (i & 1 ? v.y : v.x) + (!meet && more ? to[arr * H + c] : 0.0f);
+                            for (int i = 0; i < 2; ++i) {
+                                const float2 v = arr ? a_b[j][2 * i] : a_g[j][2 * i], u = arr ? a_b[j][2 * i + 1] : a_g[j][2 * i + 1];
+                                float4 q = make_float4(v.x, v.y, u.x, u.y);
+                                if (!meet && more) {
+                                    const float4 was = o[i];
+                                    q = make_float4(q.x + was.x, q.y + was.y, q.z + was.z, q.w + was.w);
+                                }
+                                o[i] = q;
+                            }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 v = arr ? a_b[j][i >> 1] : a_g[j][i >> 1];
+                            const int c = grp.template col<VEC>(j, i);
+                            if (c < H) to[arr * H + c] = (i & 1 ? v.y : v.x) + (!meet && more ? to[arr * H + c] : 0.0f);
+                        }
                     }
+                }
         if (meet) {
             __syncthreads();
             for (int o = threadIdx.x; o < 2 * H; o += blockDim.x)
@@ -477,7 +501,7 @@ __global__ void __launch_bounds__(MAXT, MAXT > 512 ? 1 : 512 / MAXT) ln_bwd_kern
             const uint8_t* rows = mine + buf * A * row_b;
             const size_t off = static_cast<size_t>(t) * H;
             auto get = [&](int a, int j) -> uint4 {  // vector j of staged row a; zeros past H
-                if (VEC) return (j ? in1 : in0) ? *reinterpret_cast<const uint4*>(rows + a * row_b + (j ? c1 : c0) * 2) : make_uint4(0, 0, 0, 0);
+                if (VEC) return *reinterpret_cast<const uint4*>(rows + a * row_b + (j ? c1 : c0) * 2);
                 const uint16_t* r = reinterpret_cast<const uint16_t*>(rows + a * row_b + (reinterpret_cast<uintptr_t>(src[a] + off) & 15));
                 uint32_t w[4];
 #pragma unroll
@@ -530,12 +554,11 @@ __global__ void __launch_bounds__(MAXT, MAXT > 512 ? 1 : 512 / MAXT) ln_bwd_kern
             for (int j = 0; j < V; ++j) {
                 dh[j] = get(1, j);
                 const uint4 gm = *reinterpret_cast<const uint4*>(par + j * grp.th() * 16);
+                const float mj = VEC && !(j ? in1 : in0) ? 0.0f : mean;  // 0 behind H, as z
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    z[j][i] = __fadd2_rn(z[j][i], both(-mean));
-                    if (VEC) {
-                        if (!(j ? in1 : in0)) z[j][i] = both(0.0f);
-                    } else {
+                    z[j][i] = __fadd2_rn(z[j][i], both(-mj));
+                    if (!VEC) {
                         if (grp.template col<VEC>(j, 2 * i) >= H) z[j][i].x = 0.0f;
                         if (grp.template col<VEC>(j, 2 * i + 1) >= H) z[j][i].y = 0.0f;
                     }
@@ -578,14 +601,17 @@ __global__ void __launch_bounds__(MAXT, MAXT > 512 ? 1 : 512 / MAXT) ln_bwd_kern
         }
         if (!VEC) grp.sync();  // this buffer and the mask's bytes are written again
         if (bufs == 2) buf ^= 1;
-        if (++chain == kLnChain && p.want) {
+        if (p.want && (++chain == kLnChain || r0 + step >= T)) {
             put_away(more);
             more = true;
             chain = 0;
         }
     }
     cp_async_wait<0>();
-    if (p.want && (chain || !more)) put_away(more);
+    if (p.want && !more) {  // no rows: zeros
+        float* part = p.part + static_cast<size_t>(blockIdx.x) * 2 * H;
+        for (int o = threadIdx.x; o < 2 * H; o += blockDim.x) part[o] = 0.0f;
+    }
 }
 
 struct LnSumArgs {
@@ -693,7 +719,7 @@ cudaError_t launch_ln_bwd_rows(LnArgs a, const LnLaunch& l) {
     *l.parts = n = n < most ? n : most;
     const int A = 2 + (a.y ? 1 : 0) + (a.d_x_out ? 1 : 0);
     a.bufs = a.H <= 8192 ? 2 : 1;
-    const int smem = groups * a.bufs * A * norm_row_bytes(a.H, VEC) + a.row_threads * norm_v(MODE) * 16 +
+    const int smem = groups * a.bufs * A * ln_row_bytes(a.H, VEC, a.row_threads * norm_v(MODE)) + a.row_threads * norm_v(MODE) * 16 +
                      (MODE != kRowsOne && groups > 1 ? groups * 2 * a.H * 4 : 0) +
                      (!VEC && a.drop.thr ? groups * ln_mask_bytes(a.H) : 0);
     return api_launch(kernel, n, th, smem, l.stream, a);
