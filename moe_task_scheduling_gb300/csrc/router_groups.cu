@@ -22,7 +22,7 @@ struct GroupArgs {
     int G, kg, best;         // groups, how many take part, whose `best` experts rank them
     int gs;                  // experts a group
     int lanes;               // lanes that hold a group where that is a power of two, else 0
-    int sigmoid, renorm;
+    int renorm, vec;
     float scale;
     RouterSums sums;
 };
@@ -39,37 +39,37 @@ __device__ __forceinline__ unsigned long long value_key(double v) {
 }
 
 // The whole choice in 64 bits, for the rows where 32 cannot tell.  Lane `lane` has the
-// logits of experts lane * EPL + i.  Returns lane j's expert, the j-th, or -1.
+// experts lane * EPL + i.  Returns lane j's expert, the j-th, or -1.
 // Out of line and in plain loops: one row in some hundreds comes here.
 template <int EPL>
-struct LaneLogits { float v[EPL]; };
-template <int EPL>
-__device__ __noinline__ int choose64(LaneLogits<EPL> row, const float* bias, int E, int k, int G, int kg, int best, int gs,
+__device__ __noinline__ int choose64(const float* row, const float* bias, int E, int k, int G, int kg, int best, int gs,
                                      int sigmoid, int lane) {
     constexpr uint32_t kAll = 0xffffffffu;
     unsigned long long key[EPL];  // of score + bias; 0: not available
+    float v[EPL];
     double m = 0.0, Z = 1.0;
-    if (!sigmoid) {
-        float top = row.v[0];
 #pragma unroll
-        for (int i = 1; i < EPL; ++i) top = fmaxf(top, row.v[i]);
+    for (int i = 0; i < EPL; ++i) v[i] = lane * EPL + i < E ? row[lane * EPL + i] : -INFINITY;
+    if (!sigmoid) {
+        float top = v[0];
+#pragma unroll
+        for (int i = 1; i < EPL; ++i) top = fmaxf(top, v[i]);
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
         m = top;
         Z = 0.0;
 #pragma unroll 1
-        for (int i = 0; i < EPL; ++i) Z += exp(static_cast<double>(row.v[i]) - m);  // 0 past E
+        for (int i = 0; i < EPL; ++i) Z += exp(static_cast<double>(v[i]) - m);  // 0 past E
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) Z += __shfl_xor_sync(kAll, Z, off);
     }
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        const int e = lane * EPL + i;
-        const double x = row.v[i];
+        const double x = v[i];
         key[i] = 0;
-        if (e < E && !(row.v[i] == -INFINITY)) {
-            const double s = sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - m) / Z;
-            const double c = bias ? s + static_cast<double>(bias[e]) : s;
+        if (!(v[i] == -INFINITY)) {
+            double c = sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - m) / Z;
+            if (bias) c += static_cast<double>(bias[lane * EPL + i]);
             if (!(c == -INFINITY)) key[i] = value_key(c);
         }
     }
@@ -138,138 +138,196 @@ __device__ __noinline__ int choose64(LaneLogits<EPL> row, const float* bias, int
     return mineE;
 }
 
-// The float of a key as logit_key made it, -inf for 0.
-__device__ __forceinline__ float key_or_none(uint32_t key) { return key ? key_logit(key) : -INFINITY; }
+constexpr uint32_t kNegInfKey = 0x007fffffu;  // logit_key(-inf); nothing available has it or less
+
+__device__ __forceinline__ float rcp_fast(float x) {  // within 1 ulp; 0 for +inf
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float sigmoid_fast(float v) { return rcp_fast(1.0f + __expf(-v)); }  // 0 for -inf
+
+// The float of a key, -inf where nothing is available.
+__device__ __forceinline__ float key_or_none(uint32_t key) { return key > kNegInfKey ? key_logit(key) : -INFINITY; }
+
+// logit_key of a score (>= 0 or NaN).  In assembly: as C++ it became a negation, which makes
+// the one positive NaN of -NaN.
+__device__ __forceinline__ uint32_t score_key(float s) {
+    uint32_t k;
+    asm("or.b32 %0, %1, 0x80000000;" : "=r"(k) : "r"(__float_as_uint(s)));
+    return k;
+}
+
+// Sorts a lane's keys, the largest first.
+template <int EPL>
+__device__ __forceinline__ void sort_keys(uint32_t (&k)[EPL]) {
+    auto swap = [&](int a, int b) {
+        const uint32_t hi = max(k[a], k[b]);
+        k[b] = min(k[a], k[b]);
+        k[a] = hi;
+    };
+    // odd-even merge sort
+    if (EPL == 2) swap(0, 1);
+    if (EPL >= 4) {
+#pragma unroll
+        for (int o = 0; o + 3 < EPL; o += 4) {
+            swap(o, o + 1); swap(o + 2, o + 3);
+            swap(o, o + 2); swap(o + 1, o + 3);
+            swap(o + 1, o + 2);
+        }
+    }
+    if (EPL == 8) {
+        swap(0, 4 % EPL); swap(1 % EPL, 5 % EPL); swap(2 % EPL, 6 % EPL); swap(3 % EPL, 7 % EPL);
+        swap(2 % EPL, 4 % EPL); swap(3 % EPL, 5 % EPL);
+        swap(1 % EPL, 2 % EPL); swap(3 % EPL, 4 % EPL); swap(5 % EPL, 6 % EPL);
+    }
+}
 
 // One row a warp, experts lane * EPL + i in register i, so that a group is a few
 // neighbouring lanes.  The choice runs on 32-bit values: without a bias on the logits,
 // which order as the scores do and are exact; with one on score + bias, whose error has a
-// bound.  Where two neighbours in the order, or the last group that takes part and
-// the next, are no farther apart than both errors, the row is chosen again in 64 bits.
-template <int EPL>
+// bound.  A lane's keys, cut by the bits that name its experts, are sorted once; a round
+// of the choice looks at the heads alone, and takes the lowest lane of those with the
+// largest cut key.  Where two neighbours in the order are no farther apart than the cut
+// and both errors, or the last group that takes part and the next than theirs, the row is
+// chosen again in 64 bits.
+template <int EPL, bool SIGMOID>
 __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(const GroupArgs p) {
-    constexpr uint32_t kAll = 0xffffffffu;
+    constexpr uint32_t kAll = 0xffffffffu, kLow = EPL - 1;
     constexpr float kU = 1.0f / (1 << 24);
     extern __shared__ __align__(16) float sm[];  // [warps][E], then the last CTA's sums
     __shared__ RouterShared sh;
+    __shared__ uint32_t chosen[kRouterWarpsMax][16];
+    __shared__ float bias_s[kRouterEMax];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-    const int E = p.E, k = p.k;
+    const int E = p.E, k = p.k, e0 = lane * EPL;
+    const uint32_t below = (1u << lane) - 1;
     grid_begin();
     bool ok;
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.sums.hdr, &ok);
     if (!ok) return;
     const int t0 = blockIdx.x + gridDim.x * warp, step = gridDim.x * nwarps;
     auto load = [&](int t, float (&v)[EPL], int& on) {
-        const float* L = p.logits + static_cast<size_t>(t) * E;
+        const float* L = p.logits + static_cast<size_t>(t) * E + e0;
         on = t < T && (!p.mask || p.mask[t] != 0);
+        if (EPL >= 4 && p.vec) {  // E a multiple of 4, rows 16-byte aligned
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) v[i] = t < T && lane * EPL + i < E ? L[lane * EPL + i] : -INFINITY;
+            for (int i = 0; i < EPL; i += 4) {
+                float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                if (t < T && e0 + i < E) q = *reinterpret_cast<const float4*>(L + i);
+                v[i] = q.x;
+                v[(i + 1) % EPL] = q.y;
+                v[(i + 2) % EPL] = q.z;
+                v[(i + 3) % EPL] = q.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) v[i] = t < T && e0 + i < E ? L[i] : -INFINITY;
+        }
     };
-    float nv[EPL], bias[EPL];
+    float nv[EPL];
     int non;
     load(t0, nv, non);
+    for (int e = threadIdx.x; e < kRouterEMax; e += blockDim.x) {
+        if (e < E) sh.hist[e] = 0;
+        bias_s[e] = p.bias && e < E ? p.bias[e] : 0.0f;
+    }
+    float* const big = sm + warp * E + e0;  // this lane's sums of whole batches of 32 rows
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) bias[i] = p.bias && lane * EPL + i < E ? p.bias[lane * EPL + i] : 0.0f;
-    for (int e = threadIdx.x; e < E; e += blockDim.x) sh.hist[e] = 0;
+    for (int i = 0; i < EPL; ++i)
+        if (e0 + i < E) big[i] = 0.0f;
     __syncthreads();
 
-    float accp[EPL], bigp[EPL];
+    float accp[EPL];
     int accn = 0, rows32 = 0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) accp[i] = bigp[i] = 0.0f;
+    for (int i = 0; i < EPL; ++i) accp[i] = 0.0f;
 
     for (int t = t0; t < T; t += step) {
-        float v[EPL];
+        float v[EPL], s[EPL], S = 0.0f, top = 0.0f;
         const int masked_in = non;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) v[i] = nv[i];
         load(t + step, nv, non);
 
         // scores s, their sum S
-        float s[EPL], S = 0.0f, top = v[0];
+        if (!SIGMOID) {
+            top = v[0];
 #pragma unroll
-        for (int i = 1; i < EPL; ++i) top = fmaxf(top, v[i]);
+            for (int i = 1; i < EPL; ++i) top = fmaxf(top, v[i]);
 #pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
+            for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
+        }
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            s[i] = p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-v[i])) : __expf(v[i] - top);
-            if (v[i] == -INFINITY) s[i] = 0.0f;
+            s[i] = SIGMOID ? sigmoid_fast(v[i]) : v[i] == -INFINITY ? 0.0f : __expf(v[i] - top);
             S += s[i];
         }
         S = warp_sum(S);
         const float inv = __fdividef(1.0f, S);
-        float smax = 1.0f;  // no score is larger
-        if (!p.sigmoid) {
-            smax = inv;
+        if (!SIGMOID) {
 #pragma unroll
             for (int i = 0; i < EPL; ++i) s[i] *= inv;
         }
-        // How far a score can be off: sigmoid 6.3 x 2^-24 (exp within 2 + 1.2 |x| ulp, times
-        // the slope e^x / (1 + e^x)^2 <= 1/4; an add; a quotient within 2 ulp), softmax 40 x
-        // 2^-24 of the largest (its sum's terms are off by 8.5 ulp on average at most, as
-        // their mean |x - top| is below log 256).
-        const float err = (p.sigmoid ? 10.0f : 48.0f * smax) * kU;
+        // How far a score can be off: sigmoid 6 x 2^-24 (exp within 2 + 1.2 |x| ulp, times the
+        // slope e^x / (1 + e^x)^2 <= 1/4; an add; a reciprocal within 1 ulp), softmax 40 x 2^-24
+        // of the largest, 1 / S (its sum's terms are off by 8.5 ulp on average at most, as their
+        // mean |x - top| is below log 256).
+        const float err = (SIGMOID ? 10.0f : 48.0f * inv) * kU;
 
-        uint32_t key[EPL];  // 0: not available
+        uint32_t key[EPL];  // kNegInfKey or 0: not available
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            const float c = p.bias ? __fadd_rn(s[i], bias[i]) : v[i];
-            const bool there = lane * EPL + i < E && !(v[i] == -INFINITY) && !(c == -INFINITY);
-            key[i] = there ? logit_key(c) : 0u;
+            float c = v[i];
+            if (p.bias) c = v[i] == -INFINITY ? v[i] : __fadd_rn(s[i], bias_s[e0 + i]);
+            key[i] = logit_key(c);
         }
         bool doubt = false;
         if (p.kg < p.G) {
-            // a group's best two values of score + bias
-            float score = -INFINITY;  // lane g: of group g
-            float mag = 0.0f;
-            auto group_score = [&](float hi, float lo, bool has_lo) { return hi + (p.best > 1 && has_lo ? lo : 0.0f); };
+            float score = -INFINITY, mag = 0.0f;  // lane g: of group g
+            auto group_score = [&](uint32_t hi, uint32_t lo) {  // from its best two values of score + bias
+                const float h = key_or_none(hi), l = lo > kNegInfKey ? key_logit(lo) : 0.0f;
+                score = h + (p.best > 1 ? l : 0.0f);
+                mag = fabsf(h) + fabsf(l);
+            };
+            uint32_t hi = 0, lo = 0;
             if (p.lanes) {
-                uint32_t hi = 0, lo = 0;
 #pragma unroll
                 for (int i = 0; i < EPL; ++i) {
-                    const uint32_t c = p.bias ? key[i] : key[i] ? logit_key(s[i]) : 0u;
+                    const uint32_t c = p.bias || key[i] <= kNegInfKey ? key[i] : score_key(s[i]);
                     lo = max(lo, min(hi, c));
                     hi = max(hi, c);
                 }
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
+                for (int off = 1; off < p.lanes; off <<= 1) {
                     const uint32_t h = __shfl_xor_sync(kAll, hi, off), l = __shfl_xor_sync(kAll, lo, off);
-                    if (off < p.lanes) {
-                        lo = max(max(lo, l), min(hi, h));
-                        hi = max(hi, h);
-                    }
+                    lo = max(max(lo, l), min(hi, h));
+                    hi = max(hi, h);
                 }
                 const int from = min(lane * p.lanes, 31);
                 hi = __shfl_sync(kAll, hi, from);
                 lo = __shfl_sync(kAll, lo, from);
-                if (lane < p.G) {
-                    score = group_score(key_or_none(hi), key_or_none(lo), lo != 0);
-                    mag = fabsf(key_or_none(hi)) + fabsf(lo ? key_logit(lo) : 0.0f);
-                }
             } else {
 #pragma unroll 1
                 for (int g = 0; g < p.G; ++g) {
-                    uint32_t hi = 0, lo = 0;
+                    uint32_t h = 0, l = 0;
 #pragma unroll
                     for (int i = 0; i < EPL; ++i) {
-                        const int e = lane * EPL + i;
-                        const bool in = e >= g * p.gs && e < g * p.gs + p.gs && key[i];
-                        const uint32_t c = !in ? 0u : p.bias ? key[i] : logit_key(s[i]);
-                        lo = max(lo, min(hi, c));
-                        hi = max(hi, c);
+                        const bool in = e0 + i >= g * p.gs && e0 + i < g * p.gs + p.gs;
+                        const uint32_t c = !in ? 0u : p.bias || key[i] <= kNegInfKey ? key[i] : score_key(s[i]);
+                        l = max(l, min(h, c));
+                        h = max(h, c);
                     }
-                    const uint32_t H = __reduce_max_sync(kAll, hi);
+                    const uint32_t H = __reduce_max_sync(kAll, h);
                     // its holder's second best (the first holder's, where several hold it)
-                    const uint32_t who = __ballot_sync(kAll, hi == H);
-                    const bool first = lane == __ffs(who) - 1;
-                    const uint32_t L = __reduce_max_sync(kAll, first ? lo : hi);
+                    const uint32_t who = __ballot_sync(kAll, h == H);
+                    const uint32_t L = __reduce_max_sync(kAll, lane == __ffs(who) - 1 ? l : h);
                     if (lane == g) {
-                        score = group_score(key_or_none(H), key_or_none(L), L != 0);
-                        mag = fabsf(key_or_none(H)) + fabsf(L ? key_logit(L) : 0.0f);
+                        hi = H;
+                        lo = L;
                     }
                 }
             }
+            if (lane < p.G) group_score(hi, lo);
             const uint32_t mine = logit_key(score);
             int rank = 0;
 #pragma unroll 4
@@ -285,69 +343,80 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
             const float a = __shfl_sync(kAll, score, __ffs(last_in) - 1), b = __shfl_sync(kAll, score, __ffs(next) - 1);
             const float tol = 2.0f * __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(off_by)));
             doubt = !(a - b > tol) && !(b == -INFINITY);
+            if (p.lanes) {
+                const bool out = !(in >> (lane / p.lanes & 31) & 1);
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const int e = lane * EPL + i;
-                const int g = p.lanes ? lane / p.lanes : e / p.gs;
-                if (!(in >> (g & 31) & 1)) key[i] = 0u;
+                for (int i = 0; i < EPL; ++i) key[i] = out ? 0u : key[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if (!(in >> ((e0 + i) / p.gs & 31) & 1)) key[i] = 0u;
             }
         }
-        // the best k, and with a bias the next one too; lane j: the j-th
-        auto next_best = [&](uint32_t& kmax, int& e) {
-            uint32_t bk = key[0];
+
+        // the best k and the next one; lane j: the j-th
 #pragma unroll
-            for (int i = 1; i < EPL; ++i) bk = max(bk, key[i]);
-            kmax = __reduce_max_sync(kAll, bk);
-            uint32_t low = 0xffffffffu;
+        for (int i = 0; i < EPL; ++i) key[i] = (key[i] & ~kLow) | (kLow - i);
+        sort_keys<EPL>(key);
+        auto take = [&](int j) -> uint32_t {  // the largest cut key; its expert goes to chosen[j]
+            const uint32_t best = __reduce_max_sync(kAll, key[0]);
+            const bool mine = (key[0] ^ best) <= kLow;
+            const uint32_t who = __ballot_sync(kAll, mine);
+            if (mine && !(who & below)) {
+                chosen[warp][j] = e0 + (kLow - (key[0] & kLow));
 #pragma unroll
-            for (int i = EPL - 1; i >= 0; --i)
-                if (key[i] == kmax) low = static_cast<uint32_t>(lane * EPL + i);
-            e = static_cast<int>(__reduce_min_sync(kAll, low));
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (lane * EPL + i == e) key[i] = 0u;
+                for (int i = 0; i < EPL; ++i) key[i] = i + 1 < EPL ? key[(i + 1) % EPL] : 0u;
+            }
+            return best;
         };
         uint32_t mykey = 0;
-        int myE = 0;
-        const int rounds = p.bias ? k + 1 : k;
 #pragma unroll 1
-        for (int j = 0; j < rounds; ++j) {
-            uint32_t kmax;
-            int e;
-            next_best(kmax, e);
-            if (lane == j) {
-                mykey = kmax;
-                myE = e;
-            }
+        for (int j = 0; j <= k; ++j) {
+            const uint32_t best = take(j);
+            if (lane == j) mykey = best;
         }
+        __syncwarp();
         const float* row = p.logits + static_cast<size_t>(t) * E;
-        bool on = lane < k && mykey != 0;
-        float myL = mykey ? row[myE] : -INFINITY;
-        if (p.bias) {
-            const float c = key_or_none(mykey), b = mykey ? p.bias[myE] : 0.0f;
+        const bool there = lane <= k && mykey > (kNegInfKey | kLow);
+        bool on = lane < k && there;
+        int myE = there ? static_cast<int>(chosen[warp][lane & 15]) : 0;
+        float myL = there ? row[myE] : -INFINITY;
+        {
+            const float b = there ? bias_s[myE] : 0.0f;
+            // score + bias as above
+            const float c = !there ? -INFINITY : !p.bias ? myL : __fadd_rn(SIGMOID ? sigmoid_fast(myL) : __expf(myL - top) * inv, b);
             const float cn = __shfl_down_sync(kAll, c, 1), bn = __shfl_down_sync(kAll, b, 1), Ln = __shfl_down_sync(kAll, myL, 1);
-            const bool there = __shfl_down_sync(kAll, mykey, 1) != 0;
+            const uint32_t keyn = __shfl_down_sync(kAll, mykey, 1);
             const bool equal = b == bn && myL == Ln;  // a true tie, in the order of the experts already
-            const float tol = 2.0f * err + kU * (fabsf(c) + fabsf(cn));
-            doubt |= __any_sync(kAll, on && there && !equal && !(c - cn > tol));
+            // with a bias: both errors and the cut; without: the order is the whole key's unless
+            // the cut key is one, or the scores meet at 1 or 0 in 64 bits
+            const float tol = 2.0f * err + (kU + 2.0f * EPL * kU) * (fabsf(c) + fabsf(cn));
+            const bool meet = SIGMOID ? Ln > 16.0f || Ln < -700.0f : Ln - top < -700.0f;
+            const bool close = p.bias ? !(c - cn > tol) : meet || ((mykey ^ keyn) <= kLow && (c < cn || c != c || lane == k - 1));
+            const bool pair = on && keyn > (kNegInfKey | kLow);
+            doubt |= __any_sync(kAll, pair && !equal && close);
             // after a true tie across the k-th place, whoever comes next must be apart from it, too
-            bool tie = __ballot_sync(kAll, on && there && equal) >> (k - 1) & 1;
+            bool tie = __ballot_sync(kAll, pair && equal) >> (k - 1) & 1;
             while (tie && !doubt) {
-                uint32_t kmax;
-                int e;
-                next_best(kmax, e);
-                const float Lk = __shfl_sync(kAll, myL, k - 1), bk = __shfl_sync(kAll, b, k - 1);
-                const float ck = __shfl_sync(kAll, c, k - 1), tk = __shfl_sync(kAll, tol, k - 1);
-                const bool same = kmax && row[e] == Lk && p.bias[e] == bk;
-                doubt = kmax && !same && !(ck - key_or_none(kmax) > tk);
-                tie = same;
+                const float Lk = __shfl_sync(kAll, myL, k - 1), bk = __shfl_sync(kAll, b, k - 1), ck = __shfl_sync(kAll, c, k - 1);
+                const uint32_t keyk = __shfl_sync(kAll, mykey, k - 1);
+                const uint32_t best = take(k);
+                __syncwarp();
+                const int e = static_cast<int>(chosen[warp][k]);
+                __syncwarp();
+                tie = false;
+                if (best > (kNegInfKey | kLow)) {
+                    const float L = row[e];
+                    tie = L == Lk && bias_s[e] == bk;
+                    if (!tie) {
+                        const float x = p.bias ? key_logit(best | kLow) : L;  // at least its value
+                        doubt = p.bias ? !(ck - x > 2.0f * err + (4.0f * EPL + 2.0f) * kU * fabsf(ck)) : (keyk ^ best) <= kLow;
+                    }
+                }
             }
         }
         if (doubt) {
-            LaneLogits<EPL> lr;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) lr.v[i] = v[i];
-            myE = choose64<EPL>(lr, p.bias, E, k, p.G, p.kg, p.best, p.gs, p.sigmoid, lane);
+            myE = choose64<EPL>(row, p.bias, E, k, p.G, p.kg, p.best, p.gs, SIGMOID, lane);
             on = lane < k && myE >= 0;
             myL = on ? row[myE] : -INFINITY;
         }
@@ -359,23 +428,21 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
 #pragma unroll
         for (int off = 4; off >= 1; off >>= 1) Lm = fmaxf(Lm, __shfl_xor_sync(kAll, Lm, off));
         Lm = __shfl_sync(kAll, Lm, 0);
-        float x = 0.0f;
+        float x = 0.0f, z = 1.0f;
         if (on) {
-            if (p.renorm) x = !p.sigmoid || Lm < -60.0f ? expf(myL - Lm) : 1.0f / (1.0f + expf(-myL));
-            else x = p.sigmoid ? 1.0f / (1.0f + expf(-myL)) : expf(myL - top);
-            if (!p.sigmoid && S != S) x = S;  // a NaN or infinite logit shows, chosen or not
+            if (p.renorm) x = !SIGMOID || Lm < -60.0f ? expf(myL - Lm) : 1.0f / (1.0f + expf(-myL));
+            else x = SIGMOID ? 1.0f / (1.0f + expf(-myL)) : expf(myL - top);
+            if (!SIGMOID && S != S) x = S;  // a NaN or infinite logit shows, chosen or not
         }
-        float z = 0.0f;
         if (p.renorm) {
             z = x;
 #pragma unroll
             for (int off = 4; off >= 1; off >>= 1) z += __shfl_xor_sync(kAll, z, off);
-        } else if (!p.sigmoid) {
+        } else if (!SIGMOID) {
+            z = 0.0f;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) z += v[i] == -INFINITY ? 0.0f : expf(v[i] - top);
             z = warp_sum(z);
-        } else {
-            z = 1.0f;
         }
         if (lane < k) {
             p.idx[static_cast<size_t>(t) * k + lane] = on ? myE : -1;
@@ -383,32 +450,38 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
         }
         if (on) atomicAdd(&sh.hist[myE], 1);
         if (live) {
-            if (p.sigmoid && top < -60.0f) {  // scores as small as that: their ratios
-                float q = 0.0f;
+            float q = SIGMOID ? inv : 1.0f;
+            if (SIGMOID && !(S >= 1e-24f) && S == S) {  // scores as small as that (all below e^-55): their ratios
+                top = v[0];
+#pragma unroll
+                for (int i = 1; i < EPL; ++i) top = fmaxf(top, v[i]);
+#pragma unroll
+                for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
+                q = 0.0f;
 #pragma unroll
                 for (int i = 0; i < EPL; ++i) {
                     s[i] = v[i] == -INFINITY ? 0.0f : __expf(v[i] - top);
                     q += s[i];
                 }
                 q = __fdividef(1.0f, warp_sum(q));
-#pragma unroll
-                for (int i = 0; i < EPL; ++i) accp[i] += s[i] * q;
-            } else {
-                const float q = p.sigmoid ? inv : 1.0f;
-#pragma unroll
-                for (int i = 0; i < EPL; ++i) accp[i] += s[i] * q;
             }
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) accp[i] += s[i] * q;
             ++accn;
         }
         if (++rows32 == 32) {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) { bigp[i] += accp[i]; accp[i] = 0.0f; }
+            for (int i = 0; i < EPL; ++i) {
+                if (e0 + i < E) big[i] += accp[i];
+                accp[i] = 0.0f;
+            }
             rows32 = 0;
         }
+        __syncwarp();  // `chosen` is written again
     }
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-        if (lane * EPL + i < E) sm[warp * E + lane * EPL + i] = bigp[i] + accp[i];
+        if (e0 + i < E) big[i] += accp[i];
     router_sums(p.sums, sm, sh, E, k, 0.0f, accn);
 }
 
@@ -584,11 +657,13 @@ int et_router_groups(const float* logits, const float* bias, const uint8_t* toke
         const int epl = E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : 8, gs = E / n_groups;
         const int lanes = gs % epl ? 0 : gs / epl;
         const GroupArgs a{logits, bias, token_mask, topk_idx, topk_w, d_T, T, T_max, E, k, n_groups, k_groups, group_best, gs,
-                          lanes & (lanes - 1) ? 0 : lanes, score == ET_SCORE_SIGMOID, renorm != 0, scale,
+                          lanes & (lanes - 1) ? 0 : lanes, renorm != 0, E % 4 == 0 && api_aligned(logits, 16), scale,
                           router_sums_args(workspace, L, expert_counts, n_routed, mean_prob, loss, false)};
         const RouterGrid g = router_grid(d_T ? T_max : T > 0 ? T : 1, E);
-        auto kernel = epl == 1 ? router_groups_kernel<1> : epl == 2 ? router_groups_kernel<2>
-                    : epl == 4 ? router_groups_kernel<4> : router_groups_kernel<8>;
+        auto pick = [&](auto one, auto two, auto four, auto eight) { return epl == 1 ? one : epl == 2 ? two : epl == 4 ? four : eight; };
+        auto kernel = score == ET_SCORE_SIGMOID
+            ? pick(router_groups_kernel<1, true>, router_groups_kernel<2, true>, router_groups_kernel<4, true>, router_groups_kernel<8, true>)
+            : pick(router_groups_kernel<1, false>, router_groups_kernel<2, false>, router_groups_kernel<4, false>, router_groups_kernel<8, false>);
         const cudaError_t e = api_launch(kernel, g.ctas, g.warps * 32, g.smem, stream, a);
         if (e != cudaSuccess) return api_fail_cuda(e, "launch of the grouped router kernel");
         return ET_OK;
