@@ -183,21 +183,80 @@ __device__ __forceinline__ void sort_keys(uint32_t (&k)[EPL]) {
     }
 }
 
+constexpr int kCandidates = 16;  // experts whose order is looked at again at most
+
+// score + bias in 64 bits, without a bias and with softmax scores the logit, which orders alike.
+__device__ __forceinline__ double value64(float x, float b, bool sigmoid) {
+    return sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(x))) + static_cast<double>(b) : static_cast<double>(x);
+}
+
+// Two groups whose scores 32 bits cannot tell apart: 1 if the first has the larger, or the
+// same and the lower number, 0 if the second, -1 if it takes more than their best two to
+// say.  Sigmoid scores.  floor_a, floor_b: what the experts that count are not below;
+// want_a, want_b: how many those are.  slots: 16 places of shared memory.
+template <int EPL>
+__device__ __noinline__ int compare_groups(const float* row, const float* bias_s, int E, int gs, int a, int b, float floor_a,
+                                           float floor_b, int want_a, int want_b, uint32_t* slots, int lane) {
+    constexpr uint32_t kAll = 0xffffffffu;
+    int na = 0, nb = 0;
+#pragma unroll 1
+    for (int i = 0; i < EPL; ++i) {
+        const int e = lane * EPL + i, g = e / gs;
+        const float x = e < E ? row[e] : -INFINITY;
+        const float c = x == -INFINITY ? x : __fadd_rn(sigmoid_fast(x), bias_s[min(e, E - 1)]);
+        const uint32_t in_a = __ballot_sync(kAll, e < E && g == a && c >= floor_a);
+        const uint32_t in_b = __ballot_sync(kAll, e < E && g == b && c >= floor_b);
+        const uint32_t bit = 1u << lane, below = bit - 1;
+        if ((in_a & bit) && na + __popc(in_a & below) < 8) slots[na + __popc(in_a & below)] = e;
+        if ((in_b & bit) && nb + __popc(in_b & below) < 8) slots[8 + nb + __popc(in_b & below)] = e;
+        na += __popc(in_a);
+        nb += __popc(in_b);
+    }
+    __syncwarp();
+    if (na != want_a || nb != want_b) return -1;
+    const bool mine = lane < na || (lane >= 8 && lane < 8 + nb);
+    const int e = mine ? static_cast<int>(slots[lane]) : 0;
+    double c = mine ? value64(row[e], bias_s[e], true) : 0.0;
+    c += __shfl_xor_sync(kAll, c, 1);  // two at most
+    const double sa = __shfl_sync(kAll, c, 0), sb = __shfl_sync(kAll, c, 8);
+    return sa > sb || (sa == sb && a < b) ? 1 : 0;
+}
+
+// The order of n candidates (n <= kCandidates, their experts in slots) in 64 bits: puts the
+// best k there in their order.
+__device__ __noinline__ void order_again(const float* row, const float* bias_s, bool sigmoid, int n, int k, uint32_t* slots, int lane) {
+    constexpr uint32_t kAll = 0xffffffffu;
+    const int e = lane < n ? static_cast<int>(slots[lane]) : 0;
+    const double c = lane < n ? value64(row[e], bias_s[e], sigmoid) : 0.0;
+    const unsigned long long key = value_key(c);
+    int rank = 0;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        const unsigned long long other = __shfl_sync(kAll, key, i);
+        const int oe = __shfl_sync(kAll, e, i);
+        rank += other > key || (other == key && oe < e);
+    }
+    __syncwarp();
+    if (lane < n && rank < k) slots[rank] = e;
+    __syncwarp();
+}
+
 // One row a warp, experts lane * EPL + i in register i, so that a group is a few
 // neighbouring lanes.  The choice runs on 32-bit values: without a bias on the logits,
 // which order as the scores do and are exact; with one on score + bias, whose error has a
 // bound.  A lane's keys, cut by the bits that name its experts, are sorted once; a round
 // of the choice looks at the heads alone, and takes the lowest lane of those with the
 // largest cut key.  Where two neighbours in the order are no farther apart than the cut
-// and both errors, or the last group that takes part and the next than theirs, the row is
-// chosen again in 64 bits.
+// and both errors, or the last group that takes part and the next than theirs, 64 bits
+// decide: on the candidates alone (a lane each: 1.3 us where a whole row takes 14), and on
+// the whole row if they are too many, or softmax scores with a bias.
 template <int EPL, bool SIGMOID>
 __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(const GroupArgs p) {
     constexpr uint32_t kAll = 0xffffffffu, kLow = EPL - 1;
     constexpr float kU = 1.0f / (1 << 24);
     extern __shared__ __align__(16) float sm[];  // [warps][E], then the last CTA's sums
     __shared__ RouterShared sh;
-    __shared__ uint32_t chosen[kRouterWarpsMax][16];
+    __shared__ uint32_t chosen[kRouterWarpsMax][kCandidates];
     __shared__ float bias_s[kRouterEMax];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
     const int E = p.E, k = p.k, e0 = lane * EPL;
@@ -282,7 +341,7 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
             if (p.bias) c = v[i] == -INFINITY ? v[i] : __fadd_rn(s[i], bias_s[e0 + i]);
             key[i] = logit_key(c);
         }
-        bool doubt = false;
+        bool again = false;  // the whole row in 64 bits
         if (p.kg < p.G) {
             float score = -INFINITY, mag = 0.0f;  // lane g: of group g
             auto group_score = [&](uint32_t hi, uint32_t lo) {  // from its best two values of score + bias
@@ -335,14 +394,30 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
                 const uint32_t other = __shfl_sync(kAll, mine, g);
                 rank += other > mine || (other == mine && g < lane);
             }
-            const uint32_t in = __ballot_sync(kAll, lane < p.G && rank < p.kg);
+            uint32_t in = __ballot_sync(kAll, lane < p.G && rank < p.kg);
             // the last that takes part and the next: apart by more than any two may be off
             const uint32_t last_in = __ballot_sync(kAll, lane < p.G && rank == p.kg - 1);
             const uint32_t next = __ballot_sync(kAll, lane < p.G && rank == p.kg);
             const float off_by = 2.0f * err + 2.0f * kU * mag;
             const float a = __shfl_sync(kAll, score, __ffs(last_in) - 1), b = __shfl_sync(kAll, score, __ffs(next) - 1);
             const float tol = 2.0f * __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(off_by)));
-            doubt = !(a - b > tol) && !(b == -INFINITY);
+            if (!(a - b > tol) && !(b == -INFINITY)) {
+                const int ga = __ffs(last_in) - 1, gb = __ffs(next) - 1;
+                // between these two alone?
+                const bool other = lane < p.G && !(rank < p.kg - 1 ? score - b > tol : rank > p.kg ? a - score > tol : true);
+                again = !SIGMOID || !(tol < 1.0f) || __any_sync(kAll, other);
+                if (!again) {
+                    const uint32_t last = p.best > 1 && lo > kNegInfKey ? lo : hi;  // the last that counts
+                    const float floor = key_or_none(last) - tol;
+                    const int want = last == hi && (p.best == 1 || lo <= kNegInfKey) ? 1 : 2;
+                    const int r = compare_groups<EPL>(p.logits + static_cast<size_t>(t) * E, bias_s, E, p.gs, ga, gb,
+                                                      __shfl_sync(kAll, floor, ga), __shfl_sync(kAll, floor, gb),
+                                                      __shfl_sync(kAll, want, ga), __shfl_sync(kAll, want, gb), chosen[warp], lane);
+                    again = r < 0;
+                    if (r == 0) in ^= 1u << ga | 1u << gb;
+                    __syncwarp();
+                }
+            }
             if (p.lanes) {
                 const bool out = !(in >> (lane / p.lanes & 31) & 1);
 #pragma unroll
@@ -394,11 +469,14 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
             const bool meet = SIGMOID ? Ln > 16.0f || Ln < -700.0f : Ln - top < -700.0f;
             const bool close = p.bias ? !(c - cn > tol) : meet || ((mykey ^ keyn) <= kLow && (c < cn || c != c || lane == k - 1));
             const bool pair = on && keyn > (kNegInfKey | kLow);
-            doubt |= __any_sync(kAll, pair && !equal && close);
+            bool doubt = __any_sync(kAll, pair && !equal && close);
+            const bool met = __any_sync(kAll, pair && !equal && meet);
             // after a true tie across the k-th place, whoever comes next must be apart from it, too
             bool tie = __ballot_sync(kAll, pair && equal) >> (k - 1) & 1;
-            while (tie && !doubt) {
-                const float Lk = __shfl_sync(kAll, myL, k - 1), bk = __shfl_sync(kAll, b, k - 1), ck = __shfl_sync(kAll, c, k - 1);
+            const float ck = __shfl_sync(kAll, c, k - 1), tk = __shfl_sync(kAll, tol, k - 1);
+            int n = k + 1;  // experts taken so far
+            while (tie && !doubt && !again) {
+                const float Lk = __shfl_sync(kAll, myL, k - 1), bk = __shfl_sync(kAll, b, k - 1);
                 const uint32_t keyk = __shfl_sync(kAll, mykey, k - 1);
                 const uint32_t best = take(k);
                 __syncwarp();
@@ -408,14 +486,34 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
                 if (best > (kNegInfKey | kLow)) {
                     const float L = row[e];
                     tie = L == Lk && bias_s[e] == bk;
-                    if (!tie) {
-                        const float x = p.bias ? key_logit(best | kLow) : L;  // at least its value
-                        doubt = p.bias ? !(ck - x > 2.0f * err + (4.0f * EPL + 2.0f) * kU * fabsf(ck)) : (keyk ^ best) <= kLow;
-                    }
+                    // (experts equal to the k-th are lost to the list of candidates)
+                    if (!tie) again = p.bias ? !(ck - key_logit(best | kLow) > tk) : (keyk ^ best) <= kLow;
+                }
+            }
+            if (doubt && !again) {
+                // candidates until the next one is apart from the k-th, the least of the first k
+                float ckmin = lane < k ? c : INFINITY;
+#pragma unroll
+                for (int off = 8; off >= 1; off >>= 1) ckmin = fminf(ckmin, __shfl_xor_sync(kAll, ckmin, off));
+                ckmin = __shfl_sync(kAll, ckmin, 0);
+                const float t2 = p.bias ? 2.0f * err + (4.0f * EPL + 2.0f) * kU * fabsf(ckmin) : 0.0f;
+                uint32_t last = __shfl_sync(kAll, mykey, k);
+                while (n < kCandidates && last > (kNegInfKey | kLow) && !(ckmin - key_logit(last | kLow) > t2)) last = take(n++);
+                again = (!SIGMOID && p.bias) || (!SIGMOID && met) || !(ckmin == ckmin) ||
+                        (n == kCandidates && last > (kNegInfKey | kLow) && !(ckmin - key_logit(last | kLow) > t2));
+                if (!again) {
+                    __syncwarp();
+                    // (the last taken may be none, and of the first ones too)
+                    const int base = __popc(__ballot_sync(kAll, there));
+                    const int have = base <= k ? base : last > (kNegInfKey | kLow) ? n : n - 1;
+                    order_again(row, bias_s, SIGMOID, have, k, chosen[warp], lane);
+                    myE = lane < k && lane < have ? static_cast<int>(chosen[warp][lane & 15]) : 0;
+                    on = lane < k && lane < have;
+                    myL = on ? row[myE] : -INFINITY;
                 }
             }
         }
-        if (doubt) {
+        if (again) {
             myE = choose64<EPL>(row, p.bias, E, k, p.G, p.kg, p.best, p.gs, SIGMOID, lane);
             on = lane < k && myE >= 0;
             myL = on ? row[myE] : -INFINITY;
