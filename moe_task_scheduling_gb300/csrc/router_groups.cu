@@ -158,52 +158,105 @@ __device__ __forceinline__ uint32_t score_key(float s) {
     return k;
 }
 
-// Sorts a lane's keys, the largest first.
-template <int EPL>
-__device__ __forceinline__ void sort_keys(uint32_t (&k)[EPL]) {
-    auto swap = [&](int a, int b) {
-        const uint32_t hi = max(k[a], k[b]);
-        k[b] = min(k[a], k[b]);
-        k[a] = hi;
-    };
-    // odd-even merge sort
-    if (EPL == 2) swap(0, 1);
-    if (EPL >= 4) {
+__device__ __forceinline__ void order2(uint32_t& a, uint32_t& b) {  // the larger first
+    const uint32_t hi = max(a, b);
+    b = min(a, b);
+    a = hi;
+}
+
+// Sorts k[0 .. N), first rising and then falling (or the other way), the largest first.
+template <int N>
+__device__ __forceinline__ void sort_bitonic(uint32_t* k) {
 #pragma unroll
-        for (int o = 0; o + 3 < EPL; o += 4) {
-            swap(o, o + 1); swap(o + 2, o + 3);
-            swap(o, o + 2); swap(o + 1, o + 3);
-            swap(o + 1, o + 2);
+    for (int h = N / 2; h >= 1; h /= 2)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (!(i & h)) order2(k[i], k[i + h]);
+}
+
+// The warp's eight largest keys, sorted, in every lane; a lane has N to begin with.
+template <int N>
+__device__ __forceinline__ void top8(const uint32_t (&mine)[N], uint32_t (&k)[8]) {
+    constexpr uint32_t kAll = 0xffffffffu;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) k[i] = i < N ? mine[i % N] : 0u;
+    if (N == 2) order2(k[0], k[1]);
+    if (N >= 4) {  // odd-even merge sort
+#pragma unroll
+        for (int o = 0; o < N; o += 4) {
+            order2(k[o], k[o + 1]); order2(k[o + 2], k[o + 3]);
+            order2(k[o], k[o + 2]); order2(k[o + 1], k[o + 3]);
+            order2(k[o + 1], k[o + 2]);
         }
     }
-    if (EPL == 8) {
-        swap(0, 4 % EPL); swap(1 % EPL, 5 % EPL); swap(2 % EPL, 6 % EPL); swap(3 % EPL, 7 % EPL);
-        swap(2 % EPL, 4 % EPL); swap(3 % EPL, 5 % EPL);
-        swap(1 % EPL, 2 % EPL); swap(3 % EPL, 4 % EPL); swap(5 % EPL, 6 % EPL);
+    if (N == 8) {
+        order2(k[0], k[4]); order2(k[1], k[5]); order2(k[2], k[6]); order2(k[3], k[7]);
+        order2(k[2], k[4]); order2(k[3], k[5]);
+        order2(k[1], k[2]); order2(k[3], k[4]); order2(k[5], k[6]);
+    }
+    // With a neighbour's list, turned round: the larger of each pair are the larger half of both
+    // lists.  Short lists grow to eight first.
+    int n = N;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        if (n < 8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < n) {
+                    const uint32_t other = __shfl_xor_sync(kAll, k[n - 1 - i], off);
+                    k[8 - 1 - i] = other;  // parked
+                }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < n) {
+                    const uint32_t other = k[8 - 1 - i];
+                    const uint32_t hi = max(k[i], other), lo = min(k[i], other);
+                    k[i] = hi;
+                    k[8 - 1 - i] = lo;
+                }
+            uint32_t low[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) low[i] = k[8 - 1 - i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < n) k[n + i] = low[i];
+            if (n == 2) { sort_bitonic<2>(k); sort_bitonic<2>(k + 2); }
+            if (n == 4) { sort_bitonic<4>(k); sort_bitonic<4>(k + 4); }
+            n *= 2;
+        } else {
+            uint32_t other[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) other[i] = __shfl_xor_sync(kAll, k[7 - i], off);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) k[i] = max(k[i], other[i]);
+            sort_bitonic<8>(k);
+        }
     }
 }
 
 constexpr int kCandidates = 16;  // experts whose order is looked at again at most
 
-// score + bias in 64 bits, without a bias and with softmax scores the logit, which orders alike.
-__device__ __forceinline__ double value64(float x, float b, bool sigmoid) {
-    return sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(x))) + static_cast<double>(b) : static_cast<double>(x);
+// What ranks experts and groups in 64 bits: sigmoid scores + bias; for softmax scores (without
+// a bias) their multiples e^(x - top).
+__device__ __forceinline__ double value64(float x, float b, bool sigmoid, float top) {
+    const double e = exp(sigmoid ? -static_cast<double>(x) : static_cast<double>(x) - static_cast<double>(top));
+    return sigmoid ? 1.0 / (1.0 + e) + static_cast<double>(b) : e;
 }
 
 // Two groups whose scores 32 bits cannot tell apart: 1 if the first has the larger, or the
 // same and the lower number, 0 if the second, -1 if it takes more than their best two to
-// say.  Sigmoid scores.  floor_a, floor_b: what the experts that count are not below;
+// say.  floor_a, floor_b: what the experts that count are not below;
 // want_a, want_b: how many those are.  slots: 16 places of shared memory.
 template <int EPL>
-__device__ __noinline__ int compare_groups(const float* row, const float* bias_s, int E, int gs, int a, int b, float floor_a,
-                                           float floor_b, int want_a, int want_b, uint32_t* slots, int lane) {
+__device__ __noinline__ int compare_groups(const float* row, const float* bias_s, bool sigmoid, float top, float inv, int E,
+                                           int gs, int a, int b, float floor_a, float floor_b, int want_a, int want_b, uint32_t* slots, int lane) {
     constexpr uint32_t kAll = 0xffffffffu;
     int na = 0, nb = 0;
 #pragma unroll 1
     for (int i = 0; i < EPL; ++i) {
         const int e = lane * EPL + i, g = e / gs;
         const float x = e < E ? row[e] : -INFINITY;
-        const float c = x == -INFINITY ? x : __fadd_rn(sigmoid_fast(x), bias_s[min(e, E - 1)]);
+        const float c = x == -INFINITY ? x : __fadd_rn(sigmoid ? sigmoid_fast(x) : __expf(x - top) * inv, bias_s[min(e, E - 1)]);
         const uint32_t in_a = __ballot_sync(kAll, e < E && g == a && c >= floor_a);
         const uint32_t in_b = __ballot_sync(kAll, e < E && g == b && c >= floor_b);
         const uint32_t bit = 1u << lane, below = bit - 1;
@@ -216,18 +269,18 @@ __device__ __noinline__ int compare_groups(const float* row, const float* bias_s
     if (na != want_a || nb != want_b) return -1;
     const bool mine = lane < na || (lane >= 8 && lane < 8 + nb);
     const int e = mine ? static_cast<int>(slots[lane]) : 0;
-    double c = mine ? value64(row[e], bias_s[e], true) : 0.0;
+    double c = mine ? value64(row[e], bias_s[e], sigmoid, top) : 0.0;
     c += __shfl_xor_sync(kAll, c, 1);  // two at most
     const double sa = __shfl_sync(kAll, c, 0), sb = __shfl_sync(kAll, c, 8);
     return sa > sb || (sa == sb && a < b) ? 1 : 0;
 }
 
-// The order of n candidates (n <= kCandidates, their experts in slots) in 64 bits: puts the
-// best k there in their order.
+// The order of n candidates (n <= kCandidates, their experts in slots) in 64 bits (of softmax
+// scores without a bias by the logits): puts the best k there in their order.
 __device__ __noinline__ void order_again(const float* row, const float* bias_s, bool sigmoid, int n, int k, uint32_t* slots, int lane) {
     constexpr uint32_t kAll = 0xffffffffu;
     const int e = lane < n ? static_cast<int>(slots[lane]) : 0;
-    const double c = lane < n ? value64(row[e], bias_s[e], sigmoid) : 0.0;
+    const double c = lane < n ? (sigmoid ? value64(row[e], bias_s[e], true, 0.0f) : static_cast<double>(row[e])) : 0.0;
     const unsigned long long key = value_key(c);
     int rank = 0;
 #pragma unroll 1
@@ -244,15 +297,16 @@ __device__ __noinline__ void order_again(const float* row, const float* bias_s, 
 // One row a warp, experts lane * EPL + i in register i, so that a group is a few
 // neighbouring lanes.  The choice runs on 32-bit values: without a bias on the logits,
 // which order as the scores do and are exact; with one on score + bias, whose error has a
-// bound.  A lane's keys, cut by the bits that name its experts, are sorted once; a round
-// of the choice looks at the heads alone, and takes the lowest lane of those with the
-// largest cut key.  Where two neighbours in the order are no farther apart than the cut
-// and both errors, or the last group that takes part and the next than theirs, 64 bits
+// bound.  Keys are cut by the bits that name their experts, sorted in each lane and merged
+// over the warp, a list of eight and its neighbour's at a time.  Then the chosen are looked
+// at with their whole values: where two neighbours in the order are no farther apart than
+// both errors, where more than k experts are above the k-th less both errors (those that
+// equal it apart), or the last group that takes part and the next than theirs, 64 bits
 // decide: on the candidates alone (a lane each: 1.3 us where a whole row takes 14), and on
-// the whole row if they are too many, or softmax scores with a bias.
-template <int EPL, bool SIGMOID>
+// the whole row if they are too many, or for softmax scores with a bias.
+template <int EPL, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(const GroupArgs p) {
-    constexpr uint32_t kAll = 0xffffffffu, kLow = EPL - 1;
+    constexpr uint32_t kAll = 0xffffffffu, kLow = 32 * EPL - 1;  // the bits that name an expert
     constexpr float kU = 1.0f / (1 << 24);
     extern __shared__ __align__(16) float sm[];  // [warps][E], then the last CTA's sums
     __shared__ RouterShared sh;
@@ -289,13 +343,18 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
     load(t0, nv, non);
     for (int e = threadIdx.x; e < kRouterEMax; e += blockDim.x) {
         if (e < E) sh.hist[e] = 0;
-        bias_s[e] = p.bias && e < E ? p.bias[e] : 0.0f;
+        bias_s[e] = BIAS && e < E ? p.bias[e] : 0.0f;
     }
     float* const big = sm + warp * E + e0;  // this lane's sums of whole batches of 32 rows
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
         if (e0 + i < E) big[i] = 0.0f;
     __syncthreads();
+
+    uint32_t group_of[(EPL + 3) / 4] = {};  // a byte an expert, where a group is not whole lanes
+    if (p.kg < p.G && !p.lanes)
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) group_of[i / 4] |= static_cast<uint32_t>((e0 + i) / p.gs & 31) << (8 * (i % 4));
 
     float accp[EPL];
     int accn = 0, rows32 = 0;
@@ -334,26 +393,23 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
         // mean |x - top| is below log 256).
         const float err = (SIGMOID ? 10.0f : 48.0f * inv) * kU;
 
+        // What ranks an expert: with a bias score + bias, else the logit; -inf: not available.
+        auto value = [&](int i) -> float {
+            return BIAS ? (v[i] == -INFINITY ? v[i] : __fadd_rn(s[i], bias_s[e0 + i])) : v[i];
+        };
+        const float* row = p.logits + static_cast<size_t>(t) * E;
         uint32_t key[EPL];  // kNegInfKey or 0: not available
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            float c = v[i];
-            if (p.bias) c = v[i] == -INFINITY ? v[i] : __fadd_rn(s[i], bias_s[e0 + i]);
-            key[i] = logit_key(c);
-        }
+        for (int i = 0; i < EPL; ++i) key[i] = logit_key(value(i));
         bool again = false;  // the whole row in 64 bits
+        uint32_t in = kAll;  // the groups that take part
         if (p.kg < p.G) {
-            float score = -INFINITY, mag = 0.0f;  // lane g: of group g
-            auto group_score = [&](uint32_t hi, uint32_t lo) {  // from its best two values of score + bias
-                const float h = key_or_none(hi), l = lo > kNegInfKey ? key_logit(lo) : 0.0f;
-                score = h + (p.best > 1 ? l : 0.0f);
-                mag = fabsf(h) + fabsf(l);
-            };
-            uint32_t hi = 0, lo = 0;
+            uint32_t hi = 0, lo = 0;  // of lane g: group g's best two, by score + bias
+            auto score_of = [&](int i) -> uint32_t { return BIAS || key[i] <= kNegInfKey ? key[i] : score_key(s[i]); };
             if (p.lanes) {
 #pragma unroll
                 for (int i = 0; i < EPL; ++i) {
-                    const uint32_t c = p.bias || key[i] <= kNegInfKey ? key[i] : score_key(s[i]);
+                    const uint32_t c = score_of(i);
                     lo = max(lo, min(hi, c));
                     hi = max(hi, c);
                 }
@@ -371,8 +427,7 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
                     uint32_t h = 0, l = 0;
 #pragma unroll
                     for (int i = 0; i < EPL; ++i) {
-                        const bool in = e0 + i >= g * p.gs && e0 + i < g * p.gs + p.gs;
-                        const uint32_t c = !in ? 0u : p.bias || key[i] <= kNegInfKey ? key[i] : score_key(s[i]);
+                        const uint32_t c = e0 + i >= g * p.gs && e0 + i < g * p.gs + p.gs ? score_of(i) : 0u;
                         l = max(l, min(h, c));
                         h = max(h, c);
                     }
@@ -386,7 +441,12 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
                     }
                 }
             }
-            if (lane < p.G) group_score(hi, lo);
+            float score = -INFINITY, off_by = 0.0f;
+            if (lane < p.G) {
+                const float h = key_or_none(hi), l = p.best > 1 && lo > kNegInfKey ? key_logit(lo) : 0.0f;
+                score = h + l;
+                off_by = 2.0f * err + 2.0f * kU * (fabsf(h) + fabsf(l));
+            }
             const uint32_t mine = logit_key(score);
             int rank = 0;
 #pragma unroll 4
@@ -394,121 +454,110 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
                 const uint32_t other = __shfl_sync(kAll, mine, g);
                 rank += other > mine || (other == mine && g < lane);
             }
-            uint32_t in = __ballot_sync(kAll, lane < p.G && rank < p.kg);
+            in = __ballot_sync(kAll, lane < p.G && rank < p.kg);
             // the last that takes part and the next: apart by more than any two may be off
-            const uint32_t last_in = __ballot_sync(kAll, lane < p.G && rank == p.kg - 1);
-            const uint32_t next = __ballot_sync(kAll, lane < p.G && rank == p.kg);
-            const float off_by = 2.0f * err + 2.0f * kU * mag;
-            const float a = __shfl_sync(kAll, score, __ffs(last_in) - 1), b = __shfl_sync(kAll, score, __ffs(next) - 1);
+            const int ga = __ffs(__ballot_sync(kAll, lane < p.G && rank == p.kg - 1)) - 1;
+            const int gb = __ffs(__ballot_sync(kAll, lane < p.G && rank == p.kg)) - 1;
+            const float a = __shfl_sync(kAll, score, ga), b = __shfl_sync(kAll, score, gb);
             const float tol = 2.0f * __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(off_by)));
             if (!(a - b > tol) && !(b == -INFINITY)) {
-                const int ga = __ffs(last_in) - 1, gb = __ffs(next) - 1;
                 // between these two alone?
                 const bool other = lane < p.G && !(rank < p.kg - 1 ? score - b > tol : rank > p.kg ? a - score > tol : true);
-                again = !SIGMOID || !(tol < 1.0f) || __any_sync(kAll, other);
+                again = (!SIGMOID && BIAS) || !(tol < 1.0f) || __any_sync(kAll, other);
                 if (!again) {
-                    const uint32_t last = p.best > 1 && lo > kNegInfKey ? lo : hi;  // the last that counts
-                    const float floor = key_or_none(last) - tol;
-                    const int want = last == hi && (p.best == 1 || lo <= kNegInfKey) ? 1 : 2;
-                    const int r = compare_groups<EPL>(p.logits + static_cast<size_t>(t) * E, bias_s, E, p.gs, ga, gb,
-                                                      __shfl_sync(kAll, floor, ga), __shfl_sync(kAll, floor, gb),
-                                                      __shfl_sync(kAll, want, ga), __shfl_sync(kAll, want, gb), chosen[warp], lane);
+                    const bool two = p.best > 1 && lo > kNegInfKey;
+                    const float floor = key_or_none(two ? lo : hi) - tol;  // the last that counts
+                    const int r = compare_groups<EPL>(row, bias_s, SIGMOID, top, inv, E, p.gs, ga, gb, __shfl_sync(kAll, floor, ga),
+                                                      __shfl_sync(kAll, floor, gb), __shfl_sync(kAll, two ? 2 : 1, ga),
+                                                      __shfl_sync(kAll, two ? 2 : 1, gb), chosen[warp], lane);
                     again = r < 0;
                     if (r == 0) in ^= 1u << ga | 1u << gb;
                     __syncwarp();
                 }
             }
+        }
+        // Bit i: expert e0 + i takes part.
+        uint32_t part = (1u << EPL) - 1;
+        if (p.kg < p.G) {
             if (p.lanes) {
-                const bool out = !(in >> (lane / p.lanes & 31) & 1);
-#pragma unroll
-                for (int i = 0; i < EPL; ++i) key[i] = out ? 0u : key[i];
+                if (!(in >> (lane / p.lanes & 31) & 1)) part = 0;
             } else {
 #pragma unroll
                 for (int i = 0; i < EPL; ++i)
-                    if (!(in >> ((e0 + i) / p.gs & 31) & 1)) key[i] = 0u;
+                    if (!(in >> (group_of[i / 4] >> (8 * (i % 4)) & 31) & 1)) part &= ~(1u << i);
             }
         }
 
-        // the best k and the next one; lane j: the j-th
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) key[i] = (key[i] & ~kLow) | (kLow - i);
-        sort_keys<EPL>(key);
-        auto take = [&](int j) -> uint32_t {  // the largest cut key; its expert goes to chosen[j]
-            const uint32_t best = __reduce_max_sync(kAll, key[0]);
-            const bool mine = (key[0] ^ best) <= kLow;
-            const uint32_t who = __ballot_sync(kAll, mine);
-            if (mine && !(who & below)) {
-                chosen[warp][j] = e0 + (kLow - (key[0] & kLow));
-#pragma unroll
-                for (int i = 0; i < EPL; ++i) key[i] = i + 1 < EPL ? key[(i + 1) % EPL] : 0u;
-            }
-            return best;
-        };
-        uint32_t mykey = 0;
-#pragma unroll 1
-        for (int j = 0; j <= k; ++j) {
-            const uint32_t best = take(j);
-            if (lane == j) mykey = best;
-        }
-        __syncwarp();
-        const float* row = p.logits + static_cast<size_t>(t) * E;
-        const bool there = lane <= k && mykey > (kNegInfKey | kLow);
-        bool on = lane < k && there;
-        int myE = there ? static_cast<int>(chosen[warp][lane & 15]) : 0;
-        float myL = there ? row[myE] : -INFINITY;
+        // the best k by their keys, cut to name the expert, lower experts larger; lane j: the j-th
+        uint32_t best[8];
         {
-            const float b = there ? bias_s[myE] : 0.0f;
-            // score + bias as above
-            const float c = !there ? -INFINITY : !p.bias ? myL : __fadd_rn(SIGMOID ? sigmoid_fast(myL) : __expf(myL - top) * inv, b);
-            const float cn = __shfl_down_sync(kAll, c, 1), bn = __shfl_down_sync(kAll, b, 1), Ln = __shfl_down_sync(kAll, myL, 1);
-            const uint32_t keyn = __shfl_down_sync(kAll, mykey, 1);
-            const bool equal = b == bn && myL == Ln;  // a true tie, in the order of the experts already
-            // with a bias: both errors and the cut; without: the order is the whole key's unless
-            // the cut key is one, or the scores meet at 1 or 0 in 64 bits
-            const float tol = 2.0f * err + (kU + 2.0f * EPL * kU) * (fabsf(c) + fabsf(cn));
-            const bool meet = SIGMOID ? Ln > 16.0f || Ln < -700.0f : Ln - top < -700.0f;
-            const bool close = p.bias ? !(c - cn > tol) : meet || ((mykey ^ keyn) <= kLow && (c < cn || c != c || lane == k - 1));
-            const bool pair = on && keyn > (kNegInfKey | kLow);
-            bool doubt = __any_sync(kAll, pair && !equal && close);
-            const bool met = __any_sync(kAll, pair && !equal && meet);
-            // after a true tie across the k-th place, whoever comes next must be apart from it, too
-            bool tie = __ballot_sync(kAll, pair && equal) >> (k - 1) & 1;
-            const float ck = __shfl_sync(kAll, c, k - 1), tk = __shfl_sync(kAll, tol, k - 1);
-            int n = k + 1;  // experts taken so far
-            while (tie && !doubt && !again) {
-                const float Lk = __shfl_sync(kAll, myL, k - 1), bk = __shfl_sync(kAll, b, k - 1);
-                const uint32_t keyk = __shfl_sync(kAll, mykey, k - 1);
-                const uint32_t best = take(k);
-                __syncwarp();
-                const int e = static_cast<int>(chosen[warp][k]);
-                __syncwarp();
-                tie = false;
-                if (best > (kNegInfKey | kLow)) {
-                    const float L = row[e];
-                    tie = L == Lk && bias_s[e] == bk;
-                    // (experts equal to the k-th are lost to the list of candidates)
-                    if (!tie) again = p.bias ? !(ck - key_logit(best | kLow) > tk) : (keyk ^ best) <= kLow;
-                }
-            }
-            if (doubt && !again) {
-                // candidates until the next one is apart from the k-th, the least of the first k
-                float ckmin = lane < k ? c : INFINITY;
+            uint32_t cut[EPL];
 #pragma unroll
-                for (int off = 8; off >= 1; off >>= 1) ckmin = fminf(ckmin, __shfl_xor_sync(kAll, ckmin, off));
-                ckmin = __shfl_sync(kAll, ckmin, 0);
-                const float t2 = p.bias ? 2.0f * err + (4.0f * EPL + 2.0f) * kU * fabsf(ckmin) : 0.0f;
-                uint32_t last = __shfl_sync(kAll, mykey, k);
-                while (n < kCandidates && last > (kNegInfKey | kLow) && !(ckmin - key_logit(last | kLow) > t2)) last = take(n++);
-                again = (!SIGMOID && p.bias) || (!SIGMOID && met) || !(ckmin == ckmin) ||
-                        (n == kCandidates && last > (kNegInfKey | kLow) && !(ckmin - key_logit(last | kLow) > t2));
+            for (int i = 0; i < EPL; ++i) cut[i] = part >> i & 1 ? (key[i] & ~kLow) | (kLow - (e0 + i)) : 0u;
+            top8<EPL>(cut, best);
+        }
+        uint32_t mykey = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (lane == j) mykey = best[j];
+        bool on = lane < k && mykey > kNegInfKey;
+        int myE = static_cast<int>(kLow - (mykey & kLow));
+        float myL = on ? row[myE] : -INFINITY;
+        {
+            const float b = BIAS && on ? bias_s[myE] : 0.0f;
+            // value(), again
+            const float c = !on ? -INFINITY : !BIAS ? myL : __fadd_rn(SIGMOID ? sigmoid_fast(myL) : __expf(myL - top) * inv, b);
+            const float cn = __shfl_down_sync(kAll, c, 1), Ln = __shfl_down_sync(kAll, myL, 1);
+            const float bn = BIAS ? __shfl_down_sync(kAll, b, 1) : 0.0f;
+            const int onn = __shfl_down_sync(kAll, static_cast<int>(on), 1);
+            const bool pair = on && lane < k - 1 && onn;
+            // (one that equals its neighbour comes in the order of the experts already)
+            const float tol = BIAS ? 2.0f * err + kU * (fabsf(c) + fabsf(cn)) : 0.0f;
+            bool doubt = pair && !(b == bn && myL == Ln) && (BIAS ? !(c - cn > tol) : !(c > cn));
+            // logits whose scores meet at 1 or 0 in 64 bits, chosen or not
+            const bool met = !BIAS && on && (SIGMOID ? myL > 16.0f || myL < -700.0f : myL - top < -700.0f);
+            // the least of the chosen, and what may be above it in truth: these experts, and they alone?
+            const uint32_t lanes_on = __ballot_sync(kAll, on);
+            const float ck = __shfl_sync(kAll, c, k - 1), Lk = __shfl_sync(kAll, myL, k - 1), bk = __shfl_sync(kAll, b, k - 1);
+            float cmin = on ? c : INFINITY;
+#pragma unroll
+            for (int off = 4; off >= 1; off >>= 1) cmin = fminf(cmin, __shfl_xor_sync(kAll, cmin, off));
+            cmin = __shfl_sync(kAll, cmin, 0);
+            const float floor = BIAS ? cmin - (2.0f * err + 4.0f * kU * fabsf(cmin)) : cmin;
+            uint32_t above = 0;
+            if (lanes_on >> (k - 1) & 1) {  // else all that are available are chosen
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if ((part >> i & 1) && !(value(i) < floor)) above |= 1u << i;
+            }
+            const int n = __reduce_add_sync(kAll, __popc(above));
+            if (n > k) {
+                // as many more as equal the k-th exactly may be: they come behind it
+                uint32_t ties = 0;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if ((above >> i & 1) && v[i] == Lk && (!BIAS || bias_s[e0 + i] == bk)) ties |= 1u << i;
+                const int n_ties = __reduce_add_sync(kAll, __popc(ties));
+                const int chosen_ties = __popc(__ballot_sync(kAll, on && myL == Lk && b == bk));
+                doubt |= n - n_ties != k - chosen_ties || !(ck == cmin);
+            } else if (n < k && n > 0) {
+                doubt = true;  // (a NaN)
+            }
+            if (__any_sync(kAll, doubt || met) && !again) {
+                again = (!SIGMOID && BIAS) || __any_sync(kAll, met) || n > kCandidates || n == 0;
                 if (!again) {
+                    int at = 0;
                     __syncwarp();
-                    // (the last taken may be none, and of the first ones too)
-                    const int base = __popc(__ballot_sync(kAll, there));
-                    const int have = base <= k ? base : last > (kNegInfKey | kLow) ? n : n - 1;
-                    order_again(row, bias_s, SIGMOID, have, k, chosen[warp], lane);
-                    myE = lane < k && lane < have ? static_cast<int>(chosen[warp][lane & 15]) : 0;
-                    on = lane < k && lane < have;
+#pragma unroll
+                    for (int i = 0; i < EPL; ++i) {
+                        const uint32_t who = __ballot_sync(kAll, above >> i & 1);
+                        if (above >> i & 1) chosen[warp][at + __popc(who & below)] = e0 + i;
+                        at += __popc(who);
+                    }
+                    __syncwarp();
+                    order_again(row, bias_s, SIGMOID, n, k, chosen[warp], lane);
+                    on = lane < k && lane < n;
+                    myE = on ? static_cast<int>(chosen[warp][lane & (kCandidates - 1)]) : 0;
                     myL = on ? row[myE] : -INFINITY;
                 }
             }
@@ -575,7 +624,7 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
             }
             rows32 = 0;
         }
-        __syncwarp();  // `chosen` is written again
+        __syncwarp();
     }
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
@@ -709,6 +758,12 @@ __global__ void __launch_bounds__(256) router_groups_bwd_kernel(const GroupBwdAr
     }
 }
 
+template <int EPL>
+auto pick_groups(bool sigmoid, bool bias) {
+    return sigmoid ? (bias ? router_groups_kernel<EPL, true, true> : router_groups_kernel<EPL, true, false>)
+                   : (bias ? router_groups_kernel<EPL, false, true> : router_groups_kernel<EPL, false, false>);
+}
+
 int groups_check(int T, const int32_t* d_T, int T_max, int E, int k, int score, float scale) {
     std::string why;
     if (!router_shape_ok(T_max, E, k, &why)) return api_fail(ET_ERR_UNSUPPORTED, why);
@@ -758,10 +813,9 @@ int et_router_groups(const float* logits, const float* bias, const uint8_t* toke
                           lanes & (lanes - 1) ? 0 : lanes, renorm != 0, E % 4 == 0 && api_aligned(logits, 16), scale,
                           router_sums_args(workspace, L, expert_counts, n_routed, mean_prob, loss, false)};
         const RouterGrid g = router_grid(d_T ? T_max : T > 0 ? T : 1, E);
-        auto pick = [&](auto one, auto two, auto four, auto eight) { return epl == 1 ? one : epl == 2 ? two : epl == 4 ? four : eight; };
-        auto kernel = score == ET_SCORE_SIGMOID
-            ? pick(router_groups_kernel<1, true>, router_groups_kernel<2, true>, router_groups_kernel<4, true>, router_groups_kernel<8, true>)
-            : pick(router_groups_kernel<1, false>, router_groups_kernel<2, false>, router_groups_kernel<4, false>, router_groups_kernel<8, false>);
+        const bool sig = score == ET_SCORE_SIGMOID;
+        auto kernel = epl == 1 ? pick_groups<1>(sig, bias) : epl == 2 ? pick_groups<2>(sig, bias)
+                    : epl == 4 ? pick_groups<4>(sig, bias) : pick_groups<8>(sig, bias);
         const cudaError_t e = api_launch(kernel, g.ctas, g.warps * 32, g.smem, stream, a);
         if (e != cudaSuccess) return api_fail_cuda(e, "launch of the grouped router kernel");
         return ET_OK;
