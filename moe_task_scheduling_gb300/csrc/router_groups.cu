@@ -234,6 +234,12 @@ __device__ __forceinline__ void top8(const uint32_t (&mine)[N], uint32_t (&k)[8]
     }
 }
 
+// logit_key of a sum score + bias, which is never -0 and no NaN but the positive one.
+__device__ __forceinline__ uint32_t sum_key(float v) {
+    const int b = __float_as_int(v);
+    return static_cast<uint32_t>(b ^ ((b >> 31) | static_cast<int>(0x80000000u)));
+}
+
 constexpr int kCandidates = 16;  // experts whose order is looked at again at most
 
 // What ranks experts and groups in 64 bits: sigmoid scores + bias; for softmax scores (without
@@ -311,7 +317,7 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
     extern __shared__ __align__(16) float sm[];  // [warps][E], then the last CTA's sums
     __shared__ RouterShared sh;
     __shared__ uint32_t chosen[kRouterWarpsMax][kCandidates];
-    __shared__ float bias_s[kRouterEMax];
+    __shared__ __align__(16) float bias_s[kRouterEMax];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
     const int E = p.E, k = p.k, e0 = lane * EPL;
     const uint32_t below = (1u << lane) - 1;
@@ -351,6 +357,7 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
         if (e0 + i < E) big[i] = 0.0f;
     __syncthreads();
 
+    const int my_group = p.lanes ? lane / p.lanes : lane;  // whose numbers this lane has
     uint32_t group_of[(EPL + 3) / 4] = {};  // a byte an expert, where a group is not whole lanes
     if (p.kg < p.G && !p.lanes)
 #pragma unroll
@@ -393,18 +400,32 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
         // mean |x - top| is below log 256).
         const float err = (SIGMOID ? 10.0f : 48.0f * inv) * kU;
 
-        // What ranks an expert: with a bias score + bias, else the logit; -inf: not available.
-        auto value = [&](int i) -> float {
-            return BIAS ? (v[i] == -INFINITY ? v[i] : __fadd_rn(s[i], bias_s[e0 + i])) : v[i];
-        };
+        // What ranks an expert: with a bias score + bias, else the logit.
         const float* row = p.logits + static_cast<size_t>(t) * E;
-        uint32_t key[EPL];  // kNegInfKey or 0: not available
+        uint32_t key[EPL];  // kNegInfKey: not available; 0: in a group that takes no part
+        {
+            float b[EPL];
+            if (BIAS && EPL >= 4) {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) key[i] = logit_key(value(i));
+                for (int i = 0; i < EPL; i += 4) {
+                    const float4 q = *reinterpret_cast<const float4*>(bias_s + e0 + i);
+                    b[i] = q.x;
+                    b[(i + 1) % EPL] = q.y;
+                    b[(i + 2) % EPL] = q.z;
+                    b[(i + 3) % EPL] = q.w;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) b[i] = bias_s[e0 + i];
+            }
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) key[i] = BIAS ? sum_key(v[i] == -INFINITY ? v[i] : __fadd_rn(s[i], b[i])) : logit_key(v[i]);
+        }
         bool again = false;  // the whole row in 64 bits
-        uint32_t in = kAll;  // the groups that take part
         if (p.kg < p.G) {
-            uint32_t hi = 0, lo = 0;  // of lane g: group g's best two, by score + bias
+            // a group's best two, by score + bias: of this lane's group, or (where groups are not
+            // whole lanes, or not a power of two of them) of group number `lane`
+            uint32_t hi = 0, lo = 0;
             auto score_of = [&](int i) -> uint32_t { return BIAS || key[i] <= kNegInfKey ? key[i] : score_key(s[i]); };
             if (p.lanes) {
 #pragma unroll
@@ -418,9 +439,6 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
                     lo = max(max(lo, l), min(hi, h));
                     hi = max(hi, h);
                 }
-                const int from = min(lane * p.lanes, 31);
-                hi = __shfl_sync(kAll, hi, from);
-                lo = __shfl_sync(kAll, lo, from);
             } else {
 #pragma unroll 1
                 for (int g = 0; g < p.G; ++g) {
@@ -441,8 +459,10 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
                     }
                 }
             }
+            const int wide = p.lanes ? p.lanes : 1;  // lanes that hold a group's numbers
+            const bool group = my_group < p.G;
             float score = -INFINITY, off_by = 0.0f;
-            if (lane < p.G) {
+            if (group) {
                 const float h = key_or_none(hi), l = p.best > 1 && lo > kNegInfKey ? key_logit(lo) : 0.0f;
                 score = h + l;
                 off_by = 2.0f * err + 2.0f * kU * (fabsf(h) + fabsf(l));
@@ -451,40 +471,40 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
             int rank = 0;
 #pragma unroll 4
             for (int g = 0; g < p.G; ++g) {
-                const uint32_t other = __shfl_sync(kAll, mine, g);
-                rank += other > mine || (other == mine && g < lane);
+                const uint32_t other = __shfl_sync(kAll, mine, g * wide);
+                rank += other > mine || (other == mine && g < my_group);
             }
-            in = __ballot_sync(kAll, lane < p.G && rank < p.kg);
             // the last that takes part and the next: apart by more than any two may be off
-            const int ga = __ffs(__ballot_sync(kAll, lane < p.G && rank == p.kg - 1)) - 1;
-            const int gb = __ffs(__ballot_sync(kAll, lane < p.G && rank == p.kg)) - 1;
-            const float a = __shfl_sync(kAll, score, ga), b = __shfl_sync(kAll, score, gb);
+            const int la = __ffs(__ballot_sync(kAll, group && rank == p.kg - 1)) - 1;
+            const int lb = __ffs(__ballot_sync(kAll, group && rank == p.kg)) - 1;
+            const float a = __shfl_sync(kAll, score, la), b = __shfl_sync(kAll, score, lb);
             const float tol = 2.0f * __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(off_by)));
+            bool part = group && rank < p.kg;
             if (!(a - b > tol) && !(b == -INFINITY)) {
                 // between these two alone?
-                const bool other = lane < p.G && !(rank < p.kg - 1 ? score - b > tol : rank > p.kg ? a - score > tol : true);
-                again = (!SIGMOID && BIAS) || !(tol < 1.0f) || __any_sync(kAll, other);
+                const bool other = group && !(rank < p.kg - 1 ? score - b > tol : rank > p.kg ? a - score > tol : true);
+                const bool others = __any_sync(kAll, other);
+                again = (!SIGMOID && BIAS) || !(tol < 1.0f) || others;
                 if (!again) {
                     const bool two = p.best > 1 && lo > kNegInfKey;
                     const float floor = key_or_none(two ? lo : hi) - tol;  // the last that counts
-                    const int r = compare_groups<EPL>(row, bias_s, SIGMOID, top, inv, E, p.gs, ga, gb, __shfl_sync(kAll, floor, ga),
-                                                      __shfl_sync(kAll, floor, gb), __shfl_sync(kAll, two ? 2 : 1, ga),
-                                                      __shfl_sync(kAll, two ? 2 : 1, gb), chosen[warp], lane);
+                    const int r = compare_groups<EPL>(row, bias_s, SIGMOID, top, inv, E, p.gs, la / wide, lb / wide,
+                                                      __shfl_sync(kAll, floor, la), __shfl_sync(kAll, floor, lb),
+                                                      __shfl_sync(kAll, two ? 2 : 1, la), __shfl_sync(kAll, two ? 2 : 1, lb),
+                                                      chosen[warp], lane);
                     again = r < 0;
-                    if (r == 0) in ^= 1u << ga | 1u << gb;
+                    if (r == 0 && group && (rank == p.kg - 1 || rank == p.kg)) part = rank == p.kg;
                     __syncwarp();
                 }
             }
-        }
-        // Bit i: expert e0 + i takes part.
-        uint32_t part = (1u << EPL) - 1;
-        if (p.kg < p.G) {
             if (p.lanes) {
-                if (!(in >> (lane / p.lanes & 31) & 1)) part = 0;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) key[i] = part ? key[i] : 0u;
             } else {
+                const uint32_t in = __ballot_sync(kAll, part);
 #pragma unroll
                 for (int i = 0; i < EPL; ++i)
-                    if (!(in >> (group_of[i / 4] >> (8 * (i % 4)) & 31) & 1)) part &= ~(1u << i);
+                    if (!(in >> (group_of[i / 4] >> (8 * (i % 4)) & 31) & 1)) key[i] = 0u;
             }
         }
 
@@ -493,7 +513,7 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
         {
             uint32_t cut[EPL];
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) cut[i] = part >> i & 1 ? (key[i] & ~kLow) | (kLow - (e0 + i)) : 0u;
+            for (int i = 0; i < EPL; ++i) cut[i] = (key[i] & ~kLow) | (kLow - (e0 + i));
             top8<EPL>(cut, best);
         }
         uint32_t mykey = 0;
@@ -505,7 +525,6 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
         float myL = on ? row[myE] : -INFINITY;
         {
             const float b = BIAS && on ? bias_s[myE] : 0.0f;
-            // value(), again
             const float c = !on ? -INFINITY : !BIAS ? myL : __fadd_rn(SIGMOID ? sigmoid_fast(myL) : __expf(myL - top) * inv, b);
             const float cn = __shfl_down_sync(kAll, c, 1), Ln = __shfl_down_sync(kAll, myL, 1);
             const float bn = BIAS ? __shfl_down_sync(kAll, b, 1) : 0.0f;
@@ -524,20 +543,18 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
             for (int off = 4; off >= 1; off >>= 1) cmin = fminf(cmin, __shfl_xor_sync(kAll, cmin, off));
             cmin = __shfl_sync(kAll, cmin, 0);
             const float floor = BIAS ? cmin - (2.0f * err + 4.0f * kU * fabsf(cmin)) : cmin;
-            uint32_t above = 0;
-            if (lanes_on >> (k - 1) & 1) {  // else all that are available are chosen
+            int above = 0;
+            const uint32_t floor_key = lanes_on >> (k - 1) & 1 ? logit_key(floor) : ~0u;  // else all that are available are chosen
 #pragma unroll
-                for (int i = 0; i < EPL; ++i)
-                    if ((part >> i & 1) && !(value(i) < floor)) above |= 1u << i;
-            }
-            const int n = __reduce_add_sync(kAll, __popc(above));
+            for (int i = 0; i < EPL; ++i) above += key[i] >= floor_key;
+            const int n = __reduce_add_sync(kAll, above);
             if (n > k) {
                 // as many more as equal the k-th exactly may be: they come behind it
-                uint32_t ties = 0;
+                int ties = 0;
 #pragma unroll
                 for (int i = 0; i < EPL; ++i)
-                    if ((above >> i & 1) && v[i] == Lk && (!BIAS || bias_s[e0 + i] == bk)) ties |= 1u << i;
-                const int n_ties = __reduce_add_sync(kAll, __popc(ties));
+                    if (key[i] >= floor_key) ties += row[e0 + i] == Lk && (!BIAS || bias_s[e0 + i] == bk);
+                const int n_ties = __reduce_add_sync(kAll, ties);
                 const int chosen_ties = __popc(__ballot_sync(kAll, on && myL == Lk && b == bk));
                 doubt |= n - n_ties != k - chosen_ties || !(ck == cmin);
             } else if (n < k && n > 0) {
@@ -550,8 +567,8 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
                     __syncwarp();
 #pragma unroll
                     for (int i = 0; i < EPL; ++i) {
-                        const uint32_t who = __ballot_sync(kAll, above >> i & 1);
-                        if (above >> i & 1) chosen[warp][at + __popc(who & below)] = e0 + i;
+                        const uint32_t who = __ballot_sync(kAll, key[i] >= floor_key);
+                        if (key[i] >= floor_key) chosen[warp][at + __popc(who & below)] = e0 + i;
                         at += __popc(who);
                     }
                     __syncwarp();
