@@ -829,7 +829,10 @@ int et_router_groups(const float* logits, const float* bias, const uint8_t* toke
         const GroupArgs a{logits, bias, token_mask, topk_idx, topk_w, d_T, T, T_max, E, k, n_groups, k_groups, group_best, gs,
                           lanes & (lanes - 1) ? 0 : lanes, renorm != 0, E % 4 == 0 && api_aligned(logits, 16), scale,
                           router_sums_args(workspace, L, expert_counts, n_routed, mean_prob, loss, false)};
-        const RouterGrid g = router_grid(d_T ? T_max : T > 0 ? T : 1, E);
+        // One CTA up to 16 rows, then few warps a CTA while that puts rows on more SMs.
+        const int rows = d_T ? T_max : T > 0 ? T : 1;
+        const int warps = rows <= 16 ? rows : rows <= 8 * kRouterParts ? 8 : rows <= 16 * kRouterParts ? 16 : kRouterWarpsMax;
+        const RouterGrid g = router_grid_of(rows, E, warps);
         const bool sig = score == ET_SCORE_SIGMOID;
         auto kernel = epl == 1 ? pick_groups<1>(sig, bias) : epl == 2 ? pick_groups<2>(sig, bias)
                     : epl == 4 ? pick_groups<4>(sig, bias) : pick_groups<8>(sig, bias);

@@ -196,14 +196,10 @@ struct RouterGrid {
     size_t smem;
 };
 
-// A forward kernel's launch for this many rows, one a warp.  One CTA up to 32 rows:
-// nothing to sum over CTAs.  Beyond, as few warps as let the last CTA read all sums in
-// one batch (32 warps / E groups of 19): rows share fewer SMs.
-RouterGrid router_grid(int rows, int E) {
+// A forward kernel's launch for this many rows, one a warp.
+RouterGrid router_grid_of(int rows, int E, int warps) {
     RouterGrid g;
-    g.warps = rows < kRouterWarpsMax ? rows : kRouterWarpsMax;
-    if (rows > kRouterWarpsMax)
-        while (g.warps > 8 && 4ll * rows * E <= 608ll * g.warps * g.warps) g.warps /= 2;
+    g.warps = warps;
     g.ctas = ceil_div_i(rows, g.warps);
     g.ctas = g.ctas < kRouterParts ? g.ctas : kRouterParts;
     // [warps][E] floats; the last CTA: max(1, threads / E) x E of a float and an int
@@ -211,6 +207,15 @@ RouterGrid router_grid(int rows, int E) {
     const size_t rows_p = sizeof(float) * g.warps * E;
     g.smem = rows_p > sums ? rows_p : sums;
     return g;
+}
+
+// One CTA up to 32 rows: nothing to sum over CTAs.  Beyond, as few warps as let the last
+// CTA read all sums in one batch (32 warps / E groups of 19): rows share fewer SMs.
+RouterGrid router_grid(int rows, int E) {
+    int warps = rows < kRouterWarpsMax ? rows : kRouterWarpsMax;
+    if (rows > kRouterWarpsMax)
+        while (warps > 8 && 4ll * rows * E <= 608ll * warps * warps) warps /= 2;
+    return router_grid_of(rows, E, warps);
 }
 
 }  // namespace
