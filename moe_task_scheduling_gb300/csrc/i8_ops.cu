@@ -145,8 +145,9 @@ struct I8GemmArgs {
 
 constexpr int kGemvWarps = 8;
 constexpr int kGemvRows = 16;   // channels of a CTA
-constexpr int kGemvTokens = 16; // most tokens of a call that takes this form
+constexpr int kGemvTokens = 8;  // tokens of a tile
 constexpr int kGemvAhead = 3;   // 128-byte pieces of K that a warp has on their way
+constexpr int kGemvCtas = 2;    // CTAs an SM
 
 __device__ __forceinline__ int4 load_weights(const int8_t* p) {  // streamed: the tokens keep L1
     int4 v;
@@ -161,85 +162,106 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], int a0, int a1, int a2, int 
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Up to 8 MT tokens times 16 channels a CTA, whose warps take 128-byte pieces of K in
-// turn.  A thread's 16-byte loads are its fragments as they are: the order of k within a
-// piece is the same for both operands, and no other order matters to an exact sum.  An
-// integer MMA takes 16 cycles of an SM here, 32 bytes of weights a cycle for 8 tokens,
-// where HBM brings 23.
+// 8 MT tokens times 16 channels a tile, a CTA its tiles in turn; its warps take 128-byte
+// pieces of K in turn, and the next pieces, of this tile or the next, are on their way
+// meanwhile.  A thread's 16-byte loads are its fragments as they are: the order of k within
+// a piece is the same for both operands, and no other order matters to an exact sum.  An
+// integer MMA takes 16 cycles of an SM here, 32 / MT bytes of weights a cycle, where HBM
+// brings 23: MT = 1 is bound by HBM (N = 14336, K = 4096: 11.8 us, 5.0 TB/s from launch to
+// end), MT = 2 by the MMAs (17.7 us).
 template <int MT>
-__global__ void __launch_bounds__(kGemvWarps * 32, 2) i8_gemv_kernel(const I8GemmArgs p) {
-    __shared__ int red[kGemvWarps][MT * 8][kGemvRows + 1];
+__global__ void __launch_bounds__(kGemvWarps * 32, kGemvCtas) i8_gemv_kernel(const I8GemmArgs p) {
+    __shared__ int red[2][kGemvWarps][8 * MT][kGemvRows + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-    const int n0 = blockIdx.x * kGemvRows, K = p.K;
-    const int8_t* w0 = p.w + static_cast<size_t>(min(n0 + g, p.N - 1)) * K;
-    const int8_t* w1 = p.w + static_cast<size_t>(min(n0 + g + 8, p.N - 1)) * K;
-    const int k0 = warp * 128 + q * 16;
+    const int K = p.K, tiles = (p.N + kGemvRows - 1) / kGemvRows, k0 = warp * 128 + q * 16;
+    constexpr int kStep = kGemvWarps * 128;
+    // Where this thread's next piece is.
+    int ft = blockIdx.x, fk = k0;
+    auto rows_of = [&](int t, const int8_t*& w0, const int8_t*& w1) {
+        w0 = p.w + static_cast<size_t>(min(t * kGemvRows + g, p.N - 1)) * K;
+        w1 = p.w + static_cast<size_t>(min(t * kGemvRows + g + 8, p.N - 1)) * K;
+    };
+    const int8_t *w0, *w1;
+    rows_of(ft, w0, w1);
     // Nothing is read before what comes before has ended, but the first pieces may be on
     // their way to L2 by then.
 #pragma unroll
-    for (int i = 0; i < kGemvAhead; ++i) {
-        const int k = k0 + i * kGemvWarps * 128;
-        if (k < K) {
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(w0 + k));
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(w1 + k));
+    for (int i = 0; i < kGemvAhead; ++i)
+        if (fk + i * kStep < K) {
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(w0 + fk + i * kStep));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(w1 + fk + i * kStep));
         }
-    }
     grid_begin();
     bool ok;
     const int M = row_count(p.d_M, p.M_host, p.M_max, p.hdr, &ok);
     if (M < 1) return;
     const int8_t* x[MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) x[m] = p.x + static_cast<size_t>(min(m * 8 + g, M - 1)) * K;
-    int acc[MT][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][i] = 0;
+    for (int t = 0; t < MT; ++t) x[t] = p.x + static_cast<size_t>(min(8 * t + g, M - 1)) * K;
     const int4 zero = make_int4(0, 0, 0, 0);
     int4 wv[kGemvAhead][4];  // rows g and g + 8, bytes k and k + 64
-    auto fetch = [&](int4 (&v)[4], int k) {
-        v[0] = k < K ? load_weights(w0 + k) : zero;
-        v[1] = k < K ? load_weights(w1 + k) : zero;
-        v[2] = k + 64 < K ? load_weights(w0 + k + 64) : zero;
-        v[3] = k + 64 < K ? load_weights(w1 + k + 64) : zero;
+    auto fetch = [&](int4 (&v)[4]) {
+        const bool here = ft < tiles;
+        v[0] = here && fk < K ? load_weights(w0 + fk) : zero;
+        v[1] = here && fk < K ? load_weights(w1 + fk) : zero;
+        v[2] = here && fk + 64 < K ? load_weights(w0 + fk + 64) : zero;
+        v[3] = here && fk + 64 < K ? load_weights(w1 + fk + 64) : zero;
+        fk += kStep;
+        if (fk - q * 16 >= K) {
+            fk = k0;
+            ft += gridDim.x;
+            rows_of(min(ft, tiles - 1), w0, w1);
+        }
     };
 #pragma unroll
-    for (int i = 0; i < kGemvAhead; ++i) fetch(wv[i], k0 + i * kGemvWarps * 128);
-    for (int kk = k0; kk - q * 16 < K; kk += kGemvAhead * kGemvWarps * 128) {
+    for (int i = 0; i < kGemvAhead; ++i) fetch(wv[i]);
+    int tile = blockIdx.x, k = k0, buf = 0;
+    int acc[MT][4] = {};
+    while (tile < tiles) {
 #pragma unroll
         for (int i = 0; i < kGemvAhead; ++i) {
-            const int k = kk + i * kGemvWarps * 128;
-            if (k - q * 16 >= K) break;
-            int4 xv[MT][2];
+            if (tile >= tiles) break;
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                xv[m][0] = k < K ? *reinterpret_cast<const int4*>(x[m] + k) : zero;
-                xv[m][1] = k + 64 < K ? *reinterpret_cast<const int4*>(x[m] + k + 64) : zero;
+            for (int t = 0; t < MT; ++t) {
+                const int4 x0 = k < K ? *reinterpret_cast<const int4*>(x[t] + k) : zero;
+                const int4 x1 = k + 64 < K ? *reinterpret_cast<const int4*>(x[t] + k + 64) : zero;
+                mma_s8(acc[t], wv[i][0].x, wv[i][1].x, wv[i][0].y, wv[i][1].y, x0.x, x0.y);
+                mma_s8(acc[t], wv[i][0].z, wv[i][1].z, wv[i][0].w, wv[i][1].w, x0.z, x0.w);
+                mma_s8(acc[t], wv[i][2].x, wv[i][3].x, wv[i][2].y, wv[i][3].y, x1.x, x1.y);
+                mma_s8(acc[t], wv[i][2].z, wv[i][3].z, wv[i][2].w, wv[i][3].w, x1.z, x1.w);
             }
+            fetch(wv[i]);
+            k += kStep;
+            if (k - q * 16 >= K) {  // the tile's last piece: for the warps of K's end one or two pieces sooner
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+                for (int t = 0; t < MT; ++t)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    mma_s8(acc[m], wv[i][2 * h].x, wv[i][2 * h + 1].x, wv[i][2 * h].y, wv[i][2 * h + 1].y, xv[m][h].x, xv[m][h].y);
-                    mma_s8(acc[m], wv[i][2 * h].z, wv[i][2 * h + 1].z, wv[i][2 * h].w, wv[i][2 * h + 1].w, xv[m][h].z, xv[m][h].w);
+                    for (int j = 0; j < 4; ++j) {
+                        red[buf][warp][8 * t + 2 * q + (j & 1)][g + (j >> 1) * 8] = acc[t][j];
+                        acc[t][j] = 0;
+                    }
+                __syncthreads();  // (the other buffer has been read: who comes here has left it)
+                if (threadIdx.x < 8 * MT * kGemvRows) {
+                    const int m = threadIdx.x / kGemvRows, r = threadIdx.x % kGemvRows, n = tile * kGemvRows + r;
+                    int s = 0;
+#pragma unroll
+                    for (int v = 0; v < kGemvWarps; ++v) s += red[buf][v][m][r];
+                    if (m < M && n < p.N) p.y[static_cast<size_t>(m) * p.N + n] = __float2bfloat16_rn(static_cast<float>(s) * (p.sx[m] * p.sw[n]));
                 }
-            fetch(wv[i], k + kGemvAhead * kGemvWarps * 128);
+                buf ^= 1;
+                tile += gridDim.x;
+                k = k0;
+            }
         }
     }
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) red[warp][m * 8 + 2 * q + (i & 1)][g + (i >> 1) * 8] = acc[m][i];
-    __syncthreads();
-    for (int o = threadIdx.x; o < MT * 8 * kGemvRows; o += kGemvWarps * 32) {
-        const int m = o / kGemvRows, r = o % kGemvRows;
-        int s = 0;
-#pragma unroll
-        for (int v = 0; v < kGemvWarps; ++v) s += red[v][m][r];
-        if (m < M && n0 + r < p.N)
-            p.y[static_cast<size_t>(m) * p.N + n0 + r] = __float2bfloat16_rn(static_cast<float>(s) * (p.sx[m] * p.sw[n0 + r]));
-    }
+}
+
+// Which calls take the form above: those of up to 8 tokens, and up to 16 where the weights
+// are few.  With 9 to 16 tokens it takes 2.1 us + 1 us for each 3.8 MB of weights, the
+// tcgen05 form 6 us + 1 us for each 5.5 MB (2048 x 2048: 3.2 against 6.8 us; 14336 x 4096:
+// 17.7 against 16.3 us): they meet at 48 MB.
+bool i8_gemv(int M_max, int N, int K) {
+    return M_max <= kGemvTokens || (M_max <= 2 * kGemvTokens && static_cast<long long>(N) * K <= 48000000);
 }
 
 bool i8_shape_ok(int M_max, int N, int K, std::string* why) {
@@ -313,8 +335,8 @@ I8Plan i8_plan(int M, int N, int K) {
 // weights, and the workspace of a long batch stays small.
 constexpr int kI8RowsPass = 8192;
 
-size_t i8_ws_bytes(int M_max, int K) {
-    const size_t rows = M_max <= kGemvTokens ? 0 : M_max < kI8RowsPass ? M_max : kI8RowsPass;
+size_t i8_ws_bytes(int M_max, int N, int K) {
+    const size_t rows = i8_gemv(M_max, N, K) ? 0 : M_max < kI8RowsPass ? M_max : kI8RowsPass;
     return (kHeaderBytes + 2 * rows * K + 255) / 256 * 256;
 }
 
@@ -369,7 +391,7 @@ int et_i8_quantize(const void* x, void* q, float* scale, int M, const int32_t* d
 
 size_t et_i8_gemm_workspace_bytes(int M_max, int N, int K) {
     std::string why;
-    return i8_shape_ok(M_max, N, K, &why) ? i8_ws_bytes(M_max, K) : 0;
+    return i8_shape_ok(M_max, N, K, &why) ? i8_ws_bytes(M_max, N, K) : 0;
 }
 
 int et_i8_gemm(const void* x_q, const float* s_x, const void* w_q, const float* s_w, void* Y, int M, const int32_t* d_M,
@@ -383,7 +405,7 @@ int et_i8_gemm(const void* x_q, const float* s_x, const void* w_q, const float* 
             return api_fail(ET_ERR_INVALID, "tensors must be aligned to their element size");
         int rc = i8_check_rows(M, d_M, M_max);
         if (rc) return rc;
-        if ((rc = api_check_ws(workspace, workspace_bytes, i8_ws_bytes(M_max, K)))) return rc;
+        if ((rc = api_check_ws(workspace, workspace_bytes, i8_ws_bytes(M_max, N, K)))) return rc;
         if (!d_M && M == 0) return ET_OK;
         int dev = 0, sms = 0;
         if ((rc = api_device(&dev, &sms))) return rc;
@@ -392,10 +414,10 @@ int et_i8_gemm(const void* x_q, const float* s_x, const void* w_q, const float* 
         EtHeader* hdr = reinterpret_cast<EtHeader*>(ws);
         const int8_t* x = static_cast<const int8_t*>(x_q);
         bf16* y = static_cast<bf16*>(Y);
-        if (all <= kGemvTokens) {
+        if (i8_gemv(all, N, K)) {
             const I8GemmArgs a{x, s_x, static_cast<const int8_t*>(w_q), s_w, y, d_M, M, all, N, K, hdr};
-            auto kernel = all <= 8 ? i8_gemv_kernel<1> : i8_gemv_kernel<2>;
-            const cudaError_t e = api_launch(kernel, dim3((N + kGemvRows - 1) / kGemvRows), kGemvWarps * 32, 0, stream, a);
+            const int tiles = (N + kGemvRows - 1) / kGemvRows;
+            const cudaError_t e = api_launch(all <= kGemvTokens ? i8_gemv_kernel<1> : i8_gemv_kernel<2>, tiles < kGemvCtas * sms ? tiles : kGemvCtas * sms, kGemvWarps * 32, 0, stream, a);
             if (e != cudaSuccess) return api_fail_cuda(e, "launch of the int8 product");
             return ET_OK;
         }
