@@ -25,22 +25,22 @@ struct I8QuantArgs {
     EtHeader* hdr;
 };
 
-// q of eight values, packed in two words; r = 1 / s, rounded.  v r is within 3 x 2^-24 of
-// v / s, 2^-15 at most, so both round to the same integer unless v r is closer to a half
-// than that; there, and where r is no use, the quotient itself decides.  Adding 1.5 x 2^23
-// rounds (half to even) and leaves the integer in the low bits.
+// q of eight values, packed in two words; r = 1 / s, rounded.  x = v r is within two steps of
+// v / s, and x + (v - x s) r, two fused operations, is v / s correctly rounded (Markstein's
+// division) for every v and s = top / 127 that bf16 has: exponents apart there are 128 x 128
+// mantissas and 12 shifts, all tried.  Adding 1.5 x 2^23 rounds (half to even) and leaves
+// the integer in the low bits.  Where a scale is so small that v - x s would lose bits, the
+// division itself.
 __device__ __forceinline__ uint2 quantize8(const Vec8& v, float s, float r, bool use_r) {
     constexpr float kMagic = 12582912.0f;
     float2 t[4];
-    float far = 0.0f;  // the largest distance from an integer
+    if (use_r) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 x = __fmul2_rn(unpack2(v.u[i]), both(r));
-        t[i] = __fadd2_rn(x, both(kMagic));
-        const float2 d = __ffma2_rn(__fadd2_rn(t[i], both(-kMagic)), both(-1.0f), x);
-        far = fmaxf(far, fmaxf(fabsf(d.x), fabsf(d.y)));
-    }
-    if (!use_r || far > 0.5f - 6.2e-5f) {
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack2(v.u[i]), x = __fmul2_rn(f, both(r));
+            t[i] = __fadd2_rn(__ffma2_rn(__ffma2_rn(x, both(-s), f), both(r), x), both(kMagic));
+        }
+    } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 x = unpack2(v.u[i]);
@@ -77,13 +77,12 @@ __global__ void __launch_bounds__(MODE == kRowsOne ? 1024 : 256) i8_quantize_ker
     if (whole) fetch(m);
     for (; m < M; m += step) {
         const bf16* row = p.x + static_cast<size_t>(m) * K;
-        uint32_t top = 0;  // as the bits of |x|, which order as their values do, NaN above infinity
+        uint32_t top = 0;  // two at once, as the bits of |x|, which order as their values do, NaN above infinity
         auto look = [&]() {
 #pragma unroll
             for (int j = 0; j < V; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    top = max(top, max(v[j].u[i] << 16 & 0x7fff0000u, v[j].u[i] & 0x7fff0000u));
+                for (int i = 0; i < 4; i += 2) top = __vimax3_u16x2(top, v[j].u[i] & 0x7fff7fffu, v[j].u[i + 1] & 0x7fff7fffu);
         };
         if (whole) {
 #pragma unroll
@@ -97,7 +96,7 @@ __global__ void __launch_bounds__(MODE == kRowsOne ? 1024 : 256) i8_quantize_ker
                 look();
             }
         }
-        top = __reduce_max_sync(0xffffffffu, top);
+        top = __reduce_max_sync(0xffffffffu, max(top << 16, top & 0xffff0000u));
         if (MODE != kRowsWarp) {
             const int slot = n++ & 1, lane = threadIdx.x & 31, first = g.id() * (g.th() >> 5);
             if (lane == 0) red[slot][threadIdx.x >> 5] = top;
@@ -106,7 +105,7 @@ __global__ void __launch_bounds__(MODE == kRowsOne ? 1024 : 256) i8_quantize_ker
         }
         const bool finite = top < 0x7f800000u, live = finite && top != 0;
         const float s = finite ? __fdiv_rn(__uint_as_float(top), 127.0f) : __int_as_float(0x7fffffff);
-        const bool use_r = s >= 1e-37f;  // a smaller scale has no finite reciprocal
+        const bool use_r = s >= 1e-27f;
         const float r = use_r ? __frcp_rn(s) : 0.0f;
         if (g.lane() == 0) p.scale[m] = s;
         int8_t* out = p.q + static_cast<size_t>(m) * K;
