@@ -30,16 +30,18 @@ struct DropArgs {
 
 struct DropKey {
     uint32_t k0, k1, o0, o1;
+    // What every lane holds, by a warp reduction: the ten rounds' keys stay in uniform registers.
+    static __device__ __forceinline__ uint32_t same(uint32_t v) { return __reduce_or_sync(0xffffffffu, v); }
     __device__ __forceinline__ explicit DropKey(const DropArgs& d) {
         uint64_t s = d.seed, o = d.offset;
         if (d.d_rng && d.thr) {
             s = d.d_rng[0];
             o = d.d_rng[1];
         }
-        k0 = static_cast<uint32_t>(s);
-        k1 = static_cast<uint32_t>(s >> 32);
-        o0 = static_cast<uint32_t>(o);
-        o1 = static_cast<uint32_t>(o >> 32);
+        k0 = same(static_cast<uint32_t>(s));
+        k1 = same(static_cast<uint32_t>(s >> 32));
+        o0 = same(static_cast<uint32_t>(o));
+        o1 = same(static_cast<uint32_t>(o >> 32));
     }
 };
 
@@ -60,25 +62,26 @@ __device__ __forceinline__ uint4 drop_bits(const DropKey& k, uint32_t h8, uint32
     return make_uint4(a, b, c, d);
 }
 
-// What is dropped of eight packed bf16: ones over the elements whose 16 bits are below thr
-// (a byte permutation spreads the sign of bits - thr).
+// What is kept of eight packed bf16: ones over the elements whose 16 bits are at least thr
+// (> 0), two at a time: max(bits, thr - 1) - (thr - 1), then at most 1.
 struct Mask8 { uint32_t u[4]; };
-__device__ __forceinline__ Mask8 drop_mask8(const DropKey& k, uint32_t thr, uint32_t h8, uint32_t t) {
+__device__ __forceinline__ Mask8 keep_all() { return Mask8{{~0u, ~0u, ~0u, ~0u}}; }
+__device__ __forceinline__ Mask8 keep_mask8(const DropKey& k, uint32_t thr, uint32_t h8, uint32_t t) {
     const uint4 w = drop_bits(k, h8, t);
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    const uint32_t below = (thr - 1) * 0x10001u, minus = ((1 - thr) & 0xffffu) * 0x10001u;
     Mask8 m;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        asm("prmt.b32 %0, %1, %2, 0xffbb;" : "=r"(m.u[i]) : "r"((u[i] & 0xffffu) - thr), "r"((u[i] >> 16) - thr));
+    for (int i = 0; i < 4; ++i) m.u[i] = __viaddmin_u16x2(__vmaxu2(u[i], below), minus, 0x10001u) * 0xffffu;
     return m;
 }
 
 // Bit i: element i of the eight is dropped.
-__device__ __forceinline__ uint32_t mask_bits(const Mask8& m) {
+__device__ __forceinline__ uint32_t dropped_bits(const Mask8& m) {
     uint32_t b = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) b |= (m.u[i] & 1u) << (2 * i) | (m.u[i] >> 31) << (2 * i + 1);
-    return b;
+    return b ^ 0xffu;
 }
 
 // ---------------------------------------------------------------- dropout by itself
@@ -129,12 +132,12 @@ __global__ void __launch_bounds__(kDropThreads) dropout_vec_kernel(const Dropout
             const int i = i0 + u * kDropThreads;
             if (i >= n) break;
             const uint32_t row = H8 > 1 ? __umulhi(i, p.magic) : i;
-            const Mask8 m = p.drop.thr ? drop_mask8(key, p.drop.thr, i - row * H8, t0 + row) : Mask8{};
+            const Mask8 m = p.drop.thr ? keep_mask8(key, p.drop.thr, i - row * H8, t0 + row) : keep_all();
             const uint32_t yw[4] = {yv[u].x, yv[u].y, yv[u].z, yv[u].w}, xw[4] = {xv[u].x, xv[u].y, xv[u].z, xv[u].w};
             uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                float2 v = __fmul2_rn(unpack2(yw[j] & ~m.u[j]), both(p.drop.mul));
+                float2 v = __fmul2_rn(unpack2(yw[j] & m.u[j]), both(p.drop.mul));
                 if (x) v = __fadd2_rn(v, unpack2(xw[j]));
                 o[j] = pack_bf16(v.x, v.y);
             }
@@ -156,7 +159,7 @@ __global__ void __launch_bounds__(kDropThreads) dropout_any_kernel(const Dropout
     const int n = min(kDropCols, p.H - c0);
     const DropKey key(p.drop);
     static_assert(kDropCols / 8 == kDropThreads, "a thread draws eight elements");
-    dropped[threadIdx.x] = p.drop.thr ? mask_bits(drop_mask8(key, p.drop.thr, c0 / 8 + threadIdx.x, t)) : 0u;
+    dropped[threadIdx.x] = p.drop.thr ? dropped_bits(keep_mask8(key, p.drop.thr, c0 / 8 + threadIdx.x, t)) : 0u;
     __syncthreads();
     const size_t off = static_cast<size_t>(t) * p.H + c0;
     bf16 yv[8], xv[8];
@@ -205,39 +208,87 @@ struct LnArgs {
     float* part;          // [CTAs][2][H]
 };
 
-// N sums over the row's threads at once, as row_sum; the warps' sums (eight at most, or in
-// a warp's lanes) are added in their order.
-template <int N, int MODE, int MAXT>
-__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[N][32], const RowGroup<MODE>& g, int& n) {
+// Three sums over a warp, of which lane 0 has the first, 16 the second and 8 the third:
+// half of the lanes go on with one of them each time, nine shuffles less than one by one.
+__device__ __forceinline__ float warp_sum3(const float (&v)[3]) {
+    const int lane = threadIdx.x & 31;
+    const bool b16 = lane & 16, b8 = lane & 8;
+    float s = (b16 ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, b16 ? v[0] : v[1], 16);
+    const float c = v[2] + __shfl_xor_sync(0xffffffffu, v[2], 16);
+    s = (b8 ? c : s) + __shfl_xor_sync(0xffffffffu, b8 ? s : c, 8);
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1)
+    for (int off = 4; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    return s;
+}
+
+// One or three sums over the row's threads, the same bits in every one of them, with the
+// slots of row_sum.  The warps' sums are added in their order: eight at most are read by
+// every thread (zeros behind the row's last warp), more are added by a warp's lanes.
+template <int N>
+struct RowSums {
+    float red[2][N][64];  // eight warps of up to eight rows, or a row's 32
+    __device__ __forceinline__ void clear() {  // by the whole CTA, a barrier behind it
+        for (int i = threadIdx.x; i < 2 * N * 64; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
+    }
+    template <int MODE, int MAXT>
+    __device__ __forceinline__ void sum(float (&v)[N], const RowGroup<MODE>& g, int& n) {
+        static_assert(N == 1 || N == 3, "");
+        const int lane = threadIdx.x & 31;
+        auto in_warp = [&]() { return N == 1 ? warp_sum(v[0]) : warp_sum3(reinterpret_cast<const float (&)[3]>(v)); };
+        auto spread = [&](float s) {
+            if (N == 1) { v[0] = s; return; }
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
-    if (MODE != kRowsWarp) {
-        const int slot = n++ & 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = g.th() >> 5;
-        const int first = g.id() * warps;
-        if (lane == 0)
-#pragma unroll
-            for (int i = 0; i < N; ++i) red[slot][i][warp] = v[i];
+            for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, s, i == 0 ? 0 : i == 1 ? 16 : 8);
+        };
+        float s = in_warp();
+        if (MODE == kRowsWarp) {
+            spread(s);
+            return;
+        }
+        const int slot = n++ & 1, warps = g.th() >> 5, warp = (threadIdx.x >> 5) - g.id() * warps;
+        const int first = MAXT <= 256 ? g.id() * 8 : 0;
+        if (N == 1 ? lane == 0 : (lane & 7) == 0 && lane < 24) red[slot][N == 1 ? 0 : lane == 0 ? 0 : lane == 16 ? 1 : 2][first + warp] = s;
         g.sync();
         if (MAXT <= 256) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = 0.0f;
-#pragma unroll
-            for (int w = 0; w < 8; ++w)
-                if (w < warps)
-#pragma unroll
-                    for (int i = 0; i < N; ++i) v[i] += red[slot][i][first + w];
+            for (int i = 0; i < N; ++i) {
+                const float4 a = *reinterpret_cast<const float4*>(&red[slot][i][first]), b = *reinterpret_cast<const float4*>(&red[slot][i][first + 4]);
+                const float2 t = __fadd2_rn(__fadd2_rn(make_float2(a.x, a.y), make_float2(a.z, a.w)),
+                                            __fadd2_rn(make_float2(b.x, b.y), make_float2(b.z, b.w)));
+                v[i] = t.x + t.y;
+            }
         } else {
-            const bool in = lane < warps;
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = in ? red[slot][i][first + lane] : 0.0f;
-#pragma unroll
-            for (int off = 16; off >= 1; off >>= 1)
-#pragma unroll
-                for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+            for (int i = 0; i < N; ++i) v[i] = lane < warps ? red[slot][i][lane] : 0.0f;
+            s = in_warp();
+            spread(s);
         }
     }
+};
+
+// s / H, exactly where that is a float (a row of equal values: no deviation is made up).
+__device__ __forceinline__ float row_mean(float s, float H, float inv_H) {
+    const float q = s * inv_H;
+    return fmaf(fmaf(-q, H, s), inv_H, q);
+}
+
+// A parameter vector as floats in shared memory, each thread's own values where only it
+// reads them (the groups of a CTA write the same ones); `none` where there is no vector.
+template <bool VEC, int MODE>
+__device__ __forceinline__ void stage_param(float4* to, const bf16* from, float none, const RowGroup<MODE>& g, int H) {
+#pragma unroll
+    for (int j = 0; j < norm_v(MODE); ++j) {
+        const Vec8 v = from ? load8<VEC>(from, g, j, H) : Vec8{};
+        float4 f[2] = {make_float4(v[0], v[1], v[2], v[3]), make_float4(v[4], v[5], v[6], v[7])};
+        if (!from) f[0] = f[1] = make_float4(none, none, none, none);
+        to[2 * j * g.th() + g.lane()] = f[0];
+        to[(2 * j + 1) * g.th() + g.lane()] = f[1];
+    }
+}
+// Its pairs i and i + 1 (i even) of vector j.
+template <int MODE>
+__device__ __forceinline__ float4 param4(const float4* from, const RowGroup<MODE>& g, int j, int i) {
+    return from[(2 * j + (i >> 1)) * g.th() + g.lane()];
 }
 
 // The mask of this thread's columns.  VEC: drawn here.  Else the row's threads draw the
@@ -246,21 +297,21 @@ template <bool VEC, int MODE>
 __device__ __forceinline__ void row_mask(Mask8 (&m)[norm_v(MODE)], const DropArgs& d, const DropKey& key,
                                          const RowGroup<MODE>& g, uint8_t* bytes, int t, int H) {
 #pragma unroll
-    for (int j = 0; j < norm_v(MODE); ++j) m[j] = Mask8{};
+    for (int j = 0; j < norm_v(MODE); ++j) m[j] = keep_all();
     if (!d.thr) return;
     if (VEC) {
 #pragma unroll
-        for (int j = 0; j < norm_v(MODE); ++j) m[j] = drop_mask8(key, d.thr, g.template col<true>(j, 0) >> 3, t);
+        for (int j = 0; j < norm_v(MODE); ++j) m[j] = keep_mask8(key, d.thr, g.template col<true>(j, 0) >> 3, t);
     } else {
         g.sync();  // the last row's mask has been read
-        for (int q = g.lane(); q < (H + 7) >> 3; q += g.th()) bytes[q] = mask_bits(drop_mask8(key, d.thr, q, t));
+        for (int q = g.lane(); q < (H + 7) >> 3; q += g.th()) bytes[q] = dropped_bits(keep_mask8(key, d.thr, q, t));
         g.sync();
 #pragma unroll
         for (int j = 0; j < norm_v(MODE); ++j)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int c = g.template col<false>(j, i);
-                if (c < H && (bytes[c >> 3] >> (c & 7) & 1)) m[j].u[i >> 1] |= i & 1 ? 0xffff0000u : 0xffffu;
+                if (c < H && (bytes[c >> 3] >> (c & 7) & 1)) m[j].u[i >> 1] &= i & 1 ? 0xffffu : 0xffff0000u;
             }
     }
 }
@@ -270,42 +321,53 @@ __host__ __device__ constexpr int ln_mask_bytes(int H) { return (H + 7) / 8; }
 __host__ __device__ constexpr int ln_row_bytes(int H, bool vec, int vectors) { return vec ? vectors * 16 : norm_row_bytes(H, false); }
 
 // The mean first, then the squares of the distances from it: one pass over memory,
-// two sums over the row's threads.
+// two sums over the row's threads, the next row on its way meanwhile.
 template <bool VEC, int MODE, int MAXT>
 __global__ void __launch_bounds__(MAXT) ln_fwd_kernel(const LnArgs p) {
     constexpr int V = norm_v(MODE);
-    __shared__ float red[2][1][32];
-    extern __shared__ uint8_t masks[];  // without VEC: [groups][H / 8]
+    __shared__ RowSums<1> sums;
+    extern __shared__ __align__(16) uint8_t dyn[];  // gamma, beta; without VEC [groups][H / 8] mask bytes
     int n_sums = 0;
     const RowGroup<MODE> g(p.row_threads);
+    sums.clear();
     grid_begin();
     bool ok;
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
     const int H = p.H;
-    const DropKey key(p.drop);
-    uint8_t* bytes = masks + g.id() * ln_mask_bytes(H);
-    for (int t = blockIdx.x * g.groups() + g.id(); t < T; t += gridDim.x * g.groups()) {
-        const size_t off = static_cast<size_t>(t) * H;
-        Vec8 xv[V], yv[V];
+    float4* const gam = reinterpret_cast<float4*>(dyn);
+    float4* const bet = gam + 2 * V * g.th();
+    uint8_t* bytes = reinterpret_cast<uint8_t*>(bet + 2 * V * g.th()) + g.id() * ln_mask_bytes(H);
+    Vec8 xv[V], yv[V];
+    auto fetch = [&](int t) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            xv[j] = load8<VEC>(p.x + off, g, j, H);
-            yv[j] = p.y ? load8<VEC>(p.y + off, g, j, H) : Vec8{};
+            xv[j] = t < T ? load8<VEC>(p.x + static_cast<size_t>(t) * H, g, j, H) : Vec8{};
+            yv[j] = p.y && t < T ? load8<VEC>(p.y + static_cast<size_t>(t) * H, g, j, H) : Vec8{};
         }
+    };
+    int t = blockIdx.x * g.groups() + g.id();
+    fetch(t);
+    const DropKey key(p.drop);
+    stage_param<VEC>(gam, p.gamma, 1.0f, g, H);
+    stage_param<VEC>(bet, p.beta, 0.0f, g, H);
+    __syncthreads();  // (for the cleared sums)
+    for (; t < T; t += gridDim.x * g.groups()) {
+        const size_t off = static_cast<size_t>(t) * H;
         float2 z[V][4], s2 = both(0.0f);
         if (p.y) {
             Mask8 m[V];
-            row_mask<VEC>(m, p.drop, key, g, bytes, t, H);  // while the loads are on their way
+            row_mask<VEC>(m, p.drop, key, g, bytes, t, H);
 #pragma unroll
             for (int j = 0; j < V; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) z[j][i] = __ffma2_rn(unpack2(yv[j].u[i] & ~m[j].u[i]), both(p.drop.mul), unpack2(xv[j].u[i]));
+                for (int i = 0; i < 4; ++i) z[j][i] = __ffma2_rn(unpack2(yv[j].u[i] & m[j].u[i]), both(p.drop.mul), unpack2(xv[j].u[i]));
         } else {
 #pragma unroll
             for (int j = 0; j < V; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) z[j][i] = unpack2(xv[j].u[i]);
         }
+        fetch(t + gridDim.x * g.groups());
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             if (p.x_out) store8<VEC>(p.x_out + off, g, j, H, &z[j][0].x);
@@ -313,12 +375,11 @@ __global__ void __launch_bounds__(MAXT) ln_fwd_kernel(const LnArgs p) {
             for (int i = 0; i < 4; ++i) s2 = __fadd2_rn(s2, z[j][i]);  // 0 past H
         }
         float s[1] = {s2.x + s2.y};
-        row_sums<1, MODE, MAXT>(s, red, g, n_sums);
-        const float mean = __fdiv_rn(s[0], static_cast<float>(H));  // exact for a row of equal values: no deviation is made up
+        sums.template sum<MODE, MAXT>(s, g, n_sums);
+        const float mean = row_mean(s[0], static_cast<float>(H), p.inv_H);
         s2 = both(0.0f);
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            {
+        for (int j = 0; j < V; ++j) {
             const float mj = VEC && g.template col<VEC>(j, 0) >= H ? 0.0f : mean;  // 0 behind H, as z
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -329,16 +390,18 @@ __global__ void __launch_bounds__(MAXT) ln_fwd_kernel(const LnArgs p) {
                 }
                 s2 = __ffma2_rn(z[j][i], z[j][i], s2);
             }
-            }
+        }
         s[0] = s2.x + s2.y;
-        row_sums<1, MODE, MAXT>(s, red, g, n_sums);
+        sums.template sum<MODE, MAXT>(s, g, n_sums);
         const float r = rsqrtf(s[0] * p.inv_H + p.eps);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const Vec8 one{{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u}};
-            const Vec8 gv = p.gamma ? load8<VEC>(p.gamma, g, j, H) : one, bv = p.beta ? load8<VEC>(p.beta, g, j, H) : Vec8{};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) z[j][i] = __ffma2_rn(__fmul2_rn(z[j][i], both(r)), unpack2(gv.u[i]), unpack2(bv.u[i]));
+            for (int i = 0; i < 4; i += 2) {
+                const float4 gv = param4(gam, g, j, i), bv = param4(bet, g, j, i);
+                z[j][i] = __ffma2_rn(__fmul2_rn(z[j][i], both(r)), make_float2(gv.x, gv.y), make_float2(bv.x, bv.y));
+                z[j][i + 1] = __ffma2_rn(__fmul2_rn(z[j][i + 1], both(r)), make_float2(gv.z, gv.w), make_float2(bv.z, bv.w));
+            }
             store8<VEC>(p.x_hat + off, g, j, H, &z[j][0].x);
         }
     }
@@ -362,18 +425,21 @@ __global__ void __launch_bounds__(MAXT) ln_fwd_kernel(const LnArgs p) {
 template <bool VEC, int MODE, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT > 512 ? 1 : 512 / MAXT) ln_bwd_kernel(const LnArgs p) {
     constexpr int V = norm_v(MODE);
-    __shared__ float red1[2][1][32], red3[2][3][32];
-    // [groups][bufs][A] rows; gamma, each thread's own 16 values together; [groups][2][H]
+    __shared__ RowSums<1> sums1;
+    __shared__ RowSums<3> sums3;
+    // [groups][bufs][A] rows; gamma as floats; [groups][2][H]
     // floats where several groups' sums meet; without VEC [groups][H / 8] mask bytes
     extern __shared__ __align__(16) uint8_t dyn[];
     int n1 = 0, n3 = 0;
     const RowGroup<MODE> grp(p.row_threads);
+    sums1.clear();
+    sums3.clear();
     grid_begin();
     bool ok;
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
     if (!ok) return;
     const int H = p.H, H2 = H * 2, groups = grp.groups(), bufs = p.bufs;
-    const int row_b = ln_row_bytes(H, VEC, grp.th() * V), par_b = grp.th() * V * 16;
+    const int row_b = ln_row_bytes(H, VEC, grp.th() * V), par_b = grp.th() * V * 32;
     const int ny = p.y ? 1 : 0, nd = p.d_x_out ? 1 : 0, A = 2 + ny + nd;  // staged: x, d_x_hat, y, d_x_out
     const int c0 = grp.template col<true>(0, 0), c1 = grp.template col<true>(1, 0);
     const bool in0 = c0 < H, in1 = V > 1 && c1 < H;  // VEC only
@@ -381,7 +447,7 @@ __global__ void __launch_bounds__(MAXT, MAXT > 512 ? 1 : 512 / MAXT) ln_bwd_kern
     uint8_t* par = dyn + static_cast<size_t>(groups) * bufs * A * row_b;
     float* merge = reinterpret_cast<float*>(par + par_b);
     uint8_t* bytes = par + par_b + (MODE != kRowsOne && groups > 1 ? groups * 2 * H * 4 : 0) + grp.id() * ln_mask_bytes(H);
-    par += grp.lane() * 16;
+    float4* const gam = reinterpret_cast<float4*>(par);
     const DropKey key(p.drop);
 
     const bf16* const src[4] = {p.x, p.d_x_hat, ny ? p.y : p.d_x_out, p.d_x_out};
@@ -425,11 +491,8 @@ __global__ void __launch_bounds__(MAXT, MAXT > 512 ? 1 : 512 / MAXT) ln_bwd_kern
             if (V > 1 && !in1) *reinterpret_cast<uint4*>(mine + a * row_b + c1 * 2) = make_uint4(0, 0, 0, 0);
         }
     if (bufs == 2) stage(t0 + grp.id(), 0);
-#pragma unroll
-    for (int j = 0; j < V; ++j) {  // every thread reads back what it wrote (the groups write the same)
-        const Vec8 v = p.gamma ? load8<VEC>(p.gamma, grp, j, H) : Vec8{{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u}};
-        *reinterpret_cast<uint4*>(par + j * grp.th() * 16) = make_uint4(v.u[0], v.u[1], v.u[2], v.u[3]);
-    }
+    stage_param<VEC>(gam, p.gamma, 1.0f, grp, H);
+    __syncthreads();  // (for the cleared sums)
     float2 a_g[V][4], a_b[V][4];
 #pragma unroll
     for (int j = 0; j < V; ++j)
@@ -538,7 +601,7 @@ __global__ void __launch_bounds__(MAXT, MAXT > 512 ? 1 : 512 / MAXT) ln_bwd_kern
                 for (int j = 0; j < V; ++j) {
                     const uint4 y = get(2, j);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) z[j][i] = __ffma2_rn(unpack2(word(y, i) & ~m[j].u[i]), both(p.drop.mul), z[j][i]);
+                    for (int i = 0; i < 4; ++i) z[j][i] = __ffma2_rn(unpack2(word(y, i) & m[j].u[i]), both(p.drop.mul), z[j][i]);
                 }
             }
 #pragma unroll
@@ -546,46 +609,49 @@ __global__ void __launch_bounds__(MAXT, MAXT > 512 ? 1 : 512 / MAXT) ln_bwd_kern
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s2 = __fadd2_rn(s2, z[j][i]);
             float s1[1] = {s2.x + s2.y};
-            row_sums<1, MODE, MAXT>(s1, red1, grp, n1);
-            const float mean = __fdiv_rn(s1[0], static_cast<float>(H));
+            sums1.template sum<MODE, MAXT>(s1, grp, n1);
+            const float mean = row_mean(s1[0], static_cast<float>(H), p.inv_H);
             float2 dd = both(0.0f), sa = both(0.0f), sad = both(0.0f);
-            uint4 dh[V];
+            float2 h[V][4];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                dh[j] = get(1, j);
-                const uint4 gm = *reinterpret_cast<const uint4*>(par + j * grp.th() * 16);
+                const uint4 dh = get(1, j);
                 const float mj = VEC && !(j ? in1 : in0) ? 0.0f : mean;  // 0 behind H, as z
+                float4 gm{};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
+                    if (i % 2 == 0) gm = param4(gam, grp, j, i);
+                    h[j][i] = unpack2(word(dh, i));
                     z[j][i] = __fadd2_rn(z[j][i], both(-mj));
                     if (!VEC) {
                         if (grp.template col<VEC>(j, 2 * i) >= H) z[j][i].x = 0.0f;
                         if (grp.template col<VEC>(j, 2 * i + 1) >= H) z[j][i].y = 0.0f;
                     }
-                    const float2 a = __fmul2_rn(unpack2(word(dh[j], i)), unpack2(word(gm, i)));
+                    const float2 a = __fmul2_rn(h[j][i], i % 2 ? make_float2(gm.z, gm.w) : make_float2(gm.x, gm.y));
                     dd = __ffma2_rn(z[j][i], z[j][i], dd);
                     sa = __fadd2_rn(sa, a);
                     sad = __ffma2_rn(a, z[j][i], sad);
                 }
             }
             float s3[3] = {dd.x + dd.y, sa.x + sa.y, sad.x + sad.y};
-            row_sums<3, MODE, MAXT>(s3, red3, grp, n3);
+            sums3.template sum<MODE, MAXT>(s3, grp, n3);
             const float r = rsqrtf(s3[0] * p.inv_H + p.eps);
             const float ra = -r * (s3[1] * p.inv_H), k = -r * r * (s3[2] * p.inv_H);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const uint4 gm = *reinterpret_cast<const uint4*>(par + j * grp.th() * 16);
                 const uint4 dz = nd ? get(2 + ny, j) : make_uint4(0, 0, 0, 0);
                 uint32_t odx[4];
                 float2 D[4];
+                float4 gm{};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 h = unpack2(word(dh[j], i)), n = __fmul2_rn(z[j][i], both(r));
+                    if (i % 2 == 0) gm = param4(gam, grp, j, i);
+                    const float2 n = __fmul2_rn(z[j][i], both(r));
                     D[i] = __fadd2_rn(unpack2(word(dz, i)), both(ra));
-                    D[i] = __ffma2_rn(__fmul2_rn(h, unpack2(word(gm, i))), both(r), D[i]);
+                    D[i] = __ffma2_rn(__fmul2_rn(h[j][i], i % 2 ? make_float2(gm.z, gm.w) : make_float2(gm.x, gm.y)), both(r), D[i]);
                     D[i] = __ffma2_rn(n, both(k), D[i]);
-                    a_g[j][i] = __ffma2_rn(h, n, a_g[j][i]);
-                    a_b[j][i] = __fadd2_rn(a_b[j][i], h);
+                    a_g[j][i] = __ffma2_rn(h[j][i], n, a_g[j][i]);
+                    a_b[j][i] = __fadd2_rn(a_b[j][i], h[j][i]);
                     odx[i] = pack_bf16(D[i].x, D[i].y);
                 }
                 put_row(p.dx, j, odx);
@@ -593,7 +659,7 @@ __global__ void __launch_bounds__(MAXT, MAXT > 512 ? 1 : 512 / MAXT) ln_bwd_kern
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         D[i] = __fmul2_rn(D[i], both(p.drop.mul));
-                        odx[i] = pack_bf16(D[i].x, D[i].y) & ~m[j].u[i];
+                        odx[i] = pack_bf16(D[i].x, D[i].y) & m[j].u[i];
                     }
                     put_row(p.dy, j, odx);
                 }
@@ -688,24 +754,33 @@ int ln_check(const void* x, const void* y, const void* gamma, const void* beta, 
     return ET_OK;
 }
 
-template <bool VEC>
-cudaError_t launch_ln_fwd(LnArgs a, int rows, int sms, void* stream) {
-    a.row_threads = norm_threads(a.H);
-    const RowMode mode = norm_mode(a.H, a.row_threads);
-    const int groups = norm_groups(a.row_threads, rows), th = a.row_threads * groups;
-    const int need = (rows + groups - 1) / groups, most = sms * (1024 / th);
-    const int grid = need < most ? need : most;
-    const int smem = !VEC && a.drop.thr ? groups * ln_mask_bytes(a.H) : 0;
-    auto kernel = mode == kRowsWarp ? ln_fwd_kernel<VEC, kRowsWarp, 256> : mode == kRowsGroup ? ln_fwd_kernel<VEC, kRowsGroup, 256>
-                : th <= 256 ? ln_fwd_kernel<VEC, kRowsOne, 256> : ln_fwd_kernel<VEC, kRowsOne, 1024>;
-    return api_launch(kernel, grid, th, smem, stream, a);
-}
-
 struct LnLaunch {
     int dev, sms, rows, parts_max;
     int* parts;
     void* stream;
 };
+
+template <bool VEC, int MODE, int MAXT>
+cudaError_t launch_ln_fwd_rows(LnArgs a, const LnLaunch& l) {
+    static SmemOptIn opt;
+    auto kernel = ln_fwd_kernel<VEC, MODE, MAXT>;
+    const cudaError_t e = api_smem_opt_in(opt, l.dev, kernel, kSmemLimit - 2048);
+    if (e != cudaSuccess) return e;
+    const int groups = norm_groups(a.row_threads, l.rows), th = a.row_threads * groups;
+    const int need = (l.rows + groups - 1) / groups, most = l.sms * (1024 / th);
+    const int smem = a.row_threads * norm_v(MODE) * 64 + (!VEC && a.drop.thr ? groups * ln_mask_bytes(a.H) : 0);
+    return api_launch(kernel, need < most ? need : most, th, smem, l.stream, a);
+}
+
+template <bool VEC>
+cudaError_t launch_ln_fwd(LnArgs a, const LnLaunch& l) {
+    a.row_threads = norm_threads(a.H);
+    const RowMode mode = norm_mode(a.H, a.row_threads);
+    if (mode == kRowsWarp) return launch_ln_fwd_rows<VEC, kRowsWarp, 256>(a, l);
+    if (mode == kRowsGroup) return launch_ln_fwd_rows<VEC, kRowsGroup, 256>(a, l);
+    if (a.row_threads <= 256) return launch_ln_fwd_rows<VEC, kRowsOne, 256>(a, l);
+    return launch_ln_fwd_rows<VEC, kRowsOne, 1024>(a, l);
+}
 
 template <bool VEC, int MODE, int MAXT>
 cudaError_t launch_ln_bwd_rows(LnArgs a, const LnLaunch& l) {
@@ -719,7 +794,7 @@ cudaError_t launch_ln_bwd_rows(LnArgs a, const LnLaunch& l) {
     *l.parts = n = n < most ? n : most;
     const int A = 2 + (a.y ? 1 : 0) + (a.d_x_out ? 1 : 0);
     a.bufs = a.H <= 8192 ? 2 : 1;
-    const int smem = groups * a.bufs * A * ln_row_bytes(a.H, VEC, a.row_threads * norm_v(MODE)) + a.row_threads * norm_v(MODE) * 16 +
+    const int smem = groups * a.bufs * A * ln_row_bytes(a.H, VEC, a.row_threads * norm_v(MODE)) + a.row_threads * norm_v(MODE) * 32 +
                      (MODE != kRowsOne && groups > 1 ? groups * 2 * a.H * 4 : 0) +
                      (!VEC && a.drop.thr ? groups * ln_mask_bytes(a.H) : 0);
     return api_launch(kernel, n, th, smem, l.stream, a);
@@ -829,8 +904,8 @@ int et_layer_norm(const void* x, const void* y, const void* gamma, const void* b
         a.x_out = static_cast<bf16*>(x_out);
         a.x_hat = static_cast<bf16*>(x_hat);
         const int rows = d_T ? T_max : T;
-        const cudaError_t e = norm_vec(H, {x, y, gamma, beta, x_out, x_hat}) ? launch_ln_fwd<true>(a, rows, sms, stream)
-                                                                            : launch_ln_fwd<false>(a, rows, sms, stream);
+        const LnLaunch l{dev, sms, rows, 0, nullptr, stream};
+        const cudaError_t e = norm_vec(H, {x, y, gamma, beta, x_out, x_hat}) ? launch_ln_fwd<true>(a, l) : launch_ln_fwd<false>(a, l);
         if (e != cudaSuccess) return api_fail_cuda(e, "launch of the layer norm kernel");
         return ET_OK;
     });
