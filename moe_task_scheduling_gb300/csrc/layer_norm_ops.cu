@@ -32,9 +32,10 @@ struct DropKey {
     uint32_t k0, k1, o0, o1;
     // What every lane holds, by a warp reduction: the ten rounds' keys stay in uniform registers.
     static __device__ __forceinline__ uint32_t same(uint32_t v) { return __reduce_or_sync(0xffffffffu, v); }
-    __device__ __forceinline__ explicit DropKey(const DropArgs& d) {
+    __device__ __forceinline__ explicit DropKey(const DropArgs& d) : k0(0), k1(0), o0(0), o1(0) {
+        if (!d.thr) return;
         uint64_t s = d.seed, o = d.offset;
-        if (d.d_rng && d.thr) {
+        if (d.d_rng) {
             s = d.d_rng[0];
             o = d.d_rng[1];
         }
@@ -689,7 +690,8 @@ struct LnSumArgs {
     int T_max;
 };
 
-// Column sums of the partial rows: 32 columns x 32 row groups a CTA.
+// Column sums of the partial rows: 32 columns x 32 row groups a CTA, a thread's loads all
+// on their way at once.
 __global__ void __launch_bounds__(1024) ln_sum_kernel(const LnSumArgs p) {
     __shared__ float red[32][33];
     grid_begin();
@@ -698,11 +700,15 @@ __global__ void __launch_bounds__(1024) ln_sum_kernel(const LnSumArgs p) {
     const int arr = p.arr[blockIdx.y];
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
-    float s = 0.0f;
-    if (c < p.H)
-#pragma unroll 10
-        for (int g = grp; g < p.parts; g += 32)
-            s += __ldcg(p.part + (static_cast<size_t>(g) * 2 + arr) * p.H + c);
+    constexpr int kLoads = (kLnParts + 31) / 32;
+    float v[kLoads], s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int g = grp + 32 * i;
+        v[i] = g < p.parts && c < p.H ? __ldcg(p.part + (static_cast<size_t>(g) * 2 + arr) * p.H + c) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) s += v[i];
     red[grp][lane] = s;
     __syncthreads();
     s = warp_sum(red[lane][grp]);  // warp grp: its column's 32 groups
@@ -764,7 +770,7 @@ template <bool VEC, int MODE, int MAXT>
 cudaError_t launch_ln_fwd_rows(LnArgs a, const LnLaunch& l) {
     static SmemOptIn opt;
     auto kernel = ln_fwd_kernel<VEC, MODE, MAXT>;
-    const cudaError_t e = api_smem_opt_in(opt, l.dev, kernel, kSmemLimit - 2048);
+    const cudaError_t e = api_smem_opt_in(opt, l.dev, kernel, kSmemLimit - 4096);
     if (e != cudaSuccess) return e;
     const int groups = norm_groups(a.row_threads, l.rows), th = a.row_threads * groups;
     const int need = (l.rows + groups - 1) / groups, most = l.sms * (1024 / th);
@@ -786,7 +792,7 @@ template <bool VEC, int MODE, int MAXT>
 cudaError_t launch_ln_bwd_rows(LnArgs a, const LnLaunch& l) {
     static SmemOptIn opt;
     auto kernel = ln_bwd_kernel<VEC, MODE, MAXT>;
-    const cudaError_t e = api_smem_opt_in(opt, l.dev, kernel, kSmemLimit - 2048);
+    const cudaError_t e = api_smem_opt_in(opt, l.dev, kernel, kSmemLimit - 4096);
     if (e != cudaSuccess) return e;
     const int groups = norm_groups(a.row_threads, l.rows), th = a.row_threads * groups;
     const int need = (l.rows + groups - 1) / groups, most = th <= kNormCtaThreads ? 2 * l.sms : l.sms;
