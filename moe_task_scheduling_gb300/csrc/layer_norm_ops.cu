@@ -209,19 +209,6 @@ struct LnArgs {
     float* part;          // [CTAs][2][H]
 };
 
-// Three sums over a warp, of which lane 0 has the first, 16 the second and 8 the third:
-// half of the lanes go on with one of them each time, nine shuffles less than one by one.
-__device__ __forceinline__ float warp_sum3(const float (&v)[3]) {
-    const int lane = threadIdx.x & 31;
-    const bool b16 = lane & 16, b8 = lane & 8;
-    float s = (b16 ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, b16 ? v[0] : v[1], 16);
-    const float c = v[2] + __shfl_xor_sync(0xffffffffu, v[2], 16);
-    s = (b8 ? c : s) + __shfl_xor_sync(0xffffffffu, b8 ? s : c, 8);
-#pragma unroll
-    for (int off = 4; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    return s;
-}
-
 // One or three sums over the row's threads, the same bits in every one of them, with the
 // slots of row_sum.  The warps' sums are added in their order: eight at most are read by
 // every thread (zeros behind the row's last warp), more are added by a warp's lanes.

@@ -661,7 +661,7 @@ struct GroupBwdArgs {
     float* d_logits;
     const int32_t* d_T;
     int T_host, T_max, E, k;
-    int sigmoid, renorm;
+    int renorm;
     float inv_scale;        // 0 where scale is
     EtHeader* hdr;
 };
@@ -671,16 +671,34 @@ struct GroupBwdArgs {
 //   d_L[e] = q_e (d_loss p_e (C_e - sum C p) + sum_{j: idx_j = e} (W_j - r_j)) - u p_e,
 //   r_j = w_j sum W / scale with renorm; u = sum W for softmax without; else 0.
 // A token is routed if it has an index that is not -1.
-template <int EPL>
+//
+// VEC (E a multiple of four, tensors 16-byte aligned): a lane has four neighbours in one
+// access.
+template <int EPL, bool SIGMOID, bool VEC>
 __global__ void __launch_bounds__(256) router_groups_bwd_kernel(const GroupBwdArgs p) {
     constexpr uint32_t kAll = 0xffffffffu;
-    __shared__ float add_s[8][32 * EPL];  // a row's gradients through the gate weights, by expert
+    constexpr int W4 = VEC ? 4 : 1;
+    static_assert(EPL % W4 == 0, "");
+    __shared__ __align__(16) float add_s[8][32 * EPL];  // a row's gradients through the gate weights, by expert
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
     const int E = p.E, k = p.k;
     grid_begin();
     bool ok;
     const int T = row_count(p.d_T, p.T_host, p.T_max, p.hdr, &ok);
     if (!ok) return;
+    auto expert = [&](int i) { return (lane + 32 * (i / W4)) * W4 + i % W4; };  // this lane's i-th
+    auto read = [&](const float* from, float (&to)[EPL], float none) {
+#pragma unroll
+        for (int i = 0; i < EPL; i += W4) {
+            if (VEC) {
+                float4 q = make_float4(none, none, none, none);
+                if (expert(i) < E) q = *reinterpret_cast<const float4*>(from + expert(i));
+                to[i] = q.x; to[i + 1 < EPL ? i + 1 : i] = q.y; to[i + 2 < EPL ? i + 2 : i] = q.z; to[i + 3 < EPL ? i + 3 : i] = q.w;
+            } else {
+                to[i] = expert(i) < E ? from[expert(i)] : none;
+            }
+        }
+    };
     float* add = add_s[warp];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) add[lane + 32 * i] = 0.0f;
@@ -692,16 +710,14 @@ __global__ void __launch_bounds__(256) router_groups_bwd_kernel(const GroupBwdAr
     };
     auto load = [&](int t, Row& r) {
         const bool in = t < T, sel = in && lane < k;
-        const float* L = p.logits + static_cast<size_t>(t) * E;
         const size_t o = static_cast<size_t>(t) * k + lane;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) r.v[i] = in && lane + 32 * i < E ? L[lane + 32 * i] : -INFINITY;
+        if (in) read(p.logits + static_cast<size_t>(t) * E, r.v, -INFINITY);
         r.on = in && (!p.mask || p.mask[t] != 0);
         r.e = sel ? p.idx[o] : -1;
         r.w = sel ? p.w[o] : 0.0f;
         r.dw = sel && p.d_w ? p.d_w[o] : 0.0f;
     };
-    Row nx;
+    Row nx{};
     load(t0, nx);
     const int n = *p.n_routed;
     const float rows = n > 0 ? static_cast<float>(n) : 1.0f;
@@ -709,49 +725,62 @@ __global__ void __launch_bounds__(256) router_groups_bwd_kernel(const GroupBwdAr
     float cost[EPL];  // E counts / (n^2 k): what a unit of p on expert e costs
     const float per = static_cast<float>(E) / (rows * k) / rows;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) cost[i] = lane + 32 * i < E ? per * static_cast<float>(p.counts[lane + 32 * i]) : 0.0f;
+    for (int i = 0; i < EPL; ++i) cost[i] = expert(i) < E ? per * static_cast<float>(p.counts[expert(i)]) : 0.0f;
     for (int t = t0; t < T; t += step) {
         const Row c = nx;
         load(t + step, nx);
-        float top = c.v[0];
-#pragma unroll
-        for (int i = 1; i < EPL; ++i) top = fmaxf(top, c.v[i]);
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
         const bool sel = c.e >= 0 && c.e < E;
         const bool any = __any_sync(kAll, c.e >= 0), live = c.on && any;
         float d[EPL];
         if (live) {
+            float top = c.v[0];
+#pragma unroll
+            for (int i = 1; i < EPL; ++i) top = fmaxf(top, c.v[i]);
+            // Sigmoid scores that are all tiny: as ratios of e^L, like softmax's.
+            const bool ratio = !SIGMOID || __all_sync(kAll, top < -60.0f);
+            if (ratio)
+#pragma unroll
+                for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
             const float W = c.e >= 0 ? c.w * c.dw : 0.0f;
-            const bool ratio = !p.sigmoid || top < -60.0f;  // scores as ratios of e^L
-            float s[EPL], q[EPL], S = 0.0f, cp = 0.0f, sum = W;
+            float s[EPL], q[EPL], sums[3] = {0.0f, 0.0f, W};
+            // (-inf: s = 0; NaN: s is NaN.  A row of -inf alone has no index.)
+            if (SIGMOID) {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) {
+                    const float e = __expf(-fabsf(c.v[i]));  // sigmoid of either sign without overflow
+                    const float h = rcp_fast(1.0f + e), lo = e * h;
+                    s[i] = c.v[i] < 0.0f ? lo : h;
+                    q[i] = c.v[i] < 0.0f ? h : lo;
+                }
+            }
+            if (ratio) {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) {
+                    s[i] = c.v[i] == -INFINITY ? 0.0f : __expf(c.v[i] - top);
+                }
+            }
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
-                const bool there = !(c.v[i] == -INFINITY);
-                const float e = __expf(-fabsf(c.v[i]));  // sigmoid of either sign without overflow
-                const float h = __fdividef(1.0f, 1.0f + e);
-                const float lo = e * h;
-                s[i] = !there ? 0.0f : ratio ? __expf(c.v[i] - top) : c.v[i] < 0.0f ? lo : h;
-                q[i] = !p.sigmoid ? 1.0f : c.v[i] < 0.0f ? h : lo;
-                if (c.v[i] != c.v[i]) s[i] = q[i] = c.v[i];
-                S += s[i];
-                cp += s[i] * cost[i];
+                sums[0] += s[i];
+                sums[1] += s[i] * cost[i];
             }
-#pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) {  // three sums, interleaved
-                S += __shfl_xor_sync(kAll, S, off);
-                cp += __shfl_xor_sync(kAll, cp, off);
-                sum += __shfl_xor_sync(kAll, sum, off);
-            }
-            const float inv = __fdividef(1.0f, S);
-            cp *= inv;
-            const float u = !p.renorm && !p.sigmoid ? sum : 0.0f;
+            const float mine = warp_sum3(sums);
+            const float inv = rcp_fast(__shfl_sync(kAll, mine, 0));
+            const float cp = __shfl_sync(kAll, mine, 16) * inv, sum = __shfl_sync(kAll, mine, 8);
+            const float u = !p.renorm && !SIGMOID ? sum : 0.0f;
             if (p.d_w) {
                 // an index outside [0, E) adds nothing; one that comes twice adds twice
                 if (sel) atomicAdd(add + c.e, p.renorm ? W - c.w * p.inv_scale * sum : W);
                 __syncwarp();
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) d[i] = add[lane + 32 * i];
+                for (int i = 0; i < EPL; i += W4) {
+                    if (VEC) {
+                        const float4 a = *reinterpret_cast<const float4*>(add + expert(i));
+                        d[i] = a.x; d[i + 1 < EPL ? i + 1 : i] = a.y; d[i + 2 < EPL ? i + 2 : i] = a.z; d[i + 3 < EPL ? i + 3 : i] = a.w;
+                    } else {
+                        d[i] = add[expert(i)];
+                    }
+                }
                 __syncwarp();
                 if (sel) add[c.e] = 0.0f;
                 __syncwarp();
@@ -762,7 +791,9 @@ __global__ void __launch_bounds__(256) router_groups_bwd_kernel(const GroupBwdAr
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
                 const float pr = s[i] * inv;
-                d[i] = q[i] * (dl * pr * (cost[i] - cp) + d[i]) - u * pr;
+                d[i] = dl * pr * (cost[i] - cp) + d[i];
+                if (SIGMOID) d[i] *= q[i];
+                else d[i] -= u * pr;
             }
         } else {
 #pragma unroll
@@ -770,9 +801,17 @@ __global__ void __launch_bounds__(256) router_groups_bwd_kernel(const GroupBwdAr
         }
         float* out = p.d_logits + static_cast<size_t>(t) * E;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (lane + 32 * i < E) out[lane + 32 * i] = d[i];
+        for (int i = 0; i < EPL; i += W4)
+            if (expert(i) < E) {
+                if (VEC) *reinterpret_cast<float4*>(out + expert(i)) = make_float4(d[i], d[i + 1 < EPL ? i + 1 : i], d[i + 2 < EPL ? i + 2 : i], d[i + 3 < EPL ? i + 3 : i]);
+                else out[expert(i)] = d[i];
+            }
     }
+}
+
+template <int EPL, bool VEC>
+auto pick_bwd(bool sigmoid) {
+    return sigmoid ? router_groups_bwd_kernel<EPL, true, VEC> : router_groups_bwd_kernel<EPL, false, VEC>;
 }
 
 template <int EPL>
@@ -860,13 +899,15 @@ int et_router_groups_bwd(const float* logits, const uint8_t* token_mask, int sco
         int dev = 0, sms = 0;
         if ((rc = api_device(&dev, &sms))) return rc;
         const GroupBwdArgs a{logits, token_mask, topk_idx, topk_w, expert_counts, n_routed, d_loss, d_topk_w, d_logits, d_T,
-                             T, T_max, E, k, score == ET_SCORE_SIGMOID, renorm != 0, scale != 0.0f ? 1.0f / scale : 0.0f,
+                             T, T_max, E, k, renorm != 0, scale != 0.0f ? 1.0f / scale : 0.0f,
                              static_cast<EtHeader*>(workspace)};
         const int rows = d_T ? T_max : T;
         int grid = ceil_div_i(rows, 8);
         grid = grid < 8 * sms ? grid : 8 * sms;
-        auto kernel = E <= 32 ? router_groups_bwd_kernel<1> : E <= 64 ? router_groups_bwd_kernel<2>
-                    : E <= 128 ? router_groups_bwd_kernel<4> : router_groups_bwd_kernel<8>;
+        const bool sig = score == ET_SCORE_SIGMOID, vec = E > 64 && E % 4 == 0 && api_aligned(logits, 16) && api_aligned(d_logits, 16);
+        auto kernel = E <= 32 ? pick_bwd<1, false>(sig) : E <= 64 ? pick_bwd<2, false>(sig)
+                    : E <= 128 ? (vec ? pick_bwd<4, true>(sig) : pick_bwd<4, false>(sig))
+                               : (vec ? pick_bwd<8, true>(sig) : pick_bwd<8, false>(sig));
         const cudaError_t e = api_launch(kernel, grid, 256, 0, stream, a);
         if (e != cudaSuccess) return api_fail_cuda(e, "launch of the grouped router's backward kernel");
         return ET_OK;

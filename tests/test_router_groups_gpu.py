@@ -304,3 +304,24 @@ def test_no_bias_and_one_group_choose_as_the_plain_router(cuda_lib):
     check(o["w"], w, 64 * U * w.double().cpu(), "w")
     o, _ = _forward(cuda_lib, logits.cpu(), k, 1, 1, sigmoid=True)  # sigmoid orders as its logits do
     assert torch.equal(o["idx"], idx)
+
+
+@pytest.mark.parametrize("En", [40, 128, 160, 256])
+@pytest.mark.parametrize("sigmoid", [True, False])
+def test_any_alignment(cuda_lib, En, sigmoid):
+    """Logits and gradients that start anywhere: what aligned ones give."""
+    T, k = 77, 4
+    g = _gen(En)
+    logits, dl, dw = torch.randn(T, En, generator=g), torch.randn(1, generator=g), torch.randn(T, k, generator=g).cuda()
+    o, ws = _forward(cuda_lib, logits, k, 4, 2, sigmoid=sigmoid)
+    want = _backward(cuda_lib, o, ws, logits, dl, dw, sigmoid=sigmoid)
+    score = cuda_lib.ET_SCORE_SIGMOID if sigmoid else cuda_lib.ET_SCORE_SOFTMAX
+    for shift in (1, 2, 3):
+        lo, d = (torch.zeros(T * En + 4, device="cuda")[shift:shift + T * En].view(T, En) for _ in range(2))
+        lo.copy_(logits)
+        idx, w = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+        cuda_lib.et_router_groups(lo, idx, w, score=score, n_groups=4, k_groups=2, workspace=ws)
+        assert torch.equal(idx, o["idx"]) and torch.equal(w, o["w"])
+        cuda_lib.et_router_groups_bwd(lo, idx, w, o["counts"], o["n"], d, score=score, d_loss=dl.cuda(), d_topk_w=dw, workspace=ws)
+        # other lanes hold other experts: the sums over a row go in another order, a few roundings of their terms
+        check(d, want.cpu().double(), 96 * U * (want.cpu().double().abs() + want.cpu().double().abs().amax(-1, keepdim=True)), "d_logits")
