@@ -44,10 +44,10 @@
  * Supported shapes: H and F multiples of 128; 1 <= k <= min(E, 8);
  * 1 <= E <= 256; 0 <= T <= T_max.  Anything else returns ET_ERR_UNSUPPORTED
  * or ET_ERR_INVALID.  T == 0 launches nothing and leaves `out` untouched.
- * The router, norm and 4-bit calls state their own shapes.  One workspace may
- * serve several of those three, one call after the other, if it has the bytes
- * of the largest; it must not serve the other calls too, whose counters would
- * lie under their data.
+ * The router, norm, dropout, int8 and 4-bit calls (et_router_topk and all that
+ * follow it here) state their own shapes.  One workspace may serve several of
+ * them, one call after the other, if it has the bytes of the largest; it must
+ * not serve the other calls too, whose counters would lie under their data.
  */
 #ifndef ETMOE_H
 #define ETMOE_H
@@ -571,9 +571,11 @@ int et_layer_norm_bwd(const void* x, const void* y, const void* gamma, float eps
  * bits on every run of a shape.
  *
  * K is a multiple of 16 up to 65536, 1 <= N <= 2^20, 1 <= M_max <= 2^20; x_q, w_q
- * and q 16-byte aligned, x and Y 2-byte, scales 4-byte.  Rows >= M are neither read nor written.  M and d_M as in
- * et_splitk_gemm.  et_i8_quantize needs 256 bytes of workspace (for its status);
- * one workspace may serve both calls.  Errors as et_moe_layer.
+ * and q 16-byte aligned, x and Y 2-byte, scales 4-byte.  Rows >= M are neither
+ * read nor written.  M and d_M as in et_splitk_gemm.  et_i8_quantize needs 256
+ * bytes of workspace (for its status).  A wait inside et_i8_gemm that ran out
+ * (0.2 s) is recorded as ET_ERR_TIMEOUT (et_status), and Y is then incomplete.
+ * Errors as et_moe_layer.
  * ---------------------------------------------------------------------- */
 size_t et_i8_quantize_workspace_bytes(int M_max, int K);
 
