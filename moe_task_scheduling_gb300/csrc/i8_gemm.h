@@ -34,6 +34,7 @@ struct I8TcArgs {
     int kblocks;
     int grid;            // CTAs, pairs or clusters that take tiles in turn (a cluster: one)
     int split;           // CTAs of a cluster that share a tile (1: none)
+    int blocks;          // k-blocks that a CTA has in all, at most
     int stages_w, stages_x;
     uint64_t timeout_ns;
 };
@@ -46,9 +47,9 @@ struct I8ExpandArgs {
     EtHeader* hdr;
 };
 
-// `pair`: CTA pairs of 256 channels.  i8_tc_stages: stages of either ring; returns the bytes of
-// shared memory.
-int i8_tc_stages(bool pair, int tn, int* w, int* x);
+// `pair`: CTA pairs of 256 channels.  i8_tc_stages: stages of either ring, no more than there are
+// blocks; returns the bytes of shared memory.
+int i8_tc_stages(bool pair, int tn, int blocks, int* w, int* x);
 cudaError_t launch_i8_tc(const I8TcArgs& a, const CUtensorMap* map_w, const CUtensorMap* map_x, bool pair, int dev, void* stream);
 cudaError_t launch_i8_expand(const I8ExpandArgs& a, int sms, void* stream);
 

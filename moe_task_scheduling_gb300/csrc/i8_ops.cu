@@ -439,7 +439,8 @@ int et_i8_gemm(const void* x_q, const float* s_x, const void* w_q, const float* 
             a.kblocks = pl.kblocks;
             a.grid = pl.grid;
             a.split = pl.split;
-            i8_tc_stages(pl.pair, pl.tn, &a.stages_w, &a.stages_x);
+            a.blocks = ceil_div_l(pl.kblocks, pl.split) * ceil_div_l(static_cast<long long>(ceil_div_l(rows, pl.tn)) * pl.nt, pl.grid);
+            i8_tc_stages(pl.pair, pl.tn, a.blocks, &a.stages_w, &a.stages_x);
             a.timeout_ns = 200000000ull;
             cudaError_t e = cudaSuccess;
             CUtensorMap mx = mw;
