@@ -4,301 +4,10 @@
 #include <cmath>
 
 #include "../../include/etmoe.h"
-#include "router_sums.cuh"
+#include "router_rows.cuh"
 
 namespace et {
 namespace {
-
-constexpr int kGroupsMax = 32;
-
-struct GroupArgs {
-    const float* logits;     // [T, E]
-    const float* bias;       // [E] or null
-    const uint8_t* mask;     // [T] or null
-    int32_t* idx;            // [T, k]
-    float* w;                // [T, k]
-    const int32_t* d_T;
-    int T_host, T_max, E, k;
-    int G, kg, best;         // groups, how many take part, whose `best` experts rank them
-    int gs;                  // experts a group
-    int lanes;               // lanes that hold a group where that is a power of two, else 0
-    int renorm, vec;
-    float scale;
-    RouterSums sums;
-};
-
-__device__ __forceinline__ double key_value(unsigned long long key) {
-    return __longlong_as_double(static_cast<long long>(key >> 63 ? key ^ 0x8000000000000000ull : ~key));
-}
-
-// logit_key of a 64-bit value; NaN above all, > 0 everywhere.
-__device__ __forceinline__ unsigned long long value_key(double v) {
-    if (v != v) return ~0ull;
-    const long long b = __double_as_longlong(v + 0.0);
-    return static_cast<unsigned long long>(b) ^ (static_cast<unsigned long long>(b >> 63) | 0x8000000000000000ull);
-}
-
-// The whole choice in 64 bits, for the rows where 32 cannot tell.  Lane `lane` has the
-// experts lane * EPL + i.  Returns lane j's expert, the j-th, or -1.
-// Out of line and in plain loops: one row in some hundreds comes here.
-template <int EPL>
-__device__ __noinline__ int choose64(const float* row, const float* bias, int E, int k, int G, int kg, int best, int gs,
-                                     int sigmoid, int lane) {
-    constexpr uint32_t kAll = 0xffffffffu;
-    unsigned long long key[EPL];  // of score + bias; 0: not available
-    float v[EPL];
-    double m = 0.0, Z = 1.0;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) v[i] = lane * EPL + i < E ? row[lane * EPL + i] : -INFINITY;
-    if (!sigmoid) {
-        float top = v[0];
-#pragma unroll
-        for (int i = 1; i < EPL; ++i) top = fmaxf(top, v[i]);
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
-        m = top;
-        Z = 0.0;
-#pragma unroll 1
-        for (int i = 0; i < EPL; ++i) Z += exp(static_cast<double>(v[i]) - m);  // 0 past E
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) Z += __shfl_xor_sync(kAll, Z, off);
-    }
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        const double x = v[i];
-        key[i] = 0;
-        if (!(v[i] == -INFINITY)) {
-            double c = sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - m) / Z;
-            if (bias) c += static_cast<double>(bias[lane * EPL + i]);
-            if (!(c == -INFINITY)) key[i] = value_key(c);
-        }
-    }
-    if (kg < G) {
-        double score = -INFINITY;  // lane g: of group g
-#pragma unroll 1
-        for (int g = 0; g < G; ++g) {
-            unsigned long long hi = 0, lo = 0;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const int e = lane * EPL + i;
-                if (e >= g * gs && e < g * gs + gs) {
-                    lo = max(lo, min(hi, key[i]));
-                    hi = max(hi, key[i]);
-                }
-            }
-#pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) {
-                const unsigned long long h = __shfl_xor_sync(kAll, hi, off), l = __shfl_xor_sync(kAll, lo, off);
-                lo = max(max(lo, l), min(hi, h));
-                hi = max(hi, h);
-            }
-            double s = hi ? key_value(hi) : -INFINITY;
-            if (best > 1 && lo) s += key_value(lo);
-            if (lane == g) score = s;
-        }
-        const unsigned long long mine = value_key(score);
-        int rank = 0;
-#pragma unroll 1
-        for (int g = 0; g < G; ++g) {
-            const unsigned long long other = __shfl_sync(kAll, mine, g);
-            rank += other > mine || (other == mine && g < lane);
-        }
-        const uint32_t in = __ballot_sync(kAll, lane < G && rank < kg);
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const int e = lane * EPL + i;
-            if (e >= E || !(in >> (e / gs) & 1)) key[i] = 0;
-        }
-    }
-    int mineE = -1;
-#pragma unroll 1
-    for (int j = 0; j < k; ++j) {
-        unsigned long long hi = 0;
-        int at = E;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (key[i] > hi) {
-                hi = key[i];
-                at = lane * EPL + i;
-            }
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) {
-            const unsigned long long h = __shfl_xor_sync(kAll, hi, off);
-            const int a = __shfl_xor_sync(kAll, at, off);
-            if (h > hi || (h == hi && a < at)) {
-                hi = h;
-                at = a;
-            }
-        }
-        if (hi && lane == j) mineE = at;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (lane * EPL + i == at) key[i] = 0;
-    }
-    return mineE;
-}
-
-constexpr uint32_t kNegInfKey = 0x007fffffu;  // logit_key(-inf); nothing available has it or less
-
-__device__ __forceinline__ float rcp_fast(float x) {  // within 1 ulp; 0 for +inf
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float sigmoid_fast(float v) { return rcp_fast(1.0f + __expf(-v)); }  // 0 for -inf
-
-// The float of a key, -inf where nothing is available.
-__device__ __forceinline__ float key_or_none(uint32_t key) { return key > kNegInfKey ? key_logit(key) : -INFINITY; }
-
-// logit_key of a score (>= 0 or NaN).  In assembly: as C++ it became a negation, which makes
-// the one positive NaN of -NaN.
-__device__ __forceinline__ uint32_t score_key(float s) {
-    uint32_t k;
-    asm("or.b32 %0, %1, 0x80000000;" : "=r"(k) : "r"(__float_as_uint(s)));
-    return k;
-}
-
-__device__ __forceinline__ void order2(uint32_t& a, uint32_t& b) {  // the larger first
-    const uint32_t hi = max(a, b);
-    b = min(a, b);
-    a = hi;
-}
-
-// Sorts k[0 .. N), first rising and then falling (or the other way), the largest first.
-template <int N>
-__device__ __forceinline__ void sort_bitonic(uint32_t* k) {
-#pragma unroll
-    for (int h = N / 2; h >= 1; h /= 2)
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (!(i & h)) order2(k[i], k[i + h]);
-}
-
-// The warp's eight largest keys, sorted, in every lane; a lane has N to begin with.
-template <int N>
-__device__ __forceinline__ void top8(const uint32_t (&mine)[N], uint32_t (&k)[8]) {
-    constexpr uint32_t kAll = 0xffffffffu;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) k[i] = i < N ? mine[i % N] : 0u;
-    if (N == 2) order2(k[0], k[1]);
-    if (N >= 4) {  // odd-even merge sort
-#pragma unroll
-        for (int o = 0; o < N; o += 4) {
-            order2(k[o], k[o + 1]); order2(k[o + 2], k[o + 3]);
-            order2(k[o], k[o + 2]); order2(k[o + 1], k[o + 3]);
-            order2(k[o + 1], k[o + 2]);
-        }
-    }
-    if (N == 8) {
-        order2(k[0], k[4]); order2(k[1], k[5]); order2(k[2], k[6]); order2(k[3], k[7]);
-        order2(k[2], k[4]); order2(k[3], k[5]);
-        order2(k[1], k[2]); order2(k[3], k[4]); order2(k[5], k[6]);
-    }
-    // With a neighbour's list, turned round: the larger of each pair are the larger half of both
-    // lists.  Short lists grow to eight first.
-    int n = N;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        if (n < 8) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < n) {
-                    const uint32_t other = __shfl_xor_sync(kAll, k[n - 1 - i], off);
-                    k[8 - 1 - i] = other;  // parked
-                }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < n) {
-                    const uint32_t other = k[8 - 1 - i];
-                    const uint32_t hi = max(k[i], other), lo = min(k[i], other);
-                    k[i] = hi;
-                    k[8 - 1 - i] = lo;
-                }
-            uint32_t low[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) low[i] = k[8 - 1 - i];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < n) k[n + i] = low[i];
-            if (n == 2) { sort_bitonic<2>(k); sort_bitonic<2>(k + 2); }
-            if (n == 4) { sort_bitonic<4>(k); sort_bitonic<4>(k + 4); }
-            n *= 2;
-        } else {
-            uint32_t other[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) other[i] = __shfl_xor_sync(kAll, k[7 - i], off);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) k[i] = max(k[i], other[i]);
-            sort_bitonic<8>(k);
-        }
-    }
-}
-
-// logit_key of a sum score + bias, which is never -0 and no NaN but the positive one.
-__device__ __forceinline__ uint32_t sum_key(float v) {
-    const int b = __float_as_int(v);
-    return static_cast<uint32_t>(b ^ ((b >> 31) | static_cast<int>(0x80000000u)));
-}
-
-constexpr int kCandidates = 16;  // experts whose order is looked at again at most
-
-// What ranks experts and groups in 64 bits: sigmoid scores + bias; for softmax scores (without
-// a bias) their multiples e^(x - top).
-__device__ __forceinline__ double value64(float x, float b, bool sigmoid, float top) {
-    const double e = exp(sigmoid ? -static_cast<double>(x) : static_cast<double>(x) - static_cast<double>(top));
-    return sigmoid ? 1.0 / (1.0 + e) + static_cast<double>(b) : e;
-}
-
-// Two groups whose scores 32 bits cannot tell apart: 1 if the first has the larger, or the
-// same and the lower number, 0 if the second, -1 if it takes more than their best two to
-// say.  floor_a, floor_b: what the experts that count are not below;
-// want_a, want_b: how many those are.  slots: 16 places of shared memory.
-template <int EPL>
-__device__ __noinline__ int compare_groups(const float* row, const float* bias_s, bool sigmoid, float top, float inv, int E,
-                                           int gs, int a, int b, float floor_a, float floor_b, int want_a, int want_b, uint32_t* slots, int lane) {
-    constexpr uint32_t kAll = 0xffffffffu;
-    int na = 0, nb = 0;
-#pragma unroll 1
-    for (int i = 0; i < EPL; ++i) {
-        const int e = lane * EPL + i, g = e / gs;
-        const float x = e < E ? row[e] : -INFINITY;
-        const float c = x == -INFINITY ? x : __fadd_rn(sigmoid ? sigmoid_fast(x) : __expf(x - top) * inv, bias_s[min(e, E - 1)]);
-        const uint32_t in_a = __ballot_sync(kAll, e < E && g == a && c >= floor_a);
-        const uint32_t in_b = __ballot_sync(kAll, e < E && g == b && c >= floor_b);
-        const uint32_t bit = 1u << lane, below = bit - 1;
-        if ((in_a & bit) && na + __popc(in_a & below) < 8) slots[na + __popc(in_a & below)] = e;
-        if ((in_b & bit) && nb + __popc(in_b & below) < 8) slots[8 + nb + __popc(in_b & below)] = e;
-        na += __popc(in_a);
-        nb += __popc(in_b);
-    }
-    __syncwarp();
-    if (na != want_a || nb != want_b) return -1;
-    const bool mine = lane < na || (lane >= 8 && lane < 8 + nb);
-    const int e = mine ? static_cast<int>(slots[lane]) : 0;
-    double c = mine ? value64(row[e], bias_s[e], sigmoid, top) : 0.0;
-    c += __shfl_xor_sync(kAll, c, 1);  // two at most
-    const double sa = __shfl_sync(kAll, c, 0), sb = __shfl_sync(kAll, c, 8);
-    return sa > sb || (sa == sb && a < b) ? 1 : 0;
-}
-
-// The order of n candidates (n <= kCandidates, their experts in slots) in 64 bits (of softmax
-// scores without a bias by the logits): puts the best k there in their order.
-__device__ __noinline__ void order_again(const float* row, const float* bias_s, bool sigmoid, int n, int k, uint32_t* slots, int lane) {
-    constexpr uint32_t kAll = 0xffffffffu;
-    const int e = lane < n ? static_cast<int>(slots[lane]) : 0;
-    const double c = lane < n ? (sigmoid ? value64(row[e], bias_s[e], true, 0.0f) : static_cast<double>(row[e])) : 0.0;
-    const unsigned long long key = value_key(c);
-    int rank = 0;
-#pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-        const unsigned long long other = __shfl_sync(kAll, key, i);
-        const int oe = __shfl_sync(kAll, e, i);
-        rank += other > key || (other == key && oe < e);
-    }
-    __syncwarp();
-    if (lane < n && rank < k) slots[rank] = e;
-    __syncwarp();
-}
 
 // One row a warp, experts lane * EPL + i in register i, so that a group is a few
 // neighbouring lanes.  The choice runs on 32-bit values: without a bias on the logits,
@@ -311,10 +20,10 @@ __device__ __noinline__ void order_again(const float* row, const float* bias_s, 
 // decide: on the candidates alone (a lane each: 1.3 us where a whole row takes 14), and on
 // the whole row if they are too many, or for softmax scores with a bias.
 //
-// Bound by instruction issue, not by its 1 KB a row: T = 16384, E = 256, sigmoid with bias,
-// 8 groups, k = 8 33.5 us, about 1080 instructions a row, 56 % of the slots (a warp has three
-// or four rows, so slots stand empty at the end); T = 4096, E = 128, softmax, 16 groups 13.5
-// us.  E whose groups are no power of two of lanes: 43 us (T = 16384, E = 160).
+// The form for few rows, and for E that eight lanes cannot share (router_rows4_kernel has the
+// others).  Bound by a row's latency, T = 16, E = 128 6.5 us, then by instruction issue, about
+// 1080 a row at E = 256.  E whose groups are no power of two of lanes looks at the groups one
+// by one: T = 16384, E = 160 43 us.
 template <int EPL, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(const GroupArgs p) {
     constexpr uint32_t kAll = 0xffffffffu, kLow = 32 * EPL - 1;  // the bits that name an expert
@@ -470,7 +179,7 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
             if (group) {
                 const float h = key_or_none(hi), l = p.best > 1 && lo > kNegInfKey ? key_logit(lo) : 0.0f;
                 score = h + l;
-                off_by = 2.0f * err + 2.0f * kU * (fabsf(h) + fabsf(l));
+                if (!(h == -INFINITY)) off_by = 2.0f * err + 2.0f * kU * (fabsf(h) + fabsf(l));
             }
             const uint32_t mine = logit_key(score);
             int rank = 0;
@@ -519,7 +228,10 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
             uint32_t cut[EPL];
 #pragma unroll
             for (int i = 0; i < EPL; ++i) cut[i] = (key[i] & ~kLow) | (kLow - (e0 + i));
-            top8<EPL>(cut, best);
+            sort_keys<EPL>(cut);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) best[i] = i < EPL ? cut[i % EPL] : 0u;
+            merge8<EPL, 32>(best);
         }
         uint32_t mykey = 0;
 #pragma unroll
@@ -827,6 +539,12 @@ auto pick_groups(bool sigmoid, bool bias) {
                    : (bias ? router_groups_kernel<EPL, false, true> : router_groups_kernel<EPL, false, false>);
 }
 
+// Rows from which on four share a warp, where eight lanes can have a row's experts.  Sigmoid
+// with bias, E = 256, 8 groups: T = 608 14.2 us one a warp and 14.2 four a warp, T = 1024 16.0
+// and 13.2, T = 2048 16.1 and 16.0, T = 4096 19.6 and 15.3, T = 16384 33 and 25, T = 65536 82
+// and 59; E = 64: T = 608 7.8 and 7.7, T = 16384 19 and 13, T = 65536 51 and 28.
+constexpr int kRows4Least = 1024;
+
 int groups_check(int T, const int32_t* d_T, int T_max, int E, int k, int score, float scale) {
     std::string why;
     if (!router_shape_ok(T_max, E, k, &why)) return api_fail(ET_ERR_UNSUPPORTED, why);
@@ -875,11 +593,22 @@ int et_router_groups(const float* logits, const float* bias, const uint8_t* toke
         const GroupArgs a{logits, bias, token_mask, topk_idx, topk_w, d_T, T, T_max, E, k, n_groups, k_groups, group_best, gs,
                           lanes & (lanes - 1) ? 0 : lanes, renorm != 0, E % 4 == 0 && api_aligned(logits, 16), scale,
                           router_sums_args(workspace, L, expert_counts, n_routed, mean_prob, loss, false)};
-        // One CTA up to 16 rows, then few warps a CTA while that puts rows on more SMs.
+        const bool sig = score == ET_SCORE_SIGMOID;
         const int rows = d_T ? T_max : T > 0 ? T : 1;
+        if ((E == 32 || E == 64 || E == 128 || E == 256) && rows >= kRows4Least) {
+            static SmemOptIn opt[4][4];
+            const int n = E == 32 ? 0 : E == 64 ? 1 : E == 128 ? 2 : 3;
+            auto kernel = n == 0 ? pick_rows4<4>(sig, bias) : n == 1 ? pick_rows4<8>(sig, bias)
+                        : n == 2 ? pick_rows4<16>(sig, bias) : pick_rows4<32>(sig, bias);
+            const int smem = rows4_floats(E) * 4, ctas = ceil_div_i(rows, 4);
+            cudaError_t e = api_smem_opt_in(opt[n][2 * sig + (bias != nullptr)], dev, kernel, smem);
+            if (e == cudaSuccess) e = api_launch(kernel, ctas < kRouterParts ? ctas : kRouterParts, kRows4Warps * 32, smem, stream, a);
+            if (e != cudaSuccess) return api_fail_cuda(e, "launch of the grouped router kernel");
+            return ET_OK;
+        }
+        // One CTA up to 16 rows, then few warps a CTA while that puts rows on more SMs.
         const int warps = rows <= 16 ? rows : rows <= 8 * kRouterParts ? 8 : rows <= 16 * kRouterParts ? 16 : kRouterWarpsMax;
         const RouterGrid g = router_grid_of(rows, E, warps);
-        const bool sig = score == ET_SCORE_SIGMOID;
         auto kernel = epl == 1 ? pick_groups<1>(sig, bias) : epl == 2 ? pick_groups<2>(sig, bias)
                     : epl == 4 ? pick_groups<4>(sig, bias) : pick_groups<8>(sig, bias);
         const cudaError_t e = api_launch(kernel, g.ctas, g.warps * 32, g.smem, stream, a);

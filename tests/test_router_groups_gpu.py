@@ -325,3 +325,113 @@ def test_any_alignment(cuda_lib, En, sigmoid):
         cuda_lib.et_router_groups_bwd(lo, idx, w, o["counts"], o["n"], d, score=score, d_loss=dl.cuda(), d_topk_w=dw, workspace=ws)
         # other lanes hold other experts: the sums over a row go in another order, a few roundings of their terms
         check(d, want.cpu().double(), 96 * U * (want.cpu().double().abs() + want.cpu().double().abs().amax(-1, keepdim=True)), "d_logits")
+
+
+# ------------------------------------------------------------------ many rows: four share a warp
+
+MANY = [(En, G) for En in (32, 64, 128, 256) for G in (1, 2, 4, 8, 16, 32)]
+
+
+@pytest.mark.parametrize("En,G", MANY)
+@pytest.mark.parametrize("sigmoid,bias,renorm,masked", [(True, True, True, True), (False, False, False, False)])
+def test_many_rows(cuda_lib, En, G, sigmoid, bias, renorm, masked):
+    T, kg = 1027, max(1, G // 2)
+    k, best = min(8, En // G * kg), 1 + G % 4 // 2
+    g = _gen(En * 100 + G)
+    logits = torch.randn(T, En, generator=g) * 2
+    b = torch.randn(En, generator=g) * 0.1 if bias else None
+    mask = (torch.rand(T, generator=g) > 0.3).to(torch.uint8) if masked else None
+    how = dict(sigmoid=sigmoid, renorm=renorm, scale=2.5)
+    o, ws = _forward(cuda_lib, logits, k, G, kg, best, bias=b, mask=mask, **how)
+    _check(o, logits, k, G, kg, best=best, bias=b, mask=mask, **how)
+    o2, _ = _forward(cuda_lib, logits, k, G, kg, best, bias=b, mask=mask, ws=ws, **how)
+    assert all(torch.equal(o[n], o2[n]) for n in o)
+    assert cuda_lib.et_status(ws) == (0, 0)
+
+
+def _hard_rows(T, En, G, g):
+    """Rows where choosing goes wrong if it goes wrong anywhere, in turn."""
+    L = torch.randn(T, En, generator=g)
+    i = torch.arange(T) % 12
+    gs = En // G
+    L[i == 1] = L[i == 1].bfloat16().float()                                    # coarse: equal logits
+    L[i == 2] = torch.randint(-2, 3, (int((i == 2).sum()), En), generator=g).float()  # many ties
+    L[i == 3] = 0.25                                                            # all equal
+    L[i == 4] = 0.5 + torch.randint(-3, 4, (int((i == 4).sum()), En), generator=g) * 2.0 ** -24  # a few ulp apart
+    L[i == 5] = torch.where(torch.rand(int((i == 5).sum()), En, generator=g) < 0.8, torch.tensor(-math.inf), L[i == 5])
+    L[i == 6, :gs] = -math.inf                                                  # a group that nobody can choose
+    L[i == 7] = -math.inf                                                       # a row that is not routed
+    L[i == 7, En // 2] = torch.where(torch.arange(int((i == 7).sum())) % 2 == 0, -math.inf, 1.0)
+    L[i == 8] = L[i == 8] * 3 - 100.0                                           # tiny scores
+    L[i == 9] = L[i == 9] * 4 + 25.0                                            # sigmoids that are 1
+    L[i == 10, ::5] = math.inf
+    L[i == 11, 3] = math.nan
+    return L
+
+
+@pytest.mark.parametrize("En,G,kg", [(32, 8, 4), (32, 32, 9), (64, 16, 5), (64, 1, 1), (128, 4, 2), (128, 16, 6), (256, 8, 4), (256, 32, 8), (256, 2, 1)])
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("bias", [None, "random", "zero", "some"])
+def test_four_rows_a_warp_choose_as_one(cuda_lib, En, G, kg, sigmoid, bias):
+    """Many rows in one call, and the same rows in short calls: the same choice, for hard rows in every place of a warp."""
+    T, k = 2051, min(8, En // G * kg)
+    g = _gen(En + G)
+    L = _hard_rows(T, En, G, g)
+    L = L[torch.randperm(T, generator=g)]
+    b = None
+    if bias is not None:
+        b = torch.randn(En, generator=g) * 0.05 if bias == "random" else torch.zeros(En)
+        if bias == "some":
+            b[1], b[En // 2 + 1], b[En - 1] = -math.inf, 3.0, -1e-7
+    for best in (1, 2):
+        for renorm in (True, False):
+            how = dict(sigmoid=sigmoid, bias=b, renorm=renorm)
+            o, _ = _forward(cuda_lib, L, k, G, kg, best, **how)
+            parts = [_forward(cuda_lib, L[t:t + 500], k, G, kg, best, **how)[0] for t in range(0, T, 500)]
+            assert torch.equal(o["idx"], torch.cat([q["idx"] for q in parts]))
+            assert torch.equal(o["counts"], sum(q["counts"] for q in parts)) and int(o["n"]) == sum(int(q["n"]) for q in parts)
+            w, v = o["w"].cpu().double(), torch.cat([q["w"] for q in parts]).cpu().double()
+            assert torch.equal(torch.isnan(w), torch.isnan(v))
+            # the same terms summed in another order: the sum's 256 roundings at most
+            check(torch.where(torch.isnan(w), 0.0, w), torch.where(torch.isnan(v), 0.0, v), 256 * U * torch.where(torch.isnan(v), 0.0, v).abs(), "w")
+    # and against the definition, rows without NaN or infinity above
+    rows = torch.isfinite(torch.where(L == -math.inf, 0.0, L)).all(-1).nonzero()[:, 0][:150]
+    want = ref.router_groups(L[rows], k, G, kg, 2, sigmoid=sigmoid, bias=b)
+    assert torch.equal(o["idx"][rows.cuda()].cpu().long(), want["idx"])
+
+
+def test_many_rows_device_count(cuda_lib):
+    """One call for up to 3000 rows, whatever the device says."""
+    T, En, k = 3000, 64, 4
+    g = _gen(8)
+    logits = torch.randn(T, En, generator=g)
+    d_T = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = cuda_lib.alloc_workspace(cuda_lib.et_router_groups_workspace_bytes(T, En, k))
+    for n in (3000, 1, 0, 1501, 6):
+        d_T.fill_(n)
+        o, _ = _forward(cuda_lib, logits, k, 8, 3, d_T=d_T, ws=ws)
+        _check(o, logits, k, 8, 3, T=n)
+    for n in (3001, -1):
+        d_T.fill_(n)
+        o, _ = _forward(cuda_lib, logits, k, 8, 3, d_T=d_T, ws=ws)
+        assert (o["idx"] == -7).all() and cuda_lib.et_status(ws)[0] == cuda_lib.ET_ERR_BOUNDS
+        cuda_lib.et_reset_status(ws)
+
+
+def test_long_batches_of_rows(cuda_lib):
+    """More rows than a lane adds up at a time: probabilities and loss to their bound."""
+    T, En, k = 700000, 32, 2
+    g = _gen(5)
+    rows = torch.randn(64, En, generator=g)
+    o, _ = _forward(cuda_lib, rows.repeat(T // 64 + 1, 1)[:T], k, 4, 2)
+    w = T // 64 + (torch.arange(64) < T % 64)
+    r = ref.router_groups(rows, k, 4, 2)
+    counts = torch.zeros(En, dtype=torch.float64)
+    for t in range(64):
+        counts[r["idx"][t]] += float(w[t])
+    assert torch.equal(o["counts"].cpu().double(), counts)
+    want = (r["p"] * w[:, None].double()).sum(0) / T
+    # a p's own bound, 32 rows of a lane, then batches: T / (152 16 4 32) = 2.3, 4, 16 warps, 152 CTAs
+    far = (rows.amax(-1, keepdim=True) - rows).abs().double()
+    rel = (48 + En + 4 * far + 5 * rows.abs().double()).amax() * U
+    check(o["mean_prob"], want, (rel + 256 * U) * want, "mean_prob")
