@@ -140,8 +140,8 @@ __global__ void __launch_bounds__(kDropThreads) dropout_vec_kernel(const Dropout
             uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                float2 v = __fmul2_rn(unpack2(yw[j] & m.u[j]), both(p.drop.mul));
-                if (x) v = __fadd2_rn(v, unpack2(xw[j]));
+                // (one rounding, as in the norm; without x its zeros)
+                const float2 v = __ffma2_rn(unpack2(yw[j] & m.u[j]), both(p.drop.mul), unpack2(xw[j]));
                 o[j] = pack_bf16(v.x, v.y);
             }
             out[i] = make_uint4(o[0], o[1], o[2], o[3]);
@@ -180,9 +180,8 @@ __global__ void __launch_bounds__(kDropThreads) dropout_any_kernel(const Dropout
     for (int i = 0; i < 8; ++i) {
         const int c = threadIdx.x + i * kDropThreads;
         if (c < n) {
-            float v = dropped[c >> 3] >> (c & 7) & 1 ? 0.0f : __bfloat162float(yv[i]) * p.drop.mul;
-            if (p.x) v += __bfloat162float(xv[i]);
-            p.out[off + c] = __float2bfloat16_rn(v);
+            const float y = dropped[c >> 3] >> (c & 7) & 1 ? 0.0f : __bfloat162float(yv[i]);
+            p.out[off + c] = __float2bfloat16_rn(fmaf(y, p.drop.mul, __bfloat162float(xv[i])));
         }
     }
 }
