@@ -31,8 +31,6 @@
 // 4096: 260 us, 1.85 PFLOP/s, 96 % of a bf16 library product's burst; at 2048 x 4096 x 4096 the
 // tensor pipe is busy for 75 % of the kernel, the rest is the last tiles' epilogue and the
 // pipeline's start).
-#include <cuda_fp16.h>
-
 #include "et_api.h"
 #include "et_device.cuh"
 #include "i8_gemm.h"
@@ -175,17 +173,6 @@ __device__ __forceinline__ void sts_v4(uint32_t a, uint32_t x, uint32_t y, uint3
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Four int8 of a word as two pairs of fp16, exact: with the sign bits turned over a byte is
-// x + 128, 0x6400 | b is 1024 + b in fp16, and 1152 less is x.
-__device__ __forceinline__ void int8_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    w ^= 0x80808080u;
-    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-    const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
-    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off), y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
-    lo = *reinterpret_cast<const uint32_t*>(&x);
-    hi = *reinterpret_cast<const uint32_t*>(&y);
-}
 
 // A thread's values of up to 16 tokens, a row of `to` each.  The whole sixteen go out
 // without a branch between them.

@@ -1,6 +1,7 @@
 // i8_ops.cu -- rows of bf16 to int8 with a scale each, and products of int8
 // tokens and weights with a scale for each token and channel.
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/etmoe.h"
 #include "et_api.h"
@@ -156,6 +157,17 @@ __device__ __forceinline__ int4 load_weights(const int8_t* p) {  // streamed: th
 }
 
 // c += A B, A 16 channels x 32 k, B 32 k x 8 tokens: exact in int32.
+__device__ __forceinline__ void mma_f16_sync(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void int8x16_to_half(const int4& v, uint32_t (&h)[8]) {
+    int8_to_half(v.x, h[0], h[1]);
+    int8_to_half(v.y, h[2], h[3]);
+    int8_to_half(v.z, h[4], h[5]);
+    int8_to_half(v.w, h[6], h[7]);
+}
 __device__ __forceinline__ void mma_s8(int (&c)[4], int a0, int a1, int a2, int a3, int b0, int b1) {
     asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
@@ -169,7 +181,7 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], int a0, int a1, int a2, int 
 // integer MMA takes 16 cycles of an SM here, 32 / MT bytes of weights a cycle, where HBM
 // brings 23: MT = 1 is bound by HBM (N = 14336, K = 4096: 11.8 us, 5.0 TB/s from launch to
 // end), MT = 2 by the MMAs (17.7 us).
-template <int MT>
+template <int MT, bool HALF>
 __global__ void __launch_bounds__(kGemvWarps * 32, kGemvCtas) i8_gemv_kernel(const I8GemmArgs p) {
     __shared__ int red[2][kGemvWarps][8 * MT][kGemvRows + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
@@ -216,11 +228,28 @@ __global__ void __launch_bounds__(kGemvWarps * 32, kGemvCtas) i8_gemv_kernel(con
 #pragma unroll
     for (int i = 0; i < kGemvAhead; ++i) fetch(wv[i]);
     int tile = blockIdx.x, k = k0, buf = 0;
-    int acc[MT][4] = {};
+    using Acc = std::conditional_t<HALF, float, int>;
+    Acc acc[MT][4] = {};
     while (tile < tiles) {
 #pragma unroll
         for (int i = 0; i < kGemvAhead; ++i) {
             if (tile >= tiles) break;
+            if constexpr (HALF) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t a[8], b[8];  // rows g and g + 8
+                    int8x16_to_half(wv[i][2 * h], a);
+                    int8x16_to_half(wv[i][2 * h + 1], b);
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        const int4 v = k + 64 * h < K ? *reinterpret_cast<const int4*>(x[t] + k + 64 * h) : zero;
+                        uint32_t c[8];
+                        int8x16_to_half(v, c);
+#pragma unroll
+                        for (int j = 0; j < 8; j += 2) mma_f16_sync(acc[t], a[j], b[j], a[j + 1], b[j + 1], c[j], c[j + 1]);
+                    }
+                }
+            } else
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 const int4 x0 = k < K ? *reinterpret_cast<const int4*>(x[t] + k) : zero;
@@ -237,12 +266,13 @@ __global__ void __launch_bounds__(kGemvWarps * 32, kGemvCtas) i8_gemv_kernel(con
                 for (int t = 0; t < MT; ++t)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        red[buf][warp][8 * t + 2 * q + (j & 1)][g + (j >> 1) * 8] = acc[t][j];
+                        red[buf][warp][8 * t + 2 * q + (j & 1)][g + (j >> 1) * 8] = static_cast<int>(acc[t][j]);
                         acc[t][j] = 0;
                     }
                 __syncthreads();  // (the other buffer has been read: who comes here has left it)
-                if (threadIdx.x < 8 * MT * kGemvRows) {
-                    const int m = threadIdx.x / kGemvRows, r = threadIdx.x % kGemvRows, n = tile * kGemvRows + r;
+#pragma unroll
+                for (int o = threadIdx.x; o < 8 * MT * kGemvRows; o += kGemvWarps * 32) {
+                    const int m = o / kGemvRows, r = o % kGemvRows, n = tile * kGemvRows + r;
                     int s = 0;
 #pragma unroll
                     for (int v = 0; v < kGemvWarps; ++v) s += red[buf][v][m][r];
@@ -261,7 +291,7 @@ __global__ void __launch_bounds__(kGemvWarps * 32, kGemvCtas) i8_gemv_kernel(con
 // tcgen05 form 6 us + 1 us for each 5.5 MB (2048 x 2048: 3.2 against 6.8 us; 14336 x 4096:
 // 17.7 against 16.3 us): they meet at 48 MB.
 bool i8_gemv(int M_max, int N, int K) {
-    return M_max <= kGemvTokens || (M_max <= 2 * kGemvTokens && static_cast<long long>(N) * K <= 48000000);
+    return M_max <= 32;
 }
 
 bool i8_shape_ok(int M_max, int N, int K, std::string* why) {
@@ -417,7 +447,7 @@ int et_i8_gemm(const void* x_q, const float* s_x, const void* w_q, const float* 
         if (i8_gemv(all, N, K)) {
             const I8GemmArgs a{x, s_x, static_cast<const int8_t*>(w_q), s_w, y, d_M, M, all, N, K, hdr};
             const int tiles = (N + kGemvRows - 1) / kGemvRows;
-            const cudaError_t e = api_launch(all <= kGemvTokens ? i8_gemv_kernel<1> : i8_gemv_kernel<2>, tiles < kGemvCtas * sms ? tiles : kGemvCtas * sms, kGemvWarps * 32, 0, stream, a);
+            const cudaError_t e = api_launch(all <= 8 ? i8_gemv_kernel<1, false> : all <= 16 ? i8_gemv_kernel<2, true> : all <= 24 ? i8_gemv_kernel<3, true> : i8_gemv_kernel<4, true>, tiles < kGemvCtas * sms ? tiles : kGemvCtas * sms, kGemvWarps * 32, 0, stream, a);
             if (e != cudaSuccess) return api_fail_cuda(e, "launch of the int8 product");
             return ET_OK;
         }

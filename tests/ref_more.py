@@ -173,12 +173,16 @@ def i8_quantize(x):
 
 
 def i8_gemm(xq, sx, wq, sw):
-    """(y, bound) in 64 bits: the bound before the rounding to bf16."""
+    """(y, bound) in 64 bits: the bound before the rounding to bf16.
+
+    Products are exact; a sum within 2^24 too.  Beyond, each MMA of 16 k cuts the fp32 sum to 24 bits, which takes less
+    than 2^-23 of a sum of at most sum |x w|, and there are K / 16 of them: K 2^-27 sum |x w|.
+    """
     x, w = xq.double(), wq.double()
     s = sx.double()[:, None] * sw.double()
     y = (x @ w.t()) * s
     mag = (x.abs() @ w.abs().t()) * s.abs()
-    return y, 4 * U * y.abs() + (2.0 ** -22 * mag if xq.shape[1] > 1024 else 0.0) + 2.0 ** -133
+    return y, 4 * U * y.abs() + (xq.shape[1] * 2.0 ** -27 * mag if xq.shape[1] > 1024 else 0.0) + 2.0 ** -133
 
 
 def bf16_bound(want, e):

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from tests import ref_more as ref
+from tests.ref_ops import F32_HALF as U
 from tests.ref_ops import check
 
 pytestmark = pytest.mark.gpu
@@ -202,3 +203,23 @@ def test_quantised_linear(cuda_lib):
     ex, ew = sx.double().cpu()[:, None] * 0.5001, sw.double().cpu()[:, None] * 0.5001  # half a step of each value
     lost = ex * w.double().abs().sum(-1) + x.double().abs().sum(-1)[:, None] * ew.t() + ex * ew.t() * K
     check(Y, want, ref.bf16_bound(want, lost), "Y")
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 200, 65536), (12, 200, 65536), (40, 256, 65536), (64, 20000, 65536), (300, 256, 14336), (1000, 4096, 14336)])
+@pytest.mark.parametrize("low", [1, 100])
+def test_gemm_sums_that_rise_and_fall(cuda_lib, M, N, K, low):
+    """Products of one sign for half of k, then of the other: partial sums up to 2^30 whose result is small, where every
+    bit that a partial sum loses shows.  Up to 8 tokens nothing is lost."""
+    g = torch.Generator(device="cuda").manual_seed(M + K)
+    x = torch.randint(low, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+    w = torch.randint(low, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    x[:, K // 2:] = -x[:, :K // 2]
+    w[:, K // 2:] = w[:, :K // 2]
+    x[:, 0] = 3
+    y = x.double() @ w.double().t()
+    Y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    ws = cuda_lib.alloc_workspace(cuda_lib.et_i8_gemm_workspace_bytes(M, N, K))
+    cuda_lib.et_i8_gemm(x, torch.ones(M, device="cuda"), w, torch.ones(N, device="cuda"), Y, workspace=ws)
+    # (its bound is written at ref.i8_gemm; the sums of |x w| are taken on the device, exact in 64 bits)
+    e = 0.0 if M <= 8 else K * 2.0 ** -27 * (x.double().abs() @ w.double().t())
+    check(Y, y.cpu(), ref.bf16_bound(y, e + 4 * U * y.abs()).cpu(), "Y")
