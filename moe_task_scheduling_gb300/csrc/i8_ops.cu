@@ -146,7 +146,6 @@ struct I8GemmArgs {
 
 constexpr int kGemvWarps = 8;
 constexpr int kGemvRows = 16;   // channels of a CTA
-constexpr int kGemvTokens = 8;  // tokens of a tile
 constexpr int kGemvAhead = 3;   // 128-byte pieces of K that a warp has on their way
 constexpr int kGemvCtas = 2;    // CTAs an SM
 
@@ -179,8 +178,12 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], int a0, int a1, int a2, int 
 // meanwhile.  A thread's 16-byte loads are its fragments as they are: the order of k within
 // a piece is the same for both operands, and no other order matters to an exact sum.  An
 // integer MMA takes 16 cycles of an SM here, 32 / MT bytes of weights a cycle, where HBM
-// brings 23: MT = 1 is bound by HBM (N = 14336, K = 4096: 11.8 us, 5.0 TB/s from launch to
-// end), MT = 2 by the MMAs (17.7 us).
+// brings 23: up to 8 tokens (14336 x 4096: 11.8 us, 5.0 TB/s from launch to end, bound by
+// HBM).  HALF: both operands become fp16 in registers, whose MMAs take 2 cycles for half as
+// many k; 5 instructions convert 4 bytes, and the sums of a warp, fp32, are exact up to 2^24,
+// so for K up to 8192.  16 tokens 14.8 us (17.7 with integer MMAs); bound by the tokens, which
+// every tile reads again from L2: as many bytes as its weights.  (Loading them one piece
+// ahead, 15.1.)
 template <int MT, bool HALF>
 __global__ void __launch_bounds__(kGemvWarps * 32, kGemvCtas) i8_gemv_kernel(const I8GemmArgs p) {
     __shared__ int red[2][kGemvWarps][8 * MT][kGemvRows + 1];
@@ -286,12 +289,12 @@ __global__ void __launch_bounds__(kGemvWarps * 32, kGemvCtas) i8_gemv_kernel(con
     }
 }
 
-// Which calls take the form above: those of up to 8 tokens, and up to 16 where the weights
-// are few.  With 9 to 16 tokens it takes 2.1 us + 1 us for each 3.8 MB of weights, the
-// tcgen05 form 6 us + 1 us for each 5.5 MB (2048 x 2048: 3.2 against 6.8 us; 14336 x 4096:
-// 17.7 against 16.3 us): they meet at 48 MB.
+// Which calls take the form above: up to 16 tokens, and up to 32 where the weights are few.
+// With 32 tokens it takes 2.2 us + 1 us for each 2.9 MB of weights, the tcgen05 form 6 us +
+// 1 us for each 5.6 MB (1024 x 1024: 3.1 against 6.1 us, 2048 x 2048: 4.0 and 6.5, 14336 x
+// 4096: 22.6 and 16.4): they meet at 22 MB.
 bool i8_gemv(int M_max, int N, int K) {
-    return M_max <= 32;
+    return M_max <= 16 || (M_max <= 32 && static_cast<long long>(N) * K <= 22000000);
 }
 
 bool i8_shape_ok(int M_max, int N, int K, std::string* why) {
