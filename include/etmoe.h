@@ -567,10 +567,11 @@ int et_layer_norm_bwd(const void* x, const void* y, const void* gamma, float eps
  * [M_max,K], w_q int8 [N,K], s_x fp32 [M_max], s_w fp32 [N], Y bf16 [M_max,N],
  * from one token to many.  The sum over k is exact while its partial sums stay
  * within 2^24 (always for K <= 1024, and in a call for at most 8 tokens), and
- * off by at most K 2^-27 sum |x_q w_q| beyond: fp32 sums that the tensor cores cut, not round,
- * after each 16 k.  (Far less where positive and negative products balance:
- * none was off with random signs at K = 65536.)  Every value of int8 is served,
- * -128 too.  The results are the same bits on every run of a shape.
+ * off by at most K 2^-27 sum |x_q w_q| beyond: fp32 sums that the tensor cores
+ * cut, not round, after each 16 k.  (Far less where positive and negative
+ * products balance: none was off with random signs at K = 65536.)  Every value
+ * of int8 is served, -128 too.  The results are the same bits on every run of a
+ * shape.
  *
  * K is a multiple of 16 up to 65536, 1 <= N <= 2^20, 1 <= M_max <= 2^20; x_q, w_q
  * and q 16-byte aligned, x and Y 2-byte, scales 4-byte.  Rows >= M are neither

@@ -16,10 +16,10 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libetmoe.so")
 SOURCES = ["etmoe_api.cu", "moe_kernel.cu", "splitk_kernel.cu", "mlp_kernel.cu", "router_ops.cu",
-           "norm_ops.cu", "w4_ops.cu", "router_groups.cu", "layer_norm_ops.cu", "i8_ops.cu",
+           "norm_ops.cu", "w4_ops.cu", "router_groups.cu", "router_rows.cu", "layer_norm_ops.cu", "i8_ops.cu",
            "i8_gemm_kernel.cu"]
 HEADERS = ["et_api.h", "et_device.cuh", "et_gemm.cuh", "et_layout.h", "ops_device.cuh", "router_sums.cuh", "router_choice.cuh",
-           "router_rows.cuh", "row_ops.cuh", "i8_gemm.h"]
+           "router_rows.h", "row_ops.cuh", "i8_gemm.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

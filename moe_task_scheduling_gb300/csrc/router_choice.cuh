@@ -9,6 +9,8 @@ namespace {
 
 constexpr int kGroupsMax = 32;
 
+}  // namespace
+
 struct GroupArgs {
     const float* logits;     // [T, E]
     const float* bias;       // [E] or null
@@ -24,6 +26,8 @@ struct GroupArgs {
     float scale;
     RouterSums sums;
 };
+
+namespace {
 
 __device__ __forceinline__ double key_value(unsigned long long key) {
     return __longlong_as_double(static_cast<long long>(key >> 63 ? key ^ 0x8000000000000000ull : ~key));

@@ -4,7 +4,7 @@
 #include <cmath>
 
 #include "../../include/etmoe.h"
-#include "router_rows.cuh"
+#include "router_rows.h"
 
 namespace et {
 namespace {
@@ -20,10 +20,10 @@ namespace {
 // decide: on the candidates alone (a lane each: 1.3 us where a whole row takes 14), and on
 // the whole row if they are too many, or for softmax scores with a bias.
 //
-// The form for few rows, and for E that eight lanes cannot share (router_rows4_kernel has the
-// others).  Bound by a row's latency, T = 16, E = 128 6.5 us, then by instruction issue, about
-// 1080 a row at E = 256.  E whose groups are no power of two of lanes looks at the groups one
-// by one: T = 16384, E = 160 43 us.
+// The form for few rows, and for E and groups that eight lanes cannot share
+// (router_rows4_kernel has the others).  Bound by a row's latency, T = 16, E = 128 6.3 us, then
+// by instruction issue, about 1080 a row at E = 256.  Groups that are no power of two of lanes
+// are looked at one by one (T = 16384, E = 160 in 8 groups took 43 us this way).
 template <int EPL, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(const GroupArgs p) {
     constexpr uint32_t kAll = 0xffffffffu, kLow = 32 * EPL - 1;  // the bits that name an expert
@@ -539,7 +539,7 @@ auto pick_groups(bool sigmoid, bool bias) {
                    : (bias ? router_groups_kernel<EPL, false, true> : router_groups_kernel<EPL, false, false>);
 }
 
-// Rows from which on four share a warp, where eight lanes can have a row's experts.  Sigmoid
+// Rows from which on four share a warp, where eight lanes can share a row's experts.  Sigmoid
 // with bias, E = 256, 8 groups: T = 608 14.2 us one a warp and 14.2 four a warp, T = 1024 16.0
 // and 13.2, T = 2048 16.1 and 16.0, T = 4096 19.6 and 15.3, T = 16384 33 and 25, T = 65536 82
 // and 59; E = 64: T = 608 7.8 and 7.7, T = 16384 19 and 13, T = 65536 51 and 28.
@@ -595,14 +595,8 @@ int et_router_groups(const float* logits, const float* bias, const uint8_t* toke
                           router_sums_args(workspace, L, expert_counts, n_routed, mean_prob, loss, false)};
         const bool sig = score == ET_SCORE_SIGMOID;
         const int rows = d_T ? T_max : T > 0 ? T : 1;
-        if ((E == 32 || E == 64 || E == 128 || E == 256) && rows >= kRows4Least) {
-            static SmemOptIn opt[4][4];
-            const int n = E == 32 ? 0 : E == 64 ? 1 : E == 128 ? 2 : 3;
-            auto kernel = n == 0 ? pick_rows4<4>(sig, bias) : n == 1 ? pick_rows4<8>(sig, bias)
-                        : n == 2 ? pick_rows4<16>(sig, bias) : pick_rows4<32>(sig, bias);
-            const int smem = rows4_floats(E) * 4, ctas = ceil_div_i(rows, 4);
-            cudaError_t e = api_smem_opt_in(opt[n][2 * sig + (bias != nullptr)], dev, kernel, smem);
-            if (e == cudaSuccess) e = api_launch(kernel, ctas < kRouterParts ? ctas : kRouterParts, kRows4Warps * 32, smem, stream, a);
+        if (rows >= kRows4Least && rows4_serves(E, n_groups)) {
+            const cudaError_t e = launch_router_rows4(a, sig, rows, dev, stream);
             if (e != cudaSuccess) return api_fail_cuda(e, "launch of the grouped router kernel");
             return ET_OK;
         }

@@ -1,9 +1,7 @@
-// router_rows.cuh -- the grouped router's forward for many rows, four a warp.
-#pragma once
-
+// router_rows.cu -- the grouped router's forward for many rows, four a warp.
 #include <type_traits>
 
-#include "router_choice.cuh"
+#include "router_rows.h"
 
 namespace et {
 namespace {
@@ -13,6 +11,8 @@ constexpr int kRows4Warps = 16;  // of a CTA
 // Floats of dynamic shared memory: [warps][E] sums of batches, then [warps][4][E] of rows.
 __host__ __device__ constexpr int rows4_floats(int E) { return kRows4Warps * 5 * E; }
 
+// For E a multiple of 32 and groups of a power of two in number.
+//
 // Eight lanes have a row, lane l of them experts l N .. l N + N - 1 (E = 8 N), so four rows
 // share each instruction of what is a row's and not an expert's: the eight places of the
 // chosen, ranks of groups, doubts, weights.  The choice and its doubts are those of
@@ -23,12 +23,12 @@ __host__ __device__ constexpr int rows4_floats(int E) { return kRows4Warps * 5 *
 // Bound by instructions and their latency: about 500 a row at E = 256 where one row a warp
 // takes 1080, 16 warps an SM with 128 registers (12 with 168 were slower from T = 1024 to
 // 16384 by 5 to 20 %).  T = 16384, E = 256, sigmoid with bias, 8 groups, k = 8 25-28 us, 8 of
-// them fixed (launch, the sums over CTAs); T = 65536 59 us; E = 128 16 and 35.
+// them fixed (launch, the sums over CTAs); T = 65536 59-63 us; E = 160 19 and E = 128 17 us.
 template <int N, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(kRows4Warps * 32, 1) router_rows4_kernel(const GroupArgs p) {
     constexpr uint32_t kAll = 0xffffffffu;
     constexpr int E = 8 * N;
-    constexpr uint32_t kLow = E - 1;  // the bits that name an expert
+    constexpr uint32_t kLow = E <= 32 ? 31 : E <= 64 ? 63 : E <= 128 ? 127 : 255;  // the bits that name an expert
     constexpr float kU = 1.0f / (1 << 24);
     constexpr int N8 = N < 8 ? N : 8;
     extern __shared__ __align__(16) float sm[];
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kRows4Warps * 32, 1) router_rows4_kernel(const
         for (int o = 0; o < N; o += N8) {
             uint32_t list[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) list[i] = i < N8 ? (key[o + i % N8] & ~kLow) | (kLow - (e0 + o + i)) : 0u;
+            for (int i = 0; i < 8; ++i) list[i] = o + i < N ? (key[(o + i) % N] & ~kLow) | (kLow - (e0 + o + i)) : 0u;
             sort_keys<N8>(list);
             if (o == 0) {
 #pragma unroll
@@ -433,4 +433,24 @@ auto pick_rows4(bool sigmoid, bool bias) {
 }
 
 }  // namespace
+
+cudaError_t launch_router_rows4(const GroupArgs& a, bool sigmoid, int rows, int dev, void* stream) {
+    static SmemOptIn opt[8][4];
+    const bool bias = a.bias != nullptr;
+    auto kernel = pick_rows4<4>(sigmoid, bias);
+    switch (a.E / 32) {
+        case 2: kernel = pick_rows4<8>(sigmoid, bias); break;
+        case 3: kernel = pick_rows4<12>(sigmoid, bias); break;
+        case 4: kernel = pick_rows4<16>(sigmoid, bias); break;
+        case 5: kernel = pick_rows4<20>(sigmoid, bias); break;
+        case 6: kernel = pick_rows4<24>(sigmoid, bias); break;
+        case 7: kernel = pick_rows4<28>(sigmoid, bias); break;
+        case 8: kernel = pick_rows4<32>(sigmoid, bias); break;
+    }
+    const int smem = rows4_floats(a.E) * 4, ctas = ceil_div_i(rows, 4);
+    const cudaError_t e = api_smem_opt_in(opt[a.E / 32 - 1][2 * sigmoid + bias], dev, kernel, smem);
+    if (e != cudaSuccess) return e;
+    return api_launch(kernel, ctas < kRouterParts ? ctas : kRouterParts, kRows4Warps * 32, smem, stream, a);
+}
+
 }  // namespace et

@@ -25,6 +25,8 @@ __device__ __forceinline__ float key_logit(uint32_t key) {
     return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
 }
 
+}  // namespace
+
 // Where the sums go (each output may be null) and meet.
 struct RouterSums {
     int32_t* counts;         // [E]
@@ -37,6 +39,8 @@ struct RouterSums {
     float* part_z;           // [kRouterParts]
     int32_t* part_n;         // [kRouterParts]
 };
+
+namespace {
 
 struct RouterShared {
     int hist[kRouterEMax];   // how often this CTA's tokens chose an expert

@@ -306,7 +306,7 @@ def test_no_bias_and_one_group_choose_as_the_plain_router(cuda_lib):
     assert torch.equal(o["idx"], idx)
 
 
-@pytest.mark.parametrize("T,En", [(77, 40), (77, 128), (77, 160), (77, 256), (1030, 64), (1030, 256)])
+@pytest.mark.parametrize("T,En", [(77, 40), (77, 128), (77, 160), (77, 256), (1030, 64), (1030, 160), (1030, 256)])
 @pytest.mark.parametrize("sigmoid", [True, False])
 def test_any_alignment(cuda_lib, T, En, sigmoid):
     """Logits and gradients that start anywhere: what aligned ones give."""
@@ -329,7 +329,7 @@ def test_any_alignment(cuda_lib, T, En, sigmoid):
 
 # ------------------------------------------------------------------ many rows: four share a warp
 
-MANY = [(En, G) for En in (32, 64, 128, 256) for G in (1, 2, 4, 8, 16, 32)]
+MANY = [(En, G) for En in (32, 64, 128, 256) for G in (1, 2, 4, 8, 16, 32)] + [(96, 4), (96, 32), (160, 8), (160, 32), (192, 16), (192, 3), (224, 2), (224, 8), (120, 8)]
 
 
 @pytest.mark.parametrize("En,G", MANY)
@@ -369,7 +369,8 @@ def _hard_rows(T, En, G, g):
     return L
 
 
-@pytest.mark.parametrize("En,G,kg", [(32, 8, 4), (32, 32, 9), (64, 16, 5), (64, 1, 1), (128, 4, 2), (128, 16, 6), (256, 8, 4), (256, 32, 8), (256, 2, 1)])
+@pytest.mark.parametrize("En,G,kg", [(32, 8, 4), (32, 32, 9), (64, 16, 5), (64, 1, 1), (128, 4, 2), (128, 16, 6), (256, 8, 4), (256, 32, 8), (256, 2, 1), (96, 16, 4),
+                                      (160, 8, 3), (192, 32, 11), (224, 4, 2)])
 @pytest.mark.parametrize("sigmoid", [True, False])
 @pytest.mark.parametrize("bias", [None, "random", "zero", "some"])
 def test_four_rows_a_warp_choose_as_one(cuda_lib, En, G, kg, sigmoid, bias):
