@@ -390,9 +390,9 @@ struct GroupBwdArgs {
 // A token is routed if it has an index that is not -1.
 //
 // VEC (E a multiple of four, tensors 16-byte aligned): a lane has four neighbours in one
-// access.  T = 16384, E = 256: 8.8 us, 3.8 TB/s, 64 % of the issue slots (11.1 with 4-byte
-// accesses, scores told apart at run time and three sums one by one); one to two rows a warp
-// leave little to hide a row's loads behind.
+// access.  T = 16384, E = 256: 7.6 us, 4.4 TB/s (11.1 with 4-byte accesses, scores told apart
+// at run time, three sums one by one and 8 CTAs an SM); bound by issue slots, 64 % of them,
+// and the loads of the first rows.
 template <int EPL, bool SIGMOID, bool VEC>
 __global__ void __launch_bounds__(256) router_groups_bwd_kernel(const GroupBwdArgs p) {
     constexpr uint32_t kAll = 0xffffffffu;
@@ -632,8 +632,12 @@ int et_router_groups_bwd(const float* logits, const uint8_t* token_mask, int sco
                              T, T_max, E, k, renorm != 0, scale != 0.0f ? 1.0f / scale : 0.0f,
                              static_cast<EtHeader*>(workspace)};
         const int rows = d_T ? T_max : T;
+        // With 8 experts a lane as many CTAs as find room at once, which then hide a row's loads
+        // behind the one before it (T = 16384, E = 256: 7.6 us, with 8 an SM 8.8); with fewer,
+        // rows are short and more CTAs hide more (E = 128: 5.8 us, with 3 7.7).
+        const int most = (E > 128 ? 3 : 8) * sms;
         int grid = ceil_div_i(rows, 8);
-        grid = grid < 8 * sms ? grid : 8 * sms;
+        grid = grid < most ? grid : most;
         const bool sig = score == ET_SCORE_SIGMOID, vec = E > 64 && E % 4 == 0 && api_aligned(logits, 16) && api_aligned(d_logits, 16);
         auto kernel = E <= 32 ? pick_bwd<1, false>(sig) : E <= 64 ? pick_bwd<2, false>(sig)
                     : E <= 128 ? (vec ? pick_bwd<4, true>(sig) : pick_bwd<4, false>(sig))
