@@ -315,9 +315,10 @@ __host__ __device__ constexpr int ln_row_bytes(int H, bool vec, int vectors) { r
 // are floats in shared memory (unpacked anew for each row they were two of 33 instructions
 // an element).  T = H = 4096: 20.5 us, 6.5 TB/s without dropout, bound by HBM; 23.3 us, 5.8
 // TB/s with it, by issue slots too (30 instructions an element, 62 % of the slots).
-// Without VEC by its 2-byte accesses: 4096 x 1001 13 us, 2.5 TB/s; with dropout 20.
+// Without VEC by its 2-byte accesses: 4096 x 1001 13 us, 2.5 TB/s; with dropout 18 (20 with
+// 125 registers and two CTAs an SM).
 template <bool VEC, int MODE, int MAXT>
-__global__ void __launch_bounds__(MAXT) ln_fwd_kernel(const LnArgs p) {
+__global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : VEC ? 4 : 3) ln_fwd_kernel(const LnArgs p) {
     constexpr int V = norm_v(MODE);
     __shared__ RowSums<1> sums;
     extern __shared__ __align__(16) uint8_t dyn[];  // gamma, beta; without VEC [groups][H / 8] mask bytes
