@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : VEC ? 4 : 3) ln_fwd_ker
 // Without VEC a row is copied by the 16-byte pieces that hold it (the first of a
 // tensor element by element, the last cut to its end) and read back by element,
 // with a barrier on either side.  Rows of H > 8192 do not fit twice and are copied
-// one at a time.  T = H = 4096 with dropout: 33 us, 6.1 TB/s, and 40 us with the parameter
+// one at a time.  T = H = 4096 with dropout: 33 us, 6.1 TB/s, and 39 us with the parameter
 // gradients: 304 rows of partial sums are written and read again, and a second kernel starts.
 // (512-thread CTAs of two rows, half the partial sums, took 44.)  The parameter gradients
 // are added up in registers, for 256 rows
@@ -687,29 +687,36 @@ struct LnSumArgs {
     int T_max;
 };
 
-// Column sums of the partial rows: 32 columns x 32 row groups a CTA, a thread's loads all
-// on their way at once.
-__global__ void __launch_bounds__(1024) ln_sum_kernel(const LnSumArgs p) {
-    __shared__ float red[32][33];
+// Column sums of the partial rows: 32 columns x kSumGroups row groups a CTA, a thread's loads
+// all on their way at once.  Bound by latency: with its launch 3 us for one row, 6 for 304 of
+// H = 4096.  (8 groups 6.4 of a call of one row and 11.6 of one of 304, 16 6.0 and 10.0, 32
+// 6.7 and 10.5.)
+constexpr int kSumGroups = 16;
+__global__ void __launch_bounds__(kSumGroups * 32) ln_sum_kernel(const LnSumArgs p) {
+    __shared__ float red[kSumGroups][32];
     grid_begin();
     if (p.d_T && (*p.d_T < 0 || *p.d_T > p.T_max)) return;
     float* out = p.out[blockIdx.y];
     const int arr = p.arr[blockIdx.y];
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
-    constexpr int kLoads = (kLnParts + 31) / 32;
-    float v[kLoads], s = 0.0f;
+    constexpr int kLoads = (kLnParts + kSumGroups - 1) / kSumGroups;
+    float v[kLoads], s = 0.0f, u = 0.0f;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-        const int g = grp + 32 * i;
+        const int g = grp + kSumGroups * i;
         v[i] = g < p.parts && c < p.H ? __ldcg(p.part + (static_cast<size_t>(g) * 2 + arr) * p.H + c) : 0.0f;
     }
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) s += v[i];
-    red[grp][lane] = s;
+    for (int i = 0; i < kLoads; ++i) (i & 1 ? u : s) += v[i];
+    red[grp][lane] = s + u;
     __syncthreads();
-    s = warp_sum(red[lane][grp]);  // warp grp: its column's 32 groups
-    if (lane == 0 && blockIdx.x * 32 + grp < p.H) out[blockIdx.x * 32 + grp] = s;
+    if (grp == 0 && c < p.H) {
+        s = u = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kSumGroups; ++i) (i & 1 ? u : s) += red[i][lane];
+        out[c] = s + u;
+    }
 }
 
 // ---------------------------------------------------------------- host
@@ -962,7 +969,7 @@ int et_layer_norm_bwd(const void* x, const void* y, const void* gamma, float eps
             if (e != cudaSuccess) return api_fail_cuda(e, "launch of the layer norm's backward kernel");
         }
         if (n) {
-            const cudaError_t e = api_launch(ln_sum_kernel, dim3((H + 31) / 32, n), 1024, 0, stream, s);
+            const cudaError_t e = api_launch(ln_sum_kernel, dim3((H + 31) / 32, n), kSumGroups * 32, 0, stream, s);
             if (e != cudaSuccess) return api_fail_cuda(e, "launch of the layer norm's parameter sums");
         }
         return ET_OK;
