@@ -247,11 +247,21 @@ __device__ __forceinline__ uint32_t sum_key(float v) {
 
 constexpr int kCandidates = 16;  // experts whose order is looked at again at most
 
-// What ranks experts and groups in 64 bits: sigmoid scores + bias; for softmax scores (without
-// a bias) their multiples e^(x - top).
-__device__ __forceinline__ double value64(float x, float b, bool sigmoid, float top) {
+// What ranks experts and groups in 64 bits: scores + bias, softmax scores by their row's sum Z
+// of e^(x - top); Z = 0: softmax scores without a bias, as their multiples e^(x - top).
+__device__ __forceinline__ double value64(float x, float b, bool sigmoid, float top, double Z) {
     const double e = exp(sigmoid ? -static_cast<double>(x) : static_cast<double>(x) - static_cast<double>(top));
-    return sigmoid ? 1.0 / (1.0 + e) + static_cast<double>(b) : e;
+    return sigmoid ? 1.0 / (1.0 + e) + static_cast<double>(b) : Z > 0.0 ? e / Z + static_cast<double>(b) : e;
+}
+
+// The sum of e^(x - top) over a row, in 64 bits, by the warp.
+__device__ __noinline__ double softmax_sum64(const float* row, float top, int E, int lane) {
+    double Z = 0.0;
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32) Z += exp(static_cast<double>(row[e]) - static_cast<double>(top));
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) Z += __shfl_xor_sync(0xffffffffu, Z, off);
+    return Z;
 }
 
 // Two groups whose scores 32 bits cannot tell apart: 1 if the first has the larger, or the
@@ -259,7 +269,7 @@ __device__ __forceinline__ double value64(float x, float b, bool sigmoid, float 
 // say.  floor_a, floor_b: what the experts that count are not below;
 // want_a, want_b: how many those are.  slots: 16 places of shared memory.
 template <int EPL>
-__device__ __noinline__ int compare_groups(const float* row, const float* bias_s, bool sigmoid, float top, float inv, int E,
+__device__ __noinline__ int compare_groups(const float* row, const float* bias_s, bool sigmoid, float top, float inv, double Z, int E,
                                            int gs, int a, int b, float floor_a, float floor_b, int want_a, int want_b, uint32_t* slots, int lane) {
     constexpr uint32_t kAll = 0xffffffffu;
     int na = 0, nb = 0;
@@ -280,18 +290,19 @@ __device__ __noinline__ int compare_groups(const float* row, const float* bias_s
     if (na != want_a || nb != want_b) return -1;
     const bool mine = lane < na || (lane >= 8 && lane < 8 + nb);
     const int e = mine ? static_cast<int>(slots[lane]) : 0;
-    double c = mine ? value64(row[e], bias_s[e], sigmoid, top) : 0.0;
+    double c = mine ? value64(row[e], bias_s[e], sigmoid, top, Z) : 0.0;
     c += __shfl_xor_sync(kAll, c, 1);  // two at most
     const double sa = __shfl_sync(kAll, c, 0), sb = __shfl_sync(kAll, c, 8);
     return sa > sb || (sa == sb && a < b) ? 1 : 0;
 }
 
 // The order of n candidates (n <= kCandidates, their experts in slots) in 64 bits (of softmax
-// scores without a bias by the logits): puts the best k there in their order.
-__device__ __noinline__ void order_again(const float* row, const float* bias_s, bool sigmoid, int n, int k, uint32_t* slots, int lane) {
+// scores without a bias, Z = 0, by the logits): puts the best k there in their order.
+__device__ __noinline__ void order_again(const float* row, const float* bias_s, bool sigmoid, float top, double Z, int n, int k, uint32_t* slots,
+                                         int lane) {
     constexpr uint32_t kAll = 0xffffffffu;
     const int e = lane < n ? static_cast<int>(slots[lane]) : 0;
-    const double c = lane < n ? (sigmoid ? value64(row[e], bias_s[e], true, 0.0f) : static_cast<double>(row[e])) : 0.0;
+    const double c = lane < n ? (sigmoid || Z > 0.0 ? value64(row[e], bias_s[e], sigmoid, top, Z) : static_cast<double>(row[e])) : 0.0;
     const unsigned long long key = value_key(c);
     int rank = 0;
 #pragma unroll 1

@@ -18,7 +18,7 @@ namespace {
 // both errors, where more than k experts are above the k-th less both errors (those that
 // equal it apart), or the last group that takes part and the next than theirs, 64 bits
 // decide: on the candidates alone (a lane each: 1.3 us where a whole row takes 14), and on
-// the whole row if they are too many, or for softmax scores with a bias.
+// the whole row if they are too many.
 //
 // The form for few rows, and for E and groups that eight lanes cannot share
 // (router_rows4_kernel has the others).  Bound by a row's latency, T = 16, E = 128 6.3 us, then
@@ -198,11 +198,12 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
                 // between these two alone?
                 const bool other = group && !(rank < p.kg - 1 ? score - b > tol : rank > p.kg ? a - score > tol : true);
                 const bool others = __any_sync(kAll, other);
-                again = (!SIGMOID && BIAS) || !(tol < 1.0f) || others;
+                again = !(tol < 1.0f) || others;
                 if (!again) {
                     const bool two = p.best > 1 && lo > kNegInfKey;
                     const float floor = key_or_none(two ? lo : hi) - tol;  // the last that counts
-                    const int r = compare_groups<EPL>(row, bias_s, SIGMOID, top, inv, E, p.gs, la / wide, lb / wide,
+                    const double Z = !SIGMOID && BIAS ? softmax_sum64(row, top, E, lane) : 0.0;
+                    const int r = compare_groups<EPL>(row, bias_s, SIGMOID, top, inv, Z, E, p.gs, la / wide, lb / wide,
                                                       __shfl_sync(kAll, floor, la), __shfl_sync(kAll, floor, lb),
                                                       __shfl_sync(kAll, two ? 2 : 1, la), __shfl_sync(kAll, two ? 2 : 1, lb),
                                                       chosen[warp], lane);
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
                 doubt = true;  // (a NaN)
             }
             if (__any_sync(kAll, doubt || met) && !again) {
-                again = (!SIGMOID && BIAS) || __any_sync(kAll, met) || n > kCandidates || n == 0;
+                again = __any_sync(kAll, met) || n > kCandidates || n == 0 || !(err < 1.0f);
                 if (!again) {
                     int at = 0;
                     __syncwarp();
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
                         at += __popc(who);
                     }
                     __syncwarp();
-                    order_again(row, bias_s, SIGMOID, n, k, chosen[warp], lane);
+                    order_again(row, bias_s, SIGMOID, top, !SIGMOID && BIAS ? softmax_sum64(row, top, E, lane) : 0.0, n, k, chosen[warp], lane);
                     on = lane < k && lane < n;
                     myE = on ? static_cast<int>(chosen[warp][lane & (kCandidates - 1)]) : 0;
                     myL = on ? row[myE] : -INFINITY;

@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kRows4Warps * 32, 1) router_rows4_kernel(const
                     for (int m = 0; m < M; ++m)
                         other |= rank[m] < p.kg - 1 ? !(score[m] - b > tol) : rank[m] > p.kg && !(a - score[m] > tol);
                     const bool others = of_row(__ballot_sync(kAll, other)) != 0;
-                    again = close && ((!SIGMOID && BIAS) || !(tol < 1.0f) || others);
+                    again = close && (!(tol < 1.0f) || others);
                     // between these two alone: what counts for a group is not below its floor
                     float fa = 0.0f, fb = 0.0f;
                     int na = 1, nb = 1;
@@ -250,8 +250,10 @@ __global__ void __launch_bounds__(kRows4Warps * 32, 1) router_rows4_kernel(const
                     for (int rr = 0; rr < 4; ++rr) {
                         if (!(rows >> (8 * rr) & 1)) continue;
                         const int from = 8 * rr;
-                        const int c = compare_groups<N / 4>(p.logits + static_cast<size_t>(tb + rr) * E, bias_s, SIGMOID, __shfl_sync(kAll, top, from),
-                                                            __shfl_sync(kAll, inv, from), E, p.gs, __shfl_sync(kAll, ga, from), __shfl_sync(kAll, gb, from),
+                        const float* const its_row = p.logits + static_cast<size_t>(tb + rr) * E;
+                        const float its_top = __shfl_sync(kAll, top, from);
+                        const double Z = !SIGMOID && BIAS ? softmax_sum64(its_row, its_top, E, lane) : 0.0;
+                        const int c = compare_groups<N / 4>(its_row, bias_s, SIGMOID, its_top, __shfl_sync(kAll, inv, from), Z, E, p.gs, __shfl_sync(kAll, ga, from), __shfl_sync(kAll, gb, from),
                                                             __shfl_sync(kAll, fa, from), __shfl_sync(kAll, fb, from), __shfl_sync(kAll, na, from),
                                                             __shfl_sync(kAll, nb, from), slots[rr], lane);
                         if (r == rr) {
@@ -336,7 +338,7 @@ __global__ void __launch_bounds__(kRows4Warps * 32, 1) router_rows4_kernel(const
             doubt |= n < k && n > 0;  // (a NaN)
             const bool row_met = of_row(__ballot_sync(kAll, met)) != 0;
             const bool row_doubt = of_row(__ballot_sync(kAll, doubt)) != 0 || row_met;
-            const bool whole = (!SIGMOID && BIAS) || row_met || n > kCandidates || n == 0;
+            const bool whole = row_met || n > kCandidates || n == 0 || !(err < 1.0f);
             const bool few = row_doubt && !again && !whole;
             again |= row_doubt && whole;
             const uint32_t rows = __ballot_sync(kAll, few) & 0x01010101u;
@@ -358,7 +360,10 @@ __global__ void __launch_bounds__(kRows4Warps * 32, 1) router_rows4_kernel(const
 #pragma unroll 1
                 for (int rr = 0; rr < 4; ++rr) {
                     if (!(rows >> (8 * rr) & 1)) continue;
-                    order_again(p.logits + static_cast<size_t>(tb + rr) * E, bias_s, SIGMOID, __shfl_sync(kAll, n, 8 * rr), k, slots[rr], lane);
+                    const float* const its_row = p.logits + static_cast<size_t>(tb + rr) * E;
+                    const float its_top = __shfl_sync(kAll, top, 8 * rr);
+                    const double Z = !SIGMOID && BIAS ? softmax_sum64(its_row, its_top, E, lane) : 0.0;
+                    order_again(its_row, bias_s, SIGMOID, its_top, Z, __shfl_sync(kAll, n, 8 * rr), k, slots[rr], lane);
                 }
                 if (few) {
                     on = l8 < k && l8 < n;
