@@ -438,9 +438,9 @@ int et_block_norm_bwd(const void* x, const void* y, const void* gamma_post, cons
  * The bias enters the choice alone: weights, losses and gradients do not see
  * it (a program moves it by the counts, for balance).  The choice is that of
  * exact arithmetic: rows where the fp32 values of two candidates are closer
- * than their errors are chosen again in 64 bits (a few times the time of a
- * row; logits that are all equal come there in every row).  Values that are
- * equal in 64 bits tie.  With x0 the row's largest logit (with renorm, the
+ * than their errors are chosen again in 64 bits, which takes a few times a
+ * row's time, more where many are that close (a row of equal logits and biases
+ * is not among them).  Values that are equal in 64 bits tie.  With x0 the row's largest logit (with renorm, the
  * largest chosen one), a weight is off by a factor of at most
  * 1 +- (20 + E + |x - x0|) 2^-24, a p by 1 +- (48 + E + 4 |x - x0| + 5 |x|) 2^-24.
  * Scores below 2^-126 may be 0.  Sums over tokens run in a fixed order.

@@ -194,7 +194,14 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
             const float a = __shfl_sync(kAll, score, la), b = __shfl_sync(kAll, score, lb);
             const float tol = 2.0f * __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(off_by)));
             bool part = group && rank < p.kg;
-            if (!(a - b > tol) && !(b == -INFINITY)) {
+            bool close = masked_in && !(a - b > tol) && !(b == -INFINITY);
+            if (close) {  // but for a row of equal logits and biases (an untrained router's): the order is the experts'
+                bool flat = true;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) flat = flat && (e0 + i >= E || (v[i] == row[0] && (!BIAS || bias_s[e0 + i] == bias_s[0])));
+                close = !__all_sync(kAll, flat);
+            }
+            if (close) {
                 // between these two alone?
                 const bool other = group && !(rank < p.kg - 1 ? score - b > tol : rank > p.kg ? a - score > tol : true);
                 const bool others = __any_sync(kAll, other);
@@ -278,7 +285,7 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
             } else if (n < k && n > 0) {
                 doubt = true;  // (a NaN)
             }
-            if (__any_sync(kAll, doubt || met) && !again) {
+            if (__any_sync(kAll, doubt || met) && !again && masked_in) {
                 again = __any_sync(kAll, met) || n > kCandidates || n == 0 || !(err < 1.0f);
                 if (!again) {
                     int at = 0;

@@ -197,14 +197,14 @@ __global__ void __launch_bounds__(kRows4Warps * 32, 1) router_rows4_kernel(const
                     mine[m] = logit_key(score[m]);
                     rank[m] = 0;
                 }
-                const int first = M > 1 ? l8 * M : l8 / L;  // this lane's first group
+                const int group0 = M > 1 ? l8 * M : l8 / L;  // this lane's first group
 #pragma unroll 2
                 for (int g = 0; g < G; g += M) {
 #pragma unroll
                     for (int o = 0; o < M; ++o) {
                         const uint32_t other = __shfl_sync(kAll, mine[o], M > 1 ? g / M : g * L, 8);
 #pragma unroll
-                        for (int m = 0; m < M; ++m) rank[m] += other > mine[m] || (other == mine[m] && g + o < first + m);
+                        for (int m = 0; m < M; ++m) rank[m] += other > mine[m] || (other == mine[m] && g + o < group0 + m);
                     }
                 }
                 // the last that takes part and the next: apart by more than any two may be off
@@ -225,8 +225,17 @@ __global__ void __launch_bounds__(kRows4Warps * 32, 1) router_rows4_kernel(const
                 bool part[M];
 #pragma unroll
                 for (int m = 0; m < M; ++m) part[m] = rank[m] < p.kg;
-                const bool close = have && !(a - b > tol) && !(b == -INFINITY);
+                bool close = masked_in && !(a - b > tol) && !(b == -INFINITY);
                 if (__any_sync(kAll, close)) {
+                    // a row of equal logits and biases (an untrained router's): the order is the experts'
+                    float v[N];
+                    load(row, have, v);
+                    const float first = __shfl_sync(kAll, v[0], 0, 8);
+                    bool flat = true;
+#pragma unroll
+                    for (int i = 0; i < N; ++i) flat = flat && v[i] == first && (!BIAS || bias_s[e0 + i] == bias_s[0]);
+                    const uint32_t flat_lanes = of_row(__ballot_sync(kAll, flat));
+                    close = close && flat_lanes != 0xffu;
                     bool other = false;
 #pragma unroll
                     for (int m = 0; m < M; ++m)
@@ -337,7 +346,8 @@ __global__ void __launch_bounds__(kRows4Warps * 32, 1) router_rows4_kernel(const
             }
             doubt |= n < k && n > 0;  // (a NaN)
             const bool row_met = of_row(__ballot_sync(kAll, met)) != 0;
-            const bool row_doubt = of_row(__ballot_sync(kAll, doubt)) != 0 || row_met;
+            const bool any_doubt = of_row(__ballot_sync(kAll, doubt)) != 0;
+            const bool row_doubt = masked_in && (any_doubt || row_met);
             const bool whole = row_met || n > kCandidates || n == 0 || !(err < 1.0f);
             const bool few = row_doubt && !again && !whole;
             again |= row_doubt && whole;
