@@ -146,7 +146,6 @@ struct I8GemmArgs {
 
 constexpr int kGemvWarps = 8;
 constexpr int kGemvRows = 16;   // channels of a CTA
-constexpr int kGemvAhead = 3;   // 128-byte pieces of K that a warp has on their way
 constexpr int kGemvCtas = 2;    // CTAs an SM
 
 __device__ __forceinline__ int4 load_weights(const int8_t* p) {  // streamed: the tokens keep L1
@@ -181,15 +180,16 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], int a0, int a1, int a2, int 
 // brings 23: up to 8 tokens (14336 x 4096: 11.8 us, 5.0 TB/s from launch to end, bound by
 // HBM).  HALF: both operands become fp16 in registers, whose MMAs take 2 cycles for half as
 // many k; 5 instructions convert 4 bytes, and the sums of a warp, fp32, are exact up to 2^24,
-// so for K up to 8192.  16 tokens 14.8 us (17.7 with integer MMAs); bound by the tokens, which
-// every tile reads again from L2: as many bytes as its weights.  (Loading them one piece
-// ahead, 15.1.)
+// so for K up to 8192.  16 tokens 13.8 us (17.7 with integer MMAs); bound by its instructions'
+// latency and by the tokens, which every tile reads again: as many bytes as its weights.
+// (Three pieces ahead in place of two 14.7, the tokens one piece ahead 15.1, three CTAs an SM
+// with one piece 14.1 and 20 for 4096 x 14336.)
 template <int MT, bool HALF>
 __global__ void __launch_bounds__(kGemvWarps * 32, kGemvCtas) i8_gemv_kernel(const I8GemmArgs p) {
     __shared__ int red[2][kGemvWarps][8 * MT][kGemvRows + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
     const int K = p.K, tiles = (p.N + kGemvRows - 1) / kGemvRows, k0 = warp * 128 + q * 16;
-    constexpr int kStep = kGemvWarps * 128;
+    constexpr int kStep = kGemvWarps * 128, kAhead = HALF ? 2 : 3;  // pieces of K that a warp has on their way
     // Where this thread's next piece is.
     int ft = blockIdx.x, fk = k0;
     auto rows_of = [&](int t, const int8_t*& w0, const int8_t*& w1) {
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kGemvWarps * 32, kGemvCtas) i8_gemv_kernel(con
     // Nothing is read before what comes before has ended, but the first pieces may be on
     // their way to L2 by then.
 #pragma unroll
-    for (int i = 0; i < kGemvAhead; ++i)
+    for (int i = 0; i < kAhead; ++i)
         if (fk + i * kStep < K) {
             asm volatile("prefetch.global.L2 [%0];" ::"l"(w0 + fk + i * kStep));
             asm volatile("prefetch.global.L2 [%0];" ::"l"(w1 + fk + i * kStep));
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kGemvWarps * 32, kGemvCtas) i8_gemv_kernel(con
 #pragma unroll
     for (int t = 0; t < MT; ++t) x[t] = p.x + static_cast<size_t>(min(8 * t + g, M - 1)) * K;
     const int4 zero = make_int4(0, 0, 0, 0);
-    int4 wv[kGemvAhead][4];  // rows g and g + 8, bytes k and k + 64
+    int4 wv[kAhead][4];  // rows g and g + 8, bytes k and k + 64
     auto fetch = [&](int4 (&v)[4]) {
         const bool here = ft < tiles;
         v[0] = here && fk < K ? load_weights(w0 + fk) : zero;
@@ -229,13 +229,13 @@ __global__ void __launch_bounds__(kGemvWarps * 32, kGemvCtas) i8_gemv_kernel(con
         }
     };
 #pragma unroll
-    for (int i = 0; i < kGemvAhead; ++i) fetch(wv[i]);
+    for (int i = 0; i < kAhead; ++i) fetch(wv[i]);
     int tile = blockIdx.x, k = k0, buf = 0;
     using Acc = std::conditional_t<HALF, float, int>;
     Acc acc[MT][4] = {};
     while (tile < tiles) {
 #pragma unroll
-        for (int i = 0; i < kGemvAhead; ++i) {
+        for (int i = 0; i < kAhead; ++i) {
             if (tile >= tiles) break;
             if constexpr (HALF) {
 #pragma unroll
