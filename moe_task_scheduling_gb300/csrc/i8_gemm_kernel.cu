@@ -322,18 +322,16 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
     if (warp == 0) {
         if (lane == 0) {
             const uint64_t pol = policy_evict_first();
-            if (CG == 1) {
-                // Nothing is read before what comes before this kernel has ended, but the first
-                // blocks may be on their way to L2 by then.
-                Work f = w;
-                if (f.next())
-                    for (int kb = f.kb0; kb < f.kb1 && kb < f.kb0 + p.stages_w; ++kb)
-                        tma_prefetch_l2(&tm_w, kb * kI8KBlock, (f.tile / mt) * 128);
-                grid_wait();
-                fence_proxy_async_global();
-            }
-            // (A pair's kernel comes behind the call's own first kernel, which lets it start only
-            // when all before that one has ended: its weights need no wait.)
+            // Nothing is read before what comes before this kernel has ended, but the first blocks
+            // may be on their way to L2 by then.  (A pair's kernel waits for the call's own first
+            // kernel, which has waited for what came before it, the weights' writer too.  That
+            // this kernel starts only then does not show it those writes: the wait does.)
+            Work f = w;
+            if (f.next())
+                for (int kb = f.kb0; kb < f.kb1 && kb < f.kb0 + p.stages_w; ++kb)
+                    tma_prefetch_l2(&tm_w, kb * kI8KBlock, (f.tile / mt) * 128 * CG + static_cast<int>(rank) * 128);
+            grid_wait();
+            fence_proxy_async_global();
             uint32_t s = 0, phase = 0, posted = 0;
             bool ok = true;
             while (ok && w.next()) {
@@ -562,10 +560,7 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
 }
 
 __global__ void __launch_bounds__(256) i8_expand_kernel(const I8ExpandArgs p) {
-    // In this order: the product's kernel may start when every CTA has come past the second,
-    // so all that came before this call is complete by then.
-    grid_wait();
-    grid_release();
+    grid_begin();
     const int at = blockIdx.x * blockDim.x + threadIdx.x, step = gridDim.x * blockDim.x;
     const long long n = static_cast<long long>(pass_rows(p.rows, p.hdr)) * p.K / 16;
     const uint4* x = reinterpret_cast<const uint4*>(p.x);
