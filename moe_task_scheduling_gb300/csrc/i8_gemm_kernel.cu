@@ -318,20 +318,23 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
     const int mt = ceil_div(M, p.tn), tiles = mt * p.nt;  // tile = n tile * mt + m tile
     const int slots = p.tn > 128 ? 1 : 2;                 // accumulators
     Work w(p, tiles, blockIdx.x / CG);
+    // Nothing else is read before what comes before this kernel has ended (for a pair that is
+    // the call's own first kernel, which has waited for the rest): an early start shows this
+    // kernel nothing of that, the wait does.  The first blocks of weights may be on their way
+    // to L2 by then.  Every role waits, so that the limit of its own waits runs in this
+    // kernel's time and not in an earlier one's, however long that goes on.
+    if (threadIdx.x == 0) {
+        Work f = w;
+        if (f.next())
+            for (int kb = f.kb0; kb < f.kb1 && kb < f.kb0 + p.stages_w; ++kb)
+                tma_prefetch_l2(&tm_w, kb * kI8KBlock, (f.tile / mt) * 128 * CG + static_cast<int>(rank) * 128);
+    }
+    grid_wait();
 
     if (warp == 0) {
         if (lane == 0) {
             const uint64_t pol = policy_evict_first();
-            // Nothing is read before what comes before this kernel has ended, but the first blocks
-            // may be on their way to L2 by then.  (A pair's kernel waits for the call's own first
-            // kernel, which has waited for what came before it, the weights' writer too.  That
-            // this kernel starts only then does not show it those writes: the wait does.)
-            Work f = w;
-            if (f.next())
-                for (int kb = f.kb0; kb < f.kb1 && kb < f.kb0 + p.stages_w; ++kb)
-                    tma_prefetch_l2(&tm_w, kb * kI8KBlock, (f.tile / mt) * 128 * CG + static_cast<int>(rank) * 128);
-            grid_wait();
-            fence_proxy_async_global();
+            fence_proxy_async_global();  // weights that a kernel wrote, read by TMA
             uint32_t s = 0, phase = 0, posted = 0;
             bool ok = true;
             while (ok && w.next()) {
@@ -351,7 +354,6 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
         __syncwarp();
     } else if (warp == kTokenWarp) {
         if (CG == 2 && lane == 0) {
-            grid_wait();
             fence_proxy_async_global();  // the first kernel's stores, read by TMA
             uint32_t s = 0, phase = 0, posted = 0;
             bool ok = true;
@@ -461,7 +463,6 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
         }
     } else {
         const int q = warp & 3, odd = (warp - kEpiWarpI8) >> 2, et = threadIdx.x - kEpiWarpI8 * 32, row = q * 32 + lane;
-        grid_wait();
         uint32_t acc = 0, s = 0, phase = 0;
         bool ok = true;
         while (ok && w.next()) {
