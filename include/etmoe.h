@@ -577,8 +577,12 @@ int et_layer_norm_bwd(const void* x, const void* y, const void* gamma, float eps
  * and q 16-byte aligned, x and Y 2-byte, scales 4-byte.  Rows >= M are neither
  * read nor written.  M and d_M as in et_splitk_gemm.  et_i8_quantize needs 256
  * bytes of workspace (for its status).  A wait inside et_i8_gemm that ran out
- * (0.2 s) is recorded as ET_ERR_TIMEOUT (et_status), and Y is then incomplete.
- * Errors as et_moe_layer.
+ * (0.2 s, of the call's own time) is recorded as ET_ERR_TIMEOUT (et_status), and
+ * Y is then incomplete; later calls are served as ever.  et_i8_gemm_opts is
+ * et_i8_gemm with opts (NULL: none): timeout_us sets that limit, and the test
+ * hook fault_mode 1 leaves out the weights' loads of CTA fault_arg, in each of
+ * the call's launches.  (Up to 16 tokens, 32 on few weights, nothing waits and
+ * both have no effect.)  Errors as et_moe_layer.
  * ---------------------------------------------------------------------- */
 size_t et_i8_quantize_workspace_bytes(int M_max, int K);
 
@@ -590,6 +594,10 @@ size_t et_i8_gemm_workspace_bytes(int M_max, int N, int K);
 int et_i8_gemm(const void* x_q, const float* s_x, const void* w_q, const float* s_w, void* Y,
                int M, const int32_t* d_M, int M_max, int N, int K, void* workspace,
                size_t workspace_bytes, void* stream);
+
+int et_i8_gemm_opts(const void* x_q, const float* s_x, const void* w_q, const float* s_w, void* Y,
+                    int M, const int32_t* d_M, int M_max, int N, int K, void* workspace,
+                    size_t workspace_bytes, const et_opts* opts, void* stream);
 
 /* ------------------------------------------------------------------------
  * Products with 4-bit weights, for decoding (the source paper has no

@@ -20,6 +20,7 @@ int api_fail(int code, const std::string& msg);
 int api_fail_cuda(cudaError_t e, const char* what);
 int api_device(int* dev, int* sms);  // current device (sm_103a checked) and its SM count
 int api_check_ws(const void* ws, size_t have, size_t need);
+uint64_t api_timeout_ns(const et_opts* opts);  // of a bounded wait
 // Row-major [rows, cols] of 1-byte integers or fp16 as boxes of 128 bytes x box_rows with
 // the 128-byte swizzle; zeros outside.  (api_device has been called.)
 int api_map128(CUtensorMap* m, const void* base, int elem_bytes, uint64_t rows, uint64_t cols, uint32_t box_rows, const char* what);

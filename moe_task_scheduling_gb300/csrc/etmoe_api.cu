@@ -317,6 +317,8 @@ int api_check_ws(const void* ws, size_t have, size_t need) {
     return check_ws(const_cast<void*>(ws), have, need);
 }
 
+uint64_t api_timeout_ns(const et_opts* opts) { return timeout_ns_of(opts); }
+
 int api_map128(CUtensorMap* m, const void* base, int elem_bytes, uint64_t rows, uint64_t cols, uint32_t box_rows, const char* what) {
     cuuint64_t dims[2] = {cols, rows};
     cuuint64_t strides[1] = {cols * elem_bytes};

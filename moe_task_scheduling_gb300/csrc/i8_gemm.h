@@ -37,6 +37,7 @@ struct I8TcArgs {
     int blocks;          // k-blocks that a CTA has in all, at most
     int stages_w, stages_x;
     uint64_t timeout_ns;
+    int fault_cta;       // a test's: this CTA loads no weights, so that all that wait for them give up (-1: none)
 };
 
 struct I8ExpandArgs {

@@ -53,6 +53,8 @@ struct I8Ctl {
     uint64_t full_a[kAStages], empty_a[kAStages];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drain;
+    uint32_t posted_w, posted_x[2];  // stages that copies were posted for: weights; tokens by either CTA of a pair
+    int32_t gave_up;                 // a wait of this CTA ran out
     uint32_t tmem_base;
     int32_t go[2];                   // the epilogue's: the accumulator is complete (0: an abort)
     alignas(16) float sx[2][kI8TokensMax];
@@ -75,10 +77,16 @@ __device__ __forceinline__ void arrive_leader(uint64_t* bar, uint32_t cta) {
     else asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(leader_addr<2>(bar, cta)) : "memory");
 }
 
+struct I8Wait {
+    EtHeader* hdr;
+    uint64_t timeout_ns;
+    int32_t* gave_up;
+};
+
 // mbar_wait (bounded) that polls for longer before it sleeps, and whose time alone ends it:
 // every role of a CTA whose wait ran out sees its own run out too, and no flag in memory has
 // to be taken back when the kernel ends (0.5 us of a small product).
-__device__ __forceinline__ bool wait(const WaitCtx& c, uint64_t* bar, uint32_t parity, int where) {
+__device__ __forceinline__ bool wait(const I8Wait& c, uint64_t* bar, uint32_t parity, int where) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t it = 1;; ++it) {
@@ -86,6 +94,7 @@ __device__ __forceinline__ bool wait(const WaitCtx& c, uint64_t* bar, uint32_t p
         if (it > 1024) __nanosleep(64);
         if ((it & 63u) == 0 && globaltimer_ns() - t0 > c.timeout_ns) {
             record_status(c.hdr, ET_ERR_TIMEOUT, where);
+            *c.gave_up = 1;
             return false;
         }
     }
@@ -226,7 +235,7 @@ struct Work {
 // that the MMA reads.  C: 16-byte chunks of a thread in a block; AHEAD: blocks that are on
 // their way from L2 in registers, which takes longer than the MMAs of a block of few tokens.
 template <int C, int AHEAD>
-__device__ __forceinline__ bool load_tokens(const I8TcArgs& p, I8Ctl* ctl, uint8_t* ring, const WaitCtx& wc, int m0, int rows,
+__device__ __forceinline__ bool load_tokens(const I8TcArgs& p, I8Ctl* ctl, uint8_t* ring, const I8Wait& wc, int m0, int rows,
                                             int kb0, int kb1, int et, int lane, uint32_t& s, uint32_t& phase) {
     const int chunk = et & 7, row0 = et >> 3, xbytes = p.tn * 256;
     const int8_t* x = p.x + static_cast<size_t>(m0) * p.K + chunk * 16;
@@ -300,6 +309,7 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
             mbar_init(&ctl->acc_empty[i], kEpiWarps * CG);
         }
         mbar_init(&ctl->drain, 1);
+        ctl->gave_up = 0;
         fence_mbar_init();
         tma_prefetch_map(&tm_w);
         if (CG == 2) tma_prefetch_map(&tm_x);
@@ -311,7 +321,7 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
     tc_fence_after();
     grid_release();
 
-    const WaitCtx wc{p.hdr, p.timeout_ns};
+    const I8Wait wc{p.hdr, p.timeout_ns, &ctl->gave_up};
     const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
     if (p.rows.d_M) grid_wait();
     const int M = pass_rows(p.rows, p.hdr);
@@ -336,7 +346,7 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
             const uint64_t pol = policy_evict_first();
             fence_proxy_async_global();  // weights that a kernel wrote, read by TMA
             uint32_t s = 0, phase = 0, posted = 0;
-            bool ok = true;
+            bool ok = static_cast<int>(blockIdx.x) != p.fault_cta;
             while (ok && w.next()) {
                 const int n0 = (w.tile / mt) * 128 * CG + static_cast<int>(rank) * 128;
                 for (int kb = w.kb0; kb < w.kb1; ++kb) {
@@ -347,9 +357,7 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
                     if (++s == static_cast<uint32_t>(p.stages_w)) { s = 0; phase ^= 1u; }
                 }
             }
-            if (!ok)  // unwinding: let the copies land
-                for (uint32_t i = posted > static_cast<uint32_t>(p.stages_w) ? posted - p.stages_w : 0; i < posted; ++i)
-                    mbar_drain(&ctl->full_w[i % p.stages_w], (i / p.stages_w) & 1u, 1000000ull);
+            ctl->posted_w = posted;
         }
         __syncwarp();
     } else if (warp == kTokenWarp) {
@@ -369,9 +377,10 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
                     if (++s == static_cast<uint32_t>(p.stages_x)) { s = 0; phase ^= 1u; }
                 }
             }
-            if (!ok && rank == 0)
-                for (uint32_t i = posted > static_cast<uint32_t>(p.stages_x) ? posted - p.stages_x : 0; i < posted; ++i)
-                    mbar_drain(&ctl->full_x[i % p.stages_x], (i / p.stages_x) & 1u, 1000000ull);
+            ctl->posted_x[rank] = posted;
+            uint32_t other;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(other) : "r"(smem_u32(&ctl->posted_x[rank])), "r"(crank ^ 1u));
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(other), "r"(posted) : "memory");
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -512,16 +521,41 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
     }
 
     __syncthreads();
+    if (ctl->gave_up && threadIdx.x == 0) {
+        // Every copy has landed before this CTA goes, whichever role gave up.  (Where none did, all
+        // of them were used.  The tokens' barriers count both CTAs' copies.)
+        auto landed = [](uint64_t* full, uint32_t posted, uint32_t stages) {
+            for (uint32_t i = posted > stages ? posted - stages : 0; i < posted; ++i)
+                (void)mbar_drain(&full[i % stages], (i / stages) & 1u, 1000000ull);
+        };
+        landed(ctl->full_w, ctl->posted_w, p.stages_w);
+        if (CG == 2 && rank == 0) landed(ctl->full_x, ctl->posted_x[0], p.stages_x);
+    }
     // the commits have arrived here, and no CTA goes while the pair's other may reach into it
     if (threadIdx.x == 32) (void)mbar_drain(&ctl->drain, 0, 2000000ull);
     tc_fence_before();
     __syncthreads();
-    if (CG == 2 && p.split == 1) cluster_sync();
+    if (CG == 2) {
+        cluster_sync();
+        const uint32_t armed = ctl->posted_x[0], posted = ctl->posted_x[1];
+        if (posted > armed) {
+            // A wait ran out in between: copies of the pair's second CTA that the first one never
+            // armed its barriers for.  It does so now, and both stay until they have landed.
+            if (rank == 0 && threadIdx.x == 0)
+                for (uint32_t i = armed; i < posted; ++i) {
+                    uint64_t* bar = &ctl->full_x[i % p.stages_x];
+                    mbar_arrive_expect_tx(bar, xbytes);
+                    mbar_drain(bar, (i / p.stages_x) & 1u, 1000000ull);
+                }
+            __syncthreads();
+            if (p.split == 1) cluster_sync();
+        }
+    }
     tc_fence_after();
     if (p.split > 1) {
         // Part r of the cluster sums tokens [r tn / split, (r + 1) tn / split) of the tile; what
         // the others have of them comes into its rings, which nothing uses any more.
-        cluster_sync();
+        if (CG == 1) cluster_sync();
         const int tile = blockIdx.x / (CG * p.split), mine = crank / CG, each = p.tn / p.split;
         const bool have = tile < tiles;
         if (have && warp < 16) {

@@ -429,6 +429,11 @@ size_t et_i8_gemm_workspace_bytes(int M_max, int N, int K) {
 
 int et_i8_gemm(const void* x_q, const float* s_x, const void* w_q, const float* s_w, void* Y, int M, const int32_t* d_M,
                int M_max, int N, int K, void* workspace, size_t workspace_bytes, void* stream) {
+    return et_i8_gemm_opts(x_q, s_x, w_q, s_w, Y, M, d_M, M_max, N, K, workspace, workspace_bytes, nullptr, stream);
+}
+
+int et_i8_gemm_opts(const void* x_q, const float* s_x, const void* w_q, const float* s_w, void* Y, int M, const int32_t* d_M,
+                    int M_max, int N, int K, void* workspace, size_t workspace_bytes, const et_opts* opts, void* stream) {
     return api_entry([&]() -> int {
         std::string why;
         if (!i8_shape_ok(M_max, N, K, &why)) return api_fail(ET_ERR_UNSUPPORTED, why);
@@ -475,7 +480,8 @@ int et_i8_gemm(const void* x_q, const float* s_x, const void* w_q, const float* 
             a.split = pl.split;
             a.blocks = ceil_div_l(pl.kblocks, pl.split) * ceil_div_l(static_cast<long long>(ceil_div_l(rows, pl.tn)) * pl.nt, pl.grid);
             i8_tc_stages(pl.pair, pl.tn, a.blocks, &a.stages_w, &a.stages_x);
-            a.timeout_ns = 200000000ull;
+            a.timeout_ns = api_timeout_ns(opts);
+            a.fault_cta = opts && opts->fault_mode == 1 ? opts->fault_arg : -1;
             cudaError_t e = cudaSuccess;
             CUtensorMap mx = mw;
             if (pl.pair) {

@@ -99,6 +99,7 @@ _SIGNATURES = {
     "et_i8_quantize": (_i, [_vp] * 3 + [_i, _vp, _i, _i, _vp, _sz, _vp]),
     "et_i8_gemm_workspace_bytes": (_sz, [_i] * 3),
     "et_i8_gemm": (_i, [_vp] * 5 + [_i, _vp] + [_i] * 3 + [_vp, _sz, _vp]),
+    "et_i8_gemm_opts": (_i, [_vp] * 5 + [_i, _vp] + [_i] * 3 + [_vp, _sz, _vp, _vp]),
     "et_status": (_i, [_vp, _vp, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)]),
     "et_reset_status": (_i, [_vp, _vp]),
 }
@@ -738,17 +739,19 @@ def et_i8_gemm_workspace_bytes(M_max, N, K) -> int:
     return _workspace_bytes(load().et_i8_gemm_workspace_bytes, M_max, N, K)
 
 
-def et_i8_gemm(x_q, s_x, w_q, s_w, Y, *, M=None, d_M=None, workspace, stream=None, check=True):
+def et_i8_gemm(x_q, s_x, w_q, s_w, Y, *, M=None, d_M=None, workspace, stream=None, timeout_us=0, fault_mode=0, fault_arg=0,
+               check=True):
     """Y = (s_x s_w^T) * (x_q w_q^T) for int8 x_q [M_max, K] and w_q [N, K] with their fp32 scales."""
     dev = _device_of(x_q, "x_q")
     M_max, K = x_q.shape
     N = Y.shape[-1]
     _fits(M_max | N | K)
     ws, wsb = _workspace_args(workspace, dev)
-    return _call(load().et_i8_gemm, dev, stream, (
+    opts = _opts(timeout_us, fault_mode, fault_arg)
+    return _call(load().et_i8_gemm if opts is None else load().et_i8_gemm_opts, dev, stream, (
         _arg(x_q, "x_q", _I8, (M_max, K), dev), _arg(s_x, "s_x", _F32, (M_max,), dev), _arg(w_q, "w_q", _I8, (N, K), dev),
         _arg(s_w, "s_w", _F32, (N,), dev), _arg(Y, "Y", _BF16, (M_max, N), dev), _rows(M, M_max), _count_arg(d_M, dev),
-        M_max, N, K, ws, wsb), check)
+        M_max, N, K, ws, wsb) + (() if opts is None else (opts,)), check)
 
 
 def et_status(workspace, stream=None):
