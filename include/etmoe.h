@@ -436,13 +436,15 @@ int et_block_norm_bwd(const void* x, const void* y, const void* gamma_post, cons
  *   loss[0]  = E sum_e counts[e] / (n k) * mean_prob[e].
  *
  * The bias enters the choice alone: weights, losses and gradients do not see
- * it (a program moves it by the counts, for balance).  The choice is that of
- * exact arithmetic: rows where the fp32 values of two candidates are closer
- * than their errors are chosen again in 64 bits, which takes a few times a
- * row's time, more where many are that close (a row of equal logits and biases
- * is not among them).  Values that are equal in 64 bits tie.  With x0 the row's largest logit (with renorm, the
- * largest chosen one), a weight is off by a factor of at most
- * 1 +- (20 + E + |x - x0|) 2^-24, a p by 1 +- (48 + E + 4 |x - x0| + 5 |x|) 2^-24.
+ * it (a program moves it by the counts, for balance).  The choice is by c and by
+ * group scores as 64-bit arithmetic has them, with softmax scores without a bias
+ * as e^(logit - the row's largest); values that are equal there tie.  Rows where
+ * the fp32 values of two candidates are closer than their errors are chosen again
+ * in 64 bits, which takes a few times a row's time, more where many are that
+ * close (a row of equal logits and biases is not among them).  With x0 the row's
+ * largest logit (with renorm, the largest chosen one), a weight is off by a factor
+ * of at most 1 +- (20 + E + |x - x0|) 2^-24, a p by
+ * 1 +- (48 + E + 4 |x - x0| + 5 |x|) 2^-24.
  * Scores below 2^-126 may be 0.  Sums over tokens run in a fixed order.
  * A NaN logit, and with softmax one of +inf, makes its token's softmax weights,
  * or the sigmoid weights it takes part in, and the loss NaN.

@@ -40,6 +40,24 @@ __device__ __forceinline__ unsigned long long value_key(double v) {
     return static_cast<unsigned long long>(b) ^ (static_cast<unsigned long long>(b >> 63) | 0x8000000000000000ull);
 }
 
+// What ranks experts and groups in 64 bits, everywhere (equal ones tie): scores + bias, softmax
+// scores by their row's sum Z of e^(x - top); Z = 0: softmax scores without a bias, as their
+// multiples e^(x - top).
+__device__ __forceinline__ double value64(float x, float b, bool sigmoid, float top, double Z) {
+    const double e = exp(sigmoid ? -static_cast<double>(x) : static_cast<double>(x) - static_cast<double>(top));
+    return sigmoid ? 1.0 / (1.0 + e) + static_cast<double>(b) : Z == 0.0 ? e : e / Z + static_cast<double>(b);
+}
+
+// The sum of e^(x - top) over a row, in 64 bits, by the warp.
+__device__ __noinline__ double softmax_sum64(const float* row, float top, int E, int lane) {
+    double Z = 0.0;
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32) Z += exp(static_cast<double>(row[e]) - static_cast<double>(top));
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) Z += __shfl_xor_sync(0xffffffffu, Z, off);
+    return Z;
+}
+
 // The whole choice in 64 bits, for the rows where 32 cannot tell.  Lane `lane` has the
 // experts lane * EPL + i.  Returns lane j's expert, the j-th, or -1.
 // Out of line and in plain loops: one row in some hundreds comes here.
@@ -49,29 +67,22 @@ __device__ __noinline__ int choose64(const float* row, const float* bias, int E,
     constexpr uint32_t kAll = 0xffffffffu;
     unsigned long long key[EPL];  // of score + bias; 0: not available
     float v[EPL];
-    double m = 0.0, Z = 1.0;
+    float top = 0.0f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) v[i] = lane * EPL + i < E ? row[lane * EPL + i] : -INFINITY;
     if (!sigmoid) {
-        float top = v[0];
+        top = v[0];
 #pragma unroll
         for (int i = 1; i < EPL; ++i) top = fmaxf(top, v[i]);
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
-        m = top;
-        Z = 0.0;
-#pragma unroll 1
-        for (int i = 0; i < EPL; ++i) Z += exp(static_cast<double>(v[i]) - m);  // 0 past E
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) Z += __shfl_xor_sync(kAll, Z, off);
     }
+    const double Z = !sigmoid && bias ? softmax_sum64(row, top, E, lane) : 0.0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        const double x = v[i];
         key[i] = 0;
         if (!(v[i] == -INFINITY)) {
-            double c = sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - m) / Z;
-            if (bias) c += static_cast<double>(bias[lane * EPL + i]);
+            const double c = value64(v[i], bias ? bias[lane * EPL + i] : 0.0f, sigmoid, top, Z);
             if (!(c == -INFINITY)) key[i] = value_key(c);
         }
     }
@@ -247,21 +258,15 @@ __device__ __forceinline__ uint32_t sum_key(float v) {
 
 constexpr int kCandidates = 16;  // experts whose order is looked at again at most
 
-// What ranks experts and groups in 64 bits: scores + bias, softmax scores by their row's sum Z
-// of e^(x - top); Z = 0: softmax scores without a bias, as their multiples e^(x - top).
-__device__ __forceinline__ double value64(float x, float b, bool sigmoid, float top, double Z) {
-    const double e = exp(sigmoid ? -static_cast<double>(x) : static_cast<double>(x) - static_cast<double>(top));
-    return sigmoid ? 1.0 / (1.0 + e) + static_cast<double>(b) : Z > 0.0 ? e / Z + static_cast<double>(b) : e;
-}
-
-// The sum of e^(x - top) over a row, in 64 bits, by the warp.
-__device__ __noinline__ double softmax_sum64(const float* row, float top, int E, int lane) {
-    double Z = 0.0;
-#pragma unroll 1
-    for (int e = lane; e < E; e += 32) Z += exp(static_cast<double>(row[e]) - static_cast<double>(top));
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) Z += __shfl_xor_sync(0xffffffffu, Z, off);
-    return Z;
+// Without a bias 32 bits compare logits, which are exact.  Logits this far below x or less may
+// have scores that are equal in 64 bits: a score is off by 2^-51 of itself (exp, an add, a
+// quotient), and two of them are (x - y) (1 - s) apart, with 1 - s >= 1/2 below 0; above, floats
+// are 2^-24 x apart, which outweighs 1 - s up to x = 20.  (A softmax score: 2^-52 and what x - top
+// rounds off, 2^-53 of it.)  So only logits near 0, or far below the row's largest, are that close.
+template <bool SIGMOID>
+__device__ __forceinline__ float same_score(float x, float top) {
+    constexpr float kStep = 1.0f / (1ull << 49);
+    return SIGMOID ? kStep : fmaf(top - x, kStep, kStep);
 }
 
 // Two groups whose scores 32 bits cannot tell apart: 1 if the first has the larger, or the
@@ -296,13 +301,13 @@ __device__ __noinline__ int compare_groups(const float* row, const float* bias_s
     return sa > sb || (sa == sb && a < b) ? 1 : 0;
 }
 
-// The order of n candidates (n <= kCandidates, their experts in slots) in 64 bits (of softmax
-// scores without a bias, Z = 0, by the logits): puts the best k there in their order.
+// The order of n candidates (n <= kCandidates, their experts in slots) in 64 bits: puts the
+// best k there in their order.
 __device__ __noinline__ void order_again(const float* row, const float* bias_s, bool sigmoid, float top, double Z, int n, int k, uint32_t* slots,
                                          int lane) {
     constexpr uint32_t kAll = 0xffffffffu;
     const int e = lane < n ? static_cast<int>(slots[lane]) : 0;
-    const double c = lane < n ? (sigmoid || Z > 0.0 ? value64(row[e], bias_s[e], sigmoid, top, Z) : static_cast<double>(row[e])) : 0.0;
+    const double c = lane < n ? value64(row[e], bias_s[e], sigmoid, top, Z) : 0.0;
     const unsigned long long key = value_key(c);
     int rank = 0;
 #pragma unroll 1
