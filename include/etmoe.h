@@ -439,9 +439,11 @@ int et_block_norm_bwd(const void* x, const void* y, const void* gamma_post, cons
  * it (a program moves it by the counts, for balance).  The choice is by c and by
  * group scores as 64-bit arithmetic has them, with softmax scores without a bias
  * as e^(logit - the row's largest); values that are equal there tie.  Rows where
- * the fp32 values of two candidates are closer than their errors are chosen again
- * in 64 bits, which takes a few times a row's time, more where many are that
- * close (a row of equal logits and biases is not among them).  With x0 the row's
+ * the fp32 values of two candidates are closer than their errors, or (without a
+ * bias) two candidates have sigmoid scores of logits above 20, are chosen again
+ * in 64 bits, which takes a few times a row's time; about 14 us of a warp where
+ * more than 16 candidates are that close, or a chosen score is below e^-700 (a row
+ * of equal logits and biases is not among them).  With x0 the row's
  * largest logit (with renorm, the largest chosen one), a weight is off by a factor
  * of at most 1 +- (20 + E + |x - x0|) 2^-24, a p by
  * 1 +- (48 + E + 4 |x - x0| + 5 |x|) 2^-24.

@@ -263,6 +263,7 @@ constexpr int kCandidates = 16;  // experts whose order is looked at again at mo
 // quotient), and two of them are (x - y) (1 - s) apart, with 1 - s >= 1/2 below 0; above, floats
 // are 2^-24 x apart, which outweighs 1 - s up to x = 20.  (A softmax score: 2^-52 and what x - top
 // rounds off, 2^-53 of it.)  So only logits near 0, or far below the row's largest, are that close.
+constexpr float kSigmoidOne = 20.0f;
 template <bool SIGMOID>
 __device__ __forceinline__ float same_score(float x, float top) {
     constexpr float kStep = 1.0f / (1ull << 49);

@@ -257,9 +257,11 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
             const bool pair = on && lane < k - 1 && onn;
             // (one that equals its neighbour comes in the order of the experts already)
             const float tol = BIAS ? 2.0f * err + kU * (fabsf(c) + fabsf(cn)) : same_score<SIGMOID>(cn, top);
-            bool doubt = pair && !(b == bn && myL == Ln) && !(c - cn > tol);
-            // logits whose scores meet at 1 or 0 in 64 bits, chosen or not
-            const bool met = !BIAS && on && (SIGMOID ? myL > 16.0f || myL < -700.0f : myL - top < -700.0f);
+            // (without a bias, sigmoid scores of logits above kSigmoidOne may be equal: near 1)
+            constexpr bool kOne = SIGMOID && !BIAS;
+            bool doubt = pair && !(b == bn && myL == Ln) && (!(c - cn > tol) || (kOne && cn > kSigmoidOne));
+            // logits whose scores may be equal in 64 bits near 0, chosen or not
+            const bool met = !BIAS && on && (SIGMOID ? myL < -700.0f : myL - top < -700.0f);
             // the least of the chosen, and what may be above it in truth: these experts, and they alone?
             const uint32_t lanes_on = __ballot_sync(kAll, on);
             const float ck = __shfl_sync(kAll, c, k - 1), Lk = __shfl_sync(kAll, myL, k - 1), bk = __shfl_sync(kAll, b, k - 1);
@@ -267,7 +269,8 @@ __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(con
 #pragma unroll
             for (int off = 4; off >= 1; off >>= 1) cmin = fminf(cmin, __shfl_xor_sync(kAll, cmin, off));
             cmin = __shfl_sync(kAll, cmin, 0);
-            const float floor = cmin - (BIAS ? 2.0f * err + 4.0f * kU * fabsf(cmin) : same_score<SIGMOID>(cmin, top));
+            float floor = cmin - (BIAS ? 2.0f * err + 4.0f * kU * fabsf(cmin) : same_score<SIGMOID>(cmin, top));
+            if (kOne) floor = fminf(floor, kSigmoidOne);
             int above = 0;
             const uint32_t floor_key = lanes_on >> (k - 1) & 1 ? logit_key(floor) : ~0u;  // else all that are available are chosen
 #pragma unroll
