@@ -404,8 +404,8 @@ _INT_MAX = (1 << 31) - 1
 
 
 def _fits(sizes):
-    """Refuses sizes (or-ed together) of more than 31 bits."""
-    if sizes > _INT_MAX:
+    """Refuses sizes (or-ed together) of more than 31 bits, of either sign."""
+    if not -_INT_MAX <= sizes <= _INT_MAX:
         raise ValueError("sizes must be below 2^31")
 
 
@@ -628,7 +628,7 @@ def et_router_groups(logits, topk_idx, topk_w, *, score, n_groups=1, k_groups=1,
     dev = _device_of(logits, "logits")
     T_max, E = logits.shape
     k = topk_idx.shape[-1]
-    _fits(T_max | E | k | n_groups | k_groups | group_best)
+    _fits(T_max | E | k | n_groups | k_groups | group_best | score)
     ws, wsb = _workspace_args(workspace, dev)
     return _call(load().et_router_groups, dev, stream, (
         _arg(logits, "logits", _F32, (T_max, E), dev), _arg(bias, "bias", _F32, (E,), dev),
@@ -645,7 +645,7 @@ def et_router_groups_bwd(logits, topk_idx, topk_w, expert_counts, n_routed, d_lo
     dev = _device_of(logits, "logits")
     T_max, E = logits.shape
     k = topk_idx.shape[-1]
-    _fits(T_max | E | k)
+    _fits(T_max | E | k | score)
     ws, wsb = _workspace_args(workspace, dev)
     return _call(load().et_router_groups_bwd, dev, stream, (
         _arg(logits, "logits", _F32, (T_max, E), dev), _arg(token_mask, "token_mask", _U8, (T_max,), dev),
