@@ -747,11 +747,13 @@ def et_i8_gemm(x_q, s_x, w_q, s_w, Y, *, M=None, d_M=None, workspace, stream=Non
     N = Y.shape[-1]
     _fits(M_max | N | K)
     ws, wsb = _workspace_args(workspace, dev)
-    opts = _opts(timeout_us, fault_mode, fault_arg)
-    return _call(load().et_i8_gemm if opts is None else load().et_i8_gemm_opts, dev, stream, (
+    args = (
         _arg(x_q, "x_q", _I8, (M_max, K), dev), _arg(s_x, "s_x", _F32, (M_max,), dev), _arg(w_q, "w_q", _I8, (N, K), dev),
         _arg(s_w, "s_w", _F32, (N,), dev), _arg(Y, "Y", _BF16, (M_max, N), dev), _rows(M, M_max), _count_arg(d_M, dev),
-        M_max, N, K, ws, wsb) + (() if opts is None else (opts,)), check)
+        M_max, N, K, ws, wsb)
+    if timeout_us or fault_mode:
+        return _call(load().et_i8_gemm_opts, dev, stream, (*args, _opts(timeout_us, fault_mode, fault_arg)), check)
+    return _call(load().et_i8_gemm, dev, stream, args, check)
 
 
 def et_status(workspace, stream=None):
