@@ -26,8 +26,8 @@
 // Every wait is bounded.
 //
 // What bounds it: few tokens the weights' conversion, 560 cycles a block of 16 KB where HBM
-// brings one in 700, on those SMs that have a tile (M = 32, 14336 x 4096: 16.3 us, 112 of 152
-// SMs, 3.7 TB/s with 6 us before and after); many tokens the tensor cores (M = 4096, 14336 x
+// brings one in 700, on those SMs that have a tile (M = 32, 14336 x 4096: 15.6 us, 112 of 152
+// SMs, 3.8 TB/s with 6 us before and after); many tokens the tensor cores (M = 4096, 14336 x
 // 4096: 260 us, 1.85 PFLOP/s, 96 % of a bf16 library product's burst; at 2048 x 4096 x 4096 the
 // tensor pipe is busy for 75 % of the kernel, the rest is the last tiles' epilogue and the
 // pipeline's start).
@@ -62,10 +62,9 @@ struct I8Ctl {
 
 // ---------------------------------------------------------------- PTX that et_device.cuh has for one CTA
 
-template <int CG>
 __device__ __forceinline__ uint32_t leader_addr(const void* p, uint32_t cta) {  // of this variable in the pair's first CTA
-    uint32_t a = smem_u32(p);
-    if (CG == 2) asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(cta & ~1u));
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(cta & ~1u));
     return a;
 }
 
@@ -74,7 +73,7 @@ __device__ __forceinline__ uint32_t leader_addr(const void* p, uint32_t cta) {  
 template <int CG>
 __device__ __forceinline__ void arrive_leader(uint64_t* bar, uint32_t cta) {
     if (CG == 1) mbar_arrive(bar);
-    else asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(leader_addr<2>(bar, cta)) : "memory");
+    else asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(bar, cta)) : "memory");
 }
 
 struct I8Wait {
@@ -100,16 +99,11 @@ __device__ __forceinline__ bool wait(const I8Wait& c, uint64_t* bar, uint32_t pa
     }
 }
 
-template <int CG>
+// A pair's tokens: `bar` is the first CTA's, which counts both CTAs' copies.
 __device__ __forceinline__ void tma_tokens(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
-    if (CG == 1)
-        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-                     "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
-                     : "memory");
-    else  // the barrier may be the pair's other CTA's
-        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-                     "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
-                     : "memory");
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+                 : "memory");
 }
 
 template <int CG>
@@ -370,9 +364,9 @@ i8_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ C
                 for (int kb = w.kb0; kb < w.kb1; ++kb) {
                     if (!(ok = wait(wc, &ctl->empty_x[s], phase ^ 1u, kWhereEmpty))) break;
                     if (rank == 0) mbar_arrive_expect_tx(&ctl->full_x[s], xbytes * CG);
-                    const uint32_t bar = leader_addr<CG>(&ctl->full_x[s], crank), dst = smem_u32(ring_x + s * xbytes);
-                    tma_tokens<CG>(dst, &tm_x, bar, kb * kI8KBlock, m0);
-                    tma_tokens<CG>(dst + xrows * 128, &tm_x, bar, kb * kI8KBlock + 64, m0);
+                    const uint32_t bar = leader_addr(&ctl->full_x[s], crank), dst = smem_u32(ring_x + s * xbytes);
+                    tma_tokens(dst, &tm_x, bar, kb * kI8KBlock, m0);
+                    tma_tokens(dst + xrows * 128, &tm_x, bar, kb * kI8KBlock + 64, m0);
                     ++posted;
                     if (++s == static_cast<uint32_t>(p.stages_x)) { s = 0; phase ^= 1u; }
                 }
