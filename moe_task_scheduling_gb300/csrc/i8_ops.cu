@@ -154,7 +154,7 @@ __device__ __forceinline__ int4 load_weights(const int8_t* p) {  // streamed: th
     return v;
 }
 
-// c += A B, A 16 channels x 32 k, B 32 k x 8 tokens: exact in int32.
+// d += A B, A 16 channels x 16 k, B 16 k x 8 tokens: fp32 sums, exact up to 2^24 for int8 values.
 __device__ __forceinline__ void mma_f16_sync(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -166,6 +166,7 @@ __device__ __forceinline__ void int8x16_to_half(const int4& v, uint32_t (&h)[8])
     int8_to_half(v.z, h[4], h[5]);
     int8_to_half(v.w, h[6], h[7]);
 }
+// c += A B, A 16 channels x 32 k, B 32 k x 8 tokens: exact in int32.
 __device__ __forceinline__ void mma_s8(int (&c)[4], int a0, int a1, int a2, int a3, int b0, int b1) {
     asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
@@ -177,10 +178,10 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], int a0, int a1, int a2, int 
 // meanwhile.  A thread's 16-byte loads are its fragments as they are: the order of k within
 // a piece is the same for both operands, and no other order matters to an exact sum.  An
 // integer MMA takes 16 cycles of an SM here, 32 / MT bytes of weights a cycle, where HBM
-// brings 23: up to 8 tokens (14336 x 4096: 11.8 us, 5.0 TB/s from launch to end, bound by
+// brings 23: up to 8 tokens (14336 x 4096: 11.5 us, 5.1 TB/s from launch to end, bound by
 // HBM).  HALF: both operands become fp16 in registers, whose MMAs take 2 cycles for half as
 // many k; 5 instructions convert 4 bytes, and the sums of a warp, fp32, are exact up to 2^24,
-// so for K up to 8192.  16 tokens 13.8 us (17.7 with integer MMAs); bound by its instructions'
+// so for K up to 8192.  16 tokens 13.4 us (17.7 with integer MMAs); bound by its instructions'
 // latency and by the tokens, which every tile reads again: as many bytes as its weights.
 // (Three pieces ahead in place of two 14.7, the tokens one piece ahead 15.1, three CTAs an SM
 // with one piece 14.1 and 20 for 4096 x 14336.)
@@ -290,9 +291,11 @@ __global__ void __launch_bounds__(kGemvWarps * 32, kGemvCtas) i8_gemv_kernel(con
 }
 
 // Which calls take the form above: up to 16 tokens, and up to 32 where the weights are few.
-// With 32 tokens it takes 2.2 us + 1 us for each 2.9 MB of weights, the tcgen05 form 6 us +
-// 1 us for each 5.6 MB (1024 x 1024: 3.1 against 6.1 us, 2048 x 2048: 4.0 and 6.5, 14336 x
-// 4096: 22.6 and 16.4): they meet at 22 MB.
+// Measured, 32 tokens, this form and the tcgen05 form: 1024 x 1024 2.7 and 5.6 us, 2048 x 2048
+// 3.8 and 6.6, 4096 x 4096 7.8 and 9.0; 4096 x 5120 9.1 and 9.7, 8192 x 2560 10.2 and 9.8, 5120
+// x 4096 12.1 and 11.4; 6144 x 4096 13.5 and 11.6, 14336 x 4096 19.8 and 15.6: they meet at 20 to
+// 25 MB of weights.  (17 to 24 tokens at 25 to 34 MB: 4096 x 8192 11.2 and 11.9, 14336 x 4096
+// 17.2 and 15.5.  What one limit costs them is 15 % at most, 4096 x 6144 9.1 and 10.4.)
 bool i8_gemv(int M_max, int N, int K) {
     return M_max <= 16 || (M_max <= 32 && static_cast<long long>(N) * K <= 22000000);
 }

@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kDropThreads) dropout_vec_kernel(const Dropout
 
 // Any H and alignment: a CTA takes 2048 columns of a row, draws their mask into
 // shared memory, then neighbouring threads take neighbouring elements.  Bound by its
-// 2-byte accesses and its short CTAs (8000 x 1001: 22 us, 2.2 TB/s).
+// 2-byte accesses and its short CTAs (8000 x 1001: 21 us, 2.3 TB/s).
 __global__ void __launch_bounds__(kDropThreads) dropout_any_kernel(const DropoutArgs p) {
     __shared__ uint8_t dropped[kDropCols / 8];
     grid_begin();
@@ -315,8 +315,7 @@ __host__ __device__ constexpr int ln_row_bytes(int H, bool vec, int vectors) { r
 // are floats in shared memory (unpacked anew for each row they were two of 33 instructions
 // an element).  T = H = 4096: 20.5 us, 6.5 TB/s without dropout, bound by HBM; 23.3 us, 5.8
 // TB/s with it, by issue slots too (30 instructions an element, 62 % of the slots).
-// Without VEC by its 2-byte accesses: 4096 x 1001 13 us, 2.5 TB/s; with dropout 18 (20 with
-// 125 registers and two CTAs an SM).
+// Without VEC by its 2-byte accesses: 4096 x 1001 11.8 us, 2.8 TB/s; with dropout 14.9.
 template <bool VEC, int MODE, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : VEC ? 4 : 3) ln_fwd_kernel(const LnArgs p) {
     constexpr int V = norm_v(MODE);
@@ -414,8 +413,10 @@ __global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : VEC ? 4 : 3) ln_fwd_ker
 // Without VEC a row is copied by the 16-byte pieces that hold it (the first of a
 // tensor element by element, the last cut to its end) and read back by element,
 // with a barrier on either side.  Rows of H > 8192 do not fit twice and are copied
-// one at a time.  T = H = 4096 with dropout: 33 us, 6.1 TB/s, and 39 us with the parameter
-// gradients: 304 rows of partial sums are written and read again, and a second kernel starts.
+// one at a time, and their 1024 threads have 64 registers, of which they spill 354 bytes (428
+// without VEC): T = 1000, H = 16384 84 us, a third of the copy rate.  T = H = 4096 with
+// dropout: 33 us, 6.1 TB/s, and 39 us with the parameter gradients: 304 rows of partial sums
+// are written and read again, and a second kernel starts.
 // (512-thread CTAs of two rows, half the partial sums, took 44.)  The parameter gradients
 // are added up in registers, for 256 rows
 // at most, then in this CTA's row of partial sums, then by ln_sum_kernel: a fixed

@@ -1,7 +1,7 @@
-// ops_device.cuh -- device helpers shared by the router, norm and 4-bit weight
-// kernels: warp and block sums in a fixed order, 16-byte asynchronous copies,
-// the symbolic row count and the sticky status word.  None of these kernels
-// waits on a flag or an mbarrier, so none of them needs a wait budget.
+// ops_device.cuh -- device helpers shared by the router, norm, dropout, 4-bit and
+// 8-bit weight kernels: warp and block sums in a fixed order, 16-byte asynchronous
+// copies, the symbolic row count and the sticky status word.  Nothing here waits on
+// a flag or an mbarrier.  (i8_gemm_kernel.cu does, and bounds its waits itself.)
 #pragma once
 
 #include <cuda_fp16.h>

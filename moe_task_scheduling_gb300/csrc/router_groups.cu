@@ -21,9 +21,10 @@ namespace {
 // the whole row if they are too many.
 //
 // The form for few rows, and for E and groups that eight lanes cannot share
-// (router_rows4_kernel has the others).  Bound by a row's latency, T = 16, E = 128 6.3 us, then
-// by instruction issue, about 1080 a row at E = 256.  Groups that are no power of two of lanes
-// are looked at one by one (T = 16384, E = 160 in 8 groups took 43 us this way).
+// (router_rows4_kernel has the others).  Bound by a row's latency, T = 16, E = 128 6.0 us, then
+// by instruction issue, about 1080 a row at E = 256 (with 64 registers for 32 warps a CTA, of
+// which E > 64 spills 80 to 384 bytes a thread).  Groups that are no power of two of lanes are
+// looked at one by one (T = 16384, E = 160 in 8 groups took 43 us this way; E = 60 in 5 21.6).
 template <int EPL, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(kRouterWarpsMax * 32) router_groups_kernel(const GroupArgs p) {
     constexpr uint32_t kAll = 0xffffffffu, kLow = 32 * EPL - 1;  // the bits that name an expert

@@ -22,8 +22,11 @@ __host__ __device__ constexpr int rows4_floats(int E) { return kRows4Warps * 5 *
 //
 // Bound by instructions and their latency: about 500 a row at E = 256 where one row a warp
 // takes 1080, 16 warps an SM with 128 registers (12 with 168 were slower from T = 1024 to
-// 16384 by 5 to 20 %).  T = 16384, E = 256, sigmoid with bias, 8 groups, k = 8 25-28 us, 8 of
-// them fixed (launch, the sums over CTAs); T = 65536 59-63 us; E = 160 19 and E = 128 17 us.
+// 16384 by 5 to 20 %).  With 128 the forms for E = 192 and more spill, sigmoid with a bias at
+// E = 256 the most (360 bytes out, 416 in, a thread), and 36 % of the issue slots are used: no
+// limit of the chip's is reached.  T = 16384, E = 256, sigmoid with bias, 8 groups, k = 8 25-28
+// us, 8 of them fixed (launch, the sums over CTAs); T = 65536 59-63 us; E = 160 19 and E = 128
+// 17 us.
 template <int N, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(kRows4Warps * 32, 1) router_rows4_kernel(const GroupArgs p) {
     constexpr uint32_t kAll = 0xffffffffu;
